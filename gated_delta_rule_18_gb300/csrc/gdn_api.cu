@@ -3,12 +3,12 @@
 // layout, kernel dispatch and optional per-kernel CUDA-event timing.
 #include <atomic>
 #include <mutex>
-#include <vector>
 
 #include "../../include/gdn.h"
 #include "gdn_common.cuh"
 #include "gdn_bwd_f32.cuh"
 #include "gdn_frame_bwd.cuh"
+#include "gdn_launch.cuh"
 
 namespace gdn {
 cudaError_t launch_prep_bwd(const void *x, int64_t xsb, int64_t xst, int64_t xsh, const float *dy,
@@ -22,72 +22,10 @@ cudaError_t launch_merge_bwd(const void *num, int64_t n_sb, int64_t n_st, int64_
 
 namespace {
 
-using gdn::FwdParams;
+using namespace gdn;  // launch(), its kinds, FwdParams
 
-// ------------------------------------------------------------ profiling ----
-
-enum Kind {
-    KPrepL2 = 0, KPrepRms, KTable, KIntra, KState, KFusedF32, KMerge, KFrameGram, KFrameChain,
-    KFrameOut, KSegSummary, KSegCombine, KBwdDh, KBwdDq, KBwdDk, KSum, KF32Prep, KF32Serial, KFused,
-    KFrameXt, KFrameLam, KFrameTok, KPrepBwd, KMergeBwd, KBwdF32Scan, KBwdF32Reduce, KNumKinds
-};
-const char *kKindNames[KNumKinds] = {"prep_l2",  "prep_rms", "chunk_table", "intra_bf16",
-                                     "state_tc", "fused_f32", "merge",      "frame_gram",
-                                     "frame_chain", "frame_out", "seg_summary", "seg_combine",
-                                     "bwd_dh", "bwd_dq", "bwd_dk", "dir_sum", "f32_prep", "f32_serial",
-                                     "fused_tc", "frame_xt", "frame_lam", "frame_tokgrad", "prep_bwd", "merge_bwd",
-                                     "bwd_f32_scan", "bwd_f32_reduce"};
-
-struct Profiler {
-    std::mutex mu;
-    bool on = false;
-    std::vector<cudaEvent_t> pool;
-    struct Rec {
-        int kind;
-        cudaEvent_t a, b;
-    };
-    std::vector<Rec> recs;
-};
-Profiler &prof() {
-    static Profiler *p = new Profiler();  // never destroyed: safe at exit
-    return *p;
-}
-std::atomic<long long> g_launches{0};
 // the testing aid of gdn_set_stall_test (-1: off)
 std::atomic<int> g_stall_cta{-1}, g_stall_us{1000};
-
-cudaEvent_t take_event(Profiler &P) {
-    if (!P.pool.empty()) {
-        cudaEvent_t e = P.pool.back();
-        P.pool.pop_back();
-        return e;
-    }
-    cudaEvent_t e = nullptr;
-    if (cudaEventCreate(&e) != cudaSuccess) return nullptr;
-    return e;
-}
-
-template <class F>
-cudaError_t launch(int kind, cudaStream_t st, F &&f) {
-    Profiler &P = prof();
-    cudaEvent_t a = nullptr, b = nullptr;
-    {
-        std::lock_guard<std::mutex> g(P.mu);
-        if (P.on) {
-            a = take_event(P);
-            b = take_event(P);
-        }
-    }
-    if (a && b) cudaEventRecord(a, st);
-    cudaError_t e = f();
-    if (e == cudaSuccess) g_launches.fetch_add(1);
-    if (a && b) {
-        cudaEventRecord(b, st);
-        std::lock_guard<std::mutex> g(P.mu);
-        P.recs.push_back({kind, a, b});
-    }
-    return e;
-}
 
 // ------------------------------------------------------------- workspace ---
 
@@ -1221,7 +1159,7 @@ gdn_status gdn_last_device_error(void *workspace, cudaStream_t stream, int *word
 int gdn_kernel_kinds(void) { return KNumKinds; }
 
 const char *gdn_kernel_name(int kind) {
-    return (kind >= 0 && kind < KNumKinds) ? kKindNames[kind] : "unknown";
+    return (kind >= 0 && kind < KNumKinds) ? kind_name(kind) : "unknown";
 }
 
 void gdn_set_state_tile(int bv) { gdn::set_state_tile(bv); }
@@ -1263,6 +1201,6 @@ gdn_status gdn_profile_collect(float *ms, int *launches, int n) {
     return st;
 }
 
-long long gdn_launch_count(void) { return g_launches.load(); }
+long long gdn_launch_count(void) { return launches().load(); }
 
 }  // extern "C"

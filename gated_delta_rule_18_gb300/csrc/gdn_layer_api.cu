@@ -1,0 +1,370 @@
+// gdn_layer_api.cu -- the C entry points of the state-space layer's operators
+// (include/gdn.h): host-side checks, workspace layout and dispatch.
+#include "../../include/gdn.h"
+#include "gdn_launch.cuh"
+#include "gdn_layer.cuh"
+
+namespace {
+
+using namespace gdn;
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+int elem_size(int dtype) { return dtype == GDN_BF16 ? 2 : dtype == GDN_E4M3 ? 1 : 4; }
+bool dtype_ok(int t) { return t == GDN_F32 || t == GDN_BF16; }
+uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+gdn_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
+bool ws_ok(const void *ws, size_t have, size_t need) { return ws && have >= need && addr(ws) % kAlign == 0; }
+bool f32_ok(const void *p) { return addr(p) % 4 == 0; }
+
+// Strided rows: the base on an element, no negative stride; `wide` stays set
+// while every row starts on a boundary of `bytes` (0: element rows only).
+struct Rows {
+    bool ok = true, wide = true;
+    void add(const void *p, int dtype, int64_t sb, int64_t st, int bytes = 16) {
+        if (!p) return;
+        const int64_t e = elem_size(dtype);
+        ok = ok && addr(p) % e == 0 && sb >= 0 && st >= 0;
+        wide = wide && addr(p) % bytes == 0 && sb * e % bytes == 0 && st * e % bytes == 0;
+    }
+};
+
+// shapes of a dense or packed batch
+bool batch_ok(int B, int T, int D, const int32_t *cu, int n_seq) {
+    if (B < 1 || B > 65535 || T < 0 || D < 1 || D > (1 << 20)) return false;
+    return cu ? B == 1 && n_seq >= 1 : n_seq == B;
+}
+
+struct SsmBwdWs {
+    size_t ckpt, bc, a, d, total;
+};
+bool ssm_shape_ok(int B, int T, int D, int N, int n_seq, int varlen) {
+    if (B < 1 || B > 65535 || T < 0 || D < 1 || D > (1 << 20) || N < 1 || N > kSsmMaxN) return false;
+    return varlen ? B == 1 && n_seq >= 1 && n_seq <= 65535 : n_seq == B;
+}
+SsmBwdWs ssm_bwd_ws(int B, int T, int D, int N, int n_seq, int varlen) {
+    SsmBwdWs L;
+    const int np = N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 64 : 128;
+    const size_t groups = varlen ? (size_t)T / kSsmCkpt + n_seq + 1 : (size_t)B * (T / kSsmCkpt + 1);
+    size_t off = kAlign;
+    L.ckpt = off;
+    off = align_up(off + groups * D * np * 4);
+    L.bc = off;
+    off = align_up(off + (size_t)ssm_bwd_tiles(D, N) * B * T * 2 * N * 4);
+    L.a = off;
+    off = align_up(off + (size_t)n_seq * D * N * 4);
+    L.d = off;
+    off = align_up(off + (size_t)n_seq * 2 * D * 4);
+    L.total = off;
+    return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_rmsnorm_fwd(const void *x, int64_t x_st, int x_dtype, const void *residual, int64_t res_st,
+                           int res_dtype, const float *weight, void *out, int64_t out_st, int out_dtype,
+                           void *res_out, int64_t res_out_st, float *scale, int R, int D, int group, float eps,
+                           cudaStream_t stream) {
+    if (R > 0 && (!x || !weight || !out)) return GDN_ERR_NULL;
+    if (R < 0 || D < 1 || D > kNormMaxD || !(eps >= 0.f)) return GDN_ERR_SHAPE;
+    if (!dtype_ok(x_dtype) || (residual && !dtype_ok(res_dtype))) return GDN_ERR_DTYPE;
+    if (out_dtype != GDN_E4M3 && out_dtype != x_dtype) return GDN_ERR_DTYPE;
+    if (R > 0 && ((residual != nullptr) != (res_out != nullptr) || (out_dtype == GDN_E4M3) != (scale != nullptr)))
+        return GDN_ERR_NULL;
+    if (out_dtype == GDN_E4M3 && group != 0 && group != 32 && group != 64 && group != 128 && group != 256)
+        return GDN_ERR_SHAPE;
+    Rows r;
+    r.add(x, x_dtype, 0, x_st);
+    r.add(residual, res_dtype, 0, res_st);
+    r.add(res_out, res_dtype, 0, res_out_st);
+    r.add(out, out_dtype, 0, out_st, out_dtype == GDN_E4M3 ? 8 : 16);
+    r.add(weight, GDN_F32, 0, 0);
+    if (!r.ok || !f32_ok(scale)) return GDN_ERR_LAYOUT;
+    if (R == 0) return GDN_OK;
+    NormParams p{};
+    p.x = x, p.res = residual, p.x_st = x_st, p.res_st = res_st;
+    p.x_bf16 = x_dtype == GDN_BF16, p.res_bf16 = res_dtype == GDN_BF16;
+    p.weight = weight, p.out = out, p.res_out = res_out, p.o_st = out_st, p.ro_st = res_out_st;
+    p.scale = scale, p.R = R, p.D = D, p.group = group, p.eps = eps;
+    p.vec = r.wide && D % 8 == 0;
+    return cuda_status(launch(KNorm, stream, [&] { return launch_rmsnorm(p, stream); }));
+}
+
+size_t gdn_rmsnorm_bwd_workspace_size(int R, int D) {
+    if (R < 0 || D < 1 || D > kNormMaxD) return 0;
+    return align_up((size_t)norm_bwd_parts(R, D) * D * 4) + kAlign;
+}
+
+gdn_status gdn_rmsnorm_bwd(const void *s, int64_t s_st, int s_dtype, const void *dy, int64_t dy_st, int dy_dtype,
+                           const void *dres, int64_t dres_st, const float *weight, void *dx, int64_t dx_st,
+                           float *dweight, int R, int D, float eps, void *workspace, size_t ws_bytes,
+                           cudaStream_t stream) {
+    if (!dweight || (R > 0 && (!s || !dy || !weight || !dx))) return GDN_ERR_NULL;
+    if (R < 0 || D < 1 || D > kNormMaxD || !(eps >= 0.f)) return GDN_ERR_SHAPE;
+    if (!dtype_ok(s_dtype) || !dtype_ok(dy_dtype)) return GDN_ERR_DTYPE;
+    Rows r;
+    r.add(s, s_dtype, 0, s_st);
+    r.add(dy, dy_dtype, 0, dy_st);
+    r.add(dres, s_dtype, 0, dres_st);
+    r.add(dx, s_dtype, 0, dx_st);
+    r.add(weight, GDN_F32, 0, 0);
+    if (!r.ok || !f32_ok(dweight)) return GDN_ERR_LAYOUT;
+    if (!ws_ok(workspace, ws_bytes, gdn_rmsnorm_bwd_workspace_size(R, D))) return GDN_ERR_WORKSPACE;
+    NormBwdParams p{};
+    p.s = s, p.dy = dy, p.dres = dres, p.s_st = s_st, p.dy_st = dy_st, p.dr_st = dres_st;
+    p.s_bf16 = s_dtype == GDN_BF16, p.dy_bf16 = dy_dtype == GDN_BF16;
+    p.weight = weight, p.dx = dx, p.dx_st = dx_st, p.dweight = dweight;
+    p.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + kAlign);
+    p.R = R, p.D = D, p.eps = eps;
+    p.vec = r.wide && D % 8 == 0;
+    cudaError_t e = cudaSuccess;
+    if (R > 0) e = launch(KNormBwd, stream, [&] { return launch_rmsnorm_bwd(p, stream); });
+    if (e == cudaSuccess)
+        e = launch(KColSum, stream, [&] {
+            return launch_col_sum(p.part, D, R > 0 ? norm_bwd_parts(R, D) : 0, D, dweight, 0, nullptr, stream);
+        });
+    return cuda_status(e);
+}
+
+gdn_status gdn_conv_fwd(const void *x, int64_t x_sb, int64_t x_st, const float *weight, int W, const float *bias,
+                        const void *initial_state, const int32_t *cu_seqlens, int n_seq, void *out, int64_t out_sb,
+                        int64_t out_st, void *final_state, int B, int T, int D, int dtype, int flags,
+                        void *workspace, size_t ws_bytes, cudaStream_t stream) {
+    if (!weight || (T > 0 && (!x || !out))) return GDN_ERR_NULL;
+    if (!batch_ok(B, T, D, cu_seqlens, n_seq) || W < 2 || W > kConvMaxW) return GDN_ERR_SHAPE;
+    if (!dtype_ok(dtype)) return GDN_ERR_DTYPE;
+    if (flags & ~GDN_SILU) return GDN_ERR_UNSUPPORTED;
+    Rows r;
+    r.add(x, dtype, x_sb, x_st);
+    r.add(out, dtype, out_sb, out_st);
+    r.add(initial_state, dtype, 0, D);
+    r.add(final_state, dtype, 0, D);
+    r.add(weight, GDN_F32, 0, 0);
+    r.add(bias, GDN_F32, 0, 0);
+    if (!r.ok || !f32_ok(cu_seqlens)) return GDN_ERR_LAYOUT;
+    if (cu_seqlens && !ws_ok(workspace, ws_bytes, kAlign)) return GDN_ERR_WORKSPACE;
+    if (T == 0 && !final_state && !cu_seqlens) return GDN_OK;
+    ConvParams p{};
+    p.x = x, p.x_sb = x_sb, p.x_st = x_st, p.weight = weight, p.bias = bias, p.init = initial_state;
+    p.cu = cu_seqlens, p.n_seq = n_seq, p.out = out, p.o_sb = out_sb, p.o_st = out_st, p.final_state = final_state;
+    p.B = B, p.T = T, p.D = D, p.W = W, p.silu = flags & GDN_SILU, p.bf16 = dtype == GDN_BF16;
+    p.vec = r.wide && D % 8 == 0;
+    p.err = cu_seqlens ? static_cast<int *>(workspace) : nullptr;
+    return cuda_status(launch(KConv, stream, [&] { return launch_conv(p, stream); }));
+}
+
+size_t gdn_conv_bwd_workspace_size(int B, int T, int D, int W) {
+    if (B < 1 || B > 65535 || T < 0 || D < 1 || D > (1 << 20) || W < 2 || W > kConvMaxW) return 0;
+    return align_up((size_t)conv_bwd_parts(B, T) * D * (W + 1) * 4) + kAlign;
+}
+
+gdn_status gdn_conv_bwd(const void *x, int64_t x_sb, int64_t x_st, const float *weight, int W, const float *bias,
+                        const void *initial_state, const int32_t *cu_seqlens, int n_seq, const void *dout,
+                        int64_t dout_sb, int64_t dout_st, const void *dfinal_state, void *dx, float *dweight,
+                        float *dbias, void *dinitial_state, int B, int T, int D, int dtype, int flags,
+                        void *workspace, size_t ws_bytes, cudaStream_t stream) {
+    if (!weight || !dweight || (T > 0 && (!x || !dout || !dx))) return GDN_ERR_NULL;
+    if (!batch_ok(B, T, D, cu_seqlens, n_seq) || W < 2 || W > kConvMaxW) return GDN_ERR_SHAPE;
+    if (!dtype_ok(dtype)) return GDN_ERR_DTYPE;
+    if (flags & ~GDN_SILU) return GDN_ERR_UNSUPPORTED;
+    Rows r;
+    r.add(x, dtype, x_sb, x_st);
+    r.add(dout, dtype, dout_sb, dout_st);
+    r.add(dx, dtype, 0, D);
+    r.add(initial_state, dtype, 0, D);
+    r.add(dfinal_state, dtype, 0, D);
+    r.add(dinitial_state, dtype, 0, D);
+    r.add(weight, GDN_F32, 0, 0);
+    r.add(bias, GDN_F32, 0, 0);
+    if (!r.ok || !f32_ok(cu_seqlens) || !f32_ok(dweight) || !f32_ok(dbias)) return GDN_ERR_LAYOUT;
+    if (!ws_ok(workspace, ws_bytes, gdn_conv_bwd_workspace_size(B, T, D, W))) return GDN_ERR_WORKSPACE;
+    ConvParams p{};
+    p.x = x, p.x_sb = x_sb, p.x_st = x_st, p.weight = weight, p.bias = bias, p.init = initial_state;
+    p.cu = cu_seqlens, p.n_seq = n_seq, p.dout = dout, p.do_sb = dout_sb, p.do_st = dout_st;
+    p.dfinal = dfinal_state, p.dx = dx, p.dinit = dinitial_state, p.dweight = dweight, p.dbias = dbias;
+    p.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + kAlign);
+    p.B = B, p.T = T, p.D = D, p.W = W, p.silu = flags & GDN_SILU, p.bf16 = dtype == GDN_BF16;
+    p.vec = r.wide && D % 8 == 0;
+    p.err = cu_seqlens ? static_cast<int *>(workspace) : nullptr;
+    cudaError_t e = cudaSuccess;
+    if (T > 0 || cu_seqlens || dinitial_state)
+        e = launch(KConvBwd, stream, [&] { return launch_conv_bwd(p, stream); });
+    if (e == cudaSuccess)
+        e = launch(KColSum, stream, [&] {
+            return launch_col_sum(p.part, (int64_t)D * (W + 1), conv_bwd_parts(B, T), (int64_t)D * W, dweight,
+                                  dbias ? D : 0, dbias, stream);
+        });
+    return cuda_status(e);
+}
+
+gdn_status gdn_conv_step(const void *x, int64_t x_st, const float *weight, int W, const float *bias, void *state,
+                         const int32_t *slots, int n_slots, void *out, int64_t out_st, int n, int D, int dtype,
+                         int flags, cudaStream_t stream) {
+    if (n > 0 && (!x || !weight || !out || (n_slots > 0 && !state))) return GDN_ERR_NULL;
+    if (n < 0 || n > 65535 || D < 1 || D > (1 << 20) || W < 2 || W > kConvMaxW || n_slots < 0 ||
+        (!slots && n > n_slots))
+        return GDN_ERR_SHAPE;
+    if (!dtype_ok(dtype)) return GDN_ERR_DTYPE;
+    if (flags & ~GDN_SILU) return GDN_ERR_UNSUPPORTED;
+    Rows r;
+    r.add(x, dtype, 0, x_st);
+    r.add(out, dtype, 0, out_st);
+    r.add(state, dtype, 0, D);
+    r.add(weight, GDN_F32, 0, 0);
+    r.add(bias, GDN_F32, 0, 0);
+    if (!r.ok || !f32_ok(slots)) return GDN_ERR_LAYOUT;
+    if (n == 0) return GDN_OK;
+    ConvStepParams p{};
+    p.x = x, p.x_st = x_st, p.weight = weight, p.bias = bias, p.state = state, p.slots = slots;
+    p.out = out, p.o_st = out_st, p.n = n, p.n_slots = n_slots, p.D = D, p.W = W;
+    p.silu = flags & GDN_SILU, p.bf16 = dtype == GDN_BF16;
+    p.vec = r.wide && D % 8 == 0;
+    return cuda_status(launch(KConvStep, stream, [&] { return launch_conv_step(p, stream); }));
+}
+
+}  // extern "C"
+
+namespace {
+// The checks and the parameter block gdn_ssm_fwd and gdn_ssm_bwd share.
+gdn_status ssm_setup(const void *x, int64_t x_sb, int64_t x_st, const void *dt, int64_t dt_sb, int64_t dt_st,
+                     const float *A, const void *bm, int64_t bm_sb, int64_t bm_st, const void *cm, int64_t cm_sb,
+                     int64_t cm_st, const float *Dv, const void *z, int64_t z_sb, int64_t z_st,
+                     const float *dt_bias, const float *h0, const int32_t *cu, int n_seq, int B, int T, int D, int N,
+                     int dtype, int flags, Rows &r, SsmParams &p) {
+    if (!A || (T > 0 && (!x || !dt || !bm || !cm))) return GDN_ERR_NULL;
+    if (!ssm_shape_ok(B, T, D, N, n_seq, cu != nullptr)) return GDN_ERR_SHAPE;
+    if (!dtype_ok(dtype)) return GDN_ERR_DTYPE;
+    if (flags & ~GDN_SOFTPLUS) return GDN_ERR_UNSUPPORTED;
+    r.add(x, dtype, x_sb, x_st);
+    r.add(dt, dtype, dt_sb, dt_st);
+    r.add(z, dtype, z_sb, z_st);
+    Rows bc;  // (B, T, N) rows are staged by element where they are not wide
+    bc.add(bm, dtype, bm_sb, bm_st);
+    bc.add(cm, dtype, cm_sb, cm_st);
+    if (!r.ok || !bc.ok) return GDN_ERR_LAYOUT;
+    for (const void *f : {(const void *)A, (const void *)Dv, (const void *)dt_bias, (const void *)h0, (const void *)cu})
+        if (!f32_ok(f)) return GDN_ERR_LAYOUT;
+    p = SsmParams{};
+    p.x = x, p.x_sb = x_sb, p.x_st = x_st, p.dt = dt, p.dt_sb = dt_sb, p.dt_st = dt_st;
+    p.bm = bm, p.bm_sb = bm_sb, p.bm_st = bm_st, p.cm = cm, p.cm_sb = cm_sb, p.cm_st = cm_st;
+    p.z = z, p.z_sb = z_sb, p.z_st = z_st, p.A = A, p.Dv = Dv, p.dt_bias = dt_bias, p.h0 = h0;
+    p.cu = cu, p.n_seq = n_seq, p.B = B, p.T = T, p.D = D, p.N = N;
+    p.softplus = flags & GDN_SOFTPLUS, p.bf16 = dtype == GDN_BF16;
+    return GDN_OK;
+}
+}  // namespace
+
+extern "C" {
+
+size_t gdn_ssm_workspace_size(int B, int T, int D, int N, int n_seq, int varlen) {
+    return ssm_shape_ok(B, T, D, N, n_seq, varlen) ? kAlign : 0;
+}
+
+gdn_status gdn_ssm_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *dt, int64_t dt_sb, int64_t dt_st,
+                       const float *A, const void *bm, int64_t bm_sb, int64_t bm_st, const void *cm, int64_t cm_sb,
+                       int64_t cm_st, const float *Dv, const void *z, int64_t z_sb, int64_t z_st,
+                       const float *dt_bias, const float *h0, const int32_t *cu_seqlens, int n_seq, void *out,
+                       int64_t out_sb, int64_t out_st, float *h_final, int B, int T, int D, int N, int dtype,
+                       int flags, void *workspace, size_t ws_bytes, cudaStream_t stream) {
+    Rows r;
+    SsmParams p;
+    if (T > 0 && !out) return GDN_ERR_NULL;
+    r.add(out, dtype, out_sb, out_st);
+    const gdn_status s = ssm_setup(x, x_sb, x_st, dt, dt_sb, dt_st, A, bm, bm_sb, bm_st, cm, cm_sb, cm_st, Dv, z, z_sb,
+                                   z_st, dt_bias, h0, cu_seqlens, n_seq, B, T, D, N, dtype, flags, r, p);
+    if (s != GDN_OK) return s;
+    if (!f32_ok(h_final)) return GDN_ERR_LAYOUT;
+    if (!ws_ok(workspace, ws_bytes, gdn_ssm_workspace_size(B, T, D, N, n_seq, cu_seqlens != nullptr)))
+        return GDN_ERR_WORKSPACE;
+    p.out = out, p.o_sb = out_sb, p.o_st = out_st, p.h_final = h_final;
+    p.err = cu_seqlens ? static_cast<int *>(workspace) : nullptr;
+    return cuda_status(launch(KSsmScan, stream, [&] { return launch_ssm_scan(p, stream); }));
+}
+
+size_t gdn_ssm_bwd_workspace_size(int B, int T, int D, int N, int n_seq, int varlen) {
+    if (!ssm_shape_ok(B, T, D, N, n_seq, varlen)) return 0;
+    return ssm_bwd_ws(B, T, D, N, n_seq, varlen).total;
+}
+
+gdn_status gdn_ssm_bwd(const void *x, int64_t x_sb, int64_t x_st, const void *dt, int64_t dt_sb, int64_t dt_st,
+                       const float *A, const void *bm, int64_t bm_sb, int64_t bm_st, const void *cm, int64_t cm_sb,
+                       int64_t cm_st, const float *Dv, const void *z, int64_t z_sb, int64_t z_st,
+                       const float *dt_bias, const float *h0, const int32_t *cu_seqlens, int n_seq, const void *dout,
+                       int64_t dout_sb, int64_t dout_st, const float *dh_final, void *dx, void *ddt, float *dA,
+                       void *dbm, void *dcm, float *dD, void *dz, float *ddt_bias, float *dh0, int B, int T, int D,
+                       int N, int dtype, int flags, void *workspace, size_t ws_bytes, cudaStream_t stream) {
+    Rows r;
+    SsmParams p;
+    if (!dA || (T > 0 && (!dout || !dx || !ddt || !dbm || !dcm))) return GDN_ERR_NULL;
+    if (dz && !z) return GDN_ERR_NULL;
+    r.add(dout, dtype, dout_sb, dout_st);
+    r.add(dx, dtype, 0, D);
+    r.add(ddt, dtype, 0, D);
+    r.add(dz, dtype, 0, D);
+    const gdn_status s = ssm_setup(x, x_sb, x_st, dt, dt_sb, dt_st, A, bm, bm_sb, bm_st, cm, cm_sb, cm_st, Dv, z, z_sb,
+                                   z_st, dt_bias, h0, cu_seqlens, n_seq, B, T, D, N, dtype, flags, r, p);
+    if (s != GDN_OK) return s;
+    Rows g;
+    g.add(dbm, dtype, 0, N);
+    g.add(dcm, dtype, 0, N);
+    if (!g.ok) return GDN_ERR_LAYOUT;
+    for (const void *f : {(const void *)dh_final, (const void *)dA, (const void *)dD, (const void *)ddt_bias,
+                          (const void *)dh0})
+        if (!f32_ok(f)) return GDN_ERR_LAYOUT;
+    const SsmBwdWs L = ssm_bwd_ws(B, T, D, N, n_seq, cu_seqlens != nullptr);
+    if (!ws_ok(workspace, ws_bytes, L.total)) return GDN_ERR_WORKSPACE;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    p.dout = dout, p.do_sb = dout_sb, p.do_st = dout_st, p.dh_final = dh_final;
+    p.dx = dx, p.ddt = ddt, p.dbm = dbm, p.dcm = dcm, p.dz = dz;
+    p.dA = dA, p.dD = dD, p.ddt_bias = ddt_bias, p.dh0 = dh0;
+    p.ckpt = reinterpret_cast<float *>(ws + L.ckpt);
+    p.part_bc = reinterpret_cast<float *>(ws + L.bc);
+    p.part_a = reinterpret_cast<float *>(ws + L.a);
+    p.part_d = reinterpret_cast<float *>(ws + L.d);
+    p.err = cu_seqlens ? reinterpret_cast<int *>(ws) : nullptr;
+    cudaError_t e = launch(KSsmBwd, stream, [&] { return launch_ssm_bwd(p, stream); });
+    if (e == cudaSuccess && T > 0) e = launch(KSsmBwdReduce, stream, [&] { return launch_ssm_bwd_reduce(p, stream); });
+    const int64_t dn = (int64_t)D * N;
+    if (e == cudaSuccess)
+        e = launch(KColSum, stream, [&] { return launch_col_sum(p.part_a, dn, n_seq, dn, dA, 0, nullptr, stream); });
+    // without dD the bias' columns follow by themselves
+    if (e == cudaSuccess && (dD || ddt_bias))
+        e = launch(KColSum, stream, [&] {
+            return dD ? launch_col_sum(p.part_d, 2 * D, n_seq, D, dD, ddt_bias ? D : 0, ddt_bias, stream)
+                      : launch_col_sum(p.part_d + D, 2 * D, n_seq, D, ddt_bias, 0, nullptr, stream);
+        });
+    return cuda_status(e);
+}
+
+gdn_status gdn_ssm_step(const void *x, int64_t x_st, const void *dt, int64_t dt_st, const float *A, const void *bm,
+                        int64_t bm_st, const void *cm, int64_t cm_st, const float *Dv, const void *z, int64_t z_st,
+                        const float *dt_bias, float *state, const int32_t *slots, int n_slots, void *out,
+                        int64_t out_st, int n, int D, int N, int dtype, int flags, cudaStream_t stream) {
+    if (n > 0 && (!x || !dt || !A || !bm || !cm || !out || (n_slots > 0 && !state))) return GDN_ERR_NULL;
+    if (n < 0 || n > 65535 || D < 1 || D > (1 << 20) || N < 1 || N > kSsmMaxN || n_slots < 0 ||
+        (!slots && n > n_slots))
+        return GDN_ERR_SHAPE;
+    if (!dtype_ok(dtype)) return GDN_ERR_DTYPE;
+    if (flags & ~GDN_SOFTPLUS) return GDN_ERR_UNSUPPORTED;
+    Rows r;
+    r.add(x, dtype, 0, x_st);
+    r.add(dt, dtype, 0, dt_st);
+    r.add(z, dtype, 0, z_st);
+    r.add(out, dtype, 0, out_st);
+    r.add(bm, dtype, 0, bm_st);
+    r.add(cm, dtype, 0, cm_st);
+    if (!r.ok || !f32_ok(A) || !f32_ok(Dv) || !f32_ok(dt_bias) || !f32_ok(state) || !f32_ok(slots))
+        return GDN_ERR_LAYOUT;
+    if (n == 0) return GDN_OK;
+    SsmStepParams p{};
+    p.x = x, p.dt = dt, p.bm = bm, p.cm = cm, p.z = z;
+    p.x_st = x_st, p.dt_st = dt_st, p.bm_st = bm_st, p.cm_st = cm_st, p.z_st = z_st;
+    p.A = A, p.Dv = Dv, p.dt_bias = dt_bias, p.state = state, p.slots = slots, p.out = out, p.o_st = out_st;
+    p.n = n, p.n_slots = n_slots, p.D = D, p.N = N, p.softplus = flags & GDN_SOFTPLUS, p.bf16 = dtype == GDN_BF16;
+    return cuda_status(launch(KSsmStep, stream, [&] { return launch_ssm_step(p, stream); }));
+}
+
+}  // extern "C"

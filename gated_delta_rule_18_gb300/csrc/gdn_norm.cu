@@ -1,0 +1,324 @@
+// gdn_norm.cu -- root-mean-square norm over rows of D channels, with the
+// residual's addition in front and an optional 8-bit output, and its
+// gradient. With s = x + residual (fp32):
+//   inv = 1 / sqrt(mean(s^2) + eps),  y = s inv w,  residual_out = s
+//   8 bits: per group of channels (or per row) scale = max|y| / 448 and
+//   q = e4m3(y / scale), q = 0 where scale = 0.
+// Gradient, for dy and the residual stream's own gradient dres:
+//   ds = inv w dy - s inv^3 mean(w dy s) + dres,  dw = sum over rows dy s inv.
+//
+// Both are bound by HBM: every input is read once and held in registers
+// (a row belongs to tpr threads of one CTA, 8 channels a vector, nv vectors
+// a thread), the row's sum crosses warps once through shared memory, and the
+// result is written once. Sums, the norm and the scales are fp32.
+#include "gdn_layer.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kVecN = 8;
+
+// maximum that keeps NaN, as the comparison with a NaN has to show in the scale
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// two fp32 to two e4m3 (round to nearest even, finite values saturate)
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Threads a row and vectors a thread: one vector a thread up to 512 threads.
+struct RowShape {
+    int tpr, nv, rpb;
+};
+RowShape row_shape(int D, int max_tpr) {
+    const int vecs = (D + kVecN - 1) / kVecN;
+    RowShape s;
+    s.tpr = 32;
+    while (s.tpr < max_tpr && s.tpr < vecs) s.tpr *= 2;
+    s.nv = 1;
+    while (s.nv * s.tpr < vecs) s.nv *= 2;
+    s.rpb = s.tpr >= 128 ? 1 : 128 / s.tpr;
+    return s;
+}
+
+// the row's sum (or NaN-keeping maximum) over its warps; red: a float a warp
+template <bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float *red, int tpr) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float u = __shfl_xor_sync(0xffffffffu, v, o);
+        v = MAX ? max_nan(v, u) : v + u;
+    }
+    if (tpr == 32) return v;
+    const int warp = threadIdx.x >> 5, wpr = tpr >> 5, w0 = warp & ~(wpr - 1);
+    if ((threadIdx.x & 31) == 0) red[warp] = v;
+    __syncthreads();
+    v = red[w0];
+    for (int i = 1; i < wpr; ++i) v = MAX ? max_nan(v, red[w0 + i]) : v + red[w0 + i];
+    return v;
+}
+
+template <typename TX, typename TR, bool Q8, int NV, bool VEC>
+__global__ void __launch_bounds__(512) rmsnorm_kernel(const NormParams p, int tpr) {
+    __shared__ float red[2][16];
+    const int lr = threadIdx.x / tpr, tid = threadIdx.x - lr * tpr;
+    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + lr;
+    const bool live = row < p.R;
+    float s[NV][kVecN];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + tid) * kVecN;
+        if (live && c < p.D) {
+            ld_row_f<TX, kVecN, VEC>(s[i], (const TX *)p.x + row * p.x_st + c, p.D - c);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kVecN; ++j) s[i][j] = 0.f;
+        }
+    }
+    if (p.res) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + tid) * kVecN;
+            if (live && c < p.D) {
+                float r[kVecN];
+                ld_row_f<TR, kVecN, VEC>(r, (const TR *)p.res + row * p.res_st + c, p.D - c);
+#pragma unroll
+                for (int j = 0; j < kVecN; ++j) s[i][j] += r[j];
+                st_row_f<TR, kVecN, VEC>((TR *)p.res_out + row * p.ro_st + c, s[i], p.D - c);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < kVecN; ++j) sum = fmaf(s[i][j], s[i][j], sum);
+    sum = row_reduce<false>(sum, red[0], tpr);
+    const float inv = rsqrtf(sum / (float)p.D + p.eps);
+    float row_max = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + tid) * kVecN;
+        const bool in = live && c < p.D;
+        if (in) {
+            float w[kVecN];
+            ld_row_f<float, kVecN, VEC>(w, p.weight + c, p.D - c);
+#pragma unroll
+            for (int j = 0; j < kVecN; ++j) s[i][j] = s[i][j] * inv * w[j];
+        }
+        if constexpr (!Q8) {
+            if (in) st_row_f<TX, kVecN, VEC>((TX *)p.out + row * p.o_st + c, s[i], p.D - c);
+        } else {
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < kVecN; ++j) m = max_nan(m, fabsf(s[i][j]));
+            row_max = max_nan(row_max, m);
+            if (p.group > 0) {
+                // a group's vectors sit in group / 8 neighbouring lanes
+                for (int o = p.group / kVecN / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const float sc = m / 448.f;
+                if (in) {
+                    if (c % p.group == 0) p.scale[row * ((p.D + p.group - 1) / p.group) + c / p.group] = sc;
+                    const float dv = sc == 0.f ? 1.f : sc;
+#pragma unroll
+                    for (int j = 0; j < kVecN; ++j) s[i][j] = s[i][j] / dv;
+                }
+            }
+        }
+    }
+    if constexpr (Q8) {
+        if (p.group == 0) {
+            const float sc = row_reduce<true>(row_max, red[1], tpr) / 448.f;
+            if (live && tid == 0) p.scale[row] = sc;
+            const float dv = sc == 0.f ? 1.f : sc;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < kVecN; ++j) s[i][j] = s[i][j] / dv;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + tid) * kVecN;
+            if (!(live && c < p.D)) continue;
+            uint32_t q[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                q[j] = pack_e4m3(s[i][4 * j], s[i][4 * j + 1]) | pack_e4m3(s[i][4 * j + 2], s[i][4 * j + 3]) << 16;
+            uint8_t *o = (uint8_t *)p.out + row * p.o_st + c;
+            if constexpr (VEC) {
+                st_words(o, q);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVecN; ++j)
+                    if (c + j < p.D) o[j] = (uint8_t)(q[j >> 2] >> (8 * (j & 3)));
+            }
+        }
+    }
+}
+
+// One CTA walks rows blockIdx, blockIdx + grid, ...; a thread keeps its
+// channels' share of dw and writes it once, so dw is summed in a fixed order.
+template <typename TS, typename TY, int NV, bool VEC>
+__global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdParams p, int tpr) {
+    __shared__ float red[2][2][16];
+    const int rpb = blockDim.x / tpr;
+    const int lr = threadIdx.x / tpr, tid = threadIdx.x - lr * tpr;
+    float dw[NV][kVecN], w[NV][kVecN];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + tid) * kVecN;
+#pragma unroll
+        for (int j = 0; j < kVecN; ++j) dw[i][j] = 0.f, w[i][j] = 0.f;
+        if (c < p.D) ld_row_f<float, kVecN, VEC>(w[i], p.weight + c, p.D - c);
+    }
+    const float rd = 1.f / (float)p.D;
+    int flip = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < p.R; r0 += (int64_t)gridDim.x * rpb, flip ^= 1) {
+        const int64_t row = r0 + lr;
+        const bool live = row < p.R;
+        float s[NV][kVecN], g[NV][kVecN];
+        float ss = 0.f, gs = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + tid) * kVecN;
+            if (live && c < p.D) {
+                ld_row_f<TS, kVecN, VEC>(s[i], (const TS *)p.s + row * p.s_st + c, p.D - c);
+                ld_row_f<TY, kVecN, VEC>(g[i], (const TY *)p.dy + row * p.dy_st + c, p.D - c);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVecN; ++j) s[i][j] = 0.f, g[i][j] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < kVecN; ++j) {
+                ss = fmaf(s[i][j], s[i][j], ss);
+                gs = fmaf(g[i][j] * w[i][j], s[i][j], gs);
+            }
+        ss = warp_sum(ss), gs = warp_sum(gs);
+        if (tpr > 32) {
+            const int warp = threadIdx.x >> 5, wpr = tpr >> 5, w0 = warp & ~(wpr - 1);
+            if ((threadIdx.x & 31) == 0) red[flip][0][warp] = ss, red[flip][1][warp] = gs;
+            __syncthreads();
+            ss = red[flip][0][w0], gs = red[flip][1][w0];
+            for (int i = 1; i < wpr; ++i) ss += red[flip][0][w0 + i], gs += red[flip][1][w0 + i];
+        }
+        const float inv = rsqrtf(ss * rd + p.eps);
+        const float k = inv * inv * inv * (gs * rd);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + tid) * kVecN;
+            if (!(live && c < p.D)) continue;
+            float o[kVecN];
+            if (p.dres) {
+                ld_row_f<TS, kVecN, VEC>(o, (const TS *)p.dres + row * p.dr_st + c, p.D - c);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVecN; ++j) o[j] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < kVecN; ++j) {
+                o[j] += inv * (g[i][j] * w[i][j]) - s[i][j] * k;
+                dw[i][j] = fmaf(g[i][j], s[i][j] * inv, dw[i][j]);
+            }
+            st_row_f<TS, kVecN, VEC>((TS *)p.dx + row * p.dx_st + c, o, p.D - c);
+        }
+    }
+    float *part = p.part + ((int64_t)blockIdx.x * rpb + lr) * p.D;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + tid) * kVecN;
+        if (c < p.D) st_row_f<float, kVecN, VEC>(part + c, dw[i], p.D - c);
+    }
+}
+
+// 32 columns a CTA, 8 threads a column.
+__global__ void __launch_bounds__(256) col_sum_kernel(const float *in, int64_t ld, int parts, int64_t n, float *out,
+                                                      int64_t n2, float *out2) {
+    __shared__ float red[8][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + x;
+    float a = 0.f;
+    if (c < n + n2)
+        for (int p = y; p < parts; p += 8) a += in[p * ld + c];
+    red[y][x] = a;
+    __syncthreads();
+    if (y == 0 && c < n + n2) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) a += red[i][x];
+        float *o = c < n ? out + c : out2 + (c - n);
+        *o = a;
+    }
+}
+
+template <typename TX, typename TR, bool Q8>
+cudaError_t norm_nv(const NormParams &p, cudaStream_t st) {
+    const RowShape s = row_shape(p.D, 512);
+    const unsigned grid = (unsigned)((p.R + s.rpb - 1) / s.rpb), nt = s.tpr * s.rpb;
+    if (!p.vec) {
+        rmsnorm_kernel<TX, TR, Q8, 4, false><<<grid, nt, 0, st>>>(p, s.tpr);
+    } else if (s.nv == 1) {
+        rmsnorm_kernel<TX, TR, Q8, 1, true><<<grid, nt, 0, st>>>(p, s.tpr);
+    } else if (s.nv == 2) {
+        rmsnorm_kernel<TX, TR, Q8, 2, true><<<grid, nt, 0, st>>>(p, s.tpr);
+    } else {
+        rmsnorm_kernel<TX, TR, Q8, 4, true><<<grid, nt, 0, st>>>(p, s.tpr);
+    }
+    return cudaGetLastError();
+}
+template <typename TS, typename TY>
+cudaError_t norm_bwd_nv(const NormBwdParams &p, cudaStream_t st) {
+    const RowShape s = row_shape(p.D, 512);
+    const unsigned grid = norm_bwd_parts(p.R, p.D) / s.rpb, nt = s.tpr * s.rpb;
+    if (!p.vec) {
+        rmsnorm_bwd_kernel<TS, TY, 4, false><<<grid, nt, 0, st>>>(p, s.tpr);
+    } else if (s.nv == 1) {
+        rmsnorm_bwd_kernel<TS, TY, 1, true><<<grid, nt, 0, st>>>(p, s.tpr);
+    } else if (s.nv == 2) {
+        rmsnorm_bwd_kernel<TS, TY, 2, true><<<grid, nt, 0, st>>>(p, s.tpr);
+    } else {
+        rmsnorm_bwd_kernel<TS, TY, 4, true><<<grid, nt, 0, st>>>(p, s.tpr);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm(const NormParams &p, cudaStream_t st) {
+    using bf = __nv_bfloat16;
+    const bool rb = p.res ? p.res_bf16 : p.x_bf16;
+    if (p.scale) {
+        if (p.x_bf16) return rb ? norm_nv<bf, bf, true>(p, st) : norm_nv<bf, float, true>(p, st);
+        return rb ? norm_nv<float, bf, true>(p, st) : norm_nv<float, float, true>(p, st);
+    }
+    if (p.x_bf16) return rb ? norm_nv<bf, bf, false>(p, st) : norm_nv<bf, float, false>(p, st);
+    return rb ? norm_nv<float, bf, false>(p, st) : norm_nv<float, float, false>(p, st);
+}
+
+// Rows of partial sums: at most four CTAs a SM, each rpb rows at a time.
+int norm_bwd_parts(int R, int D) {
+    const RowShape s = row_shape(D, 512);
+    const int need = (int)(((int64_t)R + s.rpb - 1) / s.rpb);
+    return (need < 608 ? need : 608) * s.rpb;
+}
+
+cudaError_t launch_rmsnorm_bwd(const NormBwdParams &p, cudaStream_t st) {
+    using bf = __nv_bfloat16;
+    if (p.s_bf16) return p.dy_bf16 ? norm_bwd_nv<bf, bf>(p, st) : norm_bwd_nv<bf, float>(p, st);
+    return p.dy_bf16 ? norm_bwd_nv<float, bf>(p, st) : norm_bwd_nv<float, float>(p, st);
+}
+
+cudaError_t launch_col_sum(const float *in, int64_t ld, int parts, int64_t n, float *out, int64_t n2, float *out2,
+                           cudaStream_t st) {
+    if (n + n2 <= 0) return cudaSuccess;
+    col_sum_kernel<<<(unsigned)((n + n2 + 31) / 32), 256, 0, st>>>(in, ld, parts, n, out, n2, out2);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

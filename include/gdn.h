@@ -61,7 +61,7 @@ typedef enum {
     GDN_ERR_DEVICE = 9       /* a device-side argument check failed */
 } gdn_status;
 
-typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
+typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_E4M3 = 2 /* gdn_rmsnorm_fwd's output only */ } gdn_dtype;
 
 /* Element strides of a (B, T, H, D) view; D is contiguous (stride 1). */
 typedef struct {
@@ -486,6 +486,178 @@ gdn_status gdn_frame_fwd(const void *q, const void *k, gdn_tensor_desc qkd,
                          int B, int T, int H, int K, int V, int frame,
                          int direction, int flags, void *workspace,
                          size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * The state-space layer beside the scan: the residual norm in front of a
+ * mixer, the short causal convolution in front of a scan, and the selective
+ * (diagonal) state-space scan, each for prompts, single tokens and training.
+ * Conventions are those above; besides:
+ *   - Activations are (B, T, D) or, for norms and single tokens, rows (R, D);
+ *     each tensor's strides are int64 arguments in elements (name_sb over B,
+ *     name_st over T or rows), non-negative, D contiguous. Rows may start at
+ *     any multiple of the element size and D may be any number: rows and
+ *     strides that keep 16-byte alignment run wide accesses, others element
+ *     accesses. All activations of a call share `dtype` unless said.
+ *   - Parameters (weights, A, D, biases) and scan states are fp32,
+ *     contiguous, 4-byte aligned.
+ *   - Packed batches: cu_seqlens as for gdn_chunk_fwd (B == 1; sequences may
+ *     be empty). A malformed cu_seqlens gives wrong values but no access out
+ *     of range, and is reported as GDN_DEVERR_SEQLENS in the workspace's
+ *     first word (gdn_last_device_error), where the call has a workspace.
+ *   - slots: int32 (n), the pool row of each request's state, distinct; a
+ *     request whose slot is not in [0, n_slots) is a padding row: its output
+ *     is zero and no state changes. NULL: request i uses row i.
+ */
+
+/* flags */
+#define GDN_SILU 0x1      /* gdn_conv_*: SiLU after the convolution */
+#define GDN_SOFTPLUS 0x1  /* gdn_ssm_*: delta = softplus(dt + dt_bias) */
+
+/*
+ * gdn_rmsnorm_fwd -- residual RMS norm, optionally with an 8-bit output:
+ *   s = x + residual (fp32; s = x without one), inv = 1 / sqrt(mean(s^2) +
+ *   eps), y = s inv weight; res_out = s rounded to the residual's type.
+ *   x: (R, D), x_dtype. residual, res_out: (R, D), res_dtype, both or neither
+ *   NULL; res_out may be residual itself. out: (R, D) of x's dtype, scale
+ *   NULL; or GDN_E4M3 with scale (R, ceil(D / group)) fp32, contiguous:
+ *     scale = max|y| / 448 over the group's channels, out = e4m3(y / scale),
+ *     and 0 where scale is 0. group: 32, 64, 128, 256, or 0 for the row.
+ *   D <= 16384. (The survey's RMSNorm rows: SANA `fused_gdn.py` page,
+ *   `_precompute_inv_rms`; the mamba-rs page's `rmsnorm_bwd`.)
+ */
+gdn_status gdn_rmsnorm_fwd(const void *x, int64_t x_st, int x_dtype,
+                           const void *residual, int64_t res_st, int res_dtype,
+                           const float *weight, void *out, int64_t out_st,
+                           int out_dtype, void *res_out, int64_t res_out_st,
+                           float *scale, int R, int D, int group, float eps,
+                           cudaStream_t stream);
+
+/*
+ * gdn_rmsnorm_bwd -- the gradient of the norm for the stored sum s:
+ *   dx = inv weight dy - s inv^3 mean(weight dy s) + dres,
+ *   dweight = sum over rows of dy s inv (fp32, in a fixed order).
+ *   s, dres (or NULL), dx: (R, D), s_dtype; dy: (R, D), dy_dtype. dx is the
+ *   gradient of s: of x and of the residual alike.
+ *   workspace: gdn_rmsnorm_bwd_workspace_size(R, D) bytes, 256-byte aligned.
+ */
+size_t gdn_rmsnorm_bwd_workspace_size(int R, int D);
+gdn_status gdn_rmsnorm_bwd(const void *s, int64_t s_st, int s_dtype,
+                           const void *dy, int64_t dy_st, int dy_dtype,
+                           const void *dres, int64_t dres_st,
+                           const float *weight, void *dx, int64_t dx_st,
+                           float *dweight, int R, int D, float eps,
+                           void *workspace, size_t ws_bytes,
+                           cudaStream_t stream);
+
+/*
+ * gdn_conv_fwd -- causal depthwise convolution of W taps (the short
+ * convolution before the scan: hyper-parallel coverage_diff page,
+ * `causal_conv1d`, and its packed-sequence halo):
+ *   p_t = bias + sum_j weight[:, j] x_{t - W + 1 + j}, out = silu(p) or p.
+ *   weight (D, W), bias (D) or NULL; W from 2 to 8.
+ *   initial_state, final_state: (n_seq, W - 1, D) of `dtype`, contiguous, or
+ *   NULL: the W - 1 inputs before the sequence (zero without), oldest first,
+ *   and the last W - 1 inputs after it.
+ *   workspace: 256 bytes, needed with cu_seqlens only.
+ */
+gdn_status gdn_conv_fwd(const void *x, int64_t x_sb, int64_t x_st,
+                        const float *weight, int W, const float *bias,
+                        const void *initial_state, const int32_t *cu_seqlens,
+                        int n_seq, void *out, int64_t out_sb, int64_t out_st,
+                        void *final_state, int B, int T, int D, int dtype,
+                        int flags, void *workspace, size_t ws_bytes,
+                        cudaStream_t stream);
+
+/*
+ * gdn_conv_bwd -- its gradient for L = sum(dout . out) + sum(dfinal_state .
+ * final_state). dx (B, T, D) and dinitial_state (n_seq, W - 1, D, or NULL)
+ * in `dtype`, contiguous; dweight (D, W) and dbias (D, or NULL) fp32, summed
+ * in a fixed order. Other arguments as for gdn_conv_fwd.
+ *   workspace: gdn_conv_bwd_workspace_size(B, T, D, W) bytes.
+ */
+size_t gdn_conv_bwd_workspace_size(int B, int T, int D, int W);
+gdn_status gdn_conv_bwd(const void *x, int64_t x_sb, int64_t x_st,
+                        const float *weight, int W, const float *bias,
+                        const void *initial_state, const int32_t *cu_seqlens,
+                        int n_seq, const void *dout, int64_t dout_sb,
+                        int64_t dout_st, const void *dfinal_state, void *dx,
+                        float *dweight, float *dbias, void *dinitial_state,
+                        int B, int T, int D, int dtype, int flags,
+                        void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * gdn_conv_step -- one token of n requests: out from the request's window
+ * and x (n, D), and the window shifted by x in place. state: (n_slots, W - 1,
+ * D) of `dtype`, contiguous.
+ */
+gdn_status gdn_conv_step(const void *x, int64_t x_st, const float *weight,
+                         int W, const float *bias, void *state,
+                         const int32_t *slots, int n_slots, void *out,
+                         int64_t out_st, int n, int D, int dtype, int flags,
+                         cudaStream_t stream);
+
+/*
+ * gdn_ssm_fwd -- the selective state-space scan (the mamba-rs page's layer,
+ * whose backward calls `ssm_backward_local` / `ssm_parallel_bwd`), per
+ * channel d and state n, per sequence:
+ *   delta = softplus(dt + dt_bias) (GDN_SOFTPLUS; else dt + dt_bias)
+ *   h_t = exp(delta A) h_{t-1} + delta x B_n          (fp32)
+ *   out = (sum_n C_n h_t + D x) silu(z)
+ *   x, dt, out: (B, T, D); bm, cm: (B, T, N), shared by the channels; A
+ *   (D, N), normally negative; Dv (D), z (B, T, D), dt_bias (D) or NULL.
+ *   h0, h_final: (n_seq, D, N) fp32 or NULL. N <= 128.
+ *   workspace: gdn_ssm_workspace_size(B, T, D, N, n_seq, varlen) bytes.
+ */
+size_t gdn_ssm_workspace_size(int B, int T, int D, int N, int n_seq,
+                              int varlen);
+gdn_status gdn_ssm_fwd(const void *x, int64_t x_sb, int64_t x_st,
+                       const void *dt, int64_t dt_sb, int64_t dt_st,
+                       const float *A, const void *bm, int64_t bm_sb,
+                       int64_t bm_st, const void *cm, int64_t cm_sb,
+                       int64_t cm_st, const float *Dv, const void *z,
+                       int64_t z_sb, int64_t z_st, const float *dt_bias,
+                       const float *h0, const int32_t *cu_seqlens, int n_seq,
+                       void *out, int64_t out_sb, int64_t out_st,
+                       float *h_final, int B, int T, int D, int N, int dtype,
+                       int flags, void *workspace, size_t ws_bytes,
+                       cudaStream_t stream);
+
+/*
+ * gdn_ssm_bwd -- its gradients for L = sum(dout . out) + sum(dh_final .
+ * h_final); the forward is recomputed. dx, ddt, dz (B, T, D) and dbm, dcm
+ * (B, T, N) in `dtype`, contiguous; dA (D, N), dD (D), ddt_bias (D), dh0
+ * (n_seq, D, N) fp32. dD, dz, ddt_bias and dh0 may be NULL; dz needs z. Every
+ * sum has a fixed order: results repeat bit for bit.
+ *   workspace: gdn_ssm_bwd_workspace_size(B, T, D, N, n_seq, varlen) bytes.
+ */
+size_t gdn_ssm_bwd_workspace_size(int B, int T, int D, int N, int n_seq,
+                                  int varlen);
+gdn_status gdn_ssm_bwd(const void *x, int64_t x_sb, int64_t x_st,
+                       const void *dt, int64_t dt_sb, int64_t dt_st,
+                       const float *A, const void *bm, int64_t bm_sb,
+                       int64_t bm_st, const void *cm, int64_t cm_sb,
+                       int64_t cm_st, const float *Dv, const void *z,
+                       int64_t z_sb, int64_t z_st, const float *dt_bias,
+                       const float *h0, const int32_t *cu_seqlens, int n_seq,
+                       const void *dout, int64_t dout_sb, int64_t dout_st,
+                       const float *dh_final, void *dx, void *ddt, float *dA,
+                       void *dbm, void *dcm, float *dD, void *dz,
+                       float *ddt_bias, float *dh0, int B, int T, int D, int N,
+                       int dtype, int flags, void *workspace, size_t ws_bytes,
+                       cudaStream_t stream);
+
+/*
+ * gdn_ssm_step -- one token of n requests of the scan; state (n_slots, D, N)
+ * fp32, updated in place. x, dt, z, out (n, D); bm, cm (n, N).
+ */
+gdn_status gdn_ssm_step(const void *x, int64_t x_st, const void *dt,
+                        int64_t dt_st, const float *A, const void *bm,
+                        int64_t bm_st, const void *cm, int64_t cm_st,
+                        const float *Dv, const void *z, int64_t z_st,
+                        const float *dt_bias, float *state,
+                        const int32_t *slots, int n_slots, void *out,
+                        int64_t out_st, int n, int D, int N, int dtype,
+                        int flags, cudaStream_t stream);
 
 const char *gdn_status_string(gdn_status s);
 
