@@ -163,9 +163,15 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormParams p, int tp
 
 // One CTA walks rows blockIdx, blockIdx + grid, ...; a thread keeps its
 // channels' share of dw and writes it once, so dw is summed in a fixed order.
-template <typename TS, typename TY, int NV, bool VEC>
+// A channel's own terms cancel exactly between the two parts of ds (they are
+// all there is when one channel dominates its row), so both sums lose them
+// first: with S = sum s^2, G = sum w dy s,
+//   ds_i = inv [ inv^2 / D (w dy_i (S - s_i^2) - s_i (G - w dy_i s_i)) + eps inv^2 w dy_i ].
+// PRE: the next row's loads are issued before this row's sum is known.
+template <typename TS, typename TY, int NV, bool VEC, bool PRE>
 __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdParams p, int tpr) {
     __shared__ float red[2][2][16];
+    constexpr int WS = RowVec<TS, kVecN>::kWords, WY = RowVec<TY, kVecN>::kWords;
     const int rpb = blockDim.x / tpr;
     const int lr = threadIdx.x / tpr, tid = threadIdx.x - lr * tpr;
     float dw[NV][kVecN], w[NV][kVecN];
@@ -176,31 +182,52 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdParams p,
         for (int j = 0; j < kVecN; ++j) dw[i][j] = 0.f, w[i][j] = 0.f;
         if (c < p.D) ld_row_f<float, kVecN, VEC>(w[i], p.weight + c, p.D - c);
     }
-    const float rd = 1.f / (float)p.D;
-    int flip = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < p.R; r0 += (int64_t)gridDim.x * rpb, flip ^= 1) {
-        const int64_t row = r0 + lr;
-        const bool live = row < p.R;
-        float s[NV][kVecN], g[NV][kVecN];
-        float ss = 0.f, gs = 0.f;
+    const int64_t step = (int64_t)gridDim.x * rpb;
+    int64_t row = (int64_t)blockIdx.x * rpb + lr;
+    uint32_t ns[NV][WS], ny[NV][WY], nr[NV][WS];
+    auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + tid) * kVecN;
-            if (live && c < p.D) {
-                ld_row_f<TS, kVecN, VEC>(s[i], (const TS *)p.s + row * p.s_st + c, p.D - c);
-                ld_row_f<TY, kVecN, VEC>(g[i], (const TY *)p.dy + row * p.dy_st + c, p.D - c);
+            if (r < p.R && c < p.D) {
+                ld_row<TS, kVecN, VEC>(ns[i], (const TS *)p.s + r * p.s_st + c, p.D - c);
+                ld_row<TY, kVecN, VEC>(ny[i], (const TY *)p.dy + r * p.dy_st + c, p.D - c);
+                if (p.dres) ld_row<TS, kVecN, VEC>(nr[i], (const TS *)p.dres + r * p.dr_st + c, p.D - c);
             } else {
 #pragma unroll
-                for (int j = 0; j < kVecN; ++j) s[i][j] = 0.f, g[i][j] = 0.f;
+                for (int j = 0; j < WS; ++j) ns[i][j] = 0u;
+#pragma unroll
+                for (int j = 0; j < WY; ++j) ny[i][j] = 0u;
             }
         }
+    };
+    if (PRE) fetch(row);
+    const float rd = 1.f / (float)p.D;
+    int flip = 0;
+    // every thread of the CTA makes the same number of turns
+    for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < p.R; r0 += step, row += step, flip ^= 1) {
+        if (!PRE) fetch(row);
+        uint32_t rs[NV][WS], ry[NV][WY], rr[NV][WS];
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int j = 0; j < WS; ++j) rs[i][j] = ns[i][j], rr[i][j] = nr[i][j];
+#pragma unroll
+            for (int j = 0; j < WY; ++j) ry[i][j] = ny[i][j];
+        }
+        if (PRE) fetch(row + step);
+        float ss = 0.f, gs = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float s[kVecN], g[kVecN];
+            words_to_f<TS, kVecN>(s, rs[i]);
+            words_to_f<TY, kVecN>(g, ry[i]);
 #pragma unroll
             for (int j = 0; j < kVecN; ++j) {
-                ss = fmaf(s[i][j], s[i][j], ss);
-                gs = fmaf(g[i][j] * w[i][j], s[i][j], gs);
+                ss += __fmul_rn(s[j], s[j]);
+                gs += __fmul_rn(g[j] * w[i][j], s[j]);
             }
+        }
         ss = warp_sum(ss), gs = warp_sum(gs);
         if (tpr > 32) {
             const int warp = threadIdx.x >> 5, wpr = tpr >> 5, w0 = warp & ~(wpr - 1);
@@ -210,22 +237,26 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdParams p,
             for (int i = 1; i < wpr; ++i) ss += red[flip][0][w0 + i], gs += red[flip][1][w0 + i];
         }
         const float inv = rsqrtf(ss * rd + p.eps);
-        const float k = inv * inv * inv * (gs * rd);
+        const float k = inv * inv * rd, ke = p.eps * inv * inv;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + tid) * kVecN;
-            if (!(live && c < p.D)) continue;
-            float o[kVecN];
+            if (!(row < p.R && c < p.D)) continue;
+            float s[kVecN], g[kVecN], o[kVecN];
+            words_to_f<TS, kVecN>(s, rs[i]);
+            words_to_f<TY, kVecN>(g, ry[i]);
             if (p.dres) {
-                ld_row_f<TS, kVecN, VEC>(o, (const TS *)p.dres + row * p.dr_st + c, p.D - c);
+                words_to_f<TS, kVecN>(o, rr[i]);
             } else {
 #pragma unroll
                 for (int j = 0; j < kVecN; ++j) o[j] = 0.f;
             }
 #pragma unroll
             for (int j = 0; j < kVecN; ++j) {
-                o[j] += inv * (g[i][j] * w[i][j]) - s[i][j] * k;
-                dw[i][j] = fmaf(g[i][j], s[i][j] * inv, dw[i][j]);
+                const float gw = g[j] * w[i][j];
+                const float rest = gw * (ss - __fmul_rn(s[j], s[j])) - s[j] * (gs - __fmul_rn(gw, s[j]));
+                o[j] += inv * fmaf(k, rest, ke * gw);
+                dw[i][j] = fmaf(g[j], s[j] * inv, dw[i][j]);
             }
             st_row_f<TS, kVecN, VEC>((TS *)p.dx + row * p.dx_st + c, o, p.D - c);
         }
@@ -277,13 +308,13 @@ cudaError_t norm_bwd_nv(const NormBwdParams &p, cudaStream_t st) {
     const RowShape s = row_shape(p.D, 512);
     const unsigned grid = norm_bwd_parts(p.R, p.D) / s.rpb, nt = s.tpr * s.rpb;
     if (!p.vec) {
-        rmsnorm_bwd_kernel<TS, TY, 4, false><<<grid, nt, 0, st>>>(p, s.tpr);
+        rmsnorm_bwd_kernel<TS, TY, 4, false, false><<<grid, nt, 0, st>>>(p, s.tpr);
     } else if (s.nv == 1) {
-        rmsnorm_bwd_kernel<TS, TY, 1, true><<<grid, nt, 0, st>>>(p, s.tpr);
+        rmsnorm_bwd_kernel<TS, TY, 1, true, true><<<grid, nt, 0, st>>>(p, s.tpr);
     } else if (s.nv == 2) {
-        rmsnorm_bwd_kernel<TS, TY, 2, true><<<grid, nt, 0, st>>>(p, s.tpr);
+        rmsnorm_bwd_kernel<TS, TY, 2, true, false><<<grid, nt, 0, st>>>(p, s.tpr);
     } else {
-        rmsnorm_bwd_kernel<TS, TY, 4, true><<<grid, nt, 0, st>>>(p, s.tpr);
+        rmsnorm_bwd_kernel<TS, TY, 4, true, false><<<grid, nt, 0, st>>>(p, s.tpr);
     }
     return cudaGetLastError();
 }

@@ -1,0 +1,498 @@
+"""The state-space layer's operators on the GPU against plain fp64 forms.
+
+Tolerances, as max|got - ref| / max|ref|, fixed from the arithmetic:
+  * bf16 results: one rounding, half a unit in the last place of 8 bits is
+    2^-9 of the value; twice that for results that meet cancellation after an
+    fp32 sum: 2^-8.
+  * fp32 results of the norm and the convolution: sums of at most D or T
+    terms, each with an error of a few 2^-24, pairwise or in chains of at most
+    a few thousand: 2e-5.
+  * fp32 results of the scan: a step's relative error is a few 2^-24 (the
+    exponential of an fp32 product, one multiply-add), and a state remembers
+    at most 1/(1 - a) ~ 1e3 steps here: 1e3 * 2 * 2^-24 = 1.2e-4.
+  * central differences of an fp32 loss with step h: checked in fp64 on the
+    reference; the kernels' gradients are compared with them at 1e-3.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_18_gb300 as gdn
+
+pytestmark = pytest.mark.gpu
+
+BF, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+TOL_BF, TOL_F32, TOL_SCAN = 2.0**-8, 2e-5, 1.2e-4
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    assert torch.cuda.is_available(), "the gpu tests need a CUDA device"
+    from gated_delta_rule_18_gb300.build import build
+    build()
+
+
+def rel(got, ref):
+    got, ref = got.detach().to("cpu", F64), ref.detach().to("cpu", F64)
+    assert got.shape == ref.shape, (got.shape, ref.shape)
+    if ref.numel() == 0:
+        return 0.0
+    assert torch.isfinite(got).all()
+    scale = ref.abs().max().item()
+    return (got - ref).abs().max().item() / (scale if scale > 0 else 1.0)
+
+
+def randn(shape, dtype=F32, seed=0, std=1.0, mean=0.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * std + mean).to(dtype)
+
+
+def dev(t):
+    return None if t is None else t.to(DEV)
+
+
+def f64(t):
+    return None if t is None else t.to("cpu", F64)
+
+
+def strided(t, lead=3, tail=5):
+    """The same values as a slice of wider rows (odd offsets and strides)."""
+    big = torch.zeros(t.shape[:-1] + (t.shape[-1] + lead + tail,), dtype=t.dtype, device=t.device)
+    big[..., lead:lead + t.shape[-1]] = t
+    return big[..., lead:lead + t.shape[-1]]
+
+
+# ------------------------------------------------------------------ norm ---
+
+
+def ref_norm(x, w, res, eps):
+    s = f64(x) if res is None else f64(x) + f64(res)
+    return s, s / torch.sqrt(s.square().mean(-1, keepdim=True) + eps) * f64(w)
+
+
+@pytest.mark.parametrize("rows,D", [(1, 1), (3, 7), (5, 64), (1, 2048), (70, 100), (9, 1000), (33, 4096), (2, 5000),
+                                    (3, 16384), (130, 72)])
+@pytest.mark.parametrize("dtype,res", [(BF, None), (BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+def test_norm(rows, D, dtype, res):
+    x, w = randn((rows, D), dtype, 1), randn((D,), F32, 2, 0.1, 1.0)
+    r = None if res is None else randn((rows, D), res, 3, 2.0)
+    s, y = ref_norm(x, w, r, 1e-6)
+    got = gdn.gdn_rmsnorm_fwd(dev(x), dev(w), residual=dev(r))
+    assert got["out"].dtype == dtype
+    assert rel(got["out"], y) <= (TOL_BF if dtype == BF else TOL_F32)
+    if res is not None:
+        assert rel(got["residual"], s) <= (TOL_BF if res == BF else TOL_F32)
+
+
+@pytest.mark.parametrize("group", [0, 32, 64, 128, 256])
+@pytest.mark.parametrize("D", [24, 100, 384, 1001, 4096, 16384])
+def test_norm_e4m3(D, group):
+    rows = 5
+    x, w, r = randn((rows, D), BF, 4), randn((D,), F32, 5, 0.1, 1.0), randn((rows, D), F32, 6)
+    x[1], r[1] = 0, 0  # a row of zeros: scale 0, output 0
+    _, y = ref_norm(x, w, r, 1e-6)
+    got = gdn.gdn_rmsnorm_fwd(dev(x), dev(w), residual=dev(r), out_dtype=torch.float8_e4m3fn, group=group)
+    g = group or D
+    pad = torch.nn.functional.pad(y, (0, -D % g)).view(rows, -1, g)
+    scale = pad.abs().amax(-1) / 448
+    assert got["scale"].shape == scale.shape
+    assert rel(got["scale"], scale) <= TOL_F32
+    assert (got["scale"][1] == 0).all() and (got["out"][1].float() == 0).all()
+    back = torch.nn.functional.pad(got["out"].to("cpu", F32).to(F64), (0, -D % g)).view(rows, -1, g) * scale[..., None]
+    # half an e4m3 step: 2^-4 of the value, or half the smallest step 2^-9 of the scale
+    assert ((back - pad).abs() <= 2.0**-4 * 1.0001 * pad.abs() + scale[..., None] * 2.0**-10).all()
+
+
+def test_norm_shapes_strides_and_in_place_residual():
+    x, w, r = randn((2, 7, 100), BF, 7), randn((100,), F32, 8, 0.1, 1.0), randn((2, 7, 100), BF, 9)
+    _, y = ref_norm(x, w, r, 1e-5)
+    rr = dev(r)
+    got = gdn.gdn_rmsnorm_fwd(strided(dev(x)), dev(w), residual=rr, residual_out=rr, eps=1e-5)
+    assert got["residual"].data_ptr() == rr.data_ptr()
+    assert rel(got["out"], y) <= TOL_BF and rel(rr, f64(x) + f64(r)) <= TOL_BF
+    assert gdn.gdn_rmsnorm_fwd(dev(x)[:0], dev(w))["out"].shape == (0, 7, 100)
+
+
+def test_norm_non_finite_rows_stay_apart():
+    x, w = randn((4, 256), F32, 10), torch.ones(256)
+    x[1, 3], x[2, 5] = float("nan"), float("inf")
+    got = gdn.gdn_rmsnorm_fwd(dev(x), dev(w), out_dtype=torch.float8_e4m3fn, group=64)
+    assert got["scale"][1].isnan().all() and got["out"][1].float().isnan().all()
+    assert got["scale"][2, 0].isnan() and (got["scale"][2, 1:] == 0).all()
+    assert got["scale"][[0, 3]].isfinite().all() and got["out"][[0, 3]].float().isfinite().all()
+
+
+@pytest.mark.parametrize("rows,D", [(1, 1), (3, 7), (700, 64), (1, 2048), (1300, 100), (9, 1000), (40, 4096),
+                                    (3, 16384), (2, 9001)])
+@pytest.mark.parametrize("ds,dy,dr", [(BF, BF, True), (F32, BF, True), (F32, F32, False), (BF, F32, False)])
+def test_norm_bwd(rows, D, ds, dy, dr):
+    s, w = randn((rows, D), ds, 11), randn((D,), F32, 12, 0.1, 1.0)
+    g, r = randn((rows, D), dy, 13), randn((rows, D), ds, 14) if dr else None
+    u, wr = f64(s).requires_grad_(), f64(w).requires_grad_()
+    loss = (ref_norm(u, wr, None, 1e-6)[1] * f64(g)).sum() + ((u * f64(r)).sum() if dr else 0)
+    dx, dw = torch.autograd.grad(loss, (u, wr))
+    got = gdn.gdn_rmsnorm_bwd(dev(s), dev(w), dev(g), dres=dev(r))
+    assert rel(got["dx"], dx) <= (TOL_BF if ds == BF else TOL_F32)
+    assert rel(got["dweight"], dw) <= TOL_F32
+    again = gdn.gdn_rmsnorm_bwd(dev(s), dev(w), dev(g), dres=dev(r))
+    assert all(torch.equal(got[k], again[k]) for k in got)
+
+
+def test_norm_bwd_no_rows():
+    got = gdn.gdn_rmsnorm_bwd(torch.empty(0, 40, device=DEV), torch.ones(40, device=DEV), torch.empty(0, 40, device=DEV))
+    assert (got["dweight"] == 0).all()
+
+
+# ----------------------------------------------------------- convolution ---
+
+
+def spans(B, T, lens):
+    if lens is None:
+        return [(b, 0, T) for b in range(B)]
+    at = np.concatenate([[0], np.cumsum(lens)])
+    return [(0, int(a), int(b)) for a, b in zip(at[:-1], at[1:])]
+
+
+def cu_of(lens):
+    if lens is None:
+        return None
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32)
+
+
+def ref_conv(x, w, b, init, lens, silu):
+    B, T, D = x.shape
+    W = w.shape[1]
+    out, final = torch.zeros(B, T, D, dtype=F64), []
+    for i, (row, p, q) in enumerate(spans(B, T, lens)):
+        head = init[i] if init is not None else torch.zeros(W - 1, D, dtype=F64)
+        line = torch.cat([head, x[row, p:q]])
+        pre = sum(w[:, j] * line[j:j + q - p] for j in range(W)) + (b if b is not None else 0)
+        out[row, p:q] = pre * torch.sigmoid(pre) if silu else pre
+        final.append(line[q - p:])
+    return out, torch.stack(final)
+
+
+CONV = [  # B, T, D, lens
+    (1, 1, 8, None), (2, 5, 3, None), (1, 3, 1, None), (3, 70, 40, None), (1, 300, 257, None), (2, 129, 1024, None),
+    (1, 64, 24, [64]), (1, 50, 33, [1, 0, 2, 3, 0, 0, 40, 4]), (1, 333, 136, [5, 0, 200, 1, 1, 126, 0]),
+    (1, 6, 16, [0, 6, 0]), (2, 0, 16, None), (1, 0, 16, [0, 0, 0]),
+]
+
+
+@pytest.mark.parametrize("B,T,D,lens", CONV)
+@pytest.mark.parametrize("W", [2, 4, 8])
+@pytest.mark.parametrize("dtype,full", [(BF, True), (BF, False), (F32, True)])
+def test_conv(B, T, D, lens, W, dtype, full):
+    n = B if lens is None else len(lens)
+    x, w = randn((B, T, D), dtype, 20), randn((D, W), F32, 21, 0.5)
+    b = randn((D,), F32, 22) if full else None
+    init = randn((n, W - 1, D), dtype, 23) if full else None
+    ref, fin = ref_conv(f64(x), f64(w), f64(b), f64(init), lens, full)
+    final = torch.full((n, W - 1, D), float("nan"), dtype=dtype, device=DEV)
+    ws = torch.empty(256, dtype=torch.uint8, device=DEV)
+    xs = strided(dev(x)) if full else dev(x)
+    got = gdn.gdn_conv_fwd(xs, dev(w), bias=dev(b), initial_state=dev(init), cu_seqlens=dev(cu_of(lens)),
+                           final_state=final, silu=full, workspace=ws)
+    assert rel(got, ref) <= (TOL_BF if dtype == BF else TOL_F32)
+    assert torch.equal(final.cpu().to(F64), fin)
+    if lens is not None:
+        assert gdn.gdn_last_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("B,T,D,lens", CONV)
+@pytest.mark.parametrize("W", [2, 4, 8])
+@pytest.mark.parametrize("dtype,full", [(BF, True), (F32, True), (F32, False)])
+def test_conv_bwd(B, T, D, lens, W, dtype, full):
+    n = B if lens is None else len(lens)
+    leaf = dict(x=randn((B, T, D), dtype, 24), weight=randn((D, W), F32, 25, 0.5))
+    if full:
+        leaf.update(bias=randn((D,), F32, 26), initial_state=randn((n, W - 1, D), dtype, 27))
+    do, df = randn((B, T, D), dtype, 28), randn((n, W - 1, D), dtype, 29) if full else None
+    v = {k: f64(t).requires_grad_() for k, t in leaf.items()}
+    out, fin = ref_conv(v["x"], v["weight"], v.get("bias"), v.get("initial_state"), lens, full)
+    loss = (out * f64(do)).sum() + ((fin * f64(df)).sum() if full else 0)
+    ref = dict.fromkeys(v)  # without a token and without states nothing depends on anything
+    if loss.requires_grad:
+        ref = dict(zip(v, torch.autograd.grad(loss, tuple(v.values()), allow_unused=True)))
+    a = {k: dev(t) for k, t in leaf.items()}
+    kw = dict(bias=a.get("bias"), initial_state=a.get("initial_state"), cu_seqlens=dev(cu_of(lens)),
+              dfinal_state=dev(df), silu=full)
+    got = gdn.gdn_conv_bwd(a["x"], a["weight"], dev(do), **kw)
+    for k, r in ref.items():
+        r = torch.zeros_like(v[k]) if r is None else r
+        tol = TOL_BF if dtype == BF and k in ("x", "initial_state") else TOL_F32
+        assert rel(got["d" + k], r) <= tol, k
+    again = gdn.gdn_conv_bwd(a["x"], a["weight"], dev(do), **kw)
+    assert all(torch.equal(got[k], again[k]) for k in got)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,D,W", [(1, 8, 4), (5, 33, 2), (3, 4096, 4), (17, 100, 8)])
+def test_conv_steps_continue_a_prompt(dtype, n, D, W):
+    T, steps = 11, 4
+    x, w, b = randn((n, T + steps, D), dtype, 30), randn((D, W), F32, 31, 0.5), randn((D,), F32, 32)
+    ref, fin = ref_conv(f64(x), f64(w), f64(b), None, None, True)
+    pool = torch.full((n + 3, W - 1, D), 7.0, dtype=dtype, device=DEV)
+    slots = torch.arange(n, 0, -1, dtype=torch.int32, device=DEV)  # n .. 1: row 0 and the last two stay
+    state = torch.empty(n, W - 1, D, dtype=dtype, device=DEV)
+    gdn.gdn_conv_fwd(dev(x)[:, :T], dev(w), bias=dev(b), final_state=state)
+    pool[slots.long()] = state
+    for t in range(T, T + steps):
+        got = gdn.gdn_conv_step(dev(x)[:, t], pool, dev(w), bias=dev(b), slots=slots)
+        assert rel(got, ref[:, t]) <= (TOL_BF if dtype == BF else TOL_F32)
+    assert torch.equal(pool[slots.long()].cpu().to(F64), fin)
+    assert (pool[0] == 7).all() and (pool[n + 1:] == 7).all()
+
+
+# -------------------------------------------------------- selective scan ---
+
+
+def ref_scan(v, lens, softplus):
+    """(out, final) from a dict of fp64 tensors, token by token."""
+    B, T, C = v["x"].shape
+    N = v["A"].shape[1]
+    rows, final = [[None] * T for _ in range(B)], []
+    for i, (row, p, q) in enumerate(spans(B, T, lens)):
+        h = v["h0"][i] if v.get("h0") is not None else torch.zeros(C, N, dtype=F64)
+        for t in range(p, q):
+            dl = v["dt"][row, t] + (v["dt_bias"] if v.get("dt_bias") is not None else 0)
+            dl = torch.nn.functional.softplus(dl, threshold=700) if softplus else dl
+            x = v["x"][row, t]
+            h = torch.exp(dl[:, None] * v["A"]) * h + (dl * x)[:, None] * v["Bm"][row, t]
+            y = (h * v["Cm"][row, t]).sum(-1)
+            if v.get("D") is not None:
+                y = y + v["D"] * x
+            if v.get("z") is not None:
+                y = y * v["z"][row, t] * torch.sigmoid(v["z"][row, t])
+            rows[row][t] = y
+        final.append(h)
+    out = torch.stack([torch.stack(r) for r in rows]) if T else torch.zeros(B, 0, C, dtype=F64)
+    return out, torch.stack(final)
+
+
+def scan_case(B, T, C, N, lens, dtype, full, seed=40):
+    n = B if lens is None else len(lens)
+    v = dict(x=randn((B, T, C), dtype, seed), dt=randn((B, T, C), dtype, seed + 1, 0.5),
+             A=-torch.arange(1, N + 1, dtype=F32) * (1 + 0.2 * randn((C, N), F32, seed + 2).clamp(-2, 2)),
+             Bm=randn((B, T, N), dtype, seed + 3), Cm=randn((B, T, N), dtype, seed + 4))
+    if full:
+        step = torch.exp(torch.linspace(math.log(1e-3), math.log(1e-1), C))
+        v.update(D=randn((C,), F32, seed + 5), z=randn((B, T, C), dtype, seed + 6),
+                 dt_bias=step + torch.log(-torch.expm1(-step)), h0=randn((n, C, N), F32, seed + 7))
+    else:
+        v["dt"] = (v["dt"].float().abs() * 0.1).to(dtype)
+    return v
+
+
+SCAN = [  # B, T, C, N, lens
+    (1, 1, 1, 1, None), (2, 3, 5, 16, None), (1, 37, 64, 16, None), (2, 130, 33, 7, None), (1, 200, 100, 16, None),
+    (3, 65, 70, 16, None), (1, 21, 17, 32, None), (2, 19, 40, 64, None), (1, 18, 9, 128, None), (1, 50, 24, 40, None),
+    (1, 600, 66, 16, None), (1, 90, 48, 16, [1, 0, 2, 30, 0, 57, 0]), (1, 133, 30, 20, [133]),
+    (1, 260, 72, 16, [64, 64, 1, 131]), (1, 700, 40, 16, [3, 0, 500, 190, 7]), (2, 0, 16, 16, None),
+    (1, 0, 16, 16, [0, 0]),
+]
+
+
+def call_scan(v, lens, full, **kw):
+    a = {k: dev(t) for k, t in v.items()}
+    a = {k: strided(t) if full and k in ("z", "Bm", "Cm") else t for k, t in a.items()}
+    return gdn.gdn_ssm_fwd(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], D=a.get("D"), z=a.get("z"),
+                           dt_bias=a.get("dt_bias"), dt_softplus=full, h0=a.get("h0"), cu_seqlens=dev(cu_of(lens)), **kw)
+
+
+@pytest.mark.parametrize("B,T,C,N,lens", SCAN)
+@pytest.mark.parametrize("dtype,full", [(BF, True), (BF, False), (F32, True), (F32, False)])
+def test_scan(B, T, C, N, lens, dtype, full):
+    v = scan_case(B, T, C, N, lens, dtype, full)
+    ref, fin = ref_scan({k: f64(t) for k, t in v.items()}, lens, full)
+    n = B if lens is None else len(lens)
+    final = torch.full((n, C, N), float("nan"), device=DEV)
+    got = call_scan(v, lens, full, h_final=final)
+    assert rel(got, ref) <= (TOL_BF if dtype == BF else TOL_SCAN)
+    assert rel(final, fin) <= TOL_SCAN
+
+
+def test_scan_state_carries_over_calls():
+    v = scan_case(2, 90, 40, 16, None, F32, True)
+    ref, fin = ref_scan({k: f64(t) for k, t in v.items()}, None, True)
+    state = v["h0"]
+    for p, q in ((0, 1), (1, 64), (64, 90)):
+        part = {k: (t[:, p:q] if t.dim() == 3 and k != "h0" else t) for k, t in v.items()}
+        part["h0"] = state
+        final = torch.empty(2, 40, 16, device=DEV)
+        assert rel(call_scan(part, None, False | True, h_final=final), ref[:, p:q]) <= TOL_SCAN
+        state = final.cpu()
+    assert rel(state, fin) <= TOL_SCAN
+
+
+@pytest.mark.parametrize("B,T,C,N,lens", SCAN)
+@pytest.mark.parametrize("dtype,full", [(BF, True), (F32, True), (F32, False)])
+def test_scan_bwd(B, T, C, N, lens, dtype, full):
+    v = scan_case(B, T, C, N, lens, dtype, full, 60)
+    n = B if lens is None else len(lens)
+    do = randn((B, T, C), dtype, 70)
+    df = randn((n, C, N), F32, 71) if full else None
+    leaf = {k: f64(t).requires_grad_() for k, t in v.items()}
+    out, fin = ref_scan(leaf, lens, full)
+    loss = (out * f64(do)).sum() + ((fin * f64(df)).sum() if full else 0.0 * fin.sum())
+    ref = dict.fromkeys(leaf)  # without a token and without states nothing depends on anything
+    if loss.requires_grad:
+        ref = dict(zip(leaf, torch.autograd.grad(loss, tuple(leaf.values()), allow_unused=True)))
+    a = {k: dev(t) for k, t in v.items()}
+
+    def run():
+        return gdn.gdn_ssm_bwd(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], dev(do), D=a.get("D"), z=a.get("z"),
+                               dt_bias=a.get("dt_bias"), dt_softplus=full, h0=a.get("h0"),
+                               cu_seqlens=dev(cu_of(lens)), dh_final=dev(df))
+    got = run()
+    assert set(got) == {"d" + k for k in leaf}
+    for k, r in ref.items():
+        r = torch.zeros_like(leaf[k]) if r is None else r
+        act = k in ("x", "dt", "Bm", "Cm", "z")
+        assert rel(got["d" + k], r) <= (TOL_BF if dtype == BF and act else TOL_SCAN), k
+    again = run()
+    assert all(torch.equal(got[k], again[k]) for k in got)
+
+
+def test_scan_gradient_by_differences():
+    v = scan_case(1, 40, 24, 16, [17, 23], F32, True, 80)
+    do, df = randn((1, 40, 24), F32, 90), randn((2, 24, 16), F32, 91)
+    a = {k: dev(t) for k, t in v.items()}
+    got = gdn.gdn_ssm_bwd(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], dev(do), D=a["D"], z=a["z"],
+                          dt_bias=a["dt_bias"], h0=a["h0"], cu_seqlens=dev(cu_of([17, 23])), dh_final=dev(df))
+
+    def loss(w):
+        out, fin = ref_scan(w, [17, 23], True)
+        return ((out * f64(do)).sum() + (fin * f64(df)).sum()).item()
+    base = {k: f64(t) for k, t in v.items()}
+    for k, t in base.items():
+        e = randn(tuple(t.shape), F64, 92)
+        h = 1e-5
+        num = (loss({**base, k: t + h * e}) - loss({**base, k: t - h * e})) / (2 * h)
+        ana = (f64(got["d" + k]) * e).sum().item()
+        norm = f64(got["d" + k]).norm().item() * math.sqrt(t.numel())  # of the same size as a typical sum
+        assert abs(num - ana) <= 1e-3 * max(abs(num), norm / math.sqrt(t.numel())), (k, num, ana)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,C,N", [(1, 8, 16), (6, 33, 16), (2, 4096, 16), (3, 20, 7), (2, 24, 32), (2, 9, 100)])
+def test_scan_steps_continue_a_prompt(dtype, n, C, N):
+    T, steps = 9, 4
+    v = scan_case(n, T + steps, C, N, None, dtype, True, 100)
+    ref, fin = ref_scan({k: f64(t) for k, t in v.items()}, None, True)
+    head = {k: (t[:, :T] if k in ("x", "dt", "Bm", "Cm", "z") else t) for k, t in v.items()}
+    final = torch.empty(n, C, N, device=DEV)
+    call_scan(head, None, True, h_final=final)
+    pool = torch.full((n + 2, C, N), 3.0, device=DEV)
+    slots = torch.arange(n, 0, -1, dtype=torch.int32, device=DEV)
+    pool[slots.long()] = final
+    a = {k: dev(t) for k, t in v.items()}
+    for t in range(T, T + steps):
+        got = gdn.gdn_ssm_step(a["x"][:, t], a["dt"][:, t], a["A"], a["Bm"][:, t], a["Cm"][:, t], pool, D=a["D"],
+                               z=a["z"][:, t], dt_bias=a["dt_bias"], slots=slots)
+        assert rel(got, ref[:, t]) <= (TOL_BF if dtype == BF else TOL_SCAN)
+    assert rel(pool[slots.long()], fin) <= TOL_SCAN
+    assert (pool[0] == 3).all() and (pool[n + 1] == 3).all()
+
+
+def test_steps_skip_padding_rows():
+    C, N, W = 40, 16, 4
+    v = scan_case(4, 1, C, N, None, BF, True, 120)
+    slots = torch.tensor([2, -1, 0, 3], dtype=torch.int32, device=DEV)  # 3: outside a pool of 3
+    a = {k: dev(t) for k, t in v.items()}
+    pool = randn((3, C, N), F32, 121).to(DEV)
+    old = pool.clone()
+    got = gdn.gdn_ssm_step(a["x"][:, 0], a["dt"][:, 0], a["A"], a["Bm"][:, 0], a["Cm"][:, 0], pool, D=a["D"],
+                           z=a["z"][:, 0], dt_bias=a["dt_bias"], slots=slots)
+    v["h0"] = old.cpu()[[2, 1, 0, 1]]
+    ref, fin = ref_scan({k: f64(t) for k, t in v.items()}, None, True)
+    assert (got[[1, 3]] == 0).all() and torch.equal(pool[1], old[1])
+    assert rel(got[[0, 2]], ref[[0, 2], 0]) <= TOL_BF and rel(pool[[2, 0]], fin[[0, 2]]) <= TOL_SCAN
+    win = randn((3, W - 1, C), BF, 122).to(DEV)
+    oldw = win.clone()
+    out = gdn.gdn_conv_step(a["x"][:, 0], win, randn((C, W), F32, 123).to(DEV), slots=slots)
+    assert (out[[1, 3]] == 0).all() and torch.equal(win[1], oldw[1]) and torch.equal(win[2, -1], a["x"][0, 0])
+
+
+def test_offsets_past_32_bits():
+    C, N = 4096, 16
+    n_slots = 2**31 // (C * N) + 3  # the last rows begin past 2^31 elements
+    pool = torch.empty(n_slots, C, N, device=DEV)
+    slots = torch.tensor([n_slots - 1], dtype=torch.int32, device=DEV)
+    v = scan_case(1, 1, C, N, None, BF, True, 130)
+    pool[n_slots - 1] = dev(v["h0"])[0]
+    a = {k: dev(t) for k, t in v.items()}
+    ref, fin = ref_scan({k: f64(t) for k, t in v.items()}, None, True)
+    got = gdn.gdn_ssm_step(a["x"][:, 0], a["dt"][:, 0], a["A"], a["Bm"][:, 0], a["Cm"][:, 0], pool, D=a["D"],
+                           z=a["z"][:, 0], dt_bias=a["dt_bias"], slots=slots)
+    assert rel(got, ref[:, 0]) <= TOL_BF and rel(pool[n_slots - 1:], fin) <= TOL_SCAN
+    del pool
+    # two batch rows more than 2^31 elements apart
+    far = 2**31 + 64
+    line = torch.empty(far + 8 * 64, dtype=BF, device=DEV)
+    x = torch.as_strided(line, (2, 8, 64), (far, 64, 1))
+    x.copy_(randn((2, 8, 64), BF, 131))
+    w = randn((64, 4), F32, 132)
+    ref, _ = ref_conv(f64(x), f64(w), None, None, None, True)
+    assert rel(gdn.gdn_conv_fwd(x, dev(w)), ref) <= TOL_BF
+    g = gdn.gdn_rmsnorm_fwd(torch.as_strided(line, (2, 64), (far, 1)), torch.ones(64, device=DEV))["out"]
+    assert rel(g, ref_norm(x[:, 0], torch.ones(64), None, 1e-6)[1]) <= TOL_BF
+
+
+def test_malformed_cu_seqlens_is_reported():
+    x, w = randn((1, 40, 16), BF, 140).to(DEV), randn((16, 4), F32, 141).to(DEV)
+    v = {k: dev(t) for k, t in scan_case(1, 40, 16, 16, [20, 20], BF, True, 142).items()}
+    for cu in ([0, 30, 20, 40], [0, 20, 39], [1, 20, 40], [0, 90, 40], [0, -5, 40]):
+        c = torch.tensor(cu, dtype=torch.int32, device=DEV)
+        n = len(cu) - 1
+        ws = torch.zeros(1 << 22, dtype=torch.uint8, device=DEV)
+        gdn.gdn_conv_fwd(x, w, cu_seqlens=c, workspace=ws, final_state=torch.empty(n, 3, 16, dtype=BF, device=DEV))
+        assert gdn.gdn_last_device_error(ws) == 1, cu
+        gdn.gdn_conv_bwd(x, w, x, cu_seqlens=c, workspace=ws)
+        assert gdn.gdn_last_device_error(ws) == 1, cu
+        args = (v["x"], v["dt"], v["A"], v["Bm"], v["Cm"])
+        gdn.gdn_ssm_fwd(*args, cu_seqlens=c, workspace=ws, h_final=torch.empty(n, 16, 16, device=DEV))
+        assert gdn.gdn_last_device_error(ws) == 1, cu
+        gdn.gdn_ssm_bwd(*args, v["x"], cu_seqlens=c, workspace=ws)
+        assert gdn.gdn_last_device_error(ws) == 1, cu
+
+
+def test_calls_run_on_the_given_stream():
+    s = torch.cuda.Stream()
+    x, w = randn((2048, 512), BF, 150), randn((512,), F32, 151, 0.1, 1.0)
+    with torch.cuda.stream(s):
+        a, b = dev(x), dev(w)
+    s.synchronize()
+    got = gdn.gdn_rmsnorm_fwd(a, b, stream=s)["out"]
+    s.synchronize()
+    assert rel(got, ref_norm(x, w, None, 1e-6)[1]) <= TOL_BF
+    v = scan_case(1, 64, 64, 16, None, BF, True, 152)
+    ref, _ = ref_scan({k: f64(t) for k, t in v.items()}, None, True)
+    torch.cuda.synchronize()
+    got = call_scan(v, None, True, stream=s)
+    torch.cuda.synchronize()
+    assert rel(got, ref) <= TOL_BF
+
+
+def test_steps_replay_in_a_graph():
+    C, N, n = 256, 16, 3
+    v = {k: dev(t) for k, t in scan_case(n, 1, C, N, None, BF, True, 160).items()}
+    pool, out = v["h0"].clone(), torch.empty(n, C, dtype=BF, device=DEV)
+    step = lambda st, o: gdn.gdn_ssm_step(v["x"][:, 0], v["dt"][:, 0], v["A"], v["Bm"][:, 0], v["Cm"][:, 0], st,  # noqa: E731
+                                          D=v["D"], z=v["z"][:, 0], dt_bias=v["dt_bias"], out=o)
+    step(pool.clone(), out.clone())
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(pool, out)
+    pool.copy_(v["h0"])
+    g.replay()
+    g.replay()
+    want, o2 = v["h0"].clone(), torch.empty_like(out)
+    step(want, o2)
+    step(want, o2)
+    torch.cuda.synchronize()
+    assert torch.equal(pool, want) and torch.equal(out, o2)
