@@ -215,6 +215,11 @@ struct SsmParams {
     int64_t o_sb, o_st;
     float *h_final;  // (n_seq, D, N) or null
     int B, T, D, N, softplus, bf16;
+    int vec;             // rows of x, dt, z, out (and the gradients) are 16-byte aligned
+    int n_wide;          // rows of A and of the states are
+    int bc_vec;          // rows of B and C are, in whole vectors of four
+    int nchunk, clen;    // chunks of a line, tokens a chunk
+    float *sums, *dsum;  // workspace: (lines, nchunk - 1, D, padded N), (lines, nchunk - 1, D)
     int *err;
     // gradient; activations' gradients contiguous in x's type
     const void *dout;
@@ -224,6 +229,9 @@ struct SsmParams {
     float *dA, *dD, *ddt_bias, *dh0;
     float *ckpt, *part_bc, *part_a, *part_d;  // workspace
 };
+void ssm_split(int lines, int T, int D, int N, int *nchunk, int *clen);
+cudaError_t launch_ssm_sum(const SsmParams &p, cudaStream_t st);
+cudaError_t launch_ssm_chain(const SsmParams &p, cudaStream_t st);
 cudaError_t launch_ssm_scan(const SsmParams &p, cudaStream_t st);
 int ssm_bwd_tiles(int D, int N);
 cudaError_t launch_ssm_bwd(const SsmParams &p, cudaStream_t st);

@@ -3,6 +3,7 @@
 #include "../../include/gdn.h"
 #include "gdn_launch.cuh"
 #include "gdn_layer.cuh"
+#include "gdn_ssm.cuh"
 
 namespace {
 
@@ -36,6 +37,20 @@ bool batch_ok(int B, int T, int D, const int32_t *cu, int n_seq) {
     return cu ? B == 1 && n_seq >= 1 : n_seq == B;
 }
 
+// the forward: the error word, and the chunks' sums where a line is cut
+struct SsmWs {
+    int nchunk, clen;
+    size_t sums, dsum, total;
+};
+SsmWs ssm_ws(int lines, int T, int D, int N) {
+    SsmWs L;
+    ssm_split(lines, T, D, N, &L.nchunk, &L.clen);
+    const size_t items = (size_t)lines * (L.nchunk - 1);
+    L.sums = kAlign;
+    L.dsum = align_up(L.sums + items * D * ssm_np(N) * 4);
+    L.total = align_up(L.dsum + items * D * 4);
+    return L;
+}
 struct SsmBwdWs {
     size_t ckpt, bc, a, d, total;
 };
@@ -242,8 +257,8 @@ gdn_status ssm_setup(const void *x, int64_t x_sb, int64_t x_st, const void *dt, 
     r.add(dt, dtype, dt_sb, dt_st);
     r.add(z, dtype, z_sb, z_st);
     Rows bc;  // (B, T, N) rows are staged by element where they are not wide
-    bc.add(bm, dtype, bm_sb, bm_st);
-    bc.add(cm, dtype, cm_sb, cm_st);
+    bc.add(bm, dtype, bm_sb, bm_st, 4 * elem_size(dtype));
+    bc.add(cm, dtype, cm_sb, cm_st, 4 * elem_size(dtype));
     if (!r.ok || !bc.ok) return GDN_ERR_LAYOUT;
     for (const void *f : {(const void *)A, (const void *)Dv, (const void *)dt_bias, (const void *)h0, (const void *)cu})
         if (!f32_ok(f)) return GDN_ERR_LAYOUT;
@@ -253,6 +268,8 @@ gdn_status ssm_setup(const void *x, int64_t x_sb, int64_t x_st, const void *dt, 
     p.z = z, p.z_sb = z_sb, p.z_st = z_st, p.A = A, p.Dv = Dv, p.dt_bias = dt_bias, p.h0 = h0;
     p.cu = cu, p.n_seq = n_seq, p.B = B, p.T = T, p.D = D, p.N = N;
     p.softplus = flags & GDN_SOFTPLUS, p.bf16 = dtype == GDN_BF16;
+    p.bc_vec = bc.wide && N % 4 == 0;
+    p.n_wide = N % 4 == 0 && addr(A) % 16 == 0 && addr(h0) % 16 == 0;
     return GDN_OK;
 }
 }  // namespace
@@ -260,7 +277,7 @@ gdn_status ssm_setup(const void *x, int64_t x_sb, int64_t x_st, const void *dt, 
 extern "C" {
 
 size_t gdn_ssm_workspace_size(int B, int T, int D, int N, int n_seq, int varlen) {
-    return ssm_shape_ok(B, T, D, N, n_seq, varlen) ? kAlign : 0;
+    return ssm_shape_ok(B, T, D, N, n_seq, varlen) ? ssm_ws(varlen ? 1 : B, T, D, N).total : 0;
 }
 
 gdn_status gdn_ssm_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *dt, int64_t dt_sb, int64_t dt_st,
@@ -277,11 +294,22 @@ gdn_status gdn_ssm_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *dt
                                    z_st, dt_bias, h0, cu_seqlens, n_seq, B, T, D, N, dtype, flags, r, p);
     if (s != GDN_OK) return s;
     if (!f32_ok(h_final)) return GDN_ERR_LAYOUT;
-    if (!ws_ok(workspace, ws_bytes, gdn_ssm_workspace_size(B, T, D, N, n_seq, cu_seqlens != nullptr)))
-        return GDN_ERR_WORKSPACE;
+    const SsmWs L = ssm_ws(cu_seqlens ? 1 : B, T, D, N);
+    if (!ws_ok(workspace, ws_bytes, L.total)) return GDN_ERR_WORKSPACE;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
     p.out = out, p.o_sb = out_sb, p.o_st = out_st, p.h_final = h_final;
-    p.err = cu_seqlens ? static_cast<int *>(workspace) : nullptr;
-    return cuda_status(launch(KSsmScan, stream, [&] { return launch_ssm_scan(p, stream); }));
+    p.nchunk = L.nchunk, p.clen = L.clen;
+    p.sums = reinterpret_cast<float *>(ws + L.sums), p.dsum = reinterpret_cast<float *>(ws + L.dsum);
+    p.err = cu_seqlens ? reinterpret_cast<int *>(ws) : nullptr;
+    p.vec = r.wide && D % 8 == 0;
+    p.n_wide = p.n_wide && addr(h_final) % 16 == 0;
+    cudaError_t e = cudaSuccess;
+    if (p.nchunk > 1) {
+        e = launch(KSsmSum, stream, [&] { return launch_ssm_sum(p, stream); });
+        if (e == cudaSuccess) e = launch(KSsmChain, stream, [&] { return launch_ssm_chain(p, stream); });
+    }
+    if (e == cudaSuccess) e = launch(KSsmScan, stream, [&] { return launch_ssm_scan(p, stream); });
+    return cuda_status(e);
 }
 
 size_t gdn_ssm_bwd_workspace_size(int B, int T, int D, int N, int n_seq, int varlen) {

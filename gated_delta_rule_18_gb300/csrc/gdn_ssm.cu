@@ -4,70 +4,332 @@
 // for whole sequences (dense or packed) and for single tokens with the
 // states in a pool. h is fp32 throughout.
 //
-// A group of LN lanes holds a channel's states, four a lane; y crosses the
-// group by shuffles.
-#include "gdn_layer.cuh"
+// What bounds the scan: a (token, channel, state) costs one exponential and
+// four multiply-adds; both pipes take 4 cycles a warp for them (32 ex2 and 128
+// fp32 operations a clock and SM, measured), so 16 states of a token and
+// channel cost 64 cycles a warp, more than the 8 bytes it moves.
+// The main loop is written in packed pairs to leave issue slots for the rest.
+//
+// A line of tokens is one CTA's from end to end while channels alone fill the
+// GPU. Where they do not, the line is cut into chunks: a first pass forms
+// each chunk's state from zero and its sum of delta (the decay of a chunk is
+// exp(A sum delta), so it needs no product of its own), a short pass chains
+// them, and the scan runs every chunk from its entering state.
+#include "gdn_ssm.cuh"
 
 namespace gdn {
 namespace {
 
-__device__ __forceinline__ float softplus_f(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+constexpr int kThreads = 64;  // a CTA: 2 * 64 / LN channels
+constexpr int kStage = 16;    // tokens a stage
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-// One CTA: 128 / LN channels of one sequence, token by token.
-template <typename T, int LN>
-__global__ void __launch_bounds__(128) ssm_scan_kernel(const SsmParams p) {
-    const int seq = blockIdx.y;
-    const int d = blockIdx.x * (128 / LN) + threadIdx.x / LN, n0 = threadIdx.x % LN * 4;
-    const bool in = d < p.D;
-    if (p.err && blockIdx.x == 0 && seq == 0) {
-        int bad = 0;
-        for (int s = threadIdx.x; s < p.n_seq; s += 128) bad |= p.cu[s + 1] < p.cu[s];
-        if (threadIdx.x == 0) bad |= p.cu[0] != 0 || p.cu[p.n_seq] != p.T;
-        bad = __syncthreads_or(bad);
-        if (threadIdx.x == 0) *p.err = bad;
-    }
-    const int row = p.cu ? 0 : seq;
-    const int t0 = p.cu ? min(max(p.cu[seq], 0), p.T) : 0, t1 = p.cu ? min(p.cu[seq + 1], p.T) : p.T;
-    float a2[4], h[4];
+// Q neighbouring states of a channel, in pairs
+template <int Q>
+__device__ __forceinline__ void ld_states(f32x2 (&v)[Q / 2], const float *p, int n, bool wide) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const bool on = in && n0 + j < p.N;
-        a2[j] = on ? p.A[(int64_t)d * p.N + n0 + j] * kLog2e : 0.f;
-        h[j] = on && p.h0 ? p.h0[((int64_t)seq * p.D + d) * p.N + n0 + j] : 0.f;
-    }
-    const float dv = in && p.Dv ? p.Dv[d] : 0.f, bias = in && p.dt_bias ? p.dt_bias[d] : 0.f;
-    for (int t = t0; t < t1; ++t) {
-        const float x = in ? ldf((const T *)p.x + row * p.x_sb + t * p.x_st + d) : 0.f;
-        float dl = in ? ldf((const T *)p.dt + row * p.dt_sb + t * p.dt_st + d) + bias : 0.f;
-        if (p.softplus) dl = softplus_f(dl);
-        const float u = dl * x;
-        float y = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool on = n0 + j < p.N;
-            const float b = on ? ldf((const T *)p.bm + row * p.bm_sb + t * p.bm_st + n0 + j) : 0.f;
-            const float c = on ? ldf((const T *)p.cm + row * p.cm_sb + t * p.cm_st + n0 + j) : 0.f;
-            h[j] = fmaf(exp2f(dl * a2[j]), h[j], u * b);
-            y = fmaf(h[j], c, y);
+    for (int j = 0; j < Q / 4; ++j) {
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (wide) {
+            if (4 * j < n) f = reinterpret_cast<const float4 *>(p)[j];
+        } else {
+            if (4 * j < n) f.x = p[4 * j];
+            if (4 * j + 1 < n) f.y = p[4 * j + 1];
+            if (4 * j + 2 < n) f.z = p[4 * j + 2];
+            if (4 * j + 3 < n) f.w = p[4 * j + 3];
         }
+        v[2 * j] = pack2(f.x, f.y), v[2 * j + 1] = pack2(f.z, f.w);
+    }
+}
+template <int Q>
+__device__ __forceinline__ void st_states(float *p, const f32x2 (&v)[Q / 2], int n, bool wide) {
 #pragma unroll
-        for (int o = LN / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-        if (in && threadIdx.x % LN == 0) {
-            y = fmaf(dv, x, y);
-            if (p.z) {
-                const float z = ldf((const T *)p.z + row * p.z_sb + t * p.z_st + d);
-                y *= z * sigmoid_f(z);
+    for (int j = 0; j < Q / 4; ++j) {
+        const float2 a = unpack2(v[2 * j]), b = unpack2(v[2 * j + 1]);
+        if (wide) {
+            if (4 * j < n) reinterpret_cast<float4 *>(p)[j] = make_float4(a.x, a.y, b.x, b.y);
+        } else {
+            if (4 * j < n) p[4 * j] = a.x;
+            if (4 * j + 1 < n) p[4 * j + 1] = a.y;
+            if (4 * j + 2 < n) p[4 * j + 2] = b.x;
+            if (4 * j + 3 < n) p[4 * j + 3] = b.y;
+        }
+    }
+}
+// of the two channels at p and p + ld; on: which of them exist
+template <int Q>
+__device__ __forceinline__ void ld_pair(f32x2 (&v)[2][Q / 2], const float *p, int ld, int n, bool wide,
+                                        const bool (&on)[2]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) ld_states<Q>(v[k], p + k * ld, on[k] ? n : 0, wide);
+}
+template <int Q>
+__device__ __forceinline__ void st_pair(float *p, const f32x2 (&v)[2][Q / 2], int ld, int n, bool wide,
+                                        const bool (&on)[2]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) st_states<Q>(p + k * ld, v[k], on[k] ? n : 0, wide);
+}
+
+// A lane has Q states, in packed pairs, of two neighbouring channels; LN lanes
+// a channel (LN = 1 up to 16 states, so nothing crosses lanes there). x, dt and z
+// come through a ring of three stages of shared memory, two stages ahead of
+// their use; B and C, the same for every channel, are staged as fp32 and read
+// by broadcast, 4 bytes a (channel, state). USUAL: softplus, a gate and rows
+// for wide accesses, known beforehand.
+template <typename T, int Q, int LN, bool SUM, bool USUAL>
+__global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const SsmParams p, int ntile) {
+    constexpr int CH = 2 * kThreads / LN, NP = Q * LN, TS = kStage, K = 1;  // K: tokens in flight
+    constexpr int VE = 16 / sizeof(T);           // elements of a 16-byte copy
+    constexpr int NA = SUM ? 2 : 3;              // x, dt, z
+    constexpr int kRow = CH * (int)sizeof(T), kTile = TS * kRow, kBuf = NA * kTile;
+    constexpr int kCopies = TS * CH / VE;        // 16-byte copies of a tile
+    constexpr int kBc = TS * 2 * NP;             // B and C values of a stage
+    constexpr int VB = kBc / kThreads < 4 ? kBc / kThreads : 4;  // values of a B, C load
+    constexpr int NBC = kBc / (kThreads * VB), WB = RowVec<T, VB>::kWords;
+    extern __shared__ __align__(16) unsigned char smem[];
+    float *bcs = reinterpret_cast<float *>(smem + 3 * kBuf);  // [2][TS][2][NP]
+    const int tid = threadIdx.x, ch = tid / LN * 2, ln = tid % LN;
+    const int tile = blockIdx.x % ntile, item = blockIdx.x / ntile;
+    const int nch = SUM ? p.nchunk - 1 : p.nchunk;
+    const int line = item / nch, chunk = item - line * nch;
+    if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
+    const int t0 = chunk * p.clen, t1 = min(p.T - t0, p.clen) + t0;
+    const int c0 = tile * CH, d = c0 + ch, n0 = ln * Q, nn = p.N - n0;
+    const bool on[2] = {d < p.D && nn > 0, d + 1 < p.D && nn > 0};
+    const int64_t hrow = (int64_t)p.D * p.N, dnp = (int64_t)p.D * NP;
+    const int64_t own = (int64_t)d * p.N + n0, own_p = (int64_t)d * NP + n0;
+
+    f32x2 a2[2][Q / 2], h[2][Q / 2];
+    ld_pair<Q>(a2, p.A + own, p.N, nn, p.n_wide, on);
+#pragma unroll
+    for (int j = 0; j < Q / 2; ++j) {
+        a2[0][j] = mul2(a2[0][j], pack2(kLog2e, kLog2e));
+        a2[1][j] = mul2(a2[1][j], pack2(kLog2e, kLog2e));
+    }
+    auto pair_of = [&](const float *v) {
+        return make_float2(v && d < p.D ? v[d] : 0.f, v && d + 1 < p.D ? v[d + 1] : 0.f);
+    };
+    const bool softplus = USUAL || p.softplus, gate = USUAL || p.z, vec = USUAL || p.vec;
+    const float2 bias = pair_of(p.dt_bias), dv = pair_of(SUM ? nullptr : p.Dv);
+    auto zero_h = [&] {
+#pragma unroll
+        for (int j = 0; j < Q / 2; ++j) h[0][j] = h[1][j] = pack2(0.f, 0.f);
+    };
+    auto first_h = [&](int seg) {
+        if (p.h0) ld_pair<Q>(h, p.h0 + seg * hrow + own, p.N, nn, p.n_wide, on);
+        else zero_h();
+    };
+    SsmSeq q{0, 0, false};
+    if (t0 < t1) q = ssm_find(p.cu, p.n_seq, p.T, line, t0);
+    bool reset = q.starts;
+    if (q.starts) first_h(q.seg);
+    else if (!SUM && chunk > 0) ld_pair<Q>(h, p.sums + ((int64_t)line * (p.nchunk - 1) + chunk - 1) * dnp + own_p, NP, Q, true, on);
+    else zero_h();
+
+    const T *src[3] = {(const T *)p.x + line * p.x_sb, (const T *)p.dt + line * p.dt_sb, (const T *)p.z + line * p.z_sb};
+    const int64_t str[3] = {p.x_st, p.dt_st, p.z_st};
+    const int na = SUM || !gate ? 2 : 3;
+    auto fetch = [&](int s, int b) {  // the stage that begins at token s into buffer b
+        if (s < t1) {
+#pragma unroll
+            for (int a = 0; a < NA; ++a) {
+                if (a >= na) break;
+                if (vec) {
+#pragma unroll
+                    for (int i = 0; i < (kCopies + kThreads - 1) / kThreads; ++i) {
+                        const int e = tid + i * kThreads, r = e / (CH / VE), c = e % (CH / VE) * VE;
+                        if ((kCopies % kThreads == 0 || e < kCopies) && s + r < t1 && c0 + c < p.D)
+                            cp_async16(smem + b * kBuf + a * kTile + r * kRow + c * (int)sizeof(T),
+                                       src[a] + (s + r) * str[a] + c0 + c, 16);
+                    }
+                } else {
+                    T *dst = reinterpret_cast<T *>(smem + b * kBuf + a * kTile);
+                    for (int e = tid; e < TS * CH; e += kThreads) {
+                        const int r = e / CH, c = e % CH;
+                        // zeros past the last channel: a pair's halves share a reciprocal
+                        dst[e] = s + r < t1 && c0 + c < p.D ? src[a][(s + r) * str[a] + c0 + c] : to_type<T>(0.f);
+                    }
+                }
             }
-            ((T *)p.out)[row * p.o_sb + t * p.o_st + d] = to_type<T>(y);
+        }
+        cp_async_commit();
+    };
+    const T *bg = (const T *)p.bm + line * p.bm_sb, *cg = (const T *)p.cm + line * p.cm_sb;
+    uint32_t nbc[NBC][WB];  // as stored: converted where they are staged, not where they are loaded
+    auto fetch_bc = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < NBC; ++i) {
+            const int e = (tid + i * kThreads) * VB, r = e / (2 * NP), k = e % (2 * NP), n = k % NP;
+#pragma unroll
+            for (int w = 0; w < WB; ++w) nbc[i][w] = 0u;
+            if (s + r < t1 && n < p.N && !(SUM && k >= NP)) {
+                const T *at = k < NP ? bg + (s + r) * p.bm_st + n : cg + (s + r) * p.cm_st + n;
+                if (p.bc_vec) ld_row<T, VB, true>(nbc[i], at, p.N - n);
+                else ld_row<T, VB, false>(nbc[i], at, p.N - n);
+            }
+        }
+    };
+    auto stage_bc = [&](float *dst) {
+#pragma unroll
+        for (int i = 0; i < NBC; ++i) {
+            float f[VB];
+            words_to_f<T, VB>(f, nbc[i]);
+#pragma unroll
+            for (int k = 0; k < VB; ++k) dst[(tid + i * kThreads) * VB + k] = f[k];
+        }
+    };
+    if (t0 < t1) {
+        fetch(t0, 0);
+        fetch(t0 + TS, 1);
+        fetch_bc(t0);
+    }
+    float2 dsum = make_float2(0.f, 0.f);
+    int buf = 0, flip = 0;
+    for (int s = t0; s < t1; s += TS) {
+        float *bc = bcs + flip * kBc;
+        stage_bc(bc);
+        if (s + TS < t1) fetch_bc(s + TS);
+        cp_async_wait<1>();
+        __syncthreads();
+        fetch(s + 2 * TS, buf == 0 ? 2 : buf - 1);
+        const int m = min(t1 - s, TS);
+        const T *xs = reinterpret_cast<const T *>(smem + buf * kBuf) + ch;
+        T *os = (T *)p.out + line * p.o_sb + s * p.o_st + d;
+        auto pair_at = [&](int i, int a) {  // the pair's x, dt or z
+            float f[2];
+            ld_row_f<T, 2, true>(f, xs + (a * TS + i) * CH, 2);
+            return make_float2(f[0], f[1]);
+        };
+        // The three parts of K tokens from token i on. Their chains are long
+        // (softplus alone some 150 cycles), so the loop below forms the next
+        // tokens' delta while it runs the states of these.
+        auto prep = [&](auto &dl, auto &u, int i) {
+#pragma unroll
+            for (int k = 0; k < (int)(sizeof(dl) / sizeof(float2)); ++k) {
+                const float2 v = pair_at(i + k, 1), x = pair_at(i + k, 0);
+                dl[k] = make_float2(v.x + bias.x, v.y + bias.y);
+                if (softplus) dl[k] = softplus2(dl[k]);
+                u[k] = make_float2(dl[k].x * x.x, dl[k].y * x.y);
+            }
+        };
+        auto states = [&](float2 &y, float2 dl, float2 u, int i) {
+            const float4 *b4 = reinterpret_cast<const float4 *>(bc + i * 2 * NP + n0);
+            const f32x2 d2[2] = {pack2(dl.x, dl.x), pack2(dl.y, dl.y)}, u2[2] = {pack2(u.x, u.x), pack2(u.y, u.y)};
+            f32x2 ya[2], yb[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) ya[k] = yb[k] = pack2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < Q / 4; ++j) {
+                const float4 b = b4[j];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    f32x2 *hk = h[k] + 2 * j;
+                    hk[0] = fma2(ex2_2(mul2(d2[k], a2[k][2 * j])), hk[0], mul2(u2[k], pack2(b.x, b.y)));
+                    hk[1] = fma2(ex2_2(mul2(d2[k], a2[k][2 * j + 1])), hk[1], mul2(u2[k], pack2(b.z, b.w)));
+                }
+                if (!SUM) {
+                    const float4 c = b4[NP / 4 + j];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        ya[k] = fma2(h[k][2 * j], pack2(c.x, c.y), ya[k]);
+                        yb[k] = fma2(h[k][2 * j + 1], pack2(c.z, c.w), yb[k]);
+                    }
+                }
+            }
+            if (SUM) {
+                dsum.x += dl.x, dsum.y += dl.y;
+            } else {
+                const float2 r0 = unpack2(add2(ya[0], yb[0])), r1 = unpack2(add2(ya[1], yb[1]));
+                y = make_float2(r0.x + r0.y, r1.x + r1.y);
+            }
+        };
+        auto finish = [&](auto &y, int i) {
+#pragma unroll
+            for (int k = 0; k < (int)(sizeof(y) / sizeof(float2)); ++k) {
+#pragma unroll
+                for (int o = LN / 2; o > 0; o >>= 1) {
+                    y[k].x += __shfl_xor_sync(0xffffffffu, y[k].x, o);
+                    y[k].y += __shfl_xor_sync(0xffffffffu, y[k].y, o);
+                }
+                const float2 x = pair_at(i + k, 0);
+                float f[2] = {fmaf(dv.x, x.x, y[k].x), fmaf(dv.y, x.y, y[k].y)};
+                if (gate) {
+                    const float2 z = pair_at(i + k, 2), g = sigmoid2(z);
+                    f[0] *= z.x * g.x, f[1] *= z.y * g.y;
+                }
+                if (d < p.D && ln == 0) {
+                    if (vec) st_row_f<T, 2, true>(os + (i + k) * p.o_st, f, 2);
+                    else st_row_f<T, 2, false>(os + (i + k) * p.o_st, f, p.D - d);
+                }
+            }
+        };
+        int t = 0;
+        while (t < m) {
+            const int run = min(m, q.end - 1 - s);
+            if (t + K <= run) {
+                float2 dl[K], u[K], y[K];
+                prep(dl, u, t);
+#pragma unroll 1
+                for (; t + K <= run; t += K) {
+                    float2 dn[K], un[K];
+                    prep(dn, un, min(t + K, TS - K));  // past the run's end: not used
+#pragma unroll
+                    for (int k = 0; k < K; ++k) states(y[k], dl[k], u[k], t + k);
+                    if (!SUM) finish(y, t);
+#pragma unroll
+                    for (int k = 0; k < K; ++k) dl[k] = dn[k], u[k] = un[k];
+                }
+            }
+            // one by one up to the stage's or the sequence's end
+#pragma unroll 1
+            for (const int stop = min(m, t + K); t < stop; ++t) {
+                float2 dl[1], u[1], y[1];
+                prep(dl, u, t);
+                states(y[0], dl[0], u[0], t);
+                if (!SUM) finish(y, t);
+                if (s + t + 1 == q.end) {
+                    if (!SUM && p.h_final) st_pair<Q>(p.h_final + q.seg * hrow + own, h, p.N, nn, p.n_wide, on);
+                    if (q.end < p.T) {
+                        ssm_next(q, p.cu, p.n_seq, p.T, q.end);
+                        first_h(q.seg);
+                        if (s + t + 1 < t1) reset = true;
+                    }
+                }
+            }
+        }
+        buf = buf == 2 ? 0 : buf + 1, flip ^= 1;
+    }
+    if (SUM) {
+        st_pair<Q>(p.sums + ((int64_t)line * nch + chunk) * dnp + own_p, h, NP, Q, true, on);
+        // a chunk in which a sequence begins passes nothing on: marked by NaN
+        float *o = p.dsum + ((int64_t)line * nch + chunk) * p.D + d;
+        if (ln == 0 && d < p.D) o[0] = reset ? __int_as_float(0x7fffffff) : dsum.x;
+        if (ln == 0 && d + 1 < p.D) o[1] = reset ? __int_as_float(0x7fffffff) : dsum.y;
+    } else if (p.h_final && chunk == 0 && (p.cu || p.T == 0)) {
+        // sequences without a token pass their state on
+        for (int s = 0; s < p.n_seq; ++s) {
+            if (p.cu ? p.cu[s + 1] > p.cu[s] : s != line) continue;
+            first_h(s);
+            st_pair<Q>(p.h_final + s * hrow + own, h, p.N, nn, p.n_wide, on);
         }
     }
-    if (p.h_final) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (in && n0 + j < p.N) p.h_final[((int64_t)seq * p.D + d) * p.N + n0 + j] = h[j];
+}
+
+// The state entering chunk c + 1 replaces chunk c's sum: h <- exp(A sum
+// delta) h + S. One thread a (line, channel, state).
+__global__ void __launch_bounds__(256) ssm_chain_kernel(const SsmParams p, int np) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, dnp = (int64_t)p.D * np;
+    const int lines = p.cu ? 1 : p.B, nch = p.nchunk - 1;
+    if (i >= lines * dnp) return;
+    const int line = (int)(i / dnp), d = (int)(i % dnp / np), n = (int)(i % np);
+    const float a = n < p.N ? p.A[(int64_t)d * p.N + n] * kLog2e : 0.f;
+    float *s = p.sums + line * nch * dnp + i % dnp;
+    const float *q = p.dsum + (int64_t)line * nch * p.D + d;
+    float h = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < nch; ++c) {
+        const float v = q[(int64_t)c * p.D], e = s[c * dnp];
+        h = isnan(v) ? e : fmaf(ex2f(a * v), h, e);
+        s[c * dnp] = h;
     }
 }
 
@@ -85,14 +347,14 @@ __global__ void __launch_bounds__(128) ssm_step_kernel(const SsmStepParams p) {
     float *state = p.state + ((int64_t)slot * p.D + d) * p.N + n0;
     const float x = in ? ldf((const T *)p.x + i * p.x_st + d) : 0.f;
     float dl = in ? ldf((const T *)p.dt + i * p.dt_st + d) + (p.dt_bias ? p.dt_bias[d] : 0.f) : 0.f;
-    if (p.softplus) dl = softplus_f(dl);
+    if (p.softplus) dl = softplus2(make_float2(dl, dl)).x;
     const float u = dl * x;
     float y = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (!in || n0 + j >= p.N) continue;
         const float b = ldf((const T *)p.bm + i * p.bm_st + n0 + j), c = ldf((const T *)p.cm + i * p.cm_st + n0 + j);
-        const float h = fmaf(exp2f(dl * (p.A[(int64_t)d * p.N + n0 + j] * kLog2e)), state[j], u * b);
+        const float h = fmaf(ex2f(dl * (p.A[(int64_t)d * p.N + n0 + j] * kLog2e)), state[j], u * b);
         state[j] = h;
         y = fmaf(h, c, y);
     }
@@ -102,13 +364,30 @@ __global__ void __launch_bounds__(128) ssm_step_kernel(const SsmStepParams p) {
         if (p.Dv) y = fmaf(p.Dv[d], x, y);
         if (p.z) {
             const float z = ldf((const T *)p.z + i * p.z_st + d);
-            y *= z * sigmoid_f(z);
+            y *= z * sigmoid2(make_float2(z, z)).x;
         }
         ((T *)p.out)[i * p.o_st + d] = to_type<T>(y);
     }
 }
 
-// calls f with the lanes a channel as a constant
+template <typename T, int Q, int LN, bool SUM>
+cudaError_t scan_t(const SsmParams &p, cudaStream_t st) {
+    constexpr int CH = 2 * kThreads / LN;
+    constexpr int smem = 3 * (SUM ? 2 : 3) * kStage * CH * (int)sizeof(T) + 2 * kStage * 2 * Q * LN * 4;
+    const bool usual = p.vec && p.softplus && (SUM || p.z);
+    auto *k = usual ? ssm_scan_kernel<T, Q, LN, SUM, true> : ssm_scan_kernel<T, Q, LN, SUM, false>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    const int ntile = (p.D + CH - 1) / CH;
+    const int64_t items = (int64_t)(p.cu ? 1 : p.B) * (SUM ? p.nchunk - 1 : p.nchunk);
+    if (items * ntile > INT32_MAX) return cudaErrorInvalidValue;
+    k<<<(unsigned)(items * ntile), kThreads, smem, st>>>(p, ntile);
+    return cudaGetLastError();
+}
+
+// lanes a channel at four states a lane
 template <class F>
 cudaError_t by_lanes(int N, F &&f) {
     if (N <= 16) return f(std::integral_constant<int, 4>());
@@ -119,12 +398,36 @@ cudaError_t by_lanes(int N, F &&f) {
 
 }  // namespace
 
+// Chunks of a line, by the number of CTAs that whole lines give.
+void ssm_split(int lines, int T, int D, int N, int *nchunk, int *clen) {
+    const int ch = 2 * kThreads / ssm_lanes(N);
+    const int64_t ctas = (int64_t)lines * ((D + ch - 1) / ch);
+    // four CTAs a SM, in chunks of at least 64 tokens; whole lines from two a SM on
+    int64_t n = 1;
+    if (ctas < 304) {
+        n = 608 / ctas;
+        if (n > (T + 63) / 64) n = (T + 63) / 64;
+        if (n < 1) n = 1;
+    }
+    const int len = (int)(((T + n - 1) / n + kStage - 1) / kStage * kStage);
+    *clen = len > 0 ? len : kStage;
+    *nchunk = T > 0 ? (int)(((int64_t)T + *clen - 1) / *clen) : 1;
+}
+
+cudaError_t launch_ssm_sum(const SsmParams &p, cudaStream_t st) {
+    return ssm_by_states(p.N, [&](auto q, auto ln) {
+        return p.bf16 ? scan_t<__nv_bfloat16, q(), ln(), true>(p, st) : scan_t<float, q(), ln(), true>(p, st);
+    });
+}
+cudaError_t launch_ssm_chain(const SsmParams &p, cudaStream_t st) {
+    const int np = ssm_np(p.N);
+    const int64_t n = (int64_t)(p.cu ? 1 : p.B) * p.D * np;
+    ssm_chain_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(p, np);
+    return cudaGetLastError();
+}
 cudaError_t launch_ssm_scan(const SsmParams &p, cudaStream_t st) {
-    return by_lanes(p.N, [&](auto ln) {
-        const dim3 grid((p.D + 128 / ln() - 1) / (128 / ln()), p.n_seq);
-        if (p.bf16) ssm_scan_kernel<__nv_bfloat16, ln()><<<grid, 128, 0, st>>>(p);
-        else ssm_scan_kernel<float, ln()><<<grid, 128, 0, st>>>(p);
-        return cudaGetLastError();
+    return ssm_by_states(p.N, [&](auto q, auto ln) {
+        return p.bf16 ? scan_t<__nv_bfloat16, q(), ln(), false>(p, st) : scan_t<float, q(), ln(), false>(p, st);
     });
 }
 cudaError_t launch_ssm_step(const SsmStepParams &p, cudaStream_t st) {
