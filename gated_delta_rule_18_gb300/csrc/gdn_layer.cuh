@@ -203,7 +203,7 @@ cudaError_t launch_conv_step(const ConvStepParams &p, cudaStream_t st);
 
 // ------------------------------------------------------ selective scan ------
 constexpr int kSsmMaxN = 128;
-constexpr int kSsmCkpt = 16;  // tokens between the gradient's state checkpoints
+constexpr int kSsmGroup = 32;  // the gradient keeps the state entering every group of so many tokens
 struct SsmParams {
     const void *x, *dt, *bm, *cm, *z;  // (B, T, D); bm, cm (B, T, N); z or null
     int64_t x_sb, x_st, dt_sb, dt_st, bm_sb, bm_st, cm_sb, cm_st, z_sb, z_st;
@@ -227,13 +227,21 @@ struct SsmParams {
     const float *dh_final;
     void *dx, *ddt, *dbm, *dcm, *dz;
     float *dA, *dD, *ddt_bias, *dh0;
-    float *ckpt, *part_bc, *part_a, *part_d;  // workspace
+    // runs of a line, tokens a run, groups of a line; workspace: sums and dsum
+    // by group, the same sums of delta for the runs (gsum), the runs' gradients
+    // (lines, nrun, D, padded N), partial sums by channel tile and by run
+    int nrun, rlen, ngroup;
+    float *gsum, *gs, *part_bc, *part_a, *part_d;
 };
 void ssm_split(int lines, int T, int D, int N, int *nchunk, int *clen);
 cudaError_t launch_ssm_sum(const SsmParams &p, cudaStream_t st);
 cudaError_t launch_ssm_chain(const SsmParams &p, cudaStream_t st);
 cudaError_t launch_ssm_scan(const SsmParams &p, cudaStream_t st);
 int ssm_bwd_tiles(int D, int N);
+int ssm_bwd_run(int lines, int T, int D, int N);
+cudaError_t launch_ssm_bwd_sum(const SsmParams &p, cudaStream_t st);
+cudaError_t launch_ssm_bwd_chain(const SsmParams &p, cudaStream_t st);
+cudaError_t launch_ssm_bwd_empty(const SsmParams &p, cudaStream_t st);
 cudaError_t launch_ssm_bwd(const SsmParams &p, cudaStream_t st);
 cudaError_t launch_ssm_bwd_reduce(const SsmParams &p, cudaStream_t st);
 struct SsmStepParams {

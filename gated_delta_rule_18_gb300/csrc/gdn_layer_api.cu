@@ -52,25 +52,33 @@ SsmWs ssm_ws(int lines, int T, int D, int N) {
     return L;
 }
 struct SsmBwdWs {
-    size_t ckpt, bc, a, d, total;
+    int nrun, rlen, ngroup;
+    size_t sums, dsum, gsum, gs, bc, a, d, total;
 };
 bool ssm_shape_ok(int B, int T, int D, int N, int n_seq, int varlen) {
     if (B < 1 || B > 65535 || T < 0 || D < 1 || D > (1 << 20) || N < 1 || N > kSsmMaxN) return false;
-    return varlen ? B == 1 && n_seq >= 1 && n_seq <= 65535 : n_seq == B;
+    return varlen ? B == 1 && n_seq >= 1 : n_seq == B;
 }
-SsmBwdWs ssm_bwd_ws(int B, int T, int D, int N, int n_seq, int varlen) {
+SsmBwdWs ssm_bwd_ws(int B, int T, int D, int N, int varlen) {
     SsmBwdWs L;
-    const int np = N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 64 : 128;
-    const size_t groups = varlen ? (size_t)T / kSsmCkpt + n_seq + 1 : (size_t)B * (T / kSsmCkpt + 1);
+    const int lines = varlen ? 1 : B;
+    L.rlen = ssm_bwd_run(lines, T, D, N);
+    L.nrun = (T + L.rlen - 1) / L.rlen;
+    L.ngroup = (T + kSsmGroup - 1) / kSsmGroup;
+    const size_t groups = (size_t)lines * L.ngroup, runs = (size_t)lines * L.nrun, dnp = (size_t)D * ssm_np(N);
     size_t off = kAlign;
-    L.ckpt = off;
-    off = align_up(off + groups * D * np * 4);
-    L.bc = off;
-    off = align_up(off + (size_t)ssm_bwd_tiles(D, N) * B * T * 2 * N * 4);
-    L.a = off;
-    off = align_up(off + (size_t)n_seq * D * N * 4);
-    L.d = off;
-    off = align_up(off + (size_t)n_seq * 2 * D * 4);
+    auto take = [&](size_t floats) {
+        const size_t at = off;
+        off = align_up(off + floats * 4);
+        return at;
+    };
+    L.sums = take(groups * dnp);
+    L.dsum = take(groups * D);
+    L.gsum = take(groups * D);
+    L.gs = take(runs * dnp);
+    L.bc = take((size_t)ssm_bwd_tiles(D, N) * B * T * 2 * N);
+    L.a = take(runs * D * N);
+    L.d = take(runs * 2 * D);
     L.total = off;
     return L;
 }
@@ -314,7 +322,7 @@ gdn_status gdn_ssm_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *dt
 
 size_t gdn_ssm_bwd_workspace_size(int B, int T, int D, int N, int n_seq, int varlen) {
     if (!ssm_shape_ok(B, T, D, N, n_seq, varlen)) return 0;
-    return ssm_bwd_ws(B, T, D, N, n_seq, varlen).total;
+    return ssm_bwd_ws(B, T, D, N, varlen).total;
 }
 
 gdn_status gdn_ssm_bwd(const void *x, int64_t x_sb, int64_t x_st, const void *dt, int64_t dt_sb, int64_t dt_st,
@@ -342,28 +350,40 @@ gdn_status gdn_ssm_bwd(const void *x, int64_t x_sb, int64_t x_st, const void *dt
     for (const void *f : {(const void *)dh_final, (const void *)dA, (const void *)dD, (const void *)ddt_bias,
                           (const void *)dh0})
         if (!f32_ok(f)) return GDN_ERR_LAYOUT;
-    const SsmBwdWs L = ssm_bwd_ws(B, T, D, N, n_seq, cu_seqlens != nullptr);
+    const SsmBwdWs L = ssm_bwd_ws(B, T, D, N, cu_seqlens != nullptr);
     if (!ws_ok(workspace, ws_bytes, L.total)) return GDN_ERR_WORKSPACE;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     p.dout = dout, p.do_sb = dout_sb, p.do_st = dout_st, p.dh_final = dh_final;
     p.dx = dx, p.ddt = ddt, p.dbm = dbm, p.dcm = dcm, p.dz = dz;
     p.dA = dA, p.dD = dD, p.ddt_bias = ddt_bias, p.dh0 = dh0;
-    p.ckpt = reinterpret_cast<float *>(ws + L.ckpt);
-    p.part_bc = reinterpret_cast<float *>(ws + L.bc);
-    p.part_a = reinterpret_cast<float *>(ws + L.a);
-    p.part_d = reinterpret_cast<float *>(ws + L.d);
+    auto at = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
+    p.nrun = L.nrun, p.rlen = L.rlen, p.ngroup = L.ngroup;
+    p.sums = at(L.sums), p.dsum = at(L.dsum), p.gsum = at(L.gsum), p.gs = at(L.gs);
+    p.part_bc = at(L.bc), p.part_a = at(L.a), p.part_d = at(L.d);
     p.err = cu_seqlens ? reinterpret_cast<int *>(ws) : nullptr;
-    cudaError_t e = launch(KSsmBwd, stream, [&] { return launch_ssm_bwd(p, stream); });
-    if (e == cudaSuccess && T > 0) e = launch(KSsmBwdReduce, stream, [&] { return launch_ssm_bwd_reduce(p, stream); });
+    p.vec = r.wide && D % 8 == 0;
+    p.n_wide = p.n_wide && addr(dh_final) % 16 == 0 && addr(dh0) % 16 == 0;
+    cudaError_t e = cudaSuccess;
+    auto run = [&](int kind, cudaError_t (*f)(const SsmParams &, cudaStream_t)) {
+        if (e == cudaSuccess) e = launch(kind, stream, [&] { return f(p, stream); });
+    };
+    auto sum = [&](const float *in, int64_t ld, int64_t n, float *out, int64_t n2, float *out2) {
+        if (e == cudaSuccess)
+            e = launch(KColSum, stream, [&] {
+                return launch_col_sum(in, ld, (cu_seqlens ? 1 : B) * L.nrun, n, out, n2, out2, stream);
+            });
+    };
+    if (T > 0) {
+        run(KSsmBwdSum, launch_ssm_bwd_sum);
+        run(KSsmBwdChain, launch_ssm_bwd_chain);
+        run(KSsmBwd, launch_ssm_bwd);
+        run(KSsmBwdReduce, launch_ssm_bwd_reduce);
+    }
+    if (dh0 && (cu_seqlens || T == 0)) run(KSsmBwdEmpty, launch_ssm_bwd_empty);
     const int64_t dn = (int64_t)D * N;
-    if (e == cudaSuccess)
-        e = launch(KColSum, stream, [&] { return launch_col_sum(p.part_a, dn, n_seq, dn, dA, 0, nullptr, stream); });
-    // without dD the bias' columns follow by themselves
-    if (e == cudaSuccess && (dD || ddt_bias))
-        e = launch(KColSum, stream, [&] {
-            return dD ? launch_col_sum(p.part_d, 2 * D, n_seq, D, dD, ddt_bias ? D : 0, ddt_bias, stream)
-                      : launch_col_sum(p.part_d + D, 2 * D, n_seq, D, ddt_bias, 0, nullptr, stream);
-        });
+    sum(p.part_a, dn, dn, dA, 0, nullptr);
+    if (dD) sum(p.part_d, 2 * D, D, dD, ddt_bias ? D : 0, ddt_bias);
+    else if (ddt_bias) sum(p.part_d + D, 2 * D, D, ddt_bias, 0, nullptr);
     return cuda_status(e);
 }
 

@@ -23,52 +23,6 @@ namespace {
 constexpr int kThreads = 64;  // a CTA: 2 * 64 / LN channels
 constexpr int kStage = 16;    // tokens a stage
 
-// Q neighbouring states of a channel, in pairs
-template <int Q>
-__device__ __forceinline__ void ld_states(f32x2 (&v)[Q / 2], const float *p, int n, bool wide) {
-#pragma unroll
-    for (int j = 0; j < Q / 4; ++j) {
-        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (wide) {
-            if (4 * j < n) f = reinterpret_cast<const float4 *>(p)[j];
-        } else {
-            if (4 * j < n) f.x = p[4 * j];
-            if (4 * j + 1 < n) f.y = p[4 * j + 1];
-            if (4 * j + 2 < n) f.z = p[4 * j + 2];
-            if (4 * j + 3 < n) f.w = p[4 * j + 3];
-        }
-        v[2 * j] = pack2(f.x, f.y), v[2 * j + 1] = pack2(f.z, f.w);
-    }
-}
-template <int Q>
-__device__ __forceinline__ void st_states(float *p, const f32x2 (&v)[Q / 2], int n, bool wide) {
-#pragma unroll
-    for (int j = 0; j < Q / 4; ++j) {
-        const float2 a = unpack2(v[2 * j]), b = unpack2(v[2 * j + 1]);
-        if (wide) {
-            if (4 * j < n) reinterpret_cast<float4 *>(p)[j] = make_float4(a.x, a.y, b.x, b.y);
-        } else {
-            if (4 * j < n) p[4 * j] = a.x;
-            if (4 * j + 1 < n) p[4 * j + 1] = a.y;
-            if (4 * j + 2 < n) p[4 * j + 2] = b.x;
-            if (4 * j + 3 < n) p[4 * j + 3] = b.y;
-        }
-    }
-}
-// of the two channels at p and p + ld; on: which of them exist
-template <int Q>
-__device__ __forceinline__ void ld_pair(f32x2 (&v)[2][Q / 2], const float *p, int ld, int n, bool wide,
-                                        const bool (&on)[2]) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) ld_states<Q>(v[k], p + k * ld, on[k] ? n : 0, wide);
-}
-template <int Q>
-__device__ __forceinline__ void st_pair(float *p, const f32x2 (&v)[2][Q / 2], int ld, int n, bool wide,
-                                        const bool (&on)[2]) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) st_states<Q>(p + k * ld, v[k], on[k] ? n : 0, wide);
-}
-
 // A lane has Q states, in packed pairs, of two neighbouring channels; LN lanes
 // a channel (LN = 1 up to 16 states, so nothing crosses lanes there). x, dt and z
 // come through a ring of three stages of shared memory, two stages ahead of
@@ -78,13 +32,8 @@ __device__ __forceinline__ void st_pair(float *p, const f32x2 (&v)[2][Q / 2], in
 template <typename T, int Q, int LN, bool SUM, bool USUAL>
 __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const SsmParams p, int ntile) {
     constexpr int CH = 2 * kThreads / LN, NP = Q * LN, TS = kStage, K = 1;  // K: tokens in flight
-    constexpr int VE = 16 / sizeof(T);           // elements of a 16-byte copy
-    constexpr int NA = SUM ? 2 : 3;              // x, dt, z
-    constexpr int kRow = CH * (int)sizeof(T), kTile = TS * kRow, kBuf = NA * kTile;
-    constexpr int kCopies = TS * CH / VE;        // 16-byte copies of a tile
-    constexpr int kBc = TS * 2 * NP;             // B and C values of a stage
-    constexpr int VB = kBc / kThreads < 4 ? kBc / kThreads : 4;  // values of a B, C load
-    constexpr int NBC = kBc / (kThreads * VB), WB = RowVec<T, VB>::kWords;
+    constexpr int NA = SUM ? 2 : 3;  // x, dt, z
+    constexpr int kTile = TS * CH * (int)sizeof(T), kBuf = NA * kTile, kBc = TS * 2 * NP;
     extern __shared__ __align__(16) unsigned char smem[];
     float *bcs = reinterpret_cast<float *>(smem + 3 * kBuf);  // [2][TS][2][NP]
     const int tid = threadIdx.x, ch = tid / LN * 2, ln = tid % LN;
@@ -131,51 +80,17 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const SsmParams p, i
     auto fetch = [&](int s, int b) {  // the stage that begins at token s into buffer b
         if (s < t1) {
 #pragma unroll
-            for (int a = 0; a < NA; ++a) {
-                if (a >= na) break;
-                if (vec) {
-#pragma unroll
-                    for (int i = 0; i < (kCopies + kThreads - 1) / kThreads; ++i) {
-                        const int e = tid + i * kThreads, r = e / (CH / VE), c = e % (CH / VE) * VE;
-                        if ((kCopies % kThreads == 0 || e < kCopies) && s + r < t1 && c0 + c < p.D)
-                            cp_async16(smem + b * kBuf + a * kTile + r * kRow + c * (int)sizeof(T),
-                                       src[a] + (s + r) * str[a] + c0 + c, 16);
-                    }
-                } else {
-                    T *dst = reinterpret_cast<T *>(smem + b * kBuf + a * kTile);
-                    for (int e = tid; e < TS * CH; e += kThreads) {
-                        const int r = e / CH, c = e % CH;
-                        // zeros past the last channel: a pair's halves share a reciprocal
-                        dst[e] = s + r < t1 && c0 + c < p.D ? src[a][(s + r) * str[a] + c0 + c] : to_type<T>(0.f);
-                    }
-                }
-            }
+            for (int a = 0; a < NA; ++a)
+                if (a < na)
+                    ssm_fetch_tile<T, CH, TS, kThreads>(reinterpret_cast<T *>(smem + b * kBuf + a * kTile),
+                                                        src[a] + s * str[a], str[a], t1 - s, c0, p.D, vec);
         }
         cp_async_commit();
     };
     const T *bg = (const T *)p.bm + line * p.bm_sb, *cg = (const T *)p.cm + line * p.cm_sb;
-    uint32_t nbc[NBC][WB];  // as stored: converted where they are staged, not where they are loaded
+    SsmBc<T, NP, TS, kThreads> nbc;
     auto fetch_bc = [&](int s) {
-#pragma unroll
-        for (int i = 0; i < NBC; ++i) {
-            const int e = (tid + i * kThreads) * VB, r = e / (2 * NP), k = e % (2 * NP), n = k % NP;
-#pragma unroll
-            for (int w = 0; w < WB; ++w) nbc[i][w] = 0u;
-            if (s + r < t1 && n < p.N && !(SUM && k >= NP)) {
-                const T *at = k < NP ? bg + (s + r) * p.bm_st + n : cg + (s + r) * p.cm_st + n;
-                if (p.bc_vec) ld_row<T, VB, true>(nbc[i], at, p.N - n);
-                else ld_row<T, VB, false>(nbc[i], at, p.N - n);
-            }
-        }
-    };
-    auto stage_bc = [&](float *dst) {
-#pragma unroll
-        for (int i = 0; i < NBC; ++i) {
-            float f[VB];
-            words_to_f<T, VB>(f, nbc[i]);
-#pragma unroll
-            for (int k = 0; k < VB; ++k) dst[(tid + i * kThreads) * VB + k] = f[k];
-        }
+        nbc.template fetch<!SUM>(bg + s * p.bm_st, p.bm_st, cg + s * p.cm_st, p.cm_st, t1 - s, p.N, p.bc_vec);
     };
     if (t0 < t1) {
         fetch(t0, 0);
@@ -186,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const SsmParams p, i
     int buf = 0, flip = 0;
     for (int s = t0; s < t1; s += TS) {
         float *bc = bcs + flip * kBc;
-        stage_bc(bc);
+        nbc.stage(bc);
         if (s + TS < t1) fetch_bc(s + TS);
         cp_async_wait<1>();
         __syncthreads();

@@ -130,6 +130,107 @@ __device__ __forceinline__ void ssm_check_cu(const int32_t *cu, int n_seq, int T
     if (threadIdx.x == 0) *err = bad ? 1 : 0;
 }
 
+// ------------------------------------------------------------ staging -------
+// `rows` rows of CH channels from channel c0 on into shared memory (row
+// stride CH), by 16-byte asynchronous copies or, for rows that are not
+// aligned, by element. Channels past D and rows past `rows` are zeros (a
+// pair's halves share a reciprocal, a warp's channels the sums of dB and dC).
+// NT threads take part.
+template <typename T, int CH, int TS, int NT>
+__device__ __forceinline__ void ssm_fetch_tile(T *dst, const T *src, int64_t stride, int rows, int c0, int D, bool vec) {
+    constexpr int VE = 16 / sizeof(T), kCopies = TS * CH / VE;
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < (kCopies + NT - 1) / NT; ++i) {
+            const int e = threadIdx.x + i * NT, r = e / (CH / VE), c = e % (CH / VE) * VE;
+            const bool in = r < rows && c0 + c < D;
+            if (kCopies % NT == 0 || e < kCopies) cp_async16(dst + r * CH + c, in ? src + r * stride + c0 + c : src, in ? 16 : 0);
+        }
+    } else {
+        for (int e = threadIdx.x; e < TS * CH; e += NT) {
+            const int r = e / CH, c = e % CH;
+            dst[e] = r < rows && c0 + c < D ? src[r * stride + c0 + c] : to_type<T>(0.f);
+        }
+    }
+}
+// The (B, C) rows of TS tokens, [TS][2][NP] fp32 in shared memory: loaded as
+// stored into registers by fetch, converted where they are staged.
+template <typename T, int NP, int TS, int NT>
+struct SsmBc {
+    static constexpr int kVals = TS * 2 * NP, V = kVals / NT < 4 ? kVals / NT : 4, kLoads = kVals / (NT * V);
+    uint32_t w[kLoads][RowVec<T, V>::kWords];
+    template <bool WITH_C>
+    __device__ __forceinline__ void fetch(const T *bg, int64_t b_st, const T *cg, int64_t c_st, int rows, int N, bool vec) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int e = (threadIdx.x + i * NT) * V, r = e / (2 * NP), k = e % (2 * NP), n = k % NP;
+#pragma unroll
+            for (int j = 0; j < RowVec<T, V>::kWords; ++j) w[i][j] = 0u;
+            if (r < rows && n < N && (WITH_C || k < NP)) {
+                const T *at = k < NP ? bg + r * b_st + n : cg + r * c_st + n;
+                if (vec) ld_row<T, V, true>(w[i], at, N - n);
+                else ld_row<T, V, false>(w[i], at, N - n);
+            }
+        }
+    }
+    __device__ __forceinline__ void stage(float *dst) const {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            float f[V];
+            words_to_f<T, V>(f, w[i]);
+#pragma unroll
+            for (int k = 0; k < V; ++k) dst[(threadIdx.x + i * NT) * V + k] = f[k];
+        }
+    }
+};
+
+// ------------------------------------------------------------- states -------
+// Q neighbouring states of a channel, in pairs
+template <int Q>
+__device__ __forceinline__ void ld_states(f32x2 (&v)[Q / 2], const float *p, int n, bool wide) {
+#pragma unroll
+    for (int j = 0; j < Q / 4; ++j) {
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (wide) {
+            if (4 * j < n) f = reinterpret_cast<const float4 *>(p)[j];
+        } else {
+            if (4 * j < n) f.x = p[4 * j];
+            if (4 * j + 1 < n) f.y = p[4 * j + 1];
+            if (4 * j + 2 < n) f.z = p[4 * j + 2];
+            if (4 * j + 3 < n) f.w = p[4 * j + 3];
+        }
+        v[2 * j] = pack2(f.x, f.y), v[2 * j + 1] = pack2(f.z, f.w);
+    }
+}
+template <int Q>
+__device__ __forceinline__ void st_states(float *p, const f32x2 (&v)[Q / 2], int n, bool wide) {
+#pragma unroll
+    for (int j = 0; j < Q / 4; ++j) {
+        const float2 a = unpack2(v[2 * j]), b = unpack2(v[2 * j + 1]);
+        if (wide) {
+            if (4 * j < n) reinterpret_cast<float4 *>(p)[j] = make_float4(a.x, a.y, b.x, b.y);
+        } else {
+            if (4 * j < n) p[4 * j] = a.x;
+            if (4 * j + 1 < n) p[4 * j + 1] = a.y;
+            if (4 * j + 2 < n) p[4 * j + 2] = b.x;
+            if (4 * j + 3 < n) p[4 * j + 3] = b.y;
+        }
+    }
+}
+// of the two channels at p and p + ld; on: which of them exist
+template <int Q>
+__device__ __forceinline__ void ld_pair(f32x2 (&v)[2][Q / 2], const float *p, int ld, int n, bool wide,
+                                        const bool (&on)[2]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) ld_states<Q>(v[k], p + k * ld, on[k] ? n : 0, wide);
+}
+template <int Q>
+__device__ __forceinline__ void st_pair(float *p, const f32x2 (&v)[2][Q / 2], int ld, int n, bool wide,
+                                        const bool (&on)[2]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) st_states<Q>(p + k * ld, v[k], on[k] ? n : 0, wide);
+}
+
 // States a lane and lanes a channel: NP = Q LN >= N.
 template <class F>
 cudaError_t ssm_by_states(int N, F &&f) {

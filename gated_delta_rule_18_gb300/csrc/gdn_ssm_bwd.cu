@@ -5,155 +5,544 @@
 //   ddelta = sum_n A a h_{t-1} g + x sum_n B g,  dA = sum_t delta a h_{t-1} g,
 //   ddt = ddelta sigmoid(dt + bias),  dz = dout y silu'(z),  dh0 = a_0 g_0.
 //
-// One CTA walks a sequence's channels forward, keeping the state every 16
-// tokens, then back, recomputing 16 tokens' states at a time in registers.
-// Sums over channels (dB, dC) and over sequences (dA, dD, dbias) leave
-// partial sums that a second kernel adds in a fixed order.
-#include "gdn_layer.cuh"
+// The line of tokens is cut into runs, a run into groups of 32 tokens:
+//   ssm_bwd_sum   per group the state from zero and the sum of delta, per run
+//                 the gradient that reaches its start from its own tokens
+//                 (sum over t of prod_{s <= t} a_s C_t dy_t);
+//   ssm_bwd_chain both chained: the state entering every group, the gradient
+//                 leaving every run;
+//   ssm_bwd       one CTA walks a run back group by group: states forward
+//                 with a checkpoint every four tokens, then back four at a
+//                 time, the four tokens' entering states and decays in
+//                 registers;
+//   ssm_bwd_reduce  dB and dC over the channel tiles; dA, dD and dbias over
+//                 the runs (col_sum). No atomics: every sum has one order.
+// Bound by instruction issue and the fp32 pipe: the states' decays are formed
+// three times (12 cycles an element on the exponential unit) and the walk back
+// has ten packed operations an element pair.
+#include "gdn_ssm.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float softplus_f(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+constexpr int kNT = 64;      // threads of every CTA here
+constexpr int kGroup = kSsmGroup;
+constexpr int kStage = 16;   // tokens a stage of the sums
 
-template <typename T, int LN>
-__global__ void __launch_bounds__(128) ssm_bwd_kernel(const SsmParams p) {
-    constexpr int CH = 128 / LN, L = kSsmCkpt;
-    __shared__ float red[4][2 * 4 * LN];
-    const int seq = blockIdx.y;
-    const int d = blockIdx.x * CH + threadIdx.x / LN, n0 = threadIdx.x % LN * 4;
-    const bool in = d < p.D;
-    if (p.err && blockIdx.x == 0 && seq == 0) {
-        int bad = 0;
-        for (int s = threadIdx.x; s < p.n_seq; s += 128) bad |= p.cu[s + 1] < p.cu[s];
-        if (threadIdx.x == 0) bad |= p.cu[0] != 0 || p.cu[p.n_seq] != p.T;
-        bad = __syncthreads_or(bad);
-        if (threadIdx.x == 0) *p.err = bad;
-    }
-    const int row = p.cu ? 0 : seq;
-    const int t0 = p.cu ? min(max(p.cu[seq], 0), p.T) : 0, t1 = p.cu ? min(p.cu[seq + 1], p.T) : p.T;
-    // checkpoints of a sequence start at (its first token / L + sequence): one more than its whole groups fits
-    const int64_t ck0 = p.cu ? t0 / L + seq : (int64_t)seq * (p.T / L + 1);
-    float a1[4], a2[4], h[4], g[4], dA[4];
+// ------------------------------------------------------------ sums ----------
+template <typename T, int Q, int LN, bool USUAL>
+__global__ void __launch_bounds__(kNT) ssm_bwd_sum_kernel(const SsmParams p, int ntile) {
+    constexpr int CH = 2 * kNT / LN, NP = Q * LN, TS = kStage, NA = 4;  // x, dt, z, dout
+    constexpr int kTile = TS * CH * (int)sizeof(T), kBuf = NA * kTile, kBc = TS * 2 * NP;
+    extern __shared__ __align__(16) unsigned char smem[];
+    float *bcs = reinterpret_cast<float *>(smem + 3 * kBuf);  // [2][TS][2][NP]
+    const int tid = threadIdx.x, ch = tid / LN * 2, ln = tid % LN;
+    const int tile = blockIdx.x % ntile, item = blockIdx.x / ntile;
+    const int line = item / p.nrun, run = item - line * p.nrun;
+    if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
+    const int t0 = run * p.rlen, t1 = min(p.T - t0, p.rlen) + t0;
+    const int c0 = tile * CH, d = c0 + ch, n0 = ln * Q, nn = p.N - n0;
+    const bool on[2] = {d < p.D && nn > 0, d + 1 < p.D && nn > 0};
+    const int64_t hrow = (int64_t)p.D * p.N, dnp = (int64_t)p.D * NP;
+    const int64_t own = (int64_t)d * p.N + n0, own_p = (int64_t)d * NP + n0;
+    const bool softplus = USUAL || p.softplus, gate = USUAL || p.z, vec = USUAL || p.vec;
+
+    f32x2 a2[2][Q / 2], h[2][Q / 2], g[2][Q / 2], w[2][Q / 2];  // w: the decay since the run's start
+    ld_pair<Q>(a2, p.A + own, p.N, nn, p.n_wide, on);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const bool on = in && n0 + j < p.N;
-        a1[j] = on ? p.A[(int64_t)d * p.N + n0 + j] : 0.f;
-        a2[j] = a1[j] * kLog2e;
-        h[j] = on && p.h0 ? p.h0[((int64_t)seq * p.D + d) * p.N + n0 + j] : 0.f;
-        g[j] = on && p.dh_final ? p.dh_final[((int64_t)seq * p.D + d) * p.N + n0 + j] : 0.f;
-        dA[j] = 0.f;
-    }
-    const float dv = in && p.Dv ? p.Dv[d] : 0.f, bias = in && p.dt_bias ? p.dt_bias[d] : 0.f;
-    auto token = [&](int t, float &x, float &v, float &dl, float (&b)[4], float (&c)[4]) {
-        x = in ? ldf((const T *)p.x + row * p.x_sb + t * p.x_st + d) : 0.f;
-        v = in ? ldf((const T *)p.dt + row * p.dt_sb + t * p.dt_st + d) + bias : 0.f;
-        dl = p.softplus ? softplus_f(v) : v;
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            b[j] = n0 + j < p.N ? ldf((const T *)p.bm + row * p.bm_sb + t * p.bm_st + n0 + j) : 0.f;
-            c[j] = n0 + j < p.N ? ldf((const T *)p.cm + row * p.cm_sb + t * p.cm_st + n0 + j) : 0.f;
+        for (int j = 0; j < Q / 2; ++j) {
+            a2[k][j] = mul2(a2[k][j], pack2(kLog2e, kLog2e));
+            g[k][j] = pack2(0.f, 0.f), w[k][j] = pack2(1.f, 1.f);
+        }
+    const float2 bias = make_float2(p.dt_bias && d < p.D ? p.dt_bias[d] : 0.f,
+                                    p.dt_bias && d + 1 < p.D ? p.dt_bias[d + 1] : 0.f);
+    auto first_h = [&](int seg, bool zero) {
+        if (p.h0 && !zero) {
+            ld_pair<Q>(h, p.h0 + seg * hrow + own, p.N, nn, p.n_wide, on);
+        } else {
+#pragma unroll
+            for (int j = 0; j < Q / 2; ++j) h[0][j] = h[1][j] = pack2(0.f, 0.f);
         }
     };
-    float x, v, dl, b[4], c[4];
-    for (int t = t0; t < t1; ++t) {
-        if ((t - t0) % L == 0 && in) {
-            float *ck = p.ckpt + ((ck0 + (t - t0) / L) * p.D + d) * (LN * 4) + n0;
-            *reinterpret_cast<float4 *>(ck) = make_float4(h[0], h[1], h[2], h[3]);
+    SsmSeq q = ssm_find(p.cu, p.n_seq, p.T, line, t0);
+    bool reset = q.starts, alive = true;
+    first_h(q.seg, !q.starts);
+
+    const T *src[4] = {(const T *)p.x + line * p.x_sb, (const T *)p.dt + line * p.dt_sb,
+                       (const T *)p.z + line * p.z_sb, (const T *)p.dout + line * p.do_sb};
+    const int64_t str[4] = {p.x_st, p.dt_st, p.z_st, p.do_st};
+    auto fetch = [&](int s, int b) {
+        if (s < t1) {
+#pragma unroll
+            for (int a = 0; a < NA; ++a)
+                if (a != 2 || gate)
+                    ssm_fetch_tile<T, CH, TS, kNT>(reinterpret_cast<T *>(smem + b * kBuf + a * kTile),
+                                                   src[a] + s * str[a], str[a], t1 - s, c0, p.D, vec);
         }
-        token(t, x, v, dl, b, c);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = fmaf(exp2f(dl * a2[j]), h[j], dl * x * b[j]);
-    }
-    float dD = 0.f, dbias = 0.f;
-    for (int q = (t1 - t0 + L - 1) / L - 1; q >= 0; --q) {
-        const int s = t0 + q * L, e = min(s + L, t1);
-        float hs[L + 1][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) hs[0][j] = 0.f;
-        if (in) {
-            const float4 k = *reinterpret_cast<const float4 *>(p.ckpt + ((ck0 + q) * p.D + d) * (LN * 4) + n0);
-            hs[0][0] = k.x, hs[0][1] = k.y, hs[0][2] = k.z, hs[0][3] = k.w;
-        }
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            if (s + i < e) token(s + i, x, v, dl, b, c);
-            else x = v = dl = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) hs[i + 1][j] = fmaf(exp2f(dl * a2[j]), hs[i][j], dl * x * b[j]);
-        }
-#pragma unroll
-        for (int i = L - 1; i >= 0; --i) {
-            const int t = s + i;
-            if (t >= e) continue;
-            token(t, x, v, dl, b, c);
-            const float go = in ? ldf((const T *)p.dout + row * p.do_sb + t * p.do_st + d) : 0.f;
-            const float z = in && p.z ? ldf((const T *)p.z + row * p.z_sb + t * p.z_st + d) : 0.f;
-            const float sz = sigmoid_f(z);
-            const float dy = p.z ? go * z * sz : go;
-            float y = 0.f, gb = 0.f, gd = 0.f, rb[4], rc[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                y = fmaf(hs[i + 1][j], c[j], y);
-                g[j] = fmaf(c[j], dy, g[j]);
-                gb = fmaf(g[j], b[j], gb);
-                rb[j] = dl * x * g[j];
-                rc[j] = dy * hs[i + 1][j];
-                g[j] *= exp2f(dl * a2[j]);
-                const float k = g[j] * hs[i][j];
-                gd = fmaf(k, a1[j], gd);
-                dA[j] = fmaf(k, dl, dA[j]);
+        cp_async_commit();
+    };
+    const T *bg = (const T *)p.bm + line * p.bm_sb, *cg = (const T *)p.cm + line * p.cm_sb;
+    SsmBc<T, NP, TS, kNT> nbc;
+    auto fetch_bc = [&](int s) {
+        nbc.template fetch<true>(bg + s * p.bm_st, p.bm_st, cg + s * p.cm_st, p.cm_st, t1 - s, p.N, p.bc_vec);
+    };
+    fetch(t0, 0);
+    fetch(t0 + TS, 1);
+    fetch_bc(t0);
+    float *gs = p.gs + ((int64_t)line * p.nrun + run) * dnp + own_p;
+    float2 dsum = make_float2(0.f, 0.f);
+    int buf = 0, flip = 0;
+    for (int s = t0; s < t1; s += TS) {
+        float *bc = bcs + flip * kBc;
+        nbc.stage(bc);
+        if (s + TS < t1) fetch_bc(s + TS);
+        cp_async_wait<1>();
+        __syncthreads();
+        fetch(s + 2 * TS, buf == 0 ? 2 : buf - 1);
+        const int m = min(t1 - s, TS);
+        const T *xs = reinterpret_cast<const T *>(smem + buf * kBuf) + ch;
+        auto pair_at = [&](int i, int a) {
+            float f[2];
+            ld_row_f<T, 2, true>(f, xs + (a * TS + i) * CH, 2);
+            return make_float2(f[0], f[1]);
+        };
+#pragma unroll 1
+        for (int t = 0; t < m; ++t) {
+            const float2 x = pair_at(t, 0), v = pair_at(t, 1);
+            float2 dl = make_float2(v.x + bias.x, v.y + bias.y), dy = pair_at(t, 3);
+            if (softplus) dl = softplus2(dl);
+            if (gate) {
+                const float2 z = pair_at(t, 2), sg = sigmoid2(z);
+                dy.x *= z.x * sg.x, dy.y *= z.y * sg.y;
             }
+            dsum.x += dl.x, dsum.y += dl.y;
+            const float4 *b4 = reinterpret_cast<const float4 *>(bc + t * 2 * NP + n0);
+            const f32x2 d2[2] = {pack2(dl.x, dl.x), pack2(dl.y, dl.y)};
+            const f32x2 u2[2] = {pack2(dl.x * x.x, dl.x * x.x), pack2(dl.y * x.y, dl.y * x.y)};
+            const f32x2 y2[2] = {pack2(dy.x, dy.x), pack2(dy.y, dy.y)};
 #pragma unroll
-            for (int o = LN / 2; o > 0; o >>= 1) {
-                y += __shfl_xor_sync(0xffffffffu, y, o);
-                gb += __shfl_xor_sync(0xffffffffu, gb, o);
-                gd += __shfl_xor_sync(0xffffffffu, gd, o);
+            for (int j = 0; j < Q / 4; ++j) {
+                const float4 b = b4[j], c = b4[NP / 4 + j];
+                const f32x2 b2[2] = {pack2(b.x, b.y), pack2(b.z, b.w)}, c2[2] = {pack2(c.x, c.y), pack2(c.z, c.w)};
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int l = 2 * j + i;
+                        const f32x2 a = ex2_2(mul2(d2[k], a2[k][l]));
+                        h[k][l] = fma2(a, h[k][l], mul2(u2[k], b2[i]));
+                        // g takes this token's share before its own decay: g is of the
+                        // state after the token, the run's start lies before it
+                        w[k][l] = mul2(w[k][l], a);
+                        g[k][l] = fma2(w[k][l], mul2(c2[i], y2[k]), g[k][l]);
+                    }
             }
-            if (in && n0 == 0) {
-                const int64_t at = ((int64_t)row * p.T + t) * p.D + d;
-                y = fmaf(dv, x, y);
-                if (p.dz) ((T *)p.dz)[at] = to_type<T>(go * y * sz * fmaf(z, 1.f - sz, 1.f));
-                ((T *)p.dx)[at] = to_type<T>(fmaf(dv, dy, dl * gb));
-                float ddl = fmaf(x, gb, gd);
-                if (p.softplus) ddl *= sigmoid_f(v);
-                ((T *)p.ddt)[at] = to_type<T>(ddl);
-                dD = fmaf(dy, x, dD);
-                dbias += ddl;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                for (int o = 16; o >= LN; o >>= 1) {
-                    rb[j] += __shfl_xor_sync(0xffffffffu, rb[j], o);
-                    rc[j] += __shfl_xor_sync(0xffffffffu, rc[j], o);
+            const int tt = s + t + 1;
+            const bool last = tt == q.end, cut = tt == t1 || tt % kGroup == 0;
+            if (cut) {  // the group's state, and zero for the next
+                const int64_t at = (int64_t)line * p.ngroup + (tt - 1) / kGroup;
+                st_pair<Q>(p.sums + at * dnp + own_p, h, NP, Q, true, on);
+                float *o = p.dsum + at * p.D + d;
+                if (ln == 0 && d < p.D) o[0] = reset ? __int_as_float(0x7fffffff) : dsum.x;
+                if (ln == 0 && d + 1 < p.D) o[1] = reset ? __int_as_float(0x7fffffff) : dsum.y;
+                if (ln == 0) {
+                    float *r = p.gsum + at * p.D + d;
+                    if (d < p.D) r[0] = dsum.x;
+                    if (d + 1 < p.D) r[1] = dsum.y;
                 }
-                if ((threadIdx.x & 31) < LN) {
-                    red[threadIdx.x >> 5][n0 + j] = rb[j];
-                    red[threadIdx.x >> 5][4 * LN + n0 + j] = rc[j];
+                dsum = make_float2(0.f, 0.f);
+                reset = false;
+                first_h(0, true);
+            }
+            if (last) {
+                if (alive) {
+                    if (p.dh_final) {
+                        f32x2 e[2][Q / 2];
+                        ld_pair<Q>(e, p.dh_final + q.seg * hrow + own, p.N, nn, p.n_wide, on);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int j = 0; j < Q / 2; ++j) g[k][j] = fma2(w[k][j], e[k][j], g[k][j]);
+                    }
+                    // what follows belongs to other sequences
+                    st_pair<Q>(gs, g, NP, Q, true, on);
+                    alive = false;
+                }
+                if (tt < p.T) {
+                    ssm_next(q, p.cu, p.n_seq, p.T, tt);
+                    first_h(q.seg, false);
+                    reset = true;
                 }
             }
-            __syncthreads();
-            for (int n = threadIdx.x; n < 2 * p.N; n += 128) {
-                const int k = n < p.N ? n : 4 * LN + n - p.N;
-                p.part_bc[((int64_t)blockIdx.x * p.B * p.T + (int64_t)row * p.T + t) * (2 * p.N) + n] =
-                    red[0][k] + red[1][k] + red[2][k] + red[3][k];
-            }
-            __syncthreads();
+        }
+        buf = buf == 2 ? 0 : buf + 1, flip ^= 1;
+    }
+    if (alive) st_pair<Q>(gs, g, NP, Q, true, on);
+    if (!alive && ln == 0) {  // nothing crosses the run: marked by NaN
+        float *r = p.gsum + ((int64_t)line * p.ngroup + t0 / kGroup) * p.D + d;
+        if (d < p.D) r[0] = __int_as_float(0x7fffffff);
+        if (d + 1 < p.D) r[1] = __int_as_float(0x7fffffff);
+    }
+}
+
+// Blocks with y = 0: the state entering group c + 1 replaces group c's, h <-
+// exp(A sum delta) h + S. With y = 1: the gradient at the start of each run,
+// G <- G + exp(A sum delta over the run) (G of the next run), from the last.
+__global__ void __launch_bounds__(256) ssm_bwd_chain_kernel(const SsmParams p, int np) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, dnp = (int64_t)p.D * np;
+    const int lines = p.cu ? 1 : p.B;
+    if (i >= lines * dnp) return;
+    const int line = (int)(i / dnp), d = (int)(i % dnp / np), n = (int)(i % np);
+    const float a = n < p.N ? p.A[(int64_t)d * p.N + n] * kLog2e : 0.f;
+    if (blockIdx.y == 0) {
+        float *s = p.sums + (int64_t)line * p.ngroup * dnp + i % dnp;
+        const float *q = p.dsum + (int64_t)line * p.ngroup * p.D + d;
+        float h = 0.f;
+#pragma unroll 8
+        for (int c = 0; c + 1 < p.ngroup; ++c) {
+            const float v = q[(int64_t)c * p.D], e = s[c * dnp];
+            h = isnan(v) ? e : fmaf(ex2f(a * v), h, e);
+            s[c * dnp] = h;
+        }
+    } else {
+        const int gpr = p.rlen / kGroup;
+        float *s = p.gs + (int64_t)line * p.nrun * dnp + i % dnp;
+        const float *q = p.gsum + (int64_t)line * p.ngroup * p.D + d;
+        float g = 0.f;
+        for (int r = p.nrun - 1; r >= 0; --r) {
+            float v = 0.f;
+            const int e = min(p.ngroup, (r + 1) * gpr);
+            for (int c = r * gpr; c < e; ++c) v += q[(int64_t)c * p.D];
+            const float own = s[r * dnp];
+            g = isnan(v) ? own : fmaf(ex2f(a * v), g, own);
+            s[r * dnp] = g;
         }
     }
+}
+
+// -------------------------------------------------------------- walk back ---
+// D += A B, m16n8k8, tf32 operands (the low 13 bits of an fp32 are ignored)
+__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Lanes: lane = ln * CL + lc has channels 2 lc, 2 lc + 1 of its warp and
+// states ln Q .. ln Q + Q - 1, Q = 8.
+//
+// dB and dC are sums over channels, i.e. over lanes: 16 values a lane and
+// token. They are summed by the tensor cores, against ones: with the
+// lane's dB and dC of state j as the two B-fragment words (rows lane % 4 and
+// lane % 4 + 4 of column lane / 4) and A rows j and j + 8 selecting them, one
+// m16n8k8 adds each over the four lanes of a column, and 8 of them leave in
+// every lane two columns of two rows; the columns of one ln are added by
+// shuffles. Products enter as tf32: for bf16 tensors truncated (an error of
+// 2^-11 of a term against the result's 2^-9), for fp32 ones as the sum of two
+// parts (2^-21).
+template <typename T, int LN, bool USUAL>
+__global__ void __launch_bounds__(kNT) ssm_bwd_kernel(const SsmParams p, int ntile) {
+    constexpr int Q = 8, NP = Q * LN, CL = 32 / LN, CH = 2 * 2 * CL, TG = kGroup, SUB = 4;
+    constexpr int kTile = TG * CH;
+    extern __shared__ __align__(16) unsigned char smem[];
+    T *tiles = reinterpret_cast<T *>(smem);                     // x, dt, z, dout: [4][TG][CH]
+    float *dls = reinterpret_cast<float *>(tiles + 4 * kTile);  // delta: [TG][CH]
+    float *bcs = dls + kTile;                                   // [TG][2][NP]
+    float *part = bcs + TG * 2 * NP;                            // [2 warps][TG][2][NP]
+    float4 *ckpt = reinterpret_cast<float4 *>(part + 2 * TG * 2 * NP);  // [TG / SUB][4][kNT]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int ln = lane / CL, lc = lane % CL;
+    const int tile = blockIdx.x % ntile, item = blockIdx.x / ntile;
+    const int line = item / p.nrun, run = item - line * p.nrun;
+    const int r0 = run * p.rlen, r1 = min(p.T - r0, p.rlen) + r0;
+    const int c0 = tile * CH, ch = warp * 2 * CL + 2 * lc, d = c0 + ch, n0 = ln * Q, nn = p.N - n0;
+    const bool on[2] = {d < p.D && nn > 0, d + 1 < p.D && nn > 0};
+    const int64_t hrow = (int64_t)p.D * p.N, dnp = (int64_t)p.D * NP;
+    const int64_t own = (int64_t)d * p.N + n0, own_p = (int64_t)d * NP + n0;
+    const bool softplus = USUAL || p.softplus, gate = USUAL || p.z, vec = USUAL || p.vec;
+
+    f32x2 a2[2][Q / 2], g[2][Q / 2], dA[2][Q / 2], hin[SUB][2][Q / 2], a[SUB][2][Q / 2];
+    ld_pair<Q>(a2, p.A + own, p.N, nn, p.n_wide, on);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (in && n0 + j < p.N) {
-            const int64_t at = ((int64_t)seq * p.D + d) * p.N + n0 + j;
-            p.part_a[at] = dA[j];
-            if (p.dh0) p.dh0[at] = g[j];
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < Q / 2; ++j) {
+            a2[k][j] = mul2(a2[k][j], pack2(kLog2e, kLog2e));
+            g[k][j] = dA[k][j] = pack2(0.f, 0.f);
         }
-    if (in && n0 == 0) {
-        p.part_d[(int64_t)seq * 2 * p.D + d] = dD;
-        p.part_d[(int64_t)seq * 2 * p.D + p.D + d] = dbias;
+    // from the run's end on
+    if (run + 1 < p.nrun) ld_pair<Q>(g, p.gs + ((int64_t)line * p.nrun + run + 1) * dnp + own_p, NP, Q, true, on);
+    // the channel this lane finishes: of each pair lane ln = k finishes k (LN > 1)
+    const int fk = LN > 1 ? ln & 1 : 0;
+    float dD[2] = {0.f, 0.f}, dbias[2] = {0.f, 0.f};
+    const float dv[2] = {p.Dv && d < p.D ? p.Dv[d] : 0.f, p.Dv && d + 1 < p.D ? p.Dv[d + 1] : 0.f};
+    const float bias[2] = {p.dt_bias && d < p.D ? p.dt_bias[d] : 0.f, p.dt_bias && d + 1 < p.D ? p.dt_bias[d + 1] : 0.f};
+    const T *src[4] = {(const T *)p.x + line * p.x_sb, (const T *)p.dt + line * p.dt_sb,
+                       (const T *)p.z + line * p.z_sb, (const T *)p.dout + line * p.do_sb};
+    const int64_t str[4] = {p.x_st, p.dt_st, p.z_st, p.do_st};
+
+    auto boundary = [&](const float *from, int seg, f32x2 (&v)[2][Q / 2]) {  // a sequence's h0 or dh_final, or zero
+        if (from) {
+            ld_pair<Q>(v, from + seg * hrow + own, p.N, nn, p.n_wide, on);
+        } else {
+#pragma unroll
+            for (int j = 0; j < Q / 2; ++j) v[0][j] = v[1][j] = pack2(0.f, 0.f);
+        }
+    };
+    for (int grp = (r1 - 1) / TG; grp * TG >= r0; --grp) {
+        const int t0 = grp * TG, m = min(p.T - t0, TG);
+        __syncthreads();  // the group before has been read
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k != 2 || gate)
+                ssm_fetch_tile<T, CH, TG, kNT>(tiles + k * kTile, src[k] + t0 * str[k], str[k], m, c0, p.D, vec);
+        cp_async_commit();
+        {
+            SsmBc<T, NP, TG, kNT> bc;
+            bc.template fetch<true>((const T *)p.bm + line * p.bm_sb + t0 * p.bm_st, p.bm_st,
+                                    (const T *)p.cm + line * p.cm_sb + t0 * p.cm_st, p.cm_st, m, p.N, p.bc_vec);
+            bc.stage(bcs);
+        }
+        // tokens at which a sequence begins, and those that end one
+        uint32_t starts;
+        {
+            bool s = false;
+            if (lane < m) s = ssm_find(p.cu, p.n_seq, p.T, line, t0 + lane).starts;
+            starts = __ballot_sync(0xffffffffu, s);
+        }
+        bool end_last = t0 + m == p.T;
+        if (!end_last && p.cu) end_last = ssm_find(p.cu, p.n_seq, p.T, line, t0 + m).starts;
+        const uint32_t ends = starts >> 1 | (end_last ? 1u << (m - 1) : 0u);
+        cp_async_wait<0>();
+        __syncthreads();
+        // delta of the tile, by pairs
+        for (int e = tid; e < TG * CH / 2; e += kNT) {
+            const int r = e / (CH / 2), c = e % (CH / 2) * 2;
+            float f[2];
+            ld_row_f<T, 2, true>(f, tiles + kTile + r * CH + c, 2);
+            float2 v = make_float2(f[0], f[1]);
+            if (p.dt_bias) {
+                if (c0 + c < p.D) v.x += p.dt_bias[c0 + c];
+                if (c0 + c + 1 < p.D) v.y += p.dt_bias[c0 + c + 1];
+            }
+            if (softplus) v = softplus2(v);
+            *reinterpret_cast<float2 *>(dls + r * CH + c) = v;
+        }
+        __syncthreads();
+        auto pair_at = [&](int i, int k) {
+            float f[2];
+            ld_row_f<T, 2, true>(f, tiles + k * kTile + i * CH + ch, 2);
+            return make_float2(f[0], f[1]);
+        };
+        // one token forward: hn from h, the decays in ad
+        auto forward = [&](f32x2 (&hn)[2][Q / 2], const f32x2 (&h)[2][Q / 2], f32x2 (&ad)[2][Q / 2], int i) {
+            const float2 dl = *reinterpret_cast<const float2 *>(dls + i * CH + ch), x = pair_at(i, 0);
+            const f32x2 d2[2] = {pack2(dl.x, dl.x), pack2(dl.y, dl.y)};
+            const f32x2 u2[2] = {pack2(dl.x * x.x, dl.x * x.x), pack2(dl.y * x.y, dl.y * x.y)};
+            const float4 *b4 = reinterpret_cast<const float4 *>(bcs + i * 2 * NP + n0);
+#pragma unroll
+            for (int j = 0; j < Q / 4; ++j) {
+                const float4 b = b4[j];
+                const f32x2 b2[2] = {pack2(b.x, b.y), pack2(b.z, b.w)};
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int l = 2 * j; l < 2 * j + 2; ++l) {
+                        ad[k][l] = ex2_2(mul2(d2[k], a2[k][l]));
+                        hn[k][l] = fma2(ad[k][l], h[k][l], mul2(u2[k], b2[l & 1]));
+                    }
+            }
+        };
+        // the state entering the group, then forward with checkpoints
+        f32x2(&h)[2][Q / 2] = hin[0];
+        if (grp > 0 && !(starts & 1u))
+            ld_pair<Q>(h, p.sums + ((int64_t)line * p.ngroup + grp - 1) * dnp + own_p, NP, Q, true, on);
+        else
+            boundary(nullptr, 0, h);
+        const int nsub = (m + SUB - 1) / SUB;
+        for (int sb = 0; sb < nsub; ++sb) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 u = unpack2(h[k >> 1][(k & 1) * 2]), v = unpack2(h[k >> 1][(k & 1) * 2 + 1]);
+                ckpt[(sb * 4 + k) * kNT + tid] = make_float4(u.x, u.y, v.x, v.y);
+            }
+            if (sb + 1 == nsub) break;
+#pragma unroll
+            for (int i = 0; i < SUB; ++i) {
+                const int t = sb * SUB + i;
+                if (starts >> t & 1u) boundary(p.h0, ssm_find(p.cu, p.n_seq, p.T, line, t0 + t).seg, h);
+                forward(h, h, a[0], t);
+            }
+        }
+        for (int sb = nsub - 1; sb >= 0; --sb) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 f = ckpt[(sb * 4 + k) * kNT + tid];
+                hin[0][k >> 1][(k & 1) * 2] = pack2(f.x, f.y), hin[0][k >> 1][(k & 1) * 2 + 1] = pack2(f.z, f.w);
+            }
+#pragma unroll
+            for (int i = 0; i < SUB; ++i) {
+                const int t = sb * SUB + i;
+                if (t >= m) continue;
+                if (starts >> t & 1u) boundary(p.h0, ssm_find(p.cu, p.n_seq, p.T, line, t0 + t).seg, hin[i]);
+                if (i + 1 < SUB) forward(hin[i + 1 < SUB ? i + 1 : 0], hin[i], a[i], t);
+                else {
+                    const float2 dl = *reinterpret_cast<const float2 *>(dls + t * CH + ch);
+                    const f32x2 d2[2] = {pack2(dl.x, dl.x), pack2(dl.y, dl.y)};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int l = 0; l < Q / 2; ++l) a[i][k][l] = ex2_2(mul2(d2[k], a2[k][l]));
+                }
+            }
+#pragma unroll
+            for (int i = SUB - 1; i >= 0; --i) {
+                const int t = sb * SUB + i;
+                if (t >= m) continue;
+                if (ends >> t & 1u) boundary(p.dh_final, ssm_find(p.cu, p.n_seq, p.T, line, t0 + t).seg, g);
+                const float2 dl = *reinterpret_cast<const float2 *>(dls + t * CH + ch), x = pair_at(t, 0);
+                const float2 go = pair_at(t, 3);
+                float2 z = make_float2(0.f, 0.f), sg = z, dy = go;
+                if (gate) {
+                    z = pair_at(t, 2), sg = sigmoid2(z);
+                    dy.x *= z.x * sg.x, dy.y *= z.y * sg.y;
+                }
+                const f32x2 d2[2] = {pack2(dl.x, dl.x), pack2(dl.y, dl.y)};
+                const f32x2 u2[2] = {pack2(dl.x * x.x, dl.x * x.x), pack2(dl.y * x.y, dl.y * x.y)};
+                const f32x2 y2[2] = {pack2(dy.x, dy.x), pack2(dy.y, dy.y)};
+                const float4 *b4 = reinterpret_cast<const float4 *>(bcs + t * 2 * NP + n0);
+                f32x2 ys[2], gb[2], gd[2], rb[Q / 2], rc[Q / 2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) ys[k] = gb[k] = gd[k] = pack2(0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < Q / 4; ++j) {
+                    const float4 b = b4[j], c = b4[NP / 4 + j];
+                    const f32x2 b2[2] = {pack2(b.x, b.y), pack2(b.z, b.w)}, c2[2] = {pack2(c.x, c.y), pack2(c.z, c.w)};
+#pragma unroll
+                    for (int l = 2 * j; l < 2 * j + 2; ++l)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const f32x2 w = mul2(a[i][k][l], hin[i][k][l]);   // a h_{t-1}
+                            const f32x2 hn = fma2(u2[k], b2[l & 1], w);       // h_t
+                            ys[k] = fma2(hn, c2[l & 1], ys[k]);
+                            const f32x2 gn = fma2(c2[l & 1], y2[k], g[k][l]);
+                            gb[k] = fma2(gn, b2[l & 1], gb[k]);
+                            rb[l] = k ? fma2(u2[k], gn, rb[l]) : mul2(u2[k], gn);
+                            rc[l] = k ? fma2(y2[k], hn, rc[l]) : mul2(y2[k], hn);
+                            const f32x2 e = mul2(gn, w);
+                            gd[k] = fma2(e, a2[k][l], gd[k]);
+                            dA[k][l] = fma2(e, d2[k], dA[k][l]);
+                            g[k][l] = mul2(gn, a[i][k][l]);
+                        }
+                }
+                if (starts >> t & 1u) {
+                    if (p.dh0)
+                        st_pair<Q>(p.dh0 + ssm_find(p.cu, p.n_seq, p.T, line, t0 + t).seg * hrow + own, g, p.N, nn,
+                                   p.n_wide, on);
+                }
+                // over the states: y, sum B g, sum A a h g of the two channels
+                float r[3][2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float2 u = unpack2(ys[k]), v = unpack2(gb[k]), e = unpack2(gd[k]);
+                    r[0][k] = u.x + u.y, r[1][k] = v.x + v.y, r[2][k] = (e.x + e.y) * 0.6931471805599453f;
+                }
+                if (LN > 1) {
+#pragma unroll
+                    for (int q = 0; q < 3; ++q) {
+#pragma unroll
+                        for (int o = 2 * CL; o < 32; o <<= 1) {
+                            r[q][0] += __shfl_xor_sync(0xffffffffu, r[q][0], o);
+                            r[q][1] += __shfl_xor_sync(0xffffffffu, r[q][1], o);
+                        }
+                        const float give = fk ? r[q][0] : r[q][1], keep = fk ? r[q][1] : r[q][0];
+                        r[q][0] = keep + __shfl_xor_sync(0xffffffffu, give, CL);
+                    }
+                }
+                T *dxp = (T *)p.dx + ((int64_t)line * p.T + t0 + t) * p.D + d;
+                T *dtp = (T *)p.ddt + ((int64_t)line * p.T + t0 + t) * p.D + d;
+                T *dzp = (T *)p.dz + ((int64_t)line * p.T + t0 + t) * p.D + d;
+                const float2 v = pair_at(t, 1);
+#pragma unroll
+                for (int q = 0; q < (LN > 1 ? 1 : 2); ++q) {  // the channel(s) this lane finishes
+                    const int k = LN > 1 ? fk : q;
+                    const float xk = k ? x.y : x.x, dk = k ? dl.y : dl.x, yk = k ? dy.y : dy.x, vk = (k ? v.y : v.x) + bias[k];
+                    const float zk = k ? z.y : z.x, sk = k ? sg.y : sg.x, ok = k ? go.y : go.x;
+                    const float y = fmaf(dv[k], xk, r[0][q]), s1 = r[1][q];
+                    float dd = fmaf(xk, s1, r[2][q]);
+                    // sigmoid(v) = exp(v - softplus(v))
+                    if (softplus) dd *= ex2f((vk - dk) * kLog2e);
+                    if (d + k < p.D && ln < 2) {
+                        dxp[k] = to_type<T>(fmaf(dv[k], yk, dk * s1));
+                        dtp[k] = to_type<T>(dd);
+                        if (gate && p.dz) dzp[k] = to_type<T>(ok * y * sk * fmaf(zk, 1.f - sk, 1.f));
+                    }
+                    dD[q] = fmaf(yk, xk, dD[q]);
+                    dbias[q] += dd;
+                }
+                // over the channels: dB and dC of this warp's
+                float *pw = part + ((warp * TG + t) * 2) * NP;
+                if constexpr (LN <= 8) {
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < Q; ++j) {
+                        const float2 b = unpack2(rb[j / 2]), c = unpack2(rc[j / 2]);
+                        const uint32_t b0 = __float_as_uint(j & 1 ? b.y : b.x), b1 = __float_as_uint(j & 1 ? c.y : c.x);
+                        const uint32_t sel = lane >> 2 == j ? 0x3f800000u : 0u;
+                        if constexpr (sizeof(T) == 2) {
+                            mma_tf32(acc, sel, 0u, 0u, sel, b0, b1);
+                        } else {
+                            const uint32_t h0 = b0 & 0xffffe000u, h1 = b1 & 0xffffe000u;
+                            mma_tf32(acc, sel, 0u, 0u, sel, h0, h1);
+                            mma_tf32(acc, sel, 0u, 0u, sel, __float_as_uint(__uint_as_float(b0) - __uint_as_float(h0)),
+                                     __float_as_uint(__uint_as_float(b1) - __uint_as_float(h1)));
+                        }
+                    }
+                    // acc: rows lane / 4 (dB of that state) and + 8 (dC), columns 2 (lane % 4) and + 1;
+                    // column c holds the lanes 4 c .. 4 c + 3, of ln = 4 c / CL
+                    const int row = lane >> 2, col = lane & 3;
+                    if constexpr (LN == 8) {
+                        pw[2 * col * Q + row] = acc[0], pw[(2 * col + 1) * Q + row] = acc[1];
+                        pw[NP + 2 * col * Q + row] = acc[2], pw[NP + (2 * col + 1) * Q + row] = acc[3];
+                    } else {
+                        float sb0 = acc[0] + acc[1], sc0 = acc[2] + acc[3];
+                        if (LN <= 2) sb0 += __shfl_xor_sync(0xffffffffu, sb0, 1), sc0 += __shfl_xor_sync(0xffffffffu, sc0, 1);
+                        if (LN == 1) sb0 += __shfl_xor_sync(0xffffffffu, sb0, 2), sc0 += __shfl_xor_sync(0xffffffffu, sc0, 2);
+                        constexpr int kPer = 4 / LN;  // lanes with the same sum
+                        if (col % kPer == 0) {
+                            pw[col / kPer * Q + row] = sb0;
+                            pw[NP + col / kPer * Q + row] = sc0;
+                        }
+                    }
+                } else {  // two channel lanes: one shuffle each
+#pragma unroll
+                    for (int j = 0; j < Q; ++j) {
+                        const float2 b = unpack2(rb[j / 2]), c = unpack2(rc[j / 2]);
+                        float u = j & 1 ? b.y : b.x, w = j & 1 ? c.y : c.x;
+                        u += __shfl_xor_sync(0xffffffffu, u, 1), w += __shfl_xor_sync(0xffffffffu, w, 1);
+                        if (lc == 0) pw[n0 + j] = u, pw[NP + n0 + j] = w;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        // the tile's dB and dC of the group
+        for (int e = tid; e < m * 2 * p.N; e += kNT) {
+            const int r = e / (2 * p.N), k = e % (2 * p.N), n = k < p.N ? k : NP + k - p.N;
+            p.part_bc[((int64_t)tile * p.B * p.T + (int64_t)line * p.T + t0 + r) * (2 * p.N) + k] =
+                part[r * 2 * NP + n] + part[(TG + r) * 2 * NP + n];
+        }
+    }
+    st_pair<Q>(p.part_a + ((int64_t)line * p.nrun + run) * hrow + own, dA, p.N, nn, p.n_wide, on);
+    float *pd = p.part_d + ((int64_t)line * p.nrun + run) * 2 * p.D + d;
+#pragma unroll
+    for (int q = 0; q < (LN > 1 ? 1 : 2); ++q) {
+        const int k = LN > 1 ? fk : q;
+        if (d + k < p.D && ln < 2) pd[k] = dD[q], pd[p.D + k] = dbias[q];
     }
 }
 
@@ -163,6 +552,7 @@ __global__ void __launch_bounds__(256) ssm_bwd_reduce_kernel(const SsmParams p, 
     const int64_t rows = (int64_t)p.B * p.T, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= rows * 2 * p.N) return;
     float a = 0.f;
+#pragma unroll 8
     for (int k = 0; k < tiles; ++k) a += p.part_bc[k * rows * 2 * p.N + i];
     const int64_t r = i / (2 * p.N);
     const int n = (int)(i - r * 2 * p.N);
@@ -170,34 +560,90 @@ __global__ void __launch_bounds__(256) ssm_bwd_reduce_kernel(const SsmParams p, 
     else ((T *)p.dcm)[r * p.N + n - p.N] = to_type<T>(a);
 }
 
-template <class F>
-cudaError_t by_lanes(int N, F &&f) {
-    if (N <= 16) return f(std::integral_constant<int, 4>());
-    if (N <= 32) return f(std::integral_constant<int, 8>());
-    if (N <= 64) return f(std::integral_constant<int, 16>());
-    return f(std::integral_constant<int, 32>());
+// without a token in a sequence its state's gradient passes through
+__global__ void __launch_bounds__(256) ssm_bwd_empty_kernel(const SsmParams p) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, dn = (int64_t)p.D * p.N;
+    if (i >= dn) return;
+    for (int s = blockIdx.y; s < p.n_seq; s += gridDim.y)
+        if (p.cu ? p.cu[s + 1] <= p.cu[s] : p.T == 0) p.dh0[s * dn + i] = p.dh_final ? p.dh_final[s * dn + i] : 0.f;
 }
-int lanes(int N) { return N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32; }
+
+template <typename T, int Q, int LN>
+cudaError_t sum_t(const SsmParams &p, cudaStream_t st) {
+    constexpr int CH = 2 * kNT / LN;
+    constexpr int smem = 3 * 4 * kStage * CH * (int)sizeof(T) + 2 * kStage * 2 * Q * LN * 4;
+    const bool usual = p.vec && p.softplus && p.z;
+    auto *k = usual ? ssm_bwd_sum_kernel<T, Q, LN, true> : ssm_bwd_sum_kernel<T, Q, LN, false>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int ntile = (p.D + CH - 1) / CH;
+    const int64_t items = (int64_t)(p.cu ? 1 : p.B) * p.nrun;
+    if (items * ntile > INT32_MAX) return cudaErrorInvalidValue;
+    k<<<(unsigned)(items * ntile), kNT, smem, st>>>(p, ntile);
+    return cudaGetLastError();
+}
+template <typename T, int LN>
+cudaError_t walk_t(const SsmParams &p, cudaStream_t st) {
+    constexpr int CH = 4 * (32 / LN), NP = 8 * LN;
+    constexpr int smem = 4 * kGroup * CH * (int)sizeof(T) + kGroup * CH * 4 + 3 * kGroup * 2 * NP * 4 + kGroup * kNT * 16;
+    const bool usual = p.vec && p.softplus && p.z;
+    auto *k = usual ? ssm_bwd_kernel<T, LN, true> : ssm_bwd_kernel<T, LN, false>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int ntile = ssm_bwd_tiles(p.D, p.N);
+    const int64_t items = (int64_t)(p.cu ? 1 : p.B) * p.nrun;
+    if (items * ntile > INT32_MAX) return cudaErrorInvalidValue;
+    k<<<(unsigned)(items * ntile), kNT, smem, st>>>(p, ntile);
+    return cudaGetLastError();
+}
+// lanes a channel pair of the walk back, at eight states a lane
+int walk_lanes(int N) { return N <= 8 ? 1 : N <= 16 ? 2 : N <= 32 ? 4 : N <= 64 ? 8 : 16; }
 
 }  // namespace
 
-int ssm_bwd_tiles(int D, int N) { return (D + 128 / lanes(N) - 1) / (128 / lanes(N)); }
+int ssm_bwd_tiles(int D, int N) {
+    const int ch = 4 * (32 / walk_lanes(N));
+    return (D + ch - 1) / ch;
+}
+// Tokens a run: 256, less where there are few channels.
+int ssm_bwd_run(int lines, int T, int D, int N) {
+    int len = 256;
+    while (len > kGroup && (int64_t)lines * ssm_bwd_tiles(D, N) * ((T + len - 1) / len) < 1216) len /= 2;
+    return len;
+}
 
-cudaError_t launch_ssm_bwd(const SsmParams &p, cudaStream_t st) {
-    return by_lanes(p.N, [&](auto ln) {
-        const dim3 grid(ssm_bwd_tiles(p.D, p.N), p.n_seq);
-        if (p.bf16) ssm_bwd_kernel<__nv_bfloat16, ln()><<<grid, 128, 0, st>>>(p);
-        else ssm_bwd_kernel<float, ln()><<<grid, 128, 0, st>>>(p);
-        return cudaGetLastError();
+cudaError_t launch_ssm_bwd_sum(const SsmParams &p, cudaStream_t st) {
+    return ssm_by_states(p.N, [&](auto q, auto ln) {
+        return p.bf16 ? sum_t<__nv_bfloat16, q(), ln()>(p, st) : sum_t<float, q(), ln()>(p, st);
     });
+}
+cudaError_t launch_ssm_bwd_chain(const SsmParams &p, cudaStream_t st) {
+    const int np = ssm_np(p.N);
+    const int64_t n = (int64_t)(p.cu ? 1 : p.B) * p.D * np;
+    ssm_bwd_chain_kernel<<<dim3((unsigned)((n + 255) / 256), 2), 256, 0, st>>>(p, np);
+    return cudaGetLastError();
+}
+cudaError_t launch_ssm_bwd(const SsmParams &p, cudaStream_t st) {
+    auto f = [&](auto ln) { return p.bf16 ? walk_t<__nv_bfloat16, ln()>(p, st) : walk_t<float, ln()>(p, st); };
+    switch (walk_lanes(p.N)) {
+        case 1: return f(std::integral_constant<int, 1>());
+        case 2: return f(std::integral_constant<int, 2>());
+        case 4: return f(std::integral_constant<int, 4>());
+        case 8: return f(std::integral_constant<int, 8>());
+    }
+    return f(std::integral_constant<int, 16>());
 }
 cudaError_t launch_ssm_bwd_reduce(const SsmParams &p, cudaStream_t st) {
     const int64_t n = (int64_t)p.B * p.T * 2 * p.N;
-    if (n == 0) return cudaSuccess;
     const unsigned grid = (unsigned)((n + 255) / 256);
     const int tiles = ssm_bwd_tiles(p.D, p.N);
     if (p.bf16) ssm_bwd_reduce_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p, tiles);
     else ssm_bwd_reduce_kernel<float><<<grid, 256, 0, st>>>(p, tiles);
+    return cudaGetLastError();
+}
+cudaError_t launch_ssm_bwd_empty(const SsmParams &p, cudaStream_t st) {
+    const int64_t n = (int64_t)p.D * p.N;
+    ssm_bwd_empty_kernel<<<dim3((unsigned)((n + 255) / 256), p.n_seq < 64 ? p.n_seq : 64), 256, 0, st>>>(p);
     return cudaGetLastError();
 }
 
