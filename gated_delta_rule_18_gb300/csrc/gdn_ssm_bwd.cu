@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(kNT) ssm_bwd_kernel(const SsmParams p, int nti
     T *tiles = reinterpret_cast<T *>(smem);                     // x, dt, z, dout: [4][TG][CH]
     float *dls = reinterpret_cast<float *>(tiles + 4 * kTile);  // delta: [TG][CH]
     float *bcs = dls + kTile;                                   // [TG][2][NP]
-    float *part = bcs + TG * 2 * NP;                            // [2 warps][TG][2][NP]
-    float4 *ckpt = reinterpret_cast<float4 *>(part + 2 * TG * 2 * NP);  // [TG / SUB][4][kNT]
+    float *part = bcs + TG * 2 * NP;                            // [TG][2][NP], both warps' sums
+    float4 *ckpt = reinterpret_cast<float4 *>(part + TG * 2 * NP);  // [TG / SUB - 2][4][kNT]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ln = lane / CL, lc = lane % CL;
     const int tile = blockIdx.x % ntile, item = blockIdx.x / ntile;
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kNT) ssm_bwd_kernel(const SsmParams p, int nti
     const int64_t own = (int64_t)d * p.N + n0, own_p = (int64_t)d * NP + n0;
     const bool softplus = USUAL || p.softplus, gate = USUAL || p.z, vec = USUAL || p.vec;
 
-    f32x2 a2[2][Q / 2], g[2][Q / 2], dA[2][Q / 2], hin[SUB][2][Q / 2], a[SUB][2][Q / 2];
+    f32x2 a2[2][Q / 2], g[2][Q / 2], dA[2][Q / 2], h[2][Q / 2], w[SUB][2][Q / 2], a[SUB][2][Q / 2];
     ld_pair<Q>(a2, p.A + own, p.N, nn, p.n_wide, on);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -276,11 +276,17 @@ __global__ void __launch_bounds__(kNT) ssm_bwd_kernel(const SsmParams p, int nti
         }
     // from the run's end on
     if (run + 1 < p.nrun) ld_pair<Q>(g, p.gs + ((int64_t)line * p.nrun + run + 1) * dnp + own_p, NP, Q, true, on);
-    // the channel this lane finishes: of each pair lane ln = k finishes k (LN > 1)
+    // the channels this lane finishes: lane ln = k of a pair finishes channel k (LN > 1), or both
     const int fk = LN > 1 ? ln & 1 : 0;
     float dD[2] = {0.f, 0.f}, dbias[2] = {0.f, 0.f};
-    const float dv[2] = {p.Dv && d < p.D ? p.Dv[d] : 0.f, p.Dv && d + 1 < p.D ? p.Dv[d + 1] : 0.f};
-    const float bias[2] = {p.dt_bias && d < p.D ? p.dt_bias[d] : 0.f, p.dt_bias && d + 1 < p.D ? p.dt_bias[d + 1] : 0.f};
+    float dvf[2], biasf[2];
+    bool fin[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int c = d + fk + q;
+        fin[q] = c < p.D && ln < 2;
+        dvf[q] = p.Dv && c < p.D ? p.Dv[c] : 0.f, biasf[q] = p.dt_bias && c < p.D ? p.dt_bias[c] : 0.f;
+    }
     const T *src[4] = {(const T *)p.x + line * p.x_sb, (const T *)p.dt + line * p.dt_sb,
                        (const T *)p.z + line * p.z_sb, (const T *)p.dout + line * p.do_sb};
     const int64_t str[4] = {p.x_st, p.dt_st, p.z_st, p.do_st};
@@ -316,10 +322,13 @@ __global__ void __launch_bounds__(kNT) ssm_bwd_kernel(const SsmParams p, int nti
         }
         bool end_last = t0 + m == p.T;
         if (!end_last && p.cu) end_last = ssm_find(p.cu, p.n_seq, p.T, line, t0 + m).starts;
+        const int64_t o0 = ((int64_t)line * p.T + t0) * p.D + d + fk;
+        T *dxp = (T *)p.dx + o0, *dtp = (T *)p.ddt + o0, *dzp = (T *)p.dz + o0;
         const uint32_t ends = starts >> 1 | (end_last ? 1u << (m - 1) : 0u);
         cp_async_wait<0>();
         __syncthreads();
         // delta of the tile, by pairs
+        for (int e = tid; e < TG * 2 * NP; e += kNT) part[e] = 0.f;
         for (int e = tid; e < TG * CH / 2; e += kNT) {
             const int r = e / (CH / 2), c = e % (CH / 2) * 2;
             float f[2];
@@ -338,212 +347,218 @@ __global__ void __launch_bounds__(kNT) ssm_bwd_kernel(const SsmParams p, int nti
             ld_row_f<T, 2, true>(f, tiles + k * kTile + i * CH + ch, 2);
             return make_float2(f[0], f[1]);
         };
-        // one token forward: hn from h, the decays in ad
-        auto forward = [&](f32x2 (&hn)[2][Q / 2], const f32x2 (&h)[2][Q / 2], f32x2 (&ad)[2][Q / 2], int i) {
-            const float2 dl = *reinterpret_cast<const float2 *>(dls + i * CH + ch), x = pair_at(i, 0);
-            const f32x2 d2[2] = {pack2(dl.x, dl.x), pack2(dl.y, dl.y)};
-            const f32x2 u2[2] = {pack2(dl.x * x.x, dl.x * x.x), pack2(dl.y * x.y, dl.y * x.y)};
-            const float4 *b4 = reinterpret_cast<const float4 *>(bcs + i * 2 * NP + n0);
+        // Edge groups, in which a sequence begins or ends or which are not
+        // whole, ask at every token; the others run without a branch.
+        auto group = [&](auto edge_c) {
+            constexpr bool EDGE = decltype(edge_c)::value;
+            const int nsub = EDGE ? (m + SUB - 1) / SUB : TG / SUB;
+            auto seg_of = [&](int t) { return ssm_find(p.cu, p.n_seq, p.T, line, t0 + t).seg; };
+            // one token forward: wd = a h, h <- wd + u B
+            auto forward = [&](f32x2 (&wd)[2][Q / 2], f32x2 (&ad)[2][Q / 2], int i) {
+                const float2 dl = *reinterpret_cast<const float2 *>(dls + i * CH + ch), x = pair_at(i, 0);
+                const f32x2 d2[2] = {pack2(dl.x, dl.x), pack2(dl.y, dl.y)};
+                const float ux = dl.x * x.x, uy = dl.y * x.y;
+                const f32x2 u2[2] = {pack2(ux, ux), pack2(uy, uy)};
+                const float4 *b4 = reinterpret_cast<const float4 *>(bcs + i * 2 * NP + n0);
 #pragma unroll
-            for (int j = 0; j < Q / 4; ++j) {
-                const float4 b = b4[j];
-                const f32x2 b2[2] = {pack2(b.x, b.y), pack2(b.z, b.w)};
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int l = 2 * j; l < 2 * j + 2; ++l) {
-                        ad[k][l] = ex2_2(mul2(d2[k], a2[k][l]));
-                        hn[k][l] = fma2(ad[k][l], h[k][l], mul2(u2[k], b2[l & 1]));
-                    }
-            }
-        };
-        // the state entering the group, then forward with checkpoints
-        f32x2(&h)[2][Q / 2] = hin[0];
-        if (grp > 0 && !(starts & 1u))
-            ld_pair<Q>(h, p.sums + ((int64_t)line * p.ngroup + grp - 1) * dnp + own_p, NP, Q, true, on);
-        else
-            boundary(nullptr, 0, h);
-        const int nsub = (m + SUB - 1) / SUB;
-        for (int sb = 0; sb < nsub; ++sb) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 u = unpack2(h[k >> 1][(k & 1) * 2]), v = unpack2(h[k >> 1][(k & 1) * 2 + 1]);
-                ckpt[(sb * 4 + k) * kNT + tid] = make_float4(u.x, u.y, v.x, v.y);
-            }
-            if (sb + 1 == nsub) break;
-#pragma unroll
-            for (int i = 0; i < SUB; ++i) {
-                const int t = sb * SUB + i;
-                if (starts >> t & 1u) boundary(p.h0, ssm_find(p.cu, p.n_seq, p.T, line, t0 + t).seg, h);
-                forward(h, h, a[0], t);
-            }
-        }
-        for (int sb = nsub - 1; sb >= 0; --sb) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float4 f = ckpt[(sb * 4 + k) * kNT + tid];
-                hin[0][k >> 1][(k & 1) * 2] = pack2(f.x, f.y), hin[0][k >> 1][(k & 1) * 2 + 1] = pack2(f.z, f.w);
-            }
-#pragma unroll
-            for (int i = 0; i < SUB; ++i) {
-                const int t = sb * SUB + i;
-                if (t >= m) continue;
-                if (starts >> t & 1u) boundary(p.h0, ssm_find(p.cu, p.n_seq, p.T, line, t0 + t).seg, hin[i]);
-                if (i + 1 < SUB) forward(hin[i + 1 < SUB ? i + 1 : 0], hin[i], a[i], t);
-                else {
-                    const float2 dl = *reinterpret_cast<const float2 *>(dls + t * CH + ch);
-                    const f32x2 d2[2] = {pack2(dl.x, dl.x), pack2(dl.y, dl.y)};
+                for (int j = 0; j < Q / 4; ++j) {
+                    const float4 b = b4[j];
+                    const f32x2 b2[2] = {pack2(b.x, b.y), pack2(b.z, b.w)};
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
 #pragma unroll
-                        for (int l = 0; l < Q / 2; ++l) a[i][k][l] = ex2_2(mul2(d2[k], a2[k][l]));
+                        for (int l = 2 * j; l < 2 * j + 2; ++l) {
+                            ad[k][l] = ex2_2(mul2(d2[k], a2[k][l]));
+                            wd[k][l] = mul2(ad[k][l], h[k][l]);
+                            h[k][l] = fma2(u2[k], b2[l & 1], wd[k][l]);
+                        }
+                }
+            };
+            // the state entering the group; the first sub-block's is read again
+            // where the walk reaches it, the last one's stays in registers
+            auto enter = [&] {
+                if (grp > 0 && !(EDGE && (starts & 1u)))
+                    ld_pair<Q>(h, p.sums + ((int64_t)line * p.ngroup + grp - 1) * dnp + own_p, NP, Q, true, on);
+                else
+                    boundary(nullptr, 0, h);
+            };
+            enter();
+#pragma unroll 1
+            for (int sb = 0; sb + 1 < nsub; ++sb) {
+                if (sb > 0) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 u = unpack2(h[k >> 1][(k & 1) * 2]), v = unpack2(h[k >> 1][(k & 1) * 2 + 1]);
+                        ckpt[((sb - 1) * 4 + k) * kNT + tid] = make_float4(u.x, u.y, v.x, v.y);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < SUB; ++i) {
+                    const int t = sb * SUB + i;
+                    if (EDGE && (starts >> t & 1u)) boundary(p.h0, seg_of(t), h);
+                    forward(w[0], a[0], t);
                 }
             }
+#pragma unroll 1
+            for (int sb = nsub - 1; sb >= 0; --sb) {
+                if (sb == 0 && nsub > 1) {
+                    enter();
+                } else if (sb + 1 < nsub) {
 #pragma unroll
-            for (int i = SUB - 1; i >= 0; --i) {
-                const int t = sb * SUB + i;
-                if (t >= m) continue;
-                if (ends >> t & 1u) boundary(p.dh_final, ssm_find(p.cu, p.n_seq, p.T, line, t0 + t).seg, g);
-                const float2 dl = *reinterpret_cast<const float2 *>(dls + t * CH + ch), x = pair_at(t, 0);
-                const float2 go = pair_at(t, 3);
-                float2 z = make_float2(0.f, 0.f), sg = z, dy = go;
-                if (gate) {
-                    z = pair_at(t, 2), sg = sigmoid2(z);
-                    dy.x *= z.x * sg.x, dy.y *= z.y * sg.y;
-                }
-                const f32x2 d2[2] = {pack2(dl.x, dl.x), pack2(dl.y, dl.y)};
-                const f32x2 u2[2] = {pack2(dl.x * x.x, dl.x * x.x), pack2(dl.y * x.y, dl.y * x.y)};
-                const f32x2 y2[2] = {pack2(dy.x, dy.x), pack2(dy.y, dy.y)};
-                const float4 *b4 = reinterpret_cast<const float4 *>(bcs + t * 2 * NP + n0);
-                f32x2 ys[2], gb[2], gd[2], rb[Q / 2], rc[Q / 2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) ys[k] = gb[k] = gd[k] = pack2(0.f, 0.f);
-#pragma unroll
-                for (int j = 0; j < Q / 4; ++j) {
-                    const float4 b = b4[j], c = b4[NP / 4 + j];
-                    const f32x2 b2[2] = {pack2(b.x, b.y), pack2(b.z, b.w)}, c2[2] = {pack2(c.x, c.y), pack2(c.z, c.w)};
-#pragma unroll
-                    for (int l = 2 * j; l < 2 * j + 2; ++l)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const f32x2 w = mul2(a[i][k][l], hin[i][k][l]);   // a h_{t-1}
-                            const f32x2 hn = fma2(u2[k], b2[l & 1], w);       // h_t
-                            ys[k] = fma2(hn, c2[l & 1], ys[k]);
-                            const f32x2 gn = fma2(c2[l & 1], y2[k], g[k][l]);
-                            gb[k] = fma2(gn, b2[l & 1], gb[k]);
-                            rb[l] = k ? fma2(u2[k], gn, rb[l]) : mul2(u2[k], gn);
-                            rc[l] = k ? fma2(y2[k], hn, rc[l]) : mul2(y2[k], hn);
-                            const f32x2 e = mul2(gn, w);
-                            gd[k] = fma2(e, a2[k][l], gd[k]);
-                            dA[k][l] = fma2(e, d2[k], dA[k][l]);
-                            g[k][l] = mul2(gn, a[i][k][l]);
-                        }
-                }
-                if (starts >> t & 1u) {
-                    if (p.dh0)
-                        st_pair<Q>(p.dh0 + ssm_find(p.cu, p.n_seq, p.T, line, t0 + t).seg * hrow + own, g, p.N, nn,
-                                   p.n_wide, on);
-                }
-                // over the states: y, sum B g, sum A a h g of the two channels
-                float r[3][2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float2 u = unpack2(ys[k]), v = unpack2(gb[k]), e = unpack2(gd[k]);
-                    r[0][k] = u.x + u.y, r[1][k] = v.x + v.y, r[2][k] = (e.x + e.y) * 0.6931471805599453f;
-                }
-                if (LN > 1) {
-#pragma unroll
-                    for (int q = 0; q < 3; ++q) {
-#pragma unroll
-                        for (int o = 2 * CL; o < 32; o <<= 1) {
-                            r[q][0] += __shfl_xor_sync(0xffffffffu, r[q][0], o);
-                            r[q][1] += __shfl_xor_sync(0xffffffffu, r[q][1], o);
-                        }
-                        const float give = fk ? r[q][0] : r[q][1], keep = fk ? r[q][1] : r[q][0];
-                        r[q][0] = keep + __shfl_xor_sync(0xffffffffu, give, CL);
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 f = ckpt[((sb - 1) * 4 + k) * kNT + tid];
+                        h[k >> 1][(k & 1) * 2] = pack2(f.x, f.y), h[k >> 1][(k & 1) * 2 + 1] = pack2(f.z, f.w);
                     }
                 }
-                T *dxp = (T *)p.dx + ((int64_t)line * p.T + t0 + t) * p.D + d;
-                T *dtp = (T *)p.ddt + ((int64_t)line * p.T + t0 + t) * p.D + d;
-                T *dzp = (T *)p.dz + ((int64_t)line * p.T + t0 + t) * p.D + d;
-                const float2 v = pair_at(t, 1);
 #pragma unroll
-                for (int q = 0; q < (LN > 1 ? 1 : 2); ++q) {  // the channel(s) this lane finishes
-                    const int k = LN > 1 ? fk : q;
-                    const float xk = k ? x.y : x.x, dk = k ? dl.y : dl.x, yk = k ? dy.y : dy.x, vk = (k ? v.y : v.x) + bias[k];
-                    const float zk = k ? z.y : z.x, sk = k ? sg.y : sg.x, ok = k ? go.y : go.x;
-                    const float y = fmaf(dv[k], xk, r[0][q]), s1 = r[1][q];
-                    float dd = fmaf(xk, s1, r[2][q]);
-                    // sigmoid(v) = exp(v - softplus(v))
-                    if (softplus) dd *= ex2f((vk - dk) * kLog2e);
-                    if (d + k < p.D && ln < 2) {
-                        dxp[k] = to_type<T>(fmaf(dv[k], yk, dk * s1));
-                        dtp[k] = to_type<T>(dd);
-                        if (gate && p.dz) dzp[k] = to_type<T>(ok * y * sk * fmaf(zk, 1.f - sk, 1.f));
-                    }
-                    dD[q] = fmaf(yk, xk, dD[q]);
-                    dbias[q] += dd;
+                for (int i = 0; i < SUB; ++i) {
+                    const int t = sb * SUB + i;
+                    if (EDGE && t >= m) continue;
+                    if (EDGE && (starts >> t & 1u)) boundary(p.h0, seg_of(t), h);
+                    forward(w[i], a[i], t);
                 }
-                // over the channels: dB and dC of this warp's
-                float *pw = part + ((warp * TG + t) * 2) * NP;
-                if constexpr (LN <= 8) {
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int j = 0; j < Q; ++j) {
-                        const float2 b = unpack2(rb[j / 2]), c = unpack2(rc[j / 2]);
-                        const uint32_t b0 = __float_as_uint(j & 1 ? b.y : b.x), b1 = __float_as_uint(j & 1 ? c.y : c.x);
-                        const uint32_t sel = lane >> 2 == j ? 0x3f800000u : 0u;
-                        if constexpr (sizeof(T) == 2) {
-                            mma_tf32(acc, sel, 0u, 0u, sel, b0, b1);
+                for (int i = SUB - 1; i >= 0; --i) {
+                    const int t = sb * SUB + i;
+                    if (EDGE && t >= m) continue;
+                    if (EDGE && (ends >> t & 1u)) boundary(p.dh_final, seg_of(t), g);
+                    const float2 dl = *reinterpret_cast<const float2 *>(dls + t * CH + ch), x = pair_at(t, 0);
+                    const float2 go = pair_at(t, 3);
+                    float2 z = make_float2(0.f, 0.f), sg = z, dy = go;
+                    if (gate) {
+                        z = pair_at(t, 2), sg = sigmoid2(z);
+                        dy.x *= z.x * sg.x, dy.y *= z.y * sg.y;
+                    }
+                    const f32x2 d2[2] = {pack2(dl.x, dl.x), pack2(dl.y, dl.y)};
+                    const float ux = dl.x * x.x, uy = dl.y * x.y;
+                    const f32x2 u2[2] = {pack2(ux, ux), pack2(uy, uy)};
+                    const f32x2 y2[2] = {pack2(dy.x, dy.x), pack2(dy.y, dy.y)};
+                    const float4 *b4 = reinterpret_cast<const float4 *>(bcs + t * 2 * NP + n0);
+                    f32x2 ys[2], gb[2], gd[2], rb[Q / 2], rc[Q / 2];
+#pragma unroll
+                    for (int j = 0; j < Q / 4; ++j) {
+                        const float4 b = b4[j], c = b4[NP / 4 + j];
+                        const f32x2 b2[2] = {pack2(b.x, b.y), pack2(b.z, b.w)}, c2[2] = {pack2(c.x, c.y), pack2(c.z, c.w)};
+#pragma unroll
+                        for (int l = 2 * j; l < 2 * j + 2; ++l)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const f32x2 hn = fma2(u2[k], b2[l & 1], w[i][k][l]);  // h_t
+                                const f32x2 gn = fma2(c2[l & 1], y2[k], g[k][l]);
+                                const f32x2 e = mul2(gn, w[i][k][l]);                 // g a h_{t-1}
+                                ys[k] = l ? fma2(hn, c2[l & 1], ys[k]) : mul2(hn, c2[0]);
+                                gb[k] = l ? fma2(gn, b2[l & 1], gb[k]) : mul2(gn, b2[0]);
+                                gd[k] = l ? fma2(e, a2[k][l], gd[k]) : mul2(e, a2[k][0]);
+                                rb[l] = k ? fma2(u2[k], gn, rb[l]) : mul2(u2[k], gn);
+                                rc[l] = k ? fma2(y2[k], hn, rc[l]) : mul2(y2[k], hn);
+                                dA[k][l] = fma2(e, d2[k], dA[k][l]);
+                                g[k][l] = mul2(gn, a[i][k][l]);
+                            }
+                    }
+                    if (EDGE && (starts >> t & 1u) && p.dh0)
+                        st_pair<Q>(p.dh0 + seg_of(t) * hrow + own, g, p.N, nn, p.n_wide, on);
+                    // over the channels: dB and dC of this warp's
+                    float *pw = part + t * 2 * NP;
+                    if constexpr (LN <= 8) {
+                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int j = 0; j < Q; ++j) {
+                            const float2 b = unpack2(rb[j / 2]), c = unpack2(rc[j / 2]);
+                            const uint32_t b0 = __float_as_uint(j & 1 ? b.y : b.x), b1 = __float_as_uint(j & 1 ? c.y : c.x);
+                            const uint32_t sel = lane >> 2 == j ? 0x3f800000u : 0u;
+                            if constexpr (sizeof(T) == 2) {
+                                mma_tf32(acc, sel, 0u, 0u, sel, b0, b1);
+                            } else {
+                                const uint32_t h0 = b0 & 0xffffe000u, h1 = b1 & 0xffffe000u;
+                                mma_tf32(acc, sel, 0u, 0u, sel, h0, h1);
+                                mma_tf32(acc, sel, 0u, 0u, sel, __float_as_uint(__uint_as_float(b0) - __uint_as_float(h0)),
+                                         __float_as_uint(__uint_as_float(b1) - __uint_as_float(h1)));
+                            }
+                        }
+                        // acc: rows lane / 4 (dB of that state) and + 8 (dC), columns 2 (lane % 4) and + 1;
+                        // column c holds the lanes 4 c .. 4 c + 3, of ln = 4 c / CL. Two warps add to
+                        // zeros: either order gives the same sum.
+                        const int row = lane >> 2, col = lane & 3;
+                        if constexpr (LN == 8) {
+                            atomicAdd(pw + 2 * col * Q + row, acc[0]), atomicAdd(pw + (2 * col + 1) * Q + row, acc[1]);
+                            atomicAdd(pw + NP + 2 * col * Q + row, acc[2]);
+                            atomicAdd(pw + NP + (2 * col + 1) * Q + row, acc[3]);
                         } else {
-                            const uint32_t h0 = b0 & 0xffffe000u, h1 = b1 & 0xffffe000u;
-                            mma_tf32(acc, sel, 0u, 0u, sel, h0, h1);
-                            mma_tf32(acc, sel, 0u, 0u, sel, __float_as_uint(__uint_as_float(b0) - __uint_as_float(h0)),
-                                     __float_as_uint(__uint_as_float(b1) - __uint_as_float(h1)));
+                            float sb0 = acc[0] + acc[1], sc0 = acc[2] + acc[3];
+                            if (LN <= 2)
+                                sb0 += __shfl_xor_sync(0xffffffffu, sb0, 1), sc0 += __shfl_xor_sync(0xffffffffu, sc0, 1);
+                            if (LN == 1)
+                                sb0 += __shfl_xor_sync(0xffffffffu, sb0, 2), sc0 += __shfl_xor_sync(0xffffffffu, sc0, 2);
+                            constexpr int kPer = 4 / LN;  // lanes with the same sum
+                            if (col % kPer == 0) {
+                                atomicAdd(pw + col / kPer * Q + row, sb0);
+                                atomicAdd(pw + NP + col / kPer * Q + row, sc0);
+                            }
                         }
-                    }
-                    // acc: rows lane / 4 (dB of that state) and + 8 (dC), columns 2 (lane % 4) and + 1;
-                    // column c holds the lanes 4 c .. 4 c + 3, of ln = 4 c / CL
-                    const int row = lane >> 2, col = lane & 3;
-                    if constexpr (LN == 8) {
-                        pw[2 * col * Q + row] = acc[0], pw[(2 * col + 1) * Q + row] = acc[1];
-                        pw[NP + 2 * col * Q + row] = acc[2], pw[NP + (2 * col + 1) * Q + row] = acc[3];
-                    } else {
-                        float sb0 = acc[0] + acc[1], sc0 = acc[2] + acc[3];
-                        if (LN <= 2) sb0 += __shfl_xor_sync(0xffffffffu, sb0, 1), sc0 += __shfl_xor_sync(0xffffffffu, sc0, 1);
-                        if (LN == 1) sb0 += __shfl_xor_sync(0xffffffffu, sb0, 2), sc0 += __shfl_xor_sync(0xffffffffu, sc0, 2);
-                        constexpr int kPer = 4 / LN;  // lanes with the same sum
-                        if (col % kPer == 0) {
-                            pw[col / kPer * Q + row] = sb0;
-                            pw[NP + col / kPer * Q + row] = sc0;
-                        }
-                    }
-                } else {  // two channel lanes: one shuffle each
+                    } else {  // two channel lanes: one shuffle each
 #pragma unroll
-                    for (int j = 0; j < Q; ++j) {
-                        const float2 b = unpack2(rb[j / 2]), c = unpack2(rc[j / 2]);
-                        float u = j & 1 ? b.y : b.x, w = j & 1 ? c.y : c.x;
-                        u += __shfl_xor_sync(0xffffffffu, u, 1), w += __shfl_xor_sync(0xffffffffu, w, 1);
-                        if (lc == 0) pw[n0 + j] = u, pw[NP + n0 + j] = w;
+                        for (int j = 0; j < Q; ++j) {
+                            const float2 b = unpack2(rb[j / 2]), c = unpack2(rc[j / 2]);
+                            float u = j & 1 ? b.y : b.x, v = j & 1 ? c.y : c.x;
+                            u += __shfl_xor_sync(0xffffffffu, u, 1), v += __shfl_xor_sync(0xffffffffu, v, 1);
+                            if (lc == 0) atomicAdd(pw + n0 + j, u), atomicAdd(pw + NP + n0 + j, v);
+                        }
+                    }
+                    // over the states: y, sum B g, sum A a h g of the two channels
+                    float r[3][2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float2 u = unpack2(ys[k]), v = unpack2(gb[k]), e = unpack2(gd[k]);
+                        r[0][k] = u.x + u.y, r[1][k] = v.x + v.y, r[2][k] = e.x + e.y;
+                    }
+                    if (LN > 1) {
+#pragma unroll
+                        for (int q = 0; q < 3; ++q) {
+#pragma unroll
+                            for (int o = 2 * CL; o < 32; o <<= 1) {
+                                r[q][0] += __shfl_xor_sync(0xffffffffu, r[q][0], o);
+                                r[q][1] += __shfl_xor_sync(0xffffffffu, r[q][1], o);
+                            }
+                            const float give = fk ? r[q][0] : r[q][1], keep = fk ? r[q][1] : r[q][0];
+                            r[q][0] = keep + __shfl_xor_sync(0xffffffffu, give, CL);
+                        }
+                    }
+                    const int64_t at = (int64_t)t * p.D;
+                    const float2 v = pair_at(t, 1);
+#pragma unroll
+                    for (int q = 0; q < (LN > 1 ? 1 : 2); ++q) {  // the channel(s) this lane finishes
+                        const int k = LN > 1 ? fk : q;
+                        const float xk = k ? x.y : x.x, dk = k ? dl.y : dl.x, yk = k ? dy.y : dy.x, vk = k ? v.y : v.x;
+                        const float zk = k ? z.y : z.x, sk = k ? sg.y : sg.x, ok = k ? go.y : go.x;
+                        const float y = fmaf(dvf[q], xk, r[0][q]), s1 = r[1][q];
+                        float dd = fmaf(xk, s1, r[2][q] * 0.6931471805599453f);
+                        // sigmoid(v) = exp(v - softplus(v))
+                        if (softplus) dd *= ex2f((vk + biasf[q] - dk) * kLog2e);
+                        if (fin[q]) {
+                            dxp[at + q] = to_type<T>(fmaf(dvf[q], yk, dk * s1));
+                            dtp[at + q] = to_type<T>(dd);
+                            if (gate && (USUAL || p.dz)) dzp[at + q] = to_type<T>(ok * y * sk * fmaf(zk, 1.f - sk, 1.f));
+                        }
+                        dD[q] = fmaf(yk, xk, dD[q]);
+                        dbias[q] += dd;
                     }
                 }
             }
-        }
+        };
+        if (m < TG || (starts | ends)) group(std::true_type());
+        else group(std::false_type());
         __syncthreads();
         // the tile's dB and dC of the group
         for (int e = tid; e < m * 2 * p.N; e += kNT) {
             const int r = e / (2 * p.N), k = e % (2 * p.N), n = k < p.N ? k : NP + k - p.N;
-            p.part_bc[((int64_t)tile * p.B * p.T + (int64_t)line * p.T + t0 + r) * (2 * p.N) + k] =
-                part[r * 2 * NP + n] + part[(TG + r) * 2 * NP + n];
+            p.part_bc[((int64_t)tile * p.B * p.T + (int64_t)line * p.T + t0 + r) * (2 * p.N) + k] = part[r * 2 * NP + n];
         }
     }
     st_pair<Q>(p.part_a + ((int64_t)line * p.nrun + run) * hrow + own, dA, p.N, nn, p.n_wide, on);
     float *pd = p.part_d + ((int64_t)line * p.nrun + run) * 2 * p.D + d;
 #pragma unroll
-    for (int q = 0; q < (LN > 1 ? 1 : 2); ++q) {
-        const int k = LN > 1 ? fk : q;
-        if (d + k < p.D && ln < 2) pd[k] = dD[q], pd[p.D + k] = dbias[q];
-    }
+    for (int q = 0; q < (LN > 1 ? 1 : 2); ++q)
+        if (fin[q]) pd[fk + q] = dD[q], pd[p.D + fk + q] = dbias[q];
 }
 
 // dB and dC: the channel tiles' partial sums, rounded once
@@ -585,7 +600,7 @@ cudaError_t sum_t(const SsmParams &p, cudaStream_t st) {
 template <typename T, int LN>
 cudaError_t walk_t(const SsmParams &p, cudaStream_t st) {
     constexpr int CH = 4 * (32 / LN), NP = 8 * LN;
-    constexpr int smem = 4 * kGroup * CH * (int)sizeof(T) + kGroup * CH * 4 + 3 * kGroup * 2 * NP * 4 + kGroup * kNT * 16;
+    constexpr int smem = 4 * kGroup * CH * (int)sizeof(T) + kGroup * CH * 4 + 2 * kGroup * 2 * NP * 4 + (kGroup - 8) * kNT * 16;
     const bool usual = p.vec && p.softplus && p.z;
     auto *k = usual ? ssm_bwd_kernel<T, LN, true> : ssm_bwd_kernel<T, LN, false>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
