@@ -232,71 +232,95 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Lanes: lane = ln * CL + lc has channels 2 lc, 2 lc + 1 of its warp and
-// states ln Q .. ln Q + Q - 1, Q = 8.
+constexpr int kWalk = 128;  // threads of the walk's CTA
+
+// Lanes: lane = ln * CL + lc has channel lc of its warp and states ln Q ..
+// ln Q + Q - 1, eight of them up to N = 64. More states a lane would spare
+// work that is repeated by a channel's lanes, but the four tokens' states and
+// decays then fill the register file (16 states a lane: 255 registers, two
+// warps a scheduler, 1.9 to 2.3 ms for 16384 tokens of 4096 channels).
 //
-// dB and dC are sums over channels, i.e. over lanes: 16 values a lane and
-// token. They are summed by the tensor cores, against ones: with the
-// lane's dB and dC of state j as the two B-fragment words (rows lane % 4 and
-// lane % 4 + 4 of column lane / 4) and A rows j and j + 8 selecting them, one
-// m16n8k8 adds each over the four lanes of a column, and 8 of them leave in
-// every lane two columns of two rows; the columns of one ln are added by
-// shuffles. Products enter as tf32: for bf16 tensors truncated (an error of
-// 2^-11 of a term against the result's 2^-9), for fp32 ones as the sum of two
-// parts (2^-21).
-template <typename T, int LN, bool USUAL>
-__global__ void __launch_bounds__(kNT) ssm_bwd_kernel(const SsmParams p, int ntile) {
-    constexpr int Q = 8, NP = Q * LN, CL = 32 / LN, CH = 2 * 2 * CL, TG = kGroup, SUB = 4;
-    constexpr int kTile = TG * CH;
+// dB and dC are sums over channels, i.e. over lanes: 2 Q values a lane and
+// token. The tensor cores add them over the lane's neighbours, against ones:
+// with four of the lane's values as the A fragment (rows lane / 4 and + 8,
+// columns lane % 4 and + 4) and B taking its upper four rows to column 2 i and
+// its lower four to 2 i + 1, an m16n8k8 adds the values over the four lanes
+// and leaves them to lane % 4 = i: four of them leave 16 sums, four a lane. The
+// lanes that still have parts of the same sums (lane / 4) share them out by
+// shuffles. Products enter as tf32: for bf16 tensors truncated (an error
+// under 2^-10 of a term against the result's 2^-9), for fp32 ones as the sum
+// of two parts (2^-21).
+template <typename T>
+__device__ __forceinline__ void mma_sum(float (&d)[4], f32x2 v0, f32x2 v1, uint32_t b0, uint32_t b1) {
+    const float2 a = unpack2(v0), c = unpack2(v1);
+    const float v[4] = {a.x, a.y, c.x, c.y};
+    if constexpr (sizeof(T) == 2) {
+        mma_tf32(d, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]), b0, b1);
+    } else {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[i] = __float_as_uint(v[i]) & 0xffffe000u;
+            l[i] = __float_as_uint(v[i] - __uint_as_float(h[i]));
+        }
+        mma_tf32(d, h[0], h[1], h[2], h[3], b0, b1);
+        mma_tf32(d, l[0], l[1], l[2], l[3], b0, b1);
+    }
+}
+
+template <typename T, int Q, int LN, bool USUAL>
+__global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const SsmParams p, int ntile) {
+    constexpr int NP = Q * LN, CL = 32 / LN, CH = 4 * CL, TG = kGroup, SUB = 4, H = Q / 2;
+    constexpr int kTile = TG * CH, kPart = TG * 2 * NP;
     extern __shared__ __align__(16) unsigned char smem[];
     T *tiles = reinterpret_cast<T *>(smem);                     // x, dt, z, dout: [4][TG][CH]
     float *dls = reinterpret_cast<float *>(tiles + 4 * kTile);  // delta: [TG][CH]
-    float *bcs = dls + kTile;                                   // [TG][2][NP]
-    float *part = bcs + TG * 2 * NP;                            // [TG][2][NP], both warps' sums
-    float4 *ckpt = reinterpret_cast<float4 *>(part + TG * 2 * NP);  // [TG / SUB - 2][4][kNT]
+    float *dys = dls + kTile;                                   // dy: [TG][CH]
+    float *bcs = dys + kTile;                                   // [TG][2][NP]
+    float *part = bcs + kPart;                                  // [2][TG][2][NP], two warps' sums each
+    float4 *ckpt = reinterpret_cast<float4 *>(part + 2 * kPart);  // [TG / SUB - 2][Q / 4][kWalk]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int ln = lane / CL, lc = lane % CL;
+    const int ln = lane / CL, lc = lane % CL, fk = ln & 1;
     const int tile = blockIdx.x % ntile, item = blockIdx.x / ntile;
     const int line = item / p.nrun, run = item - line * p.nrun;
     const int r0 = run * p.rlen, r1 = min(p.T - r0, p.rlen) + r0;
-    const int c0 = tile * CH, ch = warp * 2 * CL + 2 * lc, d = c0 + ch, n0 = ln * Q, nn = p.N - n0;
-    const bool on[2] = {d < p.D && nn > 0, d + 1 < p.D && nn > 0};
+    const int c0 = tile * CH, ch = warp * CL + lc, d = c0 + ch, n0 = ln * Q, nn = p.N - n0;
+    const bool on = d < p.D && nn > 0, fin = d < p.D && ln < 2;
+    const int ns = on ? nn : 0, qs = on ? Q : 0;
     const int64_t hrow = (int64_t)p.D * p.N, dnp = (int64_t)p.D * NP;
     const int64_t own = (int64_t)d * p.N + n0, own_p = (int64_t)d * NP + n0;
     const bool softplus = USUAL || p.softplus, gate = USUAL || p.z, vec = USUAL || p.vec;
 
-    f32x2 a2[2][Q / 2], g[2][Q / 2], dA[2][Q / 2], h[2][Q / 2], w[SUB][2][Q / 2], a[SUB][2][Q / 2];
-    ld_pair<Q>(a2, p.A + own, p.N, nn, p.n_wide, on);
+    f32x2 a2[H], g[H], dA[H], h[H], w[SUB][H], a[SUB][H];
+    ld_states<Q>(a2, p.A + own, ns, p.n_wide);
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int j = 0; j < Q / 2; ++j) {
-            a2[k][j] = mul2(a2[k][j], pack2(kLog2e, kLog2e));
-            g[k][j] = dA[k][j] = pack2(0.f, 0.f);
-        }
-    // from the run's end on
-    if (run + 1 < p.nrun) ld_pair<Q>(g, p.gs + ((int64_t)line * p.nrun + run + 1) * dnp + own_p, NP, Q, true, on);
-    // the channels this lane finishes: lane ln = k of a pair finishes channel k (LN > 1), or both
-    const int fk = LN > 1 ? ln & 1 : 0;
-    float dD[2] = {0.f, 0.f}, dbias[2] = {0.f, 0.f};
-    float dvf[2], biasf[2];
-    bool fin[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int c = d + fk + q;
-        fin[q] = c < p.D && ln < 2;
-        dvf[q] = p.Dv && c < p.D ? p.Dv[c] : 0.f, biasf[q] = p.dt_bias && c < p.D ? p.dt_bias[c] : 0.f;
+    for (int j = 0; j < H; ++j) {
+        a2[j] = mul2(a2[j], pack2(kLog2e, kLog2e));
+        g[j] = dA[j] = pack2(0.f, 0.f);
     }
+    // from the run's end on
+    if (run + 1 < p.nrun) ld_states<Q>(g, p.gs + ((int64_t)line * p.nrun + run + 1) * dnp + own_p, qs, true);
+    float dD = 0.f, dbias = 0.f;
+    const float dv = p.Dv && d < p.D ? p.Dv[d] : 0.f, bias = p.dt_bias && d < p.D ? p.dt_bias[d] : 0.f;
     const T *src[4] = {(const T *)p.x + line * p.x_sb, (const T *)p.dt + line * p.dt_sb,
                        (const T *)p.z + line * p.z_sb, (const T *)p.dout + line * p.do_sb};
     const int64_t str[4] = {p.x_st, p.dt_st, p.z_st, p.do_st};
 
-    auto boundary = [&](const float *from, int seg, f32x2 (&v)[2][Q / 2]) {  // a sequence's h0 or dh_final, or zero
+    // B fragments of the channel sums, and what a lane has of them: matrix and first state
+    uint32_t sel0[4], sel1[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        sel0[q] = lane >> 2 == 2 * q ? 0x3f800000u : 0u;
+        sel1[q] = lane >> 2 == 2 * q + 1 ? 0x3f800000u : 0u;
+    }
+    const int mat = lane >> 1 & 1, quad = (lane & 1) * 4;
+
+    auto boundary = [&](const float *from, int seg, f32x2 (&v)[H]) {  // a sequence's h0 or dh_final, or zero
         if (from) {
-            ld_pair<Q>(v, from + seg * hrow + own, p.N, nn, p.n_wide, on);
+            ld_states<Q>(v, from + seg * hrow + own, ns, p.n_wide);
         } else {
 #pragma unroll
-            for (int j = 0; j < Q / 2; ++j) v[0][j] = v[1][j] = pack2(0.f, 0.f);
+            for (int j = 0; j < H; ++j) v[j] = pack2(0.f, 0.f);
         }
     };
     for (int grp = (r1 - 1) / TG; grp * TG >= r0; --grp) {
@@ -305,10 +329,10 @@ __global__ void __launch_bounds__(kNT) ssm_bwd_kernel(const SsmParams p, int nti
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (k != 2 || gate)
-                ssm_fetch_tile<T, CH, TG, kNT>(tiles + k * kTile, src[k] + t0 * str[k], str[k], m, c0, p.D, vec);
+                ssm_fetch_tile<T, CH, TG, kWalk>(tiles + k * kTile, src[k] + t0 * str[k], str[k], m, c0, p.D, vec);
         cp_async_commit();
         {
-            SsmBc<T, NP, TG, kNT> bc;
+            SsmBc<T, NP, TG, kWalk> bc;
             bc.template fetch<true>((const T *)p.bm + line * p.bm_sb + t0 * p.bm_st, p.bm_st,
                                     (const T *)p.cm + line * p.cm_sb + t0 * p.cm_st, p.cm_st, m, p.N, p.bc_vec);
             bc.stage(bcs);
@@ -322,14 +346,12 @@ __global__ void __launch_bounds__(kNT) ssm_bwd_kernel(const SsmParams p, int nti
         }
         bool end_last = t0 + m == p.T;
         if (!end_last && p.cu) end_last = ssm_find(p.cu, p.n_seq, p.T, line, t0 + m).starts;
-        const int64_t o0 = ((int64_t)line * p.T + t0) * p.D + d + fk;
-        T *dxp = (T *)p.dx + o0, *dtp = (T *)p.ddt + o0, *dzp = (T *)p.dz + o0;
         const uint32_t ends = starts >> 1 | (end_last ? 1u << (m - 1) : 0u);
+        for (int e = tid; e < 2 * kPart; e += kWalk) part[e] = 0.f;
         cp_async_wait<0>();
         __syncthreads();
-        // delta of the tile, by pairs
-        for (int e = tid; e < TG * 2 * NP; e += kNT) part[e] = 0.f;
-        for (int e = tid; e < TG * CH / 2; e += kNT) {
+        // delta and dy of the tile, by pairs
+        for (int e = tid; e < kTile / 2; e += kWalk) {
             const int r = e / (CH / 2), c = e % (CH / 2) * 2;
             float f[2];
             ld_row_f<T, 2, true>(f, tiles + kTile + r * CH + c, 2);
@@ -340,13 +362,19 @@ __global__ void __launch_bounds__(kNT) ssm_bwd_kernel(const SsmParams p, int nti
             }
             if (softplus) v = softplus2(v);
             *reinterpret_cast<float2 *>(dls + r * CH + c) = v;
+            ld_row_f<T, 2, true>(f, tiles + 3 * kTile + r * CH + c, 2);
+            if (gate) {
+                float z[2];
+                ld_row_f<T, 2, true>(z, tiles + 2 * kTile + r * CH + c, 2);
+                const float2 sg = sigmoid2(make_float2(z[0], z[1]));
+                f[0] *= z[0] * sg.x, f[1] *= z[1] * sg.y;
+            }
+            *reinterpret_cast<float2 *>(dys + r * CH + c) = make_float2(f[0], f[1]);
         }
         __syncthreads();
-        auto pair_at = [&](int i, int k) {
-            float f[2];
-            ld_row_f<T, 2, true>(f, tiles + k * kTile + i * CH + ch, 2);
-            return make_float2(f[0], f[1]);
-        };
+        const T *xs = tiles + ch;
+        const int64_t o0 = ((int64_t)line * p.T + t0) * p.D + d;
+        T *dxp = (T *)p.dx + o0, *dtp = (T *)p.ddt + o0, *dzp = (T *)p.dz + o0;
         // Edge groups, in which a sequence begins or ends or which are not
         // whole, ask at every token; the others run without a branch.
         auto group = [&](auto edge_c) {
@@ -354,42 +382,58 @@ __global__ void __launch_bounds__(kNT) ssm_bwd_kernel(const SsmParams p, int nti
             const int nsub = EDGE ? (m + SUB - 1) / SUB : TG / SUB;
             auto seg_of = [&](int t) { return ssm_find(p.cu, p.n_seq, p.T, line, t0 + t).seg; };
             // one token forward: wd = a h, h <- wd + u B
-            auto forward = [&](f32x2 (&wd)[2][Q / 2], f32x2 (&ad)[2][Q / 2], int i) {
-                const float2 dl = *reinterpret_cast<const float2 *>(dls + i * CH + ch), x = pair_at(i, 0);
-                const f32x2 d2[2] = {pack2(dl.x, dl.x), pack2(dl.y, dl.y)};
-                const float ux = dl.x * x.x, uy = dl.y * x.y;
-                const f32x2 u2[2] = {pack2(ux, ux), pack2(uy, uy)};
+            auto forward = [&](f32x2 (&wd)[H], f32x2 (&ad)[H], int i) {
+                const float dl = dls[i * CH + ch], u = dl * ldf(xs + i * CH);
+                const f32x2 d2 = pack2(dl, dl), u2 = pack2(u, u);
                 const float4 *b4 = reinterpret_cast<const float4 *>(bcs + i * 2 * NP + n0);
 #pragma unroll
                 for (int j = 0; j < Q / 4; ++j) {
                     const float4 b = b4[j];
                     const f32x2 b2[2] = {pack2(b.x, b.y), pack2(b.z, b.w)};
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int l = 2 * j; l < 2 * j + 2; ++l) {
-                            ad[k][l] = ex2_2(mul2(d2[k], a2[k][l]));
-                            wd[k][l] = mul2(ad[k][l], h[k][l]);
-                            h[k][l] = fma2(u2[k], b2[l & 1], wd[k][l]);
-                        }
+                    for (int l = 2 * j; l < 2 * j + 2; ++l) {
+                        ad[l] = ex2_2(mul2(d2, a2[l]));
+                        wd[l] = mul2(ad[l], h[l]);
+                        h[l] = fma2(u2, b2[l & 1], wd[l]);
+                    }
                 }
             };
             // the state entering the group; the first sub-block's is read again
             // where the walk reaches it, the last one's stays in registers
             auto enter = [&] {
                 if (grp > 0 && !(EDGE && (starts & 1u)))
-                    ld_pair<Q>(h, p.sums + ((int64_t)line * p.ngroup + grp - 1) * dnp + own_p, NP, Q, true, on);
+                    ld_states<Q>(h, p.sums + ((int64_t)line * p.ngroup + grp - 1) * dnp + own_p, qs, true);
                 else
                     boundary(nullptr, 0, h);
+            };
+            // what a channel's outputs need of token t: its sums over the states
+            auto finish = [&](int t, float y, float s1, float s2, bool here) {
+                const float dl = dls[t * CH + ch], dy = dys[t * CH + ch], x = ldf(xs + t * CH);
+                y = fmaf(dv, x, y);
+                float dd = fmaf(x, s1, s2 * 0.6931471805599453f);
+                // sigmoid(v) = exp(v - softplus(v))
+                if (softplus) dd *= ex2f((ldf(xs + kTile + t * CH) + bias - dl) * kLog2e);
+                if (fin && here) {
+                    const int64_t at = (int64_t)t * p.D;
+                    dxp[at] = to_type<T>(fmaf(dv, dy, dl * s1));
+                    dtp[at] = to_type<T>(dd);
+                    if (gate && (USUAL || p.dz)) {
+                        const float z = ldf(xs + 2 * kTile + t * CH), go = ldf(xs + 3 * kTile + t * CH);
+                        const float sg = rcpf(1.f + ex2f(z * -kLog2e));
+                        dzp[at] = to_type<T>(go * y * sg * fmaf(z, 1.f - sg, 1.f));
+                    }
+                    dD = fmaf(dy, x, dD);
+                    dbias += dd;
+                }
             };
             enter();
 #pragma unroll 1
             for (int sb = 0; sb + 1 < nsub; ++sb) {
                 if (sb > 0) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 u = unpack2(h[k >> 1][(k & 1) * 2]), v = unpack2(h[k >> 1][(k & 1) * 2 + 1]);
-                        ckpt[((sb - 1) * 4 + k) * kNT + tid] = make_float4(u.x, u.y, v.x, v.y);
+                    for (int k = 0; k < Q / 4; ++k) {
+                        const float2 u = unpack2(h[2 * k]), v = unpack2(h[2 * k + 1]);
+                        ckpt[((sb - 1) * (Q / 4) + k) * kWalk + tid] = make_float4(u.x, u.y, v.x, v.y);
                     }
                 }
 #pragma unroll
@@ -405,9 +449,9 @@ __global__ void __launch_bounds__(kNT) ssm_bwd_kernel(const SsmParams p, int nti
                     enter();
                 } else if (sb + 1 < nsub) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 f = ckpt[((sb - 1) * 4 + k) * kNT + tid];
-                        h[k >> 1][(k & 1) * 2] = pack2(f.x, f.y), h[k >> 1][(k & 1) * 2 + 1] = pack2(f.z, f.w);
+                    for (int k = 0; k < Q / 4; ++k) {
+                        const float4 f = ckpt[((sb - 1) * (Q / 4) + k) * kWalk + tid];
+                        h[2 * k] = pack2(f.x, f.y), h[2 * k + 1] = pack2(f.z, f.w);
                     }
                 }
 #pragma unroll
@@ -417,130 +461,93 @@ __global__ void __launch_bounds__(kNT) ssm_bwd_kernel(const SsmParams p, int nti
                     if (EDGE && (starts >> t & 1u)) boundary(p.h0, seg_of(t), h);
                     forward(w[i], a[i], t);
                 }
+                float r[2][3];  // y, sum B g, sum A a h g of two tokens
 #pragma unroll
                 for (int i = SUB - 1; i >= 0; --i) {
                     const int t = sb * SUB + i;
-                    if (EDGE && t >= m) continue;
-                    if (EDGE && (ends >> t & 1u)) boundary(p.dh_final, seg_of(t), g);
-                    const float2 dl = *reinterpret_cast<const float2 *>(dls + t * CH + ch), x = pair_at(t, 0);
-                    const float2 go = pair_at(t, 3);
-                    float2 z = make_float2(0.f, 0.f), sg = z, dy = go;
-                    if (gate) {
-                        z = pair_at(t, 2), sg = sigmoid2(z);
-                        dy.x *= z.x * sg.x, dy.y *= z.y * sg.y;
-                    }
-                    const f32x2 d2[2] = {pack2(dl.x, dl.x), pack2(dl.y, dl.y)};
-                    const float ux = dl.x * x.x, uy = dl.y * x.y;
-                    const f32x2 u2[2] = {pack2(ux, ux), pack2(uy, uy)};
-                    const f32x2 y2[2] = {pack2(dy.x, dy.x), pack2(dy.y, dy.y)};
-                    const float4 *b4 = reinterpret_cast<const float4 *>(bcs + t * 2 * NP + n0);
-                    f32x2 ys[2], gb[2], gd[2], rb[Q / 2], rc[Q / 2];
+                    if (EDGE && t >= m) {
+                        r[i & 1][0] = r[i & 1][1] = r[i & 1][2] = 0.f;
+                    } else {
+                        if (EDGE && (ends >> t & 1u)) boundary(p.dh_final, seg_of(t), g);
+                        const float dl = dls[t * CH + ch], u = dl * ldf(xs + t * CH), dy = dys[t * CH + ch];
+                        const f32x2 d2 = pack2(dl, dl), u2 = pack2(u, u), y2 = pack2(dy, dy);
+                        const float4 *b4 = reinterpret_cast<const float4 *>(bcs + t * 2 * NP + n0);
+                        f32x2 ys, gb, gd, rb[H], rc[H];
 #pragma unroll
-                    for (int j = 0; j < Q / 4; ++j) {
-                        const float4 b = b4[j], c = b4[NP / 4 + j];
-                        const f32x2 b2[2] = {pack2(b.x, b.y), pack2(b.z, b.w)}, c2[2] = {pack2(c.x, c.y), pack2(c.z, c.w)};
-#pragma unroll
-                        for (int l = 2 * j; l < 2 * j + 2; ++l)
+                        for (int j = 0; j < Q / 4; ++j) {
+                            const float4 b = b4[j], c = b4[NP / 4 + j];
+                            const f32x2 b2[2] = {pack2(b.x, b.y), pack2(b.z, b.w)};
+                            const f32x2 c2[2] = {pack2(c.x, c.y), pack2(c.z, c.w)};
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                const f32x2 hn = fma2(u2[k], b2[l & 1], w[i][k][l]);  // h_t
-                                const f32x2 gn = fma2(c2[l & 1], y2[k], g[k][l]);
-                                const f32x2 e = mul2(gn, w[i][k][l]);                 // g a h_{t-1}
-                                ys[k] = l ? fma2(hn, c2[l & 1], ys[k]) : mul2(hn, c2[0]);
-                                gb[k] = l ? fma2(gn, b2[l & 1], gb[k]) : mul2(gn, b2[0]);
-                                gd[k] = l ? fma2(e, a2[k][l], gd[k]) : mul2(e, a2[k][0]);
-                                rb[l] = k ? fma2(u2[k], gn, rb[l]) : mul2(u2[k], gn);
-                                rc[l] = k ? fma2(y2[k], hn, rc[l]) : mul2(y2[k], hn);
-                                dA[k][l] = fma2(e, d2[k], dA[k][l]);
-                                g[k][l] = mul2(gn, a[i][k][l]);
+                                const int l = 2 * j + k;
+                                const f32x2 hn = fma2(u2, b2[k], w[i][l]);  // h_t
+                                const f32x2 gn = fma2(c2[k], y2, g[l]);
+                                const f32x2 e = mul2(gn, w[i][l]);          // g a h_{t-1}
+                                ys = l ? fma2(hn, c2[k], ys) : mul2(hn, c2[k]);
+                                gb = l ? fma2(gn, b2[k], gb) : mul2(gn, b2[k]);
+                                gd = l ? fma2(e, a2[l], gd) : mul2(e, a2[l]);
+                                rb[l] = mul2(u2, gn), rc[l] = mul2(y2, hn);
+                                dA[l] = fma2(e, d2, dA[l]);
+                                g[l] = mul2(gn, a[i][l]);
                             }
-                    }
-                    if (EDGE && (starts >> t & 1u) && p.dh0)
-                        st_pair<Q>(p.dh0 + seg_of(t) * hrow + own, g, p.N, nn, p.n_wide, on);
-                    // over the channels: dB and dC of this warp's
-                    float *pw = part + t * 2 * NP;
-                    if constexpr (LN <= 8) {
-                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                        }
+                        if (EDGE && (starts >> t & 1u) && p.dh0)
+                            st_states<Q>(p.dh0 + seg_of(t) * hrow + own, g, ns, p.n_wide);
+                        const float2 v0 = unpack2(ys), v1 = unpack2(gb), v2 = unpack2(gd);
+                        r[i & 1][0] = v0.x + v0.y, r[i & 1][1] = v1.x + v1.y, r[i & 1][2] = v2.x + v2.y;
+                        // over the channels: dB and dC. Two warps add to zeros: either order gives
+                        // the same sum.
+                        float *pw = part + (warp >> 1) * kPart + t * 2 * NP + mat * NP;
 #pragma unroll
-                        for (int j = 0; j < Q; ++j) {
-                            const float2 b = unpack2(rb[j / 2]), c = unpack2(rc[j / 2]);
-                            const uint32_t b0 = __float_as_uint(j & 1 ? b.y : b.x), b1 = __float_as_uint(j & 1 ? c.y : c.x);
-                            const uint32_t sel = lane >> 2 == j ? 0x3f800000u : 0u;
-                            if constexpr (sizeof(T) == 2) {
-                                mma_tf32(acc, sel, 0u, 0u, sel, b0, b1);
+                        for (int o = 0; o < Q / 8; ++o) {
+                            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                mma_sum<T>(acc, rb[4 * o + 2 * q], rb[4 * o + 2 * q + 1], sel0[q], sel1[q]);
+                                mma_sum<T>(acc, rc[4 * o + 2 * q], rc[4 * o + 2 * q + 1], sel0[2 + q], sel1[2 + q]);
+                            }
+                            // acc: states 0, 2, 1, 3 of quad lane % 4 (dB, dB, dC, dC), of the channels of
+                            // lanes with this lane / 4; bits 2, 3, 4 of the lane below CL are channels too
+                            float *po = pw + n0 + 8 * o + quad;
+                            if constexpr (CL == 4) {
+                                atomicAdd(po, acc[0]), atomicAdd(po + 1, acc[2]), atomicAdd(po + 2, acc[1]), atomicAdd(po + 3, acc[3]);
                             } else {
-                                const uint32_t h0 = b0 & 0xffffe000u, h1 = b1 & 0xffffe000u;
-                                mma_tf32(acc, sel, 0u, 0u, sel, h0, h1);
-                                mma_tf32(acc, sel, 0u, 0u, sel, __float_as_uint(__uint_as_float(b0) - __uint_as_float(h0)),
-                                         __float_as_uint(__uint_as_float(b1) - __uint_as_float(h1)));
+                                const bool u2 = lane & 4, u3 = lane & 8;
+                                const float g0 = u2 ? acc[0] : acc[2], g1 = u2 ? acc[1] : acc[3];
+                                float k0 = u2 ? acc[2] : acc[0], k1 = u2 ? acc[3] : acc[1];
+                                k0 += __shfl_xor_sync(0xffffffffu, g0, 4);
+                                k1 += __shfl_xor_sync(0xffffffffu, g1, 4);
+                                if constexpr (CL == 8) {
+                                    atomicAdd(po + (u2 ? 1 : 0), k0), atomicAdd(po + (u2 ? 3 : 2), k1);
+                                } else {
+                                    const float g2 = u3 ? k0 : k1;
+                                    float k2 = u3 ? k1 : k0;
+                                    k2 += __shfl_xor_sync(0xffffffffu, g2, 8);
+                                    if (CL == 32) k2 += __shfl_xor_sync(0xffffffffu, k2, 16);
+                                    if (CL == 16 || !(lane & 16)) atomicAdd(po + (u2 ? 1 : 0) + (u3 ? 2 : 0), k2);
+                                }
                             }
                         }
-                        // acc: rows lane / 4 (dB of that state) and + 8 (dC), columns 2 (lane % 4) and + 1;
-                        // column c holds the lanes 4 c .. 4 c + 3, of ln = 4 c / CL. Two warps add to
-                        // zeros: either order gives the same sum.
-                        const int row = lane >> 2, col = lane & 3;
-                        if constexpr (LN == 8) {
-                            atomicAdd(pw + 2 * col * Q + row, acc[0]), atomicAdd(pw + (2 * col + 1) * Q + row, acc[1]);
-                            atomicAdd(pw + NP + 2 * col * Q + row, acc[2]);
-                            atomicAdd(pw + NP + (2 * col + 1) * Q + row, acc[3]);
-                        } else {
-                            float sb0 = acc[0] + acc[1], sc0 = acc[2] + acc[3];
-                            if (LN <= 2)
-                                sb0 += __shfl_xor_sync(0xffffffffu, sb0, 1), sc0 += __shfl_xor_sync(0xffffffffu, sc0, 1);
-                            if (LN == 1)
-                                sb0 += __shfl_xor_sync(0xffffffffu, sb0, 2), sc0 += __shfl_xor_sync(0xffffffffu, sc0, 2);
-                            constexpr int kPer = 4 / LN;  // lanes with the same sum
-                            if (col % kPer == 0) {
-                                atomicAdd(pw + col / kPer * Q + row, sb0);
-                                atomicAdd(pw + NP + col / kPer * Q + row, sc0);
-                            }
-                        }
-                    } else {  // two channel lanes: one shuffle each
-#pragma unroll
-                        for (int j = 0; j < Q; ++j) {
-                            const float2 b = unpack2(rb[j / 2]), c = unpack2(rc[j / 2]);
-                            float u = j & 1 ? b.y : b.x, v = j & 1 ? c.y : c.x;
-                            u += __shfl_xor_sync(0xffffffffu, u, 1), v += __shfl_xor_sync(0xffffffffu, v, 1);
-                            if (lc == 0) atomicAdd(pw + n0 + j, u), atomicAdd(pw + NP + n0 + j, v);
-                        }
                     }
-                    // over the states: y, sum B g, sum A a h g of the two channels
-                    float r[3][2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float2 u = unpack2(ys[k]), v = unpack2(gb[k]), e = unpack2(gd[k]);
-                        r[0][k] = u.x + u.y, r[1][k] = v.x + v.y, r[2][k] = e.x + e.y;
-                    }
-                    if (LN > 1) {
+                    if (i & 1) continue;
+                    // two tokens are done: lanes ln = 0 and 1 finish one each
+                    if constexpr (LN == 1) {
+                        finish(t + 1, r[1][0], r[1][1], r[1][2], !EDGE || t + 1 < m);
+                        finish(t, r[0][0], r[0][1], r[0][2], !EDGE || t < m);
+                    } else {
+                        float s[3];
 #pragma unroll
                         for (int q = 0; q < 3; ++q) {
 #pragma unroll
                             for (int o = 2 * CL; o < 32; o <<= 1) {
-                                r[q][0] += __shfl_xor_sync(0xffffffffu, r[q][0], o);
-                                r[q][1] += __shfl_xor_sync(0xffffffffu, r[q][1], o);
+                                r[0][q] += __shfl_xor_sync(0xffffffffu, r[0][q], o);
+                                r[1][q] += __shfl_xor_sync(0xffffffffu, r[1][q], o);
                             }
-                            const float give = fk ? r[q][0] : r[q][1], keep = fk ? r[q][1] : r[q][0];
-                            r[q][0] = keep + __shfl_xor_sync(0xffffffffu, give, CL);
+                            const float give = fk ? r[0][q] : r[1][q], keep = fk ? r[1][q] : r[0][q];
+                            s[q] = keep + __shfl_xor_sync(0xffffffffu, give, CL);
                         }
-                    }
-                    const int64_t at = (int64_t)t * p.D;
-                    const float2 v = pair_at(t, 1);
-#pragma unroll
-                    for (int q = 0; q < (LN > 1 ? 1 : 2); ++q) {  // the channel(s) this lane finishes
-                        const int k = LN > 1 ? fk : q;
-                        const float xk = k ? x.y : x.x, dk = k ? dl.y : dl.x, yk = k ? dy.y : dy.x, vk = k ? v.y : v.x;
-                        const float zk = k ? z.y : z.x, sk = k ? sg.y : sg.x, ok = k ? go.y : go.x;
-                        const float y = fmaf(dvf[q], xk, r[0][q]), s1 = r[1][q];
-                        float dd = fmaf(xk, s1, r[2][q] * 0.6931471805599453f);
-                        // sigmoid(v) = exp(v - softplus(v))
-                        if (softplus) dd *= ex2f((vk + biasf[q] - dk) * kLog2e);
-                        if (fin[q]) {
-                            dxp[at + q] = to_type<T>(fmaf(dvf[q], yk, dk * s1));
-                            dtp[at + q] = to_type<T>(dd);
-                            if (gate && (USUAL || p.dz)) dzp[at + q] = to_type<T>(ok * y * sk * fmaf(zk, 1.f - sk, 1.f));
-                        }
-                        dD[q] = fmaf(yk, xk, dD[q]);
-                        dbias[q] += dd;
+                        finish(t + fk, s[0], s[1], s[2], !EDGE || t + fk < m);
                     }
                 }
             }
@@ -549,16 +556,21 @@ __global__ void __launch_bounds__(kNT) ssm_bwd_kernel(const SsmParams p, int nti
         else group(std::false_type());
         __syncthreads();
         // the tile's dB and dC of the group
-        for (int e = tid; e < m * 2 * p.N; e += kNT) {
-            const int r = e / (2 * p.N), k = e % (2 * p.N), n = k < p.N ? k : NP + k - p.N;
-            p.part_bc[((int64_t)tile * p.B * p.T + (int64_t)line * p.T + t0 + r) * (2 * p.N) + k] = part[r * 2 * NP + n];
+        for (int e = tid; e < m * 2 * p.N; e += kWalk) {
+            const int r = e / (2 * p.N), k = e % (2 * p.N), n = r * 2 * NP + (k < p.N ? k : NP + k - p.N);
+            p.part_bc[((int64_t)tile * p.B * p.T + (int64_t)line * p.T + t0 + r) * (2 * p.N) + k] = part[n] + part[kPart + n];
         }
     }
-    st_pair<Q>(p.part_a + ((int64_t)line * p.nrun + run) * hrow + own, dA, p.N, nn, p.n_wide, on);
-    float *pd = p.part_d + ((int64_t)line * p.nrun + run) * 2 * p.D + d;
-#pragma unroll
-    for (int q = 0; q < (LN > 1 ? 1 : 2); ++q)
-        if (fin[q]) pd[fk + q] = dD[q], pd[p.D + fk + q] = dbias[q];
+    st_states<Q>(p.part_a + ((int64_t)line * p.nrun + run) * hrow + own, dA, ns, p.n_wide);
+    // dD and dbias: each of the two lanes has half of the tokens
+    if (LN > 1) {
+        dD += __shfl_xor_sync(0xffffffffu, dD, CL);
+        dbias += __shfl_xor_sync(0xffffffffu, dbias, CL);
+    }
+    if (d < p.D && ln == 0) {
+        float *pd = p.part_d + ((int64_t)line * p.nrun + run) * 2 * p.D + d;
+        pd[0] = dD, pd[p.D] = dbias;
+    }
 }
 
 // dB and dC: the channel tiles' partial sums, rounded once
@@ -597,27 +609,28 @@ cudaError_t sum_t(const SsmParams &p, cudaStream_t st) {
     k<<<(unsigned)(items * ntile), kNT, smem, st>>>(p, ntile);
     return cudaGetLastError();
 }
-template <typename T, int LN>
+template <typename T, int Q, int LN>
 cudaError_t walk_t(const SsmParams &p, cudaStream_t st) {
-    constexpr int CH = 4 * (32 / LN), NP = 8 * LN;
-    constexpr int smem = 4 * kGroup * CH * (int)sizeof(T) + kGroup * CH * 4 + 2 * kGroup * 2 * NP * 4 + (kGroup - 8) * kNT * 16;
-    const bool usual = p.vec && p.softplus && p.z;
-    auto *k = usual ? ssm_bwd_kernel<T, LN, true> : ssm_bwd_kernel<T, LN, false>;
+    constexpr int CH = kWalk / LN, NP = Q * LN;
+    constexpr int smem = 4 * kGroup * CH * (int)sizeof(T) + 2 * kGroup * CH * 4 + 3 * kGroup * 2 * NP * 4 +
+                         (kGroup / 4 - 2) * (Q / 4) * kWalk * 16;
+    const bool usual = p.vec && p.softplus && p.z && p.dz;
+    auto *k = usual ? ssm_bwd_kernel<T, Q, LN, true> : ssm_bwd_kernel<T, Q, LN, false>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int ntile = ssm_bwd_tiles(p.D, p.N);
     const int64_t items = (int64_t)(p.cu ? 1 : p.B) * p.nrun;
     if (items * ntile > INT32_MAX) return cudaErrorInvalidValue;
-    k<<<(unsigned)(items * ntile), kNT, smem, st>>>(p, ntile);
+    k<<<(unsigned)(items * ntile), kWalk, smem, st>>>(p, ntile);
     return cudaGetLastError();
 }
-// lanes a channel pair of the walk back, at eight states a lane
-int walk_lanes(int N) { return N <= 8 ? 1 : N <= 16 ? 2 : N <= 32 ? 4 : N <= 64 ? 8 : 16; }
+// lanes a channel of the walk back: eight states a lane, sixteen above N = 64
+int walk_lanes(int N) { return N <= 8 ? 1 : N <= 16 ? 2 : N <= 32 ? 4 : 8; }
 
 }  // namespace
 
 int ssm_bwd_tiles(int D, int N) {
-    const int ch = 4 * (32 / walk_lanes(N));
+    const int ch = kWalk / walk_lanes(N);
     return (D + ch - 1) / ch;
 }
 // Tokens a run: 256, less where there are few channels.
@@ -639,14 +652,17 @@ cudaError_t launch_ssm_bwd_chain(const SsmParams &p, cudaStream_t st) {
     return cudaGetLastError();
 }
 cudaError_t launch_ssm_bwd(const SsmParams &p, cudaStream_t st) {
-    auto f = [&](auto ln) { return p.bf16 ? walk_t<__nv_bfloat16, ln()>(p, st) : walk_t<float, ln()>(p, st); };
+    auto f = [&](auto q, auto ln) {
+        return p.bf16 ? walk_t<__nv_bfloat16, q(), ln()>(p, st) : walk_t<float, q(), ln()>(p, st);
+    };
+    using I8 = std::integral_constant<int, 8>;
+    if (p.N > 64) return f(std::integral_constant<int, 16>(), I8());
     switch (walk_lanes(p.N)) {
-        case 1: return f(std::integral_constant<int, 1>());
-        case 2: return f(std::integral_constant<int, 2>());
-        case 4: return f(std::integral_constant<int, 4>());
-        case 8: return f(std::integral_constant<int, 8>());
+        case 1: return f(I8(), std::integral_constant<int, 1>());
+        case 2: return f(I8(), std::integral_constant<int, 2>());
+        case 4: return f(I8(), std::integral_constant<int, 4>());
     }
-    return f(std::integral_constant<int, 16>());
+    return f(I8(), I8());
 }
 cudaError_t launch_ssm_bwd_reduce(const SsmParams &p, cudaStream_t st) {
     const int64_t n = (int64_t)p.B * p.T * 2 * p.N;
