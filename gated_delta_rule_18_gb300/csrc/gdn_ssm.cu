@@ -21,21 +21,50 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 64;  // a CTA: 2 * 64 / LN channels
-constexpr int kStage = 16;    // tokens a stage
+constexpr int kStage = 8;     // tokens a stage
 
-// A lane has Q states, in packed pairs, of two neighbouring channels; LN lanes
-// a channel (LN = 1 up to 16 states, so nothing crosses lanes there). x, dt and z
-// come through a ring of three stages of shared memory, two stages ahead of
-// their use; B and C, the same for every channel, are staged as fp32 and read
-// by broadcast, 4 bytes a (channel, state). USUAL: softplus, a gate and rows
-// for wide accesses, known beforehand.
+// The states of two channels as pairs of one state each: v[j] = (channel 0's
+// state j, channel 1's).
+template <int Q>
+__device__ __forceinline__ void ld_across(f32x2 (&v)[Q], const float *p, int ld, int n, bool wide, const bool (&on)[2]) {
+    f32x2 a[2][Q / 2];
+    ld_pair<Q>(a, p, ld, n, wide, on);
+#pragma unroll
+    for (int j = 0; j < Q / 2; ++j) {
+        const float2 x = unpack2(a[0][j]), y = unpack2(a[1][j]);
+        v[2 * j] = pack2(x.x, y.x), v[2 * j + 1] = pack2(x.y, y.y);
+    }
+}
+template <int Q>
+__device__ __forceinline__ void st_across(float *p, const f32x2 (&v)[Q], int ld, int n, bool wide, const bool (&on)[2]) {
+    f32x2 a[2][Q / 2];
+#pragma unroll
+    for (int j = 0; j < Q / 2; ++j) {
+        const float2 x = unpack2(v[2 * j]), y = unpack2(v[2 * j + 1]);
+        a[0][j] = pack2(x.x, y.x), a[1][j] = pack2(x.y, y.y);
+    }
+    st_pair<Q>(p, a, ld, n, wide, on);
+}
+
+// A lane has Q states of two neighbouring channels, which are the halves of
+// its packed pairs; LN lanes a channel (LN = 1 up to 16 states, so nothing crosses lanes there). x, dt and
+// z come through two shared-memory buffers, a stage ahead of their use; B and
+// C, the same for every channel, are staged as fp32 and read by broadcast, 4
+// bytes a (channel, state). A stage has three loops: delta and delta x of its
+// tokens (the chain of a softplus is some 150 cycles: four tokens' side by
+// side hide it), the states, whose only chain is one multiply-add a token, and
+// the outputs; between them a thread's own slots of shared memory. One loop
+// that did all three took 0.33 ms where this takes SCAN_MS for 32768 tokens
+// of 2048 channels. USUAL: softplus, a gate and rows for wide accesses, known
+// beforehand.
 template <typename T, int Q, int LN, bool SUM, bool USUAL>
-__global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const SsmParams p, int ntile) {
-    constexpr int CH = 2 * kThreads / LN, NP = Q * LN, TS = kStage, K = 1;  // K: tokens in flight
+__global__ void __launch_bounds__(kThreads, 6) ssm_scan_kernel(const SsmParams p, int ntile) {
+    constexpr int CH = 2 * kThreads / LN, NP = Q * LN, TS = kStage;
     constexpr int NA = SUM ? 2 : 3;  // x, dt, z
     constexpr int kTile = TS * CH * (int)sizeof(T), kBuf = NA * kTile, kBc = TS * 2 * NP;
     extern __shared__ __align__(16) unsigned char smem[];
-    float *bcs = reinterpret_cast<float *>(smem + 3 * kBuf);  // [2][TS][2][NP]
+    float4 *slot = reinterpret_cast<float4 *>(smem + 2 * kBuf) + threadIdx.x;  // [TS][kThreads], delta, delta x or y
+    float *bcs = reinterpret_cast<float *>(smem + 2 * kBuf + TS * kThreads * 16);  // [2][TS][2][NP]
     const int tid = threadIdx.x, ch = tid / LN * 2, ln = tid % LN;
     const int tile = blockIdx.x % ntile, item = blockIdx.x / ntile;
     const int nch = SUM ? p.nchunk - 1 : p.nchunk;
@@ -43,17 +72,14 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const SsmParams p, i
     if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
     const int t0 = chunk * p.clen, t1 = min(p.T - t0, p.clen) + t0;
     const int c0 = tile * CH, d = c0 + ch, n0 = ln * Q, nn = p.N - n0;
-    const bool on[2] = {d < p.D && nn > 0, d + 1 < p.D && nn > 0};
+    const bool on[2] = {d < p.D && nn > 0, d + 1 < p.D && nn > 0}, out = d < p.D && ln == 0;
     const int64_t hrow = (int64_t)p.D * p.N, dnp = (int64_t)p.D * NP;
     const int64_t own = (int64_t)d * p.N + n0, own_p = (int64_t)d * NP + n0;
 
-    f32x2 a2[2][Q / 2], h[2][Q / 2];
-    ld_pair<Q>(a2, p.A + own, p.N, nn, p.n_wide, on);
+    f32x2 a2[Q], h[Q];
+    ld_across<Q>(a2, p.A + own, p.N, nn, p.n_wide, on);
 #pragma unroll
-    for (int j = 0; j < Q / 2; ++j) {
-        a2[0][j] = mul2(a2[0][j], pack2(kLog2e, kLog2e));
-        a2[1][j] = mul2(a2[1][j], pack2(kLog2e, kLog2e));
-    }
+    for (int j = 0; j < Q; ++j) a2[j] = mul2(a2[j], pack2(kLog2e, kLog2e));
     auto pair_of = [&](const float *v) {
         return make_float2(v && d < p.D ? v[d] : 0.f, v && d + 1 < p.D ? v[d + 1] : 0.f);
     };
@@ -61,27 +87,26 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const SsmParams p, i
     const float2 bias = pair_of(p.dt_bias), dv = pair_of(SUM ? nullptr : p.Dv);
     auto zero_h = [&] {
 #pragma unroll
-        for (int j = 0; j < Q / 2; ++j) h[0][j] = h[1][j] = pack2(0.f, 0.f);
+        for (int j = 0; j < Q; ++j) h[j] = pack2(0.f, 0.f);
     };
     auto first_h = [&](int seg) {
-        if (p.h0) ld_pair<Q>(h, p.h0 + seg * hrow + own, p.N, nn, p.n_wide, on);
+        if (p.h0) ld_across<Q>(h, p.h0 + seg * hrow + own, p.N, nn, p.n_wide, on);
         else zero_h();
     };
     SsmSeq q{0, 0, false};
     if (t0 < t1) q = ssm_find(p.cu, p.n_seq, p.T, line, t0);
     bool reset = q.starts;
     if (q.starts) first_h(q.seg);
-    else if (!SUM && chunk > 0) ld_pair<Q>(h, p.sums + ((int64_t)line * (p.nchunk - 1) + chunk - 1) * dnp + own_p, NP, Q, true, on);
+    else if (!SUM && chunk > 0) ld_across<Q>(h, p.sums + ((int64_t)line * (p.nchunk - 1) + chunk - 1) * dnp + own_p, NP, Q, true, on);
     else zero_h();
 
     const T *src[3] = {(const T *)p.x + line * p.x_sb, (const T *)p.dt + line * p.dt_sb, (const T *)p.z + line * p.z_sb};
     const int64_t str[3] = {p.x_st, p.dt_st, p.z_st};
-    const int na = SUM || !gate ? 2 : 3;
     auto fetch = [&](int s, int b) {  // the stage that begins at token s into buffer b
         if (s < t1) {
 #pragma unroll
             for (int a = 0; a < NA; ++a)
-                if (a < na)
+                if (a < 2 || gate)
                     ssm_fetch_tile<T, CH, TS, kThreads>(reinterpret_cast<T *>(smem + b * kBuf + a * kTile),
                                                         src[a] + s * str[a], str[a], t1 - s, c0, p.D, vec);
         }
@@ -97,112 +122,59 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const SsmParams p, i
         fetch(t0 + TS, 1);
         fetch_bc(t0);
     }
-    float2 dsum = make_float2(0.f, 0.f);
-    int buf = 0, flip = 0;
-    for (int s = t0; s < t1; s += TS) {
-        float *bc = bcs + flip * kBc;
+    f32x2 dsum = pack2(0.f, 0.f);
+    int buf = 0;
+    for (int s = t0; s < t1; s += TS, buf ^= 1) {
+        float *bc = bcs + buf * kBc;
         nbc.stage(bc);
         if (s + TS < t1) fetch_bc(s + TS);
         cp_async_wait<1>();
         __syncthreads();
-        fetch(s + 2 * TS, buf == 0 ? 2 : buf - 1);
         const int m = min(t1 - s, TS);
         const T *xs = reinterpret_cast<const T *>(smem + buf * kBuf) + ch;
-        T *os = (T *)p.out + line * p.o_sb + s * p.o_st + d;
         auto pair_at = [&](int i, int a) {  // the pair's x, dt or z
             float f[2];
             ld_row_f<T, 2, true>(f, xs + (a * TS + i) * CH, 2);
             return make_float2(f[0], f[1]);
         };
-        // The three parts of K tokens from token i on. Their chains are long
-        // (softplus alone some 150 cycles), so the loop below forms the next
-        // tokens' delta while it runs the states of these.
-        auto prep = [&](auto &dl, auto &u, int i) {
-#pragma unroll
-            for (int k = 0; k < (int)(sizeof(dl) / sizeof(float2)); ++k) {
-                const float2 v = pair_at(i + k, 1), x = pair_at(i + k, 0);
-                dl[k] = make_float2(v.x + bias.x, v.y + bias.y);
-                if (softplus) dl[k] = softplus2(dl[k]);
-                u[k] = make_float2(dl[k].x * x.x, dl[k].y * x.y);
-            }
-        };
-        auto states = [&](float2 &y, float2 dl, float2 u, int i) {
+#pragma unroll 4
+        for (int t = 0; t < TS; ++t) {
+            const float2 v = pair_at(t, 1), x = pair_at(t, 0);
+            float2 dl = make_float2(v.x + bias.x, v.y + bias.y);
+            if (softplus) dl = softplus2(dl);
+            slot[t * kThreads] = make_float4(dl.x, dl.y, dl.x * x.x, dl.y * x.y);
+        }
+        auto states = [&](int i) {
+            const ulonglong2 du = *reinterpret_cast<const ulonglong2 *>(slot + i * kThreads);
             const float4 *b4 = reinterpret_cast<const float4 *>(bc + i * 2 * NP + n0);
-            const f32x2 d2[2] = {pack2(dl.x, dl.x), pack2(dl.y, dl.y)}, u2[2] = {pack2(u.x, u.x), pack2(u.y, u.y)};
-            f32x2 ya[2], yb[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) ya[k] = yb[k] = pack2(0.f, 0.f);
+            f32x2 ya, yb;
 #pragma unroll
             for (int j = 0; j < Q / 4; ++j) {
                 const float4 b = b4[j];
+                const float bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    f32x2 *hk = h[k] + 2 * j;
-                    hk[0] = fma2(ex2_2(mul2(d2[k], a2[k][2 * j])), hk[0], mul2(u2[k], pack2(b.x, b.y)));
-                    hk[1] = fma2(ex2_2(mul2(d2[k], a2[k][2 * j + 1])), hk[1], mul2(u2[k], pack2(b.z, b.w)));
-                }
+                for (int k = 0; k < 4; ++k)
+                    h[4 * j + k] = fma2(ex2_2(mul2(du.x, a2[4 * j + k])), h[4 * j + k], mul2(du.y, pack2(bv[k], bv[k])));
                 if (!SUM) {
                     const float4 c = b4[NP / 4 + j];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        ya[k] = fma2(h[k][2 * j], pack2(c.x, c.y), ya[k]);
-                        yb[k] = fma2(h[k][2 * j + 1], pack2(c.z, c.w), yb[k]);
-                    }
+                    ya = j ? fma2(h[4 * j], pack2(c.x, c.x), ya) : mul2(h[0], pack2(c.x, c.x));
+                    yb = j ? fma2(h[4 * j + 1], pack2(c.y, c.y), yb) : mul2(h[1], pack2(c.y, c.y));
+                    ya = fma2(h[4 * j + 2], pack2(c.z, c.z), ya);
+                    yb = fma2(h[4 * j + 3], pack2(c.w, c.w), yb);
                 }
             }
-            if (SUM) {
-                dsum.x += dl.x, dsum.y += dl.y;
-            } else {
-                const float2 r0 = unpack2(add2(ya[0], yb[0])), r1 = unpack2(add2(ya[1], yb[1]));
-                y = make_float2(r0.x + r0.y, r1.x + r1.y);
-            }
+            if (SUM) dsum = add2(dsum, du.x);
+            else *reinterpret_cast<f32x2 *>(slot + i * kThreads) = add2(ya, yb);
         };
-        auto finish = [&](auto &y, int i) {
-#pragma unroll
-            for (int k = 0; k < (int)(sizeof(y) / sizeof(float2)); ++k) {
-#pragma unroll
-                for (int o = LN / 2; o > 0; o >>= 1) {
-                    y[k].x += __shfl_xor_sync(0xffffffffu, y[k].x, o);
-                    y[k].y += __shfl_xor_sync(0xffffffffu, y[k].y, o);
-                }
-                const float2 x = pair_at(i + k, 0);
-                float f[2] = {fmaf(dv.x, x.x, y[k].x), fmaf(dv.y, x.y, y[k].y)};
-                if (gate) {
-                    const float2 z = pair_at(i + k, 2), g = sigmoid2(z);
-                    f[0] *= z.x * g.x, f[1] *= z.y * g.y;
-                }
-                if (d < p.D && ln == 0) {
-                    if (vec) st_row_f<T, 2, true>(os + (i + k) * p.o_st, f, 2);
-                    else st_row_f<T, 2, false>(os + (i + k) * p.o_st, f, p.D - d);
-                }
-            }
-        };
-        int t = 0;
-        while (t < m) {
-            const int run = min(m, q.end - 1 - s);
-            if (t + K <= run) {
-                float2 dl[K], u[K], y[K];
-                prep(dl, u, t);
+        if (m == TS && q.end > s + TS) {  // no sequence ends in the stage
+#pragma unroll 4
+            for (int t = 0; t < TS; ++t) states(t);
+        } else {
 #pragma unroll 1
-                for (; t + K <= run; t += K) {
-                    float2 dn[K], un[K];
-                    prep(dn, un, min(t + K, TS - K));  // past the run's end: not used
-#pragma unroll
-                    for (int k = 0; k < K; ++k) states(y[k], dl[k], u[k], t + k);
-                    if (!SUM) finish(y, t);
-#pragma unroll
-                    for (int k = 0; k < K; ++k) dl[k] = dn[k], u[k] = un[k];
-                }
-            }
-            // one by one up to the stage's or the sequence's end
-#pragma unroll 1
-            for (const int stop = min(m, t + K); t < stop; ++t) {
-                float2 dl[1], u[1], y[1];
-                prep(dl, u, t);
-                states(y[0], dl[0], u[0], t);
-                if (!SUM) finish(y, t);
+            for (int t = 0; t < m; ++t) {
+                states(t);
                 if (s + t + 1 == q.end) {
-                    if (!SUM && p.h_final) st_pair<Q>(p.h_final + q.seg * hrow + own, h, p.N, nn, p.n_wide, on);
+                    if (!SUM && p.h_final) st_across<Q>(p.h_final + q.seg * hrow + own, h, p.N, nn, p.n_wide, on);
                     if (q.end < p.T) {
                         ssm_next(q, p.cu, p.n_seq, p.T, q.end);
                         first_h(q.seg);
@@ -211,20 +183,44 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const SsmParams p, i
                 }
             }
         }
-        buf = buf == 2 ? 0 : buf + 1, flip ^= 1;
+        if (!SUM) {
+            T *os = (T *)p.out + line * p.o_sb + s * p.o_st + d;
+#pragma unroll 4
+            for (int t = 0; t < TS; ++t, os += p.o_st) {
+                float2 y = *reinterpret_cast<const float2 *>(slot + t * kThreads);
+#pragma unroll
+                for (int o = LN / 2; o > 0; o >>= 1) {
+                    y.x += __shfl_xor_sync(0xffffffffu, y.x, o);
+                    y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
+                }
+                const float2 x = pair_at(t, 0);
+                float f[2] = {fmaf(dv.x, x.x, y.x), fmaf(dv.y, x.y, y.y)};
+                if (gate) {
+                    const float2 z = pair_at(t, 2), g = sigmoid2(z);
+                    f[0] *= z.x * g.x, f[1] *= z.y * g.y;
+                }
+                if (out && t < m) {
+                    if (vec) st_row_f<T, 2, true>(os, f, 2);
+                    else st_row_f<T, 2, false>(os, f, p.D - d);
+                }
+            }
+        }
+        __syncthreads();  // the buffer has been read
+        fetch(s + 2 * TS, buf);
     }
     if (SUM) {
-        st_pair<Q>(p.sums + ((int64_t)line * nch + chunk) * dnp + own_p, h, NP, Q, true, on);
+        st_across<Q>(p.sums + ((int64_t)line * nch + chunk) * dnp + own_p, h, NP, Q, true, on);
         // a chunk in which a sequence begins passes nothing on: marked by NaN
+        const float2 ds = unpack2(dsum);
         float *o = p.dsum + ((int64_t)line * nch + chunk) * p.D + d;
-        if (ln == 0 && d < p.D) o[0] = reset ? __int_as_float(0x7fffffff) : dsum.x;
-        if (ln == 0 && d + 1 < p.D) o[1] = reset ? __int_as_float(0x7fffffff) : dsum.y;
+        if (ln == 0 && d < p.D) o[0] = reset ? __int_as_float(0x7fffffff) : ds.x;
+        if (ln == 0 && d + 1 < p.D) o[1] = reset ? __int_as_float(0x7fffffff) : ds.y;
     } else if (p.h_final && chunk == 0 && (p.cu || p.T == 0)) {
         // sequences without a token pass their state on
         for (int s = 0; s < p.n_seq; ++s) {
             if (p.cu ? p.cu[s + 1] > p.cu[s] : s != line) continue;
             first_h(s);
-            st_pair<Q>(p.h_final + s * hrow + own, h, p.N, nn, p.n_wide, on);
+            st_across<Q>(p.h_final + s * hrow + own, h, p.N, nn, p.n_wide, on);
         }
     }
 }
@@ -240,11 +236,18 @@ __global__ void __launch_bounds__(256) ssm_chain_kernel(const SsmParams p, int n
     float *s = p.sums + line * nch * dnp + i % dnp;
     const float *q = p.dsum + (int64_t)line * nch * p.D + d;
     float h = 0.f;
-#pragma unroll 4
-    for (int c = 0; c < nch; ++c) {
-        const float v = q[(int64_t)c * p.D], e = s[c * dnp];
-        h = isnan(v) ? e : fmaf(ex2f(a * v), h, e);
-        s[c * dnp] = h;
+    for (int c = 0; c < nch; c += 8) {
+        float v[8], e[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const bool in = c + k < nch;
+            v[k] = in ? q[(int64_t)(c + k) * p.D] : 0.f, e[k] = in ? s[(c + k) * dnp] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            h = isnan(v[k]) ? e[k] : fmaf(ex2f(a * v[k]), h, e[k]);
+            if (c + k < nch) s[(c + k) * dnp] = h;
+        }
     }
 }
 
@@ -288,7 +291,7 @@ __global__ void __launch_bounds__(128) ssm_step_kernel(const SsmStepParams p) {
 template <typename T, int Q, int LN, bool SUM>
 cudaError_t scan_t(const SsmParams &p, cudaStream_t st) {
     constexpr int CH = 2 * kThreads / LN;
-    constexpr int smem = 3 * (SUM ? 2 : 3) * kStage * CH * (int)sizeof(T) + 2 * kStage * 2 * Q * LN * 4;
+    constexpr int smem = 2 * (SUM ? 2 : 3) * kStage * CH * (int)sizeof(T) + kStage * kThreads * 16 + 2 * kStage * 2 * Q * LN * 4;
     const bool usual = p.vec && p.softplus && (SUM || p.z);
     auto *k = usual ? ssm_scan_kernel<T, Q, LN, SUM, true> : ssm_scan_kernel<T, Q, LN, SUM, false>;
     if (smem > 48 * 1024) {
@@ -317,10 +320,12 @@ cudaError_t by_lanes(int N, F &&f) {
 void ssm_split(int lines, int T, int D, int N, int *nchunk, int *clen) {
     const int ch = 2 * kThreads / ssm_lanes(N);
     const int64_t ctas = (int64_t)lines * ((D + ch - 1) / ch);
-    // four CTAs a SM, in chunks of at least 64 tokens; whole lines from two a SM on
+    // Six CTAs a SM (three warps a scheduler), in chunks of at least 64 tokens;
+    // whole lines from two a SM on, where the sums would cost as much as they
+    // hide.
     int64_t n = 1;
     if (ctas < 304) {
-        n = 608 / ctas;
+        n = 912 / ctas;
         if (n > (T + 63) / 64) n = (T + 63) / 64;
         if (n < 1) n = 1;
     }

@@ -27,16 +27,22 @@ namespace {
 
 constexpr int kNT = 64;      // threads of every CTA here
 constexpr int kGroup = kSsmGroup;
-constexpr int kStage = 16;   // tokens a stage of the sums
+constexpr int kStage = 8;    // tokens a stage of the sums
 
 // ------------------------------------------------------------ sums ----------
-template <typename T, int Q, int LN, bool USUAL>
-__global__ void __launch_bounds__(kNT) ssm_bwd_sum_kernel(const SsmParams p, int ntile) {
-    constexpr int CH = 2 * kNT / LN, NP = Q * LN, TS = kStage, NA = 4;  // x, dt, z, dout
-    constexpr int kTile = TS * CH * (int)sizeof(T), kBuf = NA * kTile, kBc = TS * 2 * NP;
+// A lane has eight states of two neighbouring channels: their state, the
+// run's gradient and the decay since the run's start. What a token's channels
+// need once is formed by the warp for a stage of tokens and handed over in
+// shared memory, as in the scan.
+template <typename T, int LN, bool USUAL>
+__global__ void __launch_bounds__(kNT, 8) ssm_bwd_sum_kernel(const SsmParams p, int ntile) {
+    constexpr int Q = 8, CH = 2 * kNT / LN, NP = Q * LN, TS = kStage, NA = 4;  // x, dt, z, dout
+    constexpr int kTile = TS * CH * (int)sizeof(T), kBuf = NA * kTile, kBc = TS * 2 * NP, PW = 32 / LN;
     extern __shared__ __align__(16) unsigned char smem[];
-    float *bcs = reinterpret_cast<float *>(smem + 3 * kBuf);  // [2][TS][2][NP]
-    const int tid = threadIdx.x, ch = tid / LN * 2, ln = tid % LN;
+    float4 *dus = reinterpret_cast<float4 *>(smem + 2 * kBuf);            // [TS][CH / 2] delta, delta x
+    float2 *dys = reinterpret_cast<float2 *>(dus + TS * CH / 2);          // [TS][CH / 2] dy
+    float *bcs = reinterpret_cast<float *>(dys + TS * CH / 2);            // [2][TS][2][NP]
+    const int tid = threadIdx.x, lane = tid & 31, pr = tid / LN, ch = 2 * pr, ln = tid % LN;
     const int tile = blockIdx.x % ntile, item = blockIdx.x / ntile;
     const int line = item / p.nrun, run = item - line * p.nrun;
     if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
@@ -56,8 +62,6 @@ __global__ void __launch_bounds__(kNT) ssm_bwd_sum_kernel(const SsmParams p, int
             a2[k][j] = mul2(a2[k][j], pack2(kLog2e, kLog2e));
             g[k][j] = pack2(0.f, 0.f), w[k][j] = pack2(1.f, 1.f);
         }
-    const float2 bias = make_float2(p.dt_bias && d < p.D ? p.dt_bias[d] : 0.f,
-                                    p.dt_bias && d + 1 < p.D ? p.dt_bias[d + 1] : 0.f);
     auto first_h = [&](int seg, bool zero) {
         if (p.h0 && !zero) {
             ld_pair<Q>(h, p.h0 + seg * hrow + own, p.N, nn, p.n_wide, on);
@@ -93,34 +97,45 @@ __global__ void __launch_bounds__(kNT) ssm_bwd_sum_kernel(const SsmParams p, int
     fetch_bc(t0);
     float *gs = p.gs + ((int64_t)line * p.nrun + run) * dnp + own_p;
     float2 dsum = make_float2(0.f, 0.f);
-    int buf = 0, flip = 0;
-    for (int s = t0; s < t1; s += TS) {
-        float *bc = bcs + flip * kBc;
+    int buf = 0;
+    for (int s = t0; s < t1; s += TS, buf ^= 1) {
+        float *bc = bcs + buf * kBc;
         nbc.stage(bc);
         if (s + TS < t1) fetch_bc(s + TS);
         cp_async_wait<1>();
         __syncthreads();
-        fetch(s + 2 * TS, buf == 0 ? 2 : buf - 1);
         const int m = min(t1 - s, TS);
-        const T *xs = reinterpret_cast<const T *>(smem + buf * kBuf) + ch;
-        auto pair_at = [&](int i, int a) {
-            float f[2];
-            ld_row_f<T, 2, true>(f, xs + (a * TS + i) * CH, 2);
-            return make_float2(f[0], f[1]);
-        };
-#pragma unroll 1
-        for (int t = 0; t < m; ++t) {
-            const float2 x = pair_at(t, 0), v = pair_at(t, 1);
-            float2 dl = make_float2(v.x + bias.x, v.y + bias.y), dy = pair_at(t, 3);
+        // this warp's pairs of the stage
+#pragma unroll 2
+        for (int e = lane; e < TS * PW; e += 32) {
+            const int t = e / PW, k = tid / 32 * PW + e % PW, c = c0 + 2 * k;
+            const T *xs = reinterpret_cast<const T *>(smem + buf * kBuf) + t * CH + 2 * k;
+            float x[2], v[2], o[2];
+            ld_row_f<T, 2, true>(x, xs, 2);
+            ld_row_f<T, 2, true>(v, xs + TS * CH, 2);
+            ld_row_f<T, 2, true>(o, xs + 3 * TS * CH, 2);
+            float2 dl = make_float2(v[0], v[1]);
+            if (p.dt_bias) {
+                if (c < p.D) dl.x += p.dt_bias[c];
+                if (c + 1 < p.D) dl.y += p.dt_bias[c + 1];
+            }
             if (softplus) dl = softplus2(dl);
             if (gate) {
-                const float2 z = pair_at(t, 2), sg = sigmoid2(z);
-                dy.x *= z.x * sg.x, dy.y *= z.y * sg.y;
+                float z[2];
+                ld_row_f<T, 2, true>(z, xs + 2 * TS * CH, 2);
+                const float2 sg = sigmoid2(make_float2(z[0], z[1]));
+                o[0] *= z[0] * sg.x, o[1] *= z[1] * sg.y;
             }
-            dsum.x += dl.x, dsum.y += dl.y;
+            dus[t * (CH / 2) + k] = make_float4(dl.x, dl.y, dl.x * x[0], dl.y * x[1]);
+            dys[t * (CH / 2) + k] = make_float2(o[0], o[1]);
+        }
+        __syncwarp();
+        auto token = [&](int t) {
+            const float4 du = dus[t * (CH / 2) + pr];
+            const float2 dy = dys[t * (CH / 2) + pr];
+            dsum.x += du.x, dsum.y += du.y;
             const float4 *b4 = reinterpret_cast<const float4 *>(bc + t * 2 * NP + n0);
-            const f32x2 d2[2] = {pack2(dl.x, dl.x), pack2(dl.y, dl.y)};
-            const f32x2 u2[2] = {pack2(dl.x * x.x, dl.x * x.x), pack2(dl.y * x.y, dl.y * x.y)};
+            const f32x2 d2[2] = {pack2(du.x, du.x), pack2(du.y, du.y)}, u2[2] = {pack2(du.z, du.z), pack2(du.w, du.w)};
             const f32x2 y2[2] = {pack2(dy.x, dy.x), pack2(dy.y, dy.y)};
 #pragma unroll
             for (int j = 0; j < Q / 4; ++j) {
@@ -133,51 +148,57 @@ __global__ void __launch_bounds__(kNT) ssm_bwd_sum_kernel(const SsmParams p, int
                         const int l = 2 * j + i;
                         const f32x2 a = ex2_2(mul2(d2[k], a2[k][l]));
                         h[k][l] = fma2(a, h[k][l], mul2(u2[k], b2[i]));
-                        // g takes this token's share before its own decay: g is of the
-                        // state after the token, the run's start lies before it
+                        // the run's start lies before this token's decay
                         w[k][l] = mul2(w[k][l], a);
                         g[k][l] = fma2(w[k][l], mul2(c2[i], y2[k]), g[k][l]);
                     }
             }
-            const int tt = s + t + 1;
-            const bool last = tt == q.end, cut = tt == t1 || tt % kGroup == 0;
-            if (cut) {  // the group's state, and zero for the next
-                const int64_t at = (int64_t)line * p.ngroup + (tt - 1) / kGroup;
-                st_pair<Q>(p.sums + at * dnp + own_p, h, NP, Q, true, on);
-                float *o = p.dsum + at * p.D + d;
-                if (ln == 0 && d < p.D) o[0] = reset ? __int_as_float(0x7fffffff) : dsum.x;
-                if (ln == 0 && d + 1 < p.D) o[1] = reset ? __int_as_float(0x7fffffff) : dsum.y;
-                if (ln == 0) {
-                    float *r = p.gsum + at * p.D + d;
-                    if (d < p.D) r[0] = dsum.x;
-                    if (d + 1 < p.D) r[1] = dsum.y;
-                }
-                dsum = make_float2(0.f, 0.f);
-                reset = false;
-                first_h(0, true);
-            }
-            if (last) {
-                if (alive) {
-                    if (p.dh_final) {
-                        f32x2 e[2][Q / 2];
-                        ld_pair<Q>(e, p.dh_final + q.seg * hrow + own, p.N, nn, p.n_wide, on);
+        };
+        // a group's state, and zero for the next
+        auto cut = [&](int last) {
+            const int64_t at = (int64_t)line * p.ngroup + last / kGroup;
+            st_pair<Q>(p.sums + at * dnp + own_p, h, NP, Q, true, on);
+            float *o = p.dsum + at * p.D + d, *r = p.gsum + at * p.D + d;
+            if (ln == 0 && d < p.D) o[0] = reset ? __int_as_float(0x7fffffff) : dsum.x, r[0] = dsum.x;
+            if (ln == 0 && d + 1 < p.D) o[1] = reset ? __int_as_float(0x7fffffff) : dsum.y, r[1] = dsum.y;
+            dsum = make_float2(0.f, 0.f);
+            reset = false;
+            first_h(0, true);
+        };
+        if (m == TS && q.end > s + TS) {  // no sequence ends in the stage; groups end with stages
+#pragma unroll 2
+            for (int t = 0; t < TS; ++t) token(t);
+            if ((s + TS) % kGroup == 0 || s + TS == t1) cut(s + TS - 1);
+        } else {
+#pragma unroll 1
+            for (int t = 0; t < m; ++t) {
+                token(t);
+                const int tt = s + t + 1;
+                if (tt == t1 || tt % kGroup == 0) cut(tt - 1);
+                if (tt == q.end) {
+                    if (alive) {
+                        if (p.dh_final) {
+                            f32x2 e[2][Q / 2];
+                            ld_pair<Q>(e, p.dh_final + q.seg * hrow + own, p.N, nn, p.n_wide, on);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
+                            for (int k = 0; k < 2; ++k)
 #pragma unroll
-                            for (int j = 0; j < Q / 2; ++j) g[k][j] = fma2(w[k][j], e[k][j], g[k][j]);
+                                for (int j = 0; j < Q / 2; ++j) g[k][j] = fma2(w[k][j], e[k][j], g[k][j]);
+                        }
+                        // what follows belongs to other sequences
+                        st_pair<Q>(gs, g, NP, Q, true, on);
+                        alive = false;
                     }
-                    // what follows belongs to other sequences
-                    st_pair<Q>(gs, g, NP, Q, true, on);
-                    alive = false;
-                }
-                if (tt < p.T) {
-                    ssm_next(q, p.cu, p.n_seq, p.T, tt);
-                    first_h(q.seg, false);
-                    reset = true;
+                    if (tt < p.T) {
+                        ssm_next(q, p.cu, p.n_seq, p.T, tt);
+                        first_h(q.seg, false);
+                        reset = true;
+                    }
                 }
             }
         }
-        buf = buf == 2 ? 0 : buf + 1, flip ^= 1;
+        __syncthreads();  // the buffer has been read
+        fetch(s + 2 * TS, buf);
     }
     if (alive) st_pair<Q>(gs, g, NP, Q, true, on);
     if (!alive && ln == 0) {  // nothing crosses the run: marked by NaN
@@ -200,11 +221,18 @@ __global__ void __launch_bounds__(256) ssm_bwd_chain_kernel(const SsmParams p, i
         float *s = p.sums + (int64_t)line * p.ngroup * dnp + i % dnp;
         const float *q = p.dsum + (int64_t)line * p.ngroup * p.D + d;
         float h = 0.f;
-#pragma unroll 8
-        for (int c = 0; c + 1 < p.ngroup; ++c) {
-            const float v = q[(int64_t)c * p.D], e = s[c * dnp];
-            h = isnan(v) ? e : fmaf(ex2f(a * v), h, e);
-            s[c * dnp] = h;
+        for (int c = 0; c + 1 < p.ngroup; c += 8) {  // (loads in batches: each store would hold the next one back)
+            float v[8], e[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const bool in = c + k + 1 < p.ngroup;
+                v[k] = in ? q[(int64_t)(c + k) * p.D] : 0.f, e[k] = in ? s[(c + k) * dnp] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                h = isnan(v[k]) ? e[k] : fmaf(ex2f(a * v[k]), h, e[k]);
+                if (c + k + 1 < p.ngroup) s[(c + k) * dnp] = h;
+            }
         }
     } else {
         const int gpr = p.rlen / kGroup;
@@ -513,7 +541,7 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
                             if constexpr (CL == 4) {
                                 atomicAdd(po, acc[0]), atomicAdd(po + 1, acc[2]), atomicAdd(po + 2, acc[1]), atomicAdd(po + 3, acc[3]);
                             } else {
-                                const bool u2 = lane & 4, u3 = lane & 8;
+                                const bool u2 = lane & 4;
                                 const float g0 = u2 ? acc[0] : acc[2], g1 = u2 ? acc[1] : acc[3];
                                 float k0 = u2 ? acc[2] : acc[0], k1 = u2 ? acc[3] : acc[1];
                                 k0 += __shfl_xor_sync(0xffffffffu, g0, 4);
@@ -521,6 +549,7 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
                                 if constexpr (CL == 8) {
                                     atomicAdd(po + (u2 ? 1 : 0), k0), atomicAdd(po + (u2 ? 3 : 2), k1);
                                 } else {
+                                    const bool u3 = lane & 8;
                                     const float g2 = u3 ? k0 : k1;
                                     float k2 = u3 ? k1 : k0;
                                     k2 += __shfl_xor_sync(0xffffffffu, g2, 8);
@@ -595,14 +624,16 @@ __global__ void __launch_bounds__(256) ssm_bwd_empty_kernel(const SsmParams p) {
         if (p.cu ? p.cu[s + 1] <= p.cu[s] : p.T == 0) p.dh0[s * dn + i] = p.dh_final ? p.dh_final[s * dn + i] : 0.f;
 }
 
-template <typename T, int Q, int LN>
+template <typename T, int LN>
 cudaError_t sum_t(const SsmParams &p, cudaStream_t st) {
     constexpr int CH = 2 * kNT / LN;
-    constexpr int smem = 3 * 4 * kStage * CH * (int)sizeof(T) + 2 * kStage * 2 * Q * LN * 4;
+    constexpr int smem = 2 * 4 * kStage * CH * (int)sizeof(T) + kStage * CH / 2 * 24 + 2 * kStage * 2 * 8 * LN * 4;
     const bool usual = p.vec && p.softplus && p.z;
-    auto *k = usual ? ssm_bwd_sum_kernel<T, Q, LN, true> : ssm_bwd_sum_kernel<T, Q, LN, false>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    auto *k = usual ? ssm_bwd_sum_kernel<T, LN, true> : ssm_bwd_sum_kernel<T, LN, false>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
     const int ntile = (p.D + CH - 1) / CH;
     const int64_t items = (int64_t)(p.cu ? 1 : p.B) * p.nrun;
     if (items * ntile > INT32_MAX) return cudaErrorInvalidValue;
@@ -641,9 +672,14 @@ int ssm_bwd_run(int lines, int T, int D, int N) {
 }
 
 cudaError_t launch_ssm_bwd_sum(const SsmParams &p, cudaStream_t st) {
-    return ssm_by_states(p.N, [&](auto q, auto ln) {
-        return p.bf16 ? sum_t<__nv_bfloat16, q(), ln()>(p, st) : sum_t<float, q(), ln()>(p, st);
-    });
+    auto f = [&](auto ln) { return p.bf16 ? sum_t<__nv_bfloat16, ln()>(p, st) : sum_t<float, ln()>(p, st); };
+    switch (ssm_np(p.N) / 8) {
+        case 1: return f(std::integral_constant<int, 1>());
+        case 2: return f(std::integral_constant<int, 2>());
+        case 4: return f(std::integral_constant<int, 4>());
+        case 8: return f(std::integral_constant<int, 8>());
+    }
+    return f(std::integral_constant<int, 16>());
 }
 cudaError_t launch_ssm_bwd_chain(const SsmParams &p, cudaStream_t st) {
     const int np = ssm_np(p.N);
