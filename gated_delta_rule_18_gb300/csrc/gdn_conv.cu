@@ -10,19 +10,17 @@
 // All are bound by HBM (2 W + 5 operations per 4 bytes). A thread keeps a few
 // channels (one vector access a token), walks a run of tokens and holds the
 // window in registers, so each input is read from HBM once; the W - 1 tokens
-// before its run come from L1 or L2. Packed batches need no second form: a
+// before its run come from L1 or L2. The next four tokens' loads are under
+// way while four are computed, in packed pairs of channels. Packed batches need no second form: a
 // thread finds the sequence of its first token by bisection and swaps the
 // window for the next sequence's carried one where that begins.
-#include "gdn_layer.cuh"
+#include "gdn_ssm.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kTokL = 16;     // tokens a thread, forward
 constexpr int kTokLBwd = 32;  // tokens a thread, gradient
 constexpr int kConvY = 4, kConvYBwd = 8;
-
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
 // The sequence of a token: the last s with cu[s] <= t, its bounds clamped so
 // that a malformed cu cannot send an access out of range.
@@ -53,39 +51,83 @@ __device__ __forceinline__ void next_seq(Seq &q, const int32_t *cu, int n_seq, i
     q.s1 = max(__ldg(cu + q.seg + 1), t + 1);
 }
 
+// the taps and biases of NC channels, in pairs of channels
 template <typename T, int NC, int W, bool VEC>
-__device__ __forceinline__ void load_taps(float (&w)[W][NC], const float *weight, int c, int n) {
+__device__ __forceinline__ void load_taps(f32x2 (&w)[W][NC / 2], f32x2 (&bias)[NC / 2], const float *weight,
+                                          const float *b, int c, int n) {
+    float f[NC * W], g[NC];
     if constexpr (VEC) {
         uint32_t u[NC * W];
         ld_words(u, weight + (int64_t)c * W);
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[j][i] = __uint_as_float(u[i * W + j]);
+        for (int i = 0; i < NC * W; ++i) f[i] = __uint_as_float(u[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[j][i] = i < n ? weight[(int64_t)(c + i) * W + j] : 0.f;
+        for (int i = 0; i < NC * W; ++i) f[i] = i / W < n ? weight[(int64_t)c * W + i] : 0.f;
     }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) g[i] = 0.f;
+    if (b) ld_row_f<float, NC, VEC>(g, b + c, n);
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i) {
+        bias[i] = pack2(g[2 * i], g[2 * i + 1]);
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][i] = pack2(f[2 * i * W + j], f[(2 * i + 1) * W + j]);
+    }
+}
+template <typename T, int NC>
+__device__ __forceinline__ void words_to_pairs(f32x2 (&v)[NC / 2], const uint32_t (&w)[RowVec<T, NC>::kWords]) {
+    float f[NC];
+    words_to_f<T, NC>(f, w);
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i) v[i] = pack2(f[2 * i], f[2 * i + 1]);
+}
+template <typename T, int NC, bool VEC>
+__device__ __forceinline__ void st_pairs(T *p, const f32x2 (&v)[NC / 2], int n) {
+    float f[NC];
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i) {
+        const float2 x = unpack2(v[i]);
+        f[2 * i] = x.x, f[2 * i + 1] = x.y;
+    }
+    st_row_f<T, NC, VEC>(p, f, n);
 }
 
 // win[k] = the input k + 1 tokens before t
 template <typename T, int NC, int W, bool VEC>
-__device__ __forceinline__ void load_window(uint32_t (&win)[W - 1][RowVec<T, NC>::kWords], const ConvParams &p,
-                                            const T *x, int t, const Seq &q, int c, int n) {
+__device__ __forceinline__ void load_window(f32x2 (&win)[W - 1][NC / 2], const ConvParams &p, const T *x, int t,
+                                            const Seq &q, int c, int n) {
 #pragma unroll
     for (int k = 1; k < W; ++k) {
         const int back = t - k;
+        uint32_t v[RowVec<T, NC>::kWords] = {};
         if (back >= q.s0) {
-            ld_row<T, NC, VEC>(win[k - 1], x + (int64_t)back * p.x_st, n);
+            ld_row<T, NC, VEC>(v, x + (int64_t)back * p.x_st, n);
         } else if (p.init) {
             const int row = W - 1 - k + (t - q.s0);
-            ld_row<T, NC, VEC>(win[k - 1], (const T *)p.init + ((int64_t)q.seg * (W - 1) + row) * p.D + c, n);
-        } else {
-#pragma unroll
-            for (int i = 0; i < RowVec<T, NC>::kWords; ++i) win[k - 1][i] = 0u;
+            ld_row<T, NC, VEC>(v, (const T *)p.init + ((int64_t)q.seg * (W - 1) + row) * p.D + c, n);
         }
+        words_to_pairs<T, NC>(win[k - 1], v);
+    }
+}
+template <int NC, int W>
+__device__ __forceinline__ void push(f32x2 (&win)[W - 1][NC / 2], const f32x2 (&v)[NC / 2]) {
+#pragma unroll
+    for (int k = W - 2; k > 0; --k)
+#pragma unroll
+        for (int i = 0; i < NC / 2; ++i) win[k][i] = win[k - 1][i];
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i) win[0][i] = v[i];
+}
+// the convolution at the token whose input is v
+template <int NC, int W>
+__device__ __forceinline__ void convolve(f32x2 (&a)[NC / 2], const f32x2 (&w)[W][NC / 2], const f32x2 (&bias)[NC / 2],
+                                         const f32x2 (&win)[W - 1][NC / 2], const f32x2 (&v)[NC / 2]) {
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i) {
+        a[i] = fma2(w[W - 1][i], v[i], bias[i]);
+#pragma unroll
+        for (int k = 1; k < W; ++k) a[i] = fma2(w[W - 1 - k][i], win[k - 1][i], a[i]);
     }
 }
 
@@ -99,7 +141,7 @@ __device__ __forceinline__ void check_cu(const int32_t *cu, int n_seq, int T, in
 }
 
 template <typename T, int NC, int W, bool VEC>
-__global__ void __launch_bounds__(32 * kConvY) conv_kernel(const ConvParams p, int nblk) {
+__global__ void __launch_bounds__(32 * kConvY) conv_kernel(const ConvParams p, int nblk, int run) {
     constexpr int NW = RowVec<T, NC>::kWords, U = 4;
     const int c = (blockIdx.y * 32 + threadIdx.x) * NC, n = p.D - c, b = blockIdx.z;
     if (blockIdx.x == nblk) {  // checks, and the windows of empty sequences
@@ -116,24 +158,29 @@ __global__ void __launch_bounds__(32 * kConvY) conv_kernel(const ConvParams p, i
         }
         return;
     }
-    const int64_t first = ((int64_t)blockIdx.x * kConvY + threadIdx.y) * kTokL;
+    const int64_t first = ((int64_t)blockIdx.x * kConvY + threadIdx.y) * run;
     if (c >= p.D || first >= p.T) return;
-    const int t0 = (int)first, t1 = min(p.T - t0, kTokL) + t0;
+    const int t0 = (int)first, t1 = min(p.T - t0, run) + t0;
     const T *x = (const T *)p.x + b * p.x_sb + c;
     T *out = (T *)p.out + b * p.o_sb + c;
-    float w[W][NC], bias[NC];
-    load_taps<T, NC, W, VEC>(w, p.weight, c, n);
-#pragma unroll
-    for (int i = 0; i < NC; ++i) bias[i] = 0.f;
-    if (p.bias) ld_row_f<float, NC, VEC>(bias, p.bias + c, n);
+    f32x2 w[W][NC / 2], bias[NC / 2], win[W - 1][NC / 2];
+    load_taps<T, NC, W, VEC>(w, bias, p.weight, p.bias, c, n);
     Seq q = find_seq(p.cu, p.n_seq, p.T, b, t0);
-    uint32_t win[W - 1][NW];
     load_window<T, NC, W, VEC>(win, p, x, t0, q, c, n);
+    uint32_t next[U][NW];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t + u < t1) ld_row<T, NC, VEC>(next[u], x + (int64_t)(t + u) * p.x_st, n);
+    };
+    fetch(t0);
     for (int t = t0; t < t1; t += U) {
         uint32_t raw[U][NW];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (t + u < t1) ld_row<T, NC, VEC>(raw[u], x + (int64_t)(t + u) * p.x_st, n);
+#pragma unroll
+            for (int i = 0; i < NW; ++i) raw[u][i] = next[u][i];
+        fetch(t + U);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (t + u >= t1) break;
@@ -141,70 +188,43 @@ __global__ void __launch_bounds__(32 * kConvY) conv_kernel(const ConvParams p, i
                 next_seq(q, p.cu, p.n_seq, t + u);
                 load_window<T, NC, W, VEC>(win, p, x, t + u, q, c, n);
             }
-            float a[NC], v[NC];
-            words_to_f<T, NC>(v, raw[u]);
-#pragma unroll
-            for (int i = 0; i < NC; ++i) a[i] = fmaf(w[W - 1][i], v[i], bias[i]);
-#pragma unroll
-            for (int k = 1; k < W; ++k) {
-                words_to_f<T, NC>(v, win[k - 1]);
-#pragma unroll
-                for (int i = 0; i < NC; ++i) a[i] = fmaf(w[W - 1 - k][i], v[i], a[i]);
-            }
+            f32x2 a[NC / 2], v[NC / 2];
+            words_to_pairs<T, NC>(v, raw[u]);
+            convolve<NC, W>(a, w, bias, win, v);
             if (p.silu) {
 #pragma unroll
-                for (int i = 0; i < NC; ++i) a[i] *= sigmoid_f(a[i]);
+                for (int i = 0; i < NC / 2; ++i) {
+                    const float2 f = unpack2(a[i]), g = sigmoid2(f);
+                    a[i] = mul2(a[i], pack2(g.x, g.y));
+                }
             }
-            st_row_f<T, NC, VEC>(out + (int64_t)(t + u) * p.o_st, a, n);
-#pragma unroll
-            for (int k = W - 2; k > 0; --k)
-#pragma unroll
-                for (int i = 0; i < NW; ++i) win[k][i] = win[k - 1][i];
-#pragma unroll
-            for (int i = 0; i < NW; ++i) win[0][i] = raw[u][i];
+            st_pairs<T, NC, VEC>(out + (int64_t)(t + u) * p.o_st, a, n);
+            push<NC, W>(win, v);
             if (p.final_state && t + u + 1 == q.s1) {
 #pragma unroll
                 for (int k = 1; k < W; ++k)
-                    st_row<T, NC, VEC>((T *)p.final_state + ((int64_t)q.seg * (W - 1) + W - 1 - k) * p.D + c,
-                                       win[k - 1], n);
+                    st_pairs<T, NC, VEC>((T *)p.final_state + ((int64_t)q.seg * (W - 1) + W - 1 - k) * p.D + c,
+                                         win[k - 1], n);
             }
         }
     }
 }
 
-// dp at token t from the window before it (win), the token's own input and dout
-template <typename T, int NC, int W>
-__device__ __forceinline__ void dpre(float (&dp)[NC], const float (&w)[W][NC], const float (&bias)[NC],
-                                     const uint32_t (&win)[W - 1][RowVec<T, NC>::kWords], const float (&x)[NC],
-                                     const float (&dout)[NC], int silu) {
-    float v[NC];
+// dp at the token whose input is v
+template <int NC, int W>
+__device__ __forceinline__ void dpre(f32x2 (&dp)[NC / 2], const f32x2 (&w)[W][NC / 2], const f32x2 (&bias)[NC / 2],
+                                     const f32x2 (&win)[W - 1][NC / 2], const f32x2 (&v)[NC / 2],
+                                     const f32x2 (&dout)[NC / 2], int silu) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) dp[i] = dout[i];
+    for (int i = 0; i < NC / 2; ++i) dp[i] = dout[i];
     if (!silu) return;
-    float a[NC];
+    f32x2 a[NC / 2];
+    convolve<NC, W>(a, w, bias, win, v);
 #pragma unroll
-    for (int i = 0; i < NC; ++i) a[i] = fmaf(w[W - 1][i], x[i], bias[i]);
-#pragma unroll
-    for (int k = 1; k < W; ++k) {
-        words_to_f<T, NC>(v, win[k - 1]);
-#pragma unroll
-        for (int i = 0; i < NC; ++i) a[i] = fmaf(w[W - 1 - k][i], v[i], a[i]);
+    for (int i = 0; i < NC / 2; ++i) {
+        const float2 f = unpack2(a[i]), s = sigmoid2(f);
+        dp[i] = mul2(dp[i], pack2(s.x * fmaf(f.x, 1.f - s.x, 1.f), s.y * fmaf(f.y, 1.f - s.y, 1.f)));
     }
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const float s = sigmoid_f(a[i]);
-        dp[i] *= s * fmaf(a[i], 1.f - s, 1.f);
-    }
-}
-template <typename T, int NC, int W>
-__device__ __forceinline__ void push(uint32_t (&win)[W - 1][RowVec<T, NC>::kWords],
-                                     const uint32_t (&raw)[RowVec<T, NC>::kWords]) {
-#pragma unroll
-    for (int k = W - 2; k > 0; --k)
-#pragma unroll
-        for (int i = 0; i < RowVec<T, NC>::kWords; ++i) win[k][i] = win[k - 1][i];
-#pragma unroll
-    for (int i = 0; i < RowVec<T, NC>::kWords; ++i) win[0][i] = raw[i];
 }
 
 // pend[k] holds the part of dx of the token k + 1 back that later tokens have
@@ -218,15 +238,8 @@ __global__ void __launch_bounds__(32 * kConvYBwd) conv_bwd_kernel(const ConvPara
     const bool extra = blockIdx.x == nblk;
     if (extra && p.err && blockIdx.y == 0 && b == 0) check_cu(p.cu, p.n_seq, p.T, p.err);
     if (extra && (!p.dinit || c >= p.D || b > 0)) return;
-    float w[W][NC], bias[NC];
-#pragma unroll
-    for (int i = 0; i < NC; ++i) bias[i] = 0.f;
-    if (c < p.D) {
-        load_taps<T, NC, W, VEC>(w, p.weight, c, n);
-        if (p.bias) ld_row_f<float, NC, VEC>(bias, p.bias + c, n);
-    }
-    uint32_t win[W - 1][NW], raw[NW];
-    float x[NC], go[NC], dp[NC];
+    f32x2 w[W][NC / 2], bias[NC / 2], win[W - 1][NC / 2];
+    if (c < p.D) load_taps<T, NC, W, VEC>(w, bias, p.weight, p.bias, c, n);
     if (extra) {  // the gradient of each carried window: its sequence's first W - 1 tokens
         for (int s = threadIdx.y; s < p.n_seq; s += kConvYBwd) {
             Seq q;
@@ -236,109 +249,136 @@ __global__ void __launch_bounds__(32 * kConvYBwd) conv_bwd_kernel(const ConvPara
             const int len = q.s1 - q.s0, row_b = p.cu ? 0 : s;
             const T *xs = (const T *)p.x + row_b * p.x_sb + c;
             const T *ds = (const T *)p.dout + row_b * p.do_sb + c;
-            float acc[W - 1][NC];
+            f32x2 acc[W - 1][NC / 2];
+            uint32_t raw[NW];
 #pragma unroll
             for (int r = 0; r < W - 1; ++r) {
 #pragma unroll
-                for (int i = 0; i < NC; ++i) acc[r][i] = 0.f;
+                for (int i = 0; i < NW; ++i) raw[i] = 0u;
                 if (p.dfinal && r >= len)
-                    ld_row_f<T, NC, VEC>(acc[r], (const T *)p.dfinal + ((int64_t)s * (W - 1) + r - len) * p.D + c, n);
+                    ld_row<T, NC, VEC>(raw, (const T *)p.dfinal + ((int64_t)s * (W - 1) + r - len) * p.D + c, n);
+                words_to_pairs<T, NC>(acc[r], raw);
             }
             load_window<T, NC, W, VEC>(win, p, xs, q.s0, q, c, n);
 #pragma unroll
             for (int u = 0; u < W - 1; ++u) {
                 if (u < len) {
+                    f32x2 x[NC / 2], go[NC / 2], dp[NC / 2];
                     ld_row<T, NC, VEC>(raw, xs + (int64_t)(q.s0 + u) * p.x_st, n);
-                    words_to_f<T, NC>(x, raw);
-                    ld_row_f<T, NC, VEC>(go, ds + (int64_t)(q.s0 + u) * p.do_st, n);
-                    dpre<T, NC, W>(dp, w, bias, win, x, go, p.silu);
+                    words_to_pairs<T, NC>(x, raw);
+                    ld_row<T, NC, VEC>(raw, ds + (int64_t)(q.s0 + u) * p.do_st, n);
+                    words_to_pairs<T, NC>(go, raw);
+                    dpre<NC, W>(dp, w, bias, win, x, go, p.silu);
                     // token u reads window row r through tap r - u
 #pragma unroll
                     for (int r = u; r < W - 1; ++r)
 #pragma unroll
-                        for (int i = 0; i < NC; ++i) acc[r][i] = fmaf(w[r - u][i], dp[i], acc[r][i]);
-                    push<T, NC, W>(win, raw);
+                        for (int i = 0; i < NC / 2; ++i) acc[r][i] = fma2(w[r - u][i], dp[i], acc[r][i]);
+                    push<NC, W>(win, x);
                 }
             }
 #pragma unroll
             for (int r = 0; r < W - 1; ++r)
-                st_row_f<T, NC, VEC>((T *)p.dinit + ((int64_t)s * (W - 1) + r) * p.D + c, acc[r], n);
+                st_pairs<T, NC, VEC>((T *)p.dinit + ((int64_t)s * (W - 1) + r) * p.D + c, acc[r], n);
         }
         return;
     }
-    float dw[W][NC], db[NC];
+    f32x2 dw[W][NC / 2], db[NC / 2];
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        db[i] = 0.f;
+    for (int i = 0; i < NC / 2; ++i) {
+        db[i] = pack2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
+        for (int j = 0; j < W; ++j) dw[j][i] = pack2(0.f, 0.f);
     }
     const int64_t first = ((int64_t)blockIdx.x * kConvYBwd + threadIdx.y) * kTokLBwd;
     if (c < p.D && first < p.T) {
-        const int t0 = (int)first, t1 = min(p.T - t0, kTokLBwd) + t0;
+        constexpr int U = 4;
+        const int t0 = (int)first, t1 = min(p.T - t0, kTokLBwd) + t0, t2 = min(p.T - t1, W - 1) + t1;
         const T *xs = (const T *)p.x + b * p.x_sb + c;
         const T *ds = (const T *)p.dout + b * p.do_sb + c;
         T *dx = (T *)p.dx + (int64_t)b * p.T * p.D + c;
         Seq q = find_seq(p.cu, p.n_seq, p.T, b, t0);
         load_window<T, NC, W, VEC>(win, p, xs, t0, q, c, n);
-        float pend[W][NC];
+        f32x2 pend[W][NC / 2];
 #pragma unroll
         for (int k = 0; k < W; ++k)
 #pragma unroll
-            for (int i = 0; i < NC; ++i) pend[k][i] = 0.f;
-        for (int t = t0; t < t1 + W - 1; ++t) {
+            for (int i = 0; i < NC / 2; ++i) pend[k][i] = pack2(0.f, 0.f);
+        uint32_t nx[U][NW], nd[U][NW];
+        auto fetch = [&](int t) {
 #pragma unroll
-            for (int k = W - 1; k > 0; --k)
-#pragma unroll
-                for (int i = 0; i < NC; ++i) pend[k][i] = pend[k - 1][i];
-#pragma unroll
-            for (int i = 0; i < NC; ++i) pend[0][i] = 0.f;
-            if (t < p.T) {
-                if (t == q.s1) {
-                    next_seq(q, p.cu, p.n_seq, t);
-                    load_window<T, NC, W, VEC>(win, p, xs, t, q, c, n);
+            for (int u = 0; u < U; ++u)
+                if (t + u < t2) {
+                    ld_row<T, NC, VEC>(nx[u], xs + (int64_t)(t + u) * p.x_st, n);
+                    ld_row<T, NC, VEC>(nd[u], ds + (int64_t)(t + u) * p.do_st, n);
                 }
-                ld_row<T, NC, VEC>(raw, xs + (int64_t)t * p.x_st, n);
-                words_to_f<T, NC>(x, raw);
-                ld_row_f<T, NC, VEC>(go, ds + (int64_t)t * p.do_st, n);
-                dpre<T, NC, W>(dp, w, bias, win, x, go, p.silu);
-                if (t < t1) {
+        };
+        fetch(t0);
+        for (int tb = t0; tb < t1 + W - 1; tb += U) {
+            uint32_t rx[U][NW], rd[U][NW];
 #pragma unroll
-                    for (int i = 0; i < NC; ++i) {
-                        db[i] += dp[i];
-                        dw[W - 1][i] = fmaf(dp[i], x[i], dw[W - 1][i]);
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < NW; ++i) rx[u][i] = nx[u][i], rd[u][i] = nd[u][i];
+            fetch(tb + U);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int t = tb + u;
+#pragma unroll
+                for (int k = W - 1; k > 0; --k)
+#pragma unroll
+                    for (int i = 0; i < NC / 2; ++i) pend[k][i] = pend[k - 1][i];
+#pragma unroll
+                for (int i = 0; i < NC / 2; ++i) pend[0][i] = pack2(0.f, 0.f);
+                if (t < t2) {
+                    if (t == q.s1) {
+                        next_seq(q, p.cu, p.n_seq, t);
+                        load_window<T, NC, W, VEC>(win, p, xs, t, q, c, n);
+                    }
+                    f32x2 x[NC / 2], go[NC / 2], dp[NC / 2];
+                    words_to_pairs<T, NC>(x, rx[u]);
+                    words_to_pairs<T, NC>(go, rd[u]);
+                    dpre<NC, W>(dp, w, bias, win, x, go, p.silu);
+                    if (t < t1) {
+#pragma unroll
+                        for (int i = 0; i < NC / 2; ++i) {
+                            db[i] = add2(db[i], dp[i]);
+                            dw[W - 1][i] = fma2(dp[i], x[i], dw[W - 1][i]);
+#pragma unroll
+                            for (int k = 1; k < W; ++k) dw[W - 1 - k][i] = fma2(dp[i], win[k - 1][i], dw[W - 1 - k][i]);
+                        }
+                        if (p.dfinal && t >= q.s1 - (W - 1)) {
+                            uint32_t raw[NW];
+                            ld_row<T, NC, VEC>(
+                                raw,
+                                (const T *)p.dfinal + ((int64_t)q.seg * (W - 1) + t - (q.s1 - (W - 1))) * p.D + c, n);
+                            words_to_pairs<T, NC>(pend[0], raw);
+                        }
                     }
 #pragma unroll
-                    for (int k = 1; k < W; ++k) {
-                        float v[NC];
-                        words_to_f<T, NC>(v, win[k - 1]);
+                    for (int k = 0; k < W; ++k)
+                        if (t - k >= q.s0) {
 #pragma unroll
-                        for (int i = 0; i < NC; ++i) dw[W - 1 - k][i] = fmaf(dp[i], v[i], dw[W - 1 - k][i]);
-                    }
-                    if (p.dfinal && t >= q.s1 - (W - 1))
-                        ld_row_f<T, NC, VEC>(
-                            pend[0],
-                            (const T *)p.dfinal + ((int64_t)q.seg * (W - 1) + t - (q.s1 - (W - 1))) * p.D + c, n);
+                            for (int i = 0; i < NC / 2; ++i) pend[k][i] = fma2(w[W - 1 - k][i], dp[i], pend[k][i]);
+                        }
+                    push<NC, W>(win, x);
                 }
-#pragma unroll
-                for (int k = 0; k < W; ++k)
-                    if (t - k >= q.s0) {
-#pragma unroll
-                        for (int i = 0; i < NC; ++i) pend[k][i] = fmaf(w[W - 1 - k][i], dp[i], pend[k][i]);
-                    }
-                push<T, NC, W>(win, raw);
+                const int done = t - (W - 1);
+                if (done >= t0 && done < t1) st_pairs<T, NC, VEC>(dx + (int64_t)done * p.D, pend[W - 1], n);
             }
-            const int done = t - (W - 1);
-            if (done >= t0 && done < t1) st_row_f<T, NC, VEC>(dx + (int64_t)done * p.D, pend[W - 1], n);
         }
     }
     // the CTA's share of dw and db
     constexpr int Q = NC * (W + 1);
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
+    for (int i = 0; i < NC / 2; ++i) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) red[(threadIdx.y * Q + i * W + j) * 32 + threadIdx.x] = dw[j][i];
-        red[(threadIdx.y * Q + NC * W + i) * 32 + threadIdx.x] = db[i];
+        for (int j = 0; j <= W; ++j) {
+            const float2 f = unpack2(j < W ? dw[j < W ? j : 0][i] : db[i]);
+            const int r0 = j < W ? 2 * i * W + j : NC * W + 2 * i, r1 = j < W ? r0 + W : r0 + 1;
+            red[(threadIdx.y * Q + r0) * 32 + threadIdx.x] = f.x;
+            red[(threadIdx.y * Q + r1) * 32 + threadIdx.x] = f.y;
+        }
     }
     __syncthreads();
     float *part = p.part + ((int64_t)b * nblk + blockIdx.x) * ((int64_t)p.D * (W + 1));
@@ -360,32 +400,34 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvStepParams p) 
     if (c >= p.D) return;
     const int slot = p.slots ? p.slots[i0] : i0;
     T *out = (T *)p.out + (int64_t)i0 * p.o_st + c;
-    float a[NC], v[NC], w[W][NC];
+    f32x2 a[NC / 2], v[NC / 2], w[W][NC / 2];
     uint32_t raw[W][NW];
-#pragma unroll
-    for (int i = 0; i < NC; ++i) a[i] = 0.f;
     if (slot < 0 || slot >= p.n_slots) {  // a padding row
-        st_row_f<T, NC, VEC>(out, a, n);
+#pragma unroll
+        for (int i = 0; i < NC / 2; ++i) a[i] = pack2(0.f, 0.f);
+        st_pairs<T, NC, VEC>(out, a, n);
         return;
     }
     T *state = (T *)p.state + (int64_t)slot * (W - 1) * p.D + c;
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) ld_row<T, NC, VEC>(raw[j], state + (int64_t)j * p.D, n);
     ld_row<T, NC, VEC>(raw[W - 1], (const T *)p.x + (int64_t)i0 * p.x_st + c, n);
-    load_taps<T, NC, W, VEC>(w, p.weight, c, n);
-    if (p.bias) ld_row_f<float, NC, VEC>(a, p.bias + c, n);
+    load_taps<T, NC, W, VEC>(w, a, p.weight, p.bias, c, n);
 #pragma unroll
     for (int j = W - 1; j >= 0; --j) {
-        words_to_f<T, NC>(v, raw[j]);
+        words_to_pairs<T, NC>(v, raw[j]);
 #pragma unroll
-        for (int i = 0; i < NC; ++i) a[i] = fmaf(w[j][i], v[i], a[i]);
+        for (int i = 0; i < NC / 2; ++i) a[i] = fma2(w[j][i], v[i], a[i]);
         if (j > 0) st_row<T, NC, VEC>(state + (int64_t)(j - 1) * p.D, raw[j], n);
     }
     if (p.silu) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) a[i] *= sigmoid_f(a[i]);
+        for (int i = 0; i < NC / 2; ++i) {
+            const float2 g = sigmoid2(unpack2(a[i]));
+            a[i] = mul2(a[i], pack2(g.x, g.y));
+        }
     }
-    st_row_f<T, NC, VEC>(out, a, n);
+    st_pairs<T, NC, VEC>(out, a, n);
 }
 
 // calls f with the tap count as a constant
@@ -406,12 +448,17 @@ cudaError_t by_taps(int W, F &&f) {
 template <typename T>
 cudaError_t conv_t(const ConvParams &p, cudaStream_t st) {
     constexpr int NC = 16 / sizeof(T);
-    const int nblk = (int)(((int64_t)p.T + kConvY * kTokL - 1) / (kConvY * kTokL));
+    // Tokens a thread: 32, where W - 1 more inputs are read for each run, or down
+    // to 8 while that leaves SMs without a CTA.
+    int run = 32;
+    auto blocks = [&] { return (int)(((int64_t)p.T + kConvY * run - 1) / (kConvY * run)); };
+    while (run > 8 && (int64_t)blocks() * ((p.D + 32 * NC - 1) / (32 * NC)) * p.B < 608) run /= 2;
+    const int nblk = blocks();
     const bool extra = p.cu != nullptr || p.T == 0;
     const dim3 grid(nblk + (extra ? 1 : 0), (p.D + 32 * NC - 1) / (32 * NC), p.T == 0 ? 1 : p.B), block(32, kConvY);
     return by_taps(p.W, [&](auto w) {
-        if (p.vec) conv_kernel<T, NC, w(), true><<<grid, block, 0, st>>>(p, nblk);
-        else conv_kernel<T, NC, w(), false><<<grid, block, 0, st>>>(p, nblk);
+        if (p.vec) conv_kernel<T, NC, w(), true><<<grid, block, 0, st>>>(p, nblk, run);
+        else conv_kernel<T, NC, w(), false><<<grid, block, 0, st>>>(p, nblk, run);
         return cudaGetLastError();
     });
 }

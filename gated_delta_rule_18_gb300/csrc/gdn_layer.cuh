@@ -253,6 +253,7 @@ struct SsmStepParams {
     void *out;
     int64_t o_st;
     int n, n_slots, D, N, softplus, bf16;
+    int n_wide;  // rows of A and of the states are 16-byte aligned
 };
 cudaError_t launch_ssm_step(const SsmStepParams &p, cudaStream_t st);
 

@@ -411,6 +411,7 @@ gdn_status gdn_ssm_step(const void *x, int64_t x_st, const void *dt, int64_t dt_
     p.x = x, p.dt = dt, p.bm = bm, p.cm = cm, p.z = z;
     p.x_st = x_st, p.dt_st = dt_st, p.bm_st = bm_st, p.cm_st = cm_st, p.z_st = z_st;
     p.A = A, p.Dv = Dv, p.dt_bias = dt_bias, p.state = state, p.slots = slots, p.out = out, p.o_st = out_st;
+    p.n_wide = N % 4 == 0 && addr(A) % 16 == 0 && addr(state) % 16 == 0;
     p.n = n, p.n_slots = n_slots, p.D = D, p.N = N, p.softplus = flags & GDN_SOFTPLUS, p.bf16 = dtype == GDN_BF16;
     return cuda_status(launch(KSsmStep, stream, [&] { return launch_ssm_step(p, stream); }));
 }

@@ -31,6 +31,20 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
     return r;
 }
 
+// y / scale for one scale. An IEEE division costs some ten instructions a
+// value; one reciprocal and a correction of the quotient by its remainder
+// round the same (|y| <= 448 scale (1 + 2^-24), no intermediate overflows
+// unless the scale itself is out of range, where the plain quotient is taken).
+__device__ __forceinline__ void quantise(float (&y)[kVecN], float scale) {
+    const float dv = scale == 0.f ? 1.f : scale, r = 1.f / dv;
+    const bool safe = dv > 1e-30f && dv < 1e30f;
+#pragma unroll
+    for (int j = 0; j < kVecN; ++j) {
+        const float q = y[j] * r;
+        y[j] = safe ? fmaf(fmaf(-q, dv, y[j]), r, q) : y[j] / dv;
+    }
+}
+
 // Threads a row and vectors a thread: one vector a thread up to 512 threads.
 struct RowShape {
     int tpr, nv, rpb;
@@ -63,101 +77,114 @@ __device__ __forceinline__ float row_reduce(float v, float *red, int tpr) {
     return v;
 }
 
-template <typename TX, typename TR, bool Q8, int NV, bool VEC>
+// One CTA walks rows blockIdx, blockIdx + grid, ..., the weights in registers.
+// PRE: the next row's loads are issued before this row's sum is known.
+template <typename TX, typename TR, bool Q8, int NV, bool VEC, bool PRE>
 __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormParams p, int tpr) {
-    __shared__ float red[2][16];
-    const int lr = threadIdx.x / tpr, tid = threadIdx.x - lr * tpr;
-    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + lr;
-    const bool live = row < p.R;
-    float s[NV][kVecN];
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + tid) * kVecN;
-        if (live && c < p.D) {
-            ld_row_f<TX, kVecN, VEC>(s[i], (const TX *)p.x + row * p.x_st + c, p.D - c);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kVecN; ++j) s[i][j] = 0.f;
-        }
-    }
-    if (p.res) {
+    __shared__ float red[2][2][16];
+    constexpr int WX = RowVec<TX, kVecN>::kWords, WR = RowVec<TR, kVecN>::kWords;
+    const int rpb = blockDim.x / tpr, lr = threadIdx.x / tpr, tid = threadIdx.x - lr * tpr;
+    const int64_t step = (int64_t)gridDim.x * rpb;
+    int64_t row = (int64_t)blockIdx.x * rpb + lr;
+    uint32_t nx[NV][WX], nr[NV][WR];
+    auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + tid) * kVecN;
-            if (live && c < p.D) {
-                float r[kVecN];
-                ld_row_f<TR, kVecN, VEC>(r, (const TR *)p.res + row * p.res_st + c, p.D - c);
 #pragma unroll
-                for (int j = 0; j < kVecN; ++j) s[i][j] += r[j];
-                st_row_f<TR, kVecN, VEC>((TR *)p.res_out + row * p.ro_st + c, s[i], p.D - c);
+            for (int j = 0; j < WX; ++j) nx[i][j] = 0u;
+#pragma unroll
+            for (int j = 0; j < WR; ++j) nr[i][j] = 0u;
+            if (r < p.R && c < p.D) {
+                ld_row<TX, kVecN, VEC>(nx[i], (const TX *)p.x + r * p.x_st + c, p.D - c);
+                if (p.res) ld_row<TR, kVecN, VEC>(nr[i], (const TR *)p.res + r * p.res_st + c, p.D - c);
             }
         }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < kVecN; ++j) sum = fmaf(s[i][j], s[i][j], sum);
-    sum = row_reduce<false>(sum, red[0], tpr);
-    const float inv = rsqrtf(sum / (float)p.D + p.eps);
-    float row_max = 0.f;
+    };
+    fetch(row);
+    float w[NV][kVecN];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + tid) * kVecN;
-        const bool in = live && c < p.D;
-        if (in) {
-            float w[kVecN];
-            ld_row_f<float, kVecN, VEC>(w, p.weight + c, p.D - c);
 #pragma unroll
-            for (int j = 0; j < kVecN; ++j) s[i][j] = s[i][j] * inv * w[j];
+        for (int j = 0; j < kVecN; ++j) w[i][j] = 0.f;
+        if (c < p.D) ld_row_f<float, kVecN, VEC>(w[i], p.weight + c, p.D - c);
+    }
+    const int groups = p.group > 0 ? (p.D + p.group - 1) / p.group : 1;
+    int flip = 0;
+    // every thread of the CTA makes the same number of turns
+    for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < p.R; r0 += step, row += step, flip ^= 1) {
+        const bool live = row < p.R;
+        float s[NV][kVecN];
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + tid) * kVecN;
+            words_to_f<TX, kVecN>(s[i], nx[i]);
+            if (p.res) {
+                float r[kVecN];
+                words_to_f<TR, kVecN>(r, nr[i]);
+#pragma unroll
+                for (int j = 0; j < kVecN; ++j) s[i][j] += r[j];
+                if (live && c < p.D) st_row_f<TR, kVecN, VEC>((TR *)p.res_out + row * p.ro_st + c, s[i], p.D - c);
+            }
         }
-        if constexpr (!Q8) {
-            if (in) st_row_f<TX, kVecN, VEC>((TX *)p.out + row * p.o_st + c, s[i], p.D - c);
-        } else {
-            float m = 0.f;
+        if (PRE) fetch(row + step);
 #pragma unroll
-            for (int j = 0; j < kVecN; ++j) m = max_nan(m, fabsf(s[i][j]));
-            row_max = max_nan(row_max, m);
-            if (p.group > 0) {
-                // a group's vectors sit in group / 8 neighbouring lanes
-                for (int o = p.group / kVecN / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const float sc = m / 448.f;
-                if (in) {
-                    if (c % p.group == 0) p.scale[row * ((p.D + p.group - 1) / p.group) + c / p.group] = sc;
-                    const float dv = sc == 0.f ? 1.f : sc;
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-                    for (int j = 0; j < kVecN; ++j) s[i][j] = s[i][j] / dv;
+            for (int j = 0; j < kVecN; ++j) sum = fmaf(s[i][j], s[i][j], sum);
+        sum = row_reduce<false>(sum, red[flip][0], tpr);
+        const float inv = rsqrtf(sum / (float)p.D + p.eps);
+        float row_max = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + tid) * kVecN;
+            const bool in = live && c < p.D;
+#pragma unroll
+            for (int j = 0; j < kVecN; ++j) s[i][j] = s[i][j] * inv * w[i][j];
+            if constexpr (!Q8) {
+                if (in) st_row_f<TX, kVecN, VEC>((TX *)p.out + row * p.o_st + c, s[i], p.D - c);
+            } else {
+                float m = 0.f;
+#pragma unroll
+                for (int j = 0; j < kVecN; ++j) m = max_nan(m, fabsf(s[i][j]));
+                row_max = max_nan(row_max, m);
+                if (p.group > 0) {
+                    // a group's vectors sit in group / 8 neighbouring lanes
+                    for (int o = p.group / kVecN / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    const float sc = m / 448.f;
+                    if (in && c % p.group == 0) p.scale[row * groups + c / p.group] = sc;
+                    quantise(s[i], sc);
                 }
             }
         }
-    }
-    if constexpr (Q8) {
-        if (p.group == 0) {
-            const float sc = row_reduce<true>(row_max, red[1], tpr) / 448.f;
-            if (live && tid == 0) p.scale[row] = sc;
-            const float dv = sc == 0.f ? 1.f : sc;
+        if constexpr (Q8) {
+            if (p.group == 0) {
+                const float sc = row_reduce<true>(row_max, red[flip][1], tpr) / 448.f;
+                if (live && tid == 0) p.scale[row] = sc;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+                for (int i = 0; i < NV; ++i) quantise(s[i], sc);
+            }
 #pragma unroll
-                for (int j = 0; j < kVecN; ++j) s[i][j] = s[i][j] / dv;
-        }
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * tpr + tid) * kVecN;
+                if (!(live && c < p.D)) continue;
+                uint32_t q[2];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + tid) * kVecN;
-            if (!(live && c < p.D)) continue;
-            uint32_t q[2];
+                for (int j = 0; j < 2; ++j)
+                    q[j] = pack_e4m3(s[i][4 * j], s[i][4 * j + 1]) | pack_e4m3(s[i][4 * j + 2], s[i][4 * j + 3]) << 16;
+                uint8_t *o = (uint8_t *)p.out + row * p.o_st + c;
+                if constexpr (VEC) {
+                    st_words(o, q);
+                } else {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                q[j] = pack_e4m3(s[i][4 * j], s[i][4 * j + 1]) | pack_e4m3(s[i][4 * j + 2], s[i][4 * j + 3]) << 16;
-            uint8_t *o = (uint8_t *)p.out + row * p.o_st + c;
-            if constexpr (VEC) {
-                st_words(o, q);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kVecN; ++j)
-                    if (c + j < p.D) o[j] = (uint8_t)(q[j >> 2] >> (8 * (j & 3)));
+                    for (int j = 0; j < kVecN; ++j)
+                        if (c + j < p.D) o[j] = (uint8_t)(q[j >> 2] >> (8 * (j & 3)));
+                }
             }
         }
+        if (!PRE) fetch(row + step);
     }
 }
 
@@ -291,15 +318,16 @@ __global__ void __launch_bounds__(256) col_sum_kernel(const float *in, int64_t l
 template <typename TX, typename TR, bool Q8>
 cudaError_t norm_nv(const NormParams &p, cudaStream_t st) {
     const RowShape s = row_shape(p.D, 512);
-    const unsigned grid = (unsigned)((p.R + s.rpb - 1) / s.rpb), nt = s.tpr * s.rpb;
+    const unsigned nt = s.tpr * s.rpb, need = (unsigned)((p.R + s.rpb - 1) / s.rpb);
+    const unsigned most = 152 * (1024 / nt), grid = need < most ? need : most;
     if (!p.vec) {
-        rmsnorm_kernel<TX, TR, Q8, 4, false><<<grid, nt, 0, st>>>(p, s.tpr);
+        rmsnorm_kernel<TX, TR, Q8, 4, false, false><<<grid, nt, 0, st>>>(p, s.tpr);
     } else if (s.nv == 1) {
-        rmsnorm_kernel<TX, TR, Q8, 1, true><<<grid, nt, 0, st>>>(p, s.tpr);
+        rmsnorm_kernel<TX, TR, Q8, 1, true, true><<<grid, nt, 0, st>>>(p, s.tpr);
     } else if (s.nv == 2) {
-        rmsnorm_kernel<TX, TR, Q8, 2, true><<<grid, nt, 0, st>>>(p, s.tpr);
+        rmsnorm_kernel<TX, TR, Q8, 2, true, true><<<grid, nt, 0, st>>>(p, s.tpr);
     } else {
-        rmsnorm_kernel<TX, TR, Q8, 4, true><<<grid, nt, 0, st>>>(p, s.tpr);
+        rmsnorm_kernel<TX, TR, Q8, 4, true, false><<<grid, nt, 0, st>>>(p, s.tpr);
     }
     return cudaGetLastError();
 }

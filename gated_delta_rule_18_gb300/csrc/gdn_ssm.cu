@@ -251,40 +251,78 @@ __global__ void __launch_bounds__(256) ssm_chain_kernel(const SsmParams p, int n
     }
 }
 
-// One token of each request: the state is read, updated and written back.
+// One token of each request: the state is read, updated and written back, all
+// that counts. Four states a lane, LN lanes a channel, two channels a lane (of
+// the halves of the CTA's range) so that two states' loads are under way.
 template <typename T, int LN>
 __global__ void __launch_bounds__(128) ssm_step_kernel(const SsmStepParams p) {
-    const int i = blockIdx.y;
-    const int d = blockIdx.x * (128 / LN) + threadIdx.x / LN, n0 = threadIdx.x % LN * 4;
-    const bool in = d < p.D;
-    const int slot = p.slots ? p.slots[i] : i;
-    if (slot < 0 || slot >= p.n_slots) {  // a padding row
-        if (in && n0 == 0) ((T *)p.out)[i * p.o_st + d] = to_type<T>(0.f);
-        return;
+    constexpr int CH = 128 / LN;
+    const int i = blockIdx.y, n0 = threadIdx.x % LN * 4;
+    const int64_t slot = p.slots ? p.slots[i] : i;
+    const bool real = slot >= 0 && slot < p.n_slots;
+    int d[2];
+    float h[2][4], a[2][4], x[2], dl[2], z[2] = {0.f, 0.f}, b[4], c[4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        d[k] = (blockIdx.x * 2 + k) * CH + threadIdx.x / LN;
+        const bool on = real && d[k] < p.D && n0 < p.N;
+        const int64_t own = (int64_t)d[k] * p.N + n0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            h[k][j] = a[k][j] = 0.f;
+            if (!p.n_wide && on && n0 + j < p.N) {
+                h[k][j] = p.state[slot * p.D * p.N + own + j];
+                a[k][j] = p.A[own + j];
+            }
+        }
+        if (p.n_wide && on) {
+            const float4 u = *reinterpret_cast<const float4 *>(p.state + slot * p.D * p.N + own);
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(p.A + own));
+            h[k][0] = u.x, h[k][1] = u.y, h[k][2] = u.z, h[k][3] = u.w;
+            a[k][0] = v.x, a[k][1] = v.y, a[k][2] = v.z, a[k][3] = v.w;
+        }
+        const bool in = real && d[k] < p.D;
+        x[k] = in ? ldf((const T *)p.x + i * p.x_st + d[k]) : 0.f;
+        dl[k] = in ? ldf((const T *)p.dt + i * p.dt_st + d[k]) + (p.dt_bias ? p.dt_bias[d[k]] : 0.f) : 0.f;
+        if (in && p.z) z[k] = ldf((const T *)p.z + i * p.z_st + d[k]);
     }
-    float *state = p.state + ((int64_t)slot * p.D + d) * p.N + n0;
-    const float x = in ? ldf((const T *)p.x + i * p.x_st + d) : 0.f;
-    float dl = in ? ldf((const T *)p.dt + i * p.dt_st + d) + (p.dt_bias ? p.dt_bias[d] : 0.f) : 0.f;
-    if (p.softplus) dl = softplus2(make_float2(dl, dl)).x;
-    const float u = dl * x;
-    float y = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        if (!in || n0 + j >= p.N) continue;
-        const float b = ldf((const T *)p.bm + i * p.bm_st + n0 + j), c = ldf((const T *)p.cm + i * p.cm_st + n0 + j);
-        const float h = fmaf(ex2f(dl * (p.A[(int64_t)d * p.N + n0 + j] * kLog2e)), state[j], u * b);
-        state[j] = h;
-        y = fmaf(h, c, y);
+        const bool on = n0 + j < p.N;
+        b[j] = on ? ldf((const T *)p.bm + i * p.bm_st + n0 + j) : 0.f;
+        c[j] = on ? ldf((const T *)p.cm + i * p.cm_st + n0 + j) : 0.f;
     }
+    if (p.softplus) {
+        const float2 v = softplus2(make_float2(dl[0], dl[1]));
+        dl[0] = v.x, dl[1] = v.y;
+    }
+    const float2 g = sigmoid2(make_float2(z[0], z[1]));
 #pragma unroll
-    for (int o = LN / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (in && n0 == 0) {
-        if (p.Dv) y = fmaf(p.Dv[d], x, y);
-        if (p.z) {
-            const float z = ldf((const T *)p.z + i * p.z_st + d);
-            y *= z * sigmoid2(make_float2(z, z)).x;
+    for (int k = 0; k < 2; ++k) {
+        const float u = dl[k] * x[k], dk = dl[k] * kLog2e;
+        float y = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            h[k][j] = fmaf(ex2f(dk * a[k][j]), h[k][j], u * b[j]);
+            y = fmaf(h[k][j], c[j], y);
         }
-        ((T *)p.out)[i * p.o_st + d] = to_type<T>(y);
+        if (real && d[k] < p.D && n0 < p.N) {
+            float *state = p.state + (slot * p.D + d[k]) * p.N + n0;
+            if (p.n_wide) {
+                *reinterpret_cast<float4 *>(state) = make_float4(h[k][0], h[k][1], h[k][2], h[k][3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n0 + j < p.N) state[j] = h[k][j];
+            }
+        }
+#pragma unroll
+        for (int o = LN / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        if (d[k] < p.D && n0 == 0) {
+            if (p.Dv) y = fmaf(p.Dv[d[k]], x[k], y);
+            if (p.z) y *= z[k] * (k ? g.y : g.x);
+            ((T *)p.out)[i * p.o_st + d[k]] = to_type<T>(real ? y : 0.f);  // a padding row is zero
+        }
     }
 }
 
@@ -352,7 +390,7 @@ cudaError_t launch_ssm_scan(const SsmParams &p, cudaStream_t st) {
 }
 cudaError_t launch_ssm_step(const SsmStepParams &p, cudaStream_t st) {
     return by_lanes(p.N, [&](auto ln) {
-        const dim3 grid((p.D + 128 / ln() - 1) / (128 / ln()), p.n);
+        const dim3 grid((p.D + 256 / ln() - 1) / (256 / ln()), p.n);
         if (p.bf16) ssm_step_kernel<__nv_bfloat16, ln()><<<grid, 128, 0, st>>>(p);
         else ssm_step_kernel<float, ln()><<<grid, 128, 0, st>>>(p);
         return cudaGetLastError();
