@@ -19,7 +19,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kTokLBwd = 32;  // tokens a thread, gradient
+constexpr int kTokLBwd = 64;  // tokens a thread, gradient
 constexpr int kConvY = 4, kConvYBwd = 8;
 
 // The sequence of a token: the last s with cu[s] <= t, its bounds clamped so
@@ -119,6 +119,12 @@ __device__ __forceinline__ void push(f32x2 (&win)[W - 1][NC / 2], const f32x2 (&
 #pragma unroll
     for (int i = 0; i < NC / 2; ++i) win[0][i] = v[i];
 }
+// sigmoid of a pair; exp(-x) = inf gives 0
+__device__ __forceinline__ f32x2 sigmoid_pair(f32x2 x) {
+    const f32x2 e = add2(ex2_2(mul2(x, pack2(-kLog2e, -kLog2e))), pack2(1.f, 1.f));
+    const float2 f = unpack2(e);
+    return pack2(rcpf(f.x), rcpf(f.y));
+}
 // the convolution at the token whose input is v
 template <int NC, int W>
 __device__ __forceinline__ void convolve(f32x2 (&a)[NC / 2], const f32x2 (&w)[W][NC / 2], const f32x2 (&bias)[NC / 2],
@@ -141,7 +147,7 @@ __device__ __forceinline__ void check_cu(const int32_t *cu, int n_seq, int T, in
 }
 
 template <typename T, int NC, int W, bool VEC>
-__global__ void __launch_bounds__(32 * kConvY) conv_kernel(const ConvParams p, int nblk, int run) {
+__global__ void __launch_bounds__(32 * kConvY, 6) conv_kernel(const ConvParams p, int nblk, int run) {
     constexpr int NW = RowVec<T, NC>::kWords, U = 4;
     const int c = (blockIdx.y * 32 + threadIdx.x) * NC, n = p.D - c, b = blockIdx.z;
     if (blockIdx.x == nblk) {  // checks, and the windows of empty sequences
@@ -168,12 +174,36 @@ __global__ void __launch_bounds__(32 * kConvY) conv_kernel(const ConvParams p, i
     Seq q = find_seq(p.cu, p.n_seq, p.T, b, t0);
     load_window<T, NC, W, VEC>(win, p, x, t0, q, c, n);
     uint32_t next[U][NW];
+    const T *xp = x + (int64_t)t0 * p.x_st;  // the next load's and store's rows
+    T *op = out + (int64_t)t0 * p.o_st;
     auto fetch = [&](int t) {
+        if (t + U <= t1) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t + u < t1) ld_row<T, NC, VEC>(next[u], x + (int64_t)(t + u) * p.x_st, n);
+            for (int u = 0; u < U; ++u, xp += p.x_st) ld_row<T, NC, VEC>(next[u], xp, n);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u, xp += p.x_st)
+                if (t + u < t1) ld_row<T, NC, VEC>(next[u], xp, n);
+        }
     };
     fetch(t0);
+    auto window_out = [&](int seg) {
+#pragma unroll
+        for (int k = 1; k < W; ++k)
+            st_pairs<T, NC, VEC>((T *)p.final_state + ((int64_t)seg * (W - 1) + W - 1 - k) * p.D + c, win[k - 1], n);
+    };
+    auto token = [&](const uint32_t (&raw)[NW]) {
+        f32x2 a[NC / 2], v[NC / 2];
+        words_to_pairs<T, NC>(v, raw);
+        convolve<NC, W>(a, w, bias, win, v);
+        if (p.silu) {
+#pragma unroll
+            for (int i = 0; i < NC / 2; ++i) a[i] = mul2(a[i], sigmoid_pair(a[i]));
+        }
+        st_pairs<T, NC, VEC>(op, a, n);
+        op += p.o_st;
+        push<NC, W>(win, v);
+    };
     for (int t = t0; t < t1; t += U) {
         uint32_t raw[U][NW];
 #pragma unroll
@@ -181,30 +211,27 @@ __global__ void __launch_bounds__(32 * kConvY) conv_kernel(const ConvParams p, i
 #pragma unroll
             for (int i = 0; i < NW; ++i) raw[u][i] = next[u][i];
         fetch(t + U);
+        if (t == q.s1) {
+            next_seq(q, p.cu, p.n_seq, t);
+            load_window<T, NC, W, VEC>(win, p, x, t, q, c, n);
+        }
+        if (t + U <= t1 && t + U <= q.s1) {  // four tokens of one sequence, without a branch
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t + u >= t1) break;
-            if (t + u == q.s1) {
-                next_seq(q, p.cu, p.n_seq, t + u);
-                load_window<T, NC, W, VEC>(win, p, x, t + u, q, c, n);
-            }
-            f32x2 a[NC / 2], v[NC / 2];
-            words_to_pairs<T, NC>(v, raw[u]);
-            convolve<NC, W>(a, w, bias, win, v);
-            if (p.silu) {
-#pragma unroll
-                for (int i = 0; i < NC / 2; ++i) {
-                    const float2 f = unpack2(a[i]), g = sigmoid2(f);
-                    a[i] = mul2(a[i], pack2(g.x, g.y));
+            for (int u = 0; u < U; ++u) token(raw[u]);
+            if (p.final_state && t + U == q.s1) window_out(q.seg);
+        } else {
+#pragma unroll 1
+            for (int u = 0; u < U && t + u < t1; ++u) {
+                if (t + u == q.s1) {
+                    next_seq(q, p.cu, p.n_seq, t + u);
+                    load_window<T, NC, W, VEC>(win, p, x, t + u, q, c, n);
                 }
-            }
-            st_pairs<T, NC, VEC>(out + (int64_t)(t + u) * p.o_st, a, n);
-            push<NC, W>(win, v);
-            if (p.final_state && t + u + 1 == q.s1) {
+                uint32_t cur[NW];
 #pragma unroll
-                for (int k = 1; k < W; ++k)
-                    st_pairs<T, NC, VEC>((T *)p.final_state + ((int64_t)q.seg * (W - 1) + W - 1 - k) * p.D + c,
-                                         win[k - 1], n);
+                for (int i = 0; i < NW; ++i)
+                    cur[i] = u == 0 ? raw[0][i] : u == 1 ? raw[1][i] : u == 2 ? raw[2][i] : raw[3][i];
+                token(cur);
+                if (p.final_state && t + u + 1 == q.s1) window_out(q.seg);
             }
         }
     }
@@ -222,8 +249,10 @@ __device__ __forceinline__ void dpre(f32x2 (&dp)[NC / 2], const f32x2 (&w)[W][NC
     convolve<NC, W>(a, w, bias, win, v);
 #pragma unroll
     for (int i = 0; i < NC / 2; ++i) {
-        const float2 f = unpack2(a[i]), s = sigmoid2(f);
-        dp[i] = mul2(dp[i], pack2(s.x * fmaf(f.x, 1.f - s.x, 1.f), s.y * fmaf(f.y, 1.f - s.y, 1.f)));
+            // silu' = s + a s (1 - s)
+        const f32x2 s = sigmoid_pair(a[i]), as = mul2(a[i], s);
+        const f32x2 r = fma2(mul2(as, pack2(-1.f, -1.f)), s, as);
+        dp[i] = mul2(dp[i], add2(s, r));
     }
 }
 
@@ -231,7 +260,7 @@ __device__ __forceinline__ void dpre(f32x2 (&dp)[NC / 2], const f32x2 (&w)[W][NC
 // already given; a token's dx is complete W - 1 tokens later, so a run of
 // tokens is followed by W - 1 more that only add to the run's own.
 template <typename T, int NC, int W, bool VEC>
-__global__ void __launch_bounds__(32 * kConvYBwd) conv_bwd_kernel(const ConvParams p, int nblk) {
+__global__ void __launch_bounds__(32 * kConvYBwd, 2) conv_bwd_kernel(const ConvParams p, int nblk) {
     constexpr int NW = RowVec<T, NC>::kWords;
     extern __shared__ float red[];  // [kConvYBwd][NC * (W + 1)][32]
     const int c = (blockIdx.y * 32 + threadIdx.x) * NC, n = p.D - c, b = blockIdx.z;
@@ -305,15 +334,86 @@ __global__ void __launch_bounds__(32 * kConvYBwd) conv_bwd_kernel(const ConvPara
 #pragma unroll
             for (int i = 0; i < NC / 2; ++i) pend[k][i] = pack2(0.f, 0.f);
         uint32_t nx[U][NW], nd[U][NW];
+        const T *xp = xs + (int64_t)t0 * p.x_st, *dp_ = ds + (int64_t)t0 * p.do_st;  // the next loads' rows
+        T *op = dx + (int64_t)(t0 - (W - 1)) * p.D;                                   // of the next dx
         auto fetch = [&](int t) {
+            if (t + U <= t2) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (t + u < t2) {
-                    ld_row<T, NC, VEC>(nx[u], xs + (int64_t)(t + u) * p.x_st, n);
-                    ld_row<T, NC, VEC>(nd[u], ds + (int64_t)(t + u) * p.do_st, n);
+                for (int u = 0; u < U; ++u, xp += p.x_st, dp_ += p.do_st) {
+                    ld_row<T, NC, VEC>(nx[u], xp, n);
+                    ld_row<T, NC, VEC>(nd[u], dp_, n);
                 }
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u, xp += p.x_st, dp_ += p.do_st)
+                    if (t + u < t2) {
+                        ld_row<T, NC, VEC>(nx[u], xp, n);
+                        ld_row<T, NC, VEC>(nd[u], dp_, n);
+                    }
+            }
         };
         fetch(t0);
+        // one token: own, its dw and db count; s0, its sequence's first token
+        auto token = [&](int t, const uint32_t (&rx)[NW], const uint32_t (&rd)[NW], bool own, bool whole) {
+            f32x2 x[NC / 2], go[NC / 2], dp[NC / 2];
+            words_to_pairs<T, NC>(x, rx);
+            words_to_pairs<T, NC>(go, rd);
+            dpre<NC, W>(dp, w, bias, win, x, go, p.silu);
+            if (own) {
+#pragma unroll
+                for (int i = 0; i < NC / 2; ++i) {
+                    db[i] = add2(db[i], dp[i]);
+                    dw[W - 1][i] = fma2(dp[i], x[i], dw[W - 1][i]);
+#pragma unroll
+                    for (int k = 1; k < W; ++k) dw[W - 1 - k][i] = fma2(dp[i], win[k - 1][i], dw[W - 1 - k][i]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < W; ++k)
+                if (whole || t - k >= q.s0) {
+#pragma unroll
+                    for (int i = 0; i < NC / 2; ++i) pend[k][i] = fma2(w[W - 1 - k][i], dp[i], pend[k][i]);
+                }
+            push<NC, W>(win, x);
+        };
+        auto shift = [&] {
+#pragma unroll
+            for (int k = W - 1; k > 0; --k)
+#pragma unroll
+                for (int i = 0; i < NC / 2; ++i) pend[k][i] = pend[k - 1][i];
+#pragma unroll
+            for (int i = 0; i < NC / 2; ++i) pend[0][i] = pack2(0.f, 0.f);
+        };
+        // slow: a few tokens from tb on, of any sequences
+        auto slow = [&](int tb, const uint32_t (&rx)[U][NW], const uint32_t (&rd)[U][NW]) {
+#pragma unroll 1
+            for (int u = 0; u < U; ++u) {
+                const int t = tb + u;
+                uint32_t cx[NW], cd[NW];
+#pragma unroll
+                for (int i = 0; i < NW; ++i) {
+                    cx[i] = u == 0 ? rx[0][i] : u == 1 ? rx[1][i] : u == 2 ? rx[2][i] : rx[3][i];
+                    cd[i] = u == 0 ? rd[0][i] : u == 1 ? rd[1][i] : u == 2 ? rd[2][i] : rd[3][i];
+                }
+                shift();
+                if (t < t2) {
+                    if (t == q.s1) {
+                        next_seq(q, p.cu, p.n_seq, t);
+                        load_window<T, NC, W, VEC>(win, p, xs, t, q, c, n);
+                    }
+                    if (p.dfinal && t < t1 && t >= q.s1 - (W - 1)) {
+                        uint32_t raw[NW];
+                        ld_row<T, NC, VEC>(
+                            raw, (const T *)p.dfinal + ((int64_t)q.seg * (W - 1) + t - (q.s1 - (W - 1))) * p.D + c, n);
+                        words_to_pairs<T, NC>(pend[0], raw);
+                    }
+                    token(t, cx, cd, t < t1, false);
+                }
+                const int done = t - (W - 1);
+                if (done >= t0 && done < t1) st_pairs<T, NC, VEC>(op, pend[W - 1], n);
+                op += p.D;
+            }
+        };
         for (int tb = t0; tb < t1 + W - 1; tb += U) {
             uint32_t rx[U][NW], rd[U][NW];
 #pragma unroll
@@ -321,50 +421,26 @@ __global__ void __launch_bounds__(32 * kConvYBwd) conv_bwd_kernel(const ConvPara
 #pragma unroll
                 for (int i = 0; i < NW; ++i) rx[u][i] = nx[u][i], rd[u][i] = nd[u][i];
             fetch(tb + U);
+            // without a branch: tokens that, with the W - 1 before and after them, are one sequence's
+            const bool inside = tb - (W - 1) >= q.s0;
+            if (inside && tb + U <= t1 && tb + U <= q.s1 - (W - 1)) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int t = tb + u;
-#pragma unroll
-                for (int k = W - 1; k > 0; --k)
-#pragma unroll
-                    for (int i = 0; i < NC / 2; ++i) pend[k][i] = pend[k - 1][i];
-#pragma unroll
-                for (int i = 0; i < NC / 2; ++i) pend[0][i] = pack2(0.f, 0.f);
-                if (t < t2) {
-                    if (t == q.s1) {
-                        next_seq(q, p.cu, p.n_seq, t);
-                        load_window<T, NC, W, VEC>(win, p, xs, t, q, c, n);
-                    }
-                    f32x2 x[NC / 2], go[NC / 2], dp[NC / 2];
-                    words_to_pairs<T, NC>(x, rx[u]);
-                    words_to_pairs<T, NC>(go, rd[u]);
-                    dpre<NC, W>(dp, w, bias, win, x, go, p.silu);
-                    if (t < t1) {
-#pragma unroll
-                        for (int i = 0; i < NC / 2; ++i) {
-                            db[i] = add2(db[i], dp[i]);
-                            dw[W - 1][i] = fma2(dp[i], x[i], dw[W - 1][i]);
-#pragma unroll
-                            for (int k = 1; k < W; ++k) dw[W - 1 - k][i] = fma2(dp[i], win[k - 1][i], dw[W - 1 - k][i]);
-                        }
-                        if (p.dfinal && t >= q.s1 - (W - 1)) {
-                            uint32_t raw[NW];
-                            ld_row<T, NC, VEC>(
-                                raw,
-                                (const T *)p.dfinal + ((int64_t)q.seg * (W - 1) + t - (q.s1 - (W - 1))) * p.D + c, n);
-                            words_to_pairs<T, NC>(pend[0], raw);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < W; ++k)
-                        if (t - k >= q.s0) {
-#pragma unroll
-                            for (int i = 0; i < NC / 2; ++i) pend[k][i] = fma2(w[W - 1 - k][i], dp[i], pend[k][i]);
-                        }
-                    push<NC, W>(win, x);
+                for (int u = 0; u < U; ++u) {
+                    shift();
+                    token(tb + u, rx[u], rd[u], true, true);
+                    if (u >= W - 1 || tb + u - (W - 1) >= t0) st_pairs<T, NC, VEC>(op, pend[W - 1], n);
+                    op += p.D;
                 }
-                const int done = t - (W - 1);
-                if (done >= t0 && done < t1) st_pairs<T, NC, VEC>(dx + (int64_t)done * p.D, pend[W - 1], n);
+            } else if (W - 1 <= U && inside && tb == t1 && t2 == t1 + W - 1 && t2 <= q.s1) {  // the run's last
+#pragma unroll
+                for (int u = 0; u < (W - 1 < U ? W - 1 : U); ++u) {
+                    shift();
+                    token(tb + u, rx[u], rd[u], false, true);
+                    st_pairs<T, NC, VEC>(op, pend[W - 1], n);
+                    op += p.D;
+                }
+            } else {
+                slow(tb, rx, rd);
             }
         }
     }
@@ -423,8 +499,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvStepParams p) 
     if (p.silu) {
 #pragma unroll
         for (int i = 0; i < NC / 2; ++i) {
-            const float2 g = sigmoid2(unpack2(a[i]));
-            a[i] = mul2(a[i], pack2(g.x, g.y));
+            a[i] = mul2(a[i], sigmoid_pair(a[i]));
         }
     }
     st_pairs<T, NC, VEC>(out, a, n);
@@ -447,7 +522,7 @@ cudaError_t by_taps(int W, F &&f) {
 
 template <typename T>
 cudaError_t conv_t(const ConvParams &p, cudaStream_t st) {
-    constexpr int NC = 16 / sizeof(T);
+    constexpr int NC = 4;
     // Tokens a thread: 32, where W - 1 more inputs are read for each run, or down
     // to 8 while that leaves SMs without a CTA.
     int run = 32;

@@ -254,6 +254,7 @@ struct SsmStepParams {
     int64_t o_st;
     int n, n_slots, D, N, softplus, bf16;
     int n_wide;  // rows of A and of the states are 16-byte aligned
+    int bc_vec;  // rows of B and C are, in whole vectors of four
 };
 cudaError_t launch_ssm_step(const SsmStepParams &p, cudaStream_t st);
 

@@ -402,9 +402,10 @@ gdn_status gdn_ssm_step(const void *x, int64_t x_st, const void *dt, int64_t dt_
     r.add(dt, dtype, 0, dt_st);
     r.add(z, dtype, 0, z_st);
     r.add(out, dtype, 0, out_st);
-    r.add(bm, dtype, 0, bm_st);
-    r.add(cm, dtype, 0, cm_st);
-    if (!r.ok || !f32_ok(A) || !f32_ok(Dv) || !f32_ok(dt_bias) || !f32_ok(state) || !f32_ok(slots))
+    Rows bc;
+    bc.add(bm, dtype, 0, bm_st, 4 * elem_size(dtype));
+    bc.add(cm, dtype, 0, cm_st, 4 * elem_size(dtype));
+    if (!r.ok || !bc.ok || !f32_ok(A) || !f32_ok(Dv) || !f32_ok(dt_bias) || !f32_ok(state) || !f32_ok(slots))
         return GDN_ERR_LAYOUT;
     if (n == 0) return GDN_OK;
     SsmStepParams p{};
@@ -412,6 +413,7 @@ gdn_status gdn_ssm_step(const void *x, int64_t x_st, const void *dt, int64_t dt_
     p.x_st = x_st, p.dt_st = dt_st, p.bm_st = bm_st, p.cm_st = cm_st, p.z_st = z_st;
     p.A = A, p.Dv = Dv, p.dt_bias = dt_bias, p.state = state, p.slots = slots, p.out = out, p.o_st = out_st;
     p.n_wide = N % 4 == 0 && addr(A) % 16 == 0 && addr(state) % 16 == 0;
+    p.bc_vec = bc.wide && N % 4 == 0;
     p.n = n, p.n_slots = n_slots, p.D = D, p.N = N, p.softplus = flags & GDN_SOFTPLUS, p.bf16 = dtype == GDN_BF16;
     return cuda_status(launch(KSsmStep, stream, [&] { return launch_ssm_step(p, stream); }));
 }

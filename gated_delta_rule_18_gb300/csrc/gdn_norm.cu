@@ -11,19 +11,13 @@
 // (a row belongs to tpr threads of one CTA, 8 channels a vector, nv vectors
 // a thread), the row's sum crosses warps once through shared memory, and the
 // result is written once. Sums, the norm and the scales are fp32.
-#include "gdn_layer.cuh"
+#include "gdn_ssm.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kVecN = 8;
+constexpr int kVecN = 8, kPairs = kVecN / 2;
 
-// maximum that keeps NaN, as the comparison with a NaN has to show in the scale
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
 // two fp32 to two e4m3 (round to nearest even, finite values saturate)
 __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
     uint16_t r;
@@ -35,32 +29,70 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
 // value; one reciprocal and a correction of the quotient by its remainder
 // round the same (|y| <= 448 scale (1 + 2^-24), no intermediate overflows
 // unless the scale itself is out of range, where the plain quotient is taken).
-__device__ __forceinline__ void quantise(float (&y)[kVecN], float scale) {
-    const float dv = scale == 0.f ? 1.f : scale, r = 1.f / dv;
-    const bool safe = dv > 1e-30f && dv < 1e30f;
+__device__ __forceinline__ void quantise(f32x2 (&y)[kPairs], float scale) {
+    const float dv = scale == 0.f ? 1.f : scale;
+    if (dv > 1e-30f && dv < 1e30f) {
+        const float r = 1.f / dv;
+        const f32x2 r2 = pack2(r, r), n2 = pack2(-dv, -dv);
 #pragma unroll
-    for (int j = 0; j < kVecN; ++j) {
-        const float q = y[j] * r;
-        y[j] = safe ? fmaf(fmaf(-q, dv, y[j]), r, q) : y[j] / dv;
+        for (int j = 0; j < kPairs; ++j) {
+            const f32x2 q = mul2(y[j], r2);
+            y[j] = fma2(fma2(q, n2, y[j]), r2, q);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            const float2 f = unpack2(y[j]);
+            y[j] = pack2(f.x / dv, f.y / dv);
+        }
     }
 }
 
-// Threads a row and vectors a thread: one vector a thread up to 512 threads.
+// Threads a row (32 to 512) for so many vectors a thread, and rows a CTA.
 struct RowShape {
     int tpr, nv, rpb;
 };
-RowShape row_shape(int D, int max_tpr) {
+RowShape row_shape(int D, int vectors) {
     const int vecs = (D + kVecN - 1) / kVecN;
     RowShape s;
     s.tpr = 32;
-    while (s.tpr < max_tpr && s.tpr < vecs) s.tpr *= 2;
+    while (s.tpr < 512 && s.tpr * vectors < vecs) s.tpr *= 2;
     s.nv = 1;
     while (s.nv * s.tpr < vecs) s.nv *= 2;
     s.rpb = s.tpr >= 128 ? 1 : 128 / s.tpr;
     return s;
 }
 
-// the row's sum (or NaN-keeping maximum) over its warps; red: a float a warp
+template <typename T>
+__device__ __forceinline__ void words_to_pairs(f32x2 (&v)[kPairs], const uint32_t (&w)[RowVec<T, kVecN>::kWords]) {
+    float f[kVecN];
+    words_to_f<T, kVecN>(f, w);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) v[i] = pack2(f[2 * i], f[2 * i + 1]);
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void st_pairs(T *p, const f32x2 (&v)[kPairs], int n) {
+    float f[kVecN];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        const float2 x = unpack2(v[i]);
+        f[2 * i] = x.x, f[2 * i + 1] = x.y;
+    }
+    st_row_f<T, kVecN, VEC>(p, f, n);
+}
+// the weights of a thread's vectors
+template <int NV, bool VEC>
+__device__ __forceinline__ void ld_weights(f32x2 (&w)[NV][kPairs], const float *weight, int tpr, int tid, int D) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + tid) * kVecN;
+        uint32_t u[kVecN] = {};
+        if (c < D) ld_row<float, kVecN, VEC>(u, weight + c, D - c);
+        words_to_pairs<float>(w[i], u);
+    }
+}
+
+// the row's sum (or NaN-keeping maximum) over its warps; red: 16 floats, one a warp
 template <bool MAX>
 __device__ __forceinline__ float row_reduce(float v, float *red, int tpr) {
 #pragma unroll
@@ -72,8 +104,12 @@ __device__ __forceinline__ float row_reduce(float v, float *red, int tpr) {
     const int warp = threadIdx.x >> 5, wpr = tpr >> 5, w0 = warp & ~(wpr - 1);
     if ((threadIdx.x & 31) == 0) red[warp] = v;
     __syncthreads();
-    v = red[w0];
-    for (int i = 1; i < wpr; ++i) v = MAX ? max_nan(v, red[w0 + i]) : v + red[w0 + i];
+    if (wpr == 2) return MAX ? max_nan(red[w0], red[w0 + 1]) : red[w0] + red[w0 + 1];
+    v = MAX ? 0.f : 0.f;
+    for (int i = 0; i < wpr; i += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(red + w0 + i);
+        v = MAX ? max_nan(v, max_nan(max_nan(f.x, f.y), max_nan(f.z, f.w))) : v + ((f.x + f.y) + (f.z + f.w));
+    }
     return v;
 }
 
@@ -81,7 +117,7 @@ __device__ __forceinline__ float row_reduce(float v, float *red, int tpr) {
 // PRE: the next row's loads are issued before this row's sum is known.
 template <typename TX, typename TR, bool Q8, int NV, bool VEC, bool PRE>
 __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormParams p, int tpr) {
-    __shared__ float red[2][2][16];
+    __shared__ __align__(16) float red[2][2][16];
     constexpr int WX = RowVec<TX, kVecN>::kWords, WR = RowVec<TR, kVecN>::kWords;
     const int rpb = blockDim.x / tpr, lr = threadIdx.x / tpr, tid = threadIdx.x - lr * tpr;
     const int64_t step = (int64_t)gridDim.x * rpb;
@@ -102,59 +138,56 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormParams p, int tp
         }
     };
     fetch(row);
-    float w[NV][kVecN];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + tid) * kVecN;
-#pragma unroll
-        for (int j = 0; j < kVecN; ++j) w[i][j] = 0.f;
-        if (c < p.D) ld_row_f<float, kVecN, VEC>(w[i], p.weight + c, p.D - c);
-    }
+    f32x2 w[NV][kPairs];
+    ld_weights<NV, VEC>(w, p.weight, tpr, tid, p.D);
     const int groups = p.group > 0 ? (p.D + p.group - 1) / p.group : 1;
+    const float rd = 1.f / (float)p.D;
     int flip = 0;
     // every thread of the CTA makes the same number of turns
     for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < p.R; r0 += step, row += step, flip ^= 1) {
         const bool live = row < p.R;
-        float s[NV][kVecN];
-        float sum = 0.f;
+        f32x2 s[NV][kPairs], sum2 = pack2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + tid) * kVecN;
-            words_to_f<TX, kVecN>(s[i], nx[i]);
+            words_to_pairs<TX>(s[i], nx[i]);
             if (p.res) {
-                float r[kVecN];
-                words_to_f<TR, kVecN>(r, nr[i]);
+                f32x2 r[kPairs];
+                words_to_pairs<TR>(r, nr[i]);
 #pragma unroll
-                for (int j = 0; j < kVecN; ++j) s[i][j] += r[j];
-                if (live && c < p.D) st_row_f<TR, kVecN, VEC>((TR *)p.res_out + row * p.ro_st + c, s[i], p.D - c);
+                for (int j = 0; j < kPairs; ++j) s[i][j] = add2(s[i][j], r[j]);
+                if (live && c < p.D) st_pairs<TR, VEC>((TR *)p.res_out + row * p.ro_st + c, s[i], p.D - c);
             }
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) sum2 = fma2(s[i][j], s[i][j], sum2);
         }
         if (PRE) fetch(row + step);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < kVecN; ++j) sum = fmaf(s[i][j], s[i][j], sum);
-        sum = row_reduce<false>(sum, red[flip][0], tpr);
-        const float inv = rsqrtf(sum / (float)p.D + p.eps);
+        const float2 su = unpack2(sum2);
+        const float sum = row_reduce<false>(su.x + su.y, red[flip][0], tpr);
+        const float inv = rsqrtf(sum * rd + p.eps);
+        const f32x2 inv2 = pack2(inv, inv);
         float row_max = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + tid) * kVecN;
             const bool in = live && c < p.D;
 #pragma unroll
-            for (int j = 0; j < kVecN; ++j) s[i][j] = s[i][j] * inv * w[i][j];
+            for (int j = 0; j < kPairs; ++j) s[i][j] = mul2(mul2(s[i][j], inv2), w[i][j]);
             if constexpr (!Q8) {
-                if (in) st_row_f<TX, kVecN, VEC>((TX *)p.out + row * p.o_st + c, s[i], p.D - c);
+                if (in) st_pairs<TX, VEC>((TX *)p.out + row * p.o_st + c, s[i], p.D - c);
             } else {
                 float m = 0.f;
 #pragma unroll
-                for (int j = 0; j < kVecN; ++j) m = max_nan(m, fabsf(s[i][j]));
+                for (int j = 0; j < kPairs; ++j) {
+                    const float2 f = unpack2(s[i][j]);
+                    m = max_nan(m, max_nan(fabsf(f.x), fabsf(f.y)));
+                }
                 row_max = max_nan(row_max, m);
                 if (p.group > 0) {
                     // a group's vectors sit in group / 8 neighbouring lanes
                     for (int o = p.group / kVecN / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
                     const float sc = m / 448.f;
-                    if (in && c % p.group == 0) p.scale[row * groups + c / p.group] = sc;
+                    if (in && (c & (p.group - 1)) == 0) p.scale[row * groups + c / p.group] = sc;
                     quantise(s[i], sc);
                 }
             }
@@ -172,8 +205,10 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormParams p, int tp
                 if (!(live && c < p.D)) continue;
                 uint32_t q[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    q[j] = pack_e4m3(s[i][4 * j], s[i][4 * j + 1]) | pack_e4m3(s[i][4 * j + 2], s[i][4 * j + 3]) << 16;
+                for (int j = 0; j < 2; ++j) {
+                    const float2 a = unpack2(s[i][2 * j]), b = unpack2(s[i][2 * j + 1]);
+                    q[j] = pack_e4m3(a.x, a.y) | pack_e4m3(b.x, b.y) << 16;
+                }
                 uint8_t *o = (uint8_t *)p.out + row * p.o_st + c;
                 if constexpr (VEC) {
                     st_words(o, q);
@@ -197,18 +232,16 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormParams p, int tp
 // PRE: the next row's loads are issued before this row's sum is known.
 template <typename TS, typename TY, int NV, bool VEC, bool PRE>
 __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdParams p, int tpr) {
-    __shared__ float red[2][2][16];
+    __shared__ __align__(16) float red[2][2][16];
     constexpr int WS = RowVec<TS, kVecN>::kWords, WY = RowVec<TY, kVecN>::kWords;
     const int rpb = blockDim.x / tpr;
     const int lr = threadIdx.x / tpr, tid = threadIdx.x - lr * tpr;
-    float dw[NV][kVecN], w[NV][kVecN];
+    f32x2 dw[NV][kPairs], w[NV][kPairs];
+    ld_weights<NV, VEC>(w, p.weight, tpr, tid, p.D);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + tid) * kVecN;
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < kVecN; ++j) dw[i][j] = 0.f, w[i][j] = 0.f;
-        if (c < p.D) ld_row_f<float, kVecN, VEC>(w[i], p.weight + c, p.D - c);
-    }
+        for (int j = 0; j < kPairs; ++j) dw[i][j] = pack2(0.f, 0.f);
     const int64_t step = (int64_t)gridDim.x * rpb;
     int64_t row = (int64_t)blockIdx.x * rpb + lr;
     uint32_t ns[NV][WS], ny[NV][WY], nr[NV][WS];
@@ -243,81 +276,98 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdParams p,
             for (int j = 0; j < WY; ++j) ry[i][j] = ny[i][j];
         }
         if (PRE) fetch(row + step);
-        float ss = 0.f, gs = 0.f;
+        f32x2 ss2 = pack2(0.f, 0.f), gs2 = ss2;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float s[kVecN], g[kVecN];
-            words_to_f<TS, kVecN>(s, rs[i]);
-            words_to_f<TY, kVecN>(g, ry[i]);
+            f32x2 s[kPairs], g[kPairs];
+            words_to_pairs<TS>(s, rs[i]);
+            words_to_pairs<TY>(g, ry[i]);
 #pragma unroll
-            for (int j = 0; j < kVecN; ++j) {
-                ss += __fmul_rn(s[j], s[j]);
-                gs += __fmul_rn(g[j] * w[i][j], s[j]);
+            for (int j = 0; j < kPairs; ++j) {
+                ss2 = fma2(s[j], s[j], ss2);
+                gs2 = fma2(mul2(g[j], w[i][j]), s[j], gs2);
             }
         }
-        ss = warp_sum(ss), gs = warp_sum(gs);
+        const float2 sa = unpack2(ss2), ga = unpack2(gs2);
+        float ss = warp_sum(sa.x + sa.y), gs = warp_sum(ga.x + ga.y);
         if (tpr > 32) {
             const int warp = threadIdx.x >> 5, wpr = tpr >> 5, w0 = warp & ~(wpr - 1);
             if ((threadIdx.x & 31) == 0) red[flip][0][warp] = ss, red[flip][1][warp] = gs;
             __syncthreads();
-            ss = red[flip][0][w0], gs = red[flip][1][w0];
-            for (int i = 1; i < wpr; ++i) ss += red[flip][0][w0 + i], gs += red[flip][1][w0 + i];
+            if (wpr == 2) {
+                ss = red[flip][0][w0] + red[flip][0][w0 + 1], gs = red[flip][1][w0] + red[flip][1][w0 + 1];
+            } else {
+                ss = gs = 0.f;
+                for (int i = 0; i < wpr; i += 4) {
+                    const float4 a = *reinterpret_cast<const float4 *>(red[flip][0] + w0 + i);
+                    const float4 b = *reinterpret_cast<const float4 *>(red[flip][1] + w0 + i);
+                    ss += (a.x + a.y) + (a.z + a.w), gs += (b.x + b.y) + (b.z + b.w);
+                }
+            }
         }
         const float inv = rsqrtf(ss * rd + p.eps);
         const float k = inv * inv * rd, ke = p.eps * inv * inv;
+        const f32x2 k2 = pack2(k, k), ke2 = pack2(ke, ke), inv2 = pack2(inv, inv);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + tid) * kVecN;
             if (!(row < p.R && c < p.D)) continue;
-            float s[kVecN], g[kVecN], o[kVecN];
-            words_to_f<TS, kVecN>(s, rs[i]);
-            words_to_f<TY, kVecN>(g, ry[i]);
+            f32x2 s[kPairs], g[kPairs], o[kPairs];
+            words_to_pairs<TS>(s, rs[i]);
+            words_to_pairs<TY>(g, ry[i]);
             if (p.dres) {
-                words_to_f<TS, kVecN>(o, rr[i]);
+                words_to_pairs<TS>(o, rr[i]);
             } else {
 #pragma unroll
-                for (int j = 0; j < kVecN; ++j) o[j] = 0.f;
+                for (int j = 0; j < kPairs; ++j) o[j] = pack2(0.f, 0.f);
             }
 #pragma unroll
-            for (int j = 0; j < kVecN; ++j) {
-                const float gw = g[j] * w[i][j];
-                const float rest = gw * (ss - __fmul_rn(s[j], s[j])) - s[j] * (gs - __fmul_rn(gw, s[j]));
-                o[j] += inv * fmaf(k, rest, ke * gw);
-                dw[i][j] = fmaf(g[j], s[j] * inv, dw[i][j]);
+            for (int j = 0; j < kPairs; ++j) {
+                // products rounded as in the sums and not fused, as packed ones may be: a lone
+                // channel's cancel to zero
+                const f32x2 gw = mul2(g[j], w[i][j]);
+                const float2 sf = unpack2(s[j]), gf = unpack2(gw);
+                const f32x2 so = pack2(__fsub_rn(ss, __fmul_rn(sf.x, sf.x)), __fsub_rn(ss, __fmul_rn(sf.y, sf.y)));
+                const f32x2 go = pack2(__fsub_rn(__fmul_rn(gf.x, sf.x), gs), __fsub_rn(__fmul_rn(gf.y, sf.y), gs));
+                const f32x2 rest = fma2(gw, so, mul2(s[j], go));
+                o[j] = fma2(inv2, fma2(k2, rest, mul2(ke2, gw)), o[j]);
+                dw[i][j] = fma2(g[j], mul2(s[j], inv2), dw[i][j]);
             }
-            st_row_f<TS, kVecN, VEC>((TS *)p.dx + row * p.dx_st + c, o, p.D - c);
+            st_pairs<TS, VEC>((TS *)p.dx + row * p.dx_st + c, o, p.D - c);
         }
     }
     float *part = p.part + ((int64_t)blockIdx.x * rpb + lr) * p.D;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + tid) * kVecN;
-        if (c < p.D) st_row_f<float, kVecN, VEC>(part + c, dw[i], p.D - c);
+        if (c < p.D) st_pairs<float, VEC>(part + c, dw[i], p.D - c);
     }
 }
 
-// 32 columns a CTA, 8 threads a column.
-__global__ void __launch_bounds__(256) col_sum_kernel(const float *in, int64_t ld, int parts, int64_t n, float *out,
-                                                      int64_t n2, float *out2) {
-    __shared__ float red[8][33];
+// 32 columns a CTA, Y threads a column.
+template <int Y>
+__global__ void __launch_bounds__(32 * Y) col_sum_kernel(const float *in, int64_t ld, int parts, int64_t n, float *out,
+                                                         int64_t n2, float *out2) {
+    __shared__ float red[Y][33];
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + x;
     float a = 0.f;
-    if (c < n + n2)
-        for (int p = y; p < parts; p += 8) a += in[p * ld + c];
+    if (c < n + n2) {
+#pragma unroll 4
+        for (int p = y; p < parts; p += Y) a += in[p * ld + c];
+    }
     red[y][x] = a;
     __syncthreads();
     if (y == 0 && c < n + n2) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) a += red[i][x];
-        float *o = c < n ? out + c : out2 + (c - n);
-        *o = a;
+        for (int i = 1; i < Y; ++i) a += red[i][x];
+        *(c < n ? out + c : out2 + (c - n)) = a;
     }
 }
 
 template <typename TX, typename TR, bool Q8>
 cudaError_t norm_nv(const NormParams &p, cudaStream_t st) {
-    const RowShape s = row_shape(p.D, 512);
+    const RowShape s = row_shape(p.D, 1);
     const unsigned nt = s.tpr * s.rpb, need = (unsigned)((p.R + s.rpb - 1) / s.rpb);
     const unsigned most = 152 * (1024 / nt), grid = need < most ? need : most;
     if (!p.vec) {
@@ -333,14 +383,14 @@ cudaError_t norm_nv(const NormParams &p, cudaStream_t st) {
 }
 template <typename TS, typename TY>
 cudaError_t norm_bwd_nv(const NormBwdParams &p, cudaStream_t st) {
-    const RowShape s = row_shape(p.D, 512);
+    const RowShape s = row_shape(p.D, 2);
     const unsigned grid = norm_bwd_parts(p.R, p.D) / s.rpb, nt = s.tpr * s.rpb;
     if (!p.vec) {
         rmsnorm_bwd_kernel<TS, TY, 4, false, false><<<grid, nt, 0, st>>>(p, s.tpr);
     } else if (s.nv == 1) {
         rmsnorm_bwd_kernel<TS, TY, 1, true, true><<<grid, nt, 0, st>>>(p, s.tpr);
     } else if (s.nv == 2) {
-        rmsnorm_bwd_kernel<TS, TY, 2, true, false><<<grid, nt, 0, st>>>(p, s.tpr);
+        rmsnorm_bwd_kernel<TS, TY, 2, true, true><<<grid, nt, 0, st>>>(p, s.tpr);
     } else {
         rmsnorm_bwd_kernel<TS, TY, 4, true, false><<<grid, nt, 0, st>>>(p, s.tpr);
     }
@@ -362,7 +412,7 @@ cudaError_t launch_rmsnorm(const NormParams &p, cudaStream_t st) {
 
 // Rows of partial sums: at most four CTAs a SM, each rpb rows at a time.
 int norm_bwd_parts(int R, int D) {
-    const RowShape s = row_shape(D, 512);
+    const RowShape s = row_shape(D, 2);
     const int need = (int)(((int64_t)R + s.rpb - 1) / s.rpb);
     return (need < 608 ? need : 608) * s.rpb;
 }
@@ -376,7 +426,10 @@ cudaError_t launch_rmsnorm_bwd(const NormBwdParams &p, cudaStream_t st) {
 cudaError_t launch_col_sum(const float *in, int64_t ld, int parts, int64_t n, float *out, int64_t n2, float *out2,
                            cudaStream_t st) {
     if (n + n2 <= 0) return cudaSuccess;
-    col_sum_kernel<<<(unsigned)((n + n2 + 31) / 32), 256, 0, st>>>(in, ld, parts, n, out, n2, out2);
+    // few columns over hundreds of parts are bound by the loads' latency: more threads a column
+    const unsigned grid = (unsigned)((n + n2 + 31) / 32);
+    if (grid < 152) col_sum_kernel<32><<<grid, 1024, 0, st>>>(in, ld, parts, n, out, n2, out2);
+    else col_sum_kernel<8><<<grid, 256, 0, st>>>(in, ld, parts, n, out, n2, out2);
     return cudaGetLastError();
 }
 

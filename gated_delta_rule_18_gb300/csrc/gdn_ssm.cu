@@ -252,78 +252,97 @@ __global__ void __launch_bounds__(256) ssm_chain_kernel(const SsmParams p, int n
 }
 
 // One token of each request: the state is read, updated and written back, all
-// that counts. Four states a lane, LN lanes a channel, two channels a lane (of
-// the halves of the CTA's range) so that two states' loads are under way.
+// that counts. LN lanes a channel with four states each, four channels a lane
+// (8 states' loads under way); of a lane's four channels lane ln forms delta
+// and the gate of channel ln % 4 and finishes it. Channel 8 k + lc of the
+// warp's is a lane's k-th where LN = 4, so that every access runs over
+// neighbouring channels.
 template <typename T, int LN>
 __global__ void __launch_bounds__(128) ssm_step_kernel(const SsmStepParams p) {
-    constexpr int CH = 128 / LN;
-    const int i = blockIdx.y, n0 = threadIdx.x % LN * 4;
+    constexpr int CL = 32 / LN, CW = 4 * CL;
+    const int i = blockIdx.y, lane = threadIdx.x & 31, ln = lane % LN, lc = lane / LN, n0 = ln * 4;
     const int64_t slot = p.slots ? p.slots[i] : i;
-    const bool real = slot >= 0 && slot < p.n_slots;
-    int d[2];
-    float h[2][4], a[2][4], x[2], dl[2], z[2] = {0.f, 0.f}, b[4], c[4];
+    const int c0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * CW + lc, dm = c0 + (ln & 3) * CL;
+    T *out = (T *)p.out + i * p.o_st;
+    if (slot < 0 || slot >= p.n_slots) {  // a padding row
+        if (ln < 4 && dm < p.D) out[dm] = to_type<T>(0.f);
+        return;
+    }
+    float *state = p.state + slot * p.D * p.N;
+    float h[4][4], a[4][4], b[4], c[4];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        d[k] = (blockIdx.x * 2 + k) * CH + threadIdx.x / LN;
-        const bool on = real && d[k] < p.D && n0 < p.N;
-        const int64_t own = (int64_t)d[k] * p.N + n0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            h[k][j] = a[k][j] = 0.f;
-            if (!p.n_wide && on && n0 + j < p.N) {
-                h[k][j] = p.state[slot * p.D * p.N + own + j];
-                a[k][j] = p.A[own + j];
-            }
-        }
-        if (p.n_wide && on) {
-            const float4 u = *reinterpret_cast<const float4 *>(p.state + slot * p.D * p.N + own);
-            const float4 v = __ldg(reinterpret_cast<const float4 *>(p.A + own));
+    for (int k = 0; k < 4; ++k) {
+        const int d = c0 + k * CL;
+        const bool on = d < p.D && n0 < p.N;
+        const int64_t own = (int64_t)d * p.N + n0;
+        if (p.n_wide) {
+            const float4 u = on ? *reinterpret_cast<const float4 *>(state + own) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 v = on ? __ldg(reinterpret_cast<const float4 *>(p.A + own)) : make_float4(0.f, 0.f, 0.f, 0.f);
             h[k][0] = u.x, h[k][1] = u.y, h[k][2] = u.z, h[k][3] = u.w;
             a[k][0] = v.x, a[k][1] = v.y, a[k][2] = v.z, a[k][3] = v.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[k][j] = on && n0 + j < p.N ? state[own + j] : 0.f;
+                a[k][j] = on && n0 + j < p.N ? p.A[own + j] : 0.f;
+            }
         }
-        const bool in = real && d[k] < p.D;
-        x[k] = in ? ldf((const T *)p.x + i * p.x_st + d[k]) : 0.f;
-        dl[k] = in ? ldf((const T *)p.dt + i * p.dt_st + d[k]) + (p.dt_bias ? p.dt_bias[d[k]] : 0.f) : 0.f;
-        if (in && p.z) z[k] = ldf((const T *)p.z + i * p.z_st + d[k]);
     }
+    const T *bm = (const T *)p.bm + i * p.bm_st + n0, *cm = (const T *)p.cm + i * p.cm_st + n0;
+    if (p.bc_vec && n0 < p.N) {
+        ld_row_f<T, 4, true>(b, bm, 4);
+        ld_row_f<T, 4, true>(c, cm, 4);
+    } else {
+        ld_row_f<T, 4, false>(b, bm, p.N - n0);
+        ld_row_f<T, 4, false>(c, cm, p.N - n0);
+    }
+    float x = 0.f, dl = 0.f, z = 0.f, dv = 0.f;
+    if (dm < p.D) {
+        x = ldf((const T *)p.x + i * p.x_st + dm);
+        dl = ldf((const T *)p.dt + i * p.dt_st + dm);
+        if (p.z) z = ldf((const T *)p.z + i * p.z_st + dm);
+        if (p.dt_bias) dl += p.dt_bias[dm];
+        if (p.Dv) dv = p.Dv[dm];
+    }
+    if (p.softplus) dl = softplus2(make_float2(dl, dl)).x;
+    const float u = dl * x, dk = dl * kLog2e;
+    float y[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const bool on = n0 + j < p.N;
-        b[j] = on ? ldf((const T *)p.bm + i * p.bm_st + n0 + j) : 0.f;
-        c[j] = on ? ldf((const T *)p.cm + i * p.cm_st + n0 + j) : 0.f;
-    }
-    if (p.softplus) {
-        const float2 v = softplus2(make_float2(dl[0], dl[1]));
-        dl[0] = v.x, dl[1] = v.y;
-    }
-    const float2 g = sigmoid2(make_float2(z[0], z[1]));
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const float u = dl[k] * x[k], dk = dl[k] * kLog2e;
-        float y = 0.f;
+    for (int k = 0; k < 4; ++k) {
+        const int from = lane - (ln & 3) + k;  // the lane of this group of four that has channel k
+        const float dks = __shfl_sync(0xffffffffu, dk, from), us = __shfl_sync(0xffffffffu, u, from);
+        y[k] = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            h[k][j] = fmaf(ex2f(dk * a[k][j]), h[k][j], u * b[j]);
-            y = fmaf(h[k][j], c[j], y);
+            h[k][j] = fmaf(ex2f(dks * a[k][j]), h[k][j], us * b[j]);
+            y[k] = fmaf(h[k][j], c[j], y[k]);
         }
-        if (real && d[k] < p.D && n0 < p.N) {
-            float *state = p.state + (slot * p.D + d[k]) * p.N + n0;
+        const int d = c0 + k * CL;
+        const int64_t own = (int64_t)d * p.N + n0;
+        if (d < p.D && n0 < p.N) {
             if (p.n_wide) {
-                *reinterpret_cast<float4 *>(state) = make_float4(h[k][0], h[k][1], h[k][2], h[k][3]);
+                *reinterpret_cast<float4 *>(state + own) = make_float4(h[k][0], h[k][1], h[k][2], h[k][3]);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (n0 + j < p.N) state[j] = h[k][j];
+                    if (n0 + j < p.N) state[own + j] = h[k][j];
             }
         }
-#pragma unroll
-        for (int o = LN / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-        if (d[k] < p.D && n0 == 0) {
-            if (p.Dv) y = fmaf(p.Dv[d[k]], x[k], y);
-            if (p.z) y *= z[k] * (k ? g.y : g.x);
-            ((T *)p.out)[i * p.o_st + d[k]] = to_type<T>(real ? y : 0.f);  // a padding row is zero
-        }
     }
+    // the four sums over the lanes of a channel, one to each of four lanes
+#pragma unroll
+    for (int o = LN / 2; o >= 4; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] += __shfl_xor_sync(0xffffffffu, y[k], o);
+    const bool l1 = ln & 1, l2 = ln & 2;
+    const float g0 = l2 ? y[0] : y[2], g1 = l2 ? y[1] : y[3];
+    float k0 = l2 ? y[2] : y[0], k1 = l2 ? y[3] : y[1];
+    k0 += __shfl_xor_sync(0xffffffffu, g0, 2), k1 += __shfl_xor_sync(0xffffffffu, g1, 2);
+    const float g2 = l1 ? k0 : k1;
+    float r = (l1 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, g2, 1);
+    r = fmaf(dv, x, r);
+    if (p.z) r *= z * rcpf(1.f + ex2f(z * -kLog2e));
+    if (ln < 4 && dm < p.D) out[dm] = to_type<T>(r);
 }
 
 template <typename T, int Q, int LN, bool SUM>
@@ -390,7 +409,8 @@ cudaError_t launch_ssm_scan(const SsmParams &p, cudaStream_t st) {
 }
 cudaError_t launch_ssm_step(const SsmStepParams &p, cudaStream_t st) {
     return by_lanes(p.N, [&](auto ln) {
-        const dim3 grid((p.D + 256 / ln() - 1) / (256 / ln()), p.n);
+        const int cw = 4 * (32 / ln()) * 4;  // channels a CTA
+        const dim3 grid((p.D + cw - 1) / cw, p.n);
         if (p.bf16) ssm_step_kernel<__nv_bfloat16, ln()><<<grid, 128, 0, st>>>(p);
         else ssm_step_kernel<float, ln()><<<grid, 128, 0, st>>>(p);
         return cudaGetLastError();
