@@ -17,6 +17,7 @@ import torch
 
 F32, BF16, E4M3 = 0, 1, 2
 SILU = SOFTPLUS = 1
+_F8 = torch.float8_e4m3fn
 _CODE = {torch.float32: F32, torch.bfloat16: BF16}
 _P, _I, _L, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _lib = None
@@ -65,17 +66,24 @@ def _code(t, name):
     return c
 
 
+def _wrong(t, name, shape, like):
+    """Raises what is wrong with an activation."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != like.dtype:
+        _fail(3, f"{name} must be {like.dtype} as x is, got {t.dtype}")
+    _fail(4, f"{name} must be on {like.device} with a contiguous last dimension")
+
+
 def _act(t, name, shape, like):
     """(pointer, stride over B, stride over T) of an activation; zeros for None."""
     if t is None:
         return 0, 0, 0
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != like.dtype:
-        _fail(3, f"{name} must be {like.dtype} as x is, got {t.dtype}")
+    if t.shape != shape or t.dtype is not like.dtype or t.get_device() != like.get_device():
+        _wrong(t, name, shape, like)
     sb, st, sd = t.stride()
-    if (sd != 1 and shape[2] > 1) or t.device != like.device:
-        _fail(4, f"{name} must be on {like.device} with a contiguous last dimension")
+    if sd != 1 and shape[2] > 1:
+        _wrong(t, name, shape, like)
     return t.data_ptr(), sb, st
 
 
@@ -83,13 +91,11 @@ def _rows(t, name, shape, like):
     """(pointer, row stride) of a (n, D) tensor; zeros for None."""
     if t is None:
         return 0, 0
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != like.dtype:
-        _fail(3, f"{name} must be {like.dtype} as x is, got {t.dtype}")
+    if t.shape != shape or t.dtype is not like.dtype or t.get_device() != like.get_device():
+        _wrong(t, name, shape, like)
     st, sd = t.stride()
-    if (sd != 1 and shape[1] > 1) or t.device != like.device:
-        _fail(4, f"{name} must be on {like.device} with a contiguous last dimension")
+    if sd != 1 and shape[1] > 1:
+        _wrong(t, name, shape, like)
     return t.data_ptr(), st
 
 
@@ -101,7 +107,7 @@ def _flat(t, name, shape, dtype, like):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         _fail(3, f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous() or t.device != like.device:
+    if not t.is_contiguous() or t.get_device() != like.get_device():
         _fail(4, f"{name} must be contiguous on {like.device}")
     return t.data_ptr()
 
@@ -124,8 +130,15 @@ def _workspace(workspace, need, like):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _stream():
-    return torch.cuda.current_stream().cuda_stream
+# The current stream's handle without building a Stream object (3 us of host
+# time, more than a small call's kernel takes), where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(like):
+    if _raw_stream is not None:
+        return _raw_stream(like.get_device())
+    return torch.cuda.current_stream(like.device).cuda_stream
 
 
 def _as_rows(t, name):
@@ -150,15 +163,14 @@ def gdn_rmsnorm_fwd(x, weight, residual=None, eps=1e-6, out_dtype=None, group=0,
             return gdn_rmsnorm_fwd(x, weight, residual, eps, out_dtype, group, out, residual_out)
     L = _lib or _load()
     _on_gpu(x)
-    lead, D = x.shape[:-1], x.shape[-1]
-    x2 = _as_rows(x, "x")
-    R = x2.shape[0]
-    q8 = out_dtype is not None and out_dtype == torch.float8_e4m3fn
+    x2 = x if x.dim() == 2 else _as_rows(x, "x")
+    R, D = x2.shape
+    q8 = out_dtype is _F8
     if out_dtype is not None and not q8 and out_dtype != x.dtype:
         _fail(3, f"out_dtype must be {x.dtype} or torch.float8_e4m3fn, got {out_dtype}")
     ty = out_dtype if q8 else x.dtype
     if out is None:
-        out = torch.empty(x.shape, dtype=ty, device=x.device)
+        out = torch.empty_like(x, dtype=ty, memory_format=torch.contiguous_format)
     elif out.shape != x.shape or out.dtype != ty:
         raise ValueError(f"out must be {tuple(x.shape)} {ty}, got {tuple(out.shape)} {out.dtype}")
     o2 = _as_rows(out, "out")
@@ -169,21 +181,23 @@ def gdn_rmsnorm_fwd(x, weight, residual=None, eps=1e-6, out_dtype=None, group=0,
     if residual is not None:
         rc = _code(residual, "residual")
         if residual_out is None:
-            residual_out = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
+            residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
         elif residual_out.shape != x.shape or residual_out.dtype != residual.dtype:
             raise ValueError(f"residual_out must be {tuple(x.shape)} {residual.dtype}")
+        if residual.shape != x.shape:
+            raise ValueError(f"residual must have shape {tuple(x.shape)}, got {tuple(residual.shape)}")
         rp, rs = _rows(_as_rows(residual, "residual"), "residual", (R, D), residual)
         rop, ros = _rows(_as_rows(residual_out, "residual_out"), "residual_out", (R, D), residual)
-        if residual.device != x.device:
+        if residual.get_device() != x.get_device():
             _fail(4, f"residual must be on {x.device}")
         res["residual"] = residual_out
     if q8:
-        scale = torch.empty(lead + ((D + group - 1) // group if group > 0 else 1,), dtype=torch.float32,
+        scale = torch.empty(x.shape[:-1] + ((D + group - 1) // group if group > 0 else 1,), dtype=torch.float32,
                             device=x.device)
         res["scale"] = scale
         sp = scale.data_ptr()
     st = L.gdn_rmsnorm_fwd(xp, xs, _code(x, "x"), rp, rs, rc, _flat(weight, "weight", (D,), torch.float32, x), op, os_,
-                           E4M3 if q8 else _CODE[ty], rop, ros, sp, R, D, group, eps, _stream())
+                           E4M3 if q8 else _CODE[ty], rop, ros, sp, R, D, group, eps, _stream(x))
     if st:
         _fail(st, "gdn_rmsnorm_fwd")
     return res
@@ -212,7 +226,7 @@ def gdn_rmsnorm_bwd(s, weight, dy, dres=None, eps=1e-6, workspace=None, stream=N
     ws, wp, wn = _workspace(workspace, L.gdn_rmsnorm_bwd_workspace_size(R, D), s)
     st = L.gdn_rmsnorm_bwd(sp, ss, _code(s, "s"), yp, ys, _code(dy, "dy"), rp, rs,
                            _flat(weight, "weight", (D,), torch.float32, s), dx.data_ptr(), D, dw.data_ptr(), R, D,
-                           eps, wp, wn, _stream())
+                           eps, wp, wn, _stream(s))
     if st:
         _fail(st, "gdn_rmsnorm_bwd")
     return {"dx": dx, "dweight": dw}
@@ -241,7 +255,7 @@ def gdn_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, fina
                         _flat(bias, "bias", (D,), torch.float32, x),
                         _flat(initial_state, "initial_state", (n, W - 1, D), x.dtype, x), cp, n,
                         *_act(out, "out", (B, T, D), x), _flat(final_state, "final_state", (n, W - 1, D), x.dtype, x),
-                        B, T, D, _code(x, "x"), SILU if silu else 0, wp, wn, _stream())
+                        B, T, D, _code(x, "x"), SILU if silu else 0, wp, wn, _stream(x))
     if st:
         _fail(st, "gdn_conv_fwd")
     return out
@@ -275,7 +289,7 @@ def gdn_conv_bwd(x, weight, dout, bias=None, initial_state=None, cu_seqlens=None
                         _flat(initial_state, "initial_state", (n, W - 1, D), x.dtype, x), cp, n,
                         *_act(dout, "dout", (B, T, D), x),
                         _flat(dfinal_state, "dfinal_state", (n, W - 1, D), x.dtype, x), r["dx"].data_ptr(),
-                        r["dweight"].data_ptr(), bp, ip, B, T, D, _code(x, "x"), SILU if silu else 0, wp, wn, _stream())
+                        r["dweight"].data_ptr(), bp, ip, B, T, D, _code(x, "x"), SILU if silu else 0, wp, wn, _stream(x))
     if st:
         _fail(st, "gdn_conv_bwd")
     return r
@@ -300,7 +314,7 @@ def gdn_conv_step(x, state, weight, bias=None, slots=None, silu=True, out=None, 
                          _flat(bias, "bias", (D,), torch.float32, x),
                          _flat(state, "state", (pool, W - 1, D), x.dtype, x),
                          _flat(slots, "slots", (n,), torch.int32, x), pool, *_rows(out, "out", (n, D), x), n, D,
-                         _code(x, "x"), SILU if silu else 0, _stream())
+                         _code(x, "x"), SILU if silu else 0, _stream(x))
     if st:
         _fail(st, "gdn_conv_step")
     return out
@@ -330,7 +344,7 @@ def gdn_ssm_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_softplus=True
                        *_act(z, "z", (B, T, C), x), _flat(dt_bias, "dt_bias", (C,), f, x),
                        _flat(h0, "h0", (n, C, N), f, x), cp, n, *_act(out, "out", (B, T, C), x),
                        _flat(h_final, "h_final", (n, C, N), f, x), B, T, C, N, _code(x, "x"),
-                       SOFTPLUS if dt_softplus else 0, wp, wn, _stream())
+                       SOFTPLUS if dt_softplus else 0, wp, wn, _stream(x))
     if st:
         _fail(st, "gdn_ssm_fwd")
     return out
@@ -372,7 +386,7 @@ def gdn_ssm_bwd(x, dt, A, Bm, Cm, dout, D=None, z=None, dt_bias=None, dt_softplu
                        _flat(h0, "h0", (n, C, N), f, x), cp, n, *_act(dout, "dout", (B, T, C), x),
                        _flat(dh_final, "dh_final", (n, C, N), f, x), ptr("dx"), ptr("ddt"), ptr("dA"), ptr("dBm"),
                        ptr("dCm"), ptr("dD"), ptr("dz"), ptr("ddt_bias"), ptr("dh0"), B, T, C, N, _code(x, "x"),
-                       SOFTPLUS if dt_softplus else 0, wp, wn, _stream())
+                       SOFTPLUS if dt_softplus else 0, wp, wn, _stream(x))
     if st:
         _fail(st, "gdn_ssm_bwd")
     return r
@@ -398,7 +412,7 @@ def gdn_ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, dt_softp
                         *_rows(z, "z", (n, C), x), _flat(dt_bias, "dt_bias", (C,), f, x),
                         _flat(state, "state", (pool, C, N), f, x), _flat(slots, "slots", (n,), torch.int32, x), pool,
                         *_rows(out, "out", (n, C), x), n, C, N, _code(x, "x"), SOFTPLUS if dt_softplus else 0,
-                        _stream())
+                        _stream(x))
     if st:
         _fail(st, "gdn_ssm_step")
     return out
