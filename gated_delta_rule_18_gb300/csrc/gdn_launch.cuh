@@ -16,7 +16,7 @@ enum Kind {
     KFrameOut, KSegSummary, KSegCombine, KBwdDh, KBwdDq, KBwdDk, KSum, KF32Prep, KF32Serial, KFused,
     KFrameXt, KFrameLam, KFrameTok, KPrepBwd, KMergeBwd, KBwdF32Scan, KBwdF32Reduce, KNorm, KNormBwd,
     KColSum, KConv, KConvBwd, KConvStep, KSsmSum, KSsmChain, KSsmScan, KSsmBwdSum, KSsmBwdChain,
-    KSsmBwd, KSsmBwdReduce, KSsmBwdEmpty, KSsmStep, KNumKinds
+    KSsmBwd, KSsmBwdReduce, KSsmStep, KNumKinds
 };
 inline const char *kind_name(int kind) {
     static const char *const names[KNumKinds] = {
@@ -25,7 +25,7 @@ inline const char *kind_name(int kind) {
         "f32_prep", "f32_serial", "fused_tc", "frame_xt", "frame_lam", "frame_tokgrad", "prep_bwd",
         "merge_bwd", "bwd_f32_scan", "bwd_f32_reduce", "rmsnorm", "rmsnorm_bwd", "col_sum", "conv",
         "conv_bwd", "conv_step", "ssm_sum", "ssm_chain", "ssm_scan", "ssm_bwd_sum", "ssm_bwd_chain",
-        "ssm_bwd", "ssm_bwd_reduce", "ssm_bwd_empty", "ssm_step"};
+        "ssm_bwd", "ssm_bwd_reduce", "ssm_step"};
     return names[kind];
 }
 

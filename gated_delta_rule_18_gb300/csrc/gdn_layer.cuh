@@ -83,24 +83,54 @@ __device__ __forceinline__ void f_to_words(uint32_t (&w)[RowVec<T, N>::kWords], 
         for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
     }
 }
+// Whole vectors of 16-bit elements that start on any element: words where the
+// address allows, else an element, N / 2 - 1 words and an element.
+template <int N>
+__device__ __forceinline__ void ld_half_row(uint32_t (&w)[N / 2], const unsigned short *e) {
+    if ((reinterpret_cast<uintptr_t>(e) & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) w[i] = reinterpret_cast<const uint32_t *>(e)[i];
+    } else {
+        uint32_t m[N / 2 + 1];
+        m[0] = (uint32_t)e[0] << 16;
+#pragma unroll
+        for (int i = 0; i < N / 2 - 1; ++i) m[i + 1] = reinterpret_cast<const uint32_t *>(e + 1)[i];
+        m[N / 2] = e[N - 1];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) w[i] = __funnelshift_l(m[i], m[i + 1], 16);
+    }
+}
+template <int N>
+__device__ __forceinline__ void st_half_row(unsigned short *e, const uint32_t (&w)[N / 2]) {
+    if ((reinterpret_cast<uintptr_t>(e) & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) reinterpret_cast<uint32_t *>(e)[i] = w[i];
+    } else {
+        e[0] = (unsigned short)w[0];
+#pragma unroll
+        for (int i = 0; i < N / 2 - 1; ++i) reinterpret_cast<uint32_t *>(e + 1)[i] = __funnelshift_l(w[i], w[i + 1], 16);
+        e[N - 1] = (unsigned short)(w[N / 2 - 1] >> 16);
+    }
+}
 // raw load: zeros past n in the element form
 template <typename T, int N, bool VEC>
 __device__ __forceinline__ void ld_row(uint32_t (&w)[RowVec<T, N>::kWords], const T *p, int n) {
     if constexpr (VEC) {
         ld_words(w, p);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = i < n ? __float_as_uint(static_cast<const float *>(p)[i]) : 0u;
     } else {
-#pragma unroll
-        for (int i = 0; i < RowVec<T, N>::kWords; ++i) w[i] = 0u;
-        if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (i < n) w[i] = __float_as_uint(static_cast<const float *>(p)[i]);
-        } else {
-            const unsigned short *e = reinterpret_cast<const unsigned short *>(p);
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (i < n) w[i >> 1] |= (uint32_t)e[i] << (16 * (i & 1));
+        const unsigned short *e = reinterpret_cast<const unsigned short *>(p);
+        if (n >= N) {
+            ld_half_row<N>(w, e);
+            return;
         }
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) w[i] = 0u;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) w[i >> 1] |= (uint32_t)e[i] << (16 * (i & 1));
     }
 }
 template <typename T, int N, bool VEC>
@@ -118,9 +148,14 @@ __device__ __forceinline__ void st_row(T *p, const uint32_t (&w)[RowVec<T, N>::k
         for (int i = 0; i < N; ++i)
             if (i < n) reinterpret_cast<uint32_t *>(p)[i] = w[i];
     } else {
+        unsigned short *e = reinterpret_cast<unsigned short *>(p);
+        if (n >= N) {
+            st_half_row<N>(e, w);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (i < n) reinterpret_cast<unsigned short *>(p)[i] = (unsigned short)(w[i >> 1] >> (16 * (i & 1)));
+            if (i < n) e[i] = (unsigned short)(w[i >> 1] >> (16 * (i & 1)));
     }
 }
 template <typename T, int N, bool VEC>
@@ -241,7 +276,6 @@ int ssm_bwd_tiles(int D, int N);
 int ssm_bwd_run(int lines, int T, int D, int N);
 cudaError_t launch_ssm_bwd_sum(const SsmParams &p, cudaStream_t st);
 cudaError_t launch_ssm_bwd_chain(const SsmParams &p, cudaStream_t st);
-cudaError_t launch_ssm_bwd_empty(const SsmParams &p, cudaStream_t st);
 cudaError_t launch_ssm_bwd(const SsmParams &p, cudaStream_t st);
 cudaError_t launch_ssm_bwd_reduce(const SsmParams &p, cudaStream_t st);
 struct SsmStepParams {

@@ -367,23 +367,12 @@ gdn_status gdn_ssm_bwd(const void *x, int64_t x_sb, int64_t x_st, const void *dt
     auto run = [&](int kind, cudaError_t (*f)(const SsmParams &, cudaStream_t)) {
         if (e == cudaSuccess) e = launch(kind, stream, [&] { return f(p, stream); });
     };
-    auto sum = [&](const float *in, int64_t ld, int64_t n, float *out, int64_t n2, float *out2) {
-        if (e == cudaSuccess)
-            e = launch(KColSum, stream, [&] {
-                return launch_col_sum(in, ld, (cu_seqlens ? 1 : B) * L.nrun, n, out, n2, out2, stream);
-            });
-    };
-    if (T > 0) {
+    if (L.ngroup > 1) {  // one group's entering state and gradient are h0 and dh_final
         run(KSsmBwdSum, launch_ssm_bwd_sum);
         run(KSsmBwdChain, launch_ssm_bwd_chain);
-        run(KSsmBwd, launch_ssm_bwd);
-        run(KSsmBwdReduce, launch_ssm_bwd_reduce);
     }
-    if (dh0 && (cu_seqlens || T == 0)) run(KSsmBwdEmpty, launch_ssm_bwd_empty);
-    const int64_t dn = (int64_t)D * N;
-    sum(p.part_a, dn, dn, dA, 0, nullptr);
-    if (dD) sum(p.part_d, 2 * D, D, dD, ddt_bias ? D : 0, ddt_bias);
-    else if (ddt_bias) sum(p.part_d + D, 2 * D, D, ddt_bias, 0, nullptr);
+    if (T > 0) run(KSsmBwd, launch_ssm_bwd);
+    run(KSsmBwdReduce, launch_ssm_bwd_reduce);
     return cuda_status(e);
 }
 

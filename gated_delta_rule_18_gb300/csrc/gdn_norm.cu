@@ -370,30 +370,28 @@ cudaError_t norm_nv(const NormParams &p, cudaStream_t st) {
     const RowShape s = row_shape(p.D, 1);
     const unsigned nt = s.tpr * s.rpb, need = (unsigned)((p.R + s.rpb - 1) / s.rpb);
     const unsigned most = 152 * (1024 / nt), grid = need < most ? need : most;
-    if (!p.vec) {
-        rmsnorm_kernel<TX, TR, Q8, 4, false, false><<<grid, nt, 0, st>>>(p, s.tpr);
-    } else if (s.nv == 1) {
-        rmsnorm_kernel<TX, TR, Q8, 1, true, true><<<grid, nt, 0, st>>>(p, s.tpr);
-    } else if (s.nv == 2) {
-        rmsnorm_kernel<TX, TR, Q8, 2, true, true><<<grid, nt, 0, st>>>(p, s.tpr);
-    } else {
-        rmsnorm_kernel<TX, TR, Q8, 4, true, false><<<grid, nt, 0, st>>>(p, s.tpr);
-    }
+    auto run = [&](auto vec) {
+        constexpr bool V = decltype(vec)::value;
+        if (s.nv == 1) rmsnorm_kernel<TX, TR, Q8, 1, V, true><<<grid, nt, 0, st>>>(p, s.tpr);
+        else if (s.nv == 2) rmsnorm_kernel<TX, TR, Q8, 2, V, true><<<grid, nt, 0, st>>>(p, s.tpr);
+        else rmsnorm_kernel<TX, TR, Q8, 4, V, false><<<grid, nt, 0, st>>>(p, s.tpr);
+    };
+    if (p.vec) run(std::true_type());
+    else run(std::false_type());
     return cudaGetLastError();
 }
 template <typename TS, typename TY>
 cudaError_t norm_bwd_nv(const NormBwdParams &p, cudaStream_t st) {
     const RowShape s = row_shape(p.D, 2);
     const unsigned grid = norm_bwd_parts(p.R, p.D) / s.rpb, nt = s.tpr * s.rpb;
-    if (!p.vec) {
-        rmsnorm_bwd_kernel<TS, TY, 4, false, false><<<grid, nt, 0, st>>>(p, s.tpr);
-    } else if (s.nv == 1) {
-        rmsnorm_bwd_kernel<TS, TY, 1, true, true><<<grid, nt, 0, st>>>(p, s.tpr);
-    } else if (s.nv == 2) {
-        rmsnorm_bwd_kernel<TS, TY, 2, true, true><<<grid, nt, 0, st>>>(p, s.tpr);
-    } else {
-        rmsnorm_bwd_kernel<TS, TY, 4, true, false><<<grid, nt, 0, st>>>(p, s.tpr);
-    }
+    auto run = [&](auto vec) {
+        constexpr bool V = decltype(vec)::value;
+        if (s.nv == 1) rmsnorm_bwd_kernel<TS, TY, 1, V, true><<<grid, nt, 0, st>>>(p, s.tpr);
+        else if (s.nv == 2) rmsnorm_bwd_kernel<TS, TY, 2, V, true><<<grid, nt, 0, st>>>(p, s.tpr);
+        else rmsnorm_bwd_kernel<TS, TY, 4, V, false><<<grid, nt, 0, st>>>(p, s.tpr);
+    };
+    if (p.vec) run(std::true_type());
+    else run(std::false_type());
     return cudaGetLastError();
 }
 

@@ -102,15 +102,28 @@ __global__ void __launch_bounds__(kThreads, 6) ssm_scan_kernel(const SsmParams p
 
     const T *src[3] = {(const T *)p.x + line * p.x_sb, (const T *)p.dt + line * p.dt_sb, (const T *)p.z + line * p.z_sb};
     const int64_t str[3] = {p.x_st, p.dt_st, p.z_st};
-    auto fetch = [&](int s, int b) {  // the stage that begins at token s into buffer b
+    // The stage that begins at token s into buffer b: by asynchronous copies two
+    // stages ahead, or through registers one stage ahead.
+    auto tile_at = [&](int b, int a) { return reinterpret_cast<T *>(smem + b * kBuf + a * kTile); };
+    auto copy = [&](int s, int b) {
         if (s < t1) {
 #pragma unroll
             for (int a = 0; a < NA; ++a)
                 if (a < 2 || gate)
-                    ssm_fetch_tile<T, CH, TS, kThreads>(reinterpret_cast<T *>(smem + b * kBuf + a * kTile),
-                                                        src[a] + s * str[a], str[a], t1 - s, c0, p.D, vec);
+                    ssm_copy_tile<T, CH, TS, kThreads>(tile_at(b, a), src[a] + s * str[a], str[a], t1 - s, c0, p.D);
         }
         cp_async_commit();
+    };
+    SsmTile<T, CH, TS, kThreads> held[USUAL ? 1 : NA];
+    auto hold = [&](int s) {
+#pragma unroll
+        for (int a = 0; a < (USUAL ? 0 : NA); ++a)
+            if (a < 2 || gate) held[a].load(src[a] + s * str[a], str[a], t1 - s, c0, p.D);
+    };
+    auto release = [&](int b) {
+#pragma unroll
+        for (int a = 0; a < (USUAL ? 0 : NA); ++a)
+            if (a < 2 || gate) held[a].store(tile_at(b, a));
     };
     const T *bg = (const T *)p.bm + line * p.bm_sb, *cg = (const T *)p.cm + line * p.cm_sb;
     SsmBc<T, NP, TS, kThreads> nbc;
@@ -118,8 +131,13 @@ __global__ void __launch_bounds__(kThreads, 6) ssm_scan_kernel(const SsmParams p
         nbc.template fetch<!SUM>(bg + s * p.bm_st, p.bm_st, cg + s * p.cm_st, p.cm_st, t1 - s, p.N, p.bc_vec);
     };
     if (t0 < t1) {
-        fetch(t0, 0);
-        fetch(t0 + TS, 1);
+        if (vec) {
+            copy(t0, 0);
+            copy(t0 + TS, 1);
+        } else {
+            hold(t0);
+            release(0);
+        }
         fetch_bc(t0);
     }
     f32x2 dsum = pack2(0.f, 0.f);
@@ -128,7 +146,8 @@ __global__ void __launch_bounds__(kThreads, 6) ssm_scan_kernel(const SsmParams p
         float *bc = bcs + buf * kBc;
         nbc.stage(bc);
         if (s + TS < t1) fetch_bc(s + TS);
-        cp_async_wait<1>();
+        if (vec) cp_async_wait<1>();
+        else if (s + TS < t1) hold(s + TS);
         __syncthreads();
         const int m = min(t1 - s, TS);
         const T *xs = reinterpret_cast<const T *>(smem + buf * kBuf) + ch;
@@ -206,7 +225,8 @@ __global__ void __launch_bounds__(kThreads, 6) ssm_scan_kernel(const SsmParams p
             }
         }
         __syncthreads();  // the buffer has been read
-        fetch(s + 2 * TS, buf);
+        if (vec) copy(s + 2 * TS, buf);
+        else if (s + TS < t1) release(buf ^ 1);
     }
     if (SUM) {
         st_across<Q>(p.sums + ((int64_t)line * nch + chunk) * dnp + own_p, h, NP, Q, true, on);

@@ -132,27 +132,42 @@ __device__ __forceinline__ void ssm_check_cu(const int32_t *cu, int n_seq, int T
 
 // ------------------------------------------------------------ staging -------
 // `rows` rows of CH channels from channel c0 on into shared memory (row
-// stride CH), by 16-byte asynchronous copies or, for rows that are not
-// aligned, by element. Channels past D and rows past `rows` are zeros (a
-// pair's halves share a reciprocal, a warp's channels the sums of dB and dC).
-// NT threads take part.
+// stride CH), by 16-byte asynchronous copies. Channels past D and rows past
+// `rows` are zeros (a pair's halves share a reciprocal, a warp's channels the
+// sums of dB and dC). NT threads take part.
 template <typename T, int CH, int TS, int NT>
-__device__ __forceinline__ void ssm_fetch_tile(T *dst, const T *src, int64_t stride, int rows, int c0, int D, bool vec) {
+__device__ __forceinline__ void ssm_copy_tile(T *dst, const T *src, int64_t stride, int rows, int c0, int D) {
     constexpr int VE = 16 / sizeof(T), kCopies = TS * CH / VE;
-    if (vec) {
 #pragma unroll
-        for (int i = 0; i < (kCopies + NT - 1) / NT; ++i) {
-            const int e = threadIdx.x + i * NT, r = e / (CH / VE), c = e % (CH / VE) * VE;
-            const bool in = r < rows && c0 + c < D;
-            if (kCopies % NT == 0 || e < kCopies) cp_async16(dst + r * CH + c, in ? src + r * stride + c0 + c : src, in ? 16 : 0);
-        }
-    } else {
-        for (int e = threadIdx.x; e < TS * CH; e += NT) {
-            const int r = e / CH, c = e % CH;
-            dst[e] = r < rows && c0 + c < D ? src[r * stride + c0 + c] : to_type<T>(0.f);
-        }
+    for (int i = 0; i < (kCopies + NT - 1) / NT; ++i) {
+        const int e = threadIdx.x + i * NT, r = e / (CH / VE), c = e % (CH / VE) * VE;
+        const bool in = r < rows && c0 + c < D;
+        if (kCopies % NT == 0 || e < kCopies) cp_async16(dst + r * CH + c, in ? src + r * stride + c0 + c : src, in ? 16 : 0);
     }
 }
+// The same for rows that start on any element: loaded into registers, by
+// pairs of channels, and stored when their place is free.
+template <typename T, int CH, int TS, int NT>
+struct SsmTile {
+    static constexpr int kPairs = TS * CH / 2, kLoads = (kPairs + NT - 1) / NT, KW = RowVec<T, 2>::kWords;
+    uint32_t w[kLoads][KW];
+    __device__ __forceinline__ void load(const T *src, int64_t stride, int rows, int c0, int D) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int e = threadIdx.x + i * NT, r = e / (CH / 2), c = c0 + e % (CH / 2) * 2;
+#pragma unroll
+            for (int k = 0; k < KW; ++k) w[i][k] = 0u;
+            if ((kPairs % NT == 0 || e < kPairs) && r < rows && c < D) ld_row<T, 2, false>(w[i], src + r * stride + c, D - c);
+        }
+    }
+    __device__ __forceinline__ void store(T *dst) const {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int e = threadIdx.x + i * NT;
+            if (kPairs % NT == 0 || e < kPairs) st_row<T, 2, true>(dst + 2 * e, w[i], 2);
+        }
+    }
+};
 // The (B, C) rows of TS tokens, [TS][2][NP] fp32 in shared memory: loaded as
 // stored into registers by fetch, converted where they are staged.
 template <typename T, int NP, int TS, int NT>

@@ -16,7 +16,7 @@
 //                 time, the four tokens' entering states and decays in
 //                 registers;
 //   ssm_bwd_reduce  dB and dC over the channel tiles; dA, dD and dbias over
-//                 the runs (col_sum). No atomics: every sum has one order.
+//                 the runs. Every sum has one order.
 // Bound by instruction issue and the fp32 pipe: the states' decays are formed
 // three times (12 cycles an element on the exponential unit) and the walk back
 // has ten packed operations an element pair.
@@ -45,7 +45,6 @@ __global__ void __launch_bounds__(kNT, 8) ssm_bwd_sum_kernel(const SsmParams p, 
     const int tid = threadIdx.x, lane = tid & 31, pr = tid / LN, ch = 2 * pr, ln = tid % LN;
     const int tile = blockIdx.x % ntile, item = blockIdx.x / ntile;
     const int line = item / p.nrun, run = item - line * p.nrun;
-    if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
     const int t0 = run * p.rlen, t1 = min(p.T - t0, p.rlen) + t0;
     const int c0 = tile * CH, d = c0 + ch, n0 = ln * Q, nn = p.N - n0;
     const bool on[2] = {d < p.D && nn > 0, d + 1 < p.D && nn > 0};
@@ -77,23 +76,40 @@ __global__ void __launch_bounds__(kNT, 8) ssm_bwd_sum_kernel(const SsmParams p, 
     const T *src[4] = {(const T *)p.x + line * p.x_sb, (const T *)p.dt + line * p.dt_sb,
                        (const T *)p.z + line * p.z_sb, (const T *)p.dout + line * p.do_sb};
     const int64_t str[4] = {p.x_st, p.dt_st, p.z_st, p.do_st};
-    auto fetch = [&](int s, int b) {
+    // as in the scan
+    auto tile_at = [&](int b, int a) { return reinterpret_cast<T *>(smem + b * kBuf + a * kTile); };
+    auto copy = [&](int s, int b) {
         if (s < t1) {
 #pragma unroll
             for (int a = 0; a < NA; ++a)
                 if (a != 2 || gate)
-                    ssm_fetch_tile<T, CH, TS, kNT>(reinterpret_cast<T *>(smem + b * kBuf + a * kTile),
-                                                   src[a] + s * str[a], str[a], t1 - s, c0, p.D, vec);
+                    ssm_copy_tile<T, CH, TS, kNT>(tile_at(b, a), src[a] + s * str[a], str[a], t1 - s, c0, p.D);
         }
         cp_async_commit();
+    };
+    SsmTile<T, CH, TS, kNT> held[USUAL ? 1 : NA];
+    auto hold = [&](int s) {
+#pragma unroll
+        for (int a = 0; a < (USUAL ? 0 : NA); ++a)
+            if (a != 2 || gate) held[a].load(src[a] + s * str[a], str[a], t1 - s, c0, p.D);
+    };
+    auto release = [&](int b) {
+#pragma unroll
+        for (int a = 0; a < (USUAL ? 0 : NA); ++a)
+            if (a != 2 || gate) held[a].store(tile_at(b, a));
     };
     const T *bg = (const T *)p.bm + line * p.bm_sb, *cg = (const T *)p.cm + line * p.cm_sb;
     SsmBc<T, NP, TS, kNT> nbc;
     auto fetch_bc = [&](int s) {
         nbc.template fetch<true>(bg + s * p.bm_st, p.bm_st, cg + s * p.cm_st, p.cm_st, t1 - s, p.N, p.bc_vec);
     };
-    fetch(t0, 0);
-    fetch(t0 + TS, 1);
+    if (vec) {
+        copy(t0, 0);
+        copy(t0 + TS, 1);
+    } else {
+        hold(t0);
+        release(0);
+    }
     fetch_bc(t0);
     float *gs = p.gs + ((int64_t)line * p.nrun + run) * dnp + own_p;
     float2 dsum = make_float2(0.f, 0.f);
@@ -102,7 +118,8 @@ __global__ void __launch_bounds__(kNT, 8) ssm_bwd_sum_kernel(const SsmParams p, 
         float *bc = bcs + buf * kBc;
         nbc.stage(bc);
         if (s + TS < t1) fetch_bc(s + TS);
-        cp_async_wait<1>();
+        if (vec) cp_async_wait<1>();
+        else if (s + TS < t1) hold(s + TS);
         __syncthreads();
         const int m = min(t1 - s, TS);
         // this warp's pairs of the stage
@@ -198,7 +215,8 @@ __global__ void __launch_bounds__(kNT, 8) ssm_bwd_sum_kernel(const SsmParams p, 
             }
         }
         __syncthreads();  // the buffer has been read
-        fetch(s + 2 * TS, buf);
+        if (vec) copy(s + 2 * TS, buf);
+        else if (s + TS < t1) release(buf ^ 1);
     }
     if (alive) st_pair<Q>(gs, g, NP, Q, true, on);
     if (!alive && ln == 0) {  // nothing crosses the run: marked by NaN
@@ -355,9 +373,16 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
         const int t0 = grp * TG, m = min(p.T - t0, TG);
         __syncthreads();  // the group before has been read
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k != 2 || gate)
-                ssm_fetch_tile<T, CH, TG, kWalk>(tiles + k * kTile, src[k] + t0 * str[k], str[k], m, c0, p.D, vec);
+        for (int k = 0; k < 4; ++k) {
+            if (k == 2 && !gate) continue;
+            if (vec) {
+                ssm_copy_tile<T, CH, TG, kWalk>(tiles + k * kTile, src[k] + t0 * str[k], str[k], m, c0, p.D);
+            } else {
+                SsmTile<T, CH, TG, kWalk> tile;
+                tile.load(src[k] + t0 * str[k], str[k], m, c0, p.D);
+                tile.store(tiles + k * kTile);
+            }
+        }
         cp_async_commit();
         {
             SsmBc<T, NP, TG, kWalk> bc;
@@ -602,26 +627,54 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
     }
 }
 
-// dB and dC: the channel tiles' partial sums, rounded once
+// What the walk left in parts, in one launch. The first nbc blocks: dB and dC
+// over the channel tiles, rounded once. The next nd: dA, dD and dbias over the
+// runs, 32 columns a block. The rest: without a token in a sequence its
+// state's gradient passes through.
 template <typename T>
-__global__ void __launch_bounds__(256) ssm_bwd_reduce_kernel(const SsmParams p, int tiles) {
-    const int64_t rows = (int64_t)p.B * p.T, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= rows * 2 * p.N) return;
-    float a = 0.f;
+__global__ void __launch_bounds__(256) ssm_bwd_reduce_kernel(const SsmParams p, int tiles, unsigned nbc, unsigned nd) {
+    __shared__ float red[8][33];
+    const int64_t dn = (int64_t)p.D * p.N;
+    if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
+    if (blockIdx.x < nbc) {
+        const int64_t rows = (int64_t)p.B * p.T, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+        if (i >= rows * 2 * p.N) return;
+        float a = 0.f;
 #pragma unroll 8
-    for (int k = 0; k < tiles; ++k) a += p.part_bc[k * rows * 2 * p.N + i];
-    const int64_t r = i / (2 * p.N);
-    const int n = (int)(i - r * 2 * p.N);
-    if (n < p.N) ((T *)p.dbm)[r * p.N + n] = to_type<T>(a);
-    else ((T *)p.dcm)[r * p.N + n - p.N] = to_type<T>(a);
-}
-
-// without a token in a sequence its state's gradient passes through
-__global__ void __launch_bounds__(256) ssm_bwd_empty_kernel(const SsmParams p) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, dn = (int64_t)p.D * p.N;
-    if (i >= dn) return;
-    for (int s = blockIdx.y; s < p.n_seq; s += gridDim.y)
-        if (p.cu ? p.cu[s + 1] <= p.cu[s] : p.T == 0) p.dh0[s * dn + i] = p.dh_final ? p.dh_final[s * dn + i] : 0.f;
+        for (int k = 0; k < tiles; ++k) a += p.part_bc[k * rows * 2 * p.N + i];
+        const int64_t r = i / (2 * p.N);
+        const int n = (int)(i - r * 2 * p.N);
+        if (n < p.N) ((T *)p.dbm)[r * p.N + n] = to_type<T>(a);
+        else ((T *)p.dcm)[r * p.N + n - p.N] = to_type<T>(a);
+    } else if (blockIdx.x < nbc + nd) {
+        const int x = threadIdx.x & 31, y = threadIdx.x >> 5, parts = (p.cu ? 1 : p.B) * p.nrun;
+        const int64_t c = (int64_t)(blockIdx.x - nbc) * 32 + x;  // a column of dA, then of dD, then of dbias
+        const bool in = c < dn + 2 * p.D;
+        const float *from = c < dn ? p.part_a + c : p.part_d + (c - dn);
+        const int64_t ld = c < dn ? dn : 2 * p.D;
+        float a = 0.f;
+        if (in) {
+#pragma unroll 4
+            for (int k = y; k < parts; k += 8) a += from[k * ld];
+        }
+        red[y][x] = a;
+        __syncthreads();
+        if (y > 0 || !in) return;
+#pragma unroll
+        for (int i = 1; i < 8; ++i) a += red[i][x];
+        if (c < dn) p.dA[c] = a;
+        else if (c < dn + p.D) {
+            if (p.dD) p.dD[c - dn] = a;
+        } else if (p.ddt_bias) {
+            p.ddt_bias[c - dn - p.D] = a;
+        }
+    } else {
+        const unsigned nb = gridDim.x - nbc - nd;
+        for (int64_t i = (int64_t)(blockIdx.x - nbc - nd) * 256 + threadIdx.x; i < dn; i += (int64_t)nb * 256)
+            for (int s = 0; s < p.n_seq; ++s)
+                if (p.cu ? p.cu[s + 1] <= p.cu[s] : p.T == 0)
+                    p.dh0[s * dn + i] = p.dh_final ? p.dh_final[s * dn + i] : 0.f;
+    }
 }
 
 template <typename T, int LN>
@@ -701,16 +754,14 @@ cudaError_t launch_ssm_bwd(const SsmParams &p, cudaStream_t st) {
     return f(I8(), I8());
 }
 cudaError_t launch_ssm_bwd_reduce(const SsmParams &p, cudaStream_t st) {
-    const int64_t n = (int64_t)p.B * p.T * 2 * p.N;
-    const unsigned grid = (unsigned)((n + 255) / 256);
+    const int64_t n = (int64_t)p.B * p.T * 2 * p.N, dn = (int64_t)p.D * p.N;
+    if (n / 256 > INT32_MAX / 2) return cudaErrorInvalidValue;
+    const unsigned nbc = (unsigned)((n + 255) / 256), nd = (unsigned)((dn + 2 * p.D + 31) / 32);
+    const bool empty = p.dh0 && (p.cu || p.T == 0);
+    const unsigned ne = empty ? (unsigned)((dn + 255) / 256 < 608 ? (dn + 255) / 256 : 608) : 0;
     const int tiles = ssm_bwd_tiles(p.D, p.N);
-    if (p.bf16) ssm_bwd_reduce_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p, tiles);
-    else ssm_bwd_reduce_kernel<float><<<grid, 256, 0, st>>>(p, tiles);
-    return cudaGetLastError();
-}
-cudaError_t launch_ssm_bwd_empty(const SsmParams &p, cudaStream_t st) {
-    const int64_t n = (int64_t)p.D * p.N;
-    ssm_bwd_empty_kernel<<<dim3((unsigned)((n + 255) / 256), p.n_seq < 64 ? p.n_seq : 64), 256, 0, st>>>(p);
+    if (p.bf16) ssm_bwd_reduce_kernel<__nv_bfloat16><<<nbc + nd + ne, 256, 0, st>>>(p, tiles, nbc, nd);
+    else ssm_bwd_reduce_kernel<float><<<nbc + nd + ne, 256, 0, st>>>(p, tiles, nbc, nd);
     return cudaGetLastError();
 }
 
