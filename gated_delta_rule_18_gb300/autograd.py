@@ -2,7 +2,8 @@
 
 Each function's forward runs the CUDA forward through the C ABI; its
 backward runs the matching gradient kernels (gdn_chunk_bwd, gdn_frame_bwd,
-gdn_merge_bwd, gdn_prep_bwd).
+gdn_merge_bwd, gdn_prep_bwd; of the state-space layer gdn_rmsnorm_bwd,
+gdn_conv_bwd, gdn_ssm_bwd).
 Nothing here computes on its own: the wrappers marshal tensors and sum the
 two directions' gradients.
 
@@ -16,6 +17,7 @@ import torch
 
 from . import (PREP_RELU, PREP_RMS, gdn_chunk_bwd, gdn_chunk_fwd, gdn_chunk_fwd_bidir, gdn_frame_bwd,
                gdn_frame_fwd, gdn_merge, gdn_merge_bwd, gdn_prep, gdn_prep_bwd)
+from .layer import (gdn_conv_bwd, gdn_conv_fwd, gdn_rmsnorm_bwd, gdn_rmsnorm_fwd, gdn_ssm_bwd, gdn_ssm_fwd)
 
 
 def _bf16(t):
@@ -149,3 +151,83 @@ def frame_video_gated_delta_rule(q, k, v, beta, g_frame, frame, gate=None, eps=1
     H)), and the merge num / (den + eps) * silu(gate). q, k, v (B, T, H, D)
     bf16 (views of an interleaved qkv tensor work); beta (B, T, H) fp32."""
     return _FrameVideo.apply(q, k, v, beta, g_frame, gate, int(frame), float(eps), float(prep_eps))
+
+
+class _RMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        r = gdn_rmsnorm_fwd(x, weight, residual=residual, eps=eps)
+        s = r.get("residual", x)
+        ctx.save_for_backward(s, weight)
+        ctx.eps, ctx.with_residual = eps, residual is not None
+        return r["out"], s if residual is not None else None
+
+    @staticmethod
+    def backward(ctx, dy, ds):
+        s, weight = ctx.saved_tensors
+        r = gdn_rmsnorm_bwd(s, weight, dy.contiguous(), dres=None if ds is None else ds.to(s.dtype).contiguous(),
+                            eps=ctx.eps)
+        return r["dx"].to(dy.dtype), r["dweight"], r["dx"] if ctx.with_residual else None, None
+
+
+def rms_norm(x, weight, residual=None, eps=1e-6):
+    """The norm in front of a mixer, differentiable in x, weight (fp32) and
+    residual: (y, s) with s = x + residual in the residual's type, the
+    residual stream that goes on (None without a residual). The gradient takes
+    s as stored."""
+    return _RMSNorm.apply(x, weight, residual, float(eps))
+
+
+class _CausalConv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, initial_state, cu_seqlens, silu, output_final_state):
+        n_seq = x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+        final = (torch.empty((n_seq, weight.shape[1] - 1, x.shape[2]), dtype=x.dtype, device=x.device)
+                 if output_final_state else None)
+        y = gdn_conv_fwd(x, weight, bias=bias, initial_state=initial_state, cu_seqlens=cu_seqlens, final_state=final,
+                         silu=silu)
+        ctx.save_for_backward(x, weight, bias, initial_state, cu_seqlens)
+        ctx.silu = silu
+        return y, final
+
+    @staticmethod
+    def backward(ctx, dy, dfinal):
+        x, weight, bias, initial_state, cu_seqlens = ctx.saved_tensors
+        r = gdn_conv_bwd(x, weight, dy.contiguous(), bias=bias, initial_state=initial_state, cu_seqlens=cu_seqlens,
+                         dfinal_state=None if dfinal is None else dfinal.contiguous(), silu=ctx.silu)
+        return r["dx"], r["dweight"], r.get("dbias"), r.get("dinitial_state"), None, None, None
+
+
+def causal_conv(x, weight, bias=None, initial_state=None, cu_seqlens=None, silu=True, output_final_state=False):
+    """The short causal convolution (gdn_conv_fwd), differentiable in x,
+    weight, bias and initial_state. Returns (y, final_state or None)."""
+    return _CausalConv.apply(x, weight, bias, initial_state, cu_seqlens, bool(silu), bool(output_final_state))
+
+
+class _SelectiveScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, dt, A, Bm, Cm, D, z, dt_bias, h0, cu_seqlens, dt_softplus, output_final_state):
+        n_seq = x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+        final = (torch.empty((n_seq,) + tuple(A.shape), dtype=torch.float32, device=x.device)
+                 if output_final_state else None)
+        y = gdn_ssm_fwd(x, dt, A, Bm, Cm, D=D, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus, h0=h0,
+                        cu_seqlens=cu_seqlens, h_final=final)
+        ctx.save_for_backward(x, dt, A, Bm, Cm, D, z, dt_bias, h0, cu_seqlens)
+        ctx.dt_softplus = dt_softplus
+        return y, final
+
+    @staticmethod
+    def backward(ctx, dy, dfinal):
+        x, dt, A, Bm, Cm, D, z, dt_bias, h0, cu_seqlens = ctx.saved_tensors
+        r = gdn_ssm_bwd(x, dt, A, Bm, Cm, dy.contiguous(), D=D, z=z, dt_bias=dt_bias, dt_softplus=ctx.dt_softplus,
+                        h0=h0, cu_seqlens=cu_seqlens, dh_final=None if dfinal is None else dfinal.contiguous())
+        return (r["dx"], r["ddt"], r["dA"], r["dBm"], r["dCm"], r.get("dD"), r.get("dz"), r.get("ddt_bias"),
+                r.get("dh0"), None, None, None)
+
+
+def selective_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, initial_state=None, cu_seqlens=None,
+                   dt_softplus=True, output_final_state=False):
+    """The selective state-space scan (gdn_ssm_fwd), differentiable in every
+    tensor but cu_seqlens. Returns (y, final_state or None)."""
+    return _SelectiveScan.apply(x, dt, A, Bm, Cm, D, z, dt_bias, initial_state, cu_seqlens, bool(dt_softplus),
+                                bool(output_final_state))

@@ -19,7 +19,6 @@
 namespace gdn {
 namespace {
 
-constexpr int kTokLBwd = 64;  // tokens a thread, gradient
 constexpr int kConvY = 4, kConvYBwd = 8;
 
 // The sequence of a token: the last s with cu[s] <= t, its bounds clamped so
@@ -147,7 +146,7 @@ __device__ __forceinline__ void check_cu(const int32_t *cu, int n_seq, int T, in
 }
 
 template <typename T, int NC, int W, bool VEC>
-__global__ void __launch_bounds__(32 * kConvY, 6) conv_kernel(const ConvParams p, int nblk, int run) {
+__global__ void __launch_bounds__(32 * kConvY, sizeof(T) == 2 && W <= 4 ? 6 : 3) conv_kernel(const ConvParams p, int nblk, int run) {
     constexpr int NW = RowVec<T, NC>::kWords, U = 4;
     const int c = (blockIdx.y * 32 + threadIdx.x) * NC, n = p.D - c, b = blockIdx.z;
     if (blockIdx.x == nblk) {  // checks, and the windows of empty sequences
@@ -260,7 +259,7 @@ __device__ __forceinline__ void dpre(f32x2 (&dp)[NC / 2], const f32x2 (&w)[W][NC
 // already given; a token's dx is complete W - 1 tokens later, so a run of
 // tokens is followed by W - 1 more that only add to the run's own.
 template <typename T, int NC, int W, bool VEC>
-__global__ void __launch_bounds__(32 * kConvYBwd, 2) conv_bwd_kernel(const ConvParams p, int nblk) {
+__global__ void __launch_bounds__(32 * kConvYBwd, sizeof(T) == 2 && W <= 4 ? 2 : 1) conv_bwd_kernel(const ConvParams p, int nblk, int run) {
     constexpr int NW = RowVec<T, NC>::kWords;
     extern __shared__ float red[];  // [kConvYBwd][NC * (W + 1)][32]
     const int c = (blockIdx.y * 32 + threadIdx.x) * NC, n = p.D - c, b = blockIdx.z;
@@ -319,10 +318,10 @@ __global__ void __launch_bounds__(32 * kConvYBwd, 2) conv_bwd_kernel(const ConvP
 #pragma unroll
         for (int j = 0; j < W; ++j) dw[j][i] = pack2(0.f, 0.f);
     }
-    const int64_t first = ((int64_t)blockIdx.x * kConvYBwd + threadIdx.y) * kTokLBwd;
+    const int64_t first = ((int64_t)blockIdx.x * kConvYBwd + threadIdx.y) * run;
     if (c < p.D && first < p.T) {
         constexpr int U = 4;
-        const int t0 = (int)first, t1 = min(p.T - t0, kTokLBwd) + t0, t2 = min(p.T - t1, W - 1) + t1;
+        const int t0 = (int)first, t1 = min(p.T - t0, run) + t0, t2 = min(p.T - t1, W - 1) + t1;
         const T *xs = (const T *)p.x + b * p.x_sb + c;
         const T *ds = (const T *)p.dout + b * p.do_sb + c;
         T *dx = (T *)p.dx + (int64_t)b * p.T * p.D + c;
@@ -540,14 +539,14 @@ cudaError_t conv_t(const ConvParams &p, cudaStream_t st) {
 template <typename T>
 cudaError_t conv_bwd_t(const ConvParams &p, cudaStream_t st) {
     constexpr int NC = 4;
-    const int nblk = conv_bwd_parts(1, p.T);
+    const int run = conv_bwd_run(p.B, p.T, p.D), nblk = conv_bwd_parts(1, p.T, run);
     const bool extra = p.cu != nullptr || p.dinit;
     const dim3 grid(nblk + (extra ? 1 : 0), (p.D + 32 * NC - 1) / (32 * NC), p.T == 0 ? 1 : p.B),
         block(32, kConvYBwd);
     return by_taps(p.W, [&](auto w) {
         const size_t smem = sizeof(float) * 32 * kConvYBwd * NC * (w() + 1);
-        if (p.vec) conv_bwd_kernel<T, NC, w(), true><<<grid, block, smem, st>>>(p, nblk);
-        else conv_bwd_kernel<T, NC, w(), false><<<grid, block, smem, st>>>(p, nblk);
+        if (p.vec) conv_bwd_kernel<T, NC, w(), true><<<grid, block, smem, st>>>(p, nblk, run);
+        else conv_bwd_kernel<T, NC, w(), false><<<grid, block, smem, st>>>(p, nblk, run);
         return cudaGetLastError();
     });
 }
@@ -567,9 +566,16 @@ cudaError_t conv_step_t(const ConvStepParams &p, cudaStream_t st) {
 cudaError_t launch_conv(const ConvParams &p, cudaStream_t st) {
     return p.bf16 ? conv_t<__nv_bfloat16>(p, st) : conv_t<float>(p, st);
 }
+// Tokens a thread of the gradient: 64, whose W - 1 tokens on either side cost
+// little, or down to 16 while that leaves SMs without a CTA.
+int conv_bwd_run(int B, int T, int D) {
+    int run = 64;
+    while (run > 16 && (int64_t)conv_bwd_parts(B, T, run) * ((D + 127) / 128) < 304) run /= 2;
+    return run;
+}
 // CTAs along the tokens of all rows: each leaves one row of partial sums
-int conv_bwd_parts(int B, int T) {
-    return B * (int)(((int64_t)T + kConvYBwd * kTokLBwd - 1) / (kConvYBwd * kTokLBwd));
+int conv_bwd_parts(int B, int T, int run) {
+    return B * (int)(((int64_t)T + kConvYBwd * run - 1) / (kConvYBwd * run));
 }
 cudaError_t launch_conv_bwd(const ConvParams &p, cudaStream_t st) {
     return p.bf16 ? conv_bwd_t<__nv_bfloat16>(p, st) : conv_bwd_t<float>(p, st);

@@ -221,7 +221,8 @@ struct ConvParams {
     int B, T, D, W, silu, bf16, vec;
     int *err;  // device error word or null
 };
-int conv_bwd_parts(int B, int T);
+int conv_bwd_run(int B, int T, int D);
+int conv_bwd_parts(int B, int T, int run);
 cudaError_t launch_conv(const ConvParams &p, cudaStream_t st);
 cudaError_t launch_conv_bwd(const ConvParams &p, cudaStream_t st);
 struct ConvStepParams {

@@ -160,6 +160,8 @@ gdn_status gdn_conv_fwd(const void *x, int64_t x_sb, int64_t x_st, const float *
     if (!batch_ok(B, T, D, cu_seqlens, n_seq) || W < 2 || W > kConvMaxW) return GDN_ERR_SHAPE;
     if (!dtype_ok(dtype)) return GDN_ERR_DTYPE;
     if (flags & ~GDN_SILU) return GDN_ERR_UNSUPPORTED;
+    // (the inputs before a run of tokens are read by other threads than write there)
+    if ((x && x == out) || (initial_state && initial_state == final_state)) return GDN_ERR_UNSUPPORTED;
     Rows r;
     r.add(x, dtype, x_sb, x_st);
     r.add(out, dtype, out_sb, out_st);
@@ -181,7 +183,7 @@ gdn_status gdn_conv_fwd(const void *x, int64_t x_sb, int64_t x_st, const float *
 
 size_t gdn_conv_bwd_workspace_size(int B, int T, int D, int W) {
     if (B < 1 || B > 65535 || T < 0 || D < 1 || D > (1 << 20) || W < 2 || W > kConvMaxW) return 0;
-    return align_up((size_t)conv_bwd_parts(B, T) * D * (W + 1) * 4) + kAlign;
+    return align_up((size_t)conv_bwd_parts(B, T, conv_bwd_run(B, T, D)) * D * (W + 1) * 4) + kAlign;
 }
 
 gdn_status gdn_conv_bwd(const void *x, int64_t x_sb, int64_t x_st, const float *weight, int W, const float *bias,
@@ -217,7 +219,8 @@ gdn_status gdn_conv_bwd(const void *x, int64_t x_sb, int64_t x_st, const float *
         e = launch(KConvBwd, stream, [&] { return launch_conv_bwd(p, stream); });
     if (e == cudaSuccess)
         e = launch(KColSum, stream, [&] {
-            return launch_col_sum(p.part, (int64_t)D * (W + 1), conv_bwd_parts(B, T), (int64_t)D * W, dweight,
+            return launch_col_sum(p.part, (int64_t)D * (W + 1), conv_bwd_parts(B, T, conv_bwd_run(B, T, D)),
+                                  (int64_t)D * W, dweight,
                                   dbias ? D : 0, dbias, stream);
         });
     return cuda_status(e);
@@ -302,6 +305,7 @@ gdn_status gdn_ssm_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *dt
                                    z_st, dt_bias, h0, cu_seqlens, n_seq, B, T, D, N, dtype, flags, r, p);
     if (s != GDN_OK) return s;
     if (!f32_ok(h_final)) return GDN_ERR_LAYOUT;
+    if (h0 && h0 == h_final) return GDN_ERR_UNSUPPORTED;
     const SsmWs L = ssm_ws(cu_seqlens ? 1 : B, T, D, N);
     if (!ws_ok(workspace, ws_bytes, L.total)) return GDN_ERR_WORKSPACE;
     unsigned char *ws = static_cast<unsigned char *>(workspace);

@@ -155,7 +155,8 @@ def gdn_rmsnorm_fwd(x, weight, residual=None, eps=1e-6, out_dtype=None, group=0,
     """y = s / sqrt(mean(s^2) + eps) * weight over the last dimension, with
     s = x + residual (fp32). Returns a dict: "out"; with a residual,
     "residual": s in the residual's type (in residual_out, which may be the
-    residual itself, or a new tensor); with out_dtype=torch.float8_e4m3fn,
+    residual itself, or a new tensor); x's leading dimensions have to be rows
+    of one stride; with out_dtype=torch.float8_e4m3fn,
     "scale": fp32, one for each `group` channels (32, 64, 128 or 256; 0: the
     row), out * scale being y."""
     if stream is not None:

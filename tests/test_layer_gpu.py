@@ -496,3 +496,54 @@ def test_steps_replay_in_a_graph():
     step(want, o2)
     torch.cuda.synchronize()
     assert torch.equal(pool, want) and torch.equal(out, o2)
+
+
+# ---------------------------------------------------- autograd, example ---
+
+
+def test_autograd_functions_give_the_gradients_of_the_calls():
+    from gated_delta_rule_18_gb300 import autograd as gdr
+    lens = [9, 0, 31]
+    v = scan_case(1, 40, 24, 16, lens, F32, True, 170)
+    a = {k: dev(t).requires_grad_() for k, t in v.items()}
+    y, fin = gdr.selective_scan(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], a["D"], a["z"], a["dt_bias"], a["h0"],
+                                dev(cu_of(lens)), output_final_state=True)
+    do, df = randn(tuple(y.shape), F32, 180).to(DEV), randn(tuple(fin.shape), F32, 181).to(DEV)
+    ((y * do).sum() + (fin * df).sum()).backward()
+    ref = {k: f64(t).requires_grad_() for k, t in v.items()}
+    out, f = ref_scan(ref, lens, True)
+    ((out * f64(do)).sum() + (f * f64(df)).sum()).backward()
+    for k in v:
+        assert rel(a[k].grad, ref[k].grad) <= TOL_SCAN, k
+    x, w, b = randn((1, 40, 24), F32, 182), randn((24, 4), F32, 183), randn((24,), F32, 184)
+    c = [dev(t).requires_grad_() for t in (x, w, b)]
+    y, _ = gdr.causal_conv(*c, cu_seqlens=dev(cu_of(lens)))
+    (y * do).sum().backward()
+    r = [f64(t).requires_grad_() for t in (x, w, b)]
+    (ref_conv(*r, None, lens, True)[0] * f64(do)).sum().backward()
+    assert all(rel(g.grad, h.grad) <= TOL_F32 for g, h in zip(c, r))
+    s, q = randn((5, 24), F32, 185), randn((5, 24), F32, 186)
+    c = [dev(t).requires_grad_() for t in (s, torch.ones(24), q)]
+    y, stream = gdr.rms_norm(*c)
+    (y.square().sum() + (stream * 3).sum()).backward()
+    r = [f64(t).requires_grad_() for t in (s, torch.ones(24), q)]
+    u, y = ref_norm(r[0], r[1], r[2], 1e-6)
+    # the reference's sum keeps the gradient of both inputs
+    (ref_norm(r[0] + r[2], r[1], None, 1e-6)[1].square().sum() + ((r[0] + r[2]) * 3).sum()).backward()
+    assert all(rel(g.grad, h.grad) <= 1e-4 for g, h in zip(c, r))
+
+
+def test_state_space_layer_example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "state_space_layer.py")
+    spec = importlib.util.spec_from_file_location("state_space_layer", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    layer = m.StateSpaceLayer(128)
+    losses = m.train(layer, steps=12)
+    assert all(math.isfinite(v) for v in losses) and losses[-1] < 0.9 * losses[0]
+    # the same bf16 products in another order: a few roundings of 2^-9
+    assert m.continue_prompt(layer) <= 2.0**-6
+    # e4m3 inputs of the projection: 2^-4 of a value, averaged over 128 channels, through two gated products
+    assert m.continue_prompt(layer, eight_bit=True) <= 2.0**-3
