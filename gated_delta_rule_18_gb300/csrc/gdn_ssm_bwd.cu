@@ -269,6 +269,8 @@ __global__ void __launch_bounds__(256) ssm_bwd_chain_kernel(const SsmParams p, i
 }
 
 // -------------------------------------------------------------- walk back ---
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // D += A B, m16n8k8, tf32 operands (the low 13 bits of an fp32 are ignored)
 __device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -352,6 +354,11 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
                        (const T *)p.z + line * p.z_sb, (const T *)p.dout + line * p.do_sb};
     const int64_t str[4] = {p.x_st, p.dt_st, p.z_st, p.do_st};
 
+    // the pair of channels whose delta and dy this thread forms
+    static_assert(kWalk % (CH / 2) == 0, "a thread keeps its pair");
+    const int pc = tid % (CH / 2);
+    const float2 pbias = make_float2(p.dt_bias && c0 + 2 * pc < p.D ? p.dt_bias[c0 + 2 * pc] : 0.f,
+                                     p.dt_bias && c0 + 2 * pc + 1 < p.D ? p.dt_bias[c0 + 2 * pc + 1] : 0.f);
     // B fragments of the channel sums, and what a lane has of them: matrix and first state
     uint32_t sel0[4], sel1[4];
 #pragma unroll
@@ -403,16 +410,13 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
         for (int e = tid; e < 2 * kPart; e += kWalk) part[e] = 0.f;
         cp_async_wait<0>();
         __syncthreads();
-        // delta and dy of the tile, by pairs
-        for (int e = tid; e < kTile / 2; e += kWalk) {
-            const int r = e / (CH / 2), c = e % (CH / 2) * 2;
+        // delta and dy of the tile, by pairs of channels (each thread's own)
+#pragma unroll 2
+        for (int r = tid / (CH / 2); r < TG; r += kWalk / (CH / 2)) {
+            const int c = 2 * pc;
             float f[2];
             ld_row_f<T, 2, true>(f, tiles + kTile + r * CH + c, 2);
-            float2 v = make_float2(f[0], f[1]);
-            if (p.dt_bias) {
-                if (c0 + c < p.D) v.x += p.dt_bias[c0 + c];
-                if (c0 + c + 1 < p.D) v.y += p.dt_bias[c0 + c + 1];
-            }
+            float2 v = make_float2(f[0] + pbias.x, f[1] + pbias.y);
             if (softplus) v = softplus2(v);
             *reinterpret_cast<float2 *>(dls + r * CH + c) = v;
             ld_row_f<T, 2, true>(f, tiles + 3 * kTile + r * CH + c, 2);
@@ -425,6 +429,14 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
             *reinterpret_cast<float2 *>(dys + r * CH + c) = make_float2(f[0], f[1]);
         }
         __syncthreads();
+        if (grp * TG > r0) {  // the next group's rows and states towards L2
+            constexpr int kLine = 128 / (int)sizeof(T), kPer = (CH + kLine - 1) / kLine;
+            for (int e = tid; e < 4 * TG * kPer; e += kWalk) {
+                const int k = e / (TG * kPer), r = e / kPer % TG, c = c0 + e % kPer * kLine;
+                if ((k != 2 || gate) && c < p.D) prefetch_l2(src[k] + (t0 - TG + r) * str[k] + c);
+            }
+            if (grp > 1 && fin) prefetch_l2(p.sums + ((int64_t)line * p.ngroup + grp - 2) * dnp + own_p);
+        }
         const T *xs = tiles + ch;
         const int64_t o0 = ((int64_t)line * p.T + t0) * p.D + d;
         T *dxp = (T *)p.dx + o0, *dtp = (T *)p.ddt + o0, *dzp = (T *)p.dz + o0;
@@ -467,7 +479,7 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
                 // sigmoid(v) = exp(v - softplus(v))
                 if (softplus) dd *= ex2f((ldf(xs + kTile + t * CH) + bias - dl) * kLog2e);
                 if (fin && here) {
-                    const int64_t at = (int64_t)t * p.D;
+                    const int at = t * p.D;
                     dxp[at] = to_type<T>(fmaf(dv, dy, dl * s1));
                     dtp[at] = to_type<T>(dd);
                     if (gate && (USUAL || p.dz)) {
