@@ -264,8 +264,8 @@ struct SsmParams {
     void *dx, *ddt, *dbm, *dcm, *dz;
     float *dA, *dD, *ddt_bias, *dh0;
     // runs of a line, tokens a run, groups of a line; workspace: sums and dsum
-    // by group, the same sums of delta for the runs (gsum), the runs' gradients
-    // (lines, nrun, D, padded N), partial sums by channel tile and by run
+    // by group, the sums of delta by run (gsum), the runs' gradients (lines,
+    // nrun, D, padded N), partial sums by channel tile and by run
     int nrun, rlen, ngroup;
     float *gsum, *gs, *part_bc, *part_a, *part_d;
 };

@@ -74,7 +74,7 @@ SsmBwdWs ssm_bwd_ws(int B, int T, int D, int N, int varlen) {
     };
     L.sums = take(groups * dnp);
     L.dsum = take(groups * D);
-    L.gsum = take(groups * D);
+    L.gsum = take(runs * D);
     L.gs = take(runs * dnp);
     L.bc = take((size_t)ssm_bwd_tiles(D, N) * B * T * 2 * N);
     L.a = take(runs * D * N);

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kNT, 8) ssm_bwd_sum_kernel(const SsmParams p, 
     }
     fetch_bc(t0);
     float *gs = p.gs + ((int64_t)line * p.nrun + run) * dnp + own_p;
-    float2 dsum = make_float2(0.f, 0.f);
+    float2 dsum = make_float2(0.f, 0.f), rsum = dsum;  // of the group, of the run
     int buf = 0;
     for (int s = t0; s < t1; s += TS, buf ^= 1) {
         float *bc = bcs + buf * kBc;
@@ -175,15 +175,16 @@ __global__ void __launch_bounds__(kNT, 8) ssm_bwd_sum_kernel(const SsmParams p, 
         auto cut = [&](int last) {
             const int64_t at = (int64_t)line * p.ngroup + last / kGroup;
             st_pair<Q>(p.sums + at * dnp + own_p, h, NP, Q, true, on);
-            float *o = p.dsum + at * p.D + d, *r = p.gsum + at * p.D + d;
-            if (ln == 0 && d < p.D) o[0] = reset ? __int_as_float(0x7fffffff) : dsum.x, r[0] = dsum.x;
-            if (ln == 0 && d + 1 < p.D) o[1] = reset ? __int_as_float(0x7fffffff) : dsum.y, r[1] = dsum.y;
+            float *o = p.dsum + at * p.D + d;
+            if (ln == 0 && d < p.D) o[0] = reset ? __int_as_float(0x7fffffff) : dsum.x;
+            if (ln == 0 && d + 1 < p.D) o[1] = reset ? __int_as_float(0x7fffffff) : dsum.y;
+            rsum.x += dsum.x, rsum.y += dsum.y;
             dsum = make_float2(0.f, 0.f);
             reset = false;
             first_h(0, true);
         };
         if (m == TS && q.end > s + TS) {  // no sequence ends in the stage; groups end with stages
-#pragma unroll 2
+#pragma unroll 4
             for (int t = 0; t < TS; ++t) token(t);
             if ((s + TS) % kGroup == 0 || s + TS == t1) cut(s + TS - 1);
         } else {
@@ -219,10 +220,10 @@ __global__ void __launch_bounds__(kNT, 8) ssm_bwd_sum_kernel(const SsmParams p, 
         else if (s + TS < t1) release(buf ^ 1);
     }
     if (alive) st_pair<Q>(gs, g, NP, Q, true, on);
-    if (!alive && ln == 0) {  // nothing crosses the run: marked by NaN
-        float *r = p.gsum + ((int64_t)line * p.ngroup + t0 / kGroup) * p.D + d;
-        if (d < p.D) r[0] = __int_as_float(0x7fffffff);
-        if (d + 1 < p.D) r[1] = __int_as_float(0x7fffffff);
+    if (ln == 0) {  // where nothing crosses the run: marked by NaN
+        float *r = p.gsum + ((int64_t)line * p.nrun + run) * p.D + d;
+        if (d < p.D) r[0] = alive ? rsum.x : __int_as_float(0x7fffffff);
+        if (d + 1 < p.D) r[1] = alive ? rsum.y : __int_as_float(0x7fffffff);
     }
 }
 
@@ -253,17 +254,20 @@ __global__ void __launch_bounds__(256) ssm_bwd_chain_kernel(const SsmParams p, i
             }
         }
     } else {
-        const int gpr = p.rlen / kGroup;
         float *s = p.gs + (int64_t)line * p.nrun * dnp + i % dnp;
-        const float *q = p.gsum + (int64_t)line * p.ngroup * p.D + d;
+        const float *q = p.gsum + (int64_t)line * p.nrun * p.D + d;
         float g = 0.f;
-        for (int r = p.nrun - 1; r >= 0; --r) {
-            float v = 0.f;
-            const int e = min(p.ngroup, (r + 1) * gpr);
-            for (int c = r * gpr; c < e; ++c) v += q[(int64_t)c * p.D];
-            const float own = s[r * dnp];
-            g = isnan(v) ? own : fmaf(ex2f(a * v), g, own);
-            s[r * dnp] = g;
+        for (int r = p.nrun - 1; r >= 0; r -= 8) {
+            float v[8], e[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                v[k] = r >= k ? q[(int64_t)(r - k) * p.D] : 0.f, e[k] = r >= k ? s[(r - k) * dnp] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                g = isnan(v[k]) ? e[k] : fmaf(ex2f(a * v[k]), g, e[k]);
+                if (r >= k) s[(r - k) * dnp] = g;
+            }
         }
     }
 }
