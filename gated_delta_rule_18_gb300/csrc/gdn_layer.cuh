@@ -254,7 +254,7 @@ struct SsmParams {
     int vec;             // rows of x, dt, z, out (and the gradients) are 16-byte aligned
     int n_wide;          // rows of A and of the states are
     int bc_vec;          // rows of B and C are, in whole vectors of four
-    int nchunk, clen;    // chunks of a line, tokens a chunk
+    int nchunk, clen0, clen;  // chunks of a line, tokens of the first and of the others
     float *sums, *dsum;  // workspace: (lines, nchunk - 1, D, padded N), (lines, nchunk - 1, D)
     int *err;
     // gradient; activations' gradients contiguous in x's type
@@ -269,7 +269,7 @@ struct SsmParams {
     int nrun, rlen, ngroup;
     float *gsum, *gs, *part_bc, *part_a, *part_d;
 };
-void ssm_split(int lines, int T, int D, int N, int *nchunk, int *clen);
+void ssm_split(int lines, int T, int D, int N, int *nchunk, int *clen0, int *clen);
 cudaError_t launch_ssm_sum(const SsmParams &p, cudaStream_t st);
 cudaError_t launch_ssm_chain(const SsmParams &p, cudaStream_t st);
 cudaError_t launch_ssm_scan(const SsmParams &p, cudaStream_t st);

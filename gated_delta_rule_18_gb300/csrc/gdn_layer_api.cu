@@ -39,12 +39,12 @@ bool batch_ok(int B, int T, int D, const int32_t *cu, int n_seq) {
 
 // the forward: the error word, and the chunks' sums where a line is cut
 struct SsmWs {
-    int nchunk, clen;
+    int nchunk, clen0, clen;
     size_t sums, dsum, total;
 };
 SsmWs ssm_ws(int lines, int T, int D, int N) {
     SsmWs L;
-    ssm_split(lines, T, D, N, &L.nchunk, &L.clen);
+    ssm_split(lines, T, D, N, &L.nchunk, &L.clen0, &L.clen);
     const size_t items = (size_t)lines * (L.nchunk - 1);
     L.sums = kAlign;
     L.dsum = align_up(L.sums + items * D * ssm_np(N) * 4);
@@ -310,7 +310,7 @@ gdn_status gdn_ssm_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *dt
     if (!ws_ok(workspace, ws_bytes, L.total)) return GDN_ERR_WORKSPACE;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     p.out = out, p.o_sb = out_sb, p.o_st = out_st, p.h_final = h_final;
-    p.nchunk = L.nchunk, p.clen = L.clen;
+    p.nchunk = L.nchunk, p.clen0 = L.clen0, p.clen = L.clen;
     p.sums = reinterpret_cast<float *>(ws + L.sums), p.dsum = reinterpret_cast<float *>(ws + L.dsum);
     p.err = cu_seqlens ? reinterpret_cast<int *>(ws) : nullptr;
     p.vec = r.wide && D % 8 == 0;

@@ -11,10 +11,14 @@
 // The main loop is written in packed pairs to leave issue slots for the rest.
 //
 // A line of tokens is one CTA's from end to end while channels alone fill the
-// GPU. Where they do not, the line is cut into chunks: a first pass forms
-// each chunk's state from zero and its sum of delta (the decay of a chunk is
-// exp(A sum delta), so it needs no product of its own), a short pass chains
-// them, and the scan runs every chunk from its entering state.
+// GPU. Where they do not, the line is cut into chunks: a first pass scans the
+// first chunk and forms the others' states from zero and sums of delta (the
+// decay of a chunk is exp(A sum delta), so it needs no product of its own), a
+// short pass chains them, and a second scan runs the chunks from their
+// entering states. 4 x 4096 tokens of 4096 channels, 16 states, bf16: 205, 10
+// and 268 us (8.6 and 11.1 cycles a warp for 32 (token, channel, state); the
+// bare loops take 5.0 and 6.2, the rest is what a token and channel needs
+// once: softplus, gate and the conversions). Whole lines: 1018 us (128 CTAs).
 #include "gdn_ssm.cuh"
 
 namespace gdn {
@@ -46,19 +50,19 @@ __device__ __forceinline__ void st_across(float *p, const f32x2 (&v)[Q], int ld,
     st_pair<Q>(p, a, ld, n, wide, on);
 }
 
-// A lane has Q states of two neighbouring channels, which are the halves of
-// its packed pairs; LN lanes a channel (LN = 1 up to 16 states, so nothing crosses lanes there). x, dt and
-// z come through two shared-memory buffers, a stage ahead of their use; B and
+// One chunk of a line. A lane has Q states of two neighbouring channels, which
+// are the halves of its packed pairs; LN lanes a channel (LN = 1 up to 16
+// states, so nothing crosses lanes there). x, dt and z come through two shared-memory buffers, a stage ahead of their use; B and
 // C, the same for every channel, are staged as fp32 and read by broadcast, 4
 // bytes a (channel, state). A stage has three loops: delta and delta x of its
 // tokens (the chain of a softplus is some 150 cycles: four tokens' side by
 // side hide it), the states, whose only chain is one multiply-add a token, and
 // the outputs; between them a thread's own slots of shared memory. One loop
-// that did all three took 0.33 ms where this takes SCAN_MS for 32768 tokens
-// of 2048 channels. USUAL: softplus, a gate and rows for wide accesses, known
+// that did all three took 0.33 ms where this takes 0.29 for 32768 tokens of
+// 2048 channels. USUAL: softplus, a gate and rows for wide accesses, known
 // beforehand.
 template <typename T, int Q, int LN, bool SUM, bool USUAL>
-__global__ void __launch_bounds__(kThreads, 6) ssm_scan_kernel(const SsmParams p, int ntile) {
+__device__ __forceinline__ void ssm_walk(const SsmParams &p, int line, int chunk, int tile) {
     constexpr int CH = 2 * kThreads / LN, NP = Q * LN, TS = kStage;
     constexpr int NA = SUM ? 2 : 3;  // x, dt, z
     constexpr int kTile = TS * CH * (int)sizeof(T), kBuf = NA * kTile, kBc = TS * 2 * NP;
@@ -66,11 +70,7 @@ __global__ void __launch_bounds__(kThreads, 6) ssm_scan_kernel(const SsmParams p
     float4 *slot = reinterpret_cast<float4 *>(smem + 2 * kBuf) + threadIdx.x;  // [TS][kThreads], delta, delta x or y
     float *bcs = reinterpret_cast<float *>(smem + 2 * kBuf + TS * kThreads * 16);  // [2][TS][2][NP]
     const int tid = threadIdx.x, ch = tid / LN * 2, ln = tid % LN;
-    const int tile = blockIdx.x % ntile, item = blockIdx.x / ntile;
-    const int nch = SUM ? p.nchunk - 1 : p.nchunk;
-    const int line = item / nch, chunk = item - line * nch;
-    if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
-    const int t0 = chunk * p.clen, t1 = min(p.T - t0, p.clen) + t0;
+    const int t0 = chunk ? p.clen0 + (chunk - 1) * p.clen : 0, t1 = min(p.T - t0, chunk ? p.clen : p.clen0) + t0;
     const int c0 = tile * CH, d = c0 + ch, n0 = ln * Q, nn = p.N - n0;
     const bool on[2] = {d < p.D && nn > 0, d + 1 < p.D && nn > 0}, out = d < p.D && ln == 0;
     const int64_t hrow = (int64_t)p.D * p.N, dnp = (int64_t)p.D * NP;
@@ -228,14 +228,16 @@ __global__ void __launch_bounds__(kThreads, 6) ssm_scan_kernel(const SsmParams p
         if (vec) copy(s + 2 * TS, buf);
         else if (s + TS < t1) release(buf ^ 1);
     }
-    if (SUM) {
-        st_across<Q>(p.sums + ((int64_t)line * nch + chunk) * dnp + own_p, h, NP, Q, true, on);
+    if (SUM || (chunk == 0 && p.nchunk > 1)) {
+        const int64_t at = (int64_t)line * (p.nchunk - 1) + chunk;
+        st_across<Q>(p.sums + at * dnp + own_p, h, NP, Q, true, on);
         // a chunk in which a sequence begins passes nothing on: marked by NaN
         const float2 ds = unpack2(dsum);
-        float *o = p.dsum + ((int64_t)line * nch + chunk) * p.D + d;
+        float *o = p.dsum + at * p.D + d;
         if (ln == 0 && d < p.D) o[0] = reset ? __int_as_float(0x7fffffff) : ds.x;
         if (ln == 0 && d + 1 < p.D) o[1] = reset ? __int_as_float(0x7fffffff) : ds.y;
-    } else if (p.h_final && chunk == 0 && (p.cu || p.T == 0)) {
+    }
+    if (!SUM && p.h_final && chunk == 0 && (p.cu || p.T == 0)) {
         // sequences without a token pass their state on
         for (int s = 0; s < p.n_seq; ++s) {
             if (p.cu ? p.cu[s + 1] > p.cu[s] : s != line) continue;
@@ -243,6 +245,23 @@ __global__ void __launch_bounds__(kThreads, 6) ssm_scan_kernel(const SsmParams p
             st_across<Q>(p.h_final + s * hrow + own, h, p.N, nn, p.n_wide, on);
         }
     }
+}
+
+// Every chunk but the first, or whole lines. Six CTAs a SM: eight have to do
+// with 128 registers and took 0.31 ms for 0.30.
+template <typename T, int Q, int LN, bool USUAL>
+__global__ void __launch_bounds__(kThreads, 6) ssm_scan_kernel(const SsmParams p, int ntile) {
+    if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
+    const int item = blockIdx.x / ntile, nch = max(p.nchunk - 1, 1), line = item / nch;
+    ssm_walk<T, Q, LN, false, USUAL>(p, line, item - line * nch + (p.nchunk > 1), blockIdx.x % ntile);
+}
+// The first launch over a line in chunks: the first chunk's scan, whose state
+// is its sum, beside the sums of the others but the last.
+template <typename T, int Q, int LN, bool USUAL>
+__global__ void __launch_bounds__(kThreads, 6) ssm_sum_kernel(const SsmParams p, int ntile) {
+    const int item = blockIdx.x / ntile, nch = p.nchunk - 1, line = item / nch, chunk = item - line * nch;
+    if (chunk > 0) return ssm_walk<T, Q, LN, true, USUAL>(p, line, chunk, blockIdx.x % ntile);
+    ssm_walk<T, Q, LN, false, USUAL>(p, line, 0, blockIdx.x % ntile);
 }
 
 // The state entering chunk c + 1 replaces chunk c's sum: h <- exp(A sum
@@ -368,15 +387,16 @@ __global__ void __launch_bounds__(128) ssm_step_kernel(const SsmStepParams p) {
 template <typename T, int Q, int LN, bool SUM>
 cudaError_t scan_t(const SsmParams &p, cudaStream_t st) {
     constexpr int CH = 2 * kThreads / LN;
-    constexpr int smem = 2 * (SUM ? 2 : 3) * kStage * CH * (int)sizeof(T) + kStage * kThreads * 16 + 2 * kStage * 2 * Q * LN * 4;
-    const bool usual = p.vec && p.softplus && (SUM || p.z);
-    auto *k = usual ? ssm_scan_kernel<T, Q, LN, SUM, true> : ssm_scan_kernel<T, Q, LN, SUM, false>;
+    constexpr int smem = 2 * 3 * kStage * CH * (int)sizeof(T) + kStage * kThreads * 16 + 2 * kStage * 2 * Q * LN * 4;
+    const bool usual = p.vec && p.softplus && p.z;
+    auto *k = SUM ? (usual ? ssm_sum_kernel<T, Q, LN, true> : ssm_sum_kernel<T, Q, LN, false>)
+                  : (usual ? ssm_scan_kernel<T, Q, LN, true> : ssm_scan_kernel<T, Q, LN, false>);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
     const int ntile = (p.D + CH - 1) / CH;
-    const int64_t items = (int64_t)(p.cu ? 1 : p.B) * (SUM ? p.nchunk - 1 : p.nchunk);
+    const int64_t items = (int64_t)(p.cu ? 1 : p.B) * (p.nchunk > 1 ? p.nchunk - 1 : 1);
     if (items * ntile > INT32_MAX) return cudaErrorInvalidValue;
     k<<<(unsigned)(items * ntile), kThreads, smem, st>>>(p, ntile);
     return cudaGetLastError();
@@ -394,21 +414,24 @@ cudaError_t by_lanes(int N, F &&f) {
 }  // namespace
 
 // Chunks of a line, by the number of CTAs that whole lines give.
-void ssm_split(int lines, int T, int D, int N, int *nchunk, int *clen) {
+void ssm_split(int lines, int T, int D, int N, int *nchunk, int *clen0, int *clen) {
     const int ch = 2 * kThreads / ssm_lanes(N);
     const int64_t ctas = (int64_t)lines * ((D + ch - 1) / ch);
-    // Six CTAs a SM (three warps a scheduler), in chunks of at least 64 tokens;
-    // whole lines from two a SM on, where the sums would cost as much as they
-    // hide.
-    int64_t n = 1;
-    if (ctas < 304) {
-        n = 912 / ctas;
-        if (n > (T + 63) / 64) n = (T + 63) / 64;
-        if (n < 1) n = 1;
+    // Each launch takes n chunks of a line, with six CTAs a SM (three warps a
+    // scheduler), chunks of at least 64 tokens; whole lines where n would be
+    // one. 4096 channels: 10 x 3000 tokens (320 CTAs) 1067 us whole, 969 cut;
+    // 16 x 2048 (512 CTAs) 736 whole.
+    int64_t n = 912 / ctas;
+    if (n > (T + 63) / 64 - 1) n = (T + 63) / 64 - 1;
+    if (n < 2) {
+        *clen0 = *clen = T > 0 ? T : 1, *nchunk = 1;
+        return;
     }
-    const int len = (int)(((T + n - 1) / n + kStage - 1) / kStage * kStage);
-    *clen = len > 0 ? len : kStage;
-    *nchunk = T > 0 ? (int)(((int64_t)T + *clen - 1) / *clen) : 1;
+    // a token's scan takes 1.3 times its sum: so much shorter is the first chunk
+    auto stages = [](int64_t v) { return (int)((v + kStage - 1) / kStage * kStage); };
+    *clen = stages((int64_t)T * 4 / (4 * n + 3));
+    *clen0 = stages((int64_t)*clen * 3 / 4);
+    *nchunk = 1 + (int)(((int64_t)T - *clen0 + *clen - 1) / *clen);
 }
 
 cudaError_t launch_ssm_sum(const SsmParams &p, cudaStream_t st) {
