@@ -357,6 +357,42 @@ def test_scan_bwd(B, T, C, N, lens, dtype, full):
     assert all(torch.equal(got[k], again[k]) for k in got)
 
 
+@pytest.mark.parametrize("dtype,C,N", [(BF, 64, 16), (BF, 37, 16), (F32, 48, 16), (BF, 40, 40)])
+def test_scan_non_finite_values_stay_in_their_channel_and_sequence(dtype, C, N):
+    lens = [70, 1, 150, 40, 0, 200]
+    v, do = scan_case(1, 461, C, N, lens, dtype, True, 80), randn((1, 461, C), dtype, 90)
+    bad = {k: t.clone() for k, t in v.items()}
+    bad["x"][0, 80, 10] = float("inf")  # all in the third sequence, tokens 71 to 220
+    bad["dt"][0, 100, 21] = float("nan")
+    bad["z"][0, 150, 30] = float("nan")
+    final = torch.empty((2, len(lens), C, N), device=DEV)
+    out = [call_scan(w, lens, True, h_final=f) for w, f in zip((v, bad), final)]
+
+    def gradients(w):
+        a = {k: dev(t) for k, t in w.items()}
+        return gdn.gdn_ssm_bwd(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], dev(do), D=a["D"], z=a["z"],
+                               dt_bias=a["dt_bias"], dt_softplus=True, h0=a["h0"], cu_seqlens=dev(cu_of(lens)))
+    clean, got = gradients(v), gradients(bad)
+    apart = torch.ones(461, C, dtype=torch.bool)  # of what must not change
+    apart[80:221, 10] = apart[100:221, 21] = apart[150, 30] = False
+    assert not out[1][0, 80:221, 10].isfinite().any() and out[1][0, 100:221, 21].isnan().all()
+    tol = TOL_BF if dtype == BF else TOL_SCAN  # (a neighbour's shared reciprocal may round differently)
+    assert rel(out[1][0].cpu()[apart], out[0][0].cpu()[apart]) <= tol
+    channels = [c for c in range(C) if c not in (10, 21, 30)]
+    others = [i for i in range(len(lens)) if i != 2]
+    apart[71:221, [10, 21, 30]] = False
+    tokens = [t for t in range(461) if not 71 <= t < 221]
+    for f in (final.cpu(), torch.stack([clean["dh0"], got["dh0"]]).cpu()):
+        assert rel(f[1][others], f[0][others]) <= TOL_SCAN
+        assert rel(f[1][2][channels], f[0][2][channels]) <= TOL_SCAN
+    for k in ("dx", "ddt", "dz"):
+        assert rel(got[k][0].cpu()[apart], clean[k][0].cpu()[apart]) <= tol, k
+    for k in ("dBm", "dCm"):
+        assert rel(got[k][0, tokens], clean[k][0, tokens]) <= tol, k
+    for k in ("dA", "dD", "ddt_bias"):
+        assert rel(got[k][channels], clean[k][channels]) <= TOL_SCAN, k
+
+
 def test_scan_gradient_by_differences():
     v = scan_case(1, 40, 24, 16, [17, 23], F32, True, 80)
     do, df = randn((1, 40, 24), F32, 90), randn((2, 24, 16), F32, 91)
