@@ -11,9 +11,13 @@
 // channels (one vector access a token), walks a run of tokens and holds the
 // window in registers, so each input is read from HBM once; the W - 1 tokens
 // before its run come from L1 or L2. The next four tokens' loads are under
-// way while four are computed, in packed pairs of channels. Packed batches need no second form: a
-// thread finds the sequence of its first token by bisection and swaps the
-// window for the next sequence's carried one where that begins.
+// way while four are computed, in packed pairs of channels; four tokens of one
+// sequence run without a branch. Packed batches need no second form: a thread
+// finds the sequence of its first token by bisection and swaps the window for
+// the next sequence's carried one where that begins. 16384 tokens of 4096
+// channels, 4 taps, bf16: 57 us for 268 MB (69% of the measured copy rate),
+// the gradient 92 us for 403 MB (64%). What holds them is the loads'
+// latency at the 21 warps a SM that 80 registers leave (15 at 128).
 #include "gdn_ssm.cuh"
 
 namespace gdn {

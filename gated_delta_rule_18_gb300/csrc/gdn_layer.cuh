@@ -15,15 +15,10 @@ namespace gdn {
 // access; otherwise element accesses, of which only the first n are made
 // (rows of any length and alignment).
 template <typename T, int N>
-struct RowVec {
+struct RowVec {  // in 32-bit words
     static constexpr int kBytes = N * (int)sizeof(T);
     static constexpr int kWords = kBytes / 4;
     static_assert(kBytes == 4 || kBytes == 8 || kBytes % 16 == 0, "vector size");
-    union U {
-        uint32_t w[kWords];
-        T e[N];
-        __device__ U() {}
-    };
 };
 template <int WORDS>
 __device__ __forceinline__ void ld_words(uint32_t (&w)[WORDS], const void *p) {

@@ -17,9 +17,11 @@
 //                 registers;
 //   ssm_bwd_reduce  dB and dC over the channel tiles; dA, dD and dbias over
 //                 the runs. Every sum has one order.
-// Bound by instruction issue and the fp32 pipe: the states' decays are formed
-// three times (12 cycles an element on the exponential unit) and the walk back
-// has ten packed operations an element pair.
+// Bound by instruction issue and the latencies between dependent ones (12
+// warps a SM): the states' decays are formed three times (12 cycles a warp for
+// 32 elements on the exponential unit) and the walk back has ten packed
+// operations an element pair. 4 x 4096 tokens of 4096 channels, 16 states,
+// bf16: sums 409 us, chain 72, walk 1476, sums of parts 35.
 #include "gdn_ssm.cuh"
 
 namespace gdn {
@@ -733,7 +735,9 @@ int ssm_bwd_tiles(int D, int N) {
     const int ch = kWalk / walk_lanes(N);
     return (D + ch - 1) / ch;
 }
-// Tokens a run: 256, less where there are few channels.
+// Tokens a run: 256, less while that leaves under eight CTAs a SM. 4 x 4096
+// tokens of 4096 channels: runs of 512 make the walk 1.55 ms for 1.48 (a last
+// wave of long CTAs), runs of 128 store and chain twice as many gradients.
 int ssm_bwd_run(int lines, int T, int D, int N) {
     int len = 256;
     while (len > kGroup && (int64_t)lines * ssm_bwd_tiles(D, N) * ((T + len - 1) / len) < 1216) len /= 2;
