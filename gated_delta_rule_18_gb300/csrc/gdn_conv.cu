@@ -10,20 +10,27 @@
 // All are bound by HBM (2 W + 5 operations per 4 bytes). A thread keeps a few
 // channels (one vector access a token), walks a run of tokens and holds the
 // window in registers, so each input is read from HBM once; the W - 1 tokens
-// before its run come from L1 or L2. The next four tokens' loads are under
-// way while four are computed, in packed pairs of channels; four tokens of one
-// sequence run without a branch. Packed batches need no second form: a thread
-// finds the sequence of its first token by bisection and swaps the window for
-// the next sequence's carried one where that begins. 16384 tokens of 4096
-// channels, 4 taps, bf16: 57 us for 268 MB (69% of the measured copy rate),
-// the gradient 92 us for 403 MB (64%). What holds them is the loads'
-// latency at the 21 warps a SM that 80 registers leave (15 at 128).
+// before its run come from L1 or L2. The next twelve tokens' rows are under
+// way to shared memory while four are computed, in packed pairs of channels;
+// four tokens of one sequence run without a branch. Packed batches need no
+// second form: a thread finds the sequence of its first token by bisection and
+// swaps the window for the next sequence's carried one where that begins.
+// 16384 tokens of 4096 channels, 4 taps: bf16 54.5 us for 268 MB (73% of the
+// measured copy rate), fp32 90.5 (87%); the gradient 90 us for 403 MB (66%)
+// and 144 (82%). With the rows held in registers, four tokens ahead: 59, 95,
+// 95 and 171. In bf16 the instructions of a value (conversions, taps, sigmoid)
+// weigh as much as its bytes.
 #include "gdn_ssm.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kConvY = 4, kConvYBwd = 8;
+// Groups of four tokens in shared memory. Gradient, 4 x 4096 tokens of 4096
+// channels: bf16 89, 86, 90 us for 4, 3, 2 (two CTAs a SM), fp32 138, 144, 167.
+constexpr int kAhead = 4;
+template <typename T>
+constexpr int kAheadBwd = sizeof(T) == 4 ? 4 : 3;
 
 // The sequence of a token: the last s with cu[s] <= t, its bounds clamped so
 // that a malformed cu cannot send an access out of range.
@@ -149,6 +156,41 @@ __device__ __forceinline__ void check_cu(const int32_t *cu, int n_seq, int T, in
     if (tid == 0) *err = bad ? 1 : 0;
 }
 
+// A thread's own rows on their way: groups of U tokens of one tensor, S - 1 of
+// them under way while one is used. Wide rows go by asynchronous copies to
+// slots of shared memory that only this thread touches (so nothing is waited
+// for but its own copies, and no registers hold what is under way); others
+// through registers, one group ahead.
+template <typename T, int NC, int U, bool VEC, int NT, int GROUPS>
+struct Ahead {
+    static constexpr int NW = RowVec<T, NC>::kWords, S = VEC ? GROUPS : 2;
+    static constexpr int words() { return VEC ? S * U * NT * NW : 0; }  // of all threads
+    uint32_t *slots;                                              // this thread's first one
+    uint32_t next[VEC ? 1 : U][NW];
+    __device__ __forceinline__ uint32_t *slot(int g, int u) { return slots + ((g % S) * U + u) * NT * NW; }
+    // row u of group g; on: it exists
+    __device__ __forceinline__ void fetch(int g, int u, const T *row, int n, bool on) {
+        if (!on) return;
+        if constexpr (VEC) copy_async<NW * 4>(slot(g, u), row);
+        else ld_row<T, NC, false>(next[u], row, n);
+    }
+    // this thread's copies but those of the last S - 2 groups have arrived
+    static __device__ __forceinline__ void arrived() {
+        if (VEC) copies_arrived<S - 2>();
+    }
+    __device__ __forceinline__ void take(uint32_t (&raw)[U][NW], int g) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if constexpr (VEC) {
+                ld_words(raw[u], slot(g, u));
+            } else {
+#pragma unroll
+                for (int i = 0; i < NW; ++i) raw[u][i] = next[u][i];
+            }
+        }
+    }
+};
+
 template <typename T, int NC, int W, bool VEC>
 __global__ void __launch_bounds__(32 * kConvY, sizeof(T) == 2 && W <= 4 ? 6 : 3) conv_kernel(const ConvParams p, int nblk, int run) {
     constexpr int NW = RowVec<T, NC>::kWords, U = 4;
@@ -176,20 +218,26 @@ __global__ void __launch_bounds__(32 * kConvY, sizeof(T) == 2 && W <= 4 ? 6 : 3)
     load_taps<T, NC, W, VEC>(w, bias, p.weight, p.bias, c, n);
     Seq q = find_seq(p.cu, p.n_seq, p.T, b, t0);
     load_window<T, NC, W, VEC>(win, p, x, t0, q, c, n);
-    uint32_t next[U][NW];
+    using Rows = Ahead<T, NC, U, VEC, 32 * kConvY, kAhead>;
+    extern __shared__ __align__(16) uint32_t ring[];
+    Rows in;
+    in.slots = ring + (threadIdx.y * 32 + threadIdx.x) * NW;
     const T *xp = x + (int64_t)t0 * p.x_st;  // the next load's and store's rows
     T *op = out + (int64_t)t0 * p.o_st;
-    auto fetch = [&](int t) {
+    int put = 0, got = 0;
+    auto fetch = [&] {
+        const int t = t0 + put * U;
         if (t + U <= t1) {
 #pragma unroll
-            for (int u = 0; u < U; ++u, xp += p.x_st) ld_row<T, NC, VEC>(next[u], xp, n);
+            for (int u = 0; u < U; ++u, xp += p.x_st) in.fetch(put, u, xp, n, true);
         } else {
 #pragma unroll
-            for (int u = 0; u < U; ++u, xp += p.x_st)
-                if (t + u < t1) ld_row<T, NC, VEC>(next[u], xp, n);
+            for (int u = 0; u < U; ++u, xp += p.x_st) in.fetch(put, u, xp, n, t + u < t1);
         }
+        if (VEC) cp_async_commit();
+        ++put;
     };
-    fetch(t0);
+    for (int i = 0; i + 1 < Rows::S; ++i) fetch();
     auto window_out = [&](int seg) {
 #pragma unroll
         for (int k = 1; k < W; ++k)
@@ -209,11 +257,9 @@ __global__ void __launch_bounds__(32 * kConvY, sizeof(T) == 2 && W <= 4 ? 6 : 3)
     };
     for (int t = t0; t < t1; t += U) {
         uint32_t raw[U][NW];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < NW; ++i) raw[u][i] = next[u][i];
-        fetch(t + U);
+        Rows::arrived();
+        in.take(raw, got++);
+        fetch();
         if (t == q.s1) {
             next_seq(q, p.cu, p.n_seq, t);
             load_window<T, NC, W, VEC>(win, p, x, t, q, c, n);
@@ -324,7 +370,7 @@ __global__ void __launch_bounds__(32 * kConvYBwd, sizeof(T) == 2 && W <= 4 ? 2 :
     }
     const int64_t first = ((int64_t)blockIdx.x * kConvYBwd + threadIdx.y) * run;
     if (c < p.D && first < p.T) {
-        constexpr int U = 4;
+        constexpr int U = VEC ? 4 : 2;
         const int t0 = (int)first, t1 = min(p.T - t0, run) + t0, t2 = min(p.T - t1, W - 1) + t1;
         const T *xs = (const T *)p.x + b * p.x_sb + c;
         const T *ds = (const T *)p.dout + b * p.do_sb + c;
@@ -336,26 +382,32 @@ __global__ void __launch_bounds__(32 * kConvYBwd, sizeof(T) == 2 && W <= 4 ? 2 :
         for (int k = 0; k < W; ++k)
 #pragma unroll
             for (int i = 0; i < NC / 2; ++i) pend[k][i] = pack2(0.f, 0.f);
-        uint32_t nx[U][NW], nd[U][NW];
+        using Rows = Ahead<T, NC, U, VEC, 32 * kConvYBwd, kAheadBwd<T>>;
+        Rows in_x, in_d;
+        in_x.slots = reinterpret_cast<uint32_t *>(red + 32 * kConvYBwd * NC * (W + 1)) + (threadIdx.y * 32 + threadIdx.x) * NW;
+        in_d.slots = in_x.slots + Rows::words();
         const T *xp = xs + (int64_t)t0 * p.x_st, *dp_ = ds + (int64_t)t0 * p.do_st;  // the next loads' rows
         T *op = dx + (int64_t)(t0 - (W - 1)) * p.D;                                   // of the next dx
-        auto fetch = [&](int t) {
+        int put = 0, got = 0;
+        auto fetch = [&] {
+            const int t = t0 + put * U;
             if (t + U <= t2) {
 #pragma unroll
                 for (int u = 0; u < U; ++u, xp += p.x_st, dp_ += p.do_st) {
-                    ld_row<T, NC, VEC>(nx[u], xp, n);
-                    ld_row<T, NC, VEC>(nd[u], dp_, n);
+                    in_x.fetch(put, u, xp, n, true);
+                    in_d.fetch(put, u, dp_, n, true);
                 }
             } else {
 #pragma unroll
-                for (int u = 0; u < U; ++u, xp += p.x_st, dp_ += p.do_st)
-                    if (t + u < t2) {
-                        ld_row<T, NC, VEC>(nx[u], xp, n);
-                        ld_row<T, NC, VEC>(nd[u], dp_, n);
-                    }
+                for (int u = 0; u < U; ++u, xp += p.x_st, dp_ += p.do_st) {
+                    in_x.fetch(put, u, xp, n, t + u < t2);
+                    in_d.fetch(put, u, dp_, n, t + u < t2);
+                }
             }
+            if (VEC) cp_async_commit();
+            ++put;
         };
-        fetch(t0);
+        for (int i = 0; i + 1 < Rows::S; ++i) fetch();
         // one token: own, its dw and db count; s0, its sequence's first token
         auto token = [&](int t, const uint32_t (&rx)[NW], const uint32_t (&rd)[NW], bool own, bool whole) {
             f32x2 x[NC / 2], go[NC / 2], dp[NC / 2];
@@ -395,8 +447,10 @@ __global__ void __launch_bounds__(32 * kConvYBwd, sizeof(T) == 2 && W <= 4 ? 2 :
                 uint32_t cx[NW], cd[NW];
 #pragma unroll
                 for (int i = 0; i < NW; ++i) {
-                    cx[i] = u == 0 ? rx[0][i] : u == 1 ? rx[1][i] : u == 2 ? rx[2][i] : rx[3][i];
-                    cd[i] = u == 0 ? rd[0][i] : u == 1 ? rd[1][i] : u == 2 ? rd[2][i] : rd[3][i];
+                    cx[i] = rx[0][i], cd[i] = rd[0][i];
+#pragma unroll
+                    for (int k = 1; k < U; ++k)
+                        if (u == k) cx[i] = rx[k][i], cd[i] = rd[k][i];
                 }
                 shift();
                 if (t < t2) {
@@ -419,11 +473,9 @@ __global__ void __launch_bounds__(32 * kConvYBwd, sizeof(T) == 2 && W <= 4 ? 2 :
         };
         for (int tb = t0; tb < t1 + W - 1; tb += U) {
             uint32_t rx[U][NW], rd[U][NW];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < NW; ++i) rx[u][i] = nx[u][i], rd[u][i] = nd[u][i];
-            fetch(tb + U);
+            Rows::arrived();
+            in_x.take(rx, got), in_d.take(rd, got++);
+            fetch();
             // without a branch: tokens that, with the W - 1 before and after them, are one sequence's
             const bool inside = tb - (W - 1) >= q.s0;
             if (inside && tb + U <= t1 && tb + U <= q.s1 - (W - 1)) {
@@ -535,7 +587,7 @@ cudaError_t conv_t(const ConvParams &p, cudaStream_t st) {
     const bool extra = p.cu != nullptr || p.T == 0;
     const dim3 grid(nblk + (extra ? 1 : 0), (p.D + 32 * NC - 1) / (32 * NC), p.T == 0 ? 1 : p.B), block(32, kConvY);
     return by_taps(p.W, [&](auto w) {
-        if (p.vec) conv_kernel<T, NC, w(), true><<<grid, block, 0, st>>>(p, nblk, run);
+        if (p.vec) conv_kernel<T, NC, w(), true><<<grid, block, 4 * Ahead<T, NC, 4, true, 32 * kConvY, kAhead>::words(), st>>>(p, nblk, run);
         else conv_kernel<T, NC, w(), false><<<grid, block, 0, st>>>(p, nblk, run);
         return cudaGetLastError();
     });
@@ -548,9 +600,16 @@ cudaError_t conv_bwd_t(const ConvParams &p, cudaStream_t st) {
     const dim3 grid(nblk + (extra ? 1 : 0), (p.D + 32 * NC - 1) / (32 * NC), p.T == 0 ? 1 : p.B),
         block(32, kConvYBwd);
     return by_taps(p.W, [&](auto w) {
-        const size_t smem = sizeof(float) * 32 * kConvYBwd * NC * (w() + 1);
-        if (p.vec) conv_bwd_kernel<T, NC, w(), true><<<grid, block, smem, st>>>(p, nblk, run);
-        else conv_bwd_kernel<T, NC, w(), false><<<grid, block, smem, st>>>(p, nblk, run);
+        constexpr int smem = (int)sizeof(float) * 32 * kConvYBwd * NC * (w() + 1);
+        if (p.vec) {
+            constexpr int all = smem + 8 * Ahead<T, NC, 4, true, 32 * kConvYBwd, kAheadBwd<T>>::words();
+            const cudaError_t e =
+                cudaFuncSetAttribute(conv_bwd_kernel<T, NC, w(), true>, cudaFuncAttributeMaxDynamicSharedMemorySize, all);
+            if (e != cudaSuccess) return e;
+            conv_bwd_kernel<T, NC, w(), true><<<grid, block, all, st>>>(p, nblk, run);
+            return cudaGetLastError();
+        }
+        conv_bwd_kernel<T, NC, w(), false><<<grid, block, smem, st>>>(p, nblk, run);
         return cudaGetLastError();
     });
 }

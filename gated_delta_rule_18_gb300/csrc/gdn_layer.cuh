@@ -47,6 +47,16 @@ __device__ __forceinline__ void st_words(void *p, const uint32_t (&w)[WORDS]) {
             static_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
 }
+// Asynchronous copies that only the issuing thread waits for and reads
+// (ordered against its other accesses, hence the clobbers).
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *smem, const void *gmem) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(smem_u32(smem)), "l"(gmem), "n"(BYTES) : "memory");
+}
+template <int LEFT>  // all but the last LEFT groups
+__device__ __forceinline__ void copies_arrived() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(LEFT) : "memory");
+}
 template <typename T>
 __device__ __forceinline__ T to_type(float x);
 template <>
