@@ -164,7 +164,7 @@ __device__ __forceinline__ void check_cu(const int32_t *cu, int n_seq, int T, in
 template <typename T, int NC, int U, bool VEC, int NT, int GROUPS>
 struct Ahead {
     static constexpr int NW = RowVec<T, NC>::kWords, S = VEC ? GROUPS : 2;
-    static constexpr int words() { return VEC ? S * U * NT * NW : 0; }  // of all threads
+    static constexpr __host__ __device__ int words() { return VEC ? S * U * NT * NW : 0; }  // of all threads
     uint32_t *slots;                                              // this thread's first one
     uint32_t next[VEC ? 1 : U][NW];
     __device__ __forceinline__ uint32_t *slot(int g, int u) { return slots + ((g % S) * U + u) * NT * NW; }
