@@ -12,8 +12,10 @@
 // a thread), the row's sum crosses warps once through shared memory, and the
 // result is written once. Sums, the norm and the scales are fp32. 16384 rows
 // of 4096 bf16 channels with an fp32 residual to 8 bits: 115 us, 6.5 TB/s or
-// 95% of the measured copy rate. 16384 rows of 2048, bf16, the gradient: 53 us
-// for its 268 MB (75%), limited by its registers (97 a thread: 16 warps a SM).
+// 95% of the measured copy rate. 16384 rows of 2048, bf16, the gradient: 48 us
+// for 268 MB (82%) and 5 more for the sum of dw's parts; 8192 rows of 8192,
+// fp32: 183 us for 1.07 GB (86%). With the next row in registers instead of
+// shared memory: 49 and 244.
 #include "gdn_ssm.cuh"
 
 namespace gdn {
@@ -234,8 +236,11 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormParams p, int tp
 // all there is when one channel dominates its row), so both sums lose them
 // first: with S = sum s^2, G = sum w dy s,
 //   ds_i = inv [ inv^2 / D (w dy_i (S - s_i^2) - s_i (G - w dy_i s_i)) + eps inv^2 w dy_i ].
-// PRE: the next row's loads are issued before this row's sum is known.
-template <typename TS, typename TY, int NV, bool VEC, bool PRE>
+// Rows in shared memory: of three, four CTAs a SM keep theirs (2048 channels, bf16: 51, 48
+// and 60 us with two, three and four); two of fp32 take as much.
+template <typename TS, typename TY>
+constexpr int kRowsAhead = sizeof(TS) + sizeof(TY) == 4 ? 3 : 2;
+template <typename TS, typename TY, int NV, bool VEC, bool AHEAD>
 __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdParams p, int tpr) {
     __shared__ __align__(16) float red[2][2][16];
     constexpr int WS = RowVec<TS, kVecN>::kWords, WY = RowVec<TY, kVecN>::kWords;
@@ -249,38 +254,76 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdParams p,
         for (int j = 0; j < kPairs; ++j) dw[i][j] = pack2(0.f, 0.f);
     const int64_t step = (int64_t)gridDim.x * rpb;
     int64_t row = (int64_t)blockIdx.x * rpb + lr;
-    uint32_t ns[NV][WS], ny[NV][WY], nr[NV][WS];
-    auto fetch = [&](int64_t r) {
+    // Rows on their way: asynchronous copies to this thread's own slots of
+    // shared memory, S - 1 rows ahead, where rows are wide (AHEAD); else loaded
+    // where they are used.
+    constexpr int S = kRowsAhead<TS, TY>, P = NV * (2 * WS + WY) / 4;
+    extern __shared__ __align__(16) uint4 slots[];
+    auto slot = [&](int g, int k) { return slots + ((g % S) * P + k) * blockDim.x + threadIdx.x; };
+    uint32_t rs[NV][WS], ry[NV][WY], rr[NV][WS];
+    int got = 0;
+    auto fetch = [&](int64_t r, int g) {
+        if (r < p.R) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * tpr + tid) * kVecN;
+                if (c >= p.D) continue;
+                const TS *s = (const TS *)p.s + r * p.s_st + c, *q = (const TS *)p.dres + r * p.dr_st + c;
+                const TY *y = (const TY *)p.dy + r * p.dy_st + c;
+#pragma unroll
+                for (int k = 0; k < WS / 4; ++k) copy_async<16>(slot(g, i * (WS / 4) + k), s + k * 16 / sizeof(TS));
+#pragma unroll
+                for (int k = 0; k < WY / 4; ++k)
+                    copy_async<16>(slot(g, NV * WS / 4 + i * (WY / 4) + k), y + k * 16 / sizeof(TY));
+                if (p.dres) {
+#pragma unroll
+                    for (int k = 0; k < WS / 4; ++k)
+                        copy_async<16>(slot(g, NV * (WS + WY) / 4 + i * (WS / 4) + k), q + k * 16 / sizeof(TS));
+                }
+            }
+        }
+        cp_async_commit();
+    };
+    auto take = [&](int64_t r) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + tid) * kVecN;
             if (r < p.R && c < p.D) {
-                ld_row<TS, kVecN, VEC>(ns[i], (const TS *)p.s + r * p.s_st + c, p.D - c);
-                ld_row<TY, kVecN, VEC>(ny[i], (const TY *)p.dy + r * p.dy_st + c, p.D - c);
-                if (p.dres) ld_row<TS, kVecN, VEC>(nr[i], (const TS *)p.dres + r * p.dr_st + c, p.D - c);
+                if constexpr (AHEAD) {
+                    auto read = [&](auto &w, int k0) {
+                        constexpr int N = sizeof(w) / 16;
+#pragma unroll
+                        for (int k = 0; k < N; ++k) {
+                            const uint4 u = *slot(got, k0 + i * N + k);
+                            w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
+                        }
+                    };
+                    read(rs[i], 0), read(ry[i], NV * WS / 4);
+                    if (p.dres) read(rr[i], NV * (WS + WY) / 4);
+                } else {
+                    ld_row<TS, kVecN, VEC>(rs[i], (const TS *)p.s + r * p.s_st + c, p.D - c);
+                    ld_row<TY, kVecN, VEC>(ry[i], (const TY *)p.dy + r * p.dy_st + c, p.D - c);
+                    if (p.dres) ld_row<TS, kVecN, VEC>(rr[i], (const TS *)p.dres + r * p.dr_st + c, p.D - c);
+                }
             } else {
 #pragma unroll
-                for (int j = 0; j < WS; ++j) ns[i][j] = 0u;
+                for (int j = 0; j < WS; ++j) rs[i][j] = 0u;
 #pragma unroll
-                for (int j = 0; j < WY; ++j) ny[i][j] = 0u;
+                for (int j = 0; j < WY; ++j) ry[i][j] = 0u;
             }
         }
     };
-    if (PRE) fetch(row);
+    if constexpr (AHEAD) {
+#pragma unroll
+        for (int g = 0; g + 1 < S; ++g) fetch(row + g * step, g);
+    }
     const float rd = 1.f / (float)p.D;
     int flip = 0;
     // every thread of the CTA makes the same number of turns
-    for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < p.R; r0 += step, row += step, flip ^= 1) {
-        if (!PRE) fetch(row);
-        uint32_t rs[NV][WS], ry[NV][WY], rr[NV][WS];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-#pragma unroll
-            for (int j = 0; j < WS; ++j) rs[i][j] = ns[i][j], rr[i][j] = nr[i][j];
-#pragma unroll
-            for (int j = 0; j < WY; ++j) ry[i][j] = ny[i][j];
-        }
-        if (PRE) fetch(row + step);
+    for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < p.R; r0 += step, row += step, flip ^= 1, ++got) {
+        if constexpr (AHEAD) copies_arrived<S - 2>();
+        take(row);
+        if constexpr (AHEAD) fetch(row + (S - 1) * step, got + S - 1);
         f32x2 ss2 = pack2(0.f, 0.f), gs2 = ss2;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -389,15 +432,22 @@ template <typename TS, typename TY>
 cudaError_t norm_bwd_nv(const NormBwdParams &p, cudaStream_t st) {
     const RowShape s = row_shape(p.D, 2);
     const unsigned grid = norm_bwd_parts(p.R, p.D) / s.rpb, nt = s.tpr * s.rpb;
-    auto run = [&](auto vec) {
-        constexpr bool V = decltype(vec)::value;
-        if (s.nv == 1) rmsnorm_bwd_kernel<TS, TY, 1, V, true><<<grid, nt, 0, st>>>(p, s.tpr);
-        else if (s.nv == 2) rmsnorm_bwd_kernel<TS, TY, 2, V, true><<<grid, nt, 0, st>>>(p, s.tpr);
-        else rmsnorm_bwd_kernel<TS, TY, 4, V, false><<<grid, nt, 0, st>>>(p, s.tpr);
+    auto run = [&](auto nv, auto vec, auto ahead) -> cudaError_t {
+        auto *k = rmsnorm_bwd_kernel<TS, TY, nv(), vec(), ahead()>;
+        const int smem = ahead() ? kRowsAhead<TS, TY> * nv() * (2 * sizeof(TS) + sizeof(TY)) * kVecN * nt : 0;
+        if (smem > 40 * 1024) {  // 48 KB with the static part
+            const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+        }
+        k<<<grid, nt, smem, st>>>(p, s.tpr);
+        return cudaGetLastError();
     };
-    if (p.vec) run(std::true_type());
-    else run(std::false_type());
-    return cudaGetLastError();
+    auto by_vectors = [&](auto vec) {
+        if (s.nv == 1) return run(std::integral_constant<int, 1>(), vec, vec);
+        if (s.nv == 2) return run(std::integral_constant<int, 2>(), vec, vec);
+        return run(std::integral_constant<int, 4>(), vec, std::false_type());
+    };
+    return p.vec ? by_vectors(std::true_type()) : by_vectors(std::false_type());
 }
 
 }  // namespace
