@@ -200,35 +200,38 @@ struct SsmBc {
 };
 
 // ------------------------------------------------------------- states -------
-// Q neighbouring states of a channel, in pairs
+// Q neighbouring states of a channel, in pairs; swap = 1: neighbouring quads
+// change places
 template <int Q>
-__device__ __forceinline__ void ld_states(f32x2 (&v)[Q / 2], const float *p, int n, bool wide) {
+__device__ __forceinline__ void ld_states(f32x2 (&v)[Q / 2], const float *p, int n, bool wide, int swap = 0) {
 #pragma unroll
     for (int j = 0; j < Q / 4; ++j) {
+        const int k = 4 * (j ^ swap);
         float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
         if (wide) {
-            if (4 * j < n) f = reinterpret_cast<const float4 *>(p)[j];
+            if (k < n) f = *reinterpret_cast<const float4 *>(p + k);
         } else {
-            if (4 * j < n) f.x = p[4 * j];
-            if (4 * j + 1 < n) f.y = p[4 * j + 1];
-            if (4 * j + 2 < n) f.z = p[4 * j + 2];
-            if (4 * j + 3 < n) f.w = p[4 * j + 3];
+            if (k < n) f.x = p[k];
+            if (k + 1 < n) f.y = p[k + 1];
+            if (k + 2 < n) f.z = p[k + 2];
+            if (k + 3 < n) f.w = p[k + 3];
         }
         v[2 * j] = pack2(f.x, f.y), v[2 * j + 1] = pack2(f.z, f.w);
     }
 }
 template <int Q>
-__device__ __forceinline__ void st_states(float *p, const f32x2 (&v)[Q / 2], int n, bool wide) {
+__device__ __forceinline__ void st_states(float *p, const f32x2 (&v)[Q / 2], int n, bool wide, int swap = 0) {
 #pragma unroll
     for (int j = 0; j < Q / 4; ++j) {
+        const int k = 4 * (j ^ swap);
         const float2 a = unpack2(v[2 * j]), b = unpack2(v[2 * j + 1]);
         if (wide) {
-            if (4 * j < n) reinterpret_cast<float4 *>(p)[j] = make_float4(a.x, a.y, b.x, b.y);
+            if (k < n) *reinterpret_cast<float4 *>(p + k) = make_float4(a.x, a.y, b.x, b.y);
         } else {
-            if (4 * j < n) p[4 * j] = a.x;
-            if (4 * j + 1 < n) p[4 * j + 1] = a.y;
-            if (4 * j + 2 < n) p[4 * j + 2] = b.x;
-            if (4 * j + 3 < n) p[4 * j + 3] = b.y;
+            if (k < n) p[k] = a.x;
+            if (k + 1 < n) p[k + 1] = a.y;
+            if (k + 2 < n) p[k + 2] = b.x;
+            if (k + 3 < n) p[k + 3] = b.y;
         }
     }
 }

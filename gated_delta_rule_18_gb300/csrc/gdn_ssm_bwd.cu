@@ -21,7 +21,7 @@
 // warps a SM): the states' decays are formed three times (12 cycles a warp for
 // 32 elements on the exponential unit) and the walk back has ten packed
 // operations an element pair. 4 x 4096 tokens of 4096 channels, 16 states,
-// bf16: sums 409 us, chain 61, walk 1476, sums of parts 35.
+// bf16: sums 409 us, chain 61, walk 1403 (fp32 1726), sums of parts 35.
 #include "gdn_ssm.cuh"
 
 namespace gdn {
@@ -279,15 +279,6 @@ __global__ void __launch_bounds__(256) ssm_bwd_chain_kernel(const SsmParams p, i
 // -------------------------------------------------------------- walk back ---
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// D += A B, m16n8k8, tf32 operands (the low 13 bits of an fp32 are ignored)
-__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 constexpr int kWalk = 128;  // threads of the walk's CTA
 
 // Lanes: lane = ln * CL + lc has channel lc of its warp and states ln Q ..
@@ -297,30 +288,47 @@ constexpr int kWalk = 128;  // threads of the walk's CTA
 // warps a scheduler, 1.9 to 2.3 ms for 16384 tokens of 4096 channels).
 //
 // dB and dC are sums over channels, i.e. over lanes: 2 Q values a lane and
-// token. The tensor cores add them over the lane's neighbours, against ones:
-// with four of the lane's values as the A fragment (rows lane / 4 and + 8,
-// columns lane % 4 and + 4) and B taking its upper four rows to column 2 i and
-// its lower four to 2 i + 1, an m16n8k8 adds the values over the four lanes
-// and leaves them to lane % 4 = i: four of them leave 16 sums, four a lane. The
-// lanes that still have parts of the same sums (lane / 4) share them out by
-// shuffles. Products enter as tf32: for bf16 tensors truncated (an error
-// under 2^-10 of a term against the result's 2^-9), for fp32 ones as the sum
-// of two parts (2^-21).
-template <typename T>
-__device__ __forceinline__ void mma_sum(float (&d)[4], f32x2 v0, f32x2 v1, uint32_t b0, uint32_t b1) {
-    const float2 a = unpack2(v0), c = unpack2(v1);
-    const float v[4] = {a.x, a.y, c.x, c.y};
-    if constexpr (sizeof(T) == 2) {
-        mma_tf32(d, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]), b0, b1);
-    } else {
-        uint32_t h[4], l[4];
+// token, in fp32 and apart for every state, so that a rounding or a value that
+// is not finite stays in its own sum. Eight states at a time: at each step two
+// lanes, one bit of the channel apart, exchange the half of the values that
+// the other one goes on with: quads of states, dB or dC, pairs, elements
+// (8 + 4 + 2 + 1 shuffles of 16 values for 16 lanes). Lanes of odd channels hold
+// their quads in swapped order, so that the first exchange, of half of all
+// shuffles, selects nothing. (By tensor-core products against ones: in tf32,
+// 1476 us for 1403 here, in two parts for fp32 tensors 2053 for 1726, and a
+// value that is not finite spread over eight states of both sums.)
+__device__ __forceinline__ f32x2 shfl_xor2(f32x2 v, int lanes) {
+    const float2 f = unpack2(v);
+    return pack2(__shfl_xor_sync(0xffffffffu, f.x, lanes), __shfl_xor_sync(0xffffffffu, f.y, lanes));
+}
+// rb, rc: eight states of a channel, own quad first. Adds the sums over CL
+// neighbouring lanes to to[0 .. 7] (dB) and to[np .. np + 7] (dC), where two
+// warps add to zeros: either order gives the same sum.
+template <int CL>
+__device__ __forceinline__ void channel_sums(const f32x2 *rb, const f32x2 *rc, float *to, int np, int lane) {
+    const bool u1 = lane & 2;
+    f32x2 k[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            h[i] = __float_as_uint(v[i]) & 0xffffe000u;
-            l[i] = __float_as_uint(v[i] - __uint_as_float(h[i]));
+    for (int i = 0; i < 2; ++i) {
+        const f32x2 b = add2(rb[i], shfl_xor2(rb[2 + i], 1)), c = add2(rc[i], shfl_xor2(rc[2 + i], 1));
+        k[i] = add2(u1 ? c : b, shfl_xor2(u1 ? b : c, 2));
+    }
+    to += (u1 ? np : 0) + (lane & 1) * 4;
+    if constexpr (CL == 4) {
+        const float2 f0 = unpack2(k[0]), f1 = unpack2(k[1]);
+        atomicAdd(to, f0.x), atomicAdd(to + 1, f0.y), atomicAdd(to + 2, f1.x), atomicAdd(to + 3, f1.y);
+    } else {
+        const bool u2 = lane & 4;
+        const float2 f = unpack2(add2(u2 ? k[1] : k[0], shfl_xor2(u2 ? k[0] : k[1], 4)));
+        to += u2 ? 2 : 0;
+        if constexpr (CL == 8) {
+            atomicAdd(to, f.x), atomicAdd(to + 1, f.y);
+        } else {
+            const bool u3 = lane & 8;
+            float s = (u3 ? f.y : f.x) + __shfl_xor_sync(0xffffffffu, u3 ? f.x : f.y, 8);
+            if (CL == 32) s += __shfl_xor_sync(0xffffffffu, s, 16);
+            if (CL == 16 || !(lane & 16)) atomicAdd(to + (u3 ? 1 : 0), s);
         }
-        mma_tf32(d, h[0], h[1], h[2], h[3], b0, b1);
-        mma_tf32(d, l[0], l[1], l[2], l[3], b0, b1);
     }
 }
 
@@ -336,7 +344,7 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
     float *part = bcs + kPart;                                  // [2][TG][2][NP], two warps' sums each
     float4 *ckpt = reinterpret_cast<float4 *>(part + 2 * kPart);  // [TG / SUB - 2][Q / 4][kWalk]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int ln = lane / CL, lc = lane % CL, fk = ln & 1;
+    const int ln = lane / CL, lc = lane % CL, fk = ln & 1, sw = lc & 1;  // sw: quads of states swapped
     const int tile = blockIdx.x % ntile, item = blockIdx.x / ntile;
     const int line = item / p.nrun, run = item - line * p.nrun;
     const int r0 = run * p.rlen, r1 = min(p.T - r0, p.rlen) + r0;
@@ -348,14 +356,14 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
     const bool softplus = USUAL || p.softplus, gate = USUAL || p.z, vec = USUAL || p.vec;
 
     f32x2 a2[H], g[H], dA[H], h[H], w[SUB][H], a[SUB][H];
-    ld_states<Q>(a2, p.A + own, ns, p.n_wide);
+    ld_states<Q>(a2, p.A + own, ns, p.n_wide, sw);
 #pragma unroll
     for (int j = 0; j < H; ++j) {
         a2[j] = mul2(a2[j], pack2(kLog2e, kLog2e));
         g[j] = dA[j] = pack2(0.f, 0.f);
     }
     // from the run's end on
-    if (run + 1 < p.nrun) ld_states<Q>(g, p.gs + ((int64_t)line * p.nrun + run + 1) * dnp + own_p, qs, true);
+    if (run + 1 < p.nrun) ld_states<Q>(g, p.gs + ((int64_t)line * p.nrun + run + 1) * dnp + own_p, qs, true, sw);
     float dD = 0.f, dbias = 0.f;
     const float dv = p.Dv && d < p.D ? p.Dv[d] : 0.f, bias = p.dt_bias && d < p.D ? p.dt_bias[d] : 0.f;
     const T *src[4] = {(const T *)p.x + line * p.x_sb, (const T *)p.dt + line * p.dt_sb,
@@ -367,18 +375,9 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
     const int pc = tid % (CH / 2);
     const float2 pbias = make_float2(p.dt_bias && c0 + 2 * pc < p.D ? p.dt_bias[c0 + 2 * pc] : 0.f,
                                      p.dt_bias && c0 + 2 * pc + 1 < p.D ? p.dt_bias[c0 + 2 * pc + 1] : 0.f);
-    // B fragments of the channel sums, and what a lane has of them: matrix and first state
-    uint32_t sel0[4], sel1[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        sel0[q] = lane >> 2 == 2 * q ? 0x3f800000u : 0u;
-        sel1[q] = lane >> 2 == 2 * q + 1 ? 0x3f800000u : 0u;
-    }
-    const int mat = lane >> 1 & 1, quad = (lane & 1) * 4;
-
     auto boundary = [&](const float *from, int seg, f32x2 (&v)[H]) {  // a sequence's h0 or dh_final, or zero
         if (from) {
-            ld_states<Q>(v, from + seg * hrow + own, ns, p.n_wide);
+            ld_states<Q>(v, from + seg * hrow + own, ns, p.n_wide, sw);
         } else {
 #pragma unroll
             for (int j = 0; j < H; ++j) v[j] = pack2(0.f, 0.f);
@@ -461,7 +460,7 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
                 const float4 *b4 = reinterpret_cast<const float4 *>(bcs + i * 2 * NP + n0);
 #pragma unroll
                 for (int j = 0; j < Q / 4; ++j) {
-                    const float4 b = b4[j];
+                    const float4 b = b4[j ^ sw];
                     const f32x2 b2[2] = {pack2(b.x, b.y), pack2(b.z, b.w)};
 #pragma unroll
                     for (int l = 2 * j; l < 2 * j + 2; ++l) {
@@ -475,7 +474,7 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
             // where the walk reaches it, the last one's stays in registers
             auto enter = [&] {
                 if (grp > 0 && !(EDGE && (starts & 1u)))
-                    ld_states<Q>(h, p.sums + ((int64_t)line * p.ngroup + grp - 1) * dnp + own_p, qs, true);
+                    ld_states<Q>(h, p.sums + ((int64_t)line * p.ngroup + grp - 1) * dnp + own_p, qs, true, sw);
                 else
                     boundary(nullptr, 0, h);
             };
@@ -548,7 +547,7 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
                         f32x2 ys, gb, gd, rb[H], rc[H];
 #pragma unroll
                         for (int j = 0; j < Q / 4; ++j) {
-                            const float4 b = b4[j], c = b4[NP / 4 + j];
+                            const float4 b = b4[j ^ sw], c = b4[NP / 4 + (j ^ sw)];
                             const f32x2 b2[2] = {pack2(b.x, b.y), pack2(b.z, b.w)};
                             const f32x2 c2[2] = {pack2(c.x, c.y), pack2(c.z, c.w)};
 #pragma unroll
@@ -566,43 +565,15 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
                             }
                         }
                         if (EDGE && (starts >> t & 1u) && p.dh0)
-                            st_states<Q>(p.dh0 + seg_of(t) * hrow + own, g, ns, p.n_wide);
+                            st_states<Q>(p.dh0 + seg_of(t) * hrow + own, g, ns, p.n_wide, sw);
                         const float2 v0 = unpack2(ys), v1 = unpack2(gb), v2 = unpack2(gd);
                         r[i & 1][0] = v0.x + v0.y, r[i & 1][1] = v1.x + v1.y, r[i & 1][2] = v2.x + v2.y;
                         // over the channels: dB and dC. Two warps add to zeros: either order gives
                         // the same sum.
-                        float *pw = part + (warp >> 1) * kPart + t * 2 * NP + mat * NP;
+                        float *pw = part + (warp >> 1) * kPart + t * 2 * NP + n0;
 #pragma unroll
-                        for (int o = 0; o < Q / 8; ++o) {
-                            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                mma_sum<T>(acc, rb[4 * o + 2 * q], rb[4 * o + 2 * q + 1], sel0[q], sel1[q]);
-                                mma_sum<T>(acc, rc[4 * o + 2 * q], rc[4 * o + 2 * q + 1], sel0[2 + q], sel1[2 + q]);
-                            }
-                            // acc: states 0, 2, 1, 3 of quad lane % 4 (dB, dB, dC, dC), of the channels of
-                            // lanes with this lane / 4; bits 2, 3, 4 of the lane below CL are channels too
-                            float *po = pw + n0 + 8 * o + quad;
-                            if constexpr (CL == 4) {
-                                atomicAdd(po, acc[0]), atomicAdd(po + 1, acc[2]), atomicAdd(po + 2, acc[1]), atomicAdd(po + 3, acc[3]);
-                            } else {
-                                const bool u2 = lane & 4;
-                                const float g0 = u2 ? acc[0] : acc[2], g1 = u2 ? acc[1] : acc[3];
-                                float k0 = u2 ? acc[2] : acc[0], k1 = u2 ? acc[3] : acc[1];
-                                k0 += __shfl_xor_sync(0xffffffffu, g0, 4);
-                                k1 += __shfl_xor_sync(0xffffffffu, g1, 4);
-                                if constexpr (CL == 8) {
-                                    atomicAdd(po + (u2 ? 1 : 0), k0), atomicAdd(po + (u2 ? 3 : 2), k1);
-                                } else {
-                                    const bool u3 = lane & 8;
-                                    const float g2 = u3 ? k0 : k1;
-                                    float k2 = u3 ? k1 : k0;
-                                    k2 += __shfl_xor_sync(0xffffffffu, g2, 8);
-                                    if (CL == 32) k2 += __shfl_xor_sync(0xffffffffu, k2, 16);
-                                    if (CL == 16 || !(lane & 16)) atomicAdd(po + (u2 ? 1 : 0) + (u3 ? 2 : 0), k2);
-                                }
-                            }
-                        }
+                        for (int o = 0; o < Q / 8; ++o)
+                            channel_sums<CL>(rb + 4 * o, rc + 4 * o, pw + 8 * o, NP, lane);
                     }
                     if (i & 1) continue;
                     // two tokens are done: lanes ln = 0 and 1 finish one each
@@ -635,7 +606,7 @@ __global__ void __launch_bounds__(kWalk, Q == 8 ? 3 : 2) ssm_bwd_kernel(const Ss
             p.part_bc[((int64_t)tile * p.B * p.T + (int64_t)line * p.T + t0 + r) * (2 * p.N) + k] = part[n] + part[kPart + n];
         }
     }
-    st_states<Q>(p.part_a + ((int64_t)line * p.nrun + run) * hrow + own, dA, ns, p.n_wide);
+    st_states<Q>(p.part_a + ((int64_t)line * p.nrun + run) * hrow + own, dA, ns, p.n_wide, sw);
     // dD and dbias: each of the two lanes has half of the tokens
     if (LN > 1) {
         dD += __shfl_xor_sync(0xffffffffu, dD, CL);

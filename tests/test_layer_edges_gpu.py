@@ -1,0 +1,41 @@
+"""The state-space layer's operators where rounding, non-finite values, extreme
+gates and layouts matter, against plain fp64 forms. Tolerances are those of
+test_layer_gpu.py unless a test derives its own."""
+import pytest
+import torch
+
+import gated_delta_rule_18_gb300 as gdn
+from test_layer_gpu import (BF, DEV, F32, F64, TOL_BF, TOL_SCAN, built, cu_of, dev, f64, randn, ref_scan, rel,  # noqa: F401
+                            scan_case)
+
+pytestmark = pytest.mark.gpu
+
+
+def scan_gradients(v, do, lens=None, df=None, softplus=True, place=lambda k, t: t):
+    """gdn_ssm_bwd of scan_case's tensors; place(name, tensor on the GPU) may lay them out anew."""
+    a = {k: place(k, dev(t)) for k, t in v.items()}
+    return gdn.gdn_ssm_bwd(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], place("dout", dev(do)), D=a.get("D"),
+                           z=a.get("z"), dt_bias=a.get("dt_bias"), dt_softplus=softplus, h0=a.get("h0"),
+                           cu_seqlens=dev(cu_of(lens)), dh_final=dev(df))
+
+
+def ref_gradients(v, do, lens=None, df=None, softplus=True):
+    leaf = {k: f64(t).requires_grad_() for k, t in v.items()}
+    out, fin = ref_scan(leaf, lens, softplus)
+    loss = (out * f64(do)).sum() + (0.0 if df is None else (fin * f64(df)).sum())
+    return {"d" + k: g for k, g in zip(leaf, torch.autograd.grad(loss, tuple(leaf.values())))}
+
+
+@pytest.mark.parametrize("N", [5, 16, 40, 100])
+def test_channel_sums_of_the_scan_gradient_are_rounded_once(N):
+    """dB and dC are sums over the channels in fp32, rounded once to bf16.
+    All terms are positive here, so a sum's relative error is at most that of
+    fp32 sums (2e-5), and the chance that it takes a value to the other side
+    of a rounding boundary 2 * 2e-5 / 2^-8 = 1 %. Products cut to ten bits
+    would shrink every sum by some 3.4e-4 and move nine in a hundred."""
+    v = {k: t if k == "A" else t.abs() for k, t in scan_case(1, 64, 512, N, None, BF, True, 200).items()}
+    v["dt_bias"] = -v["dt_bias"] - 4
+    do = randn((1, 64, 512), BF, 210).abs()
+    got, ref = scan_gradients(v, do), ref_gradients(v, do)
+    for k in ("dBm", "dCm"):
+        assert (got[k].cpu() != ref[k].to(BF)).float().mean().item() <= 0.01, k
