@@ -39,3 +39,34 @@ def test_channel_sums_of_the_scan_gradient_are_rounded_once(N):
     got, ref = scan_gradients(v, do), ref_gradients(v, do)
     for k in ("dBm", "dCm"):
         assert (got[k].cpu() != ref[k].to(BF)).float().mean().item() <= 0.01, k
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N", [5, 16, 40, 100])
+def test_non_finite_values_stay_in_their_state_of_the_channel_sums(dtype, N):
+    T, C, at, n = 150, 48, 70, 3
+    v, do = scan_case(1, T, C, N, None, dtype, True, 220), randn((1, T, C), dtype, 230)
+    clean, tol = scan_gradients(v, do), TOL_BF if dtype == BF else TOL_SCAN
+    others = [i for i in range(N) if i != n]
+
+    def same(got, key, rows, states):
+        return rel(got[key][0, rows][:, states], clean[key][0, rows][:, states]) <= tol
+    # B of one state: dB does not depend on it, dC of that state alone does
+    bad = dict(v, Bm=v["Bm"].clone())
+    bad["Bm"][0, at, n] = float("nan")
+    got = scan_gradients(bad, do)
+    assert same(got, "dBm", slice(0, T), slice(0, N)) and same(got, "dCm", slice(0, T), others)
+    assert same(got, "dCm", slice(0, at), [n]) and got["dCm"][0, at:, n].isnan().all()
+    # an output's gradient: dC of its token, dB of that token and those before
+    bad_do = do.clone()
+    bad_do[0, at, 10] = float("nan")
+    got = scan_gradients(v, bad_do)
+    rest = [t for t in range(T) if t != at]
+    assert same(got, "dCm", rest, slice(0, N)) and got["dCm"][0, at].isnan().all()
+    assert same(got, "dBm", slice(at + 1, T), slice(0, N)) and got["dBm"][0, :at + 1].isnan().all()
+    # an infinite input: dB of its token, dC from there on
+    bad = dict(v, x=v["x"].clone())
+    bad["x"][0, at, 10] = float("inf")
+    got = scan_gradients(bad, do)
+    assert same(got, "dBm", rest, slice(0, N)) and not got["dBm"][0, at].isfinite().any()
+    assert same(got, "dCm", slice(0, at), slice(0, N)) and not got["dCm"][0, at:].isfinite().any()
