@@ -85,10 +85,14 @@ __device__ __forceinline__ float2 softplus2(float2 v) {
     const float2 r = rcp2(e0 + 2.f, e1 + 2.f);
     return make_float2(log1p_of(e0, r.x) + max_nan(v.x, 0.f), log1p_of(e1, r.y) + max_nan(v.y, 0.f));
 }
-// sigmoid of a pair: 1 / (1 + exp(-x)); exp(-x) is held under 2^60 for rcp2,
-// where the sigmoid is under 2^-60.
+// sigmoid of a pair by e = exp(-|x|) <= 1: 1 / (1 + e), and e times that for
+// x < 0, so that it goes to 0 with e and x sigmoid(x) to -0 for the lowest x
+// (a NaN takes no part in e, nor so in the shared reciprocal, and comes back
+// where the caller multiplies by x).
 __device__ __forceinline__ float2 sigmoid2(float2 x) {
-    return rcp2(ex2f(fminf(x.x * -kLog2e, 60.f)) + 1.f, ex2f(fminf(x.y * -kLog2e, 60.f)) + 1.f);
+    const float e0 = ex2f(fmaxf(-fabsf(x.x) * kLog2e, -200.f)), e1 = ex2f(fmaxf(-fabsf(x.y) * kLog2e, -200.f));
+    const float2 r = rcp2(e0 + 1.f, e1 + 1.f);
+    return make_float2(x.x < 0.f ? e0 * r.x : r.x, x.y < 0.f ? e1 * r.y : r.y);
 }
 
 // ------------------------------------------------------------ sequences -----

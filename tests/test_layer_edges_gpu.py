@@ -70,3 +70,31 @@ def test_non_finite_values_stay_in_their_state_of_the_channel_sums(dtype, N):
     got = scan_gradients(bad, do)
     assert same(got, "dBm", rest, slice(0, N)) and not got["dBm"][0, at].isfinite().any()
     assert same(got, "dCm", slice(0, at), slice(0, N)) and not got["dCm"][0, at:].isfinite().any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("C", [64, 37])  # wide rows, and rows of any alignment
+def test_very_low_and_high_gates(dtype, C):
+    """silu(z) -> -0 for z down to the type's lowest value, as a mask has it;
+    a prompt, its continuation and the gradients agree with the definition."""
+    T, N = 300, 16
+    v, do = scan_case(1, T, C, N, None, dtype, True, 240), randn((1, T, C), dtype, 250)
+    gates = torch.tensor([torch.finfo(dtype).min, -1e30, -1e20, -1e4, -100.0, -60.0, -45.0, -41.0, -20.0, 60.0, 1e4])
+    v["z"][0, 10:10 + 11 * 20] = gates.to(dtype).repeat(20)[:, None]
+    silu = f64(v["z"]) * torch.sigmoid(f64(v["z"]))
+    ref, fin = ref_scan({k: f64(t) for k, t in v.items()}, None, True)
+    y, _ = ref_scan({k: f64(t) for k, t in v.items() if k != "z"}, None, True)
+    a = {k: dev(t) for k, t in v.items()}
+    got = gdn.gdn_ssm_fwd(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], D=a["D"], z=a["z"], dt_bias=a["dt_bias"], h0=a["h0"])
+    # y's error is relative to the largest y, and its gate scales it (the smallest normal number: what may be flushed)
+    tol = (TOL_BF if dtype == BF else TOL_SCAN) * silu.abs() * y.abs().max() + torch.finfo(F32).tiny * y.abs().max()
+    assert ((f64(got) - ref).abs() <= tol).all()
+    state, steps = a["h0"].clone(), []
+    for t in range(T):
+        steps.append(gdn.gdn_ssm_step(a["x"][:, t], a["dt"][:, t], a["A"], a["Bm"][:, t], a["Cm"][:, t], state, D=a["D"],
+                                      z=a["z"][:, t], dt_bias=a["dt_bias"]))
+    assert ((f64(torch.stack(steps, 1)) - ref).abs() <= tol).all() and rel(state, fin) <= TOL_SCAN
+    got, ref = scan_gradients(v, do), ref_gradients(v, do)
+    for k, r in ref.items():
+        act = k in ("dx", "ddt", "dBm", "dCm", "dz")
+        assert rel(got[k], r) <= (TOL_BF if dtype == BF and act else TOL_SCAN), k
