@@ -174,6 +174,8 @@ def gdn_rmsnorm_fwd(x, weight, residual=None, eps=1e-6, out_dtype=None, group=0,
         out = torch.empty_like(x, dtype=ty, memory_format=torch.contiguous_format)
     elif out.shape != x.shape or out.dtype != ty:
         raise ValueError(f"out must be {tuple(x.shape)} {ty}, got {tuple(out.shape)} {out.dtype}")
+    elif out.get_device() != x.get_device():
+        _fail(4, f"out must be on {x.device}")
     o2 = _as_rows(out, "out")
     xp, xs = _rows(x2, "x", (R, D), x)
     op, os_ = _rows(o2, "out", (R, D), out)

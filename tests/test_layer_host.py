@@ -1,0 +1,72 @@
+"""The Python checks of the state-space layer's operators, on the CPU: tensors
+that claim a GPU, and a library that records its calls instead of launching."""
+import contextlib
+
+import pytest
+import torch
+
+import gated_delta_rule_18_gb300 as gdn
+from gated_delta_rule_18_gb300 import GDNError, layer
+
+LAYOUT = "GDN_ERR_LAYOUT"
+F8 = torch.float8_e4m3fn
+
+
+class OnGpu(torch.Tensor):
+    """A CPU tensor that says it is on a GPU."""
+    index = 0
+    is_cuda = True
+
+    def get_device(self):
+        return self.index
+
+    __torch_function__ = torch._C._disabled_torch_function_impl
+
+
+def on(index, *shape, dtype=torch.float32):
+    t = torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+    t.index = index
+    return t
+
+
+class Library:
+    """Every entry point: returns 0 (for sizes, 1024) and notes its name and the current device."""
+
+    def __init__(self):
+        self.current, self.calls = 0, []
+
+    def __getattr__(self, name):
+        def entry(*args):
+            self.calls.append((name, self.current))
+            return 1024 if name.endswith("_size") else 0
+        return entry
+
+    @property
+    def launched(self):
+        return [(n, d) for n, d in self.calls if not n.endswith("_size")]
+
+
+@pytest.fixture
+def L(monkeypatch):
+    lib = Library()
+    monkeypatch.setattr(layer, "_lib", lib)
+    monkeypatch.setattr(layer, "_stream", lambda like: 0)
+    return lib
+
+
+def refused(L, name, f):
+    with pytest.raises(GDNError) as e:
+        f()
+    assert e.value.name == name
+    assert L.launched == []
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_norm_output_on_another_device_is_refused(L, q8):
+    x, w = on(0, 4, 64), on(0, 64)
+    kw = dict(out_dtype=F8) if q8 else {}
+    ty = F8 if q8 else x.dtype
+    refused(L, LAYOUT, lambda: gdn.gdn_rmsnorm_fwd(x, w, out=torch.zeros(4, 64).to(ty), **kw))
+    refused(L, LAYOUT, lambda: gdn.gdn_rmsnorm_fwd(x, w, out=on(1, 4, 64, dtype=ty), **kw))
+    gdn.gdn_rmsnorm_fwd(x, w, out=on(0, 4, 64, dtype=ty), **kw)
+    assert len(L.launched) == 1
