@@ -125,6 +125,8 @@ def _n_seq(cu_seqlens, B, like):
 
 
 def _workspace(workspace, need, like):
+    if workspace is not None and (workspace.get_device() != like.get_device() or not workspace.is_contiguous()):
+        _fail(4, f"workspace must be contiguous on {like.device}")
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(max(int(need), 256), dtype=torch.uint8, device=like.device)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()

@@ -23,10 +23,14 @@ class OnGpu(torch.Tensor):
     __torch_function__ = torch._C._disabled_torch_function_impl
 
 
-def on(index, *shape, dtype=torch.float32):
-    t = torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+def claim(t, index=0):
+    t = t.as_subclass(OnGpu)
     t.index = index
     return t
+
+
+def on(index, *shape, dtype=torch.float32):
+    return claim(torch.zeros(*shape, dtype=dtype), index)
 
 
 class Library:
@@ -70,3 +74,28 @@ def test_norm_output_on_another_device_is_refused(L, q8):
     refused(L, LAYOUT, lambda: gdn.gdn_rmsnorm_fwd(x, w, out=on(1, 4, 64, dtype=ty), **kw))
     gdn.gdn_rmsnorm_fwd(x, w, out=on(0, 4, 64, dtype=ty), **kw)
     assert len(L.launched) == 1
+
+
+def packed(index):
+    """The calls that take a workspace, on a packed batch."""
+    x, cu = on(index, 1, 6, 16), on(index, 3, dtype=torch.int32)
+    taps, a, bc = on(index, 16, 4), on(index, 16, 8), on(index, 1, 6, 8)
+    out = on(index, 1, 6, 16)
+    return [
+        lambda **k: gdn.gdn_rmsnorm_bwd(x, on(index, 16), x, **k),
+        lambda **k: gdn.gdn_conv_fwd(x, taps, cu_seqlens=cu, out=out, **k),
+        lambda **k: gdn.gdn_conv_bwd(x, taps, out, cu_seqlens=cu, **k),
+        lambda **k: gdn.gdn_ssm_fwd(x, x, a, bc, bc, cu_seqlens=cu, out=out, **k),
+        lambda **k: gdn.gdn_ssm_bwd(x, x, a, bc, bc, out, cu_seqlens=cu, **k),
+    ]
+
+
+@pytest.mark.parametrize("call", range(5))
+def test_workspace_on_another_device_or_with_gaps_is_refused(L, call):
+    f = packed(0)[call]
+    plain = torch.zeros(1 << 16, dtype=torch.uint8)
+    for ws in (plain, claim(plain, 1), claim(plain[::2])):
+        refused(L, LAYOUT, lambda: f(workspace=ws))
+    f(workspace=on(0, 1 << 16, dtype=torch.uint8))
+    f()
+    assert len(L.launched) == 2
