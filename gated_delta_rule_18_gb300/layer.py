@@ -5,9 +5,10 @@ for prompts, single tokens and training.
 Activations are (B, T, D), bf16 or fp32, with any strides over B and T and a
 contiguous last dimension; norms take rows of any leading shape, single-token
 calls (n, D). Parameters and scan states are contiguous fp32. Every call runs
-on the current stream, or on `stream`; what it allocates then belongs to that
-stream. Wrong shapes raise ValueError, wrong types and layouts GDNError, both
-before anything is launched.
+on the current stream of its tensors' device, or on `stream`, which has to be
+one of that device; what it allocates then belongs to that stream. Wrong
+shapes raise ValueError, wrong types and layouts GDNError, both before anything
+is launched.
 """
 from __future__ import annotations
 
@@ -143,6 +144,22 @@ def _stream(like):
     return torch.cuda.current_stream(like.device).cuda_stream
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _away(x):
+    return x.is_cuda and x.get_device() != _current_device()
+
+
+def _guard(x, stream):
+    """The context of a call on x's device: its current stream, or `stream`."""
+    if stream is None:
+        return torch.cuda.device(x.get_device())
+    if stream.device.index != x.get_device():
+        _fail(4, f"stream must be on {x.device}, not on {stream.device}")
+    return torch.cuda.stream(stream)
+
+
 def _as_rows(t, name):
     if t is None or t.dim() == 2:
         return t
@@ -161,8 +178,8 @@ def gdn_rmsnorm_fwd(x, weight, residual=None, eps=1e-6, out_dtype=None, group=0,
     of one stride; with out_dtype=torch.float8_e4m3fn,
     "scale": fp32, one for each `group` channels (32, 64, 128 or 256; 0: the
     row), out * scale being y."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
+    if stream is not None or _away(x):
+        with _guard(x, stream):
             return gdn_rmsnorm_fwd(x, weight, residual, eps, out_dtype, group, out, residual_out)
     L = _lib or _load()
     _on_gpu(x)
@@ -213,8 +230,8 @@ def gdn_rmsnorm_bwd(s, weight, dy, dres=None, eps=1e-6, workspace=None, stream=N
     x, without a residual), the output's gradient dy and the residual
     stream's own gradient dres (s's type): a dict of "dx" (s's type; the
     gradient of x and of the residual alike) and "dweight" (fp32)."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
+    if stream is not None or _away(s):
+        with _guard(s, stream):
             return gdn_rmsnorm_bwd(s, weight, dy, dres, eps, workspace)
     L = _lib or _load()
     _on_gpu(s, "s")
@@ -243,8 +260,8 @@ def gdn_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, fina
     (D, W), bias (D) fp32; initial_state / final_state (n_seq, W - 1, D) in
     x's type, the inputs before and at the end of each sequence, oldest
     first; cu_seqlens int32 (n_seq + 1) with B == 1. Returns out."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
+    if stream is not None or _away(x):
+        with _guard(x, stream):
             return gdn_conv_fwd(x, weight, bias, initial_state, cu_seqlens, final_state, silu, out, workspace)
     L = _lib or _load()
     _on_gpu(x)
@@ -271,8 +288,8 @@ def gdn_conv_bwd(x, weight, dout, bias=None, initial_state=None, cu_seqlens=None
     """Gradients of gdn_conv_fwd for L = sum(dout * out) + sum(dfinal_state *
     final_state): a dict of "dx" (x's type), "dweight" (fp32), with a bias
     "dbias" (fp32) and with an initial state "dinitial_state" (x's type)."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
+    if stream is not None or _away(x):
+        with _guard(x, stream):
             return gdn_conv_bwd(x, weight, dout, bias, initial_state, cu_seqlens, dfinal_state, silu, workspace)
     L = _lib or _load()
     _on_gpu(x)
@@ -305,8 +322,8 @@ def gdn_conv_step(x, state, weight, bias=None, slots=None, silu=True, out=None, 
     type, the requests' windows, shifted by x in place; slots int32 (n), each
     request's row of state (distinct; a value outside [0, n_slots) marks a
     padding row, whose output is 0), or None for rows 0 .. n - 1. Returns out."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
+    if stream is not None or _away(x):
+        with _guard(x, stream):
             return gdn_conv_step(x, state, weight, bias, slots, silu, out)
     L = _lib or _load()
     _on_gpu(x)
@@ -332,8 +349,8 @@ def gdn_ssm_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_softplus=True
     * silu(z). x, dt, z (B, T, C); Bm, Cm (B, T, N); A (C, N), D, dt_bias (C)
     fp32; h0 / h_final (n_seq, C, N) fp32; cu_seqlens int32 (n_seq + 1) with
     B == 1. Returns out."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
+    if stream is not None or _away(x):
+        with _guard(x, stream):
             return gdn_ssm_fwd(x, dt, A, Bm, Cm, D, z, dt_bias, dt_softplus, h0, cu_seqlens, h_final, out, workspace)
     L = _lib or _load()
     _on_gpu(x)
@@ -360,8 +377,8 @@ def gdn_ssm_bwd(x, dt, A, Bm, Cm, dout, D=None, z=None, dt_bias=None, dt_softplu
     """Gradients of gdn_ssm_fwd for L = sum(dout * out) + sum(dh_final *
     h_final), the forward recomputed: a dict of dx, ddt, dBm, dCm (x's type),
     dA (fp32) and, for what was given, dD, dz, ddt_bias, dh0."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
+    if stream is not None or _away(x):
+        with _guard(x, stream):
             return gdn_ssm_bwd(x, dt, A, Bm, Cm, dout, D, z, dt_bias, dt_softplus, h0, cu_seqlens, dh_final, workspace)
     L = _lib or _load()
     _on_gpu(x)
@@ -402,8 +419,8 @@ def gdn_ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, dt_softp
     """One token of n requests of the scan: x, dt, z (n, C); Bm, Cm (n, N);
     state (n_slots, C, N) fp32, updated in place; slots as for gdn_conv_step.
     Returns out."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
+    if stream is not None or _away(x):
+        with _guard(x, stream):
             return gdn_ssm_step(x, dt, A, Bm, Cm, state, D, z, dt_bias, dt_softplus, slots, out)
     L = _lib or _load()
     _on_gpu(x)

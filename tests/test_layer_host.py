@@ -1,5 +1,7 @@
 """The Python checks of the state-space layer's operators, on the CPU: tensors
 that claim a GPU, and a library that records its calls instead of launching."""
+import contextlib
+
 import pytest
 import torch
 
@@ -56,6 +58,7 @@ def L(monkeypatch):
     lib = Library()
     monkeypatch.setattr(layer, "_lib", lib)
     monkeypatch.setattr(layer, "_stream", lambda like: 0)
+    monkeypatch.setattr(layer, "_current_device", lambda: lib.current)
     return lib
 
 
@@ -100,3 +103,39 @@ def test_workspace_on_another_device_or_with_gaps_is_refused(L, call):
     f(workspace=on(0, 1 << 16, dtype=torch.uint8))
     f()
     assert len(L.launched) == 2
+
+
+def calls(index):
+    """Every call of the layer on tensors of a device, outputs given where the call takes them."""
+    x, w, taps, a, bc = on(index, 4, 16), on(index, 16), on(index, 16, 4), on(index, 16, 8), on(index, 4, 8)
+    out = on(index, 4, 16)
+    step = [
+        lambda **k: gdn.gdn_rmsnorm_fwd(x, w, out=out, **k),
+        lambda **k: gdn.gdn_conv_step(x, on(index, 4, 3, 16), taps, out=out, **k),
+        lambda **k: gdn.gdn_ssm_step(x, x, a, bc, bc, on(index, 4, 16, 8), out=out, **k),
+    ]
+    return step + packed(index)
+
+
+class FakeStream:
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+
+@pytest.mark.parametrize("call", range(8))
+def test_calls_run_on_the_device_of_their_tensors(L, monkeypatch, call):
+    @contextlib.contextmanager
+    def device(d):
+        before, L.current = L.current, d.index if isinstance(d, torch.device) else d
+        yield
+        L.current = before
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: device(s.device))
+    calls(1)[call]()
+    calls(0)[call]()
+    calls(1)[call](stream=FakeStream(1))
+    assert [d for _, d in L.launched] == [1, 0, 1] and L.current == 0
+    L.calls.clear()
+    refused(L, LAYOUT, lambda: calls(1)[call](stream=FakeStream(0)))
+    refused(L, LAYOUT, lambda: calls(0)[call](stream=FakeStream(1)))
