@@ -144,6 +144,13 @@ def _stream(like):
     return torch.cuda.current_stream(like.device).cuda_stream
 
 
+def _wrote(*tensors):
+    """Tensors that a call has written: autograd notices if it had saved one of them."""
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
@@ -222,6 +229,7 @@ def gdn_rmsnorm_fwd(x, weight, residual=None, eps=1e-6, out_dtype=None, group=0,
                            E4M3 if q8 else _CODE[ty], rop, ros, sp, R, D, group, eps, _stream(x))
     if st:
         _fail(st, "gdn_rmsnorm_fwd")
+    _wrote(out, residual_out)
     return res
 
 
@@ -280,6 +288,7 @@ def gdn_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, fina
                         B, T, D, _code(x, "x"), SILU if silu else 0, wp, wn, _stream(x))
     if st:
         _fail(st, "gdn_conv_fwd")
+    _wrote(out, final_state)
     return out
 
 
@@ -339,6 +348,7 @@ def gdn_conv_step(x, state, weight, bias=None, slots=None, silu=True, out=None, 
                          _code(x, "x"), SILU if silu else 0, _stream(x))
     if st:
         _fail(st, "gdn_conv_step")
+    _wrote(out, state)
     return out
 
 
@@ -369,6 +379,7 @@ def gdn_ssm_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_softplus=True
                        SOFTPLUS if dt_softplus else 0, wp, wn, _stream(x))
     if st:
         _fail(st, "gdn_ssm_fwd")
+    _wrote(out, h_final)
     return out
 
 
@@ -437,4 +448,5 @@ def gdn_ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, dt_softp
                         _stream(x))
     if st:
         _fail(st, "gdn_ssm_step")
+    _wrote(out, state)
     return out

@@ -139,3 +139,27 @@ def test_calls_run_on_the_device_of_their_tensors(L, monkeypatch, call):
     L.calls.clear()
     refused(L, LAYOUT, lambda: calls(1)[call](stream=FakeStream(0)))
     refused(L, LAYOUT, lambda: calls(0)[call](stream=FakeStream(1)))
+
+
+def test_tensors_written_in_place_count_a_version(L):
+    """A tensor saved for a gradient and then overwritten by a call is noticed."""
+    x, w, taps, a, bc = on(0, 4, 16), on(0, 16), on(0, 16, 4), on(0, 16, 8), on(0, 4, 8)
+    line, rows = on(0, 4, 1, 16), on(0, 4, 1, 8)
+    res, window, h = on(0, 4, 16), on(0, 4, 3, 16), on(0, 4, 16, 8)
+    out, out3 = on(0, 4, 16), on(0, 4, 1, 16)
+    for written, f in (
+            ([out, res], lambda: gdn.gdn_rmsnorm_fwd(x, w, residual=res, residual_out=res, out=out)),
+            ([out3, window], lambda: gdn.gdn_conv_fwd(line, taps, final_state=window, out=out3)),
+            ([out, window], lambda: gdn.gdn_conv_step(x, window, taps, out=out)),
+            ([out3, h], lambda: gdn.gdn_ssm_fwd(line, line, a, rows, rows, h_final=h, out=out3)),
+            ([out, h], lambda: gdn.gdn_ssm_step(x, x, a, bc, bc, h, out=out))):
+        before = [t._version for t in written]
+        f()
+        assert all(t._version > b for t, b in zip(written, before))
+    assert [t._version for t in (x, w, taps, a, bc, line, rows)] == [0] * 7
+    leaf = torch.ones(4, 16, requires_grad=True)
+    h = on(0, 4, 16, 8)
+    loss = (leaf[..., None] * h).sum()
+    gdn.gdn_ssm_step(x, x, a, bc, bc, h, out=out)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
