@@ -13,6 +13,8 @@ bf16 first; fp32 inputs (the fp32 path) keep it in fp32.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import (PREP_RELU, PREP_RMS, gdn_chunk_bwd, gdn_chunk_fwd, gdn_chunk_fwd_bidir, gdn_frame_bwd,
@@ -153,6 +155,31 @@ def frame_video_gated_delta_rule(q, k, v, beta, g_frame, frame, gate=None, eps=1
     return _FrameVideo.apply(q, k, v, beta, g_frame, gate, int(frame), float(eps), float(prep_eps))
 
 
+class _Once(torch.autograd.Function):
+    """Passes a backward's results on; to differentiate them again raises."""
+
+    @staticmethod
+    def forward(ctx, anchor, *grads):
+        return grads
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the state-space layer's gradients are not differentiable")
+
+
+def _once(backward):
+    # (torch's once_differentiable guards the path over the upstream gradients
+    # only: a second derivative of y.sum() would go by it)
+    @functools.wraps(backward)
+    def call(ctx, *grads):
+        with torch.no_grad():
+            r = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return r
+        return _Once.apply(torch.ones((), requires_grad=True), *r)
+    return call
+
+
 class _RMSNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
@@ -163,6 +190,7 @@ class _RMSNorm(torch.autograd.Function):
         return r["out"], s if residual is not None else None
 
     @staticmethod
+    @_once
     def backward(ctx, dy, ds):
         s, weight = ctx.saved_tensors
         r = gdn_rmsnorm_bwd(s, weight, dy.contiguous(), dres=None if ds is None else ds.to(s.dtype).contiguous(),
@@ -191,6 +219,7 @@ class _CausalConv(torch.autograd.Function):
         return y, final
 
     @staticmethod
+    @_once
     def backward(ctx, dy, dfinal):
         x, weight, bias, initial_state, cu_seqlens = ctx.saved_tensors
         r = gdn_conv_bwd(x, weight, dy.contiguous(), bias=bias, initial_state=initial_state, cu_seqlens=cu_seqlens,
@@ -217,6 +246,7 @@ class _SelectiveScan(torch.autograd.Function):
         return y, final
 
     @staticmethod
+    @_once
     def backward(ctx, dy, dfinal):
         x, dt, A, Bm, Cm, D, z, dt_bias, h0, cu_seqlens = ctx.saved_tensors
         r = gdn_ssm_bwd(x, dt, A, Bm, Cm, dy.contiguous(), D=D, z=z, dt_bias=dt_bias, dt_softplus=ctx.dt_softplus,

@@ -163,3 +163,24 @@ def test_tensors_written_in_place_count_a_version(L):
     gdn.gdn_ssm_step(x, x, a, bc, bc, h, out=out)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+@pytest.mark.parametrize("name", ["rms_norm", "causal_conv", "selective_scan"])
+def test_second_derivatives_are_refused(monkeypatch, name):
+    """The gradient calls are not differentiable: a loss of a gradient raises instead of missing its part."""
+    from gated_delta_rule_18_gb300 import autograd as gdr
+
+    def gradients(x, *args, **kw):
+        return {k: torch.ones_like(x) for k in ("dx", "ddt", "dBm", "dCm")} | {"dweight": torch.ones(16), "dA": torch.ones(16, 8)}
+    for k in ("gdn_rmsnorm", "gdn_conv", "gdn_ssm"):
+        monkeypatch.setattr(gdr, k + "_fwd", lambda x, *a, **kw: {"out": x * 2} if kw.get("eps") else x * 2)
+        monkeypatch.setattr(gdr, k + "_bwd", gradients)
+    x, w, a = torch.randn(1, 4, 16, requires_grad=True), torch.ones(16), torch.ones(16, 8)
+    y = {"rms_norm": lambda: gdr.rms_norm(x, w)[0], "causal_conv": lambda: gdr.causal_conv(x, torch.ones(16, 4))[0],
+         "selective_scan": lambda: gdr.selective_scan(x, x, a, x.detach()[..., :8], x.detach()[..., :8])[0]}[name]()
+    for loss in (y.sum(), y.square().sum()):
+        (g,) = torch.autograd.grad(loss, x, create_graph=True)
+        with pytest.raises(RuntimeError, match="not differentiable"):
+            (g.square().sum() + loss).backward(retain_graph=True)
+    y.sum().backward()
+    assert torch.equal(x.grad, torch.full_like(x, 2.0 if name == "selective_scan" else 1.0))
