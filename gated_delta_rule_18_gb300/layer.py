@@ -118,10 +118,17 @@ def _on_gpu(x, name="x"):
         _fail(4, f"{name} must be on a GPU")
 
 
+def _fits(*sizes):
+    """The library's sizes are 32-bit integers, and ctypes would pass the low half of a larger one."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"a size must be at most 2147483647, got {max(sizes)}")
+
+
 def _n_seq(cu_seqlens, B, like):
     """(pointer, sequences) of a batch."""
     if cu_seqlens is None:
         return 0, B
+    _fits(cu_seqlens.numel())
     return _flat(cu_seqlens, "cu_seqlens", (cu_seqlens.numel(),), torch.int32, like), cu_seqlens.numel() - 1
 
 
@@ -192,6 +199,7 @@ def gdn_rmsnorm_fwd(x, weight, residual=None, eps=1e-6, out_dtype=None, group=0,
     _on_gpu(x)
     x2 = x if x.dim() == 2 else _as_rows(x, "x")
     R, D = x2.shape
+    _fits(R, D, group, -group)
     q8 = out_dtype is _F8
     if out_dtype is not None and not q8 and out_dtype != x.dtype:
         _fail(3, f"out_dtype must be {x.dtype} or torch.float8_e4m3fn, got {out_dtype}")
@@ -246,6 +254,7 @@ def gdn_rmsnorm_bwd(s, weight, dy, dres=None, eps=1e-6, workspace=None, stream=N
     D = s.shape[-1]
     s2 = _as_rows(s, "s")
     R = s2.shape[0]
+    _fits(R, D)
     if dy.shape != s.shape or dy.device != s.device:
         raise ValueError(f"dy must have shape {tuple(s.shape)} on {s.device}, got {tuple(dy.shape)}")
     dx = torch.empty(s.shape, dtype=s.dtype, device=s.device)
@@ -275,6 +284,7 @@ def gdn_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, fina
     _on_gpu(x)
     B, T, D = x.shape
     W = weight.shape[1]
+    _fits(B, T, D, W)
     cp, n = _n_seq(cu_seqlens, B, x)
     if out is None:
         out = torch.empty((B, T, D), dtype=x.dtype, device=x.device)
@@ -304,6 +314,7 @@ def gdn_conv_bwd(x, weight, dout, bias=None, initial_state=None, cu_seqlens=None
     _on_gpu(x)
     B, T, D = x.shape
     W = weight.shape[1]
+    _fits(B, T, D, W)
     cp, n = _n_seq(cu_seqlens, B, x)
     f32 = dict(dtype=torch.float32, device=x.device)
     r = {"dx": torch.empty((B, T, D), dtype=x.dtype, device=x.device), "dweight": torch.empty((D, W), **f32)}
@@ -337,10 +348,10 @@ def gdn_conv_step(x, state, weight, bias=None, slots=None, silu=True, out=None, 
     L = _lib or _load()
     _on_gpu(x)
     n, D = x.shape
-    W = weight.shape[1]
+    W, pool = weight.shape[1], state.shape[0]
+    _fits(n, D, W, pool)
     if out is None:
         out = torch.empty((n, D), dtype=x.dtype, device=x.device)
-    pool = state.shape[0]
     st = L.gdn_conv_step(*_rows(x, "x", (n, D), x), _flat(weight, "weight", (D, W), torch.float32, x), W,
                          _flat(bias, "bias", (D,), torch.float32, x),
                          _flat(state, "state", (pool, W - 1, D), x.dtype, x),
@@ -366,6 +377,7 @@ def gdn_ssm_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_softplus=True
     _on_gpu(x)
     B, T, C = x.shape
     N = A.shape[1]
+    _fits(B, T, C, N)
     cp, n = _n_seq(cu_seqlens, B, x)
     if out is None:
         out = torch.empty((B, T, C), dtype=x.dtype, device=x.device)
@@ -395,6 +407,7 @@ def gdn_ssm_bwd(x, dt, A, Bm, Cm, dout, D=None, z=None, dt_bias=None, dt_softplu
     _on_gpu(x)
     B, T, C = x.shape
     N = A.shape[1]
+    _fits(B, T, C, N)
     cp, n = _n_seq(cu_seqlens, B, x)
     like, f32 = dict(dtype=x.dtype, device=x.device), dict(dtype=torch.float32, device=x.device)
     r = {"dx": torch.empty((B, T, C), **like), "ddt": torch.empty((B, T, C), **like), "dA": torch.empty((C, N), **f32),
@@ -436,10 +449,11 @@ def gdn_ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, dt_softp
     L = _lib or _load()
     _on_gpu(x)
     n, C = x.shape
-    N = A.shape[1]
+    N, pool = A.shape[1], state.shape[0]
+    _fits(n, C, N, pool)
     if out is None:
         out = torch.empty((n, C), dtype=x.dtype, device=x.device)
-    pool, f = state.shape[0], torch.float32
+    f = torch.float32
     st = L.gdn_ssm_step(*_rows(x, "x", (n, C), x), *_rows(dt, "dt", (n, C), x), _flat(A, "A", (C, N), f, x),
                         *_rows(Bm, "Bm", (n, N), x), *_rows(Cm, "Cm", (n, N), x), _flat(D, "D", (C,), f, x),
                         *_rows(z, "z", (n, C), x), _flat(dt_bias, "dt_bias", (C,), f, x),

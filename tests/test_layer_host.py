@@ -184,3 +184,31 @@ def test_second_derivatives_are_refused(monkeypatch, name):
             (g.square().sum() + loss).backward(retain_graph=True)
     y.sum().backward()
     assert torch.equal(x.grad, torch.full_like(x, 2.0 if name == "selective_scan" else 1.0))
+
+
+def tall(*shape, dtype=torch.float32):
+    """A tensor of any size in a few bytes (stride 0)."""
+    return claim(torch.zeros((1,) * len(shape), dtype=dtype).expand(*shape))
+
+
+@pytest.mark.parametrize("n", [2**31, 2**32 + 4])
+def test_sizes_past_32_bits_are_refused_and_not_cut(L, n):
+    """The library's sizes are 32-bit: a larger one must not arrive as its low half."""
+    x, out = tall(n, 1), tall(n, 1)
+    line, w, taps, a = tall(1, n, 1), on(0, 1), on(0, 1, 4), on(0, 1, 8)
+    rows = tall(1, n, 8)
+    for f in (lambda: gdn.gdn_rmsnorm_fwd(x, w, out=out),
+              lambda: gdn.gdn_rmsnorm_fwd(on(0, 4, 64), on(0, 64), out_dtype=F8, group=2**32 + 32,
+                                          out=on(0, 4, 64, dtype=F8)),
+              lambda: gdn.gdn_rmsnorm_bwd(x, w, out),
+              lambda: gdn.gdn_conv_fwd(line, taps, out=line),
+              lambda: gdn.gdn_conv_bwd(line, taps, line),
+              lambda: gdn.gdn_conv_step(x, on(0, 1, 3, 1), taps, out=out),
+              lambda: gdn.gdn_conv_step(on(0, 4, 1), tall(n, 3, 1), taps, out=on(0, 4, 1)),
+              lambda: gdn.gdn_conv_fwd(on(0, 1, 4, 1), tall(1, n), out=on(0, 1, 4, 1)),
+              lambda: gdn.gdn_ssm_fwd(line, line, a, rows, rows, out=line),
+              lambda: gdn.gdn_ssm_bwd(line, line, a, rows, rows, line),
+              lambda: gdn.gdn_ssm_step(x, x, a, tall(n, 8), tall(n, 8), on(0, 4, 1, 8), out=out)):
+        with pytest.raises(ValueError, match="2147483647"):
+            f()
+    assert L.launched == []
