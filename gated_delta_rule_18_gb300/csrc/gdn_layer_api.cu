@@ -31,10 +31,13 @@ struct Rows {
     }
 };
 
+// Tokens or rows: with room for what kernels and sizes add to them (a tile, a run).
+bool length_ok(int n) { return n >= 0 && n <= INT32_MAX - 65535; }
+bool norm_shape_ok(int R, int D) { return length_ok(R) && D >= 1 && D <= kNormMaxD; }
+bool dense_ok(int B, int T, int D) { return B >= 1 && B <= 65535 && length_ok(T) && D >= 1 && D <= (1 << 20); }
 // shapes of a dense or packed batch
 bool batch_ok(int B, int T, int D, const int32_t *cu, int n_seq) {
-    if (B < 1 || B > 65535 || T < 0 || D < 1 || D > (1 << 20)) return false;
-    return cu ? B == 1 && n_seq >= 1 : n_seq == B;
+    return dense_ok(B, T, D) && (cu ? B == 1 && n_seq >= 1 : n_seq == B);
 }
 
 // the forward: the error word, and the chunks' sums where a line is cut
@@ -56,7 +59,7 @@ struct SsmBwdWs {
     size_t sums, dsum, gsum, gs, bc, a, d, total;
 };
 bool ssm_shape_ok(int B, int T, int D, int N, int n_seq, int varlen) {
-    if (B < 1 || B > 65535 || T < 0 || D < 1 || D > (1 << 20) || N < 1 || N > kSsmMaxN) return false;
+    if (!dense_ok(B, T, D) || N < 1 || N > kSsmMaxN) return false;
     return varlen ? B == 1 && n_seq >= 1 : n_seq == B;
 }
 SsmBwdWs ssm_bwd_ws(int B, int T, int D, int N, int varlen) {
@@ -92,7 +95,7 @@ gdn_status gdn_rmsnorm_fwd(const void *x, int64_t x_st, int x_dtype, const void 
                            void *res_out, int64_t res_out_st, float *scale, int R, int D, int group, float eps,
                            cudaStream_t stream) {
     if (R > 0 && (!x || !weight || !out)) return GDN_ERR_NULL;
-    if (R < 0 || D < 1 || D > kNormMaxD || !(eps >= 0.f)) return GDN_ERR_SHAPE;
+    if (!norm_shape_ok(R, D) || !(eps >= 0.f)) return GDN_ERR_SHAPE;
     if (!dtype_ok(x_dtype) || (residual && !dtype_ok(res_dtype))) return GDN_ERR_DTYPE;
     if (out_dtype != GDN_E4M3 && out_dtype != x_dtype) return GDN_ERR_DTYPE;
     if (R > 0 && ((residual != nullptr) != (res_out != nullptr) || (out_dtype == GDN_E4M3) != (scale != nullptr)))
@@ -117,7 +120,7 @@ gdn_status gdn_rmsnorm_fwd(const void *x, int64_t x_st, int x_dtype, const void 
 }
 
 size_t gdn_rmsnorm_bwd_workspace_size(int R, int D) {
-    if (R < 0 || D < 1 || D > kNormMaxD) return 0;
+    if (!norm_shape_ok(R, D)) return 0;
     return align_up((size_t)norm_bwd_parts(R, D) * D * 4) + kAlign;
 }
 
@@ -126,7 +129,7 @@ gdn_status gdn_rmsnorm_bwd(const void *s, int64_t s_st, int s_dtype, const void 
                            float *dweight, int R, int D, float eps, void *workspace, size_t ws_bytes,
                            cudaStream_t stream) {
     if (!dweight || (R > 0 && (!s || !dy || !weight || !dx))) return GDN_ERR_NULL;
-    if (R < 0 || D < 1 || D > kNormMaxD || !(eps >= 0.f)) return GDN_ERR_SHAPE;
+    if (!norm_shape_ok(R, D) || !(eps >= 0.f)) return GDN_ERR_SHAPE;
     if (!dtype_ok(s_dtype) || !dtype_ok(dy_dtype)) return GDN_ERR_DTYPE;
     Rows r;
     r.add(s, s_dtype, 0, s_st);
@@ -182,7 +185,7 @@ gdn_status gdn_conv_fwd(const void *x, int64_t x_sb, int64_t x_st, const float *
 }
 
 size_t gdn_conv_bwd_workspace_size(int B, int T, int D, int W) {
-    if (B < 1 || B > 65535 || T < 0 || D < 1 || D > (1 << 20) || W < 2 || W > kConvMaxW) return 0;
+    if (!dense_ok(B, T, D) || W < 2 || W > kConvMaxW) return 0;
     return align_up((size_t)conv_bwd_parts(B, T, conv_bwd_run(B, T, D)) * D * (W + 1) * 4) + kAlign;
 }
 

@@ -497,7 +497,8 @@ gdn_status gdn_frame_fwd(const void *q, const void *k, gdn_tensor_desc qkd,
  *     name_st over T or rows), non-negative, D contiguous. Rows may start at
  *     any multiple of the element size and D may be any number: rows and
  *     strides that keep 16-byte alignment run wide accesses, others element
- *     accesses. All activations of a call share `dtype` unless said.
+ *     accesses. All activations of a call share `dtype` unless said. T and R
+ *     are at most 2^31 - 65536, B 65535, D 2^20 (norms 16384).
  *   - Parameters (weights, A, D, biases) and scan states are fp32,
  *     contiguous, 4-byte aligned.
  *   - Packed batches: cu_seqlens as for gdn_chunk_fwd (B == 1; sequences may

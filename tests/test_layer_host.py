@@ -212,3 +212,21 @@ def test_sizes_past_32_bits_are_refused_and_not_cut(L, n):
         with pytest.raises(ValueError, match="2147483647"):
             f()
     assert L.launched == []
+
+
+def test_lengths_whose_sums_would_pass_32_bits_are_refused():
+    """Kernels and workspace sizes add a tile's or a group's tokens to T and R: room for that is kept."""
+    from gated_delta_rule_18_gb300.build import build
+    from test_layer_abi import CONV, CONV_BWD, NORM, NORM_BWD, SHAPE, SSM, SSM_BWD, call
+    build()
+    lib, most = gdn.lib(), 2**31 - 1
+    for fn, spec, kw in ((lib.gdn_rmsnorm_fwd, NORM, dict(R=most)), (lib.gdn_rmsnorm_bwd, NORM_BWD, dict(R=most)),
+                         (lib.gdn_conv_fwd, CONV, dict(T=most)), (lib.gdn_conv_bwd, CONV_BWD, dict(T=most)),
+                         (lib.gdn_ssm_fwd, SSM, dict(T=most)), (lib.gdn_ssm_bwd, SSM_BWD, dict(T=most))):
+        assert call(fn, spec, **kw) == SHAPE, fn
+    assert lib.gdn_rmsnorm_bwd_workspace_size(most, 64) == 0 and lib.gdn_conv_bwd_workspace_size(1, most, 64, 4) == 0
+    assert lib.gdn_ssm_workspace_size(1, most, 64, 16, 1, 0) == 0
+    assert lib.gdn_ssm_bwd_workspace_size(1, most, 64, 16, 1, 0) == 0
+    long = 2**31 - 2**16
+    assert lib.gdn_conv_bwd_workspace_size(1, long, 64, 4) > 0 and lib.gdn_rmsnorm_bwd_workspace_size(long, 64) > 0
+    assert lib.gdn_ssm_bwd_workspace_size(1, long, 64, 16, 1, 0) > 2**31
