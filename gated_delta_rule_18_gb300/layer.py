@@ -118,6 +118,13 @@ def _on_gpu(x, name="x"):
         _fail(4, f"{name} must be on a GPU")
 
 
+def _dim(t, name, dims, i):
+    """Size i of a tensor that has to have so many dimensions."""
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
+    return t.shape[i]
+
+
 def _fits(*sizes):
     """The library's sizes are 32-bit integers, and ctypes would pass the low half of a larger one."""
     if max(sizes) > 0x7fffffff:
@@ -177,6 +184,8 @@ def _guard(x, stream):
 def _as_rows(t, name):
     if t is None or t.dim() == 2:
         return t
+    if t.dim() == 0:
+        raise ValueError(f"{name} must have at least one dimension")
     try:
         return t.view(-1, t.shape[-1])
     except RuntimeError:
@@ -251,9 +260,8 @@ def gdn_rmsnorm_bwd(s, weight, dy, dres=None, eps=1e-6, workspace=None, stream=N
             return gdn_rmsnorm_bwd(s, weight, dy, dres, eps, workspace)
     L = _lib or _load()
     _on_gpu(s, "s")
-    D = s.shape[-1]
     s2 = _as_rows(s, "s")
-    R = s2.shape[0]
+    R, D = s2.shape
     _fits(R, D)
     if dy.shape != s.shape or dy.device != s.device:
         raise ValueError(f"dy must have shape {tuple(s.shape)} on {s.device}, got {tuple(dy.shape)}")
@@ -283,7 +291,7 @@ def gdn_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, fina
     L = _lib or _load()
     _on_gpu(x)
     B, T, D = x.shape
-    W = weight.shape[1]
+    W = _dim(weight, "weight", 2, 1)
     _fits(B, T, D, W)
     cp, n = _n_seq(cu_seqlens, B, x)
     if out is None:
@@ -313,7 +321,7 @@ def gdn_conv_bwd(x, weight, dout, bias=None, initial_state=None, cu_seqlens=None
     L = _lib or _load()
     _on_gpu(x)
     B, T, D = x.shape
-    W = weight.shape[1]
+    W = _dim(weight, "weight", 2, 1)
     _fits(B, T, D, W)
     cp, n = _n_seq(cu_seqlens, B, x)
     f32 = dict(dtype=torch.float32, device=x.device)
@@ -348,7 +356,7 @@ def gdn_conv_step(x, state, weight, bias=None, slots=None, silu=True, out=None, 
     L = _lib or _load()
     _on_gpu(x)
     n, D = x.shape
-    W, pool = weight.shape[1], state.shape[0]
+    W, pool = _dim(weight, "weight", 2, 1), _dim(state, "state", 3, 0)
     _fits(n, D, W, pool)
     if out is None:
         out = torch.empty((n, D), dtype=x.dtype, device=x.device)
@@ -376,7 +384,7 @@ def gdn_ssm_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_softplus=True
     L = _lib or _load()
     _on_gpu(x)
     B, T, C = x.shape
-    N = A.shape[1]
+    N = _dim(A, "A", 2, 1)
     _fits(B, T, C, N)
     cp, n = _n_seq(cu_seqlens, B, x)
     if out is None:
@@ -406,7 +414,7 @@ def gdn_ssm_bwd(x, dt, A, Bm, Cm, dout, D=None, z=None, dt_bias=None, dt_softplu
     L = _lib or _load()
     _on_gpu(x)
     B, T, C = x.shape
-    N = A.shape[1]
+    N = _dim(A, "A", 2, 1)
     _fits(B, T, C, N)
     cp, n = _n_seq(cu_seqlens, B, x)
     like, f32 = dict(dtype=x.dtype, device=x.device), dict(dtype=torch.float32, device=x.device)
@@ -449,7 +457,7 @@ def gdn_ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, dt_softp
     L = _lib or _load()
     _on_gpu(x)
     n, C = x.shape
-    N, pool = A.shape[1], state.shape[0]
+    N, pool = _dim(A, "A", 2, 1), _dim(state, "state", 3, 0)
     _fits(n, C, N, pool)
     if out is None:
         out = torch.empty((n, C), dtype=x.dtype, device=x.device)

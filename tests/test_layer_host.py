@@ -33,7 +33,7 @@ def claim(t, index=0):
 
 
 def on(index, *shape, dtype=torch.float32):
-    return claim(torch.zeros(*shape, dtype=dtype), index)
+    return claim(torch.zeros(shape, dtype=dtype), index)
 
 
 class Library:
@@ -230,3 +230,17 @@ def test_lengths_whose_sums_would_pass_32_bits_are_refused():
     long = 2**31 - 2**16
     assert lib.gdn_conv_bwd_workspace_size(1, long, 64, 4) > 0 and lib.gdn_rmsnorm_bwd_workspace_size(long, 64) > 0
     assert lib.gdn_ssm_bwd_workspace_size(1, long, 64, 16, 1, 0) > 2**31
+
+
+def test_tensors_of_too_few_dimensions_raise_value_errors(L):
+    line, x, w, one = on(0, 1, 4, 16), on(0, 4, 16), on(0, 16), on(0)
+    taps, a, bc, rows = on(0, 16, 4), on(0, 16, 8), on(0, 4, 8), on(0, 1, 4, 8)
+    for f in (lambda: gdn.gdn_rmsnorm_fwd(one, w), lambda: gdn.gdn_rmsnorm_bwd(one, w, one),
+              lambda: gdn.gdn_conv_fwd(line, w), lambda: gdn.gdn_conv_bwd(line, w, line),
+              lambda: gdn.gdn_conv_step(x, on(0, 4, 3, 16), w), lambda: gdn.gdn_conv_step(x, one, taps),
+              lambda: gdn.gdn_ssm_fwd(line, line, w, rows, rows), lambda: gdn.gdn_ssm_bwd(line, line, w, rows, rows, line),
+              lambda: gdn.gdn_ssm_step(x, x, w, bc, bc, on(0, 4, 16, 8)), lambda: gdn.gdn_ssm_step(x, x, a, bc, bc, one),
+              lambda: gdn.gdn_conv_fwd(x, taps), lambda: gdn.gdn_ssm_step(line, x, a, bc, bc, on(0, 4, 16, 8))):
+        with pytest.raises(ValueError):
+            f()
+    assert L.launched == []
