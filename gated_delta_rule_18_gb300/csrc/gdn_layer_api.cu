@@ -1,5 +1,7 @@
 // gdn_layer_api.cu -- the C entry points of the state-space layer's operators
 // (include/gdn.h): host-side checks, workspace layout and dispatch.
+#include <initializer_list>
+
 #include "../../include/gdn.h"
 #include "gdn_launch.cuh"
 #include "gdn_layer.cuh"
@@ -30,6 +32,83 @@ struct Rows {
         wide = wide && addr(p) % bytes == 0 && sb * e % bytes == 0 && st * e % bytes == 0;
     }
 };
+
+// The bytes of a tensor: T rows of `row` bytes, `st` apart, in B lines, `sb`
+// apart; none for a null pointer.
+struct Area {
+    int64_t at, sb, st, B, T, row;
+    int elem;
+    Area(const void *p, int dtype, int64_t sb_, int64_t st_, int64_t B_, int64_t T_, int64_t n)
+        : at((int64_t)addr(p)), sb(sb_ * elem_size(dtype)), st(st_ * elem_size(dtype)), B(p ? B_ : 0), T(T_),
+          row(n * elem_size(dtype)), elem(elem_size(dtype)) {
+        if (sb == T * st) T *= B, B = B > 0, sb = 0;  // lines that continue one another
+    }
+    Area(const void *p, int dtype, int64_t n) : Area(p, dtype, 0, 0, 1, 1, n) {}  // contiguous
+    bool empty() const { return B <= 0 || T <= 0 || row <= 0; }
+    int64_t line_bytes() const { return (T - 1) * st + row; }
+    int64_t bytes() const { return (B - 1) * sb + line_bytes(); }
+};
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0); }
+// Whether a row of line a and one of line b share a byte; b begins d bytes after a.
+bool lines_meet(const Area &a, const Area &b, int64_t d) {
+    if (d >= a.line_bytes() || -d >= b.line_bytes()) return false;
+    // some k >= k0 with k <= k1 and from + k step in (-b.row, a.row)
+    auto hit = [&](int64_t from, int64_t step, int64_t k0, int64_t k1) {
+        int64_t k = step > 0 ? floor_div(-b.row - from, step) + 1 : k0;
+        if (k < k0) k = k0;
+        return k <= k1 && from + k * step < a.row && from + k * step > -b.row;
+    };
+    if (a.st == b.st) return hit(d, a.st, -(a.T - 1), b.T - 1);
+    if (a.T > b.T) return lines_meet(b, a, -d);
+    for (int64_t t = 0; t < a.T; ++t)
+        if (hit(d - t * a.st, b.st, 0, b.T - 1)) return true;
+    return false;
+}
+bool meet(const Area &a, const Area &b) {
+    const int64_t d = b.at - a.at;
+    if (a.empty() || b.empty() || d >= a.bytes() || -d >= b.bytes()) return false;
+    if (a.sb == b.sb) {  // (only the difference of the lines counts)
+        for (int64_t k = 1 - a.B; k < b.B; ++k)
+            if (lines_meet(a, b, d + k * a.sb)) return true;
+        return false;
+    }
+    if (a.B * b.B > 1 << 20) return true;  // too many pairs of lines to tell them apart here
+    for (int64_t i = 0; i < a.B; ++i)
+        for (int64_t j = 0; j < b.B; ++j)
+            if (lines_meet(a, b, d + j * b.sb - i * a.sb)) return true;
+    return false;
+}
+bool rows_apart(const Area &a) {  // of an output
+    if (a.empty()) return true;
+    if (a.T > 1 && a.st < a.row) return false;
+    for (int64_t k = 1; k < a.B && k * a.sb < a.line_bytes(); ++k)
+        if (lines_meet(a, a, k * a.sb)) return false;
+    return true;
+}
+// Outputs must have rows of their own and overlap nothing; those in `placed`
+// may lie exactly on an input of the same layout in `same`, which is read
+// there by the threads that write it.
+gdn_status areas_ok(std::initializer_list<Area> placed, std::initializer_list<Area> other,
+                    std::initializer_list<Area> same, std::initializer_list<Area> in) {
+    const auto exact = [](const Area &a, const Area &b) {
+        return a.at == b.at && a.elem == b.elem && a.row == b.row && a.B == b.B && a.T == b.T &&
+               (a.B == 1 || a.sb == b.sb) && (a.T == 1 || a.st == b.st);
+    };
+    for (const auto *outs : {&placed, &other})
+        for (const Area *o = outs->begin(); o != outs->end(); ++o) {
+            if (!rows_apart(*o)) return GDN_ERR_LAYOUT;
+            for (const Area *q = o + 1; q != outs->end(); ++q)
+                if (meet(*o, *q)) return GDN_ERR_UNSUPPORTED;
+            for (const Area &q : same)
+                if (meet(*o, q) && !(outs == &placed && exact(*o, q))) return GDN_ERR_UNSUPPORTED;
+            for (const Area &q : in)
+                if (meet(*o, q)) return GDN_ERR_UNSUPPORTED;
+        }
+    for (const Area &o : placed)
+        for (const Area &q : other)
+            if (meet(o, q)) return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
 
 // Tokens or rows: with room for what kernels and sizes add to them (a tile, a run).
 bool length_ok(int n) { return n >= 0 && n <= INT32_MAX - 65535; }
@@ -110,6 +189,11 @@ gdn_status gdn_rmsnorm_fwd(const void *x, int64_t x_st, int x_dtype, const void 
     r.add(weight, GDN_F32, 0, 0);
     if (!r.ok || !f32_ok(scale)) return GDN_ERR_LAYOUT;
     if (R == 0) return GDN_OK;
+    const int64_t groups = group > 0 ? ((int64_t)D + group - 1) / group : 1;
+    const gdn_status a = areas_ok({Area(out, out_dtype, 0, out_st, 1, R, D), Area(res_out, res_dtype, 0, res_out_st, 1, R, D)},
+                                  {Area(scale, GDN_F32, R * groups)},
+                                  {Area(x, x_dtype, 0, x_st, 1, R, D), Area(residual, res_dtype, 0, res_st, 1, R, D)}, {});
+    if (a != GDN_OK) return a;
     NormParams p{};
     p.x = x, p.res = residual, p.x_st = x_st, p.res_st = res_st;
     p.x_bf16 = x_dtype == GDN_BF16, p.res_bf16 = res_dtype == GDN_BF16;
@@ -138,6 +222,10 @@ gdn_status gdn_rmsnorm_bwd(const void *s, int64_t s_st, int s_dtype, const void 
     r.add(dx, s_dtype, 0, dx_st);
     r.add(weight, GDN_F32, 0, 0);
     if (!r.ok || !f32_ok(dweight)) return GDN_ERR_LAYOUT;
+    const gdn_status a = areas_ok({Area(dx, s_dtype, 0, dx_st, 1, R, D)}, {Area(dweight, GDN_F32, D)},
+                                  {Area(s, s_dtype, 0, s_st, 1, R, D), Area(dy, dy_dtype, 0, dy_st, 1, R, D),
+                                   Area(dres, s_dtype, 0, dres_st, 1, R, D)}, {});
+    if (a != GDN_OK) return a;
     if (!ws_ok(workspace, ws_bytes, gdn_rmsnorm_bwd_workspace_size(R, D))) return GDN_ERR_WORKSPACE;
     NormBwdParams p{};
     p.s = s, p.dy = dy, p.dres = dres, p.s_st = s_st, p.dy_st = dy_st, p.dr_st = dres_st;
@@ -163,8 +251,6 @@ gdn_status gdn_conv_fwd(const void *x, int64_t x_sb, int64_t x_st, const float *
     if (!batch_ok(B, T, D, cu_seqlens, n_seq) || W < 2 || W > kConvMaxW) return GDN_ERR_SHAPE;
     if (!dtype_ok(dtype)) return GDN_ERR_DTYPE;
     if (flags & ~GDN_SILU) return GDN_ERR_UNSUPPORTED;
-    // (the inputs before a run of tokens are read by other threads than write there)
-    if ((x && x == out) || (initial_state && initial_state == final_state)) return GDN_ERR_UNSUPPORTED;
     Rows r;
     r.add(x, dtype, x_sb, x_st);
     r.add(out, dtype, out_sb, out_st);
@@ -173,6 +259,11 @@ gdn_status gdn_conv_fwd(const void *x, int64_t x_sb, int64_t x_st, const float *
     r.add(weight, GDN_F32, 0, 0);
     r.add(bias, GDN_F32, 0, 0);
     if (!r.ok || !f32_ok(cu_seqlens)) return GDN_ERR_LAYOUT;
+    // (the inputs before a run of tokens are read by other threads than write there)
+    const int64_t window = (int64_t)n_seq * (W - 1) * D;
+    const gdn_status a = areas_ok({}, {Area(out, dtype, out_sb, out_st, B, T, D), Area(final_state, dtype, window)}, {},
+                                  {Area(x, dtype, x_sb, x_st, B, T, D), Area(initial_state, dtype, window)});
+    if (a != GDN_OK) return a;
     if (cu_seqlens && !ws_ok(workspace, ws_bytes, kAlign)) return GDN_ERR_WORKSPACE;
     if (T == 0 && !final_state && !cu_seqlens) return GDN_OK;
     ConvParams p{};
@@ -208,6 +299,13 @@ gdn_status gdn_conv_bwd(const void *x, int64_t x_sb, int64_t x_st, const float *
     r.add(weight, GDN_F32, 0, 0);
     r.add(bias, GDN_F32, 0, 0);
     if (!r.ok || !f32_ok(cu_seqlens) || !f32_ok(dweight) || !f32_ok(dbias)) return GDN_ERR_LAYOUT;
+    const int64_t window = (int64_t)n_seq * (W - 1) * D;
+    const gdn_status a =
+        areas_ok({}, {Area(dx, dtype, (int64_t)B * T * D), Area(dinitial_state, dtype, window),
+                      Area(dweight, GDN_F32, (int64_t)D * W), Area(dbias, GDN_F32, D)}, {},
+                 {Area(x, dtype, x_sb, x_st, B, T, D), Area(dout, dtype, dout_sb, dout_st, B, T, D),
+                  Area(initial_state, dtype, window), Area(dfinal_state, dtype, window)});
+    if (a != GDN_OK) return a;
     if (!ws_ok(workspace, ws_bytes, gdn_conv_bwd_workspace_size(B, T, D, W))) return GDN_ERR_WORKSPACE;
     ConvParams p{};
     p.x = x, p.x_sb = x_sb, p.x_st = x_st, p.weight = weight, p.bias = bias, p.init = initial_state;
@@ -246,6 +344,9 @@ gdn_status gdn_conv_step(const void *x, int64_t x_st, const float *weight, int W
     r.add(bias, GDN_F32, 0, 0);
     if (!r.ok || !f32_ok(slots)) return GDN_ERR_LAYOUT;
     if (n == 0) return GDN_OK;
+    const gdn_status a = areas_ok({Area(out, dtype, 0, out_st, 1, n, D)}, {Area(state, dtype, (int64_t)n_slots * (W - 1) * D)},
+                                  {Area(x, dtype, 0, x_st, 1, n, D)}, {});
+    if (a != GDN_OK) return a;
     ConvStepParams p{};
     p.x = x, p.x_st = x_st, p.weight = weight, p.bias = bias, p.state = state, p.slots = slots;
     p.out = out, p.o_st = out_st, p.n = n, p.n_slots = n_slots, p.D = D, p.W = W;
@@ -308,7 +409,12 @@ gdn_status gdn_ssm_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *dt
                                    z_st, dt_bias, h0, cu_seqlens, n_seq, B, T, D, N, dtype, flags, r, p);
     if (s != GDN_OK) return s;
     if (!f32_ok(h_final)) return GDN_ERR_LAYOUT;
-    if (h0 && h0 == h_final) return GDN_ERR_UNSUPPORTED;
+    const int64_t states = (int64_t)n_seq * D * N;
+    const gdn_status a =
+        areas_ok({Area(out, dtype, out_sb, out_st, B, T, D)}, {Area(h_final, GDN_F32, states)},
+                 {Area(x, dtype, x_sb, x_st, B, T, D), Area(dt, dtype, dt_sb, dt_st, B, T, D), Area(z, dtype, z_sb, z_st, B, T, D)},
+                 {Area(bm, dtype, bm_sb, bm_st, B, T, N), Area(cm, dtype, cm_sb, cm_st, B, T, N), Area(h0, GDN_F32, states)});
+    if (a != GDN_OK) return a;
     const SsmWs L = ssm_ws(cu_seqlens ? 1 : B, T, D, N);
     if (!ws_ok(workspace, ws_bytes, L.total)) return GDN_ERR_WORKSPACE;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
@@ -357,6 +463,16 @@ gdn_status gdn_ssm_bwd(const void *x, int64_t x_sb, int64_t x_st, const void *dt
     for (const void *f : {(const void *)dh_final, (const void *)dA, (const void *)dD, (const void *)ddt_bias,
                           (const void *)dh0})
         if (!f32_ok(f)) return GDN_ERR_LAYOUT;
+    const int64_t states = (int64_t)n_seq * D * N, rows = (int64_t)B * T;
+    const gdn_status a =
+        areas_ok({Area(dx, dtype, 0, D, 1, rows, D), Area(ddt, dtype, 0, D, 1, rows, D), Area(dz, dtype, 0, D, 1, rows, D)},
+                 {Area(dbm, dtype, rows * N), Area(dcm, dtype, rows * N), Area(dA, GDN_F32, (int64_t)D * N),
+                  Area(dD, GDN_F32, D), Area(ddt_bias, GDN_F32, D), Area(dh0, GDN_F32, states)},
+                 {Area(x, dtype, x_sb, x_st, B, T, D), Area(dt, dtype, dt_sb, dt_st, B, T, D),
+                  Area(z, dtype, z_sb, z_st, B, T, D), Area(dout, dtype, dout_sb, dout_st, B, T, D)},
+                 {Area(bm, dtype, bm_sb, bm_st, B, T, N), Area(cm, dtype, cm_sb, cm_st, B, T, N),
+                  Area(h0, GDN_F32, states), Area(dh_final, GDN_F32, states)});
+    if (a != GDN_OK) return a;
     const SsmBwdWs L = ssm_bwd_ws(B, T, D, N, cu_seqlens != nullptr);
     if (!ws_ok(workspace, ws_bytes, L.total)) return GDN_ERR_WORKSPACE;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
@@ -404,6 +520,11 @@ gdn_status gdn_ssm_step(const void *x, int64_t x_st, const void *dt, int64_t dt_
     if (!r.ok || !bc.ok || !f32_ok(A) || !f32_ok(Dv) || !f32_ok(dt_bias) || !f32_ok(state) || !f32_ok(slots))
         return GDN_ERR_LAYOUT;
     if (n == 0) return GDN_OK;
+    const gdn_status a =
+        areas_ok({Area(out, dtype, 0, out_st, 1, n, D)}, {Area(state, GDN_F32, (int64_t)n_slots * D * N)},
+                 {Area(x, dtype, 0, x_st, 1, n, D), Area(dt, dtype, 0, dt_st, 1, n, D), Area(z, dtype, 0, z_st, 1, n, D)},
+                 {Area(bm, dtype, 0, bm_st, 1, n, N), Area(cm, dtype, 0, cm_st, 1, n, N)});
+    if (a != GDN_OK) return a;
     SsmStepParams p{};
     p.x = x, p.dt = dt, p.bm = bm, p.cm = cm, p.z = z;
     p.x_st = x_st, p.dt_st = dt_st, p.bm_st = bm_st, p.cm_st = cm_st, p.z_st = z_st;

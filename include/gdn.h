@@ -505,10 +505,11 @@ gdn_status gdn_frame_fwd(const void *q, const void *k, gdn_tensor_desc qkd,
  *     be empty). A malformed cu_seqlens gives wrong values but no access out
  *     of range, and is reported as GDN_DEVERR_SEQLENS in the workspace's
  *     first word (gdn_last_device_error), where the call has a workspace.
- *   - Outputs do not overlap inputs, except res_out with residual and the
- *     states that are updated in place (gdn_conv_fwd with out == x or
- *     final_state == initial_state, gdn_ssm_fwd with h_final == h0 return
- *     GDN_ERR_UNSUPPORTED).
+ *   - Outputs have rows of their own (else GDN_ERR_LAYOUT) and overlap
+ *     neither inputs nor one another (else GDN_ERR_UNSUPPORTED), except the
+ *     states that are updated in place and, in the norm and the scan, outputs
+ *     of x's shape that lie exactly on an input of their type and strides
+ *     (res_out on residual, out on x).
  *   - slots: int32 (n), the pool row of each request's state, distinct; a
  *     request whose slot is not in [0, n_slots) is a padding row: its output
  *     is zero and no state changes. NULL: request i uses row i.

@@ -98,3 +98,22 @@ def test_very_low_and_high_gates(dtype, C):
     for k, r in ref.items():
         act = k in ("dx", "ddt", "dBm", "dCm", "dz")
         assert rel(got[k], r) <= (TOL_BF if dtype == BF and act else TOL_SCAN), k
+
+
+@pytest.mark.parametrize("C", [64, 37])
+def test_outputs_in_place_of_an_input(C):
+    T, N = 400, 16
+    v = {k: dev(t) for k, t in scan_case(2, T, C, N, None, BF, True, 260).items()}
+
+    def scan(out):
+        return gdn.gdn_ssm_fwd(v["x"], v["dt"], v["A"], v["Bm"], v["Cm"], D=v["D"], z=v["z"], dt_bias=v["dt_bias"],
+                               h0=v["h0"], out=out)
+    want = scan(None)
+    for k in ("x", "dt", "z"):
+        keep = v[k].clone()
+        assert torch.equal(scan(v[k]), want) and torch.equal(v[k], want)
+        v[k].copy_(keep)
+    x, r, w = randn((700, C), BF, 270).to(DEV), randn((700, C), BF, 271).to(DEV), randn((C,), F32, 272, 0.1, 1.0).to(DEV)
+    want = gdn.gdn_rmsnorm_fwd(x, w, residual=r)
+    got = gdn.gdn_rmsnorm_fwd(x, w, residual=r, out=x, residual_out=r)
+    assert torch.equal(got["out"], want["out"]) and torch.equal(r, want["residual"]) and got["out"] is x
