@@ -5,8 +5,8 @@ import pytest
 import torch
 
 import gated_delta_rule_18_gb300 as gdn
-from test_layer_gpu import (BF, DEV, F32, F64, TOL_BF, TOL_SCAN, built, cu_of, dev, f64, randn, ref_scan, rel,  # noqa: F401
-                            scan_case)
+from test_layer_gpu import (BF, DEV, F32, TOL_BF, TOL_F32, TOL_SCAN, built, cu_of, dev, f64, randn, ref_conv,  # noqa: F401
+                            ref_norm, ref_scan, rel, scan_case, strided)
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +117,73 @@ def test_outputs_in_place_of_an_input(C):
     want = gdn.gdn_rmsnorm_fwd(x, w, residual=r)
     got = gdn.gdn_rmsnorm_fwd(x, w, residual=r, out=x, residual_out=r)
     assert torch.equal(got["out"], want["out"]) and torch.equal(r, want["residual"]) and got["out"] is x
+
+
+# How the rows of a call's activations lie: whole tensors; slices of wider rows that keep 16-byte
+# boundaries, as halves and parts of projections do; slices at odd offsets.
+PLACES = {"whole": lambda t: t, "wide": lambda t: strided(t, 8, 24), "odd": strided}
+places = pytest.mark.parametrize("place", PLACES)
+
+
+@places
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,T,C,N,lens", [(2, 300, 64, 16, None), (1, 700, 136, 16, [3, 0, 500, 190, 7]),
+                                          (3, 260, 40, 32, None), (1, 300, 24, 64, [100, 200]), (2, 200, 16, 128, None)])
+def test_scan_and_gradient_over_rows_of_any_layout(place, dtype, B, T, C, N, lens):
+    """Gated, with softplus, skip, bias and states, over lines cut into chunks and runs."""
+    n = B if lens is None else len(lens)
+    v, do, df = scan_case(B, T, C, N, lens, dtype, True, 300), randn((B, T, C), dtype, 310), randn((n, C, N), F32, 311)
+    lay = lambda k, t: PLACES[place](t) if k in ("x", "dt", "z", "Bm", "Cm", "dout") else t  # noqa: E731
+    a = {k: lay(k, dev(t)) for k, t in v.items()}
+    final, out = torch.full((n, C, N), float("nan"), device=DEV), lay("x", torch.zeros(B, T, C, dtype=dtype, device=DEV))
+    got = gdn.gdn_ssm_fwd(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], D=a["D"], z=a["z"], dt_bias=a["dt_bias"], h0=a["h0"],
+                          cu_seqlens=dev(cu_of(lens)), h_final=final, out=out)
+    ref, fin = ref_scan({k: f64(t) for k, t in v.items()}, lens, True)
+    assert rel(got, ref) <= (TOL_BF if dtype == BF else TOL_SCAN) and rel(final, fin) <= TOL_SCAN
+    got, ref = scan_gradients(v, do, lens, df, place=lay), ref_gradients(v, do, lens, df)
+    assert set(got) == set(ref)
+    for k, r in ref.items():
+        act = k in ("dx", "ddt", "dBm", "dCm", "dz")
+        assert rel(got[k], r) <= (TOL_BF if dtype == BF and act else TOL_SCAN), k
+
+
+@places
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("W", [2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("B,T,D,lens", [(2, 129, 264, None), (1, 333, 136, [5, 0, 200, 1, 1, 126, 0])])
+def test_convolution_and_gradient_over_rows_of_any_layout(place, dtype, W, B, T, D, lens):
+    n, lay = B if lens is None else len(lens), PLACES[place]
+    leaf = dict(x=randn((B, T, D), dtype, 320), weight=randn((D, W), F32, 321, 0.5), bias=randn((D,), F32, 322),
+                initial_state=randn((n, W - 1, D), dtype, 323))
+    do, df = randn((B, T, D), dtype, 324), randn((n, W - 1, D), dtype, 325)
+    v = {k: f64(t).requires_grad_() for k, t in leaf.items()}
+    ref, fin = ref_conv(v["x"], v["weight"], v["bias"], v["initial_state"], lens, True)
+    grad = torch.autograd.grad((ref * f64(do)).sum() + (fin * f64(df)).sum(), tuple(v.values()))
+    a = {k: dev(t) for k, t in leaf.items()}
+    final, out = torch.full((n, W - 1, D), float("nan"), dtype=dtype, device=DEV), lay(torch.zeros(B, T, D, dtype=dtype, device=DEV))
+    kw = dict(bias=a["bias"], initial_state=a["initial_state"], cu_seqlens=dev(cu_of(lens)))
+    got = gdn.gdn_conv_fwd(lay(a["x"]), a["weight"], final_state=final, out=out, **kw)
+    assert rel(got, ref) <= (TOL_BF if dtype == BF else TOL_F32) and torch.equal(f64(final), fin)
+    got = gdn.gdn_conv_bwd(lay(a["x"]), a["weight"], lay(dev(do)), dfinal_state=dev(df), **kw)
+    for k, r in zip(v, grad):
+        assert rel(got["d" + k], r) <= (TOL_BF if dtype == BF and k in ("x", "initial_state") else TOL_F32), k
+
+
+@places
+@pytest.mark.parametrize("ds,dy", [(BF, BF), (F32, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("rows,D", [(700, 72), (40, 1000), (9, 4096), (5, 9000), (3, 16384)])
+def test_norm_and_gradient_over_rows_of_any_layout(place, ds, dy, rows, D):
+    """The norm of an input of one type with a residual stream of the other, and its gradient."""
+    lay = PLACES[place]
+    x, r, w = randn((rows, D), dy, 330), randn((rows, D), ds, 331, 2.0), randn((D,), F32, 332, 0.1, 1.0)
+    ref_s, ref = ref_norm(x, w, r, 1e-6)
+    got = gdn.gdn_rmsnorm_fwd(lay(dev(x)), dev(w), residual=lay(dev(r)), out=lay(torch.zeros(rows, D, dtype=dy, device=DEV)),
+                              residual_out=lay(torch.zeros(rows, D, dtype=ds, device=DEV)))
+    assert rel(got["out"], ref) <= (TOL_BF if dy == BF else TOL_F32)
+    assert rel(got["residual"], ref_s) <= (TOL_BF if ds == BF else TOL_F32)
+    g, q = randn((rows, D), dy, 333), randn((rows, D), ds, 334)
+    u, wr = f64(r).requires_grad_(), f64(w).requires_grad_()
+    loss = (ref_norm(u, wr, None, 1e-6)[1] * f64(g)).sum() + (u * f64(q)).sum()
+    dx, dw = torch.autograd.grad(loss, (u, wr))
+    got = gdn.gdn_rmsnorm_bwd(lay(dev(r)), dev(w), lay(dev(g)), dres=lay(dev(q)))
+    assert rel(got["dx"], dx) <= (TOL_BF if ds == BF else TOL_F32) and rel(got["dweight"], dw) <= TOL_F32
