@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(256) ssm_chain_kernel(const SsmParams p, int n
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            h = isnan(v[k]) ? e[k] : fmaf(ex2f(a * v[k]), h, e[k]);
+            h = isnan(v[k]) || h == 0.f ? e[k] : fmaf(ex2f(a * v[k]), h, e[k]);  // (A > 0 may overflow)
             if (c + k < nch) s[(c + k) * dnp] = h;
         }
     }

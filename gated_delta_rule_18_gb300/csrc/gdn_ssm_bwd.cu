@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(256) ssm_bwd_chain_kernel(const SsmParams p, i
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                h = isnan(v[k]) ? e[k] : fmaf(ex2f(a * v[k]), h, e[k]);
+                h = isnan(v[k]) || h == 0.f ? e[k] : fmaf(ex2f(a * v[k]), h, e[k]);  // (A > 0 may overflow)
                 if (c + k + 1 < p.ngroup) s[(c + k) * dnp] = h;
             }
         }
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(256) ssm_bwd_chain_kernel(const SsmParams p, i
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                g = isnan(v[k]) ? e[k] : fmaf(ex2f(a * v[k]), g, e[k]);
+                g = isnan(v[k]) || g == 0.f ? e[k] : fmaf(ex2f(a * v[k]), g, e[k]);
                 if (r >= k) s[(r - k) * dnp] = g;
             }
         }

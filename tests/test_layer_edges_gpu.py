@@ -187,3 +187,21 @@ def test_norm_and_gradient_over_rows_of_any_layout(place, ds, dy, rows, D):
     dx, dw = torch.autograd.grad(loss, (u, wr))
     got = gdn.gdn_rmsnorm_bwd(lay(dev(r)), dev(w), lay(dev(g)), dres=lay(dev(q)))
     assert rel(got["dx"], dx) <= (TOL_BF if ds == BF else TOL_F32) and rel(got["dweight"], dw) <= TOL_F32
+
+
+@pytest.mark.parametrize("C", [64, 37])
+def test_growing_states_that_no_input_has_reached_stay_zero(C):
+    """A > 0 and a line that begins with zeros: a chunk's growth passes fp32's range, the zero state does not."""
+    T, N = 1024, 16
+    v = scan_case(1, T, C, N, None, F32, False, 340)
+    v["A"], v["dt"] = v["A"].abs() * 0 + 2, torch.ones(1, T, C)
+    v["x"][:, :T - 8] = 0
+    ref, fin = ref_scan({k: f64(t) for k, t in v.items()}, None, False)
+    final = torch.empty(1, C, N, device=DEV)
+    a = {k: dev(t) for k, t in v.items()}
+    got = gdn.gdn_ssm_fwd(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], dt_softplus=False, h_final=final)
+    assert rel(got, ref) <= TOL_SCAN and rel(final, fin) <= TOL_SCAN
+    do = randn((1, T, C), F32, 350)
+    do[:, :T - 8] = 0
+    got, ref = scan_gradients(v, do, softplus=False), ref_gradients(v, do, softplus=False)
+    assert rel(got["dCm"], ref["dCm"]) <= TOL_SCAN
