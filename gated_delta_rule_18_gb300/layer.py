@@ -113,29 +113,18 @@ def _flat(t, name, shape, dtype, like):
     return t.data_ptr()
 
 
-def _on_gpu(x, name="x"):
-    if not x.is_cuda:
-        _fail(4, f"{name} must be on a GPU")
-
-
-def _dim(t, name, dims, i):
-    """Size i of a tensor that has to have so many dimensions."""
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
-    return t.shape[i]
-
-
-def _fits(*sizes):
-    """The library's sizes are 32-bit integers, and ctypes would pass the low half of a larger one."""
-    if max(sizes) > 0x7fffffff:
-        raise ValueError(f"a size must be at most 2147483647, got {max(sizes)}")
+# (The library's sizes are 32-bit integers, and ctypes would pass the low half of
+# a larger one. The checks stand inline: a call of its own is 0.2 us.)
+def _too_large(*sizes):
+    raise ValueError(f"a size must be at most 2147483647, got {max(sizes)}")
 
 
 def _n_seq(cu_seqlens, B, like):
     """(pointer, sequences) of a batch."""
     if cu_seqlens is None:
         return 0, B
-    _fits(cu_seqlens.numel())
+    if cu_seqlens.numel() >> 31:
+        _too_large(cu_seqlens.numel())
     return _flat(cu_seqlens, "cu_seqlens", (cu_seqlens.numel(),), torch.int32, like), cu_seqlens.numel() - 1
 
 
@@ -158,18 +147,16 @@ def _stream(like):
     return torch.cuda.current_stream(like.device).cuda_stream
 
 
-def _wrote(*tensors):
-    """Tensors that a call has written: autograd notices if it had saved one of them."""
-    for t in tensors:
-        if t is not None:
-            torch.autograd.graph.increment_version(t)
-
-
+# of a tensor of the caller's that a call has written: autograd notices if it had saved one
+_count_version = torch.autograd.graph.increment_version
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _away(x):
-    return x.is_cuda and x.get_device() != _current_device()
+def _elsewhere(x):
+    """Whether x lies on another GPU than the current one."""
+    if not x.is_cuda:
+        _fail(4, "the tensors must be on a GPU")
+    return x.get_device() != _current_device()
 
 
 def _guard(x, stream):
@@ -201,18 +188,19 @@ def gdn_rmsnorm_fwd(x, weight, residual=None, eps=1e-6, out_dtype=None, group=0,
     of one stride; with out_dtype=torch.float8_e4m3fn,
     "scale": fp32, one for each `group` channels (32, 64, 128 or 256; 0: the
     row), out * scale being y."""
-    if stream is not None or _away(x):
+    if stream is not None or _elsewhere(x):
         with _guard(x, stream):
             return gdn_rmsnorm_fwd(x, weight, residual, eps, out_dtype, group, out, residual_out)
     L = _lib or _load()
-    _on_gpu(x)
     x2 = x if x.dim() == 2 else _as_rows(x, "x")
     R, D = x2.shape
-    _fits(R, D, group, -group)
+    if (R | D | abs(group)) >> 31:
+        _too_large(R, D, abs(group))
     q8 = out_dtype is _F8
     if out_dtype is not None and not q8 and out_dtype != x.dtype:
         _fail(3, f"out_dtype must be {x.dtype} or torch.float8_e4m3fn, got {out_dtype}")
     ty = out_dtype if q8 else x.dtype
+    given = (out, residual_out)
     if out is None:
         out = torch.empty_like(x, dtype=ty, memory_format=torch.contiguous_format)
     elif out.shape != x.shape or out.dtype != ty:
@@ -246,7 +234,9 @@ def gdn_rmsnorm_fwd(x, weight, residual=None, eps=1e-6, out_dtype=None, group=0,
                            E4M3 if q8 else _CODE[ty], rop, ros, sp, R, D, group, eps, _stream(x))
     if st:
         _fail(st, "gdn_rmsnorm_fwd")
-    _wrote(out, residual_out)
+    for t in given:
+        if t is not None:
+            _count_version(t)
     return res
 
 
@@ -255,14 +245,14 @@ def gdn_rmsnorm_bwd(s, weight, dy, dres=None, eps=1e-6, workspace=None, stream=N
     x, without a residual), the output's gradient dy and the residual
     stream's own gradient dres (s's type): a dict of "dx" (s's type; the
     gradient of x and of the residual alike) and "dweight" (fp32)."""
-    if stream is not None or _away(s):
+    if stream is not None or _elsewhere(s):
         with _guard(s, stream):
             return gdn_rmsnorm_bwd(s, weight, dy, dres, eps, workspace)
     L = _lib or _load()
-    _on_gpu(s, "s")
     s2 = _as_rows(s, "s")
     R, D = s2.shape
-    _fits(R, D)
+    if (R | D) >> 31:
+        _too_large(R, D)
     if dy.shape != s.shape or dy.device != s.device:
         raise ValueError(f"dy must have shape {tuple(s.shape)} on {s.device}, got {tuple(dy.shape)}")
     dx = torch.empty(s.shape, dtype=s.dtype, device=s.device)
@@ -285,15 +275,16 @@ def gdn_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, fina
     (D, W), bias (D) fp32; initial_state / final_state (n_seq, W - 1, D) in
     x's type, the inputs before and at the end of each sequence, oldest
     first; cu_seqlens int32 (n_seq + 1) with B == 1. Returns out."""
-    if stream is not None or _away(x):
+    if stream is not None or _elsewhere(x):
         with _guard(x, stream):
             return gdn_conv_fwd(x, weight, bias, initial_state, cu_seqlens, final_state, silu, out, workspace)
     L = _lib or _load()
-    _on_gpu(x)
     B, T, D = x.shape
-    W = _dim(weight, "weight", 2, 1)
-    _fits(B, T, D, W)
+    _, W = weight.shape
+    if (B | T | D | W) >> 31:
+        _too_large(B, T, D, W)
     cp, n = _n_seq(cu_seqlens, B, x)
+    given = out
     if out is None:
         out = torch.empty((B, T, D), dtype=x.dtype, device=x.device)
     ws = wp = wn = 0
@@ -306,7 +297,9 @@ def gdn_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, fina
                         B, T, D, _code(x, "x"), SILU if silu else 0, wp, wn, _stream(x))
     if st:
         _fail(st, "gdn_conv_fwd")
-    _wrote(out, final_state)
+    for t in (given, final_state):
+        if t is not None:
+            _count_version(t)
     return out
 
 
@@ -315,14 +308,14 @@ def gdn_conv_bwd(x, weight, dout, bias=None, initial_state=None, cu_seqlens=None
     """Gradients of gdn_conv_fwd for L = sum(dout * out) + sum(dfinal_state *
     final_state): a dict of "dx" (x's type), "dweight" (fp32), with a bias
     "dbias" (fp32) and with an initial state "dinitial_state" (x's type)."""
-    if stream is not None or _away(x):
+    if stream is not None or _elsewhere(x):
         with _guard(x, stream):
             return gdn_conv_bwd(x, weight, dout, bias, initial_state, cu_seqlens, dfinal_state, silu, workspace)
     L = _lib or _load()
-    _on_gpu(x)
     B, T, D = x.shape
-    W = _dim(weight, "weight", 2, 1)
-    _fits(B, T, D, W)
+    _, W = weight.shape
+    if (B | T | D | W) >> 31:
+        _too_large(B, T, D, W)
     cp, n = _n_seq(cu_seqlens, B, x)
     f32 = dict(dtype=torch.float32, device=x.device)
     r = {"dx": torch.empty((B, T, D), dtype=x.dtype, device=x.device), "dweight": torch.empty((D, W), **f32)}
@@ -350,24 +343,30 @@ def gdn_conv_step(x, state, weight, bias=None, slots=None, silu=True, out=None, 
     type, the requests' windows, shifted by x in place; slots int32 (n), each
     request's row of state (distinct; a value outside [0, n_slots) marks a
     padding row, whose output is 0), or None for rows 0 .. n - 1. Returns out."""
-    if stream is not None or _away(x):
+    if stream is not None or _elsewhere(x):
         with _guard(x, stream):
             return gdn_conv_step(x, state, weight, bias, slots, silu, out)
     L = _lib or _load()
-    _on_gpu(x)
     n, D = x.shape
-    W, pool = _dim(weight, "weight", 2, 1), _dim(state, "state", 3, 0)
-    _fits(n, D, W, pool)
+    (_, W), (pool, _, _) = weight.shape, state.shape
+    if (n | D | W | pool) >> 31:
+        _too_large(n, D, W, pool)
+    given = out
     if out is None:
         out = torch.empty((n, D), dtype=x.dtype, device=x.device)
+        at = out.data_ptr(), D
+    else:
+        at = _rows(out, "out", (n, D), x)
     st = L.gdn_conv_step(*_rows(x, "x", (n, D), x), _flat(weight, "weight", (D, W), torch.float32, x), W,
                          _flat(bias, "bias", (D,), torch.float32, x),
                          _flat(state, "state", (pool, W - 1, D), x.dtype, x),
-                         _flat(slots, "slots", (n,), torch.int32, x), pool, *_rows(out, "out", (n, D), x), n, D,
+                         _flat(slots, "slots", (n,), torch.int32, x), pool, *at, n, D,
                          _code(x, "x"), SILU if silu else 0, _stream(x))
     if st:
         _fail(st, "gdn_conv_step")
-    _wrote(out, state)
+    if given is not None:
+        _count_version(given)
+    _count_version(state)
     return out
 
 
@@ -378,15 +377,16 @@ def gdn_ssm_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_softplus=True
     * silu(z). x, dt, z (B, T, C); Bm, Cm (B, T, N); A (C, N), D, dt_bias (C)
     fp32; h0 / h_final (n_seq, C, N) fp32; cu_seqlens int32 (n_seq + 1) with
     B == 1. Returns out."""
-    if stream is not None or _away(x):
+    if stream is not None or _elsewhere(x):
         with _guard(x, stream):
             return gdn_ssm_fwd(x, dt, A, Bm, Cm, D, z, dt_bias, dt_softplus, h0, cu_seqlens, h_final, out, workspace)
     L = _lib or _load()
-    _on_gpu(x)
     B, T, C = x.shape
-    N = _dim(A, "A", 2, 1)
-    _fits(B, T, C, N)
+    _, N = A.shape
+    if (B | T | C | N) >> 31:
+        _too_large(B, T, C, N)
     cp, n = _n_seq(cu_seqlens, B, x)
+    given = out
     if out is None:
         out = torch.empty((B, T, C), dtype=x.dtype, device=x.device)
     ws, wp, wn = _workspace(workspace, L.gdn_ssm_workspace_size(B, T, C, N, n, 1 if cp else 0), x)
@@ -399,7 +399,9 @@ def gdn_ssm_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_softplus=True
                        SOFTPLUS if dt_softplus else 0, wp, wn, _stream(x))
     if st:
         _fail(st, "gdn_ssm_fwd")
-    _wrote(out, h_final)
+    for t in (given, h_final):
+        if t is not None:
+            _count_version(t)
     return out
 
 
@@ -408,14 +410,14 @@ def gdn_ssm_bwd(x, dt, A, Bm, Cm, dout, D=None, z=None, dt_bias=None, dt_softplu
     """Gradients of gdn_ssm_fwd for L = sum(dout * out) + sum(dh_final *
     h_final), the forward recomputed: a dict of dx, ddt, dBm, dCm (x's type),
     dA (fp32) and, for what was given, dD, dz, ddt_bias, dh0."""
-    if stream is not None or _away(x):
+    if stream is not None or _elsewhere(x):
         with _guard(x, stream):
             return gdn_ssm_bwd(x, dt, A, Bm, Cm, dout, D, z, dt_bias, dt_softplus, h0, cu_seqlens, dh_final, workspace)
     L = _lib or _load()
-    _on_gpu(x)
     B, T, C = x.shape
-    N = _dim(A, "A", 2, 1)
-    _fits(B, T, C, N)
+    _, N = A.shape
+    if (B | T | C | N) >> 31:
+        _too_large(B, T, C, N)
     cp, n = _n_seq(cu_seqlens, B, x)
     like, f32 = dict(dtype=x.dtype, device=x.device), dict(dtype=torch.float32, device=x.device)
     r = {"dx": torch.empty((B, T, C), **like), "ddt": torch.empty((B, T, C), **like), "dA": torch.empty((C, N), **f32),
@@ -451,24 +453,30 @@ def gdn_ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, dt_softp
     """One token of n requests of the scan: x, dt, z (n, C); Bm, Cm (n, N);
     state (n_slots, C, N) fp32, updated in place; slots as for gdn_conv_step.
     Returns out."""
-    if stream is not None or _away(x):
+    if stream is not None or _elsewhere(x):
         with _guard(x, stream):
             return gdn_ssm_step(x, dt, A, Bm, Cm, state, D, z, dt_bias, dt_softplus, slots, out)
     L = _lib or _load()
-    _on_gpu(x)
     n, C = x.shape
-    N, pool = _dim(A, "A", 2, 1), _dim(state, "state", 3, 0)
-    _fits(n, C, N, pool)
+    (_, N), (pool, _, _) = A.shape, state.shape
+    if (n | C | N | pool) >> 31:
+        _too_large(n, C, N, pool)
+    given = out
     if out is None:
         out = torch.empty((n, C), dtype=x.dtype, device=x.device)
+        at = out.data_ptr(), C
+    else:
+        at = _rows(out, "out", (n, C), x)
     f = torch.float32
     st = L.gdn_ssm_step(*_rows(x, "x", (n, C), x), *_rows(dt, "dt", (n, C), x), _flat(A, "A", (C, N), f, x),
                         *_rows(Bm, "Bm", (n, N), x), *_rows(Cm, "Cm", (n, N), x), _flat(D, "D", (C,), f, x),
                         *_rows(z, "z", (n, C), x), _flat(dt_bias, "dt_bias", (C,), f, x),
                         _flat(state, "state", (pool, C, N), f, x), _flat(slots, "slots", (n,), torch.int32, x), pool,
-                        *_rows(out, "out", (n, C), x), n, C, N, _code(x, "x"), SOFTPLUS if dt_softplus else 0,
+                        *at, n, C, N, _code(x, "x"), SOFTPLUS if dt_softplus else 0,
                         _stream(x))
     if st:
         _fail(st, "gdn_ssm_step")
-    _wrote(out, state)
+    if given is not None:
+        _count_version(given)
+    _count_version(state)
     return out
