@@ -30,13 +30,16 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
     return r;
 }
 
-// y / scale for one scale. An IEEE division costs some ten instructions a
-// value; one reciprocal and a correction of the quotient by its remainder
-// round the same (|y| <= 448 scale (1 + 2^-24), no intermediate overflows
-// unless the scale itself is out of range, where the plain quotient is taken).
+// y / scale for one scale, rounded to nearest, by Markstein's theorem (IBM J.
+// Res. Dev. 34, 1990): with r the nearest to 1 / scale and q = y r, the
+// remainder y - q scale is exact in a fused multiply-add and q + r (y - q scale)
+// rounds to the nearest quotient. It needs the remainder's bits above 2^-149
+// for every y that is not 0 in e4m3 (y >= 2^-10 scale, remainder >= 2^-47 y) and
+// a normal r: scales out of that range are divided by. One reciprocal serves
+// the eight values of a vector.
 __device__ __forceinline__ void quantise(f32x2 (&y)[kPairs], float scale) {
     const float dv = scale == 0.f ? 1.f : scale;
-    if (dv > 1e-30f && dv < 1e30f) {
+    if (dv > 1e-27f && dv < 1e30f) {
         const float r = 1.f / dv;
         const f32x2 r2 = pack2(r, r), n2 = pack2(-dv, -dv);
 #pragma unroll

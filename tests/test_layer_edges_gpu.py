@@ -205,3 +205,18 @@ def test_growing_states_that_no_input_has_reached_stay_zero(C):
     do[:, :T - 8] = 0
     got, ref = scan_gradients(v, do, softplus=False), ref_gradients(v, do, softplus=False)
     assert rel(got["dCm"], ref["dCm"]) <= TOL_SCAN
+
+
+@pytest.mark.parametrize("group", [0, 64])
+@pytest.mark.parametrize("size", [1e-36, 1e-28, 3e-26, 1e-20, 1.0, 1e20, 1e29, 1e34])
+def test_eight_bit_values_are_the_nearest_to_the_quotient(group, size):
+    """out = e4m3(y / scale) with the quotient rounded to nearest, for scales of any size."""
+    rows, D = 40, 4096
+    x, w = randn((rows, D), F32, 360).to(DEV), (randn((D,), F32, 361, 0.1, 1.0) * size).to(DEV)
+    y = gdn.gdn_rmsnorm_fwd(x, w)["out"].cpu()
+    got = gdn.gdn_rmsnorm_fwd(x, w, out_dtype=torch.float8_e4m3fn, group=group)
+    g = group or D
+    scale = got["scale"].cpu()
+    assert torch.equal(scale, y.view(rows, -1, g).abs().amax(-1) / 448)
+    want = (y.view(rows, -1, g) / scale[..., None]).view(rows, D).to(torch.float8_e4m3fn)
+    assert torch.equal(got["out"].cpu().float(), want.float())
