@@ -220,3 +220,29 @@ def test_eight_bit_values_are_the_nearest_to_the_quotient(group, size):
     assert torch.equal(scale, y.view(rows, -1, g).abs().amax(-1) / 448)
     want = (y.view(rows, -1, g) / scale[..., None]).view(rows, D).to(torch.float8_e4m3fn)
     assert torch.equal(got["out"].cpu().float(), want.float())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("low", ["lowest", "-inf"])
+@pytest.mark.parametrize("C", [64, 37])
+def test_steps_masked_by_the_lowest_dt_leave_the_state(dtype, low, C):
+    """softplus(dt) = 0 there: the state passes, the token's x and B have no part, and no gradient is lost."""
+    T, N = 300, 16
+    v, do = scan_case(1, T, C, N, None, dtype, True, 370), randn((1, T, C), dtype, 380)
+    masked = torch.zeros(T, dtype=torch.bool)
+    masked[20:60] = masked[128:200] = masked[299] = True
+    v["dt"][0, masked] = torch.finfo(dtype).min if low == "lowest" else float("-inf")
+    a = {k: dev(t) for k, t in v.items()}
+    final = torch.empty(1, C, N, device=DEV)
+    got = gdn.gdn_ssm_fwd(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], D=a["D"], z=a["z"], dt_bias=a["dt_bias"], h0=a["h0"],
+                          h_final=final)
+    v["dt"][0, masked] = -1e30  # (the reference's softplus of -inf has no gradient of its own)
+    ref, fin = ref_scan({k: f64(t) for k, t in v.items()}, None, True)
+    assert rel(got, ref) <= (TOL_BF if dtype == BF else TOL_SCAN) and rel(final, fin) <= TOL_SCAN
+    ref = ref_gradients(v, do)
+    v["dt"][0, masked] = torch.finfo(dtype).min if low == "lowest" else float("-inf")
+    got = scan_gradients(v, do)
+    for k, r in ref.items():
+        act = k in ("dx", "ddt", "dBm", "dCm", "dz")
+        assert rel(got[k], r) <= (TOL_BF if dtype == BF and act else TOL_SCAN), k
+    assert (got["ddt"][0, dev(masked)] == 0).all() and (got["dBm"][0, dev(masked)] == 0).all()
