@@ -9,14 +9,16 @@
 // fp32 operations a clock and SM, measured), so 16 states of a token and
 // channel cost 64 cycles a warp, more than the 8 bytes it moves.
 // The main loop is written in packed pairs to leave issue slots for the rest.
+// What is left idle is latency: with 10 to 11 warps a SM (164 registers) the
+// issue slots are 56 to 61 % used, the exponential unit 42 to 51 %, DRAM 14 to 19.
 //
 // A line of tokens is one CTA's from end to end while channels alone fill the
 // GPU. Where they do not, the line is cut into chunks: a first pass scans the
 // first chunk and forms the others' states from zero and sums of delta (the
 // decay of a chunk is exp(A sum delta), so it needs no product of its own), a
 // short pass chains them, and a second scan runs the chunks from their
-// entering states. 4 x 4096 tokens of 4096 channels, 16 states, bf16: 205, 10
-// and 268 us (8.6 and 11.1 cycles a warp for 32 (token, channel, state); the
+// entering states. 4 x 4096 tokens of 4096 channels, 16 states, bf16: 206, 10
+// and 270 us (8.6 and 11.2 cycles a warp for 32 (token, channel, state); the
 // bare loops take 5.0 and 6.2, the rest is what a token and channel needs
 // once: softplus, gate and the conversions). Whole lines: 1018 us (128 CTAs).
 #include "gdn_ssm.cuh"
@@ -420,7 +422,8 @@ void ssm_split(int lines, int T, int D, int N, int *nchunk, int *clen0, int *cle
     const int ch = 2 * kThreads / ssm_lanes(N);
     const int64_t ctas = (int64_t)lines * ((D + ch - 1) / ch);
     // Each launch takes n chunks of a line, with six CTAs a SM (three warps a
-    // scheduler), chunks of at least 64 tokens; whole lines where n would be
+    // scheduler), one chunk more than n of at least 64 tokens to a line (so 48
+    // and 40 for the shortest cut line, 129 tokens); whole lines where n would be
     // one. 4096 channels: 10 x 3000 tokens (320 CTAs) 1067 us whole, 969 cut;
     // 16 x 2048 (512 CTAs) 736 whole.
     int64_t n = 912 / ctas;

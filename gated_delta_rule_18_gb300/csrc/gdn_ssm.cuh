@@ -69,7 +69,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|) <= 1, by
 //   log1p(e) = 2 artanh(s), s = e / (2 + e) <= 1/3, artanh(s) = s P(s^2).
 // P interpolates artanh(sqrt t) / sqrt t on [0, 1/9] at five Chebyshev points
-// (relative error 4e-9); no cancellation for small e, as log(1 + e) has.
+// (relative error of log1p 8e-9); no cancellation for small e, as log(1 + e) has.
 constexpr float SP1 = 0.333331608f, SP2 = 0.200122976f, SP3 = 0.139825789f, SP4 = 0.140788892f;
 __device__ __forceinline__ float log1p_of(float e, float r) {  // r = 1 / (2 + e)
     const float s = e * r, t = s * s;

@@ -528,8 +528,7 @@ gdn_status gdn_frame_fwd(const void *q, const void *k, gdn_tensor_desc qkd,
  *   NULL; or GDN_E4M3 with scale (R, ceil(D / group)) fp32, contiguous:
  *     scale = max|y| / 448 over the group's channels, out = e4m3(y / scale),
  *     and 0 where scale is 0. group: 32, 64, 128, 256, or 0 for the row.
- *   D <= 16384. (The survey's RMSNorm rows: SANA `fused_gdn.py` page,
- *   `_precompute_inv_rms`; the mamba-rs page's `rmsnorm_bwd`.)
+ *   D <= 16384.
  */
 gdn_status gdn_rmsnorm_fwd(const void *x, int64_t x_st, int x_dtype,
                            const void *residual, int64_t res_st, int res_dtype,
@@ -557,8 +556,7 @@ gdn_status gdn_rmsnorm_bwd(const void *s, int64_t s_st, int s_dtype,
 
 /*
  * gdn_conv_fwd -- causal depthwise convolution of W taps (the short
- * convolution before the scan: hyper-parallel coverage_diff page,
- * `causal_conv1d`, and its packed-sequence halo):
+ * convolution before the scan):
  *   p_t = bias + sum_j weight[:, j] x_{t - W + 1 + j}, out = silu(p) or p.
  *   weight (D, W), bias (D) or NULL; W from 2 to 8.
  *   initial_state, final_state: (n_seq, W - 1, D) of `dtype`, contiguous, or
@@ -603,9 +601,8 @@ gdn_status gdn_conv_step(const void *x, int64_t x_st, const float *weight,
                          cudaStream_t stream);
 
 /*
- * gdn_ssm_fwd -- the selective state-space scan (the mamba-rs page's layer,
- * whose backward calls `ssm_backward_local` / `ssm_parallel_bwd`), per
- * channel d and state n, per sequence:
+ * gdn_ssm_fwd -- the selective state-space scan, per channel d and state n,
+ * per sequence:
  *   delta = softplus(dt + dt_bias) (GDN_SOFTPLUS; else dt + dt_bias)
  *   h_t = exp(delta A) h_{t-1} + delta x B_n          (fp32)
  *   out = (sum_n C_n h_t + D x) silu(z)

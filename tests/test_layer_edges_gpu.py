@@ -32,7 +32,7 @@ def test_channel_sums_of_the_scan_gradient_are_rounded_once(N):
     All terms are positive here, so a sum's relative error is at most that of
     fp32 sums (2e-5), and the chance that it takes a value to the other side
     of a rounding boundary 2 * 2e-5 / 2^-8 = 1 %. Products cut to ten bits
-    would shrink every sum by some 3.4e-4 and move nine in a hundred."""
+    shrink every sum by some 3.4e-4 and move four to nine in a hundred."""
     v = {k: t if k == "A" else t.abs() for k, t in scan_case(1, 64, 512, N, None, BF, True, 200).items()}
     v["dt_bias"] = -v["dt_bias"] - 4
     do = randn((1, 64, 512), BF, 210).abs()
