@@ -244,3 +244,14 @@ def test_tensors_of_too_few_dimensions_raise_value_errors(L):
         with pytest.raises(ValueError):
             f()
     assert L.launched == []
+
+
+@pytest.mark.parametrize("outside", [False, True])
+def test_calls_run_in_inference_mode(L, outside):
+    """Inference tensors have no version to count; others written there count theirs."""
+    h, x, bc, out = (on(0, *s) for s in ((4, 16, 8), (4, 16), (4, 8), (4, 16)))
+    with torch.inference_mode():
+        if not outside:
+            h, x, bc, out = (on(0, *s) for s in ((4, 16, 8), (4, 16), (4, 8), (4, 16)))
+        assert gdn.gdn_ssm_step(x, x, on(0, 16, 8), bc, bc, h, out=out) is out
+    assert len(L.launched) == 1 and (not outside or h._version == 1)
