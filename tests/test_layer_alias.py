@@ -78,3 +78,24 @@ def test_outputs_whose_rows_overlap_are_refused(L, fn, spec, kw):
 ])
 def test_outputs_apart_from_inputs_pass(L, fn, spec, kw):
     assert call(getattr(L, fn), spec, ws=0, **kw) == WS
+
+
+def test_overlap_agrees_with_the_bytes(L):
+    """Random small layouts of x and out against the sets of their elements."""
+    import random
+    rng, seen = random.Random(0), set()
+    for _ in range(6000):
+        B, T, D = rng.randint(1, 3), rng.randint(1, 5), rng.randint(1, 4)
+        x_sb, x_st, o_sb, o_st = (rng.randint(0, 24) for _ in range(4))
+        if rng.random() < 0.5:
+            o_sb, o_st = x_sb, x_st
+        shift = rng.randint(-40, 40)
+        at = lambda base, sb, st: [base + b * sb + t * st + d for b in range(B) for t in range(T) for d in range(D)]  # noqa: E731
+        x, out = at(0, x_sb, x_st), at(shift, o_sb, o_st)
+        same = shift == 0 and (B == 1 or x_sb == o_sb) and (T == 1 or x_st == o_st)
+        want = LAYOUT if len(set(out)) < len(out) else UNSUP if set(x) & set(out) and not same else WS
+        got = call(L.gdn_ssm_fwd, SSM, B=B, T=T, D=D, n_seq=B, x_sb=x_sb, x_st=x_st, out=p(0) + 2 * shift, out_sb=o_sb,
+                   out_st=o_st, ws=0)
+        assert got == want, (B, T, D, x_sb, x_st, o_sb, o_st, shift)
+        seen.add(got)
+    assert seen == {LAYOUT, UNSUP, WS}
