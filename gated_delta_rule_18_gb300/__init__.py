@@ -9,7 +9,8 @@ Entry points mirror the C ABI:
   gdn_prep, gdn_chunk_fwd, gdn_merge, gdn_workspace_size, gdn_status_string,
   gdn_last_device_error, and gdn_forward (prep + one or both scan directions,
   optionally merged). The state-space layer's operators (residual norm, short
-  convolution, selective scan) are in .layer and re-exported here.
+  convolution, selective scan) are in .layer, those around a mixer and the gated
+  recurrence (rotary positions, block norm) in .block; both re-exported here.
 """
 from __future__ import annotations
 
@@ -24,18 +25,26 @@ __all__ = ["GDNError", "gdn_prep", "gdn_chunk_fwd", "gdn_chunk_fwd_noalloc",
            "gdn_set_stall_test", "gdn_set_fused", "gdn_forward", "lib",
            "PREP_L2", "PREP_RMS", "PREP_RELU", "gdn_prep_bwd", "gdn_frame_bwd", "gdn_merge_bwd", "profile_enable", "profile_collect", "gdn_set_state_tile",
            "launch_count", "kernel_names", "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd", "gdn_conv_fwd", "gdn_conv_bwd",
-           "gdn_conv_step", "gdn_ssm_fwd", "gdn_ssm_bwd", "gdn_ssm_step"]
+           "gdn_conv_step", "gdn_ssm_fwd", "gdn_ssm_bwd", "gdn_ssm_step", "gdn_rotary", "rotary_frequencies",
+           "gdn_block_norm_fwd", "gdn_block_norm_bwd", "gdn_lru_fwd", "gdn_lru_bwd", "gdn_lru_step", "LRU_TILE"]
 
 # the state-space layer's operators (.layer imports torch, which the package
 # otherwise leaves to the first call)
 _LAYER = ("gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd", "gdn_conv_fwd", "gdn_conv_bwd", "gdn_conv_step", "gdn_ssm_fwd",
           "gdn_ssm_bwd", "gdn_ssm_step")
+# and those around a mixer (.block)
+_BLOCK = ("gdn_rotary", "rotary_frequencies", "gdn_block_norm_fwd", "gdn_block_norm_bwd", "gdn_lru_fwd", "gdn_lru_bwd",
+          "gdn_lru_step", "LRU_TILE")
 
 
 def __getattr__(name):
     if name in _LAYER:
         from . import layer
         globals().update({k: getattr(layer, k) for k in _LAYER})
+        return globals()[name]
+    if name in _BLOCK:
+        from . import block
+        globals().update({k: getattr(block, k) for k in _BLOCK})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
@@ -146,8 +155,9 @@ def lib():
     L.gdn_profile_collect.argtypes = [ctypes.POINTER(F), ctypes.POINTER(I), I]
     L.gdn_launch_count.restype = ctypes.c_longlong
     L.gdn_launch_count.argtypes = []
-    from .layer import bind
-    bind(L)
+    from . import block, layer
+    layer.bind(L)
+    block.bind(L)
     _lib = L
     return L
 

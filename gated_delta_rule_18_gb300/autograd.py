@@ -3,7 +3,8 @@
 Each function's forward runs the CUDA forward through the C ABI; its
 backward runs the matching gradient kernels (gdn_chunk_bwd, gdn_frame_bwd,
 gdn_merge_bwd, gdn_prep_bwd; of the state-space layer gdn_rmsnorm_bwd,
-gdn_conv_bwd, gdn_ssm_bwd).
+gdn_conv_bwd, gdn_ssm_bwd; around a mixer gdn_rotary, gdn_block_norm_bwd,
+gdn_lru_bwd).
 Nothing here computes on its own: the wrappers marshal tensors and sum the
 two directions' gradients.
 
@@ -19,6 +20,7 @@ import torch
 
 from . import (PREP_RELU, PREP_RMS, gdn_chunk_bwd, gdn_chunk_fwd, gdn_chunk_fwd_bidir, gdn_frame_bwd,
                gdn_frame_fwd, gdn_merge, gdn_merge_bwd, gdn_prep, gdn_prep_bwd)
+from .block import (LRU_TILE, gdn_block_norm_bwd, gdn_block_norm_fwd, gdn_lru_bwd, gdn_lru_fwd, gdn_rotary)
 from .layer import (gdn_conv_bwd, gdn_conv_fwd, gdn_rmsnorm_bwd, gdn_rmsnorm_fwd, gdn_ssm_bwd, gdn_ssm_fwd)
 
 
@@ -261,3 +263,86 @@ def selective_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, initial_state
     tensor but cu_seqlens. Returns (y, final_state or None)."""
     return _SelectiveScan.apply(x, dt, A, Bm, Cm, D, z, dt_bias, initial_state, cu_seqlens, bool(dt_softplus),
                                 bool(output_final_state))
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, inv_freq, positions, offset, interleaved, scale):
+        ctx.save_for_backward(inv_freq, positions)
+        ctx.how = offset, interleaved, scale
+        r = gdn_rotary(q, inv_freq, k=k, positions=positions, offset=offset, interleaved=interleaved, scale=scale)
+        return (r, None) if k is None else r
+
+    @staticmethod
+    @_once
+    def backward(ctx, dq, dk):
+        inv_freq, positions = ctx.saved_tensors
+        offset, interleaved, scale = ctx.how
+        r = gdn_rotary(dq.contiguous(), inv_freq, k=None if dk is None else dk.contiguous(), positions=positions,
+                       offset=offset, interleaved=interleaved, scale=scale, inverse=True)
+        dq, dk = (r, None) if dk is None else r
+        return dq, dk, None, None, None, None, None
+
+
+def rotary(q, inv_freq, k=None, positions=None, offset=0, interleaved=False, scale=1.0):
+    """Rotary positions (gdn_rotary), differentiable in q and k. Returns the
+    turned q, or (q, k)."""
+    q, k = _Rotary.apply(q, k, inv_freq, positions, int(offset), bool(interleaved), float(scale))
+    return q if k is None else (q, k)
+
+
+class _BlockNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, residual, post, pre, gate, scale, gate_act, alpha, eps):
+        r = gdn_block_norm_fwd(y, residual, post_weight=post, pre_weight=pre, gate=gate, gate_act=gate_act, scale=scale,
+                               alpha=alpha, eps=eps)
+        ctx.save_for_backward(y, r["residual"], post, pre, gate, scale)
+        ctx.how = gate_act, alpha, eps
+        return r.get("out"), r["residual"]
+
+    @staticmethod
+    @_once
+    def backward(ctx, dout, dres):
+        y, s, post, pre, gate, scale = ctx.saved_tensors
+        gate_act, alpha, eps = ctx.how
+        r = gdn_block_norm_bwd(y, s, dout=None if pre is None else dout.contiguous(), dres=dres.to(s.dtype).contiguous(),
+                               post_weight=post, pre_weight=pre, gate=gate, gate_act=gate_act, scale=scale, alpha=alpha,
+                               eps=eps)
+        return (r["dy"], r["dresidual"], r.get("dpost_weight"), r.get("dpre_weight"), r.get("dgate"), r.get("dscale"), None,
+                None, None)
+
+
+def block_norm(y, residual, post_weight=None, pre_weight=None, gate=None, gate_act=None, scale=None, alpha=1.0, eps=1e-6):
+    """What stands between two blocks (gdn_block_norm_fwd), differentiable in
+    every tensor: (out, s), the normed input of the next block (None without
+    pre_weight) and the residual stream that goes on. The gradient takes s as
+    stored."""
+    return _BlockNorm.apply(y, residual, post_weight, pre_weight, gate, scale, gate_act, float(alpha), float(eps))
+
+
+class _GatedRecurrence(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, r, i, lam, z, h0, cu_seqlens, c, output_final_state):
+        B, T, C = x.shape
+        f32 = dict(dtype=torch.float32, device=x.device)
+        n_seq = B if cu_seqlens is None else cu_seqlens.numel() - 1
+        final = torch.empty((n_seq, C), **f32) if output_final_state else None
+        saved = torch.empty((B, (T + LRU_TILE - 1) // LRU_TILE, C), **f32)
+        y = gdn_lru_fwd(x, r, i, lam, z=z, c=c, h0=h0, cu_seqlens=cu_seqlens, h_final=final, checkpoints=saved)
+        ctx.save_for_backward(x, r, i, lam, z, h0, cu_seqlens, saved)
+        ctx.c = c
+        return y, final
+
+    @staticmethod
+    @_once
+    def backward(ctx, dy, dfinal):
+        x, r, i, lam, z, h0, cu_seqlens, saved = ctx.saved_tensors
+        g = gdn_lru_bwd(x, r, i, lam, dy.contiguous(), z=z, c=ctx.c, h0=h0, cu_seqlens=cu_seqlens,
+                        dh_final=None if dfinal is None else dfinal.contiguous(), checkpoints=saved)
+        return g["dx"], g["dr"], g["di"], g["dlam"], g.get("dz"), g.get("dh0"), None, None, None
+
+
+def gated_recurrence(x, r, i, lam, z=None, initial_state=None, cu_seqlens=None, c=8.0, output_final_state=False):
+    """The gated linear recurrence (gdn_lru_fwd), differentiable in every tensor
+    but cu_seqlens. Returns (y, final_state or None)."""
+    return _GatedRecurrence.apply(x, r, i, lam, z, initial_state, cu_seqlens, float(c), bool(output_final_state))

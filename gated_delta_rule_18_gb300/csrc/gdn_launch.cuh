@@ -16,7 +16,8 @@ enum Kind {
     KFrameOut, KSegSummary, KSegCombine, KBwdDh, KBwdDq, KBwdDk, KSum, KF32Prep, KF32Serial, KFused,
     KFrameXt, KFrameLam, KFrameTok, KPrepBwd, KMergeBwd, KBwdF32Scan, KBwdF32Reduce, KNorm, KNormBwd,
     KColSum, KConv, KConvBwd, KConvStep, KSsmSum, KSsmChain, KSsmScan, KSsmBwdSum, KSsmBwdChain,
-    KSsmBwd, KSsmBwdReduce, KSsmStep, KNumKinds
+    KSsmBwd, KSsmBwdReduce, KSsmStep, KRotary, KBlockNorm, KBlockNormBwd, KBlockNormSeq, KBlockNormReduce,
+    KLru, KLruBwd, KLruStep, KNumKinds
 };
 inline const char *kind_name(int kind) {
     static const char *const names[KNumKinds] = {
@@ -25,7 +26,8 @@ inline const char *kind_name(int kind) {
         "f32_prep", "f32_serial", "fused_tc", "frame_xt", "frame_lam", "frame_tokgrad", "prep_bwd",
         "merge_bwd", "bwd_f32_scan", "bwd_f32_reduce", "rmsnorm", "rmsnorm_bwd", "col_sum", "conv",
         "conv_bwd", "conv_step", "ssm_sum", "ssm_chain", "ssm_scan", "ssm_bwd_sum", "ssm_bwd_chain",
-        "ssm_bwd", "ssm_bwd_reduce", "ssm_step"};
+        "ssm_bwd", "ssm_bwd_reduce", "ssm_step", "rotary", "block_norm", "block_norm_bwd", "block_norm_sequences",
+        "block_norm_reduce", "lru", "lru_bwd", "lru_step"};
     return names[kind];
 }
 

@@ -662,6 +662,146 @@ gdn_status gdn_ssm_step(const void *x, int64_t x_st, const void *dt,
                         int64_t out_st, int n, int D, int N, int dtype,
                         int flags, cudaStream_t stream);
 
+/*
+ * The operators around a mixer, and the gated linear recurrence that can stand
+ * in its place, each for prompts, single tokens and training. Conventions are
+ * those of the state-space layer's operators above. Activations may lie at
+ * any multiple of the element size; the gradients' outputs overlap no input.
+ */
+
+/* flags of gdn_rotary */
+#define GDN_INTERLEAVED 0x1 /* pairs (2 j, 2 j + 1) instead of (j, j + rot / 2) */
+#define GDN_INVERSE 0x2     /* the opposite angle: the gradient */
+
+/*
+ * gdn_rotary -- rotary positions of q and k. The first rot channels of each
+ * head turn in pairs, pair j of a token at position p by p inv_freq[j]:
+ *   (a, b) -> scale (a cos - b sin, b cos + a sin);
+ * the other channels pass unscaled.
+ *   q, q_out: (B, T, Hq, D), k, k_out: (B, T, Hk, D) of `dtype`, D contiguous,
+ *   strides over B, T and H in elements; k and k_out both NULL with Hk == 0
+ *   for q alone. An output may be its own input (same strides); else outputs
+ *   overlap neither inputs nor one another (layouts of three separate strides
+ *   are told apart by the range of their bytes; an output's have to nest). inv_freq: rot / 2 doubles,
+ *   radians a position. positions: int32 or int64 (pos_bits), strides pos_sb
+ *   over B and pos_st over T (0 shares), or NULL: offset + t.
+ *   rot even, 2 <= rot <= D <= 512; B T <= 2^31 - 65536.
+ *   The angle is kept to 2^-64 of a turn a position: positions up to 2^31 are
+ *   as good as small ones, and so are negative ones.
+ */
+gdn_status gdn_rotary(const void *q, int64_t q_sb, int64_t q_st, int64_t q_sh,
+                      int Hq, void *q_out, int64_t qo_sb, int64_t qo_st,
+                      int64_t qo_sh, const void *k, int64_t k_sb, int64_t k_st,
+                      int64_t k_sh, int Hk, void *k_out, int64_t ko_sb,
+                      int64_t ko_st, int64_t ko_sh, const double *inv_freq,
+                      const void *positions, int pos_bits, int64_t pos_sb,
+                      int64_t pos_st, int64_t offset, int B, int T, int D,
+                      int rot, float scale, int dtype, int flags,
+                      cudaStream_t stream);
+
+/* act of gdn_block_norm_*: the factor a gate value g stands for */
+#define GDN_GATE_NONE 0    /* no gate */
+#define GDN_GATE_LINEAR 1  /* g */
+#define GDN_GATE_SIGMOID 2 /* 1 / (1 + exp(-g)) */
+#define GDN_GATE_SILU 3    /* g / (1 + exp(-g)) */
+
+/*
+ * gdn_block_norm_fwd -- the norm behind a block, its gate and residual scale,
+ * the residual's addition and the norm in front of the next block:
+ *   u = y post_weight / sqrt(mean(y^2) + eps)   (y, with post_weight NULL)
+ *   s = residual + alpha scale act(gate) u      (fp32; scale NULL: 1)
+ *   res_out = s in the residual's type, out = s pre_weight / sqrt(mean(s^2) + eps)
+ *   y, gate, out: y_dtype; residual, res_out: res_dtype. Rows (R, D); row r
+ *   takes row r / gate_rows of the gate (gate_rows divides R: tokens of a
+ *   sequence that share one; at most 65535 rows of a shared gate; 1 without). out and
+ *   pre_weight both or neither NULL; not both norms NULL. res_out may lie on
+ *   residual, out on y, and both on inputs of their type and strides.
+ *   D <= 16384.
+ */
+gdn_status gdn_block_norm_fwd(const void *y, int64_t y_st, int y_dtype,
+                              const void *residual, int64_t res_st,
+                              int res_dtype, const void *gate, int64_t gate_st,
+                              int gate_rows, int act, const float *post_weight,
+                              const float *pre_weight, const float *scale,
+                              float alpha, void *res_out, int64_t res_out_st,
+                              void *out, int64_t out_st, int R, int D,
+                              float eps, cudaStream_t stream);
+
+/*
+ * gdn_block_norm_bwd -- its gradients at s = res_out as stored, for dout and
+ * the stream's own gradient dres (or NULL; s_dtype as s). dy, dgate: y_dtype
+ * (dgate (R / gate_rows, D), summed in fp32); dresidual: s_dtype; dpost_weight,
+ * dpre_weight, dscale: (D) fp32, or NULL. s and dout are not read without
+ * pre_weight. Every sum has a fixed order.
+ *   workspace: gdn_block_norm_bwd_workspace_size(R, D, gate_rows) bytes.
+ */
+size_t gdn_block_norm_bwd_workspace_size(int R, int D, int gate_rows);
+gdn_status gdn_block_norm_bwd(const void *y, int64_t y_st, int y_dtype,
+                              const void *s, int64_t s_st, int s_dtype,
+                              const void *gate, int64_t gate_st, int gate_rows,
+                              int act, const void *dout, int64_t dout_st,
+                              const void *dres, int64_t dres_st,
+                              const float *post_weight, const float *pre_weight,
+                              const float *scale, float alpha, void *dy,
+                              int64_t dy_st, void *dresidual,
+                              int64_t dresidual_st, void *dgate,
+                              int64_t dgate_st, float *dpost_weight,
+                              float *dpre_weight, float *dscale, int R, int D,
+                              float eps, void *workspace, size_t ws_bytes,
+                              cudaStream_t stream);
+
+/*
+ * gdn_lru_fwd -- the gated linear recurrence, per channel and sequence:
+ *   u_t = c softplus(lam) sigmoid(r_t),  a_t = exp(-u_t)
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t      (fp32)
+ *   out = h_t silu(z_t)  (h_t with z NULL)
+ *   x, r, i, z, out: (B, T, C) of `dtype`; lam (C) fp32; c >= 0.
+ *   h0, h_final: (n_seq, C) fp32 or NULL. checkpoints: (B, ceil(T / 64), C)
+ *   fp32 or NULL: the state before every 64th token, for the gradient.
+ *   out may lie on x, r, i or z. workspace: 256 bytes, needed with cu_seqlens
+ *   only.
+ */
+#define GDN_LRU_TILE 64 /* tokens a checkpoint stands for */
+gdn_status gdn_lru_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
+                       int64_t r_sb, int64_t r_st, const void *i, int64_t i_sb,
+                       int64_t i_st, const float *lam, const void *z,
+                       int64_t z_sb, int64_t z_st, float c, const float *h0,
+                       const int32_t *cu_seqlens, int n_seq, void *out,
+                       int64_t out_sb, int64_t out_st, float *h_final,
+                       float *checkpoints, int B, int T, int C, int dtype,
+                       void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * gdn_lru_bwd -- its gradients for L = sum(dout . out) + sum(dh_final .
+ * h_final). dx, dr, di, dz (B, T, C) in `dtype`, contiguous; dlam (C), dh0
+ * (n_seq, C) fp32. dz goes with z; dh0 may be NULL. checkpoints: the
+ * forward's for the same inputs, or NULL: they are formed again. Every sum
+ * has a fixed order: results repeat bit for bit.
+ *   workspace: gdn_lru_bwd_workspace_size(B, T, C, with_checkpoints) bytes.
+ */
+size_t gdn_lru_bwd_workspace_size(int B, int T, int C, int with_checkpoints);
+gdn_status gdn_lru_bwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
+                       int64_t r_sb, int64_t r_st, const void *i, int64_t i_sb,
+                       int64_t i_st, const float *lam, const void *z,
+                       int64_t z_sb, int64_t z_st, float c, const float *h0,
+                       const int32_t *cu_seqlens, int n_seq, const void *dout,
+                       int64_t dout_sb, int64_t dout_st, const float *dh_final,
+                       const float *checkpoints, void *dx, void *dr, void *di,
+                       float *dlam, void *dz, float *dh0, int B, int T, int C,
+                       int dtype, void *workspace, size_t ws_bytes,
+                       cudaStream_t stream);
+
+/*
+ * gdn_lru_step -- one token of n requests of the recurrence; state (n_slots,
+ * C) fp32, updated in place. x, r, i, z, out (n, C).
+ */
+gdn_status gdn_lru_step(const void *x, int64_t x_st, const void *r, int64_t r_st,
+                        const void *i, int64_t i_st, const float *lam,
+                        const void *z, int64_t z_st, float c, float *state,
+                        const int32_t *slots, int n_slots, void *out,
+                        int64_t out_st, int n, int C, int dtype,
+                        cudaStream_t stream);
+
 const char *gdn_status_string(gdn_status s);
 
 /*
