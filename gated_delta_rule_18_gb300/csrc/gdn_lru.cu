@@ -18,151 +18,156 @@
 namespace gdn {
 namespace {
 
-constexpr int kRanks = 8;  // most CTAs of a cluster
-
-struct Exchange {
-    LruRun warps[2][kLruWarps][32];
-    LruRun ranks[2][kRanks][32];
-};
-
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(32 * kLruWarps, 2) lru_kernel(const LruParams p) {
+template <typename T, bool VEC, bool PACKED, bool Z>
+__global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ Exchange ex;
-    constexpr int KW = RowVec<T, 2>::kWords, kRow = kLruCh;
+    __shared__ LruRun runs[2][kLruWarps][32];
+    __shared__ LruRanks ranks;
+    constexpr int kRow = kLruCh, kTensor = kLruLen * kRow;  // elements of a warp's rows of one tensor
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int K = p.ranks, rank = K > 1 ? blockIdx.x % K : 0, line = blockIdx.y;
+    const int K = p.ranks, rank = blockIdx.x % K, line = blockIdx.y;
     const int c0 = (blockIdx.x / K) * kLruCh, c = c0 + 2 * lane, nc = p.C - c;  // nc: channels of the pair that exist
-    if (p.err && blockIdx.x == 0 && blockIdx.y == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
-    auto ld_state = [&](const float *s, int64_t row) {
-        float2 f = make_float2(0.f, 0.f);
-        if (s && nc > 0) f.x = s[row * p.C + c];
-        if (s && nc > 1) f.y = s[row * p.C + c + 1];
-        return pack2(f.x, f.y);
-    };
-    auto st_state = [&](float *s, int64_t row, f32x2 v) {
-        const float2 f = unpack2(v);
-        if (nc > 0) s[row * p.C + c] = f.x;
-        if (nc > 1) s[row * p.C + c + 1] = f.y;
-    };
-    // sequences without tokens keep their states
-    if (p.h_final && rank == 0) {
-        if (!p.cu) {
-            if (p.T == 0 && warp == 0) st_state(p.h_final, line, ld_state(p.h0, line));
-        } else {
+    const f32x2 one = pack2(1.f, 1.f), zero = pack2(0.f, 0.f);
+    if (PACKED) {
+        if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
+        if (p.h_final && rank == 0) {  // sequences without tokens keep their states
             for (int s = warp; s < p.n_seq; s += kLruWarps)
-                if (p.cu[s + 1] <= p.cu[s]) st_state(p.h_final, s, ld_state(p.h0, s));
+                if (p.cu[s + 1] <= p.cu[s]) lru_st_state(p.h_final, s, p.C, c, nc, lru_ld_state(p.h0, s, p.C, c, nc));
         }
     }
     const int steps = (p.T + K * kLruTile - 1) / (K * kLruTile);
-    const T *x = (const T *)p.x + line * p.x_sb, *r = (const T *)p.r + line * p.r_sb, *in = (const T *)p.i + line * p.i_sb;
-    const T *z = p.z ? (const T *)p.z + line * p.z_sb : nullptr;
-    T *out = p.out ? (T *)p.out + line * p.o_sb : nullptr;
-    constexpr int kTensor = kLruLen * kRow;  // elements of a warp's rows of one tensor
-    T *stage = (T *)smem + warp * 4 * kTensor;
+    const T *x = (const T *)p.x + line * p.x_sb + c0, *r = (const T *)p.r + line * p.r_sb + c0;
+    const T *in = (const T *)p.i + line * p.i_sb + c0, *z = Z ? (const T *)p.z + line * p.z_sb + c0 : nullptr;
+    T *out = p.out ? (T *)p.out + line * p.o_sb + c : nullptr;
+    T *stage = (T *)smem + warp * (Z ? 4 : 3) * kTensor;
     auto first = [&](int n) { return (n * K + rank) * kLruTile + warp * kLruLen; };  // token of step n
-    auto fetch = [&](int n) {
-        if constexpr (VEC) {
-            const int t = first(n), rows = n < steps ? min(max(p.T - t, 0), kLruLen) : 0;
-            if (rows > 0) {
-                lru_copy(stage, x + t * p.x_st, p.x_st, rows, c0, p.C);
-                lru_copy(stage + kTensor, r + t * p.r_st, p.r_st, rows, c0, p.C);
-                lru_copy(stage + 2 * kTensor, in + t * p.i_st, p.i_st, rows, c0, p.C);
-                if (z) lru_copy(stage + 3 * kTensor, z + t * p.z_st, p.z_st, rows, c0, p.C);
-            }
-            cp_async_commit();
-        }
+    auto copy = [&](int n, int k, const T *src, int64_t st) {
+        const int t = first(n), rows = n < steps ? min(p.T - t, kLruLen) : 0;
+        if (rows > 0) lru_copy(stage + k * kTensor, src + t * st, st, rows, p.C - c0);
     };
-    fetch(0);
+    // two groups of copies a step: x, r and i are free for the next step's once
+    // a and b are formed, z once the outputs are
+    auto fetch = [&](int n) {
+        if (VEC) copy(n, 0, x, p.x_st), copy(n, 1, r, p.r_st), copy(n, 2, in, p.i_st), cp_async_commit();
+    };
+    auto fetch_z = [&](int n) {
+        if (VEC && Z) copy(n, 3, z, p.z_st), cp_async_commit();
+    };
+    // a pair of x, r, i or z at token j of the warp
+    auto get = [&](int k, const T *src, int64_t st, int t0, int j) -> f32x2 {
+        if (VEC) return lru_pair(stage + k * kTensor + j * kRow + 2 * lane);
+        float f[2] = {0.f, 0.f};
+        if (nc > 0) ld_row_f<T, 2, false>(f, src + (int64_t)(t0 + j) * st + 2 * lane, nc);
+        return pack2(f[0], f[1]);
+    };
+    fetch(0), fetch_z(0);
     float cl[2] = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < 2; ++k)
         if (k < nc) cl[k] = lru_decay(p.lam[c + k], p.c);
     const f32x2 cl2 = pack2(cl[0], cl[1]);
-    f32x2 carry = pack2(0.f, 0.f);  // the state before the cluster's tiles
-    if (K > 1) cluster_arrive(), cluster_wait();  // every CTA's shared memory is there
+    f32x2 carry = PACKED ? zero : lru_ld_state(p.h0, line, p.C, c, nc);  // the state before the cluster's tiles
+    bool lost = false;
+    if (K > 1) {
+        if (threadIdx.x == 0) ranks.init();
+        cluster_sync();
+    }
     for (int n = 0; n < steps; ++n) {
         const int t0 = first(n), len = min(max(p.T - t0, 0), kLruLen), flip = n & 1;
-        const LruMarks m = lru_marks(p.cu, p.n_seq, p.T, t0);
-        if constexpr (VEC) {
-            cp_async_wait<0>();
+        LruMarks m{0u, 0u};
+        if (PACKED) m = lru_marks(p.cu, p.n_seq, p.T, t0);
+        if (VEC) {
+            cp_async_wait<Z ? 1 : 0>();
             __syncwarp();
         }
         f32x2 a[kLruLen], b[kLruLen];
-        uint32_t zw[kLruLen][KW];
-        LruRun run{pack2(1.f, 1.f), pack2(0.f, 0.f)};
+        LruRun run{one, zero};
+        auto gates = [&](auto form) {  // whole: eight tokens, none of which begins a sequence
+            constexpr bool whole = decltype(form)::value;
 #pragma unroll
-        for (int j = 0; j < kLruLen; ++j) {
-            uint32_t wx[KW] = {}, wr[KW] = {}, wi[KW] = {};
-#pragma unroll
-            for (int k = 0; k < KW; ++k) zw[j][k] = 0u;
-            a[j] = pack2(1.f, 1.f), b[j] = pack2(0.f, 0.f);
-            if (j >= len) continue;
-            if constexpr (VEC) {
-                const T *s = stage + j * kRow + 2 * lane;
-                ld_words(wx, s), ld_words(wr, s + kTensor), ld_words(wi, s + 2 * kTensor);
-                if (z) ld_words(zw[j], s + 3 * kTensor);
-            } else if (nc > 0) {
-                const int64_t t = t0 + j;
-                ld_row<T, 2, false>(wx, x + t * p.x_st + c, nc), ld_row<T, 2, false>(wr, r + t * p.r_st + c, nc);
-                ld_row<T, 2, false>(wi, in + t * p.i_st + c, nc);
-                if (z) ld_row<T, 2, false>(zw[j], z + t * p.z_st + c, nc);
+            for (int j = 0; j < kLruLen; ++j) {
+                if (!whole && j >= len) {
+                    a[j] = one, b[j] = zero;
+                    continue;
+                }
+                const LruGate g(get(1, r, p.r_st, t0, j), get(2, in, p.i_st, t0, j), cl2);
+                a[j] = g.a, b[j] = mul2(mul2(sqrt_2(g.q), g.gi), get(0, x, p.x_st, t0, j));
+                if (PACKED && !whole && m.cut >> j & 1) {
+                    if (p.h0) b[j] = fma2(g.a, lru_ld_state(p.h0, lru_seq(p.cu, p.n_seq, p.T, t0 + j), p.C, c, nc), b[j]);
+                    run.A = pack2(-0.f, -0.f), run.H = b[j];
+                } else {
+                    run.A = mul2(run.A, a[j]), run.H = fma2(a[j], run.H, b[j]);
+                }
             }
-            const LruGate g(lru_pair<T>(wr), lru_pair<T>(wi), cl2);
-            a[j] = g.a, b[j] = mul2(mul2(g.beta(), g.gi), lru_pair<T>(wx));
-            if (m.cut >> j & 1) {
-                if (p.h0) b[j] = fma2(g.a, ld_state(p.h0, lru_seq(p.cu, p.n_seq, p.T, line, t0 + j)), b[j]);
-                a[j] = pack2(-0.f, -0.f);
-                run.A = a[j], run.H = b[j];
-            } else {
-                run.A = mul2(run.A, a[j]), run.H = fma2(a[j], run.H, b[j]);
-            }
-        }
-        if constexpr (VEC) __syncwarp();
+        };
+        if (len == kLruLen && !m.cut) gates(std::true_type());
+        else gates(std::false_type());
+        if (VEC) __syncwarp();  // every lane has read what the next copies overwrite
         fetch(n + 1);
-        ex.warps[flip][warp][lane] = run;
+        runs[flip][warp][lane] = run;
         __syncthreads();
-        // the CTA's run, and the part of it before this warp
-        LruRun all{pack2(1.f, 1.f), pack2(0.f, 0.f)}, before = all;
-#pragma unroll
-        for (int w = 0; w < kLruWarps; ++w) {
-            const LruRun v = ex.warps[flip][w][lane];
-            if (w == warp) before = all;
-            all.H = lru_apply2(v.A, v.H, all.H), all.A = lru_join(all.A, v.A);
-        }
         f32x2 h = carry;
         if (K > 1) {
-            if (warp < K) st_cluster(&ex.ranks[flip][rank][lane], warp, all);
-            cluster_arrive(), cluster_wait();
-            for (int k = 0; k < K; ++k) {
-                const LruRun v = ex.ranks[flip][k][lane];
-                if (k == rank) h = carry;
-                carry = lru_apply2(v.A, v.H, carry);
-            }
-        } else {
-            carry = lru_apply2(all.A, all.H, carry);
-        }
-        h = lru_apply2(before.A, before.H, h);
-        if (p.ck && warp * kLruLen % kLruTile == 0 && t0 < p.T)
-            st_state(p.ck, (int64_t)line * ((p.T + kLruTile - 1) / kLruTile) + t0 / kLruTile, h);
-        if (!p.out && !m.fin) continue;
+            if (warp == 0) {
+                LruRun all = run;
 #pragma unroll
-        for (int j = 0; j < kLruLen; ++j) {
-            if (j >= len) break;
-            h = m.cut >> j & 1 ? b[j] : fma2(a[j], h, b[j]);
-            if (p.out && nc > 0) {
-                float o[2];
-                float2 f = unpack2(h);
-                if (z) {
-                    const float2 v = unpack2(lru_pair<T>(zw[j])), s = sigmoid2(v);
-                    f.x *= v.x * s.x, f.y *= v.y * s.y;
+                for (int w = 1; w < kLruWarps; ++w) {
+                    const LruRun v = runs[flip][w][lane];
+                    all.H = lru_apply2<PACKED>(v.A, v.H, all.H), all.A = lru_join<PACKED>(all.A, v.A);
                 }
-                o[0] = f.x, o[1] = f.y;
-                st_row_f<T, 2, VEC>(out + (int64_t)(t0 + j) * p.o_st + c, o, nc);
+                ranks.send(n, K, rank, all);
             }
-            if (p.h_final && m.fin >> j & 1) st_state(p.h_final, lru_seq(p.cu, p.n_seq, p.T, line, t0 + j), h);
+            if (!lost) lost = !ranks.wait(n);
+            for (int k = 0; k < K; ++k) {
+                const LruRun v = ranks.runs[flip][k][lane];
+                if (k == rank) h = carry;
+                carry = lru_apply2<PACKED>(v.A, v.H, carry);
+            }
         }
+#pragma unroll
+        for (int w = 0; w < kLruWarps; ++w) {
+            if (K > 1 && w >= warp) break;
+            const LruRun v = runs[flip][w][lane];
+            if (K == 1) {
+                if (w == warp) h = carry;
+                carry = lru_apply2<PACKED>(v.A, v.H, carry);
+            } else {
+                h = lru_apply2<PACKED>(v.A, v.H, h);
+            }
+        }
+        if (lost) h = carry = pack2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
+        if (p.ck && warp == 0 && t0 < p.T)
+            lru_st_state(p.ck, (int64_t)line * ((p.T + kLruTile - 1) / kLruTile) + t0 / kLruTile, p.C, c, nc, h);
+        if (VEC && Z) {
+            cp_async_wait<1>();
+            __syncwarp();
+        }
+        T *o = out + (int64_t)t0 * p.o_st;
+        auto walk = [&](auto form) {
+            constexpr bool whole = decltype(form)::value;
+#pragma unroll
+            for (int j = 0; j < kLruLen; ++j) {
+                if (!whole && j >= len) break;
+                h = PACKED && !whole && m.cut >> j & 1 ? b[j] : fma2(a[j], h, b[j]);
+                f32x2 y = h;
+                if (Z) {
+                    const f32x2 v = get(3, z, p.z_st, t0, j);
+                    y = mul2(h, mul2(v, sigmoid_2(v)));
+                }
+                if (nc > 0) lru_put<T, VEC>(o + j * p.o_st, y, nc);
+                if (PACKED && !whole && p.h_final && m.fin >> j & 1)
+                    lru_st_state(p.h_final, lru_seq(p.cu, p.n_seq, p.T, t0 + j), p.C, c, nc, h);
+            }
+        };
+        if (p.out) {
+            if (len == kLruLen && !(m.cut | m.fin)) walk(std::true_type());
+            else walk(std::false_type());
+        }
+        if (VEC && Z) __syncwarp();
+        fetch_z(n + 1);
     }
+    if (!PACKED && p.h_final && rank == 0 && warp == 0) lru_st_state(p.h_final, line, p.C, c, nc, carry);
+    if (K > 1) cluster_sync();  // no CTA leaves before all have what it sent
 }
 
 // One token of n requests: four channels a thread.
@@ -186,7 +191,7 @@ __global__ void __launch_bounds__(128) lru_step_kernel(const LruStepParams p) {
     for (int k = 0; k < 4; k += 2) {
         const float2 sp = softplus2(make_float2(lam[k], lam[k + 1]));
         const LruGate g(pack2(r[k], r[k + 1]), pack2(i[k], i[k + 1]), pack2(p.c * sp.x, p.c * sp.y));
-        const float2 v = unpack2(fma2(g.a, pack2(h[k], h[k + 1]), mul2(mul2(g.beta(), g.gi), pack2(x[k], x[k + 1]))));
+        const float2 v = unpack2(fma2(g.a, pack2(h[k], h[k + 1]), mul2(mul2(sqrt_2(g.q), g.gi), pack2(x[k], x[k + 1]))));
         h[k] = o[k] = v.x, h[k + 1] = o[k + 1] = v.y;
         if (p.z) {
             const float2 s = sigmoid2(make_float2(z[k], z[k + 1]));
@@ -206,7 +211,7 @@ int lru_ranks(int lines, int T, int C) {
     const int64_t ctas = (int64_t)lines * ((C + kLruCh - 1) / kLruCh);
     const int tiles = (T + kLruTile - 1) / kLruTile;
     int k = 1;
-    while (k < kRanks && k < tiles && ctas * k < 8 * 152) k *= 2;
+    while (k < kLruRanks && k < tiles && ctas * k < 8 * 152) k *= 2;
     return k;
 }
 
@@ -227,11 +232,11 @@ cudaError_t lru_launch(const void *kernel, int lines, int C, int ranks, int smem
 }
 
 cudaError_t launch_lru(const LruParams &p, cudaStream_t st) {
-    using bf = __nv_bfloat16;
-    const void *k = p.bf16 ? (p.vec ? (const void *)lru_kernel<bf, true> : (const void *)lru_kernel<bf, false>)
-                           : (p.vec ? (const void *)lru_kernel<float, true> : (const void *)lru_kernel<float, false>);
-    const int smem = p.vec ? 4 * kLruTile * kLruCh * (p.bf16 ? 2 : 4) : 0;
-    return lru_launch(k, p.B, p.C, p.ranks, smem, p, st);
+    return lru_by_form(p, p.z != nullptr, [&](auto type, auto vec, auto packed, auto z) {
+        using T = decltype(type);
+        const int smem = vec() ? (z() ? 4 : 3) * kLruTile * kLruCh * (int)sizeof(T) : 0;
+        return lru_launch((const void *)lru_kernel<T, vec(), packed(), z()>, p.B, p.C, p.ranks, smem, p, st);
+    });
 }
 
 cudaError_t launch_lru_step(const LruStepParams &p, cudaStream_t st) {

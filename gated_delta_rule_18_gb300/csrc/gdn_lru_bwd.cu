@@ -16,202 +16,207 @@
 namespace gdn {
 namespace {
 
-constexpr int kRanks = 8;
-
-struct Exchange {
-    LruRun fwd[2][kLruWarps][32];  // A, H of a warp's tokens
-    f32x2 back[2][kLruWarps][32];  // what they add to the gradient before them
-    LruRun ranks[2][kRanks][32];
-};
-
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool PACKED, bool Z>
 __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ Exchange ex;
-    constexpr int KW = RowVec<T, 2>::kWords, kRow = kLruCh;
+    __shared__ LruRun runs[2][kLruWarps][32];  // A, H of a warp's tokens
+    __shared__ f32x2 backs[2][kLruWarps][32];  // what they add to the gradient before them
+    __shared__ LruRanks ranks;
+    constexpr int kRow = kLruCh, kTensor = kLruLen * kRow, kTensors = Z ? 5 : 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int K = p.ranks, rank = K > 1 ? blockIdx.x % K : 0, line = blockIdx.y;
+    const int K = p.ranks, rank = blockIdx.x % K, line = blockIdx.y;
     const int c0 = (blockIdx.x / K) * kLruCh, c = c0 + 2 * lane, nc = p.C - c;
-    if (p.err && blockIdx.x == 0 && blockIdx.y == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
-    auto ld_state = [&](const float *s, int64_t row) {
-        float2 f = make_float2(0.f, 0.f);
-        if (s && nc > 0) f.x = s[row * p.C + c];
-        if (s && nc > 1) f.y = s[row * p.C + c + 1];
-        return pack2(f.x, f.y);
-    };
-    auto st_state = [&](float *s, int64_t row, f32x2 v) {
-        const float2 f = unpack2(v);
-        if (nc > 0) s[row * p.C + c] = f.x;
-        if (nc > 1) s[row * p.C + c + 1] = f.y;
-    };
-    if (p.dh0 && rank == 0) {  // of sequences without tokens
-        if (!p.cu) {
-            if (p.T == 0 && warp == 0) st_state(p.dh0, line, ld_state(p.dh_final, line));
-        } else {
+    const f32x2 one = pack2(1.f, 1.f), zero = pack2(0.f, 0.f), minus = pack2(-1.f, -1.f);
+    if (PACKED) {
+        if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
+        if (p.dh0 && rank == 0) {  // of sequences without tokens
             for (int s = warp; s < p.n_seq; s += kLruWarps)
-                if (p.cu[s + 1] <= p.cu[s]) st_state(p.dh0, s, ld_state(p.dh_final, s));
+                if (p.cu[s + 1] <= p.cu[s]) lru_st_state(p.dh0, s, p.C, c, nc, lru_ld_state(p.dh_final, s, p.C, c, nc));
         }
     }
     const int steps = (p.T + K * kLruTile - 1) / (K * kLruTile), tiles = (p.T + kLruTile - 1) / kLruTile;
-    const T *x = (const T *)p.x + line * p.x_sb, *r = (const T *)p.r + line * p.r_sb, *in = (const T *)p.i + line * p.i_sb;
-    const T *z = p.z ? (const T *)p.z + line * p.z_sb : nullptr, *dout = (const T *)p.dout + line * p.do_sb;
-    constexpr int kTensor = kLruLen * kRow;
-    T *stage = (T *)smem + warp * 5 * kTensor;
-    constexpr int kStage = kLruWarps * 5 * kTensor;  // elements of a stage
+    const T *x = (const T *)p.x + line * p.x_sb + c0, *r = (const T *)p.r + line * p.r_sb + c0;
+    const T *in = (const T *)p.i + line * p.i_sb + c0, *dout = (const T *)p.dout + line * p.do_sb + c0;
+    const T *z = Z ? (const T *)p.z + line * p.z_sb + c0 : nullptr;
+    constexpr int kStage = kLruWarps * kTensors * kTensor;  // elements of a stage
+    T *const stage = (T *)smem + warp * kTensors * kTensor;
     auto first = [&](int n) { return ((steps - 1 - n) * K + rank) * kLruTile + warp * kLruLen; };
     auto fetch = [&](int n) {
-        if constexpr (VEC) {
-            if (n < steps) {
-                const int t = first(n), rows = min(max(p.T - t, 0), kLruLen);
-                T *s = stage + (n & 1) * kStage;
-                if (rows > 0) {
-                    lru_copy(s, x + t * p.x_st, p.x_st, rows, c0, p.C);
-                    lru_copy(s + kTensor, r + t * p.r_st, p.r_st, rows, c0, p.C);
-                    lru_copy(s + 2 * kTensor, in + t * p.i_st, p.i_st, rows, c0, p.C);
-                    lru_copy(s + 3 * kTensor, dout + t * p.do_st, p.do_st, rows, c0, p.C);
-                    if (z) lru_copy(s + 4 * kTensor, z + t * p.z_st, p.z_st, rows, c0, p.C);
-                }
-            }
-            cp_async_commit();
+        if (!VEC) return;
+        const int t = n < steps ? first(n) : p.T, rows = min(p.T - t, kLruLen);
+        if (rows > 0) {
+            T *s = stage + (n & 1) * kStage;
+            lru_copy(s, x + t * p.x_st, p.x_st, rows, p.C - c0);
+            lru_copy(s + kTensor, r + t * p.r_st, p.r_st, rows, p.C - c0);
+            lru_copy(s + 2 * kTensor, in + t * p.i_st, p.i_st, rows, p.C - c0);
+            lru_copy(s + 3 * kTensor, dout + t * p.do_st, p.do_st, rows, p.C - c0);
+            if (Z) lru_copy(s + 4 * kTensor, z + t * p.z_st, p.z_st, rows, p.C - c0);
         }
+        cp_async_commit();
     };
     fetch(0);
     float cl[2] = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < 2; ++k)
         if (k < nc) cl[k] = lru_decay(p.lam[c + k], p.c);
-    const f32x2 cl2 = pack2(cl[0], cl[1]), one = pack2(1.f, 1.f), zero = pack2(0.f, 0.f);
-    f32x2 carry = zero;  // a g of the token behind the cluster's tiles
-    f32x2 dlam = zero;
-    if (K > 1) cluster_arrive(), cluster_wait();
+    const f32x2 cl2 = pack2(cl[0], cl[1]);
+    // a g of the token behind the cluster's tiles
+    f32x2 carry = PACKED ? zero : lru_ld_state(p.dh_final, line, p.C, c, nc), dlam = zero;
+    bool lost = false;
+    if (K > 1) {
+        if (threadIdx.x == 0) ranks.init();
+        cluster_sync();
+    }
     for (int n = 0; n < steps; ++n) {
         const int t0 = first(n), len = min(max(p.T - t0, 0), kLruLen), flip = n & 1, tile = (steps - 1 - n) * K + rank;
-        const LruMarks m = lru_marks(p.cu, p.n_seq, p.T, t0);
-        f32x2 h = tile < tiles ? ld_state(p.ck, (int64_t)line * tiles + tile) : zero;
+        LruMarks m{0u, 0u};
+        if (PACKED) m = lru_marks(p.cu, p.n_seq, p.T, t0);
+        f32x2 h = tile < tiles ? lru_ld_state(p.ck, (int64_t)line * tiles + tile, p.C, c, nc) : zero;
         __syncwarp();  // every lane has read what the next copies overwrite
         fetch(n + 1);
-        if constexpr (VEC) {
+        if (VEC) {
             cp_async_wait<1>();
             __syncwarp();
         }
-        const T *staged = stage + flip * kStage;
-        // a pair of tensor k (x, r, i, dout, z) at token j of the warp
+        const T *staged = stage + flip * kStage + 2 * lane;
+        // a pair of tensor k at token j of the warp
         auto get = [&](int k, int j) -> f32x2 {
-            uint32_t w[KW] = {};
-            if constexpr (VEC) {
-                ld_words(w, staged + k * kTensor + j * kRow + 2 * lane);
-            } else if (nc > 0) {
+            if (VEC) return lru_pair(staged + k * kTensor + j * kRow);
+            float f[2] = {0.f, 0.f};
+            if (nc > 0) {
                 const int64_t t = t0 + j;
                 const T *at = k == 0 ? x + t * p.x_st : k == 1 ? r + t * p.r_st : k == 2 ? in + t * p.i_st
                               : k == 3 ? dout + t * p.do_st : z + t * p.z_st;
-                ld_row<T, 2, false>(w, at + c, nc);
+                ld_row_f<T, 2, false>(f, at + 2 * lane, nc);
             }
-            return lru_pair<T>(w);
+            return pack2(f[0], f[1]);
         };
-        f32x2 a[kLruLen], b[kLruLen], gd[kLruLen];
+        const bool all_inside = len == kLruLen && !(m.cut | m.fin);
+        f32x2 a[kLruLen], b[kLruLen], back = zero;
         LruRun run{one, zero};
+        auto gates = [&](auto form) {  // whole: eight tokens within a sequence
+            constexpr bool whole = decltype(form)::value;
+            bool open = true;  // no sequence has begun in the run
 #pragma unroll
-        for (int j = 0; j < kLruLen; ++j) {
-            a[j] = one, b[j] = gd[j] = zero;
-            if (j >= len) continue;
-            const LruGate g(get(1, j), get(2, j), cl2);
-            a[j] = g.a, b[j] = mul2(mul2(g.beta(), g.gi), get(0, j));
-            gd[j] = get(3, j);
-            if (z) {
-                const float2 v = unpack2(get(4, j)), s = sigmoid2(v);
-                gd[j] = mul2(gd[j], pack2(v.x * s.x, v.y * s.y));
-            }
-            if (m.fin >> j & 1 && p.dh_final)
-                gd[j] = add2(gd[j], ld_state(p.dh_final, lru_seq(p.cu, p.n_seq, p.T, line, t0 + j)));
-            if (m.cut >> j & 1) {
-                if (p.h0) b[j] = fma2(a[j], ld_state(p.h0, lru_seq(p.cu, p.n_seq, p.T, line, t0 + j)), b[j]);
-                run.A = pack2(-0.f, -0.f), run.H = b[j];
-            } else {
+            for (int j = 0; j < kLruLen; ++j) {
+                if (!whole && j >= len) {
+                    a[j] = one, b[j] = zero;
+                    continue;
+                }
+                const LruGate g(get(1, j), get(2, j), cl2);
+                a[j] = g.a, b[j] = mul2(mul2(sqrt_2(g.q), g.gi), get(0, j));
+                f32x2 gd = get(3, j);
+                if (Z) {
+                    const f32x2 v = get(4, j);
+                    gd = mul2(gd, mul2(v, sigmoid_2(v)));
+                }
+                if (PACKED && !whole) {
+                    if (m.fin >> j & 1 && p.dh_final)
+                        gd = add2(gd, lru_ld_state(p.dh_final, lru_seq(p.cu, p.n_seq, p.T, t0 + j), p.C, c, nc));
+                    if (m.cut >> j & 1) {
+                        if (p.h0) b[j] = fma2(a[j], lru_ld_state(p.h0, lru_seq(p.cu, p.n_seq, p.T, t0 + j), p.C, c, nc), b[j]);
+                        run.A = pack2(-0.f, -0.f), run.H = b[j];
+                        open = false;
+                        continue;
+                    }
+                }
                 run.A = mul2(run.A, a[j]), run.H = fma2(a[j], run.H, b[j]);
+                if (whole || open) back = fma2(run.A, gd, back);
+            }
+        };
+        if (all_inside) gates(std::true_type());
+        else gates(std::false_type());
+        runs[flip][warp][lane] = run, backs[flip][warp][lane] = back;
+        __syncthreads();
+        f32x2 gm = carry;  // a g of the token behind this one
+        if (K > 1) {
+            if (warp == 0) {
+                LruRun all{runs[flip][kLruWarps - 1][lane].A, backs[flip][kLruWarps - 1][lane]};
+#pragma unroll
+                for (int w = kLruWarps - 2; w >= 0; --w) {
+                    const f32x2 A = runs[flip][w][lane].A;
+                    all.H = lru_apply2<PACKED>(A, backs[flip][w][lane], all.H), all.A = lru_join<PACKED>(all.A, A);
+                }
+                ranks.send(n, K, rank, all);
             }
         }
-        f32x2 back = zero;
-#pragma unroll
-        for (int j = kLruLen - 1; j >= 0; --j) {
-            if (j < len) back = m.cut >> j & 1 ? zero : mul2(a[j], add2(gd[j], back));
-        }
-        ex.fwd[flip][warp][lane] = run, ex.back[flip][warp][lane] = back;
-        __syncthreads();
-        // the state before this warp's tokens; the CTA's run backwards and the part behind this warp
-        LruRun all{one, zero}, behind = all;
+        // the state before this warp's tokens
 #pragma unroll
         for (int w = 0; w < kLruWarps; ++w) {
-            if (w < warp) {
-                const LruRun v = ex.fwd[flip][w][lane];
-                h = lru_apply2(v.A, v.H, h);
+            if (w >= warp) break;
+            const LruRun v = runs[flip][w][lane];
+            h = lru_apply2<PACKED>(v.A, v.H, h);
+        }
+        const f32x2 h_in = h;
+#pragma unroll
+        for (int j = 0; j < kLruLen; ++j)  // b becomes h (it stays where tokens end)
+            h = b[j] = PACKED && m.cut >> j & 1 ? b[j] : fma2(a[j], h, b[j]);
+        if (K > 1) {
+            if (!lost) lost = !ranks.wait(n);
+            for (int k = K - 1; k >= 0; --k) {
+                const LruRun v = ranks.runs[flip][k][lane];
+                if (k == rank) gm = carry;
+                carry = lru_apply2<PACKED>(v.A, v.H, carry);
             }
         }
 #pragma unroll
         for (int w = kLruWarps - 1; w >= 0; --w) {
-            if (w == warp) behind = all;
-            const f32x2 A = ex.fwd[flip][w][lane].A;
-            all.H = lru_apply2(A, ex.back[flip][w][lane], all.H), all.A = lru_join(all.A, A);
-        }
-        f32x2 gm = carry;  // a g of the token behind this one
-        if (K > 1) {
-            if (warp < K) st_cluster(&ex.ranks[flip][rank][lane], warp, all);
-            cluster_arrive(), cluster_wait();
-            for (int k = K - 1; k >= 0; --k) {
-                const LruRun v = ex.ranks[flip][k][lane];
-                if (k == rank) gm = carry;
-                carry = lru_apply2(v.A, v.H, carry);
+            if (K > 1 && w <= warp) break;
+            const f32x2 A = runs[flip][w][lane].A, H = backs[flip][w][lane];
+            if (K == 1) {
+                if (w == warp) gm = carry;
+                carry = lru_apply2<PACKED>(A, H, carry);
+            } else {
+                gm = lru_apply2<PACKED>(A, H, gm);
             }
-        } else {
-            carry = lru_apply2(all.A, all.H, carry);
         }
-        gm = lru_apply2(behind.A, behind.H, gm);
-        const f32x2 h_in = h;
-#pragma unroll
-        for (int j = 0; j < kLruLen; ++j) {  // b becomes h
-            if (j >= len) break;
-            h = b[j] = m.cut >> j & 1 ? b[j] : fma2(a[j], h, b[j]);
-        }
+        if (lost) gm = carry = pack2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
         const int64_t at0 = ((int64_t)line * p.T + t0) * p.C + c;
+        auto walk = [&](auto form) {
+            constexpr bool whole = decltype(form)::value;
 #pragma unroll
-        for (int j = kLruLen - 1; j >= 0; --j) {
-            if (j >= len) continue;
-            const f32x2 xv = get(0, j), g = add2(gd[j], gm);
-            const LruGate gt(get(1, j), get(2, j), cl2);
-            f32x2 prev = j > 0 ? b[j > 0 ? j - 1 : 0] : h_in;
-            const f32x2 ag = mul2(a[j], g);
-            gm = ag;
-            if (m.cut >> j & 1) {
-                const int seq = lru_seq(p.cu, p.n_seq, p.T, line, t0 + j);
-                prev = ld_state(p.h0, seq);
-                if (p.dh0) st_state(p.dh0, seq, ag);
-                gm = zero;
+            for (int j = kLruLen - 1; j >= 0; --j) {
+                if (!whole && j >= len) continue;
+                const int64_t at = at0 + (int64_t)j * p.C;
+                f32x2 g = get(3, j);
+                if (Z) {
+                    // silu' = s + v s (1 - s)
+                    const f32x2 v = get(4, j), s = sigmoid_2(v), vs = mul2(v, s);
+                    const f32x2 ds = fma2(vs, fma2(s, minus, one), s);
+                    if (nc > 0) lru_put<T, VEC>((T *)p.dz + at, mul2(mul2(g, b[j]), ds), nc);
+                    g = mul2(g, vs);
+                }
+                f32x2 prev = j > 0 ? b[j > 0 ? j - 1 : 0] : h_in;
+                if (PACKED && !whole && m.fin >> j & 1 && p.dh_final)
+                    g = add2(g, lru_ld_state(p.dh_final, lru_seq(p.cu, p.n_seq, p.T, t0 + j), p.C, c, nc));
+                g = add2(g, gm);
+                gm = mul2(a[j], g);
+                const f32x2 ag = gm;
+                if (PACKED && !whole && m.cut >> j & 1) {
+                    const int seq = lru_seq(p.cu, p.n_seq, p.T, t0 + j);
+                    prev = lru_ld_state(p.h0, seq, p.C, c, nc);
+                    if (p.dh0) lru_st_state(p.dh0, seq, p.C, c, nc, ag);
+                    gm = zero;
+                }
+                const LruGate gt(get(1, j), get(2, j), cl2);
+                const f32x2 xv = get(0, j), rs = rsqrt_2(gt.q), ix = mul2(gt.gi, xv);
+                const f32x2 dx = mul2(mul2(g, mul2(gt.q, rs)), gt.gi), di = mul2(mul2(dx, xv), fma2(gt.gi, minus, one));
+                // u g (a^2 i x / sqrt(q) - a prev)
+                const f32x2 w = mul2(mul2(ag, gt.u), fma2(prev, minus, mul2(mul2(rs, a[j]), ix)));
+                dlam = add2(dlam, w);
+                if (nc > 0) {
+                    lru_put<T, VEC>((T *)p.dx + at, dx, nc), lru_put<T, VEC>((T *)p.di + at, di, nc);
+                    lru_put<T, VEC>((T *)p.dr + at, mul2(w, fma2(gt.gr, minus, one)), nc);
+                }
             }
-            const float2 q = unpack2(gt.q);
-            const f32x2 rs = pack2(rsqrt_approx(fmaxf(q.x, 1e-37f)), rsqrt_approx(fmaxf(q.y, 1e-37f)));
-            const f32x2 beta = mul2(gt.q, rs), gbi = mul2(mul2(g, beta), gt.gi), ix = mul2(gt.gi, xv);
-            const f32x2 di = mul2(mul2(gbi, xv), fma2(gt.gi, pack2(-1.f, -1.f), one));
-            // u g (a^2 i x / sqrt(q) - a prev)
-            const f32x2 in_term = mul2(mul2(gt.u, rs), mul2(a[j], ix));
-            const f32x2 w = mul2(ag, fma2(mul2(gt.u, pack2(-1.f, -1.f)), prev, in_term));
-            const f32x2 dr = mul2(w, fma2(gt.gr, pack2(-1.f, -1.f), one));
-            dlam = add2(dlam, w);
-            if (nc <= 0) continue;
-            const int64_t at = at0 + (int64_t)j * p.C;
-            auto put = [&](void *to, f32x2 v) {
-                const float2 f = unpack2(v);
-                const float o[2] = {f.x, f.y};
-                st_row_f<T, 2, VEC>((T *)to + at, o, nc);
-            };
-            put(p.dx, gbi), put(p.di, di), put(p.dr, dr);
-            if (z) {
-                const float2 v = unpack2(get(4, j)), s = sigmoid2(v), d = unpack2(mul2(get(3, j), b[j]));
-                put(p.dz, pack2(d.x * (s.x + v.x * s.x * (1.f - s.x)), d.y * (s.y + v.y * s.y * (1.f - s.y))));
-            }
-        }
+        };
+        if (all_inside) walk(std::true_type());
+        else walk(std::false_type());
     }
+    if (!PACKED && p.dh0 && rank == 0 && warp == 0) lru_st_state(p.dh0, line, p.C, c, nc, carry);
     // the channels' sums over the warps, in one order
     __syncthreads();
-    f32x2 *sums = &ex.back[0][0][0];
+    f32x2 *sums = &backs[0][0][0];
     sums[warp * 32 + lane] = dlam;
     __syncthreads();
     if (warp == 0 && nc > 0) {
@@ -226,16 +231,17 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
             p.part[((int64_t)line * K + rank) * p.C + c + k] = o[k];
         }
     }
+    if (K > 1) cluster_sync();  // no CTA leaves before all have what it sent
 }
 
 }  // namespace
 
 cudaError_t launch_lru_bwd(const LruParams &p, cudaStream_t st) {
-    using bf = __nv_bfloat16;
-    const void *k = p.bf16 ? (p.vec ? (const void *)lru_bwd_kernel<bf, true> : (const void *)lru_bwd_kernel<bf, false>)
-                           : (p.vec ? (const void *)lru_bwd_kernel<float, true> : (const void *)lru_bwd_kernel<float, false>);
-    const int smem = p.vec ? 2 * 5 * kLruTile * kLruCh * (p.bf16 ? 2 : 4) : 0;
-    return lru_launch(k, p.B, p.C, p.ranks, smem, p, st);
+    return lru_by_form(p, p.z != nullptr, [&](auto type, auto vec, auto packed, auto z) {
+        using T = decltype(type);
+        const int smem = vec() ? 2 * (z() ? 5 : 4) * kLruTile * kLruCh * (int)sizeof(T) : 0;
+        return lru_launch((const void *)lru_bwd_kernel<T, vec(), packed(), z()>, p.B, p.C, p.ranks, smem, p, st);
+    });
 }
 
 }  // namespace gdn
