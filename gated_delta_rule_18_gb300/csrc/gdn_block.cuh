@@ -39,6 +39,8 @@ struct BlockNormParams {
     int64_t ro_st, o_st;
     int R, D, gate_rows, act;  // gate_rows: rows that share one of the gate
     int y_bf16, r_bf16;
+    int shared;     // gate_rows > 1 rows share one of the gate: runs keep to one sequence
+    int runs, run;  // of a sequence's rows (of all rows, where nothing is shared)
     float alpha, eps;
     int vec;
 };
@@ -52,8 +54,7 @@ struct BlockNormBwdParams {
     float *dpost, *dpre, *dscale;
     float *part, *part2;  // workspace: sums by run of rows (parts, 2, D), by sequence (sequences, 2, D)
     int R, D, gate_rows, act, y_bf16, r_bf16;
-    int shared;       // gate_rows > 1 rows share one of the gate: runs keep to one sequence
-    int runs, run;    // of a sequence's rows (of all rows, where nothing is shared)
+    int shared, runs, run;
     float alpha, eps;
     int vec;
 };
@@ -76,7 +77,8 @@ struct LruParams {
     int64_t o_sb, o_st;
     float *h_final;  // (n_seq, C) or null
     float *ck;       // (B, ceil(T / 64), C) or null: the states entering the tiles
-    int B, T, C, bf16, vec;
+    int B, T, C, bf16;
+    int how;    // rows of all activations lie on 16 bytes (0), on words in pairs (1) or anywhere (2)
     int ranks;  // CTAs of a cluster, which take a line's tiles in turn
     int *err;
     // gradient; activations' gradients contiguous in x's type

@@ -55,6 +55,16 @@ struct Heads {
     }
 };
 
+// rows that lie on 16 bytes, on words in pairs, or anywhere (LruParams::how)
+struct LruLayout {
+    Rows wide, words;
+    void add(const void *p, int dtype, int64_t sb, int64_t st) { wide.add(p, dtype, sb, st), words.add(p, dtype, sb, st, 4); }
+    bool ok() const { return wide.ok; }
+    int how(int C, int dtype) const {
+        if (wide.wide && C % 8 == 0) return 0;
+        return words.wide && (dtype == GDN_F32 || C % 2 == 0) ? 1 : 2;
+    }
+};
 struct LruWs {
     size_t ck, part, total;
 };
@@ -149,6 +159,9 @@ gdn_status gdn_block_norm_fwd(const void *y, int64_t y_st, int y_dtype, const vo
     p.post = post_weight, p.pre = pre_weight, p.scale = scale, p.res_out = res_out, p.out = out;
     p.ro_st = res_out_st, p.o_st = out_st, p.R = R, p.D = D, p.gate_rows = gate_rows, p.act = act;
     p.y_bf16 = y_dtype == GDN_BF16, p.r_bf16 = res_dtype == GDN_BF16, p.alpha = alpha, p.eps = eps;
+    p.shared = gate_rows > 1;
+    int64_t parts;
+    block_norm_runs(R, D, gate_rows, &p.runs, &p.run, &parts);
     p.vec = r.wide && D % 8 == 0;
     return cuda_status(launch(KBlockNorm, stream, [&] { return launch_block_norm(p, stream); }));
 }
@@ -226,7 +239,7 @@ namespace {
 // The checks and the parameter block gdn_lru_fwd and gdn_lru_bwd share.
 gdn_status lru_setup(const void *x, int64_t x_sb, int64_t x_st, const void *r, int64_t r_sb, int64_t r_st, const void *i,
                      int64_t i_sb, int64_t i_st, const float *lam, const void *z, int64_t z_sb, int64_t z_st, float c,
-                     const float *h0, const int32_t *cu, int n_seq, int B, int T, int C, int dtype, Rows &rows, LruParams &p) {
+                     const float *h0, const int32_t *cu, int n_seq, int B, int T, int C, int dtype, LruLayout &rows, LruParams &p) {
     if (!lam || (T > 0 && (!x || !r || !i))) return GDN_ERR_NULL;
     if (!batch_ok(B, T, C, cu, n_seq) || !(c >= 0.f && c <= FLT_MAX)) return GDN_ERR_SHAPE;
     if (!dtype_ok(dtype)) return GDN_ERR_DTYPE;
@@ -234,7 +247,7 @@ gdn_status lru_setup(const void *x, int64_t x_sb, int64_t x_st, const void *r, i
     rows.add(r, dtype, r_sb, r_st);
     rows.add(i, dtype, i_sb, i_st);
     rows.add(z, dtype, z_sb, z_st);
-    if (!rows.ok || !f32_ok(lam) || !f32_ok(h0) || !f32_ok(cu)) return GDN_ERR_LAYOUT;
+    if (!rows.ok() || !f32_ok(lam) || !f32_ok(h0) || !f32_ok(cu)) return GDN_ERR_LAYOUT;
     p = LruParams{};
     p.x = x, p.x_sb = x_sb, p.x_st = x_st, p.r = r, p.r_sb = r_sb, p.r_st = r_st, p.i = i, p.i_sb = i_sb, p.i_st = i_st;
     p.lam = lam, p.z = z, p.z_sb = z_sb, p.z_st = z_st, p.c = c, p.h0 = h0, p.cu = cu, p.n_seq = n_seq;
@@ -250,7 +263,7 @@ gdn_status gdn_lru_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
                        int64_t z_st, float c, const float *h0, const int32_t *cu_seqlens, int n_seq, void *out,
                        int64_t out_sb, int64_t out_st, float *h_final, float *checkpoints, int B, int T, int C,
                        int dtype, void *workspace, size_t ws_bytes, cudaStream_t stream) {
-    Rows rows;
+    LruLayout rows;
     LruParams p;
     if (T > 0 && !out) return GDN_ERR_NULL;
     rows.add(out, dtype, out_sb, out_st);
@@ -268,7 +281,7 @@ gdn_status gdn_lru_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
     if (cu_seqlens && !ws_ok(workspace, ws_bytes, kAlign)) return GDN_ERR_WORKSPACE;
     if (T == 0 && !h_final && !cu_seqlens) return GDN_OK;
     p.out = out, p.o_sb = out_sb, p.o_st = out_st, p.h_final = h_final, p.ck = checkpoints;
-    p.vec = rows.wide && C % 8 == 0;
+    p.how = rows.how(C, dtype);
     p.err = cu_seqlens ? static_cast<int *>(workspace) : nullptr;
     return cuda_status(launch(KLru, stream, [&] { return launch_lru(p, stream); }));
 }
@@ -283,7 +296,7 @@ gdn_status gdn_lru_bwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
                        int64_t dout_sb, int64_t dout_st, const float *dh_final, const float *checkpoints, void *dx,
                        void *dr, void *di, float *dlam, void *dz, float *dh0, int B, int T, int C, int dtype,
                        void *workspace, size_t ws_bytes, cudaStream_t stream) {
-    Rows rows;
+    LruLayout rows;
     LruParams p;
     if (!dlam || (T > 0 && (!dout || !dx || !dr || !di || (z && !dz)))) return GDN_ERR_NULL;
     if ((dz && !z) || (dh0 && !h0)) return GDN_ERR_NULL;
@@ -305,7 +318,7 @@ gdn_status gdn_lru_bwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
     if (!ws_ok(workspace, ws_bytes, L.total)) return GDN_ERR_WORKSPACE;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     p.err = cu_seqlens ? reinterpret_cast<int *>(ws) : nullptr;
-    p.vec = rows.wide && C % 8 == 0;
+    p.how = rows.how(C, dtype);
     cudaError_t e = cudaSuccess;
     p.ck = const_cast<float *>(checkpoints);
     if (!checkpoints && T > 0) {  // the states that enter the tiles, by a forward pass without outputs

@@ -18,7 +18,7 @@
 namespace gdn {
 namespace {
 
-template <typename T, bool VEC, bool PACKED, bool Z>
+template <typename T, int HOW, bool PACKED, bool Z>
 __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ LruRun runs[2][kLruWarps][32];
@@ -36,50 +36,41 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
         }
     }
     const int steps = (p.T + K * kLruTile - 1) / (K * kLruTile);
-    const T *x = (const T *)p.x + line * p.x_sb + c0, *r = (const T *)p.r + line * p.r_sb + c0;
-    const T *in = (const T *)p.i + line * p.i_sb + c0, *z = Z ? (const T *)p.z + line * p.z_sb + c0 : nullptr;
-    T *out = p.out ? (T *)p.out + line * p.o_sb + c : nullptr;
-    T *stage = (T *)smem + warp * (Z ? 4 : 3) * kTensor;
+    const LruRows<T, HOW> x((const T *)p.x + line * p.x_sb + c0, p.x_st), r((const T *)p.r + line * p.r_sb + c0, p.r_st),
+        in((const T *)p.i + line * p.i_sb + c0, p.i_st), z((const T *)p.z + (Z ? line * p.z_sb + c0 : 0), p.z_st);
+    T *out = (T *)p.out + (p.out ? line * p.o_sb + c : 0);
+    T *const stage = (T *)smem + warp * (Z ? 4 : 3) * kTensor, *const staged = stage + 2 * lane;
     auto first = [&](int n) { return (n * K + rank) * kLruTile + warp * kLruLen; };  // token of step n
-    auto copy = [&](int n, int k, const T *src, int64_t st) {
-        const int t = first(n), rows = n < steps ? min(p.T - t, kLruLen) : 0;
-        if (rows > 0) lru_copy(stage + k * kTensor, src + t * st, st, rows, p.C - c0);
-    };
     // two groups of copies a step: x, r and i are free for the next step's once
     // a and b are formed, z once the outputs are
     auto fetch = [&](int n) {
-        if (VEC) copy(n, 0, x, p.x_st), copy(n, 1, r, p.r_st), copy(n, 2, in, p.i_st), cp_async_commit();
+        const int t = first(n), rows = p.T - t;
+        if (n < steps && rows > 0) {
+            x.copy(stage, t, rows, p.C - c0), r.copy(stage + kTensor, t, rows, p.C - c0);
+            in.copy(stage + 2 * kTensor, t, rows, p.C - c0);
+        }
+        cp_async_commit();
     };
     auto fetch_z = [&](int n) {
-        if (VEC && Z) copy(n, 3, z, p.z_st), cp_async_commit();
+        const int t = first(n), rows = p.T - t;
+        if (Z && n < steps && rows > 0) z.copy(stage + 3 * kTensor, t, rows, p.C - c0);
+        cp_async_commit();
     };
-    // a pair of x, r, i or z at token j of the warp
-    auto get = [&](int k, const T *src, int64_t st, int t0, int j) -> f32x2 {
-        if (VEC) return lru_pair(stage + k * kTensor + j * kRow + 2 * lane);
-        float f[2] = {0.f, 0.f};
-        if (nc > 0) ld_row_f<T, 2, false>(f, src + (int64_t)(t0 + j) * st + 2 * lane, nc);
-        return pack2(f[0], f[1]);
-    };
+    auto get = [&](int k, int j) { return lru_pair(staged + k * kTensor + j * kRow); };  // a pair of x, r, i or z
     fetch(0), fetch_z(0);
-    float cl[2] = {0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-        if (k < nc) cl[k] = lru_decay(p.lam[c + k], p.c);
-    const f32x2 cl2 = pack2(cl[0], cl[1]);
+    const LruDecay decay(p.lam + c, p.c, nc);
     f32x2 carry = PACKED ? zero : lru_ld_state(p.h0, line, p.C, c, nc);  // the state before the cluster's tiles
     bool lost = false;
     if (K > 1) {
-        if (threadIdx.x == 0) ranks.init();
+        ranks.init(K);
         cluster_sync();
     }
     for (int n = 0; n < steps; ++n) {
         const int t0 = first(n), len = min(max(p.T - t0, 0), kLruLen), flip = n & 1;
         LruMarks m{0u, 0u};
         if (PACKED) m = lru_marks(p.cu, p.n_seq, p.T, t0);
-        if (VEC) {
-            cp_async_wait<Z ? 1 : 0>();
-            __syncwarp();
-        }
+        cp_async_wait<1>();
+        __syncwarp();
         f32x2 a[kLruLen], b[kLruLen];
         LruRun run{one, zero};
         auto gates = [&](auto form) {  // whole: eight tokens, none of which begins a sequence
@@ -90,8 +81,8 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
                     a[j] = one, b[j] = zero;
                     continue;
                 }
-                const LruGate g(get(1, r, p.r_st, t0, j), get(2, in, p.i_st, t0, j), cl2);
-                a[j] = g.a, b[j] = mul2(mul2(sqrt_2(g.q), g.gi), get(0, x, p.x_st, t0, j));
+                const LruGate g(get(1, j), get(2, j), decay);
+                a[j] = g.a, b[j] = mul2(mul2(sqrt_2(g.q), g.gi), get(0, j));
                 if (PACKED && !whole && m.cut >> j & 1) {
                     if (p.h0) b[j] = fma2(g.a, lru_ld_state(p.h0, lru_seq(p.cu, p.n_seq, p.T, t0 + j), p.C, c, nc), b[j]);
                     run.A = pack2(-0.f, -0.f), run.H = b[j];
@@ -102,7 +93,7 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
         };
         if (len == kLruLen && !m.cut) gates(std::true_type());
         else gates(std::false_type());
-        if (VEC) __syncwarp();  // every lane has read what the next copies overwrite
+        __syncwarp();  // every lane has read what the next copies overwrite
         fetch(n + 1);
         runs[flip][warp][lane] = run;
         __syncthreads();
@@ -118,43 +109,44 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
                 ranks.send(n, K, rank, all);
             }
             if (!lost) lost = !ranks.wait(n);
-            for (int k = 0; k < K; ++k) {
+#pragma unroll 8
+            for (int k = 0; k < (K > 8 ? 16 : 8); ++k) {
                 const LruRun v = ranks.runs[flip][k][lane];
                 if (k == rank) h = carry;
                 carry = lru_apply2<PACKED>(v.A, v.H, carry);
             }
-        }
 #pragma unroll
-        for (int w = 0; w < kLruWarps; ++w) {
-            if (K > 1 && w >= warp) break;
-            const LruRun v = runs[flip][w][lane];
-            if (K == 1) {
+            for (int w = 0; w < kLruWarps - 1; ++w) {
+                if (w >= warp) break;
+                const LruRun v = runs[flip][w][lane];
+                h = lru_apply2<PACKED>(v.A, v.H, h);
+            }
+        } else {
+#pragma unroll
+            for (int w = 0; w < kLruWarps; ++w) {
+                const LruRun v = runs[flip][w][lane];
                 if (w == warp) h = carry;
                 carry = lru_apply2<PACKED>(v.A, v.H, carry);
-            } else {
-                h = lru_apply2<PACKED>(v.A, v.H, h);
             }
         }
         if (lost) h = carry = pack2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
         if (p.ck && warp == 0 && t0 < p.T)
             lru_st_state(p.ck, (int64_t)line * ((p.T + kLruTile - 1) / kLruTile) + t0 / kLruTile, p.C, c, nc, h);
-        if (VEC && Z) {
-            cp_async_wait<1>();
-            __syncwarp();
-        }
+        cp_async_wait<1>();
+        __syncwarp();
         T *o = out + (int64_t)t0 * p.o_st;
         auto walk = [&](auto form) {
             constexpr bool whole = decltype(form)::value;
 #pragma unroll
-            for (int j = 0; j < kLruLen; ++j) {
+            for (int j = 0; j < kLruLen; ++j, o += p.o_st) {
                 if (!whole && j >= len) break;
                 h = PACKED && !whole && m.cut >> j & 1 ? b[j] : fma2(a[j], h, b[j]);
                 f32x2 y = h;
                 if (Z) {
-                    const f32x2 v = get(3, z, p.z_st, t0, j);
+                    const f32x2 v = get(3, j);
                     y = mul2(h, mul2(v, sigmoid_2(v)));
                 }
-                if (nc > 0) lru_put<T, VEC>(o + j * p.o_st, y, nc);
+                if (nc > 0) lru_put<T, HOW>(o, y, nc);
                 if (PACKED && !whole && p.h_final && m.fin >> j & 1)
                     lru_st_state(p.h_final, lru_seq(p.cu, p.n_seq, p.T, t0 + j), p.C, c, nc, h);
             }
@@ -163,7 +155,7 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
             if (len == kLruLen && !(m.cut | m.fin)) walk(std::true_type());
             else walk(std::false_type());
         }
-        if (VEC && Z) __syncwarp();
+        __syncwarp();
         fetch_z(n + 1);
     }
     if (!PACKED && p.h_final && rank == 0 && warp == 0) lru_st_state(p.h_final, line, p.C, c, nc, carry);
@@ -189,8 +181,7 @@ __global__ void __launch_bounds__(128) lru_step_kernel(const LruStepParams p) {
     float o[4];
 #pragma unroll
     for (int k = 0; k < 4; k += 2) {
-        const float2 sp = softplus2(make_float2(lam[k], lam[k + 1]));
-        const LruGate g(pack2(r[k], r[k + 1]), pack2(i[k], i[k + 1]), pack2(p.c * sp.x, p.c * sp.y));
+        const LruGate g(pack2(r[k], r[k + 1]), pack2(i[k], i[k + 1]), LruDecay(lam + k, p.c, 2));
         const float2 v = unpack2(fma2(g.a, pack2(h[k], h[k + 1]), mul2(mul2(sqrt_2(g.q), g.gi), pack2(x[k], x[k + 1]))));
         h[k] = o[k] = v.x, h[k + 1] = o[k + 1] = v.y;
         if (p.z) {
@@ -205,18 +196,24 @@ __global__ void __launch_bounds__(128) lru_step_kernel(const LruStepParams p) {
 
 }  // namespace
 
-// CTAs of a cluster: a line's tiles side by side, up to eight, while the
-// channels alone do not fill the GPU and the line is long enough.
+// CTAs of a cluster: a line's tiles side by side, up to eight, while all lines
+// have fewer than four CTAs a SM and are long enough; sixteen only where that
+// leaves two a SM (clusters of sixteen fit an SM group badly). Forward, bf16,
+// with z: 4 x 4096 tokens of 4096 channels 180, 191, 171, 187, 246 us for 1, 2,
+// 4, 8, 16; 32768 tokens of 1024 channels 885, 543, 277, 200, 152; fp32, 5003
+// tokens of 1792 channels 148, 93, 56, 42, 50.
 int lru_ranks(int lines, int T, int C) {
     const int64_t ctas = (int64_t)lines * ((C + kLruCh - 1) / kLruCh);
     const int tiles = (T + kLruTile - 1) / kLruTile;
     int k = 1;
-    while (k < kLruRanks && k < tiles && ctas * k < 8 * 152) k *= 2;
-    return k;
+    while (k < 8 && k < tiles && ctas * k < 608) k *= 2;
+    return k == 8 && k < tiles && ctas * 16 <= 304 ? 16 : k;
 }
 
 cudaError_t lru_launch(const void *kernel, int lines, int C, int ranks, int smem, const LruParams &p, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (ranks > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((C + kLruCh - 1) / kLruCh * ranks, lines);
@@ -232,10 +229,10 @@ cudaError_t lru_launch(const void *kernel, int lines, int C, int ranks, int smem
 }
 
 cudaError_t launch_lru(const LruParams &p, cudaStream_t st) {
-    return lru_by_form(p, p.z != nullptr, [&](auto type, auto vec, auto packed, auto z) {
+    return lru_by_form(p, p.z != nullptr, [&](auto type, auto how, auto packed, auto z) {
         using T = decltype(type);
-        const int smem = vec() ? (z() ? 4 : 3) * kLruTile * kLruCh * (int)sizeof(T) : 0;
-        return lru_launch((const void *)lru_kernel<T, vec(), packed(), z()>, p.B, p.C, p.ranks, smem, p, st);
+        const int smem = (z() ? 4 : 3) * kLruTile * kLruCh * (int)sizeof(T);
+        return lru_launch((const void *)lru_kernel<T, how(), packed(), z()>, p.B, p.C, p.ranks, smem, p, st);
     });
 }
 

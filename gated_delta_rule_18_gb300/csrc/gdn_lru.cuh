@@ -13,15 +13,15 @@ constexpr int kLruWarps = 8, kLruLen = 8;  // a tile: eight warps of eight token
 constexpr int kLruCh = 64;                 // channels a CTA, two a lane
 static_assert(kLruWarps * kLruLen == kLruTile, "a CTA's tile");
 
-// 1 - exp(-y) for y >= 0 and a2 = exp(-y): by the series where the difference
-// cancels (y < 1/8: the first term left out is y^5 / 720 of the value, 4e-8)
-__device__ __forceinline__ f32x2 one_minus_exp(f32x2 y, f32x2 a2) {
-    f32x2 s = fma2(y, pack2(1.f / 120.f, 1.f / 120.f), pack2(-1.f / 24.f, -1.f / 24.f));
-    s = fma2(s, y, pack2(1.f / 6.f, 1.f / 6.f));
-    s = fma2(s, y, pack2(-0.5f, -0.5f));
-    s = fma2(s, y, pack2(1.f, 1.f));
-    const float2 t = unpack2(mul2(s, y)), v = unpack2(y), f = unpack2(fma2(a2, pack2(-1.f, -1.f), pack2(1.f, 1.f)));
-    return pack2(v.x < 0.125f ? t.x : f.x, v.y < 0.125f ? t.y : f.y);
+// 1 - a^2 = 1 - exp(-y) for y >= 0: by the series where the difference cancels
+// (y < 1/8: the first term left out is y^5 / 720 of the value, 4e-8). In
+// scalar instructions: their constants are immediates.
+__device__ __forceinline__ float one_minus_square(float a, float y) {
+    float s = fmaf(y, 1.f / 120.f, -1.f / 24.f);
+    s = fmaf(s, y, 1.f / 6.f);
+    s = fmaf(s, y, -0.5f);
+    s = fmaf(s, y, 1.f);
+    return y < 0.125f ? s * y : fmaf(-a, a, 1.f);
 }
 __device__ __forceinline__ f32x2 sqrt_2(f32x2 x) {
     float2 v = unpack2(x);
@@ -37,29 +37,24 @@ __device__ __forceinline__ f32x2 rsqrt_2(f32x2 x) {
     asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(v.y));
     return pack2(v.x, v.y);
 }
-// Sigmoids of a pair, 1 / (1 + exp(-v)): exactly 0 where exp(-v) overflows, and
-// a NaN stays a NaN and its own. A reciprocal each: one for two values would
-// have to keep their product finite (comparisons and selections, which cost
-// more than the reciprocal does).
-__device__ __forceinline__ f32x2 sigmoid_2(f32x2 v) {
-    const float2 d = unpack2(add2(ex2_2(mul2(v, pack2(-kLog2e, -kLog2e))), pack2(1.f, 1.f)));
-    return pack2(rcpf(d.x), rcpf(d.y));
-}
-// u = c softplus(lam) sigmoid(r): a = exp(-u), q = 1 - a^2. cl: c softplus(lam).
-struct LruGate {
-    f32x2 u, a, q, gr, gi;
-    __device__ __forceinline__ LruGate(f32x2 r, f32x2 i, f32x2 cl) {
-        gr = sigmoid_2(r), gi = sigmoid_2(i);
-        u = mul2(cl, gr);
-        a = ex2_2(mul2(u, pack2(-kLog2e, -kLog2e)));
-        q = one_minus_exp(add2(u, u), mul2(a, a));
+// What a channel pair's gates are made with: -c softplus(lam) log2(e), 2 c softplus(lam).
+struct LruDecay {
+    f32x2 base, twice;
+    __device__ __forceinline__ LruDecay(const float *lam, float c, int nc) {
+        const float2 s = softplus2(make_float2(nc > 0 ? lam[0] : 0.f, nc > 1 ? lam[1] : 0.f));
+        base = pack2(-kLog2e * (c * s.x), -kLog2e * (c * s.y)), twice = pack2(2.f * (c * s.x), 2.f * (c * s.y));
     }
 };
-// c softplus(lam) of a channel
-__device__ __forceinline__ float lru_decay(float lam, float c) {
-    return c * softplus2(make_float2(lam, lam)).x;
-}
-
+// u = c softplus(lam) sigmoid(r): a = exp(-u), q = 1 - a^2, u2 = 2 u
+struct LruGate {
+    f32x2 u2, a, q, gr, gi;
+    __device__ __forceinline__ LruGate(f32x2 r, f32x2 i, const LruDecay &d) {
+        gr = sigmoid_2(r), gi = sigmoid_2(i);
+        u2 = mul2(d.twice, gr), a = ex2_2(mul2(d.base, gr));
+        const float2 y = unpack2(u2), f = unpack2(a);
+        q = pack2(one_minus_square(f.x, y.x), one_minus_square(f.y, y.y));
+    }
+};
 // Which of a warp's tokens t0 .. t0 + kLruLen - 1 of a packed batch begin a
 // sequence (cut) and which end one (fin); nothing past the line. A dense
 // line has none: its state and gradient go in and out as the carries.
@@ -105,7 +100,7 @@ struct alignas(16) LruRun {
 };
 
 // --------------------------------------------------------- clusters ---------
-constexpr int kLruRanks = 8;  // most CTAs of a cluster
+constexpr int kLruRanks = 16;  // most CTAs of a cluster
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -118,9 +113,14 @@ __device__ __forceinline__ void cluster_sync() {
 struct LruRanks {
     LruRun runs[2][kLruRanks][32];
     unsigned long long bar[2];
-    __device__ __forceinline__ void init() {  // one thread; then a sync of the cluster
-        mbar_init(smem_u32(&bar[0]), 1), mbar_init(smem_u32(&bar[1]), 1);
-        fence_mbar_init();
+    // all threads; then a sync of the cluster. Ranks that are not there change nothing.
+    __device__ __forceinline__ void init(int K) {
+        for (int e = threadIdx.x; e < 2 * kLruRanks * 32; e += 32 * kLruWarps)
+            if (e / 32 % kLruRanks >= K) (&runs[0][0][0])[e] = LruRun{pack2(1.f, 1.f), pack2(0.f, 0.f)};
+        if (threadIdx.x == 0) {
+            mbar_init(smem_u32(&bar[0]), 1), mbar_init(smem_u32(&bar[1]), 1);
+            fence_mbar_init();
+        }
     }
     // one warp: this CTA's run of step n to every CTA of the cluster
     __device__ __forceinline__ void send(int n, int K, int rank, const LruRun &v) {
@@ -160,20 +160,57 @@ struct LruRanks {
 };
 
 // --------------------------------------------------------- staging ----------
-// A warp's rows of one tensor (kLruLen tokens x kLruCh channels) into shared
-// memory by 16-byte asynchronous copies; rows from `rows` on and channels from n
-// on are zeros. Only the warp itself reads them.
-template <typename T>
-__device__ __forceinline__ void lru_copy(T *dst, const T *src, int64_t st, int rows, int n) {
-    constexpr int VE = 16 / (int)sizeof(T), kRow = kLruCh / VE, kCopies = kLruLen * kRow;
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int k = 0; k < kCopies / 32; ++k) {
-        const int e = lane + 32 * k, r = e / kRow, c = e % kRow * VE;
-        const bool in = r < rows && c < n;
-        cp_async16(dst + r * kLruCh + c, in ? src + r * st + c : src, in ? 16 : 0);
+// How a warp's rows of a tensor (kLruLen tokens x kLruCh channels) get into its
+// part of shared memory, which only the warp itself reads: by asynchronous
+// copies of 16 bytes, of 4 (a word of each lane's pair; rows on any word), or
+// through registers (bf16 rows on odd elements).
+enum { kLruWide, kLruWords, kLruElements };
+template <typename T, int HOW>
+struct LruRows {
+    static constexpr int VE = 16 / (int)sizeof(T), kRow = kLruCh / VE, kStep = 32 / kRow, kN = kLruLen / kStep;
+    const T *at;   // this lane's first piece of the line's first token
+    int64_t st;
+    // src: the tile's first channel; n: channels that exist from there
+    __device__ __forceinline__ LruRows(const T *src, int64_t st_) : st(st_) {
+        const int lane = threadIdx.x & 31;
+        at = HOW == kLruWide ? src + lane / kRow * st + lane % kRow * VE : src + 2 * lane;
     }
-}
+    // rows t .. t + rows - 1, rows > 0; n as above. What is past them is zero.
+    __device__ __forceinline__ void copy(T *dst, int t, int rows, int n) const {
+        const int lane = threadIdx.x & 31;
+        const T *p = at + t * st;
+        if constexpr (HOW == kLruWide) {
+            const bool in = lane % kRow * VE < n;
+#pragma unroll
+            for (int k = 0; k < kN; ++k) {
+                const bool on = in && lane / kRow + k * kStep < rows;
+                cp_async16(dst + (lane + 32 * k) * VE, on ? p + k * kStep * st : at, on ? 16 : 0);
+            }
+        } else if constexpr (HOW == kLruWords) {
+            constexpr int kWords = 2 * (int)sizeof(T) / 4;
+#pragma unroll
+            for (int j = 0; j < kLruLen; ++j)
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) {
+                    const bool on = j < rows && 2 * lane + (kWords == 2 ? k : 1) < n;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(
+                                     smem_u32(reinterpret_cast<uint32_t *>(dst + j * kLruCh + 2 * lane) + k)),
+                                 "l"(reinterpret_cast<const uint32_t *>(on ? p + j * st : at) + (on ? k : 0)), "r"(on ? 4 : 0)
+                                 : "memory");
+                }
+        } else {
+            uint32_t w[kLruLen];
+#pragma unroll
+            for (int j = 0; j < kLruLen; ++j) {
+                const unsigned short *e = reinterpret_cast<const unsigned short *>(p + j * st);
+                w[j] = j < rows && 2 * lane < n ? e[0] : 0u;
+                if (j < rows && 2 * lane + 1 < n) w[j] |= (uint32_t)e[1] << 16;
+            }
+#pragma unroll
+            for (int j = 0; j < kLruLen; ++j) *reinterpret_cast<uint32_t *>(dst + j * kLruCh + 2 * lane) = w[j];
+        }
+    }
+};
 template <typename T>
 __device__ __forceinline__ f32x2 lru_pair(const T *p) {  // of a staged row
     uint32_t w[RowVec<T, 2>::kWords];
@@ -182,11 +219,12 @@ __device__ __forceinline__ f32x2 lru_pair(const T *p) {  // of a staged row
     words_to_f<T, 2>(f, w);
     return pack2(f[0], f[1]);
 }
-template <typename T, bool VEC>
+// pairs on a boundary of their own size are stored whole
+template <typename T, int HOW>
 __device__ __forceinline__ void lru_put(T *p, f32x2 v, int nc) {
     const float2 f = unpack2(v);
     const float o[2] = {f.x, f.y};
-    st_row_f<T, 2, VEC>(p, o, nc);
+    st_row_f<T, 2, HOW == kLruWide || (HOW == kLruWords && sizeof(T) == 2)>(p, o, nc);
 }
 // two channels of a row of states, of which nc exist; zeros without a tensor
 __device__ __forceinline__ f32x2 lru_ld_state(const float *s, int64_t row, int C, int c, int nc) {
@@ -201,15 +239,21 @@ __device__ __forceinline__ void lru_st_state(float *s, int64_t row, int C, int c
     if (nc > 1) s[row * C + c + 1] = f.y;
 }
 
-// f(element, wide rows, packed batch, with z) for a call's form
+// f(element, how rows are copied, packed batch, with z) for a call's form
 template <class F>
 cudaError_t lru_by_form(const LruParams &p, bool with_z, F &&f) {
     const std::true_type yes;
     const std::false_type no;
-    auto by_z = [&](auto t, auto v, auto k) { return with_z ? f(t, v, k, yes) : f(t, v, k, no); };
-    auto by_cu = [&](auto t, auto v) { return p.cu ? by_z(t, v, yes) : by_z(t, v, no); };
-    auto by_vec = [&](auto t) { return p.vec ? by_cu(t, yes) : by_cu(t, no); };
-    return p.bf16 ? by_vec(__nv_bfloat16()) : by_vec(float());
+    auto by_z = [&](auto t, auto h, auto k) { return with_z ? f(t, h, k, yes) : f(t, h, k, no); };
+    auto by_cu = [&](auto t, auto h) { return p.cu ? by_z(t, h, yes) : by_z(t, h, no); };
+    if (!p.bf16) {
+        if (p.how == kLruWide) return by_cu(float(), std::integral_constant<int, kLruWide>());
+        return by_cu(float(), std::integral_constant<int, kLruWords>());
+    }
+    const __nv_bfloat16 t{};
+    if (p.how == kLruWide) return by_cu(t, std::integral_constant<int, kLruWide>());
+    if (p.how == kLruWords) return by_cu(t, std::integral_constant<int, kLruWords>());
+    return by_cu(t, std::integral_constant<int, kLruElements>());
 }
 cudaError_t lru_launch(const void *kernel, int lines, int C, int ranks, int smem, const LruParams &p, cudaStream_t st);
 

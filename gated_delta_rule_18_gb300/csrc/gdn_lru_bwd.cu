@@ -16,7 +16,7 @@
 namespace gdn {
 namespace {
 
-template <typename T, bool VEC, bool PACKED, bool Z>
+template <typename T, int HOW, bool PACKED, bool Z>
 __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ LruRun runs[2][kLruWarps][32];  // A, H of a warp's tokens
@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int K = p.ranks, rank = blockIdx.x % K, line = blockIdx.y;
     const int c0 = (blockIdx.x / K) * kLruCh, c = c0 + 2 * lane, nc = p.C - c;
-    const f32x2 one = pack2(1.f, 1.f), zero = pack2(0.f, 0.f), minus = pack2(-1.f, -1.f);
+    const f32x2 one = pack2(1.f, 1.f), zero = pack2(0.f, 0.f), minus = pack2(-1.f, -1.f), half = pack2(0.5f, 0.5f);
     if (PACKED) {
         if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
         if (p.dh0 && rank == 0) {  // of sequences without tokens
@@ -35,36 +35,29 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
         }
     }
     const int steps = (p.T + K * kLruTile - 1) / (K * kLruTile), tiles = (p.T + kLruTile - 1) / kLruTile;
-    const T *x = (const T *)p.x + line * p.x_sb + c0, *r = (const T *)p.r + line * p.r_sb + c0;
-    const T *in = (const T *)p.i + line * p.i_sb + c0, *dout = (const T *)p.dout + line * p.do_sb + c0;
-    const T *z = Z ? (const T *)p.z + line * p.z_sb + c0 : nullptr;
+    const LruRows<T, HOW> x((const T *)p.x + line * p.x_sb + c0, p.x_st), r((const T *)p.r + line * p.r_sb + c0, p.r_st),
+        in((const T *)p.i + line * p.i_sb + c0, p.i_st), dout((const T *)p.dout + line * p.do_sb + c0, p.do_st),
+        z((const T *)p.z + (Z ? line * p.z_sb + c0 : 0), p.z_st);
     constexpr int kStage = kLruWarps * kTensors * kTensor;  // elements of a stage
     T *const stage = (T *)smem + warp * kTensors * kTensor;
     auto first = [&](int n) { return ((steps - 1 - n) * K + rank) * kLruTile + warp * kLruLen; };
     auto fetch = [&](int n) {
-        if (!VEC) return;
-        const int t = n < steps ? first(n) : p.T, rows = min(p.T - t, kLruLen);
+        const int t = n < steps ? first(n) : p.T, rows = p.T - t, nch = p.C - c0;
         if (rows > 0) {
             T *s = stage + (n & 1) * kStage;
-            lru_copy(s, x + t * p.x_st, p.x_st, rows, p.C - c0);
-            lru_copy(s + kTensor, r + t * p.r_st, p.r_st, rows, p.C - c0);
-            lru_copy(s + 2 * kTensor, in + t * p.i_st, p.i_st, rows, p.C - c0);
-            lru_copy(s + 3 * kTensor, dout + t * p.do_st, p.do_st, rows, p.C - c0);
-            if (Z) lru_copy(s + 4 * kTensor, z + t * p.z_st, p.z_st, rows, p.C - c0);
+            x.copy(s, t, rows, nch), r.copy(s + kTensor, t, rows, nch), in.copy(s + 2 * kTensor, t, rows, nch);
+            dout.copy(s + 3 * kTensor, t, rows, nch);
+            if (Z) z.copy(s + 4 * kTensor, t, rows, nch);
         }
         cp_async_commit();
     };
     fetch(0);
-    float cl[2] = {0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-        if (k < nc) cl[k] = lru_decay(p.lam[c + k], p.c);
-    const f32x2 cl2 = pack2(cl[0], cl[1]);
+    const LruDecay decay(p.lam + c, p.c, nc);
     // a g of the token behind the cluster's tiles
     f32x2 carry = PACKED ? zero : lru_ld_state(p.dh_final, line, p.C, c, nc), dlam = zero;
     bool lost = false;
     if (K > 1) {
-        if (threadIdx.x == 0) ranks.init();
+        ranks.init(K);
         cluster_sync();
     }
     for (int n = 0; n < steps; ++n) {
@@ -74,23 +67,10 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
         f32x2 h = tile < tiles ? lru_ld_state(p.ck, (int64_t)line * tiles + tile, p.C, c, nc) : zero;
         __syncwarp();  // every lane has read what the next copies overwrite
         fetch(n + 1);
-        if (VEC) {
-            cp_async_wait<1>();
-            __syncwarp();
-        }
+        cp_async_wait<1>();
+        __syncwarp();
         const T *staged = stage + flip * kStage + 2 * lane;
-        // a pair of tensor k at token j of the warp
-        auto get = [&](int k, int j) -> f32x2 {
-            if (VEC) return lru_pair(staged + k * kTensor + j * kRow);
-            float f[2] = {0.f, 0.f};
-            if (nc > 0) {
-                const int64_t t = t0 + j;
-                const T *at = k == 0 ? x + t * p.x_st : k == 1 ? r + t * p.r_st : k == 2 ? in + t * p.i_st
-                              : k == 3 ? dout + t * p.do_st : z + t * p.z_st;
-                ld_row_f<T, 2, false>(f, at + 2 * lane, nc);
-            }
-            return pack2(f[0], f[1]);
-        };
+        auto get = [&](int k, int j) { return lru_pair(staged + k * kTensor + j * kRow); };  // of x, r, i, dout, z
         const bool all_inside = len == kLruLen && !(m.cut | m.fin);
         f32x2 a[kLruLen], b[kLruLen], back = zero;
         LruRun run{one, zero};
@@ -103,7 +83,7 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
                     a[j] = one, b[j] = zero;
                     continue;
                 }
-                const LruGate g(get(1, j), get(2, j), cl2);
+                const LruGate g(get(1, j), get(2, j), decay);
                 a[j] = g.a, b[j] = mul2(mul2(sqrt_2(g.q), g.gi), get(0, j));
                 f32x2 gd = get(3, j);
                 if (Z) {
@@ -153,21 +133,22 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
             h = b[j] = PACKED && m.cut >> j & 1 ? b[j] : fma2(a[j], h, b[j]);
         if (K > 1) {
             if (!lost) lost = !ranks.wait(n);
-            for (int k = K - 1; k >= 0; --k) {
+#pragma unroll 8
+            for (int k = K > 8 ? 15 : 7; k >= 0; --k) {
                 const LruRun v = ranks.runs[flip][k][lane];
                 if (k == rank) gm = carry;
                 carry = lru_apply2<PACKED>(v.A, v.H, carry);
             }
-        }
 #pragma unroll
-        for (int w = kLruWarps - 1; w >= 0; --w) {
-            if (K > 1 && w <= warp) break;
-            const f32x2 A = runs[flip][w][lane].A, H = backs[flip][w][lane];
-            if (K == 1) {
+            for (int w = kLruWarps - 1; w > 0; --w) {
+                if (w <= warp) break;
+                gm = lru_apply2<PACKED>(runs[flip][w][lane].A, backs[flip][w][lane], gm);
+            }
+        } else {
+#pragma unroll
+            for (int w = kLruWarps - 1; w >= 0; --w) {
                 if (w == warp) gm = carry;
-                carry = lru_apply2<PACKED>(A, H, carry);
-            } else {
-                gm = lru_apply2<PACKED>(A, H, gm);
+                carry = lru_apply2<PACKED>(runs[flip][w][lane].A, backs[flip][w][lane], carry);
             }
         }
         if (lost) gm = carry = pack2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
@@ -183,7 +164,7 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
                     // silu' = s + v s (1 - s)
                     const f32x2 v = get(4, j), s = sigmoid_2(v), vs = mul2(v, s);
                     const f32x2 ds = fma2(vs, fma2(s, minus, one), s);
-                    if (nc > 0) lru_put<T, VEC>((T *)p.dz + at, mul2(mul2(g, b[j]), ds), nc);
+                    if (nc > 0) lru_put<T, HOW>((T *)p.dz + at, mul2(mul2(g, b[j]), ds), nc);
                     g = mul2(g, vs);
                 }
                 f32x2 prev = j > 0 ? b[j > 0 ? j - 1 : 0] : h_in;
@@ -198,15 +179,15 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
                     if (p.dh0) lru_st_state(p.dh0, seq, p.C, c, nc, ag);
                     gm = zero;
                 }
-                const LruGate gt(get(1, j), get(2, j), cl2);
+                const LruGate gt(get(1, j), get(2, j), decay);
                 const f32x2 xv = get(0, j), rs = rsqrt_2(gt.q), ix = mul2(gt.gi, xv);
                 const f32x2 dx = mul2(mul2(g, mul2(gt.q, rs)), gt.gi), di = mul2(mul2(dx, xv), fma2(gt.gi, minus, one));
                 // u g (a^2 i x / sqrt(q) - a prev)
-                const f32x2 w = mul2(mul2(ag, gt.u), fma2(prev, minus, mul2(mul2(rs, a[j]), ix)));
+                const f32x2 w = mul2(mul2(ag, mul2(gt.u2, half)), fma2(prev, minus, mul2(mul2(rs, a[j]), ix)));
                 dlam = add2(dlam, w);
                 if (nc > 0) {
-                    lru_put<T, VEC>((T *)p.dx + at, dx, nc), lru_put<T, VEC>((T *)p.di + at, di, nc);
-                    lru_put<T, VEC>((T *)p.dr + at, mul2(w, fma2(gt.gr, minus, one)), nc);
+                    lru_put<T, HOW>((T *)p.dx + at, dx, nc), lru_put<T, HOW>((T *)p.di + at, di, nc);
+                    lru_put<T, HOW>((T *)p.dr + at, mul2(w, fma2(gt.gr, minus, one)), nc);
                 }
             }
         };
@@ -237,10 +218,10 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
 }  // namespace
 
 cudaError_t launch_lru_bwd(const LruParams &p, cudaStream_t st) {
-    return lru_by_form(p, p.z != nullptr, [&](auto type, auto vec, auto packed, auto z) {
+    return lru_by_form(p, p.z != nullptr, [&](auto type, auto how, auto packed, auto z) {
         using T = decltype(type);
-        const int smem = vec() ? 2 * (z() ? 5 : 4) * kLruTile * kLruCh * (int)sizeof(T) : 0;
-        return lru_launch((const void *)lru_bwd_kernel<T, vec(), packed(), z()>, p.B, p.C, p.ranks, smem, p, st);
+        const int smem = 2 * (z() ? 5 : 4) * kLruTile * kLruCh * (int)sizeof(T);
+        return lru_launch((const void *)lru_bwd_kernel<T, how(), packed(), z()>, p.B, p.C, p.ranks, smem, p, st);
     });
 }
 

@@ -94,6 +94,14 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) {
     const float2 r = rcp2(e0 + 1.f, e1 + 1.f);
     return make_float2(x.x < 0.f ? e0 * r.x : r.x, x.y < 0.f ? e1 * r.y : r.y);
 }
+// Sigmoids of a pair, 1 / (1 + exp(-v)): exactly 0 where exp(-v) overflows, and
+// a NaN stays a NaN and its own. A reciprocal each: one for two values would
+// have to keep their product finite (comparisons and selections, which cost
+// more than the reciprocal does).
+__device__ __forceinline__ f32x2 sigmoid_2(f32x2 v) {
+    const float2 d = unpack2(add2(ex2_2(mul2(v, pack2(-kLog2e, -kLog2e))), pack2(1.f, 1.f)));
+    return pack2(rcpf(d.x), rcpf(d.y));
+}
 
 // ------------------------------------------------------------ sequences -----
 // The line of tokens a chunk lies on, and the sequence it is in: `end` is the
