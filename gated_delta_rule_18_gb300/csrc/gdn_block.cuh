@@ -40,7 +40,7 @@ struct BlockNormParams {
     int R, D, gate_rows, act;  // gate_rows: rows that share one of the gate
     int y_bf16, r_bf16;
     int shared;     // gate_rows > 1 rows share one of the gate: runs keep to one sequence
-    int runs, run;  // of a sequence's rows (of all rows, where nothing is shared)
+    int runs, run;  // of a sequence's rows (of all rows, where nothing is shared): set by the launch
     float alpha, eps;
     int vec;
 };
@@ -58,7 +58,7 @@ struct BlockNormBwdParams {
     float alpha, eps;
     int vec;
 };
-void block_norm_runs(int R, int D, int gate_rows, int *runs, int *run, int64_t *parts);
+int64_t block_norm_parts(int R, int D, int gate_rows);  // most rows of partial sums
 cudaError_t launch_block_norm_bwd(const BlockNormBwdParams &p, cudaStream_t st);
 cudaError_t launch_block_norm_sequences(const BlockNormBwdParams &p, cudaStream_t st);
 cudaError_t launch_block_norm_reduce(const BlockNormBwdParams &p, cudaStream_t st);

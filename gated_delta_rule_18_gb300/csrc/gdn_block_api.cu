@@ -160,19 +160,14 @@ gdn_status gdn_block_norm_fwd(const void *y, int64_t y_st, int y_dtype, const vo
     p.ro_st = res_out_st, p.o_st = out_st, p.R = R, p.D = D, p.gate_rows = gate_rows, p.act = act;
     p.y_bf16 = y_dtype == GDN_BF16, p.r_bf16 = res_dtype == GDN_BF16, p.alpha = alpha, p.eps = eps;
     p.shared = gate_rows > 1;
-    int64_t parts;
-    block_norm_runs(R, D, gate_rows, &p.runs, &p.run, &parts);
     p.vec = r.wide && D % 8 == 0;
     return cuda_status(launch(KBlockNorm, stream, [&] { return launch_block_norm(p, stream); }));
 }
 
 size_t gdn_block_norm_bwd_workspace_size(int R, int D, int gate_rows) {
     if (!norm_shape_ok(R, D) || gate_rows < 1 || (gate_rows > 1 && (R % gate_rows || R / gate_rows > 65535))) return 0;
-    int runs, run;
-    int64_t parts;
-    block_norm_runs(R, D, gate_rows, &runs, &run, &parts);
     const size_t row = (size_t)2 * D * 4;
-    return align_up((size_t)parts * row) + (gate_rows > 1 ? align_up((size_t)(R / gate_rows) * row) : 0) + kAlign;
+    return align_up((size_t)block_norm_parts(R, D, gate_rows) * row) + (gate_rows > 1 ? align_up((size_t)(R / gate_rows) * row) : 0) + kAlign;
 }
 
 gdn_status gdn_block_norm_bwd(const void *y, int64_t y_st, int y_dtype, const void *s, int64_t s_st, int s_dtype,
@@ -219,11 +214,9 @@ gdn_status gdn_block_norm_bwd(const void *y, int64_t y_st, int y_dtype, const vo
     p.R = R, p.D = D, p.gate_rows = gate_rows, p.act = act, p.y_bf16 = y_dtype == GDN_BF16, p.r_bf16 = s_dtype == GDN_BF16;
     p.shared = gate && gate_rows > 1, p.alpha = alpha, p.eps = eps;
     p.vec = r.wide && D % 8 == 0;
-    int64_t parts;
-    block_norm_runs(R, D, p.shared ? gate_rows : 1, &p.runs, &p.run, &parts);
     unsigned char *ws = static_cast<unsigned char *>(workspace) + kAlign;
     p.part = reinterpret_cast<float *>(ws);
-    p.part2 = reinterpret_cast<float *>(ws + align_up((size_t)parts * 2 * D * 4));
+    p.part2 = reinterpret_cast<float *>(ws + align_up((size_t)block_norm_parts(R, D, gate_rows) * 2 * D * 4));
     cudaError_t e = cudaSuccess;
     if (R > 0) e = launch(KBlockNormBwd, stream, [&] { return launch_block_norm_bwd(p, stream); });
     if (e == cudaSuccess && R > 0 && p.shared)

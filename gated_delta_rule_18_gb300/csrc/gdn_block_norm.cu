@@ -27,15 +27,36 @@ constexpr int kVecN = 8, kPairs = kVecN / 2;
 struct RowShape {
     int tpr, nv, rpb;  // threads a row, vectors a thread, rows a CTA
 };
-// Whole warps, as few as cover the row (1792 channels: 7, not 8), up to 512
-// threads; rows of up to two warps share a CTA.
-RowShape row_shape(int D) {
+// `two`: two vectors a thread where that leaves a row two warps, as what a row
+// costs each warp (its two sums, pointers, barriers) is as much as four pairs
+// of channels. Not for the gradient with a gate value a token, whose two
+// vectors do not fit the registers (4 x 4096 x 4096, bf16, fp32 stream: 366 us
+// for 323), nor for rows that are not wide. Whole warps, as few as cover the
+// row, up to 512 threads; rows of up to two warps share a CTA.
+RowShape row_shape(int D, bool two) {
     const int vecs = (D + kVecN - 1) / kVecN;
     RowShape s;
-    s.nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;
+    s.nv = vecs <= (two ? 64 : 512) ? 1 : vecs <= 1024 ? 2 : 4;
     s.tpr = ((vecs + s.nv - 1) / s.nv + 31) / 32 * 32;
     s.rpb = s.tpr > 64 ? 1 : 128 / s.tpr;
     return s;
+}
+RowShape row_shape(const BlockNormParams &p) { return row_shape(p.D, p.vec); }
+RowShape row_shape(const BlockNormBwdParams &p) { return row_shape(p.D, p.vec && !(p.act && !p.shared)); }
+// Runs of a sequence's rows: as many CTAs as make 1024 threads a SM, two at least.
+struct Runs {
+    int n, len;
+    int64_t parts;
+};
+Runs runs_of(int R, int gate_rows, const RowShape &s) {
+    const int rows = gate_rows > 1 ? gate_rows : R, n = gate_rows > 1 ? R / gate_rows : 1;
+    const int nt = s.tpr * s.rpb, ctas = 152 * (nt <= 128 ? 8 : nt <= 256 ? 4 : 2), most = n < ctas ? ctas / n : 1;
+    const int need = (int)(((int64_t)rows + s.rpb - 1) / s.rpb), want = need < most ? need : most;
+    Runs r;
+    r.len = want > 0 ? (need + want - 1) / want * s.rpb : s.rpb;
+    r.n = (int)(((int64_t)rows + r.len - 1) / r.len);
+    r.parts = (int64_t)n * r.n * s.rpb;
+    return r;
 }
 
 template <typename T>
@@ -97,41 +118,61 @@ __device__ __forceinline__ f32x2 gate_of(f32x2 x, int act, f32x2 &d) {
     return f;
 }
 
-// sums of N values over a row's warps; red: N rows of 16 floats, one a warp,
-// zeros past the CTA's
-template <int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[16], int tpr) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    if (tpr == 32) return;
-    const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) red[k][warp] = v[k];
-    }
+// The warps of a thread's row: `n` from `w0` on, whose sums lie side by side.
+struct RowWarps {
+    int w0, n;
+    __device__ __forceinline__ RowWarps(int tpr) : w0(tpr == 64 ? (threadIdx.x >> 5) & ~1 : 0), n(tpr >> 5) {}
+};
+// The row's sum of v; red: 16 floats, one a warp, zeros past the CTA's.
+__device__ __forceinline__ float row_sum(float v, float *red, RowWarps r) {
+    v = warp_sum(v);
+    if (r.n == 1) return v;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        if (tpr == 64) {
-            v[k] = red[k][warp & ~1] + red[k][warp | 1];
-        } else {
-            v[k] = 0.f;
-            for (int i = 0; i < tpr >> 5; i += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(red[k] + i);
-                v[k] += (f.x + f.y) + (f.z + f.w);
-            }
-        }
+    if (r.n == 2) return red[r.w0] + red[r.w0 + 1];
+    v = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < r.n; i += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(red + i);
+        v += (f.x + f.y) + (f.z + f.w);
     }
+    return v;
+}
+// The row's sums of three values: lanes halve what they carry as they halve
+// the lanes (6 shuffles where one value at a time takes 15). red as above, of
+// four values a warp.
+__device__ __forceinline__ void row_sums3(float (&v)[3], float4 *red, RowWarps r) {
+    const int lane = threadIdx.x & 31;
+    const bool up = lane & 16, half = lane & 8;
+    float a = (up ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
+    const float b = (up ? 0.f : v[1]) + __shfl_xor_sync(0xffffffffu, up ? v[1] : 0.f, 16);
+    a = (half ? b : a) + __shfl_xor_sync(0xffffffffu, half ? a : b, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (r.n == 1) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) v[k] = __shfl_sync(0xffffffffu, a, 8 * k);
+        return;
+    }
+    if ((lane & 7) == 0) reinterpret_cast<float *>(red + (threadIdx.x >> 5))[lane >> 3] = a;
+    __syncthreads();
+    f32x2 xy = pack2(0.f, 0.f);
+    v[2] = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < r.n; i += 2) {
+        const float4 f = red[r.w0 + i], g = red[r.w0 + i + 1];
+        xy = add2(xy, add2(pack2(f.x, f.y), pack2(g.x, g.y))), v[2] += f.z + g.z;
+    }
+    const float2 f = unpack2(xy);
+    v[0] = f.x, v[1] = f.y;
 }
 
 // The rows of a run on their way: asynchronous copies of 16 bytes to a thread's
 // own slots of shared memory, which no other thread reads, `stages` - 1 rows
-// ahead. A tensor's vector is N = 16 or 32 bytes of a thread's channels.
+// ahead.
 struct Slots {
-    uint4 *base;     // this thread's first
-    int pieces, stages;
+    uint4 *base;  // this thread's first
+    int pieces;   // of 16 bytes a row
     __device__ __forceinline__ uint4 *at(int stage, int piece) const { return base + (stage * pieces + piece) * blockDim.x; }
     template <typename T>
     __device__ __forceinline__ void copy(int stage, int piece, const T *src) const {
@@ -153,40 +194,61 @@ __device__ __forceinline__ void slots_arrived(int ahead) {  // all but the last 
     if (ahead == 1) copies_arrived<1>();
     else copies_arrived<0>();
 }
+// A tensor's row pointer of this thread. The elements from one of its rows to
+// the next, stride times rows a CTA, come with the parameters: in registers
+// they would be two more a tensor.
+struct Steps {
+    int64_t y, res, gate, out, res_out;               // forward
+    int64_t s, dout, dres, dy, ds, dgate;             // gradient (and y, gate)
+};
+template <typename T>
+__device__ __forceinline__ T *row_of(T *p, int64_t st, int64_t row, int c) { return p + row * st + c; }
 
 // A CTA walks a run of one sequence's rows (blockIdx.y; all rows are one where
 // no gate is shared). AHEAD: rows come by asynchronous copies; else (rows that
-// are not wide, or of more than 8192 channels) loads where they are used, and
-// the weights, which do not fit the registers there, too.
+// are not wide, or of more than 8192 channels) they are loaded where the row
+// begins. Weights stay in registers for up to two vectors a thread.
 template <typename TX, typename TR, int NV, bool VEC, bool AHEAD>
-__global__ void __launch_bounds__(512) block_norm_kernel(const BlockNormParams p, int tpr, int stages) {
+__global__ void __launch_bounds__(NV == 1 && VEC ? 128 : 512, NV == 1 && VEC ? 8 : 1) block_norm_kernel(const BlockNormParams p, const Steps step, int tpr, int stages) {
     __shared__ __align__(16) float red[2][2][16];
     extern __shared__ __align__(16) uint4 staged[];
     constexpr int NX = kVecN * sizeof(TX) / 16, NR = kVecN * sizeof(TR) / 16;
-    constexpr bool HOLD = NV <= 2;  // weights in registers
-    const int rpb = blockDim.x / tpr, lr = threadIdx.x / tpr, tid = threadIdx.x - lr * tpr;
-    const int64_t rows = p.shared ? p.gate_rows : p.R, first = (int64_t)blockIdx.y * rows;
-    const int64_t run0 = first + (int64_t)blockIdx.x * p.run, run1 = min(run0 + p.run, first + rows);
+    constexpr bool HOLD = NV <= 2;
+    const int rpb = blockDim.x / tpr, lr = threadIdx.x / tpr, tid = threadIdx.x - lr * tpr, c0 = tid * kVecN, cs = tpr * kVecN;
+    const int rows = p.shared ? p.gate_rows : p.R;
+    const int64_t run0 = (int64_t)blockIdx.y * rows + (int64_t)blockIdx.x * p.run;
+    const int n_rows = min(p.run, rows - (int)blockIdx.x * p.run);
     const bool token = p.act && !p.shared;
-    const Slots slots{staged + threadIdx.x, NV * (NX * (token ? 2 : 1) + NR), stages};
-    auto piece = [&](int i, int k) { return i * (NX * (token ? 2 : 1) + NR) + (k == 0 ? 0 : k == 1 ? NX : NX + NR); };
-    auto channel = [&](int i) { return (i * tpr + tid) * kVecN; };
+    const RowWarps warps(tpr);
+    const int vec_pieces = NX * (token ? 2 : 1) + NR;
+    const Slots slots{staged + threadIdx.x, NV * vec_pieces};
     if (threadIdx.x < 64) (&red[0][0][0])[threadIdx.x] = 0.f;
-    auto fetch = [&](int64_t row, int stage) {
-        if (row < run1) {
+    const TX *y = row_of((const TX *)p.y, p.y_st, run0 + lr, c0);
+    const TX *gate = token ? row_of((const TX *)p.gate, p.g_st, run0 + lr, c0) : nullptr;
+    const TR *res = row_of((const TR *)p.res, p.r_st, run0 + lr, c0);
+    TR *res_out = row_of((TR *)p.res_out, p.ro_st, run0 + lr, c0);
+    TX *out = row_of((TX *)p.out, p.o_st, run0 + lr, c0);
+    auto next_in = [&]() {
+        y += step.y, res += step.res;
+        if (token) gate += step.gate;
+    };
+    int left = n_rows - lr;  // the copies' row exists
+    auto fetch = [&](int stage) {
+        if (left > 0) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = channel(i);
-                if (c >= p.D) continue;
-                slots.copy(stage, piece(i, 0), (const TX *)p.y + row * p.y_st + c);
-                slots.copy(stage, piece(i, 1), (const TR *)p.res + row * p.r_st + c);
-                if (token) slots.copy(stage, piece(i, 2), (const TX *)p.gate + row * p.g_st + c);
+                if (c0 + i * cs >= p.D) continue;
+                slots.copy(stage, i * vec_pieces, y + i * cs);
+                slots.copy(stage, i * vec_pieces + NX, res + i * cs);
+                if (token) slots.copy(stage, i * vec_pieces + NX + NR, gate + i * cs);
             }
         }
         cp_async_commit();
+        left -= rpb;
+        next_in();
     };
     if (AHEAD)
-        for (int g = 0; g + 1 < stages; ++g) fetch(run0 + lr + (int64_t)g * rpb, g);
+        for (int g = 0; g + 1 < stages; ++g) fetch(g);
     // alpha scale post, with the gate's factor where the run shares it; pre
     f32x2 w1[HOLD ? NV : 1][kPairs], w2[HOLD ? NV : 1][kPairs];
     auto weights = [&](int c, int at) {
@@ -203,20 +265,34 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const BlockNormParams p
     if (HOLD) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (channel(i) < p.D) weights(channel(i), i);
+            if (c0 + i * cs < p.D) weights(c0 + i * cs, i);
     }
     const float rd = 1.f / (float)p.D;
     int flip = 0, stage = 0;
     __syncthreads();
-    for (int64_t r0 = run0; r0 < run1; r0 += rpb, flip ^= 1) {
-        const int64_t row = r0 + lr;
-        const bool live = row < run1;
-        int ahead = stage + stages - 1;
-        if (ahead >= stages) ahead -= stages;
-        if (AHEAD) slots_arrived(stages - 2), fetch(row + (int64_t)(stages - 1) * rpb, ahead);
-        auto take_y = [&](f32x2 (&v)[kPairs], int i, int c) {
-            if (AHEAD) slots.get<TX>(v, stage, piece(i, 0));
-            else get<TX, VEC>(v, (const TX *)p.y + row * p.y_st + c, p.D - c);
+#pragma unroll 1
+    for (int k = lr; k - lr < n_rows; k += rpb, flip ^= 1) {
+        const bool live = k < n_rows;
+        if (AHEAD) {
+            const int ahead = stage == 0 ? stages - 1 : stage - 1;
+            slots_arrived(stages - 2), fetch(ahead);
+        }
+        // (not ahead: the whole row is asked for before its first use)
+        uint32_t ny[NV][RowVec<TX, kVecN>::kWords], ng[NV][RowVec<TX, kVecN>::kWords], nr[NV][RowVec<TR, kVecN>::kWords];
+        if (!AHEAD) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int o = i * cs, n = p.D - c0 - o;
+                if (!(live && n > 0)) continue;
+                ld_row<TX, kVecN, VEC>(ny[i], y + o, n);
+                ld_row<TR, kVecN, VEC>(nr[i], res + o, n);
+                if (token) ld_row<TX, kVecN, VEC>(ng[i], gate + o, n);
+            }
+            next_in();
+        }
+        auto take_y = [&](f32x2 (&v)[kPairs], int i) {
+            if (AHEAD) slots.get<TX>(v, stage, i * vec_pieces);
+            else to_pairs<TX>(v, ny[i]);
         };
         f32x2 s[NV][kPairs];
         float inv = 1.f;
@@ -224,60 +300,56 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const BlockNormParams p
             f32x2 sum2 = pack2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = channel(i);
-                if (!(live && c < p.D)) continue;
-                take_y(s[i], i, c);
+                if (!(live && c0 + i * cs < p.D)) continue;
+                take_y(s[i], i);
 #pragma unroll
                 for (int j = 0; j < kPairs; ++j) sum2 = fma2(s[i][j], s[i][j], sum2);
             }
             const float2 su = unpack2(sum2);
-            float v[1] = {su.x + su.y};
-            row_sums<1>(v, red[flip], tpr);
-            inv = rsqrtf(v[0] * rd + p.eps);
+            inv = rsqrtf(row_sum(su.x + su.y, red[flip][0], warps) * rd + p.eps);
         }
         const f32x2 inv2 = pack2(inv, inv);
         f32x2 sum2 = pack2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = channel(i), at = HOLD ? i : 0;
-            if (!(live && c < p.D)) continue;
-            if (!HOLD) weights(c, 0);
+            const int at = HOLD ? i : 0, o = i * cs, n = p.D - c0 - o;
+            if (!(live && n > 0)) continue;
+            if (!HOLD) weights(c0 + o, 0);
             f32x2 g[kPairs], r[kPairs];
-            if (!p.post) take_y(s[i], i, c);
-            if (AHEAD) slots.get<TR>(r, stage, piece(i, 1));
-            else get<TR, VEC>(r, (const TR *)p.res + row * p.r_st + c, p.D - c);
+            if (NV > 2 || !p.post) take_y(s[i], i);  // (four vectors: as stored until here, for the registers)
+            if (AHEAD) slots.get<TR>(r, stage, i * vec_pieces + NX);
+            else to_pairs<TR>(r, nr[i]);
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) s[i][j] = mul2(s[i][j], inv2);
             if (token) {
-                if (AHEAD) slots.get<TX>(g, stage, piece(i, 2));
-                else get<TX, VEC>(g, (const TX *)p.gate + row * p.g_st + c, p.D - c);
+                if (AHEAD) slots.get<TX>(g, stage, i * vec_pieces + NX + NR);
+                else to_pairs<TX>(g, ng[i]);
 #pragma unroll
-                for (int j = 0; j < kPairs; ++j) s[i][j] = mul2(mul2(s[i][j], inv2), gate_of(g[j], p.act));
-            } else {
-#pragma unroll
-                for (int j = 0; j < kPairs; ++j) s[i][j] = mul2(s[i][j], inv2);
+                for (int j = 0; j < kPairs; ++j) s[i][j] = mul2(s[i][j], gate_of(g[j], p.act));
             }
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) s[i][j] = fma2(s[i][j], w1[at][j], r[j]);
-            put<TR, VEC>((TR *)p.res_out + row * p.ro_st + c, s[i], p.D - c);
+            put<TR, VEC>(res_out + o, s[i], n);
+            // (channels past D are zeros: y, residual and weights are loaded so)
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) sum2 = fma2(s[i][j], s[i][j], sum2);
         }
         if (p.pre) {
-            // (channels past D are zeros: y, residual and weights are loaded so)
             const float2 su = unpack2(sum2);
-            float v[1] = {su.x + su.y};
-            row_sums<1>(v, red[flip] + 1, tpr);
-            const float q = rsqrtf(v[0] * rd + p.eps);
+            const float q = rsqrtf(row_sum(su.x + su.y, red[flip][1], warps) * rd + p.eps);
             const f32x2 q2 = pack2(q, q);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = channel(i);
-                if (!(live && c < p.D)) continue;
-                if (!HOLD) weights(c, 0);
+                const int o = i * cs, n = p.D - c0 - o;
+                if (!(live && n > 0)) continue;
+                if (!HOLD) weights(c0 + o, 0);
 #pragma unroll
                 for (int j = 0; j < kPairs; ++j) s[i][j] = mul2(mul2(s[i][j], q2), w2[HOLD ? i : 0][j]);
-                put<TX, VEC>((TX *)p.out + row * p.o_st + c, s[i], p.D - c);
+                put<TX, VEC>(out + o, s[i], n);
             }
+            out += step.out;
         }
+        res_out += step.res_out;
         if (++stage == stages) stage = 0;
     }
 }
@@ -303,201 +375,216 @@ struct NormGrad {
 };
 
 // Runs as in the forward. A thread keeps its channels' sums, in registers with
-// one vector a thread (rows of up to 4096 channels), else in its own slots of
-// shared memory. A row is read from its slots once a phase rather than held.
+// up to two vectors a thread, else in its own slots of shared memory. A row is
+// read from its slots once a phase rather than held.
 template <typename TX, typename TR, int NV, bool VEC, bool AHEAD, bool TOKEN>
-__global__ void __launch_bounds__(512) block_norm_bwd_kernel(const BlockNormBwdParams p, int tpr, int stages) {
-    __shared__ __align__(16) float red[2][4][16];
+__global__ void __launch_bounds__(NV == 1 && VEC && !TOKEN ? 128 : 512, NV == 1 && VEC && !TOKEN ? 5 : 1) block_norm_bwd_kernel(const BlockNormBwdParams p, const Steps step, int tpr, int stages) {
+    __shared__ __align__(16) float4 red3[2][16];
+    __shared__ __align__(16) float red1[2][16];
     extern __shared__ __align__(16) uint4 staged[];
     constexpr int NX = kVecN * sizeof(TX) / 16, NR = kVecN * sizeof(TR) / 16;
-    constexpr bool HOLD = NV == 1;  // sums and weights in registers
-    constexpr int kKept = HOLD ? 0 : NV * 2 * kPairs / 2;  // 16-byte slots a thread of sums
-    const int rpb = blockDim.x / tpr, lr = threadIdx.x / tpr, tid = threadIdx.x - lr * tpr;
-    const int64_t rows = p.shared ? p.gate_rows : p.R, first = (int64_t)blockIdx.y * rows;
-    const int64_t run0 = first + (int64_t)blockIdx.x * p.run, run1 = min(run0 + p.run, first + rows);
+    constexpr bool HOLD = NV <= 2;  // sums and weights in registers
+    constexpr int kKept = HOLD ? 0 : NV * 2 * kPairs / 2, kHeld = HOLD ? NV : 1;  // 16-byte slots a thread of sums
+    const int rpb = blockDim.x / tpr, lr = threadIdx.x / tpr, tid = threadIdx.x - lr * tpr, c0 = tid * kVecN, cs = tpr * kVecN;
+    const int rows = p.shared ? p.gate_rows : p.R;
+    const int64_t run0 = (int64_t)blockIdx.y * rows + (int64_t)blockIdx.x * p.run, row0 = run0 + lr;
+    const int n_rows = min(p.run, rows - (int)blockIdx.x * p.run);
+    const RowWarps warps(tpr);
     // y, dres, then s and dout with pre, then the gate
     const int n_dres = p.dres ? NR : 0, n_pre = p.pre ? NR + NX : 0, vec_pieces = NX + n_dres + n_pre + (TOKEN ? NX : 0);
-    const Slots slots{staged + kKept * blockDim.x + threadIdx.x, NV * vec_pieces, stages};
-    auto sums = [&](int i, int q, int j) -> f32x2 & {
+    const Slots slots{staged + kKept * blockDim.x + threadIdx.x, NV * vec_pieces};
+    auto kept = [&](int i, int q, int j) -> f32x2 & {
         return reinterpret_cast<f32x2 *>(staged)[((i * 2 + q) * kPairs + j) * blockDim.x + threadIdx.x];
     };
-    auto channel = [&](int i) { return (i * tpr + tid) * kVecN; };
     const f32x2 zero = pack2(0.f, 0.f);
-    for (int e = threadIdx.x; e < 128; e += blockDim.x) (&red[0][0][0])[e] = 0.f;
-    auto fetch = [&](int64_t row, int stage) {
-        if (row < run1) {
+    for (int e = threadIdx.x; e < 32; e += blockDim.x) (&red3[0][0])[e] = make_float4(0.f, 0.f, 0.f, 0.f), (&red1[0][0])[e] = 0.f;
+    const TX *y = row_of((const TX *)p.y, p.y_st, row0, c0), *dout = row_of((const TX *)p.dout, p.do_st, row0, c0);
+    const TX *gate = TOKEN ? row_of((const TX *)p.gate, p.g_st, row0, c0) : nullptr;
+    const TR *s = row_of((const TR *)p.s, p.s_st, row0, c0), *dres = row_of((const TR *)p.dres, p.dr_st, row0, c0);
+    TX *dy = row_of((TX *)p.dy, p.dy_st, row0, c0), *dgate = TOKEN ? row_of((TX *)p.dgate, p.dg_st, row0, c0) : nullptr;
+    TR *ds_out = row_of((TR *)p.ds, p.ds_st, row0, c0);
+    auto next_in = [&]() {
+        y += step.y, dres += step.dres;
+        if (p.pre) s += step.s, dout += step.dout;
+        if (TOKEN) gate += step.gate;
+    };
+    int left = n_rows - lr;  // the copies' row exists
+    auto fetch = [&](int stage) {
+        if (left > 0) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = channel(i), o = i * vec_pieces;
-                if (c >= p.D) continue;
-                slots.copy(stage, o, (const TX *)p.y + row * p.y_st + c);
-                if (p.dres) slots.copy(stage, o + NX, (const TR *)p.dres + row * p.dr_st + c);
-                if (p.pre) {
-                    slots.copy(stage, o + NX + n_dres, (const TR *)p.s + row * p.s_st + c);
-                    slots.copy(stage, o + NX + n_dres + NR, (const TX *)p.dout + row * p.do_st + c);
-                }
-                if (TOKEN) slots.copy(stage, o + NX + n_dres + n_pre, (const TX *)p.gate + row * p.g_st + c);
+                const int c = i * cs, o = i * vec_pieces;
+                if (c0 + c >= p.D) continue;
+                slots.copy(stage, o, y + c);
+                if (p.dres) slots.copy(stage, o + NX, dres + c);
+                if (p.pre) slots.copy(stage, o + NX + n_dres, s + c), slots.copy(stage, o + NX + n_dres + NR, dout + c);
+                if (TOKEN) slots.copy(stage, o + NX + n_dres + n_pre, gate + c);
             }
         }
         cp_async_commit();
+        left -= rpb;
+        next_in();
     };
     if (AHEAD)
-        for (int g = 0; g + 1 < stages; ++g) fetch(run0 + lr + (int64_t)g * rpb, g);
-    f32x2 w1[kPairs], w2[kPairs], sa[kPairs], sr[kPairs];  // as in the forward; the sums
-    auto weights = [&](int c) {
+        for (int g = 0; g + 1 < stages; ++g) fetch(g);
+    f32x2 w1[kHeld][kPairs], w2[kHeld][kPairs], sa[kHeld][kPairs], sr[kHeld][kPairs];  // as in the forward; the sums
+    auto weights = [&](int c, int at) {
         const int n = p.D - c;
-        get_factor<VEC>(w1, p.scale, p.post, p.alpha, c, n);
-        get<float, VEC>(w2, p.pre ? p.pre + c : nullptr, n);
+        get_factor<VEC>(w1[at], p.scale, p.post, p.alpha, c, n);
+        get<float, VEC>(w2[at], p.pre ? p.pre + c : nullptr, n);
         if (!TOKEN && p.shared) {
             f32x2 g[kPairs];
             get<TX, VEC>(g, (const TX *)p.gate + (int64_t)blockIdx.y * p.g_st + c, n);
 #pragma unroll
-            for (int j = 0; j < kPairs; ++j) w1[j] = mul2(w1[j], gate_of(g[j], p.act));
+            for (int j = 0; j < kPairs; ++j) w1[at][j] = mul2(w1[at][j], gate_of(g[j], p.act));
         }
     };
 #pragma unroll
-    for (int j = 0; j < kPairs; ++j) w1[j] = w2[j] = sa[j] = sr[j] = zero;
-    if constexpr (HOLD) {
-        if (tid * kVecN < p.D) weights(tid * kVecN);
-    } else {
+    for (int i = 0; i < NV; ++i) {
+        if (HOLD) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+            for (int j = 0; j < kPairs; ++j) w1[i % kHeld][j] = w2[i % kHeld][j] = sa[i % kHeld][j] = sr[i % kHeld][j] = zero;
+            if (c0 + i * cs < p.D) weights(c0 + i * cs, i % kHeld);
+        } else {
 #pragma unroll
-            for (int j = 0; j < kPairs; ++j) sums(i, 0, j) = sums(i, 1, j) = zero;
+            for (int j = 0; j < kPairs; ++j) kept(i, 0, j) = kept(i, 1, j) = zero;
+        }
     }
     const float rd = 1.f / (float)p.D;
     int flip = 0, stage = 0;
     __syncthreads();
-    for (int64_t r0 = run0; r0 < run1; r0 += rpb, flip ^= 1) {
-        const int64_t row = r0 + lr;
-        const bool live = row < run1;
-        int ahead = stage + stages - 1;
-        if (ahead >= stages) ahead -= stages;
-        if (AHEAD) slots_arrived(stages - 2), fetch(row + (int64_t)(stages - 1) * rpb, ahead);
-        auto take_y = [&](f32x2 (&v)[kPairs], int i, int c) {
+#pragma unroll 1
+    for (int k = lr; k - lr < n_rows; k += rpb, flip ^= 1) {
+        const bool live = k < n_rows;
+        if (AHEAD) {
+            const int ahead = stage == 0 ? stages - 1 : stage - 1;
+            slots_arrived(stages - 2), fetch(ahead);
+        }
+        auto take_y = [&](f32x2 (&v)[kPairs], int i, int n) {
             if (AHEAD) slots.get<TX>(v, stage, i * vec_pieces);
-            else get<TX, VEC>(v, (const TX *)p.y + row * p.y_st + c, p.D - c);
+            else get<TX, VEC>(v, y + i * cs, n);
         };
-        auto take_s = [&](f32x2 (&s)[kPairs], f32x2 (&d)[kPairs], int i, int c) {  // and dout
+        auto take_s = [&](f32x2 (&vs)[kPairs], f32x2 (&vd)[kPairs], int i, int n) {  // and dout
             const int o = i * vec_pieces + NX + n_dres;
-            if (AHEAD) slots.get<TR>(s, stage, o), slots.get<TX>(d, stage, o + NR);
-            else get<TR, VEC>(s, (const TR *)p.s + row * p.s_st + c, p.D - c), get<TX, VEC>(d, (const TX *)p.dout + row * p.do_st + c, p.D - c);
+            if (AHEAD) slots.get<TR>(vs, stage, o), slots.get<TX>(vd, stage, o + NR);
+            else get<TR, VEC>(vs, s + i * cs, n), get<TX, VEC>(vd, dout + i * cs, n);
         };
-        float v[3] = {0.f, 0.f, 0.f};  // of s^2, pre dout s, y^2
+        f32x2 a = zero, b = zero, d = zero;  // of s^2, pre dout s, y^2
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = channel(i);
+            const int c = c0 + i * cs, at = HOLD ? i : 0;
             if (!(live && c < p.D)) continue;
-            if (!HOLD) weights(c);
-            f32x2 a = zero, b = zero, d = zero, hs[kPairs], hd[kPairs], hy[kPairs];
+            if (!HOLD) weights(c, 0);
+            f32x2 hs[kPairs], hd[kPairs], hy[kPairs];
             if (p.pre) {
-                take_s(hs, hd, i, c);
+                take_s(hs, hd, i, p.D - c);
 #pragma unroll
-                for (int j = 0; j < kPairs; ++j) a = fma2(hs[j], hs[j], a), b = fma2(mul2(hd[j], w2[j]), hs[j], b);
+                for (int j = 0; j < kPairs; ++j) a = fma2(hs[j], hs[j], a), b = fma2(mul2(hd[j], w2[at][j]), hs[j], b);
             }
             if (p.post) {
-                take_y(hy, i, c);
+                take_y(hy, i, p.D - c);
 #pragma unroll
                 for (int j = 0; j < kPairs; ++j) d = fma2(hy[j], hy[j], d);
             }
-            const float2 fa = unpack2(a), fb = unpack2(b), fd = unpack2(d);
-            v[0] += fa.x + fa.y, v[1] += fb.x + fb.y, v[2] += fd.x + fd.y;
         }
-        row_sums<3>(v, red[flip], tpr);
+        const float2 fa = unpack2(a), fb = unpack2(b), fd = unpack2(d);
+        float v[3] = {fa.x + fa.y, fb.x + fb.y, fd.x + fd.y};
+        row_sums3(v, red3[flip], warps);
         const NormGrad ns(v[0], v[1], rd, p.eps);
         const float inv_y = p.post ? rsqrtf(v[2] * rd + p.eps) : 1.f;
         const f32x2 iy2 = pack2(inv_y, inv_y), is2 = pack2(ns.inv, ns.inv);
-        f32x2 e[kPairs];  // k post f ds, the gradient behind y's norm
-        float ge[1] = {0.f};
+        f32x2 e[kHeld][kPairs], g2 = zero;  // k post f ds, the gradient behind y's norm; of e y
         // The stream's gradient and what follows from it. again: e alone (rows
         // whose e is not held).
-        auto stream = [&](int i, int c, auto form) {
+        auto stream = [&](int i, int n, auto form) {
             constexpr bool again = decltype(form)::value;
-            f32x2 ds[kPairs], hy[kPairs];
+            const int at = HOLD ? i : 0;
+            f32x2 ds[kPairs], hy[kPairs], hg[kPairs];
             if (p.dres) {
                 if (AHEAD) slots.get<TR>(ds, stage, i * vec_pieces + NX);
-                else get<TR, VEC>(ds, (const TR *)p.dres + row * p.dr_st + c, p.D - c);
+                else get<TR, VEC>(ds, dres + i * cs, n);
             } else {
 #pragma unroll
                 for (int j = 0; j < kPairs; ++j) ds[j] = zero;
             }
             if (p.pre) {
                 f32x2 hs[kPairs], hd[kPairs];
-                take_s(hs, hd, i, c);
+                take_s(hs, hd, i, n);
 #pragma unroll
                 for (int j = 0; j < kPairs; ++j) {
-                    ds[j] = ns.at(hs[j], mul2(hd[j], w2[j]), ds[j]);
+                    ds[j] = ns.at(hs[j], mul2(hd[j], w2[at][j]), ds[j]);
                     if (!again) {
                         const f32x2 sn = mul2(hs[j], is2);
-                        if constexpr (HOLD) sr[j] = fma2(hd[j], sn, sr[j]);
-                        else sums(i, 1, j) = fma2(hd[j], sn, sums(i, 1, j));
+                        if constexpr (HOLD) sr[at][j] = fma2(hd[j], sn, sr[at][j]);
+                        else kept(i, 1, j) = fma2(hd[j], sn, kept(i, 1, j));
                     }
                 }
             }
             if (!again) {
-                put<TR, VEC>((TR *)p.ds + row * p.ds_st + c, ds, p.D - c);
-                take_y(hy, i, c);
+                put<TR, VEC>(ds_out + i * cs, ds, n);
+                take_y(hy, i, n);
             }
-            f32x2 hg[kPairs];
             if (TOKEN) {
                 if (AHEAD) slots.get<TX>(hg, stage, i * vec_pieces + NX + n_dres + n_pre);
-                else get<TX, VEC>(hg, (const TX *)p.gate + row * p.g_st + c, p.D - c);
+                else get<TX, VEC>(hg, gate + i * cs, n);
             }
-            f32x2 g2 = zero;
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) {
                 f32x2 dsf = ds[j], df;
                 if (TOKEN) dsf = mul2(ds[j], gate_of(hg[j], p.act, df));
-                e[j] = mul2(dsf, w1[j]);
+                e[at][j] = mul2(dsf, w1[at][j]);
                 if (!again) {
                     const f32x2 yn = mul2(hy[j], iy2);
-                    if (TOKEN) hg[j] = mul2(mul2(mul2(ds[j], w1[j]), yn), df);
-                    g2 = fma2(e[j], hy[j], g2);
-                    if constexpr (HOLD) sa[j] = fma2(dsf, yn, sa[j]);
-                    else sums(i, 0, j) = fma2(dsf, yn, sums(i, 0, j));
+                    if (TOKEN) hg[j] = mul2(mul2(mul2(ds[j], w1[at][j]), yn), df);
+                    g2 = fma2(e[at][j], hy[j], g2);
+                    if constexpr (HOLD) sa[at][j] = fma2(dsf, yn, sa[at][j]);
+                    else kept(i, 0, j) = fma2(dsf, yn, kept(i, 0, j));
                 }
             }
-            if (!again) {
-                const float2 fg = unpack2(g2);
-                ge[0] += fg.x + fg.y;
-                if (TOKEN) put<TX, VEC>((TX *)p.dgate + row * p.dg_st + c, hg, p.D - c);
-            }
+            if (TOKEN && !again) put<TX, VEC>(dgate + i * cs, hg, n);
         };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = channel(i);
+            const int c = c0 + i * cs;
             if (!(live && c < p.D)) continue;
-            if (!HOLD) weights(c);
-            stream(i, c, std::false_type());
+            if (!HOLD) weights(c, 0);
+            stream(i, p.D - c, std::false_type());
         }
-        if (p.post) row_sums<1>(ge, red[flip] + 3, tpr);
-        const NormGrad ny(v[2], ge[0], rd, p.eps);
+        float ge = 0.f;
+        if (p.post) {
+            const float2 fg = unpack2(g2);
+            ge = row_sum(fg.x + fg.y, red1[flip], warps);
+        }
+        const NormGrad ny(v[2], ge, rd, p.eps);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = channel(i);
+            const int c = c0 + i * cs, at = HOLD ? i : 0;
             if (!(live && c < p.D)) continue;
-            if (!HOLD) weights(c), stream(i, c, std::true_type());
+            if (!HOLD) weights(c, 0), stream(i, p.D - c, std::true_type());
             if (p.post) {
                 f32x2 hy[kPairs];
-                take_y(hy, i, c);
+                take_y(hy, i, p.D - c);
 #pragma unroll
-                for (int j = 0; j < kPairs; ++j) e[j] = ny.at(hy[j], e[j], zero);
+                for (int j = 0; j < kPairs; ++j) e[at][j] = ny.at(hy[j], e[at][j], zero);
             }
-            put<TX, VEC>((TX *)p.dy + row * p.dy_st + c, e, p.D - c);
+            put<TX, VEC>(dy + i * cs, e[at], p.D - c);
         }
+        if (!AHEAD) next_in();
+        dy += step.dy, ds_out += step.ds;
+        if (TOKEN) dgate += step.dgate;
         if (++stage == stages) stage = 0;
     }
     float *part = p.part + (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * rpb + lr) * 2 * p.D;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = channel(i);
+        const int c = c0 + i * cs, at = HOLD ? i : 0;
         if (c >= p.D) continue;
         if constexpr (!HOLD) {
 #pragma unroll
-            for (int j = 0; j < kPairs; ++j) sa[j] = sums(i, 0, j), sr[j] = sums(i, 1, j);
+            for (int j = 0; j < kPairs; ++j) sa[0][j] = kept(i, 0, j), sr[0][j] = kept(i, 1, j);
         }
-        put<float, VEC>(part + c, sa, p.D - c);
-        put<float, VEC>(part + p.D + c, sr, p.D - c);
+        put<float, VEC>(part + c, sa[at], p.D - c);
+        put<float, VEC>(part + p.D + c, sr[at], p.D - c);
     }
 }
 
@@ -507,7 +594,7 @@ __device__ __forceinline__ float2 column_sums(const float *in, int64_t parts, in
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     float a = 0.f, b = 0.f;
     if (c < D) {
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t q = y; q < parts; q += Y) a += in[q * 2 * D + c], b += in[q * 2 * D + D + c];
     }
     red[y][x][0] = a, red[y][x][1] = b;
@@ -518,7 +605,7 @@ __device__ __forceinline__ float2 column_sums(const float *in, int64_t parts, in
     }
     return make_float2(a, b);
 }
-constexpr int kSumY = 16;
+constexpr int kSumY = 32;
 // of one sequence (blockIdx.y): its gate row's gradient, and its share of the sums
 template <typename TX>
 __global__ void __launch_bounds__(32 * kSumY) block_norm_sequences_kernel(const BlockNormBwdParams p, int parts) {
@@ -553,8 +640,10 @@ cudaError_t with_smem(K *k, int smem) {
     return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 template <typename TX, typename TR>
-cudaError_t norm_nv(const BlockNormParams &p, cudaStream_t st) {
-    const RowShape s = row_shape(p.D);
+cudaError_t norm_nv(BlockNormParams p, cudaStream_t st) {
+    const RowShape s = row_shape(p);
+    const Runs r = runs_of(p.R, p.gate_rows, s);
+    p.runs = r.n, p.run = r.len;
     const int nt = s.tpr * s.rpb, token = p.act && !p.shared;
     const dim3 grid(p.runs, p.shared ? p.R / p.gate_rows : 1);
     auto run = [&](auto nv, auto vec, auto ahead) -> cudaError_t {
@@ -563,7 +652,8 @@ cudaError_t norm_nv(const BlockNormParams &p, cudaStream_t st) {
         const int stages = stages_for(row, 0, 1024 / nt < 4 ? 1024 / nt : 4), smem = ahead() ? stages * row : 0;
         const cudaError_t e = with_smem(k, smem);
         if (e != cudaSuccess) return e;
-        k<<<grid, nt, smem, st>>>(p, s.tpr, stages);
+        const Steps step{p.y_st * s.rpb, p.r_st * s.rpb, p.g_st * s.rpb, p.o_st * s.rpb, p.ro_st * s.rpb};
+        k<<<grid, nt, smem, st>>>(p, step, s.tpr, stages);
         return cudaGetLastError();
     };
     auto by_vectors = [&](auto vec) {
@@ -574,19 +664,24 @@ cudaError_t norm_nv(const BlockNormParams &p, cudaStream_t st) {
     return p.vec ? by_vectors(std::true_type()) : by_vectors(std::false_type());
 }
 template <typename TX, typename TR>
-cudaError_t norm_bwd_nv(const BlockNormBwdParams &p, cudaStream_t st) {
-    const RowShape s = row_shape(p.D);
+cudaError_t norm_bwd_nv(BlockNormBwdParams p, cudaStream_t st) {
+    const RowShape s = row_shape(p);
+    const Runs runs = runs_of(p.R, p.gate_rows, s);
+    p.runs = runs.n, p.run = runs.len;
     const int nt = s.tpr * s.rpb;
     const bool token = p.act && !p.shared;
     const dim3 grid(p.runs, p.shared ? p.R / p.gate_rows : 1);
     auto run = [&](auto nv, auto vec, auto ahead, auto tok) -> cudaError_t {
         auto *k = block_norm_bwd_kernel<TX, TR, nv(), vec(), ahead(), tok()>;
-        const int kept = nv() > 1 ? nv() * 2 * kPairs * 8 * nt : 0, x = sizeof(TX), r = sizeof(TR);
+        const int kept = nv() > 2 ? nv() * 2 * kPairs * 8 * nt : 0, x = sizeof(TX), r = sizeof(TR);
         const int row = ahead() ? nv() * kVecN * (x * (1 + tok() + (p.pre ? 1 : 0)) + r * ((p.dres ? 1 : 0) + (p.pre ? 1 : 0))) * nt : 0;
-        const int stages = stages_for(row, kept, nv() > 1 ? 1 : nt > 256 ? 1 : 2), smem = kept + (ahead() ? stages * row : 0);
+        const int stages = stages_for(row, kept, nt > 256 ? 1 : nt > 128 ? 2 : 4), smem = kept + (ahead() ? stages * row : 0);
         const cudaError_t e = with_smem(k, smem);
         if (e != cudaSuccess) return e;
-        k<<<grid, nt, smem, st>>>(p, s.tpr, stages);
+        Steps step{};
+        step.y = p.y_st * s.rpb, step.gate = p.g_st * s.rpb, step.s = p.s_st * s.rpb, step.dout = p.do_st * s.rpb;
+        step.dres = p.dr_st * s.rpb, step.dy = p.dy_st * s.rpb, step.ds = p.ds_st * s.rpb, step.dgate = p.dg_st * s.rpb;
+        k<<<grid, nt, smem, st>>>(p, step, s.tpr, stages);
         return cudaGetLastError();
     };
     auto by_gate = [&](auto nv, auto vec, auto ahead) {
@@ -594,7 +689,10 @@ cudaError_t norm_bwd_nv(const BlockNormBwdParams &p, cudaStream_t st) {
     };
     auto by_vectors = [&](auto vec) {
         if (s.nv == 1) return by_gate(std::integral_constant<int, 1>(), vec, vec);
-        if (s.nv == 2) return by_gate(std::integral_constant<int, 2>(), vec, std::false_type());
+        // (two rows of five tensors have to fit: not those of 8192 fp32 channels)
+        const int x = sizeof(TX), r = sizeof(TR), row = kVecN * 2 * nt * (x * (1 + token + (p.pre ? 1 : 0)) + r * ((p.dres ? 1 : 0) + (p.pre ? 1 : 0)));
+        if (s.nv == 2 && 2 * row > 216 * 1024) return by_gate(std::integral_constant<int, 2>(), vec, std::false_type());
+        if (s.nv == 2) return by_gate(std::integral_constant<int, 2>(), vec, vec);
         return by_gate(std::integral_constant<int, 4>(), vec, std::false_type());
     };
     return p.vec ? by_vectors(std::true_type()) : by_vectors(std::false_type());
@@ -608,16 +706,9 @@ cudaError_t launch_block_norm(const BlockNormParams &p, cudaStream_t st) {
     return p.r_bf16 ? norm_nv<float, bf>(p, st) : norm_nv<float, float>(p, st);
 }
 
-// Runs of a sequence's rows: as many CTAs as make 1024 threads a SM, two at least.
-void block_norm_runs(int R, int D, int gate_rows, int *runs, int *run, int64_t *parts) {
-    const RowShape s = row_shape(D);
-    const int rows = gate_rows > 1 ? gate_rows : R, n = gate_rows > 1 ? R / gate_rows : 1;
-    const int nt = s.tpr * s.rpb, ctas = 152 * (nt <= 128 ? 8 : nt <= 256 ? 4 : 2), most = n < ctas ? ctas / n : 1;
-    const int need = (int)(((int64_t)rows + s.rpb - 1) / s.rpb);
-    const int want = need < most ? need : most;
-    *run = want > 0 ? (need + want - 1) / want * s.rpb : s.rpb;
-    *runs = (int)(((int64_t)rows + *run - 1) / *run);
-    *parts = (int64_t)n * *runs * s.rpb;
+int64_t block_norm_parts(int R, int D, int gate_rows) {
+    const int64_t a = runs_of(R, gate_rows, row_shape(D, false)).parts, b = runs_of(R, gate_rows, row_shape(D, true)).parts;
+    return a > b ? a : b;
 }
 
 cudaError_t launch_block_norm_bwd(const BlockNormBwdParams &p, cudaStream_t st) {
@@ -627,16 +718,16 @@ cudaError_t launch_block_norm_bwd(const BlockNormBwdParams &p, cudaStream_t st) 
 }
 
 cudaError_t launch_block_norm_sequences(const BlockNormBwdParams &p, cudaStream_t st) {
-    const RowShape s = row_shape(p.D);
+    const RowShape s = row_shape(p);
+    const int parts = runs_of(p.R, p.gate_rows, s).n * s.rpb;
     const dim3 grid((p.D + 31) / 32, p.R / p.gate_rows);
-    if (p.y_bf16) block_norm_sequences_kernel<__nv_bfloat16><<<grid, 32 * kSumY, 0, st>>>(p, p.runs * s.rpb);
-    else block_norm_sequences_kernel<float><<<grid, 32 * kSumY, 0, st>>>(p, p.runs * s.rpb);
+    if (p.y_bf16) block_norm_sequences_kernel<__nv_bfloat16><<<grid, 32 * kSumY, 0, st>>>(p, parts);
+    else block_norm_sequences_kernel<float><<<grid, 32 * kSumY, 0, st>>>(p, parts);
     return cudaGetLastError();
 }
 
 cudaError_t launch_block_norm_reduce(const BlockNormBwdParams &p, cudaStream_t st) {
-    const RowShape s = row_shape(p.D);
-    const int64_t parts = p.R == 0 ? 0 : p.shared ? p.R / p.gate_rows : (int64_t)p.runs * s.rpb;
+    const int64_t parts = p.R == 0 ? 0 : p.shared ? p.R / p.gate_rows : runs_of(p.R, 1, row_shape(p)).parts;
     block_norm_reduce_kernel<<<(p.D + 31) / 32, 32 * kSumY, 0, st>>>(p, p.shared ? p.part2 : p.part, parts);
     return cudaGetLastError();
 }
