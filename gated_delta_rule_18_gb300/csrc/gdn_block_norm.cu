@@ -588,32 +588,32 @@ __global__ void __launch_bounds__(NV == 1 && VEC && !TOKEN ? 128 : 512, NV == 1 
     }
 }
 
-// Sums over the runs, 32 columns a CTA, Y threads a column, in a fixed order.
-template <int Y>
-__device__ __forceinline__ float2 column_sums(const float *in, int64_t parts, int D, int c, float (*red)[33][2]) {
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+// Sums over the runs in a fixed order: 8 columns a CTA (a row's 32 bytes), 32
+// threads a column.
+constexpr int kSumX = 8, kSumY = 32;
+__device__ __forceinline__ float2 column_sums(const float *in, int64_t parts, int D, int c) {
+    __shared__ float red[kSumY][kSumX][2];
+    const int x = threadIdx.x % kSumX, y = threadIdx.x / kSumX;
     float a = 0.f, b = 0.f;
     if (c < D) {
 #pragma unroll 8
-        for (int64_t q = y; q < parts; q += Y) a += in[q * 2 * D + c], b += in[q * 2 * D + D + c];
+        for (int64_t q = y; q < parts; q += kSumY) a += in[q * 2 * D + c], b += in[q * 2 * D + D + c];
     }
     red[y][x][0] = a, red[y][x][1] = b;
     __syncthreads();
     if (y == 0) {
 #pragma unroll
-        for (int i = 1; i < Y; ++i) a += red[i][x][0], b += red[i][x][1];
+        for (int i = 1; i < kSumY; ++i) a += red[i][x][0], b += red[i][x][1];
     }
     return make_float2(a, b);
 }
-constexpr int kSumY = 32;
 // of one sequence (blockIdx.y): its gate row's gradient, and its share of the sums
 template <typename TX>
-__global__ void __launch_bounds__(32 * kSumY) block_norm_sequences_kernel(const BlockNormBwdParams p, int parts) {
-    __shared__ float red[kSumY][33][2];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31);
+__global__ void __launch_bounds__(kSumX *kSumY) block_norm_sequences_kernel(const BlockNormBwdParams p, int parts) {
+    const int c = blockIdx.x * kSumX + threadIdx.x % kSumX;
     const int64_t q = blockIdx.y;
-    const float2 v = column_sums<kSumY>(p.part + q * parts * 2 * p.D, parts, p.D, c, red);
-    if (threadIdx.x >= 32 || c >= p.D) return;
+    const float2 v = column_sums(p.part + q * parts * 2 * p.D, parts, p.D, c);
+    if (threadIdx.x >= kSumX || c >= p.D) return;
     const float g = (float)((const TX *)p.gate)[q * p.g_st + c];
     f32x2 df2;
     const float2 f = unpack2(gate_of(pack2(g, g), p.act, df2));
@@ -622,11 +622,10 @@ __global__ void __launch_bounds__(32 * kSumY) block_norm_sequences_kernel(const 
     p.part2[q * 2 * p.D + c] = v.x * f.x;
     p.part2[q * 2 * p.D + p.D + c] = v.y;
 }
-__global__ void __launch_bounds__(32 * kSumY) block_norm_reduce_kernel(const BlockNormBwdParams p, const float *in, int64_t parts) {
-    __shared__ float red[kSumY][33][2];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31);
-    const float2 v = column_sums<kSumY>(in, parts, p.D, c, red);
-    if (threadIdx.x >= 32 || c >= p.D) return;
+__global__ void __launch_bounds__(kSumX *kSumY) block_norm_reduce_kernel(const BlockNormBwdParams p, const float *in, int64_t parts) {
+    const int c = blockIdx.x * kSumX + threadIdx.x % kSumX;
+    const float2 v = column_sums(in, parts, p.D, c);
+    if (threadIdx.x >= kSumX || c >= p.D) return;
     if (p.dpost) p.dpost[c] = v.x * (p.alpha * (p.scale ? p.scale[c] : 1.f));
     if (p.dscale) p.dscale[c] = v.x * (p.alpha * (p.post ? p.post[c] : 1.f));
     if (p.dpre) p.dpre[c] = v.y;
@@ -720,15 +719,15 @@ cudaError_t launch_block_norm_bwd(const BlockNormBwdParams &p, cudaStream_t st) 
 cudaError_t launch_block_norm_sequences(const BlockNormBwdParams &p, cudaStream_t st) {
     const RowShape s = row_shape(p);
     const int parts = runs_of(p.R, p.gate_rows, s).n * s.rpb;
-    const dim3 grid((p.D + 31) / 32, p.R / p.gate_rows);
-    if (p.y_bf16) block_norm_sequences_kernel<__nv_bfloat16><<<grid, 32 * kSumY, 0, st>>>(p, parts);
-    else block_norm_sequences_kernel<float><<<grid, 32 * kSumY, 0, st>>>(p, parts);
+    const dim3 grid((p.D + kSumX - 1) / kSumX, p.R / p.gate_rows);
+    if (p.y_bf16) block_norm_sequences_kernel<__nv_bfloat16><<<grid, kSumX * kSumY, 0, st>>>(p, parts);
+    else block_norm_sequences_kernel<float><<<grid, kSumX * kSumY, 0, st>>>(p, parts);
     return cudaGetLastError();
 }
 
 cudaError_t launch_block_norm_reduce(const BlockNormBwdParams &p, cudaStream_t st) {
     const int64_t parts = p.R == 0 ? 0 : p.shared ? p.R / p.gate_rows : runs_of(p.R, 1, row_shape(p)).parts;
-    block_norm_reduce_kernel<<<(p.D + 31) / 32, 32 * kSumY, 0, st>>>(p, p.shared ? p.part2 : p.part, parts);
+    block_norm_reduce_kernel<<<(p.D + kSumX - 1) / kSumX, kSumX * kSumY, 0, st>>>(p, p.shared ? p.part2 : p.part, parts);
     return cudaGetLastError();
 }
 

@@ -686,8 +686,8 @@ gdn_status gdn_ssm_step(const void *x, int64_t x_st, const void *dt,
  *   radians a position. positions: int32 or int64 (pos_bits), strides pos_sb
  *   over B and pos_st over T (0 shares), or NULL: offset + t.
  *   rot even, 2 <= rot <= D <= 512; B T <= 2^31 - 65536.
- *   The angle is kept to 2^-64 of a turn a position: positions up to 2^31 are
- *   as good as small ones, and so are negative ones.
+ *   The angle is reduced in fixed point: any int64 position is as good as its
+ *   frequency's own 53 bits.
  */
 gdn_status gdn_rotary(const void *q, int64_t q_sb, int64_t q_st, int64_t q_sh,
                       int Hq, void *q_out, int64_t qo_sb, int64_t qo_st,
