@@ -52,7 +52,7 @@ struct Piece {
     static constexpr bool kTwo = HALF || !VEC;           // two vectors, else one of whole pairs
     static constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;  // channels of a vector
     static constexpr int P = kTwo ? V : V / 2;               // pairs
-    static constexpr int kHeads = VEC ? 4 : 2;               // heads under way
+    static constexpr int kHeads = VEC ? HALF ? 4 : 8 : 2;    // heads under way
 };
 
 template <typename T, bool VEC, bool HALF>
@@ -179,10 +179,10 @@ cudaError_t rotary(const RotaryParams &p, cudaStream_t st) {
     const int vecs = X::V * (X::kTwo ? 2 : 1);
     const int pieces = p.rot / 2 / X::P + (p.x[0].copy | p.x[1].copy ? (p.D - p.rot + vecs - 1) / vecs : 0);
     const int groups = kThreads / (pieces < kThreads ? pieces : kThreads), heads = p.x[0].H > p.x[1].H ? p.x[0].H : p.x[1].H;
-    // A thread's heads: four, fewer where the tokens alone would not fill the
+    // A thread's heads: as many as are under way, fewer where the tokens alone would not fill the
     // GPU; what the CTA's groups leave takes tokens.
     int lanes = 1;
-    while (lanes < groups && lanes < heads && (lanes * 4 < heads || n_tok * lanes < (int64_t)groups * 608)) lanes *= 2;
+    while (lanes < groups && lanes < heads && (lanes * (VEC ? X::kHeads : 4) < heads || n_tok * lanes < (int64_t)groups * 608)) lanes *= 2;
     if (lanes > groups) lanes = groups;
     int tokens = groups / lanes;
     const int most = 32 * 1024 / (((p.rot / 2 + 3) & ~3) * 8);  // of shared memory
