@@ -13,17 +13,33 @@
 // through distributed shared memory, in one order, and each warp then walks its
 // tokens from its entering state. Inputs are read once, by asynchronous copies
 // one tile ahead, and results repeat bit for bit.
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
 #include "gdn_lru.cuh"
 
 namespace gdn {
 namespace {
 
+// Stages of x, r and i: 16-bit rows are two steps ahead of their use (three CTAs
+// a SM still fit), 32-bit ones one.
+template <typename T>
+constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
+// shared memory: stages of x, r, i by warp, z by warp, the warps' runs, the ranks'
+template <typename T, bool Z>
+struct LruSmem {
+    static constexpr int kStage = 3 * kLruRows, kWarp = kStages<T> * kStage + (Z ? kLruRows : 0);
+    static constexpr int kRuns = kLruWarps * kWarp * (int)sizeof(T), kRanks = kRuns + 2 * kLruWarps * 32 * (int)sizeof(LruRun);
+    static constexpr int bytes(int K) { return kRanks + 2 * LruRanks::places_of(K) * 32 * (int)sizeof(LruRun); }
+};
+
 template <typename T, int HOW, bool PACKED, bool Z>
-__global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams p) {
-    extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ LruRun runs[2][kLruWarps][32];
-    __shared__ LruRanks ranks;
-    constexpr int kRow = kLruCh, kTensor = kLruLen * kRow;  // elements of a warp's rows of one tensor
+__global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams p, const __grid_constant__ LruMaps maps) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ unsigned long long bars[kLruWarps][3], rank_bars[2];
+    using M = LruSmem<T, Z>;
+    constexpr int S = kStages<T>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int K = p.ranks, rank = blockIdx.x % K, line = blockIdx.y;
     const int c0 = (blockIdx.x / K) * kLruCh, c = c0 + 2 * lane, nc = p.C - c;  // nc: channels of the pair that exist
@@ -36,41 +52,41 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
         }
     }
     const int steps = (p.T + K * kLruTile - 1) / (K * kLruTile);
-    const LruRows<T, HOW> x((const T *)p.x + line * p.x_sb + c0, p.x_st), r((const T *)p.r + line * p.r_sb + c0, p.r_st),
-        in((const T *)p.i + line * p.i_sb + c0, p.i_st), z((const T *)p.z + (Z ? line * p.z_sb + c0 : 0), p.z_st);
+    const LruFetch<T, HOW, 3> xri({(const T *)p.x + line * p.x_sb + c0, (const T *)p.r + line * p.r_sb + c0,
+                                   (const T *)p.i + line * p.i_sb + c0}, {p.x_st, p.r_st, p.i_st}, maps.m, c0, line, p.C);
+    const LruFetch<T, HOW, 1> zs({(const T *)p.z + (Z ? line * p.z_sb + c0 : 0)}, {p.z_st}, maps.m + 3, c0, line, p.C);
     T *out = (T *)p.out + (p.out ? line * p.o_sb + c : 0);
-    T *const stage = (T *)smem + warp * (Z ? 4 : 3) * kTensor, *const staged = stage + 2 * lane;
+    T *const stage = (T *)smem + warp * M::kWarp, *const z_stage = stage + S * M::kStage;
+    auto runs = reinterpret_cast<LruRun(*)[kLruWarps][32]>(smem + M::kRuns);
+    const LruRanks ranks{reinterpret_cast<LruRun *>(smem + M::kRanks), rank_bars, K, LruRanks::places_of(K)};
+    if (lane == 0) lru_init_bars(bars[warp], 3);
+    __syncwarp();
     auto first = [&](int n) { return (n * K + rank) * kLruTile + warp * kLruLen; };  // token of step n
-    // two groups of copies a step: x, r and i are free for the next step's once
-    // a and b are formed, z once the outputs are
     auto fetch = [&](int n) {
-        const int t = first(n), rows = p.T - t;
-        if (n < steps && rows > 0) {
-            x.copy(stage, t, rows, p.C - c0), r.copy(stage + kTensor, t, rows, p.C - c0);
-            in.copy(stage + 2 * kTensor, t, rows, p.C - c0);
-        }
-        cp_async_commit();
+        if (n < steps) xri.copy(stage + n % S * M::kStage, first(n), p.T - first(n), smem_u32(&bars[warp][n % S]));
+        else cp_async_commit();
     };
     auto fetch_z = [&](int n) {
-        const int t = first(n), rows = p.T - t;
-        if (Z && n < steps && rows > 0) z.copy(stage + 3 * kTensor, t, rows, p.C - c0);
-        cp_async_commit();
+        if (Z && n < steps) zs.copy(z_stage, first(n), p.T - first(n), smem_u32(&bars[warp][2]));
+        else cp_async_commit();
     };
-    auto get = [&](int k, int j) { return lru_pair(staged + k * kTensor + j * kRow); };  // a pair of x, r, i or z
     fetch(0), fetch_z(0);
     const LruDecay decay(p.lam + c, p.c, nc);
     f32x2 carry = PACKED ? zero : lru_ld_state(p.h0, line, p.C, c, nc);  // the state before the cluster's tiles
     bool lost = false;
     if (K > 1) {
-        ranks.init(K);
+        ranks.init();
         cluster_sync();
     }
+#pragma unroll 1
     for (int n = 0; n < steps; ++n) {
         const int t0 = first(n), len = min(max(p.T - t0, 0), kLruLen), flip = n & 1;
         LruMarks m{0u, 0u};
         if (PACKED) m = lru_marks(p.cu, p.n_seq, p.T, t0);
-        cp_async_wait<1>();
-        __syncwarp();
+        if (S == 2) fetch(n + 1);  // (its place was read a step ago, before z's copies)
+        if (!xri.template wait<S>(smem_u32(&bars[warp][n % S]), n / S & 1)) lost = true;
+        const T *const staged = stage + n % S * M::kStage + 2 * lane;
+        auto get = [&](int k, int j) { return lru_pair(staged + k * kLruRows + j * kLruCh); };  // a pair of x, r or i
         f32x2 a[kLruLen], b[kLruLen];
         LruRun run{one, zero};
         auto gates = [&](auto form) {  // whole: eight tokens, none of which begins a sequence
@@ -93,9 +109,11 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
         };
         if (len == kLruLen && !m.cut) gates(std::true_type());
         else gates(std::false_type());
-        __syncwarp();  // every lane has read what the next copies overwrite
-        fetch(n + 1);
         runs[flip][warp][lane] = run;
+        if (S == 1) {
+            __syncwarp();  // every lane has read what the next copies overwrite
+            fetch(n + 1);
+        }
         __syncthreads();
         f32x2 h = carry;
         if (K > 1) {
@@ -106,12 +124,12 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
                     const LruRun v = runs[flip][w][lane];
                     all.H = lru_apply2<PACKED>(v.A, v.H, all.H), all.A = lru_join<PACKED>(all.A, v.A);
                 }
-                ranks.send(n, K, rank, all);
+                ranks.send(n, rank, all);
             }
-            if (!lost) lost = !ranks.wait(n);
+            if (!lost && !ranks.wait(n)) lost = true;  // (once is enough)
 #pragma unroll 8
-            for (int k = 0; k < (K > 8 ? 16 : 8); ++k) {
-                const LruRun v = ranks.runs[flip][k][lane];
+            for (int k = 0; k < ranks.places; ++k) {
+                const LruRun v = ranks.at(n, k);
                 if (k == rank) h = carry;
                 carry = lru_apply2<PACKED>(v.A, v.H, carry);
             }
@@ -129,11 +147,10 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
                 carry = lru_apply2<PACKED>(v.A, v.H, carry);
             }
         }
-        if (lost) h = carry = pack2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
         if (p.ck && warp == 0 && t0 < p.T)
             lru_st_state(p.ck, (int64_t)line * ((p.T + kLruTile - 1) / kLruTile) + t0 / kLruTile, p.C, c, nc, h);
-        cp_async_wait<1>();
-        __syncwarp();
+        if (Z && !zs.template wait<1>(smem_u32(&bars[warp][2]), n & 1)) lost = true;
+        if (lost) h = carry = pack2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
         T *o = out + (int64_t)t0 * p.o_st;
         auto walk = [&](auto form) {
             constexpr bool whole = decltype(form)::value;
@@ -143,7 +160,7 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
                 h = PACKED && !whole && m.cut >> j & 1 ? b[j] : fma2(a[j], h, b[j]);
                 f32x2 y = h;
                 if (Z) {
-                    const f32x2 v = get(3, j);
+                    const f32x2 v = lru_pair(z_stage + 2 * lane + j * kLruCh);
                     y = mul2(h, mul2(v, sigmoid_2(v)));
                 }
                 if (nc > 0) lru_put<T, HOW>(o, y, nc);
@@ -155,7 +172,7 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
             if (len == kLruLen && !(m.cut | m.fin)) walk(std::true_type());
             else walk(std::false_type());
         }
-        __syncwarp();
+        __syncwarp();  // every lane is through with the stages
         fetch_z(n + 1);
     }
     if (!PACKED && p.h_final && rank == 0 && warp == 0) lru_st_state(p.h_final, line, p.C, c, nc, carry);
@@ -210,7 +227,37 @@ int lru_ranks(int lines, int T, int C) {
     return k == 8 && k < tiles && ctas * 16 <= 304 ? 16 : k;
 }
 
-cudaError_t lru_launch(const void *kernel, int lines, int C, int ranks, int smem, const LruParams &p, cudaStream_t st) {
+bool lru_maps(const LruParams &p, bool gradient, LruMaps *m) {
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    if (!fn || p.T < 1) return false;
+    const int e = p.bf16 ? 2 : 4;
+    int n = 0;
+    auto add = [&](const void *at, int64_t sb, int64_t st) {
+        if (!at) return true;
+        cuuint64_t dims[3] = {(cuuint64_t)p.C, (cuuint64_t)p.T, (cuuint64_t)p.B};
+        // (the stride of a dimension of one is free)
+        cuuint64_t strides[2] = {(cuuint64_t)((p.T > 1 ? st : p.C) * e), (cuuint64_t)((p.B > 1 ? sb : p.C) * e)};
+        for (const cuuint64_t s : strides)
+            if (s == 0 || s % 16 != 0 || s >= 1ull << 40) return false;
+        cuuint32_t box[3] = {kLruCh, kLruLen, 1}, es[3] = {1, 1, 1};
+        return fn(&m->m[n++], p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(at),
+                  dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return add(p.x, p.x_sb, p.x_st) && add(p.r, p.r_sb, p.r_st) && add(p.i, p.i_sb, p.i_st) &&
+           (!gradient || add(p.dout, p.do_sb, p.do_st)) && add(p.z, p.z_sb, p.z_st);
+}
+
+cudaError_t lru_launch(const void *kernel, int lines, int C, int ranks, int smem, const LruParams &p, const LruMaps &m,
+                       cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (ranks > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -223,16 +270,18 @@ cudaError_t lru_launch(const void *kernel, int lines, int C, int ranks, int smem
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = ranks, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
     cfg.attrs = &at, cfg.numAttrs = 1;
-    void *args[] = {const_cast<LruParams *>(&p)};
+    void *args[] = {const_cast<LruParams *>(&p), const_cast<LruMaps *>(&m)};
     e = cudaLaunchKernelExC(&cfg, kernel, args);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 cudaError_t launch_lru(const LruParams &p, cudaStream_t st) {
-    return lru_by_form(p, p.z != nullptr, [&](auto type, auto how, auto packed, auto z) {
+    LruMaps m{};
+    const int how = p.how == kLruWide && !lru_maps(p, false, &m) ? (int)kLruWords : p.how;
+    return lru_by_form(p, how, p.z != nullptr, [&](auto type, auto how, auto packed, auto z) {
         using T = decltype(type);
-        const int smem = (z() ? 4 : 3) * kLruTile * kLruCh * (int)sizeof(T);
-        return lru_launch((const void *)lru_kernel<T, how(), packed(), z()>, p.B, p.C, p.ranks, smem, p, st);
+        const int smem = LruSmem<T, z()>::bytes(p.ranks);
+        return lru_launch((const void *)lru_kernel<T, how(), packed(), z()>, p.B, p.C, p.ranks, smem, p, m, st);
     });
 }
 

@@ -2,6 +2,8 @@
 // channel pair, the marks of a warp's tokens, the joining of runs.
 #pragma once
 
+#include <cuda.h>
+
 #include "gdn_block.cuh"
 #include "gdn_ssm.cuh"
 
@@ -104,31 +106,61 @@ constexpr int kLruRanks = 16;  // most CTAs of a cluster
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The runs of a step's tiles, of the warps here and of the cluster's CTAs. The
-// ranks' are sent by asynchronous stores that count their bytes on the
-// receiver's barrier: no fence, and no wait for a CTA's outputs on their way
-// to memory, as a barrier of the cluster has it. Two steps' places: a CTA
-// sends step n + 2 after it has step n + 1 of all others, and they send that
-// after they have read step n.
+// Waits for a phase of a barrier; false after about half a second. CLUSTER:
+// what other CTAs sent is read next.
+template <bool CLUSTER>
+__device__ __forceinline__ bool lru_wait(uint32_t bar, uint32_t parity) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        uint32_t ok;
+        if (CLUSTER)
+            asm volatile(
+                "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+                " selp.u32 %0, 1, 0, p;\n}"
+                : "=r"(ok)
+                : "r"(bar), "r"(parity)
+                : "memory");
+        else
+            asm volatile(
+                "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+                " selp.u32 %0, 1, 0, p;\n}"
+                : "=r"(ok)
+                : "r"(bar), "r"(parity)
+                : "memory");
+        if (ok) return true;
+        if ((it & 255) == 255) {
+            const uint64_t t = now_ns();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > 500000000ull) return false;
+        }
+    }
+}
+// The runs of the cluster's CTAs in a step. They are sent by asynchronous
+// stores that count their bytes on the receiver's barrier: no fence, and no
+// wait for a CTA's outputs on their way to memory, as a barrier of the cluster
+// has it. Two steps' places: a CTA sends step n + 2 after it has step n + 1 of
+// all others, and they send that after they have read step n.
 struct LruRanks {
-    LruRun runs[2][kLruRanks][32];
-    unsigned long long bar[2];
-    // all threads; then a sync of the cluster. Ranks that are not there change nothing.
-    __device__ __forceinline__ void init(int K) {
-        for (int e = threadIdx.x; e < 2 * kLruRanks * 32; e += 32 * kLruWarps)
-            if (e / 32 % kLruRanks >= K) (&runs[0][0][0])[e] = LruRun{pack2(1.f, 1.f), pack2(0.f, 0.f)};
+    LruRun *runs;  // [2][places][32]
+    unsigned long long *bar;
+    int K, places;  // ranks that are not there change nothing
+    static __host__ __device__ constexpr int places_of(int K) { return K == 1 ? 0 : K <= 8 ? 8 : 16; }
+    __device__ __forceinline__ LruRun &at(int n, int rank) const { return runs[((n & 1) * places + rank) * 32 + (threadIdx.x & 31)]; }
+    // all threads; then a sync of the cluster
+    __device__ __forceinline__ void init() const {
+        for (int e = threadIdx.x; e < 2 * places * 32; e += 32 * kLruWarps)
+            if (e / 32 % places >= K) runs[e] = LruRun{pack2(1.f, 1.f), pack2(0.f, 0.f)};
         if (threadIdx.x == 0) {
             mbar_init(smem_u32(&bar[0]), 1), mbar_init(smem_u32(&bar[1]), 1);
             fence_mbar_init();
         }
     }
     // one warp: this CTA's run of step n to every CTA of the cluster
-    __device__ __forceinline__ void send(int n, int K, int rank, const LruRun &v) {
-        const int flip = n & 1, lane = threadIdx.x & 31;
-        if (lane == 0) arrive_expect_tx(smem_u32(&bar[flip]), K * 32 * (int)sizeof(LruRun));
+    __device__ __forceinline__ void send(int n, int rank, const LruRun &v) const {
+        const uint32_t on = smem_u32(&bar[n & 1]), to = smem_u32(&at(n, rank));
+        if ((threadIdx.x & 31) == 0) arrive_expect_tx(on, K * 32 * (int)sizeof(LruRun));
         __syncwarp();
         const float2 A = unpack2(v.A), H = unpack2(v.H);
-        const uint32_t to = smem_u32(&runs[flip][rank][lane]), on = smem_u32(&bar[flip]);
         for (int k = 0; k < K; ++k)
             asm volatile(
                 "{\n .reg .b32 a, b;\n mapa.shared::cluster.u32 a, %0, %2;\n mapa.shared::cluster.u32 b, %1, %2;\n"
@@ -137,80 +169,103 @@ struct LruRanks {
                 "r"(__float_as_uint(H.y))
                 : "memory");
     }
-    // false after about half a second
-    __device__ __forceinline__ bool wait(int n) const {
-        const uint32_t at = smem_u32(&bar[n & 1]), parity = n >> 1 & 1;
-        uint64_t t0 = 0;
-        for (uint32_t it = 0;; ++it) {
-            uint32_t ok;
-            asm volatile(
-                "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-                " selp.u32 %0, 1, 0, p;\n}"
-                : "=r"(ok)
-                : "r"(at), "r"(parity)
-                : "memory");
-            if (ok) return true;
-            if ((it & 255) == 255) {
-                const uint64_t t = now_ns();
-                if (t0 == 0) t0 = t;
-                else if (t - t0 > 500000000ull) return false;
-            }
-        }
-    }
+    __device__ __forceinline__ bool wait(int n) const { return lru_wait<true>(smem_u32(&bar[n & 1]), n >> 1 & 1); }
 };
 
 // --------------------------------------------------------- staging ----------
-// How a warp's rows of a tensor (kLruLen tokens x kLruCh channels) get into its
-// part of shared memory, which only the warp itself reads: by asynchronous
-// copies of 16 bytes, of 4 (a word of each lane's pair; rows on any word), or
-// through registers (bf16 rows on odd elements).
+// How a warp's rows of its tensors (kLruLen tokens x kLruCh channels each) get
+// into its part of shared memory, which only the warp itself reads: by tensor
+// copies, one lane's (rows on 16 bytes; 16-byte copies by all lanes took a
+// quarter of the forward's instructions, and a bulk copy a row, which a warp's
+// lanes issue one by one, 236 us where all together take 171); by asynchronous
+// copies of a word of each lane's pair (rows on any word); or through registers
+// (bf16 rows on odd elements).
 enum { kLruWide, kLruWords, kLruElements };
-template <typename T, int HOW>
-struct LruRows {
-    static constexpr int VE = 16 / (int)sizeof(T), kRow = kLruCh / VE, kStep = 32 / kRow, kN = kLruLen / kStep;
-    const T *at;   // this lane's first piece of the line's first token
-    int64_t st;
-    // src: the tile's first channel; n: channels that exist from there
-    __device__ __forceinline__ LruRows(const T *src, int64_t st_) : st(st_) {
-        const int lane = threadIdx.x & 31;
-        at = HOW == kLruWide ? src + lane / kRow * st + lane % kRow * VE : src + 2 * lane;
-    }
-    // rows t .. t + rows - 1, rows > 0; n as above. What is past them is zero.
-    __device__ __forceinline__ void copy(T *dst, int t, int rows, int n) const {
-        const int lane = threadIdx.x & 31;
-        const T *p = at + t * st;
-        if constexpr (HOW == kLruWide) {
-            const bool in = lane % kRow * VE < n;
+constexpr int kLruRows = kLruLen * kLruCh;  // elements of a warp's rows of a tensor
+// x, r, i, then z, or dout and z: (B, T, C), boxes of a warp's rows
+struct LruMaps {
+    CUtensorMap m[5];
+};
+__device__ __forceinline__ void lru_tensor_copy(uint32_t dst, const CUtensorMap *m, int c, int t, int line, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(c), "r"(t), "r"(line), "r"(bar)
+        : "memory");
+}
+// N tensors whose rows are copied together. Rows past the line and channels
+// past C hold anything: no lane that exists reads them.
+template <typename T, int HOW, int N>
+struct LruFetch {
+    static constexpr int kHeld = HOW == kLruWide ? 1 : N;
+    const T *at[kHeld];
+    int64_t st[kHeld];
+    const CUtensorMap *maps;  // the tensors', one after another
+    int c0, line, n;          // n: channels that exist from the tile's first, c0
+    // base[k]: tensor k's line at c0
+    __device__ __forceinline__ LruFetch(const T *const (&base)[N], const int64_t (&stride)[N], const CUtensorMap *m, int c, int l, int C)
+        : maps(m), c0(c), line(l), n(C - c) {
 #pragma unroll
-            for (int k = 0; k < kN; ++k) {
-                const bool on = in && lane / kRow + k * kStep < rows;
-                cp_async16(dst + (lane + 32 * k) * VE, on ? p + k * kStep * st : at, on ? 16 : 0);
+        for (int q = 0; q < kHeld; ++q)
+            if (HOW != kLruWide) at[q] = base[q] + 2 * (threadIdx.x & 31), st[q] = stride[q];
+    }
+    // rows t .. t + rows - 1 (none for rows <= 0) into dst[tensor][kLruRows];
+    // `bar` counts them (one phase a call), or the lane's next group of copies
+    __device__ __forceinline__ void copy(T *dst, int t, int rows, uint32_t bar) const {
+        const int lane = threadIdx.x & 31;
+        if constexpr (HOW == kLruWide) {
+            if (lane == 0) {
+                if (rows > 0) {
+                    arrive_expect_tx(bar, N * kLruRows * (int)sizeof(T));  // (whole boxes, zeros outside the tensor)
+#pragma unroll
+                    for (int k = 0; k < N; ++k) lru_tensor_copy(smem_u32(dst + k * kLruRows), maps + k, c0, t, line, bar);
+                } else {
+                    arrive(bar);
+                }
             }
         } else if constexpr (HOW == kLruWords) {
             constexpr int kWords = 2 * (int)sizeof(T) / 4;
 #pragma unroll
-            for (int j = 0; j < kLruLen; ++j)
+            for (int k = 0; k < N; ++k)
 #pragma unroll
-                for (int k = 0; k < kWords; ++k) {
-                    const bool on = j < rows && 2 * lane + (kWords == 2 ? k : 1) < n;
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(
-                                     smem_u32(reinterpret_cast<uint32_t *>(dst + j * kLruCh + 2 * lane) + k)),
-                                 "l"(reinterpret_cast<const uint32_t *>(on ? p + j * st : at) + (on ? k : 0)), "r"(on ? 4 : 0)
-                                 : "memory");
-                }
+                for (int j = 0; j < kLruLen; ++j)
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w)
+                        if (j < rows && 2 * lane + (kWords == 2 ? w : 1) < n)
+                            copy_async<4>(reinterpret_cast<uint32_t *>(dst + k * kLruRows + j * kLruCh + 2 * lane) + w,
+                                          reinterpret_cast<const uint32_t *>(at[k] + (t + j) * st[k]) + w);
+            cp_async_commit();
         } else {
-            uint32_t w[kLruLen];
 #pragma unroll
-            for (int j = 0; j < kLruLen; ++j) {
-                const unsigned short *e = reinterpret_cast<const unsigned short *>(p + j * st);
-                w[j] = j < rows && 2 * lane < n ? e[0] : 0u;
-                if (j < rows && 2 * lane + 1 < n) w[j] |= (uint32_t)e[1] << 16;
+            for (int k = 0; k < N; ++k) {
+                uint32_t w[kLruLen];
+#pragma unroll
+                for (int j = 0; j < kLruLen; ++j) {
+                    const unsigned short *e = reinterpret_cast<const unsigned short *>(at[k] + (int64_t)(t + j) * st[k]);
+                    w[j] = j < rows && 2 * lane < n ? e[0] : 0u;
+                    if (j < rows && 2 * lane + 1 < n) w[j] |= (uint32_t)e[1] << 16;
+                }
+#pragma unroll
+                for (int j = 0; j < kLruLen; ++j)
+                    *reinterpret_cast<uint32_t *>(dst + k * kLruRows + j * kLruCh + 2 * lane) = w[j];
             }
-#pragma unroll
-            for (int j = 0; j < kLruLen; ++j) *reinterpret_cast<uint32_t *>(dst + j * kLruCh + 2 * lane) = w[j];
+            cp_async_commit();
         }
     }
+    // the copy that is followed by LATER others has arrived
+    template <int LATER>
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
+        bool ok = true;
+        if constexpr (HOW == kLruWide) ok = lru_wait<false>(bar, parity);
+        else cp_async_wait<LATER>();
+        __syncwarp();
+        return ok;
+    }
 };
+// the barriers of a warp's stages: one thread of it; then a sync of the CTA
+__device__ __forceinline__ void lru_init_bars(unsigned long long *bars, int n) {
+    for (int k = 0; k < n; ++k) mbar_init(smem_u32(bars + k), 1);
+    fence_mbar_init();
+}
 template <typename T>
 __device__ __forceinline__ f32x2 lru_pair(const T *p) {  // of a staged row
     uint32_t w[RowVec<T, 2>::kWords];
@@ -241,20 +296,24 @@ __device__ __forceinline__ void lru_st_state(float *s, int64_t row, int C, int c
 
 // f(element, how rows are copied, packed batch, with z) for a call's form
 template <class F>
-cudaError_t lru_by_form(const LruParams &p, bool with_z, F &&f) {
+cudaError_t lru_by_form(const LruParams &p, int how, bool with_z, F &&f) {
     const std::true_type yes;
     const std::false_type no;
     auto by_z = [&](auto t, auto h, auto k) { return with_z ? f(t, h, k, yes) : f(t, h, k, no); };
     auto by_cu = [&](auto t, auto h) { return p.cu ? by_z(t, h, yes) : by_z(t, h, no); };
     if (!p.bf16) {
-        if (p.how == kLruWide) return by_cu(float(), std::integral_constant<int, kLruWide>());
+        if (how == kLruWide) return by_cu(float(), std::integral_constant<int, kLruWide>());
         return by_cu(float(), std::integral_constant<int, kLruWords>());
     }
     const __nv_bfloat16 t{};
-    if (p.how == kLruWide) return by_cu(t, std::integral_constant<int, kLruWide>());
-    if (p.how == kLruWords) return by_cu(t, std::integral_constant<int, kLruWords>());
+    if (how == kLruWide) return by_cu(t, std::integral_constant<int, kLruWide>());
+    if (how == kLruWords) return by_cu(t, std::integral_constant<int, kLruWords>());
     return by_cu(t, std::integral_constant<int, kLruElements>());
 }
-cudaError_t lru_launch(const void *kernel, int lines, int C, int ranks, int smem, const LruParams &p, cudaStream_t st);
+// the maps of a call's tensors into m; false where they have none (a stride
+// of zero): its rows are then copied by words
+bool lru_maps(const LruParams &p, bool gradient, LruMaps *m);
+cudaError_t lru_launch(const void *kernel, int lines, int C, int ranks, int smem, const LruParams &p, const LruMaps &m,
+                       cudaStream_t st);
 
 }  // namespace gdn

@@ -16,16 +16,30 @@
 namespace gdn {
 namespace {
 
+// shared memory: two stages of the tensors by warp (one of 32-bit rows, so that
+// two CTAs fit a SM), the warps' runs both ways, the ranks'
+template <typename T>
+constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
+template <typename T, bool Z>
+struct LruBwdSmem {
+    static constexpr int kTensors = Z ? 5 : 4, kStage = kTensors * kLruRows, kWarp = kStages<T> * kStage;
+    static constexpr int kRuns = kLruWarps * kWarp * (int)sizeof(T), kBacks = kRuns + 2 * kLruWarps * 32 * (int)sizeof(LruRun);
+    static constexpr int kRanks = kBacks + 2 * kLruWarps * 32 * 8;
+    static constexpr int bytes(int K) { return kRanks + 2 * LruRanks::places_of(K) * 32 * (int)sizeof(LruRun); }
+};
+
 template <typename T, int HOW, bool PACKED, bool Z>
-__global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruParams p) {
-    extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ LruRun runs[2][kLruWarps][32];  // A, H of a warp's tokens
-    __shared__ f32x2 backs[2][kLruWarps][32];  // what they add to the gradient before them
-    __shared__ LruRanks ranks;
-    constexpr int kRow = kLruCh, kTensor = kLruLen * kRow, kTensors = Z ? 5 : 4;
+__global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruParams p, const __grid_constant__ LruMaps maps) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ unsigned long long bars[kLruWarps][2], rank_bars[2];
+    using M = LruBwdSmem<T, Z>;
+    constexpr int S = kStages<T>, N = M::kTensors;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int K = p.ranks, rank = blockIdx.x % K, line = blockIdx.y;
     const int c0 = (blockIdx.x / K) * kLruCh, c = c0 + 2 * lane, nc = p.C - c;
+    auto runs = reinterpret_cast<LruRun(*)[kLruWarps][32]>(smem + M::kRuns);   // A, H of a warp's tokens
+    auto backs = reinterpret_cast<f32x2(*)[kLruWarps][32]>(smem + M::kBacks);  // what they add to the gradient before them
+    const LruRanks ranks{reinterpret_cast<LruRun *>(smem + M::kRanks), rank_bars, K, LruRanks::places_of(K)};
     const f32x2 one = pack2(1.f, 1.f), zero = pack2(0.f, 0.f), minus = pack2(-1.f, -1.f), half = pack2(0.5f, 0.5f);
     if (PACKED) {
         if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
@@ -35,21 +49,21 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
         }
     }
     const int steps = (p.T + K * kLruTile - 1) / (K * kLruTile), tiles = (p.T + kLruTile - 1) / kLruTile;
-    const LruRows<T, HOW> x((const T *)p.x + line * p.x_sb + c0, p.x_st), r((const T *)p.r + line * p.r_sb + c0, p.r_st),
-        in((const T *)p.i + line * p.i_sb + c0, p.i_st), dout((const T *)p.dout + line * p.do_sb + c0, p.do_st),
-        z((const T *)p.z + (Z ? line * p.z_sb + c0 : 0), p.z_st);
-    constexpr int kStage = kLruWarps * kTensors * kTensor;  // elements of a stage
-    T *const stage = (T *)smem + warp * kTensors * kTensor;
+    const T *bases[5] = {(const T *)p.x + line * p.x_sb + c0, (const T *)p.r + line * p.r_sb + c0, (const T *)p.i + line * p.i_sb + c0,
+                         (const T *)p.dout + line * p.do_sb + c0, (const T *)p.z + (Z ? line * p.z_sb + c0 : 0)};
+    const T *base[N];
+    int64_t stride[N];
+    const int64_t strides[5] = {p.x_st, p.r_st, p.i_st, p.do_st, p.z_st};
+#pragma unroll
+    for (int k = 0; k < N; ++k) base[k] = bases[k], stride[k] = strides[k];
+    const LruFetch<T, HOW, N> rows(base, stride, maps.m, c0, line, p.C);
+    T *const stage = (T *)smem + warp * M::kWarp;
+    if (lane == 0) lru_init_bars(bars[warp], 2);
+    __syncwarp();
     auto first = [&](int n) { return ((steps - 1 - n) * K + rank) * kLruTile + warp * kLruLen; };
     auto fetch = [&](int n) {
-        const int t = n < steps ? first(n) : p.T, rows = p.T - t, nch = p.C - c0;
-        if (rows > 0) {
-            T *s = stage + (n & 1) * kStage;
-            x.copy(s, t, rows, nch), r.copy(s + kTensor, t, rows, nch), in.copy(s + 2 * kTensor, t, rows, nch);
-            dout.copy(s + 3 * kTensor, t, rows, nch);
-            if (Z) z.copy(s + 4 * kTensor, t, rows, nch);
-        }
-        cp_async_commit();
+        if (n < steps) rows.copy(stage + n % S * M::kStage, first(n), p.T - first(n), smem_u32(&bars[warp][n % S]));
+        else cp_async_commit();
     };
     fetch(0);
     const LruDecay decay(p.lam + c, p.c, nc);
@@ -57,20 +71,19 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
     f32x2 carry = PACKED ? zero : lru_ld_state(p.dh_final, line, p.C, c, nc), dlam = zero;
     bool lost = false;
     if (K > 1) {
-        ranks.init(K);
+        ranks.init();
         cluster_sync();
     }
+#pragma unroll 1
     for (int n = 0; n < steps; ++n) {
         const int t0 = first(n), len = min(max(p.T - t0, 0), kLruLen), flip = n & 1, tile = (steps - 1 - n) * K + rank;
         LruMarks m{0u, 0u};
         if (PACKED) m = lru_marks(p.cu, p.n_seq, p.T, t0);
         f32x2 h = tile < tiles ? lru_ld_state(p.ck, (int64_t)line * tiles + tile, p.C, c, nc) : zero;
-        __syncwarp();  // every lane has read what the next copies overwrite
-        fetch(n + 1);
-        cp_async_wait<1>();
-        __syncwarp();
-        const T *staged = stage + flip * kStage + 2 * lane;
-        auto get = [&](int k, int j) { return lru_pair(staged + k * kTensor + j * kRow); };  // of x, r, i, dout, z
+        if (S == 2) fetch(n + 1);  // (its place was read a step ago)
+        if (!rows.template wait<S - 1>(smem_u32(&bars[warp][n % S]), n / S & 1)) lost = true;
+        const T *staged = stage + n % S * M::kStage + 2 * lane;
+        auto get = [&](int k, int j) { return lru_pair(staged + k * kLruRows + j * kLruCh); };  // of x, r, i, dout, z
         const bool all_inside = len == kLruLen && !(m.cut | m.fin);
         f32x2 a[kLruLen], b[kLruLen], back = zero;
         LruRun run{one, zero};
@@ -117,7 +130,7 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
                     const f32x2 A = runs[flip][w][lane].A;
                     all.H = lru_apply2<PACKED>(A, backs[flip][w][lane], all.H), all.A = lru_join<PACKED>(all.A, A);
                 }
-                ranks.send(n, K, rank, all);
+                ranks.send(n, rank, all);
             }
         }
         // the state before this warp's tokens
@@ -132,10 +145,10 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
         for (int j = 0; j < kLruLen; ++j)  // b becomes h (it stays where tokens end)
             h = b[j] = PACKED && m.cut >> j & 1 ? b[j] : fma2(a[j], h, b[j]);
         if (K > 1) {
-            if (!lost) lost = !ranks.wait(n);
+            if (!lost && !ranks.wait(n)) lost = true;  // (once is enough)
 #pragma unroll 8
-            for (int k = K > 8 ? 15 : 7; k >= 0; --k) {
-                const LruRun v = ranks.runs[flip][k][lane];
+            for (int k = ranks.places - 1; k >= 0; --k) {
+                const LruRun v = ranks.at(n, k);
                 if (k == rank) gm = carry;
                 carry = lru_apply2<PACKED>(v.A, v.H, carry);
             }
@@ -193,6 +206,8 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
         };
         if (all_inside) walk(std::true_type());
         else walk(std::false_type());
+        __syncwarp();  // every lane is through with the stage
+        if (S == 1) fetch(n + 1);
     }
     if (!PACKED && p.dh0 && rank == 0 && warp == 0) lru_st_state(p.dh0, line, p.C, c, nc, carry);
     // the channels' sums over the warps, in one order
@@ -218,10 +233,12 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
 }  // namespace
 
 cudaError_t launch_lru_bwd(const LruParams &p, cudaStream_t st) {
-    return lru_by_form(p, p.z != nullptr, [&](auto type, auto how, auto packed, auto z) {
+    LruMaps m{};
+    const int how = p.how == kLruWide && !lru_maps(p, true, &m) ? (int)kLruWords : p.how;
+    return lru_by_form(p, how, p.z != nullptr, [&](auto type, auto how, auto packed, auto z) {
         using T = decltype(type);
-        const int smem = 2 * (z() ? 5 : 4) * kLruTile * kLruCh * (int)sizeof(T);
-        return lru_launch((const void *)lru_bwd_kernel<T, how(), packed(), z()>, p.B, p.C, p.ranks, smem, p, st);
+        const int smem = LruBwdSmem<T, z()>::bytes(p.ranks);
+        return lru_launch((const void *)lru_bwd_kernel<T, how(), packed(), z()>, p.B, p.C, p.ranks, smem, p, m, st);
     });
 }
 
