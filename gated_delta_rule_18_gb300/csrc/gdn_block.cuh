@@ -80,6 +80,7 @@ struct LruParams {
     int B, T, C, bf16;
     int how;    // rows of all activations lie on 16 bytes (0), on words in pairs (1) or anywhere (2)
     int ranks;  // CTAs of a cluster, which take a line's tiles in turn
+    int warps;  // of a CTA (the forward over wide rows): 4 or 8
     int *err;
     // gradient; activations' gradients contiguous in x's type
     const void *dout;
@@ -89,7 +90,11 @@ struct LruParams {
     float *part;  // workspace: partial sums of dlam, (B ranks, C)
     float *dlam, *dh0;
 };
-int lru_ranks(int lines, int T, int C);
+struct LruShape {
+    int ranks, warps;
+};
+LruShape lru_shape(int lines, int T, int C, bool bf16, bool wide);
+int lru_bwd_ranks(int lines, int T, int C, bool bf16);
 cudaError_t launch_lru(const LruParams &p, cudaStream_t st);
 cudaError_t launch_lru_bwd(const LruParams &p, cudaStream_t st);
 struct LruStepParams {

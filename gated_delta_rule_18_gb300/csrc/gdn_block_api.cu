@@ -72,7 +72,8 @@ LruWs lru_bwd_ws(int B, int T, int C, bool saved) {
     LruWs L;
     L.ck = kAlign;
     L.part = align_up(L.ck + (saved ? 0 : (size_t)B * ((T + kLruTile - 1) / kLruTile) * C * 4));
-    L.total = align_up(L.part + (size_t)B * lru_ranks(B, T, C) * C * 4);
+    const int a = lru_bwd_ranks(B, T, C, false), b = lru_bwd_ranks(B, T, C, true);
+    L.total = align_up(L.part + (size_t)B * (a > b ? a : b) * C * 4);
     return L;
 }
 
@@ -244,7 +245,7 @@ gdn_status lru_setup(const void *x, int64_t x_sb, int64_t x_st, const void *r, i
     p = LruParams{};
     p.x = x, p.x_sb = x_sb, p.x_st = x_st, p.r = r, p.r_sb = r_sb, p.r_st = r_st, p.i = i, p.i_sb = i_sb, p.i_st = i_st;
     p.lam = lam, p.z = z, p.z_sb = z_sb, p.z_st = z_st, p.c = c, p.h0 = h0, p.cu = cu, p.n_seq = n_seq;
-    p.B = B, p.T = T, p.C = C, p.bf16 = dtype == GDN_BF16, p.ranks = lru_ranks(B, T, C);
+    p.B = B, p.T = T, p.C = C, p.bf16 = dtype == GDN_BF16;
     return GDN_OK;
 }
 }  // namespace
@@ -275,6 +276,8 @@ gdn_status gdn_lru_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
     if (T == 0 && !h_final && !cu_seqlens) return GDN_OK;
     p.out = out, p.o_sb = out_sb, p.o_st = out_st, p.h_final = h_final, p.ck = checkpoints;
     p.how = rows.how(C, dtype);
+    const LruShape shape = lru_shape(B, T, C, p.bf16, p.how == 0);
+    p.ranks = shape.ranks, p.warps = shape.warps;
     p.err = cu_seqlens ? static_cast<int *>(workspace) : nullptr;
     return cuda_status(launch(KLru, stream, [&] { return launch_lru(p, stream); }));
 }
@@ -318,11 +321,14 @@ gdn_status gdn_lru_bwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
         p.ck = reinterpret_cast<float *>(ws + L.ck);
         LruParams f = p;
         f.z = nullptr;
+        const LruShape shape = lru_shape(B, T, C, p.bf16, p.how == 0);
+        f.ranks = shape.ranks, f.warps = shape.warps;
         e = launch(KLru, stream, [&] { return launch_lru(f, stream); });
     }
     p.dout = dout, p.do_sb = dout_sb, p.do_st = dout_st, p.dh_final = dh_final;
     p.dx = dx, p.dr = dr, p.di = di, p.dz = dz, p.dlam = dlam, p.dh0 = dh0;
     p.part = reinterpret_cast<float *>(ws + L.part);
+    p.ranks = lru_bwd_ranks(B, T, C, p.bf16);
     if (e == cudaSuccess) e = launch(KLruBwd, stream, [&] { return launch_lru_bwd(p, stream); });
     if (e == cudaSuccess)
         e = launch(KColSum, stream, [&] { return launch_col_sum(p.part, C, B * p.ranks, C, dlam, 0, nullptr, stream); });

@@ -22,24 +22,25 @@
 namespace gdn {
 namespace {
 
-// Stages of x, r and i: 16-bit rows are two steps ahead of their use (three CTAs
-// a SM still fit), 32-bit ones one.
-template <typename T>
-constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
-// shared memory: stages of x, r, i by warp, z by warp, the warps' runs, the ranks'
-template <typename T, bool Z>
+// A warp's tokens. With eight what a warp does once a tile (waits, joins,
+// addresses) was a fifth of its instructions: 160 us for 131 (4 x 4096 tokens of
+// 4096 channels, bf16).
+constexpr int L = 16;
+
+// shared memory: a stage of x, r, i and one of z by warp, the warps' runs, the ranks'
+template <typename T, bool Z, int W>
 struct LruSmem {
-    static constexpr int kStage = 3 * kLruRows, kWarp = kStages<T> * kStage + (Z ? kLruRows : 0);
-    static constexpr int kRuns = kLruWarps * kWarp * (int)sizeof(T), kRanks = kRuns + 2 * kLruWarps * 32 * (int)sizeof(LruRun);
+    static constexpr int kRows = L * kLruCh, kWarp = (Z ? 4 : 3) * kRows;
+    static constexpr int kRuns = W * kWarp * (int)sizeof(T), kRanks = kRuns + 2 * W * 32 * (int)sizeof(LruRun);
     static constexpr int bytes(int K) { return kRanks + 2 * LruRanks::places_of(K) * 32 * (int)sizeof(LruRun); }
 };
 
-template <typename T, int HOW, bool PACKED, bool Z>
-__global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams p, const __grid_constant__ LruMaps maps) {
+template <typename T, int HOW, bool PACKED, bool Z, int W>
+__global__ void __launch_bounds__(32 * W, 16 / W) lru_kernel(const LruParams p, const __grid_constant__ LruMaps maps) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ unsigned long long bars[kLruWarps][3], rank_bars[2];
-    using M = LruSmem<T, Z>;
-    constexpr int S = kStages<T>;
+    __shared__ unsigned long long bars[W][2], rank_bars[2];
+    using M = LruSmem<T, Z, W>;
+    constexpr int kTile = W * L;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int K = p.ranks, rank = blockIdx.x % K, line = blockIdx.y;
     const int c0 = (blockIdx.x / K) * kLruCh, c = c0 + 2 * lane, nc = p.C - c;  // nc: channels of the pair that exist
@@ -47,27 +48,27 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
     if (PACKED) {
         if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
         if (p.h_final && rank == 0) {  // sequences without tokens keep their states
-            for (int s = warp; s < p.n_seq; s += kLruWarps)
+            for (int s = warp; s < p.n_seq; s += W)
                 if (p.cu[s + 1] <= p.cu[s]) lru_st_state(p.h_final, s, p.C, c, nc, lru_ld_state(p.h0, s, p.C, c, nc));
         }
     }
-    const int steps = (p.T + K * kLruTile - 1) / (K * kLruTile);
-    const LruFetch<T, HOW, 3> xri({(const T *)p.x + line * p.x_sb + c0, (const T *)p.r + line * p.r_sb + c0,
+    const int steps = (p.T + K * kTile - 1) / (K * kTile);
+    const LruFetch<T, HOW, 3, L> xri({(const T *)p.x + line * p.x_sb + c0, (const T *)p.r + line * p.r_sb + c0,
                                    (const T *)p.i + line * p.i_sb + c0}, {p.x_st, p.r_st, p.i_st}, maps.m, c0, line, p.C);
-    const LruFetch<T, HOW, 1> zs({(const T *)p.z + (Z ? line * p.z_sb + c0 : 0)}, {p.z_st}, maps.m + 3, c0, line, p.C);
+    const LruFetch<T, HOW, 1, L> zs({(const T *)p.z + (Z ? line * p.z_sb + c0 : 0)}, {p.z_st}, maps.m + 3, c0, line, p.C);
     T *out = (T *)p.out + (p.out ? line * p.o_sb + c : 0);
-    T *const stage = (T *)smem + warp * M::kWarp, *const z_stage = stage + S * M::kStage;
-    auto runs = reinterpret_cast<LruRun(*)[kLruWarps][32]>(smem + M::kRuns);
+    T *const stage = (T *)smem + warp * M::kWarp, *const z_stage = stage + 3 * M::kRows;
+    auto runs = reinterpret_cast<LruRun(*)[W][32]>(smem + M::kRuns);
     const LruRanks ranks{reinterpret_cast<LruRun *>(smem + M::kRanks), rank_bars, K, LruRanks::places_of(K)};
-    if (lane == 0) lru_init_bars(bars[warp], 3);
+    if (lane == 0) lru_init_bars(bars[warp], 2);
     __syncwarp();
-    auto first = [&](int n) { return (n * K + rank) * kLruTile + warp * kLruLen; };  // token of step n
+    auto first = [&](int n) { return (n * K + rank) * kTile + warp * L; };  // token of step n
     auto fetch = [&](int n) {
-        if (n < steps) xri.copy(stage + n % S * M::kStage, first(n), p.T - first(n), smem_u32(&bars[warp][n % S]));
+        if (n < steps) xri.copy(stage, first(n), p.T - first(n), smem_u32(&bars[warp][0]));
         else cp_async_commit();
     };
     auto fetch_z = [&](int n) {
-        if (Z && n < steps) zs.copy(z_stage, first(n), p.T - first(n), smem_u32(&bars[warp][2]));
+        if (Z && n < steps) zs.copy(z_stage, first(n), p.T - first(n), smem_u32(&bars[warp][1]));
         else cp_async_commit();
     };
     fetch(0), fetch_z(0);
@@ -80,19 +81,17 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
     }
 #pragma unroll 1
     for (int n = 0; n < steps; ++n) {
-        const int t0 = first(n), len = min(max(p.T - t0, 0), kLruLen), flip = n & 1;
+        const int t0 = first(n), len = min(max(p.T - t0, 0), L), flip = n & 1;
         LruMarks m{0u, 0u};
-        if (PACKED) m = lru_marks(p.cu, p.n_seq, p.T, t0);
-        if (S == 2) fetch(n + 1);  // (its place was read a step ago, before z's copies)
-        if (!xri.template wait<S>(smem_u32(&bars[warp][n % S]), n / S & 1)) lost = true;
-        const T *const staged = stage + n % S * M::kStage + 2 * lane;
-        auto get = [&](int k, int j) { return lru_pair(staged + k * kLruRows + j * kLruCh); };  // a pair of x, r or i
-        f32x2 a[kLruLen], b[kLruLen];
+        if (PACKED) m = lru_marks<L>(p.cu, p.n_seq, p.T, t0);
+        if (!xri.template wait<1>(smem_u32(&bars[warp][0]), n & 1)) lost = true;
+        auto get = [&](int k, int j) { return lru_pair(stage + 2 * lane + k * M::kRows + j * kLruCh); };  // a pair of x, r or i
+        f32x2 a[L], b[L];
         LruRun run{one, zero};
-        auto gates = [&](auto form) {  // whole: eight tokens, none of which begins a sequence
+        auto gates = [&](auto form) {  // whole: all tokens are there, none begins a sequence
             constexpr bool whole = decltype(form)::value;
 #pragma unroll
-            for (int j = 0; j < kLruLen; ++j) {
+            for (int j = 0; j < L; ++j) {
                 if (!whole && j >= len) {
                     a[j] = one, b[j] = zero;
                     continue;
@@ -107,20 +106,18 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
                 }
             }
         };
-        if (len == kLruLen && !m.cut) gates(std::true_type());
+        if (len == L && !m.cut) gates(std::true_type());
         else gates(std::false_type());
         runs[flip][warp][lane] = run;
-        if (S == 1) {
-            __syncwarp();  // every lane has read what the next copies overwrite
-            fetch(n + 1);
-        }
+        __syncwarp();  // every lane has read what the next copies overwrite
+        fetch(n + 1);
         __syncthreads();
         f32x2 h = carry;
         if (K > 1) {
             if (warp == 0) {
                 LruRun all = run;
 #pragma unroll
-                for (int w = 1; w < kLruWarps; ++w) {
+                for (int w = 1; w < W; ++w) {
                     const LruRun v = runs[flip][w][lane];
                     all.H = lru_apply2<PACKED>(v.A, v.H, all.H), all.A = lru_join<PACKED>(all.A, v.A);
                 }
@@ -134,28 +131,28 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
                 carry = lru_apply2<PACKED>(v.A, v.H, carry);
             }
 #pragma unroll
-            for (int w = 0; w < kLruWarps - 1; ++w) {
+            for (int w = 0; w < W - 1; ++w) {
                 if (w >= warp) break;
                 const LruRun v = runs[flip][w][lane];
                 h = lru_apply2<PACKED>(v.A, v.H, h);
             }
         } else {
 #pragma unroll
-            for (int w = 0; w < kLruWarps; ++w) {
+            for (int w = 0; w < W; ++w) {
                 const LruRun v = runs[flip][w][lane];
                 if (w == warp) h = carry;
                 carry = lru_apply2<PACKED>(v.A, v.H, carry);
             }
         }
-        if (p.ck && warp == 0 && t0 < p.T)
+        if (p.ck && warp * L % kLruTile == 0 && t0 < p.T)
             lru_st_state(p.ck, (int64_t)line * ((p.T + kLruTile - 1) / kLruTile) + t0 / kLruTile, p.C, c, nc, h);
-        if (Z && !zs.template wait<1>(smem_u32(&bars[warp][2]), n & 1)) lost = true;
+        if (Z && !zs.template wait<1>(smem_u32(&bars[warp][1]), n & 1)) lost = true;
         if (lost) h = carry = pack2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
         T *o = out + (int64_t)t0 * p.o_st;
         auto walk = [&](auto form) {
             constexpr bool whole = decltype(form)::value;
 #pragma unroll
-            for (int j = 0; j < kLruLen; ++j, o += p.o_st) {
+            for (int j = 0; j < L; ++j, o += p.o_st) {
                 if (!whole && j >= len) break;
                 h = PACKED && !whole && m.cut >> j & 1 ? b[j] : fma2(a[j], h, b[j]);
                 f32x2 y = h;
@@ -169,7 +166,7 @@ __global__ void __launch_bounds__(32 * kLruWarps, 3) lru_kernel(const LruParams 
             }
         };
         if (p.out) {
-            if (len == kLruLen && !(m.cut | m.fin)) walk(std::true_type());
+            if (len == L && !(m.cut | m.fin)) walk(std::true_type());
             else walk(std::false_type());
         }
         __syncwarp();  // every lane is through with the stages
@@ -213,21 +210,37 @@ __global__ void __launch_bounds__(128) lru_step_kernel(const LruStepParams p) {
 
 }  // namespace
 
-// CTAs of a cluster: a line's tiles side by side, up to eight, while all lines
-// have fewer than four CTAs a SM and are long enough; sixteen only where that
-// leaves two a SM (clusters of sixteen fit an SM group badly). Forward, bf16,
-// with z: 4 x 4096 tokens of 4096 channels 180, 191, 171, 187, 246 us for 1, 2,
-// 4, 8, 16; 32768 tokens of 1024 channels 885, 543, 277, 200, 152; fp32, 5003
-// tokens of 1792 channels 148, 93, 56, 42, 50.
-int lru_ranks(int lines, int T, int C) {
-    const int64_t ctas = (int64_t)lines * ((C + kLruCh - 1) / kLruCh);
-    const int tiles = (T + kLruTile - 1) / kLruTile;
-    int k = 1;
-    while (k < 8 && k < tiles && ctas * k < 608) k *= 2;
-    return k == 8 && k < tiles && ctas * 16 <= 304 ? 16 : k;
+// CTAs of a cluster, which take a line's tiles side by side, and warps of a CTA.
+// Where the lines' channel tiles alone are more than the SMs, four CTAs a line
+// in bf16 even the SMs' loads out (4 x 4096 tokens of 4096 channels, 1, 2, 4, 8:
+// 160, 148, 138, 144 us) and one is best in fp32, which HBM bounds (210, 216,
+// 224, 235). With fewer, tiles of 128 tokens and as many CTAs as make 256, up to
+// twelve a line (16 tiles of 32768 tokens with 8, 12, 16: 148, 111, 130 us;
+// tiles of 64 tokens with 16: 128).
+LruShape lru_shape(int lines, int T, int C, bool bf16, bool wide) {
+    const int64_t tiles = (int64_t)lines * ((C + kLruCh - 1) / kLruCh);
+    LruShape s{1, 4};
+    if (tiles >= 192) {
+        s.ranks = !bf16 || tiles >= 2432 ? 1 : tiles >= 1216 ? 2 : 4;
+    } else {
+        const int most = wide ? 12 : 16, all = wide ? 256 : 512;
+        s.warps = wide && T > 64 ? 8 : 4;
+        s.ranks = (int)(tiles * most <= all ? most : all / tiles);
+        if (wide && s.ranks > 8 && s.ranks < most) s.ranks = 8;  // (larger clusters fit an SM group badly)
+    }
+    const int steps = (T + s.warps * L - 1) / (s.warps * L);
+    if (s.ranks > steps) s.ranks = steps > 0 ? steps : 1;
+    return s;
+}
+// of the gradient: eight warps of eight tokens
+int lru_bwd_ranks(int lines, int T, int C, bool bf16) {
+    const int64_t tiles = (int64_t)lines * ((C + kLruCh - 1) / kLruCh);
+    int k = tiles >= 192 ? !bf16 || tiles >= 2432 ? 1 : tiles >= 1216 ? 2 : 4 : (int)(tiles * 12 <= 256 ? 12 : 256 / tiles);
+    const int steps = (T + kLruTile - 1) / kLruTile;
+    return k > steps ? steps > 0 ? steps : 1 : k;
 }
 
-bool lru_maps(const LruParams &p, bool gradient, LruMaps *m) {
+bool lru_maps(const LruParams &p, bool gradient, int len, LruMaps *m) {
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     std::call_once(once, [] {
@@ -247,7 +260,7 @@ bool lru_maps(const LruParams &p, bool gradient, LruMaps *m) {
         cuuint64_t strides[2] = {(cuuint64_t)((p.T > 1 ? st : p.C) * e), (cuuint64_t)((p.B > 1 ? sb : p.C) * e)};
         for (const cuuint64_t s : strides)
             if (s == 0 || s % 16 != 0 || s >= 1ull << 40) return false;
-        cuuint32_t box[3] = {kLruCh, kLruLen, 1}, es[3] = {1, 1, 1};
+        cuuint32_t box[3] = {kLruCh, (cuuint32_t)len, 1}, es[3] = {1, 1, 1};
         return fn(&m->m[n++], p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(at),
                   dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -256,19 +269,17 @@ bool lru_maps(const LruParams &p, bool gradient, LruMaps *m) {
            (!gradient || add(p.dout, p.do_sb, p.do_st)) && add(p.z, p.z_sb, p.z_st);
 }
 
-cudaError_t lru_launch(const void *kernel, int lines, int C, int ranks, int smem, const LruParams &p, const LruMaps &m,
-                       cudaStream_t st) {
+cudaError_t lru_launch(const void *kernel, int warps, int smem, const LruParams &p, const LruMaps &m, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (ranks > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && p.ranks > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((C + kLruCh - 1) / kLruCh * ranks, lines);
-    cfg.blockDim = dim3(32 * kLruWarps);
+    cfg.gridDim = dim3((p.C + kLruCh - 1) / kLruCh * p.ranks, p.B);
+    cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = smem, cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = ranks, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+    at.val.clusterDim.x = p.ranks, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
     cfg.attrs = &at, cfg.numAttrs = 1;
     void *args[] = {const_cast<LruParams *>(&p), const_cast<LruMaps *>(&m)};
     e = cudaLaunchKernelExC(&cfg, kernel, args);
@@ -277,11 +288,16 @@ cudaError_t lru_launch(const void *kernel, int lines, int C, int ranks, int smem
 
 cudaError_t launch_lru(const LruParams &p, cudaStream_t st) {
     LruMaps m{};
-    const int how = p.how == kLruWide && !lru_maps(p, false, &m) ? (int)kLruWords : p.how;
+    const int how = p.how == kLruWide && !lru_maps(p, false, L, &m) ? (int)kLruWords : p.how;
     return lru_by_form(p, how, p.z != nullptr, [&](auto type, auto how, auto packed, auto z) {
         using T = decltype(type);
-        const int smem = LruSmem<T, z()>::bytes(p.ranks);
-        return lru_launch((const void *)lru_kernel<T, how(), packed(), z()>, p.B, p.C, p.ranks, smem, p, m, st);
+        auto run = [&](auto w) {
+            return lru_launch((const void *)lru_kernel<T, how(), packed(), z(), w()>, w(), LruSmem<T, z(), w()>::bytes(p.ranks), p, m, st);
+        };
+        if constexpr (how() == kLruWide) {
+            if (p.warps == 8) return run(std::integral_constant<int, 8>());
+        }
+        return run(std::integral_constant<int, 4>());
     });
 }
 

@@ -11,9 +11,9 @@
 
 namespace gdn {
 
-constexpr int kLruWarps = 8, kLruLen = 8;  // a tile: eight warps of eight tokens
-constexpr int kLruCh = 64;                 // channels a CTA, two a lane
-static_assert(kLruWarps * kLruLen == kLruTile, "a CTA's tile");
+// A CTA's tile: W warps of L tokens, 64 channels, two a lane; saved states lie
+// where warps begin.
+constexpr int kLruCh = 64;
 
 // 1 - a^2 = 1 - exp(-y) for y >= 0: by the series where the difference cancels
 // (y < 1/8: the first term left out is y^5 / 720 of the value, 4e-8). In
@@ -24,6 +24,10 @@ __device__ __forceinline__ float one_minus_square(float a, float y) {
     s = fmaf(s, y, -0.5f);
     s = fmaf(s, y, 1.f);
     return y < 0.125f ? s * y : fmaf(-a, a, 1.f);
+}
+__device__ __forceinline__ f32x2 one_minus_square2(f32x2 a, f32x2 y) {
+    const float2 f = unpack2(a), v = unpack2(y);
+    return pack2(one_minus_square(f.x, v.x), one_minus_square(f.y, v.y));
 }
 __device__ __forceinline__ f32x2 sqrt_2(f32x2 x) {
     float2 v = unpack2(x);
@@ -53,25 +57,25 @@ struct LruGate {
     __device__ __forceinline__ LruGate(f32x2 r, f32x2 i, const LruDecay &d) {
         gr = sigmoid_2(r), gi = sigmoid_2(i);
         u2 = mul2(d.twice, gr), a = ex2_2(mul2(d.base, gr));
-        const float2 y = unpack2(u2), f = unpack2(a);
-        q = pack2(one_minus_square(f.x, y.x), one_minus_square(f.y, y.y));
+        q = one_minus_square2(a, u2);
     }
 };
-// Which of a warp's tokens t0 .. t0 + kLruLen - 1 of a packed batch begin a
+// Which of a warp's tokens t0 .. t0 + L - 1 of a packed batch begin a
 // sequence (cut) and which end one (fin); nothing past the line. A dense
 // line has none: its state and gradient go in and out as the carries.
 struct LruMarks {
     unsigned cut, fin;
 };
+template <int L>
 __device__ __forceinline__ LruMarks lru_marks(const int32_t *cu, int n_seq, int T, int t0) {
     LruMarks m{0u, 0u};
     if (t0 >= T) return m;
     SsmSeq q = ssm_find(cu, n_seq, T, 0, t0);
     m.cut = q.starts;
-    while (q.end - t0 <= kLruLen) {
+    while (q.end - t0 <= L) {
         m.fin |= 1u << (q.end - 1 - t0);
         const int t = q.end;
-        if (t >= T || t - t0 >= kLruLen) break;
+        if (t >= T || t - t0 >= L) break;
         m.cut |= 1u << (t - t0);
         ssm_next(q, cu, n_seq, T, t);
     }
@@ -106,35 +110,8 @@ constexpr int kLruRanks = 16;  // most CTAs of a cluster
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Waits for a phase of a barrier; false after about half a second. CLUSTER:
-// what other CTAs sent is read next.
-template <bool CLUSTER>
-__device__ __forceinline__ bool lru_wait(uint32_t bar, uint32_t parity) {
-    uint64_t t0 = 0;
-    for (uint32_t it = 0;; ++it) {
-        uint32_t ok;
-        if (CLUSTER)
-            asm volatile(
-                "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-                " selp.u32 %0, 1, 0, p;\n}"
-                : "=r"(ok)
-                : "r"(bar), "r"(parity)
-                : "memory");
-        else
-            asm volatile(
-                "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-                " selp.u32 %0, 1, 0, p;\n}"
-                : "=r"(ok)
-                : "r"(bar), "r"(parity)
-                : "memory");
-        if (ok) return true;
-        if ((it & 255) == 255) {
-            const uint64_t t = now_ns();
-            if (t0 == 0) t0 = t;
-            else if (t - t0 > 500000000ull) return false;
-        }
-    }
-}
+// Waits for a phase of a barrier of this CTA; false after about half a second.
+__device__ __forceinline__ bool lru_wait(uint32_t bar, uint32_t parity) { return wait_bar(bar, parity, nullptr); }
 // The runs of the cluster's CTAs in a step. They are sent by asynchronous
 // stores that count their bytes on the receiver's barrier: no fence, and no
 // wait for a CTA's outputs on their way to memory, as a barrier of the cluster
@@ -148,7 +125,7 @@ struct LruRanks {
     __device__ __forceinline__ LruRun &at(int n, int rank) const { return runs[((n & 1) * places + rank) * 32 + (threadIdx.x & 31)]; }
     // all threads; then a sync of the cluster
     __device__ __forceinline__ void init() const {
-        for (int e = threadIdx.x; e < 2 * places * 32; e += 32 * kLruWarps)
+        for (int e = threadIdx.x; e < 2 * places * 32; e += blockDim.x)
             if (e / 32 % places >= K) runs[e] = LruRun{pack2(1.f, 1.f), pack2(0.f, 0.f)};
         if (threadIdx.x == 0) {
             mbar_init(smem_u32(&bar[0]), 1), mbar_init(smem_u32(&bar[1]), 1);
@@ -169,11 +146,11 @@ struct LruRanks {
                 "r"(__float_as_uint(H.y))
                 : "memory");
     }
-    __device__ __forceinline__ bool wait(int n) const { return lru_wait<true>(smem_u32(&bar[n & 1]), n >> 1 & 1); }
+    __device__ __forceinline__ bool wait(int n) const { return lru_wait(smem_u32(&bar[n & 1]), n >> 1 & 1); }
 };
 
 // --------------------------------------------------------- staging ----------
-// How a warp's rows of its tensors (kLruLen tokens x kLruCh channels each) get
+// How a warp's rows of its tensors (L tokens x kLruCh channels each) get
 // into its part of shared memory, which only the warp itself reads: by tensor
 // copies, one lane's (rows on 16 bytes; 16-byte copies by all lanes took a
 // quarter of the forward's instructions, and a bulk copy a row, which a warp's
@@ -181,7 +158,6 @@ struct LruRanks {
 // copies of a word of each lane's pair (rows on any word); or through registers
 // (bf16 rows on odd elements).
 enum { kLruWide, kLruWords, kLruElements };
-constexpr int kLruRows = kLruLen * kLruCh;  // elements of a warp's rows of a tensor
 // x, r, i, then z, or dout and z: (B, T, C), boxes of a warp's rows
 struct LruMaps {
     CUtensorMap m[5];
@@ -194,8 +170,9 @@ __device__ __forceinline__ void lru_tensor_copy(uint32_t dst, const CUtensorMap 
 }
 // N tensors whose rows are copied together. Rows past the line and channels
 // past C hold anything: no lane that exists reads them.
-template <typename T, int HOW, int N>
+template <typename T, int HOW, int N, int L>
 struct LruFetch {
+    static constexpr int kRows = L * kLruCh;  // elements of a warp's rows of a tensor
     static constexpr int kHeld = HOW == kLruWide ? 1 : N;
     const T *at[kHeld];
     int64_t st[kHeld];
@@ -208,16 +185,16 @@ struct LruFetch {
         for (int q = 0; q < kHeld; ++q)
             if (HOW != kLruWide) at[q] = base[q] + 2 * (threadIdx.x & 31), st[q] = stride[q];
     }
-    // rows t .. t + rows - 1 (none for rows <= 0) into dst[tensor][kLruRows];
+    // rows t .. t + rows - 1 (none for rows <= 0) into dst[tensor][kRows];
     // `bar` counts them (one phase a call), or the lane's next group of copies
     __device__ __forceinline__ void copy(T *dst, int t, int rows, uint32_t bar) const {
         const int lane = threadIdx.x & 31;
         if constexpr (HOW == kLruWide) {
             if (lane == 0) {
                 if (rows > 0) {
-                    arrive_expect_tx(bar, N * kLruRows * (int)sizeof(T));  // (whole boxes, zeros outside the tensor)
+                    arrive_expect_tx(bar, N * kRows * (int)sizeof(T));  // (whole boxes, zeros outside the tensor)
 #pragma unroll
-                    for (int k = 0; k < N; ++k) lru_tensor_copy(smem_u32(dst + k * kLruRows), maps + k, c0, t, line, bar);
+                    for (int k = 0; k < N; ++k) lru_tensor_copy(smem_u32(dst + k * kRows), maps + k, c0, t, line, bar);
                 } else {
                     arrive(bar);
                 }
@@ -227,26 +204,26 @@ struct LruFetch {
 #pragma unroll
             for (int k = 0; k < N; ++k)
 #pragma unroll
-                for (int j = 0; j < kLruLen; ++j)
+                for (int j = 0; j < L; ++j)
 #pragma unroll
                     for (int w = 0; w < kWords; ++w)
                         if (j < rows && 2 * lane + (kWords == 2 ? w : 1) < n)
-                            copy_async<4>(reinterpret_cast<uint32_t *>(dst + k * kLruRows + j * kLruCh + 2 * lane) + w,
+                            copy_async<4>(reinterpret_cast<uint32_t *>(dst + k * kRows + j * kLruCh + 2 * lane) + w,
                                           reinterpret_cast<const uint32_t *>(at[k] + (t + j) * st[k]) + w);
             cp_async_commit();
         } else {
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                uint32_t w[kLruLen];
+                uint32_t w[L];
 #pragma unroll
-                for (int j = 0; j < kLruLen; ++j) {
+                for (int j = 0; j < L; ++j) {
                     const unsigned short *e = reinterpret_cast<const unsigned short *>(at[k] + (int64_t)(t + j) * st[k]);
                     w[j] = j < rows && 2 * lane < n ? e[0] : 0u;
                     if (j < rows && 2 * lane + 1 < n) w[j] |= (uint32_t)e[1] << 16;
                 }
 #pragma unroll
-                for (int j = 0; j < kLruLen; ++j)
-                    *reinterpret_cast<uint32_t *>(dst + k * kLruRows + j * kLruCh + 2 * lane) = w[j];
+                for (int j = 0; j < L; ++j)
+                    *reinterpret_cast<uint32_t *>(dst + k * kRows + j * kLruCh + 2 * lane) = w[j];
             }
             cp_async_commit();
         }
@@ -255,7 +232,7 @@ struct LruFetch {
     template <int LATER>
     __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
         bool ok = true;
-        if constexpr (HOW == kLruWide) ok = lru_wait<false>(bar, parity);
+        if constexpr (HOW == kLruWide) ok = lru_wait(bar, parity);
         else cp_async_wait<LATER>();
         __syncwarp();
         return ok;
@@ -310,10 +287,9 @@ cudaError_t lru_by_form(const LruParams &p, int how, bool with_z, F &&f) {
     if (how == kLruWords) return by_cu(t, std::integral_constant<int, kLruWords>());
     return by_cu(t, std::integral_constant<int, kLruElements>());
 }
-// the maps of a call's tensors into m; false where they have none (a stride
+// the maps of a call's tensors, boxes of len tokens, into m; false where they have none (a stride
 // of zero): its rows are then copied by words
-bool lru_maps(const LruParams &p, bool gradient, LruMaps *m);
-cudaError_t lru_launch(const void *kernel, int lines, int C, int ranks, int smem, const LruParams &p, const LruMaps &m,
-                       cudaStream_t st);
+bool lru_maps(const LruParams &p, bool gradient, int len, LruMaps *m);
+cudaError_t lru_launch(const void *kernel, int warps, int smem, const LruParams &p, const LruMaps &m, cudaStream_t st);
 
 }  // namespace gdn

@@ -16,39 +16,39 @@
 namespace gdn {
 namespace {
 
-// shared memory: two stages of the tensors by warp (one of 32-bit rows, so that
-// two CTAs fit a SM), the warps' runs both ways, the ranks'
-template <typename T>
-constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
-template <typename T, bool Z>
+// L tokens a warp, W warps, S stages.
+// shared memory: the stages of the tensors by warp, the warps' runs both ways, the ranks'
+template <typename T, bool Z, int L, int W, int S>
 struct LruBwdSmem {
-    static constexpr int kTensors = Z ? 5 : 4, kStage = kTensors * kLruRows, kWarp = kStages<T> * kStage;
-    static constexpr int kRuns = kLruWarps * kWarp * (int)sizeof(T), kBacks = kRuns + 2 * kLruWarps * 32 * (int)sizeof(LruRun);
-    static constexpr int kRanks = kBacks + 2 * kLruWarps * 32 * 8;
+    static constexpr int kTensors = Z ? 5 : 4, kRows = L * kLruCh, kStage = kTensors * kRows, kWarp = S * kStage;
+    static constexpr bool kInPlace = sizeof(T) == 4;  // the gates take the places of r and i
+    static constexpr int kGates = W * kWarp * (int)sizeof(T);
+    static constexpr int kRuns = kGates + (kInPlace ? 0 : W * L * 32 * (int)sizeof(uint4)), kBacks = kRuns + 2 * W * 32 * (int)sizeof(LruRun);
+    static constexpr int kRanks = kBacks + 2 * W * 32 * 8;
     static constexpr int bytes(int K) { return kRanks + 2 * LruRanks::places_of(K) * 32 * (int)sizeof(LruRun); }
 };
 
-template <typename T, int HOW, bool PACKED, bool Z>
-__global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruParams p, const __grid_constant__ LruMaps maps) {
+template <typename T, int HOW, bool PACKED, bool Z, int L, int W, int S>
+__global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams p, const __grid_constant__ LruMaps maps) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ unsigned long long bars[kLruWarps][2], rank_bars[2];
-    using M = LruBwdSmem<T, Z>;
-    constexpr int S = kStages<T>, N = M::kTensors;
+    __shared__ unsigned long long bars[W][S], rank_bars[2];
+    using M = LruBwdSmem<T, Z, L, W, S>;
+    constexpr int N = M::kTensors, kTile = W * L;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int K = p.ranks, rank = blockIdx.x % K, line = blockIdx.y;
     const int c0 = (blockIdx.x / K) * kLruCh, c = c0 + 2 * lane, nc = p.C - c;
-    auto runs = reinterpret_cast<LruRun(*)[kLruWarps][32]>(smem + M::kRuns);   // A, H of a warp's tokens
-    auto backs = reinterpret_cast<f32x2(*)[kLruWarps][32]>(smem + M::kBacks);  // what they add to the gradient before them
+    auto runs = reinterpret_cast<LruRun(*)[W][32]>(smem + M::kRuns);   // A, H of a warp's tokens
+    auto backs = reinterpret_cast<f32x2(*)[W][32]>(smem + M::kBacks);  // what they add to the gradient before them
     const LruRanks ranks{reinterpret_cast<LruRun *>(smem + M::kRanks), rank_bars, K, LruRanks::places_of(K)};
     const f32x2 one = pack2(1.f, 1.f), zero = pack2(0.f, 0.f), minus = pack2(-1.f, -1.f), half = pack2(0.5f, 0.5f);
     if (PACKED) {
         if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
         if (p.dh0 && rank == 0) {  // of sequences without tokens
-            for (int s = warp; s < p.n_seq; s += kLruWarps)
+            for (int s = warp; s < p.n_seq; s += W)
                 if (p.cu[s + 1] <= p.cu[s]) lru_st_state(p.dh0, s, p.C, c, nc, lru_ld_state(p.dh_final, s, p.C, c, nc));
         }
     }
-    const int steps = (p.T + K * kLruTile - 1) / (K * kLruTile), tiles = (p.T + kLruTile - 1) / kLruTile;
+    const int steps = (p.T + K * kTile - 1) / (K * kTile), tiles = (p.T + kLruTile - 1) / kLruTile;
     const T *bases[5] = {(const T *)p.x + line * p.x_sb + c0, (const T *)p.r + line * p.r_sb + c0, (const T *)p.i + line * p.i_sb + c0,
                          (const T *)p.dout + line * p.do_sb + c0, (const T *)p.z + (Z ? line * p.z_sb + c0 : 0)};
     const T *base[N];
@@ -56,11 +56,12 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
     const int64_t strides[5] = {p.x_st, p.r_st, p.i_st, p.do_st, p.z_st};
 #pragma unroll
     for (int k = 0; k < N; ++k) base[k] = bases[k], stride[k] = strides[k];
-    const LruFetch<T, HOW, N> rows(base, stride, maps.m, c0, line, p.C);
+    const LruFetch<T, HOW, N, L> rows(base, stride, maps.m, c0, line, p.C);
     T *const stage = (T *)smem + warp * M::kWarp;
-    if (lane == 0) lru_init_bars(bars[warp], 2);
+    uint4 *const gates_at = reinterpret_cast<uint4 *>(smem + M::kGates) + warp * L * 32 + lane;
+    if (lane == 0) lru_init_bars(bars[warp], S);
     __syncwarp();
-    auto first = [&](int n) { return ((steps - 1 - n) * K + rank) * kLruTile + warp * kLruLen; };
+    auto first = [&](int n) { return ((steps - 1 - n) * K + rank) * kTile + warp * L; };
     auto fetch = [&](int n) {
         if (n < steps) rows.copy(stage + n % S * M::kStage, first(n), p.T - first(n), smem_u32(&bars[warp][n % S]));
         else cp_async_commit();
@@ -76,28 +77,35 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
     }
 #pragma unroll 1
     for (int n = 0; n < steps; ++n) {
-        const int t0 = first(n), len = min(max(p.T - t0, 0), kLruLen), flip = n & 1, tile = (steps - 1 - n) * K + rank;
+        const int t0 = first(n), len = min(max(p.T - t0, 0), L), flip = n & 1, tile = t0 / kLruTile;
         LruMarks m{0u, 0u};
-        if (PACKED) m = lru_marks(p.cu, p.n_seq, p.T, t0);
+        if (PACKED) m = lru_marks<L>(p.cu, p.n_seq, p.T, t0);
         f32x2 h = tile < tiles ? lru_ld_state(p.ck, (int64_t)line * tiles + tile, p.C, c, nc) : zero;
         if (S == 2) fetch(n + 1);  // (its place was read a step ago)
         if (!rows.template wait<S - 1>(smem_u32(&bars[warp][n % S]), n / S & 1)) lost = true;
-        const T *staged = stage + n % S * M::kStage + 2 * lane;
-        auto get = [&](int k, int j) { return lru_pair(staged + k * kLruRows + j * kLruCh); };  // of x, r, i, dout, z
-        const bool all_inside = len == kLruLen && !(m.cut | m.fin);
-        f32x2 a[kLruLen], b[kLruLen], back = zero;
+        T *const staged = stage + n % S * M::kStage + 2 * lane;
+        auto get = [&](int k, int j) { return lru_pair(staged + k * M::kRows + j * kLruCh); };  // of x, r, i, dout, z
+        const bool all_inside = len == L && !(m.cut | m.fin);
+        f32x2 a[L], b[L], back = zero;
         LruRun run{one, zero};
-        auto gates = [&](auto form) {  // whole: eight tokens within a sequence
+        auto gates = [&](auto form) {  // whole: all tokens are there, within a sequence
             constexpr bool whole = decltype(form)::value;
             bool open = true;  // no sequence has begun in the run
 #pragma unroll
-            for (int j = 0; j < kLruLen; ++j) {
+            for (int j = 0; j < L; ++j) {
                 if (!whole && j >= len) {
                     a[j] = one, b[j] = zero;
                     continue;
                 }
                 const LruGate g(get(1, j), get(2, j), decay);
                 a[j] = g.a, b[j] = mul2(mul2(sqrt_2(g.q), g.gi), get(0, j));
+                if constexpr (M::kInPlace) {
+                    *reinterpret_cast<f32x2 *>(staged + M::kRows + j * kLruCh) = g.gr;
+                    *reinterpret_cast<f32x2 *>(staged + 2 * M::kRows + j * kLruCh) = g.gi;
+                } else {
+                    const float2 gr = unpack2(g.gr), gi = unpack2(g.gi);
+                    gates_at[j * 32] = make_uint4(__float_as_uint(gr.x), __float_as_uint(gr.y), __float_as_uint(gi.x), __float_as_uint(gi.y));
+                }
                 f32x2 gd = get(3, j);
                 if (Z) {
                     const f32x2 v = get(4, j);
@@ -124,25 +132,26 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
         f32x2 gm = carry;  // a g of the token behind this one
         if (K > 1) {
             if (warp == 0) {
-                LruRun all{runs[flip][kLruWarps - 1][lane].A, backs[flip][kLruWarps - 1][lane]};
+                LruRun all{runs[flip][W - 1][lane].A, backs[flip][W - 1][lane]};
 #pragma unroll
-                for (int w = kLruWarps - 2; w >= 0; --w) {
+                for (int w = W - 2; w >= 0; --w) {
                     const f32x2 A = runs[flip][w][lane].A;
                     all.H = lru_apply2<PACKED>(A, backs[flip][w][lane], all.H), all.A = lru_join<PACKED>(all.A, A);
                 }
                 ranks.send(n, rank, all);
             }
         }
-        // the state before this warp's tokens
+        // the state before this warp's tokens, from the one saved for its 64
 #pragma unroll
-        for (int w = 0; w < kLruWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
+            if (w / (kLruTile / L) != warp / (kLruTile / L)) continue;
             if (w >= warp) break;
             const LruRun v = runs[flip][w][lane];
             h = lru_apply2<PACKED>(v.A, v.H, h);
         }
         const f32x2 h_in = h;
 #pragma unroll
-        for (int j = 0; j < kLruLen; ++j)  // b becomes h (it stays where tokens end)
+        for (int j = 0; j < L; ++j)  // b becomes h (it stays where tokens end)
             h = b[j] = PACKED && m.cut >> j & 1 ? b[j] : fma2(a[j], h, b[j]);
         if (K > 1) {
             if (!lost && !ranks.wait(n)) lost = true;  // (once is enough)
@@ -153,13 +162,13 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
                 carry = lru_apply2<PACKED>(v.A, v.H, carry);
             }
 #pragma unroll
-            for (int w = kLruWarps - 1; w > 0; --w) {
+            for (int w = W - 1; w > 0; --w) {
                 if (w <= warp) break;
                 gm = lru_apply2<PACKED>(runs[flip][w][lane].A, backs[flip][w][lane], gm);
             }
         } else {
 #pragma unroll
-            for (int w = kLruWarps - 1; w >= 0; --w) {
+            for (int w = W - 1; w >= 0; --w) {
                 if (w == warp) gm = carry;
                 carry = lru_apply2<PACKED>(runs[flip][w][lane].A, backs[flip][w][lane], carry);
             }
@@ -169,7 +178,7 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
         auto walk = [&](auto form) {
             constexpr bool whole = decltype(form)::value;
 #pragma unroll
-            for (int j = kLruLen - 1; j >= 0; --j) {
+            for (int j = L - 1; j >= 0; --j) {
                 if (!whole && j >= len) continue;
                 const int64_t at = at0 + (int64_t)j * p.C;
                 f32x2 g = get(3, j);
@@ -192,15 +201,22 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
                     if (p.dh0) lru_st_state(p.dh0, seq, p.C, c, nc, ag);
                     gm = zero;
                 }
-                const LruGate gt(get(1, j), get(2, j), decay);
-                const f32x2 xv = get(0, j), rs = rsqrt_2(gt.q), ix = mul2(gt.gi, xv);
-                const f32x2 dx = mul2(mul2(g, mul2(gt.q, rs)), gt.gi), di = mul2(mul2(dx, xv), fma2(gt.gi, minus, one));
+                f32x2 gr, gi;
+                if constexpr (M::kInPlace) {
+                    gr = get(1, j), gi = get(2, j);
+                } else {
+                    const uint4 v = gates_at[j * 32];
+                    gr = pack2(__uint_as_float(v.x), __uint_as_float(v.y)), gi = pack2(__uint_as_float(v.z), __uint_as_float(v.w));
+                }
+                const f32x2 u2 = mul2(decay.twice, gr), q = one_minus_square2(a[j], u2);
+                const f32x2 xv = get(0, j), rs = rsqrt_2(q), ix = mul2(gi, xv);
+                const f32x2 dx = mul2(mul2(g, mul2(q, rs)), gi), di = mul2(mul2(dx, xv), fma2(gi, minus, one));
                 // u g (a^2 i x / sqrt(q) - a prev)
-                const f32x2 w = mul2(mul2(ag, mul2(gt.u2, half)), fma2(prev, minus, mul2(mul2(rs, a[j]), ix)));
+                const f32x2 w = mul2(mul2(ag, mul2(u2, half)), fma2(prev, minus, mul2(mul2(rs, a[j]), ix)));
                 dlam = add2(dlam, w);
                 if (nc > 0) {
                     lru_put<T, HOW>((T *)p.dx + at, dx, nc), lru_put<T, HOW>((T *)p.di + at, di, nc);
-                    lru_put<T, HOW>((T *)p.dr + at, mul2(w, fma2(gt.gr, minus, one)), nc);
+                    lru_put<T, HOW>((T *)p.dr + at, mul2(w, fma2(gr, minus, one)), nc);
                 }
             }
         };
@@ -217,7 +233,7 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
     __syncthreads();
     if (warp == 0 && nc > 0) {
 #pragma unroll
-        for (int w = 1; w < kLruWarps; ++w) dlam = add2(dlam, sums[w * 32 + lane]);
+        for (int w = 1; w < W; ++w) dlam = add2(dlam, sums[w * 32 + lane]);
         const float2 f = unpack2(dlam);
         float o[2] = {f.x, f.y};
         for (int k = 0; k < 2; ++k) {
@@ -234,11 +250,12 @@ __global__ void __launch_bounds__(32 * kLruWarps, 2) lru_bwd_kernel(const LruPar
 
 cudaError_t launch_lru_bwd(const LruParams &p, cudaStream_t st) {
     LruMaps m{};
-    const int how = p.how == kLruWide && !lru_maps(p, true, &m) ? (int)kLruWords : p.how;
+    constexpr int L = 8, W = 8, S = 1;
+    const int how = p.how == kLruWide && !lru_maps(p, true, L, &m) ? (int)kLruWords : p.how;
     return lru_by_form(p, how, p.z != nullptr, [&](auto type, auto how, auto packed, auto z) {
         using T = decltype(type);
-        const int smem = LruBwdSmem<T, z()>::bytes(p.ranks);
-        return lru_launch((const void *)lru_bwd_kernel<T, how(), packed(), z()>, p.B, p.C, p.ranks, smem, p, m, st);
+        const int smem = LruBwdSmem<T, z(), L, W, S>::bytes(p.ranks);
+        return lru_launch((const void *)lru_bwd_kernel<T, how(), packed(), z(), L, W, S>, W, smem, p, m, st);
     });
 }
 
