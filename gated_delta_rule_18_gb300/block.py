@@ -159,6 +159,30 @@ def gdn_rotary(q, inv_freq, k=None, positions=None, offset=0, interleaved=False,
 # ------------------------------------------------------------ block norm ---
 
 
+def _lines(t, name, shape, like):
+    """(pointer, row stride) of rows of any leading shape; zeros for None."""
+    if t is None:
+        return 0, 0
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is like.dtype and t.get_device() == like.get_device() and t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    rows = _as_rows(t, name)
+    return _rows(rows, name, rows.shape, like)
+
+
+def _sizes(y):
+    """Rows and channels of y."""
+    shape = y.shape
+    if not shape:
+        raise ValueError("y must have at least one dimension")
+    D = shape[-1]
+    R = y.numel() // D if D else 0
+    if (R | D) >> 31:
+        _too_large(R, D)
+    return shape, R, D
+
+
 def _gate(gate, gate_act, y):
     """(pointer, row stride, rows that share one, act) of the gate: y's shape,
     or (B, 1, D) for y (B, T, D)."""
@@ -168,15 +192,12 @@ def _gate(gate, gate_act, y):
         return 0, 0, 1, 0
     if gate_act not in _ACT:
         raise ValueError(f"gate_act must be None, 'sigmoid' or 'silu', got {gate_act!r}")
-    D = y.shape[-1]
-    if gate.shape == y.shape:
-        g2, each = _as_rows(gate, "gate"), 1
-    elif y.dim() == 3 and gate.shape == (y.shape[0], 1, D) and y.shape[1] > 1:
-        g2, each = _as_rows(gate, "gate"), y.shape[1]
-    else:
-        raise ValueError(f"gate must have shape {tuple(y.shape)}, or one row a sequence of a (B, T, D) y, got {tuple(gate.shape)}")
-    p, st = _rows(g2, "gate", (g2.shape[0], D), y)
-    return p, st, each, _ACT[gate_act]
+    shape = y.shape
+    if gate.shape == shape:
+        return *_lines(gate, "gate", shape, y), 1, _ACT[gate_act]
+    if len(shape) == 3 and gate.shape == (shape[0], 1, shape[2]) and shape[1] > 1:
+        return *_lines(gate, "gate", gate.shape, y), shape[1], _ACT[gate_act]
+    raise ValueError(f"gate must have shape {tuple(shape)}, or one row a sequence of a (B, T, D) y, got {tuple(gate.shape)}")
 
 
 def gdn_block_norm_fwd(y, residual, post_weight=None, pre_weight=None, gate=None, gate_act=None, scale=None, alpha=1.0,
@@ -196,42 +217,31 @@ def gdn_block_norm_fwd(y, residual, post_weight=None, pre_weight=None, gate=None
             return gdn_block_norm_fwd(y, residual, post_weight, pre_weight, gate, gate_act, scale, alpha, eps, residual_out,
                                       out)
     L = layer._lib or layer._load()
-    y2 = y if y.dim() == 2 else _as_rows(y, "y")
-    R, D = y2.shape
-    if (R | D) >> 31:
-        _too_large(R, D)
+    shape, R, D = _sizes(y)
     if post_weight is None and pre_weight is None:
         raise ValueError("at least one of post_weight and pre_weight must be given")
-    if residual.shape != y.shape:
-        raise ValueError(f"residual must have shape {tuple(y.shape)}, got {tuple(residual.shape)}")
-    rc = _code(residual, "residual")
+    at = _lines(residual, "residual", shape, residual)
     if residual.get_device() != y.get_device():
         _fail(4, f"residual must be on {y.device}")
     given = (residual_out, out)
     if residual_out is None:
-        residual_out = torch.empty(y.shape, dtype=residual.dtype, device=y.device)
+        residual_out = torch.empty(shape, dtype=residual.dtype, device=y.device)
         ro = residual_out.data_ptr(), D
-    elif residual_out.shape != y.shape or residual_out.dtype != residual.dtype:
-        raise ValueError(f"residual_out must be {tuple(y.shape)} {residual.dtype}")
     else:
-        ro = _rows(_as_rows(residual_out, "residual_out"), "residual_out", (R, D), residual)
+        ro = _lines(residual_out, "residual_out", shape, residual)
     res = {"residual": residual_out}
     o = 0, 0
     if pre_weight is not None:
         if out is None:
-            out = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+            out = torch.empty(shape, dtype=y.dtype, device=y.device)
             o = out.data_ptr(), D
-        elif out.shape != y.shape:
-            raise ValueError(f"out must have shape {tuple(y.shape)}, got {tuple(out.shape)}")
         else:
-            o = _rows(_as_rows(out, "out"), "out", (R, D), y)
+            o = _lines(out, "out", shape, y)
         res["out"] = out
     elif out is not None:
         raise ValueError("out is given without pre_weight")
     f = torch.float32
-    yp, ys = _rows(y2, "y", (R, D), y)
-    rp, rs = _rows(_as_rows(residual, "residual"), "residual", (R, D), residual)
-    st = L.gdn_block_norm_fwd(yp, ys, _code(y, "y"), rp, rs, rc, *_gate(gate, gate_act, y),
+    st = L.gdn_block_norm_fwd(*_lines(y, "y", shape, y), _code(y, "y"), *at, _code(residual, "residual"), *_gate(gate, gate_act, y),
                               _flat(post_weight, "post_weight", (D,), f, y), _flat(pre_weight, "pre_weight", (D,), f, y),
                               _flat(scale, "scale", (D,), f, y), alpha, *ro, *o, R, D, eps, layer._stream(y))
     if st:
@@ -253,20 +263,14 @@ def gdn_block_norm_bwd(y, s, dout=None, dres=None, post_weight=None, pre_weight=
         with _guard(y, stream):
             return gdn_block_norm_bwd(y, s, dout, dres, post_weight, pre_weight, gate, gate_act, scale, alpha, eps, workspace)
     L = layer._lib or layer._load()
-    y2 = y if y.dim() == 2 else _as_rows(y, "y")
-    R, D = y2.shape
-    if (R | D) >> 31:
-        _too_large(R, D)
+    shape, R, D = _sizes(y)
     if post_weight is None and pre_weight is None:
         raise ValueError("at least one of post_weight and pre_weight must be given")
     if (dout is None) != (pre_weight is None):
         raise ValueError("dout goes with pre_weight")
     if dout is None and dres is None:
         raise ValueError("without pre_weight dres must be given")
-    for t, name in ((s, "s"), (dout, "dout"), (dres, "dres")):
-        if t is not None and t.shape != y.shape:
-            raise ValueError(f"{name} must have shape {tuple(y.shape)}, got {tuple(t.shape)}")
-    sc = _code(s, "s")
+    s_at = _lines(s, "s", shape, s)
     if s.get_device() != y.get_device():
         _fail(4, f"s must be on {y.device}")
     f32 = dict(dtype=torch.float32, device=y.device)
@@ -285,12 +289,9 @@ def gdn_block_norm_bwd(y, s, dout=None, dres=None, post_weight=None, pre_weight=
         return r[k].data_ptr() if k in r else 0
 
     f = torch.float32
-    yp, ys = _rows(y2, "y", (R, D), y)
-    sp, ss = _rows(_as_rows(s, "s"), "s", (R, D), s)
-    dop, dos = _rows(_as_rows(dout, "dout"), "dout", (R, D), y)
-    drp, drs = _rows(_as_rows(dres, "dres"), "dres", (R, D), s)
     ws, wp, wn = _workspace(workspace, L.gdn_block_norm_bwd_workspace_size(R, D, each), y)
-    st = L.gdn_block_norm_bwd(yp, ys, _code(y, "y"), sp, ss, sc, gp, gs, each, act, dop, dos, drp, drs,
+    st = L.gdn_block_norm_bwd(*_lines(y, "y", shape, y), _code(y, "y"), *s_at, _code(s, "s"), gp, gs, each, act,
+                              *_lines(dout, "dout", shape, y), *_lines(dres, "dres", shape, s),
                               _flat(post_weight, "post_weight", (D,), f, y), _flat(pre_weight, "pre_weight", (D,), f, y),
                               _flat(scale, "scale", (D,), f, y), alpha, r["dy"].data_ptr(), D, r["dresidual"].data_ptr(), D,
                               dg, D, ptr("dpost_weight"), ptr("dpre_weight"), ptr("dscale"), R, D, eps, wp, wn, layer._stream(y))

@@ -60,6 +60,7 @@ struct BlockNormBwdParams {
 };
 int64_t block_norm_parts(int R, int D, int gate_rows);  // most rows of partial sums
 cudaError_t launch_block_norm_bwd(const BlockNormBwdParams &p, cudaStream_t st);
+bool block_norm_by_sequence(const BlockNormBwdParams &p);  // needs the launch below before the last
 cudaError_t launch_block_norm_sequences(const BlockNormBwdParams &p, cudaStream_t st);
 cudaError_t launch_block_norm_reduce(const BlockNormBwdParams &p, cudaStream_t st);
 

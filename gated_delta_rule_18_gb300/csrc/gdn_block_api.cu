@@ -220,9 +220,9 @@ gdn_status gdn_block_norm_bwd(const void *y, int64_t y_st, int y_dtype, const vo
     p.part2 = reinterpret_cast<float *>(ws + align_up((size_t)block_norm_parts(R, D, gate_rows) * 2 * D * 4));
     cudaError_t e = cudaSuccess;
     if (R > 0) e = launch(KBlockNormBwd, stream, [&] { return launch_block_norm_bwd(p, stream); });
-    if (e == cudaSuccess && R > 0 && p.shared)
+    if (e == cudaSuccess && R > 0 && block_norm_by_sequence(p))
         e = launch(KBlockNormSeq, stream, [&] { return launch_block_norm_sequences(p, stream); });
-    if (e == cudaSuccess && (dpost_weight || dpre_weight || dscale))
+    if (e == cudaSuccess && (dpost_weight || dpre_weight || dscale || p.shared))
         e = launch(KBlockNormReduce, stream, [&] { return launch_block_norm_reduce(p, stream); });
     return cuda_status(e);
 }

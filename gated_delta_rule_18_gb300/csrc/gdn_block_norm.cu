@@ -607,6 +607,17 @@ __device__ __forceinline__ float2 column_sums(const float *in, int64_t parts, in
     }
     return make_float2(a, b);
 }
+// the gradient of sequence q's gate row at channel c from its sum of ds y
+// inv_y; returns the factor of the sum that the weights' gradients take
+template <typename TX>
+__device__ __forceinline__ float gate_gradient(const BlockNormBwdParams &p, int64_t q, int c, float sum) {
+    const float g = (float)((const TX *)p.gate)[q * p.g_st + c];
+    f32x2 df2;
+    const float2 f = unpack2(gate_of(pack2(g, g), p.act, df2));
+    const float w = p.alpha * (p.scale ? p.scale[c] : 1.f) * (p.post ? p.post[c] : 1.f);
+    ((TX *)p.dgate)[q * p.dg_st + c] = to_type<TX>(sum * w * unpack2(df2).x);
+    return f.x;
+}
 // of one sequence (blockIdx.y): its gate row's gradient, and its share of the sums
 template <typename TX>
 __global__ void __launch_bounds__(kSumX *kSumY) block_norm_sequences_kernel(const BlockNormBwdParams p, int parts) {
@@ -614,18 +625,16 @@ __global__ void __launch_bounds__(kSumX *kSumY) block_norm_sequences_kernel(cons
     const int64_t q = blockIdx.y;
     const float2 v = column_sums(p.part + q * parts * 2 * p.D, parts, p.D, c);
     if (threadIdx.x >= kSumX || c >= p.D) return;
-    const float g = (float)((const TX *)p.gate)[q * p.g_st + c];
-    f32x2 df2;
-    const float2 f = unpack2(gate_of(pack2(g, g), p.act, df2));
-    const float w = p.alpha * (p.scale ? p.scale[c] : 1.f) * (p.post ? p.post[c] : 1.f);
-    ((TX *)p.dgate)[q * p.dg_st + c] = to_type<TX>(v.x * w * unpack2(df2).x);
-    p.part2[q * 2 * p.D + c] = v.x * f.x;
+    p.part2[q * 2 * p.D + c] = v.x * gate_gradient<TX>(p, q, c, v.x);
     p.part2[q * 2 * p.D + p.D + c] = v.y;
 }
+// of all of them; a single sequence's shared gate row gets its gradient here
+template <typename TX>
 __global__ void __launch_bounds__(kSumX *kSumY) block_norm_reduce_kernel(const BlockNormBwdParams p, const float *in, int64_t parts) {
     const int c = blockIdx.x * kSumX + threadIdx.x % kSumX;
-    const float2 v = column_sums(in, parts, p.D, c);
+    float2 v = column_sums(in, parts, p.D, c);
     if (threadIdx.x >= kSumX || c >= p.D) return;
+    if (p.shared && in == p.part) v.x *= gate_gradient<TX>(p, 0, c, v.x);
     if (p.dpost) p.dpost[c] = v.x * (p.alpha * (p.scale ? p.scale[c] : 1.f));
     if (p.dscale) p.dscale[c] = v.x * (p.alpha * (p.post ? p.post[c] : 1.f));
     if (p.dpre) p.dpre[c] = v.y;
@@ -725,9 +734,15 @@ cudaError_t launch_block_norm_sequences(const BlockNormBwdParams &p, cudaStream_
     return cudaGetLastError();
 }
 
+bool block_norm_by_sequence(const BlockNormBwdParams &p) { return p.shared && p.R > p.gate_rows; }
+
 cudaError_t launch_block_norm_reduce(const BlockNormBwdParams &p, cudaStream_t st) {
-    const int64_t parts = p.R == 0 ? 0 : p.shared ? p.R / p.gate_rows : runs_of(p.R, 1, row_shape(p)).parts;
-    block_norm_reduce_kernel<<<(p.D + kSumX - 1) / kSumX, kSumX * kSumY, 0, st>>>(p, p.shared ? p.part2 : p.part, parts);
+    const bool joined = block_norm_by_sequence(p);
+    const int64_t parts = p.R == 0 ? 0 : joined ? p.R / p.gate_rows : runs_of(p.R, p.gate_rows, row_shape(p)).parts;
+    const float *in = joined ? p.part2 : p.part;
+    const unsigned grid = (p.D + kSumX - 1) / kSumX;
+    if (p.y_bf16) block_norm_reduce_kernel<__nv_bfloat16><<<grid, kSumX * kSumY, 0, st>>>(p, in, parts);
+    else block_norm_reduce_kernel<float><<<grid, kSumX * kSumY, 0, st>>>(p, in, parts);
     return cudaGetLastError();
 }
 

@@ -169,7 +169,7 @@ def block_inputs(B, T, D, dtype, res, post, pre, gate, scale, seed=20):
 
 
 SIZES = [(1, 1, 1), (1, 3, 7), (2, 5, 64), (1, 1, 2048), (3, 70, 100), (2, 9, 1000), (2, 33, 4096), (1, 2, 5000), (1, 3, 16384), (3, 43, 72),
-         (1, 5, 8192), (2, 700, 40)]
+         (1, 5, 8192), (2, 700, 40), (12, 5, 48), (9, 33, 1792)]
 FORMS = [  # dtype, residual, post, pre, gate, act, scale
     (BF, BF, True, True, None, None, False), (BF, F32, True, True, "token", "sigmoid", True), (F32, F32, True, True, "sequence", "silu", True),
     (F32, BF, True, False, "token", None, False), (BF, BF, False, True, "sequence", None, False), (F32, F32, False, True, "token", "silu", True),
