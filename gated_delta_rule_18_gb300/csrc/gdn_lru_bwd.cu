@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
         };
         if (all_inside) walk(std::true_type());
         else walk(std::false_type());
+        if (M::kInPlace && HOW == kLruWide) fence_async_smem();  // (the gates' stores, before the copies')
         __syncwarp();  // every lane is through with the stage
         if (S == 1) fetch(n + 1);
     }
