@@ -195,8 +195,8 @@ def _gate(gate, gate_act, y):
     shape = y.shape
     if gate.shape == shape:
         return *_lines(gate, "gate", shape, y), 1, _ACT[gate_act]
-    if len(shape) == 3 and gate.shape == (shape[0], 1, shape[2]) and shape[1] > 1:
-        return *_lines(gate, "gate", gate.shape, y), shape[1], _ACT[gate_act]
+    if len(shape) == 3 and gate.shape == (shape[0], 1, shape[2]):
+        return *_lines(gate, "gate", gate.shape, y), max(shape[1], 1), _ACT[gate_act]
     raise ValueError(f"gate must have shape {tuple(shape)}, or one row a sequence of a (B, T, D) y, got {tuple(gate.shape)}")
 
 
@@ -279,7 +279,7 @@ def gdn_block_norm_bwd(y, s, dout=None, dres=None, post_weight=None, pre_weight=
          "dresidual": torch.empty(s.shape, dtype=s.dtype, device=s.device)}
     dg = 0
     if gate is not None:
-        r["dgate"] = torch.empty(gate.shape, dtype=y.dtype, device=y.device)
+        r["dgate"] = (torch.empty if R else torch.zeros)(gate.shape, dtype=y.dtype, device=y.device)
         dg = r["dgate"].data_ptr()
     for name, w in (("dpost_weight", post_weight), ("dpre_weight", pre_weight), ("dscale", scale)):
         if w is not None:

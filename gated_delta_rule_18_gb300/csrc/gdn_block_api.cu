@@ -213,7 +213,7 @@ gdn_status gdn_block_norm_bwd(const void *y, int64_t y_st, int y_dtype, const vo
     p.dy_st = dy_st, p.ds_st = dresidual_st, p.dg_st = dgate_st;
     p.dpost = dpost_weight, p.dpre = dpre_weight, p.dscale = dscale;
     p.R = R, p.D = D, p.gate_rows = gate_rows, p.act = act, p.y_bf16 = y_dtype == GDN_BF16, p.r_bf16 = s_dtype == GDN_BF16;
-    p.shared = gate && gate_rows > 1, p.alpha = alpha, p.eps = eps;
+    p.shared = gate && gate_rows > 1 && R > 0, p.alpha = alpha, p.eps = eps;
     p.vec = r.wide && D % 8 == 0;
     unsigned char *ws = static_cast<unsigned char *>(workspace) + kAlign;
     p.part = reinterpret_cast<float *>(ws);

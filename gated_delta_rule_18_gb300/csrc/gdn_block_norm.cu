@@ -49,7 +49,8 @@ struct Runs {
     int64_t parts;
 };
 Runs runs_of(int R, int gate_rows, const RowShape &s) {
-    const int rows = gate_rows > 1 ? gate_rows : R, n = gate_rows > 1 ? R / gate_rows : 1;
+    const bool shared = gate_rows > 1 && R > 0;
+    const int rows = shared ? gate_rows : R, n = shared ? R / gate_rows : 1;
     const int nt = s.tpr * s.rpb, ctas = 152 * (nt <= 128 ? 8 : nt <= 256 ? 4 : 2), most = n < ctas ? ctas / n : 1;
     const int need = (int)(((int64_t)rows + s.rpb - 1) / s.rpb), want = need < most ? need : most;
     Runs r;

@@ -118,6 +118,11 @@ def test_block_norm_workspace_sizes(L):
     assert size(10**6, 4096, 1) <= 608 * 2 * 4096 * 4 + 4096
 
 
+def test_block_norm_workspace_of_an_empty_batch(L):
+    """A shared gate without rows: a size, and no division by the number of its rows."""
+    assert L.gdn_block_norm_bwd_workspace_size(0, 64, 5) > 0
+
+
 def act(name, i):
     return [(name, p(i)), (name + "_sb", 6400), (name + "_st", 64)]
 

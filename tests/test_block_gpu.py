@@ -24,7 +24,7 @@ import pytest
 import torch
 
 import gated_delta_rule_18_gb300 as gdn
-from gated_delta_rule_18_gb300 import autograd as gdr
+from gated_delta_rule_18_gb300 import autograd as gdr, layer
 from test_layer_gpu import BF, DEV, F32, F64, built, cu_of, dev, f64, randn, rel, spans, strided  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -238,6 +238,23 @@ def test_block_norm_strides_rows_and_in_place():
     assert empty["out"].shape == (0, 7, 100)
     z = gdn.gdn_block_norm_bwd(dev(y)[:0], dev(r)[:0], dout=dev(y)[:0], gate=dev(g)[:0], **kw)
     assert (z["dpost_weight"] == 0).all() and (z["dscale"] == 0).all() and (z["dpre_weight"] == 0).all() and z["dgate"].shape == (0, 1, 100)
+
+
+def test_block_norm_of_sequences_without_tokens():
+    """A shared gate row nobody takes: its gradient is zeros, and so are the weights'; below Python nothing of it is touched."""
+    y, g, w = torch.empty(2, 0, 64, device=DEV), dev(randn((2, 1, 64), F32, 43)), dev(randn((64,), F32, 44))
+    kw = dict(post_weight=w, pre_weight=w, gate=g, gate_act="silu")
+    got = gdn.gdn_block_norm_fwd(y, y.clone(), **kw)
+    assert got["out"].shape == got["residual"].shape == (2, 0, 64)
+    b = gdn.gdn_block_norm_bwd(y, got["residual"], dout=y.clone(), **kw)
+    assert b["dgate"].shape == (2, 1, 64) and all((b[k] == 0).all() for k in ("dgate", "dpost_weight", "dpre_weight"))
+    L = layer._load()
+    dg, dw, ws = torch.full((2, 64), 7.0, device=DEV), torch.ones(64, device=DEV), torch.empty(1 << 16, dtype=torch.uint8, device=DEV)
+    st = L.gdn_block_norm_bwd(0, 64, 0, 0, 64, 0, g.data_ptr(), 64, 5, 3, 0, 64, 0, 64, w.data_ptr(), w.data_ptr(), 0, 1.0, 0, 64, 0, 64,
+                              dg.data_ptr(), 64, dw.data_ptr(), 0, 0, 0, 64, 1e-6, ws.data_ptr(), ws.numel(),
+                              torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0 and (dg == 7).all() and (dw == 0).all()
 
 
 def test_block_norm_closed_and_non_finite_rows_stay_apart():
