@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
     auto runs = reinterpret_cast<LruRun(*)[W][32]>(smem + M::kRuns);   // A, H of a warp's tokens
     auto backs = reinterpret_cast<f32x2(*)[W][32]>(smem + M::kBacks);  // what they add to the gradient before them
     const LruRanks ranks{reinterpret_cast<LruRun *>(smem + M::kRanks), rank_bars, K, LruRanks::places_of(K)};
-    const f32x2 one = pack2(1.f, 1.f), zero = pack2(0.f, 0.f), minus = pack2(-1.f, -1.f), half = pack2(0.5f, 0.5f);
+    const f32x2 one = pack2(1.f, 1.f), zero = pack2(0.f, 0.f), minus = pack2(-1.f, -1.f);
     if (PACKED) {
         if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
         if (p.dh0 && rank == 0) {  // of sequences without tokens
@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
     };
     fetch(0);
     const LruDecay decay(p.lam + c, p.c, nc);
+    const f32x2 once = mul2(decay.twice, pack2(0.5f, 0.5f));
     // a g of the token behind the cluster's tiles
     f32x2 carry = PACKED ? zero : lru_ld_state(p.dh_final, line, p.C, c, nc), dlam = zero;
     bool lost = false;
@@ -98,13 +99,17 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
                     continue;
                 }
                 const LruGate g(get(1, j), get(2, j), decay);
-                a[j] = g.a, b[j] = mul2(mul2(sqrt_2(g.q), g.gi), get(0, j));
+                const f32x2 root = sqrt_2(g.q);
+                a[j] = g.a, b[j] = mul2(mul2(root, g.gi), get(0, j));
                 if constexpr (M::kInPlace) {
                     *reinterpret_cast<f32x2 *>(staged + M::kRows + j * kLruCh) = g.gr;
                     *reinterpret_cast<f32x2 *>(staged + 2 * M::kRows + j * kLruCh) = g.gi;
                 } else {
                     const float2 gr = unpack2(g.gr), gi = unpack2(g.gi);
                     gates_at[j * 32] = make_uint4(__float_as_uint(gr.x), __float_as_uint(gr.y), __float_as_uint(gi.x), __float_as_uint(gi.y));
+                    const float2 q = unpack2(root);
+                    *reinterpret_cast<float *>(staged + M::kRows + j * kLruCh) = q.x;
+                    *reinterpret_cast<float *>(staged + 2 * M::kRows + j * kLruCh) = q.y;
                 }
                 f32x2 gd = get(3, j);
                 if (Z) {
@@ -201,18 +206,24 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
                     if (p.dh0) lru_st_state(p.dh0, seq, p.C, c, nc, ag);
                     gm = zero;
                 }
-                f32x2 gr, gi;
+                f32x2 gr, gi, root, rs;  // sqrt(q) and its reciprocal
                 if constexpr (M::kInPlace) {
                     gr = get(1, j), gi = get(2, j);
+                    const f32x2 q = one_minus_square2(a[j], mul2(decay.twice, gr));
+                    rs = rsqrt_2(q), root = mul2(q, rs);
                 } else {
                     const uint4 v = gates_at[j * 32];
                     gr = pack2(__uint_as_float(v.x), __uint_as_float(v.y)), gi = pack2(__uint_as_float(v.z), __uint_as_float(v.w));
+                    root = pack2(*reinterpret_cast<const float *>(staged + M::kRows + j * kLruCh),
+                                 *reinterpret_cast<const float *>(staged + 2 * M::kRows + j * kLruCh));
+                    const float2 q = unpack2(root);
+                    rs = pack2(rcpf(fmaxf(q.x, 1e-18f)), rcpf(fmaxf(q.y, 1e-18f)));
                 }
-                const f32x2 u2 = mul2(decay.twice, gr), q = one_minus_square2(a[j], u2);
-                const f32x2 xv = get(0, j), rs = rsqrt_2(q), ix = mul2(gi, xv);
-                const f32x2 dx = mul2(mul2(g, mul2(q, rs)), gi), di = mul2(mul2(dx, xv), fma2(gi, minus, one));
+                const f32x2 u = mul2(once, gr);
+                const f32x2 xv = get(0, j), ix = mul2(gi, xv);
+                const f32x2 dx = mul2(mul2(g, root), gi), di = mul2(mul2(dx, xv), fma2(gi, minus, one));
                 // u g (a^2 i x / sqrt(q) - a prev)
-                const f32x2 w = mul2(mul2(ag, mul2(u2, half)), fma2(prev, minus, mul2(mul2(rs, a[j]), ix)));
+                const f32x2 w = mul2(mul2(ag, u), fma2(prev, minus, mul2(mul2(rs, a[j]), ix)));
                 dlam = add2(dlam, w);
                 if (nc > 0) {
                     lru_put<T, HOW>((T *)p.dx + at, dx, nc), lru_put<T, HOW>((T *)p.di + at, di, nc);
@@ -222,7 +233,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
         };
         if (all_inside) walk(std::true_type());
         else walk(std::false_type());
-        if (M::kInPlace && HOW == kLruWide) fence_async_smem();  // (the gates' stores, before the copies')
+        if (HOW == kLruWide) fence_async_smem();  // (what was kept in their places, before the copies)
         __syncwarp();  // every lane is through with the stage
         if (S == 1) fetch(n + 1);
     }
