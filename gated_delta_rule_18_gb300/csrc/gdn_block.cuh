@@ -95,7 +95,7 @@ struct LruShape {
     int ranks, warps;
 };
 LruShape lru_shape(int lines, int T, int C, bool bf16, bool wide);
-int lru_bwd_ranks(int lines, int T, int C, bool bf16);
+int lru_bwd_ranks(int lines, int T, int C);
 cudaError_t launch_lru(const LruParams &p, cudaStream_t st);
 cudaError_t launch_lru_bwd(const LruParams &p, cudaStream_t st);
 struct LruStepParams {

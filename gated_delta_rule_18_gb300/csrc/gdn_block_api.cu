@@ -72,8 +72,7 @@ LruWs lru_bwd_ws(int B, int T, int C, bool saved) {
     LruWs L;
     L.ck = kAlign;
     L.part = align_up(L.ck + (saved ? 0 : (size_t)B * ((T + kLruTile - 1) / kLruTile) * C * 4));
-    const int a = lru_bwd_ranks(B, T, C, false), b = lru_bwd_ranks(B, T, C, true);
-    L.total = align_up(L.part + (size_t)B * (a > b ? a : b) * C * 4);
+    L.total = align_up(L.part + (size_t)B * lru_bwd_ranks(B, T, C) * C * 4);
     return L;
 }
 
@@ -328,7 +327,7 @@ gdn_status gdn_lru_bwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
     p.dout = dout, p.do_sb = dout_sb, p.do_st = dout_st, p.dh_final = dh_final;
     p.dx = dx, p.dr = dr, p.di = di, p.dz = dz, p.dlam = dlam, p.dh0 = dh0;
     p.part = reinterpret_cast<float *>(ws + L.part);
-    p.ranks = lru_bwd_ranks(B, T, C, p.bf16);
+    p.ranks = lru_bwd_ranks(B, T, C);
     if (e == cudaSuccess) e = launch(KLruBwd, stream, [&] { return launch_lru_bwd(p, stream); });
     if (e == cudaSuccess)
         e = launch(KColSum, stream, [&] { return launch_col_sum(p.part, C, B * p.ranks, C, dlam, 0, nullptr, stream); });

@@ -210,18 +210,25 @@ __global__ void __launch_bounds__(128) lru_step_kernel(const LruStepParams p) {
 
 }  // namespace
 
+// Whether `tiles` CTAs fill what waves they take of `slots` at a time to three quarters.
+static bool lru_fills(int64_t tiles, int slots) { return tiles * 4 >= (tiles + slots - 1) / slots * slots * 3; }
 // CTAs of a cluster, which take a line's tiles side by side, and warps of a CTA.
-// Where the lines' channel tiles alone are more than the SMs, four CTAs a line
-// in bf16 even the SMs' loads out (4 x 4096 tokens of 4096 channels, 1, 2, 4, 8:
-// 160, 148, 138, 144 us) and one is best in fp32, which HBM bounds (210, 216,
-// 224, 235). With fewer, tiles of 128 tokens and as many CTAs as make 256, up to
-// twelve a line (16 tiles of 32768 tokens with 8, 12, 16: 148, 111, 130 us;
-// tiles of 64 tokens with 16: 128).
+// In bf16 a cluster pays for its exchange at every step, so a line's channel
+// tile goes to one CTA of eight warps where those fill the SMs (16 x 1024 tokens
+// of 4096 channels: 126 us, to four CTAs of four warps 144; 24 x 512: 99 for
+// 132), and to four where they do not (8 x 2048 tokens of 2560 channels: 101 for
+// 109) or lines are long (4 x 4096 and 8 x 4096 tokens of 4096 channels: 138 and
+// 261 for 141 and 267). In fp32, which HBM bounds, one CTA of four warps is best
+// (8 x 1024 tokens of 2048 channels: 62, with eight warps 64, four CTAs 72). With
+// few tiles, eight warps and as many CTAs as make 256, up to twelve a line (32768
+// tokens of 1024 channels with 8, 12, 16: 148, 109, 130 us; sixteen warps with
+// 6, 8, 12: 113, 163, 124).
 LruShape lru_shape(int lines, int T, int C, bool bf16, bool wide) {
     const int64_t tiles = (int64_t)lines * ((C + kLruCh - 1) / kLruCh);
     LruShape s{1, 4};
     if (tiles >= 192) {
-        s.ranks = !bf16 || tiles >= 2432 ? 1 : tiles >= 1216 ? 2 : 4;
+        const bool whole = lru_fills(tiles, wide ? 304 : 608) && T < 4096;
+        s.ranks = !bf16 || whole ? 1 : 4, s.warps = bf16 && whole && wide ? 8 : 4;
     } else {
         const int most = wide ? 12 : 16, all = wide ? 256 : 512;
         s.warps = wide && T > 64 ? 8 : 4;
@@ -232,10 +239,12 @@ LruShape lru_shape(int lines, int T, int C, bool bf16, bool wide) {
     if (s.ranks > steps) s.ranks = steps > 0 ? steps : 1;
     return s;
 }
-// of the gradient: eight warps of eight tokens
-int lru_bwd_ranks(int lines, int T, int C, bool bf16) {
+// Of the gradient: eight warps of eight tokens, by the same rules in both types
+// (16 x 1024 tokens of 4096 channels, bf16, one CTA a line 294 us, four 339;
+// 8 x 2048 of 2560 channels 262 and 217, fp32 349 and 265).
+int lru_bwd_ranks(int lines, int T, int C) {
     const int64_t tiles = (int64_t)lines * ((C + kLruCh - 1) / kLruCh);
-    int k = tiles >= 192 ? !bf16 || tiles >= 2432 ? 1 : tiles >= 1216 ? 2 : 4 : (int)(tiles * 12 <= 256 ? 12 : 256 / tiles);
+    int k = tiles >= 192 ? lru_fills(tiles, 304) ? 1 : 4 : (int)(tiles * 12 <= 256 ? 12 : 256 / tiles);
     const int steps = (T + kLruTile - 1) / kLruTile;
     return k > steps ? steps > 0 ? steps : 1 : k;
 }
