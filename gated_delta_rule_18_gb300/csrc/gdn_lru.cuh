@@ -15,19 +15,26 @@ namespace gdn {
 // where warps begin.
 constexpr int kLruCh = 64;
 
-// 1 - a^2 = 1 - exp(-y) for y >= 0: by the series where the difference cancels
-// (y < 1/8: the first term left out is y^5 / 720 of the value, 4e-8). In
-// scalar instructions: their constants are immediates.
-__device__ __forceinline__ float one_minus_square(float a, float y) {
-    float s = fmaf(y, 1.f / 120.f, -1.f / 24.f);
-    s = fmaf(s, y, 1.f / 6.f);
-    s = fmaf(s, y, -0.5f);
-    s = fmaf(s, y, 1.f);
-    return y < 0.125f ? s * y : fmaf(-a, a, 1.f);
+// a = exp(-u) (as the unit forms it) and q = 1 - a^2 = (1 - a)(1 + a), for u >=
+// 0. Where u < 1/8, both from 1 - a by its series (the first term left out is
+// u^5 / 720 of the value, 4e-8): q would cancel, and a product of many a near
+// one keeps the unit's error of each (2^-22, of one sign), not a rounding's:
+// dlam was 2.5e-6 off after 348 tokens. In scalar instructions: their constants
+// are immediates.
+__device__ __forceinline__ void lru_decay(float &a, float &q, float u) {
+    float t = fmaf(u, 1.f / 120.f, -1.f / 24.f);
+    t = fmaf(t, u, 1.f / 6.f);
+    t = fmaf(t, u, -0.5f);
+    t = fmaf(t, u, 1.f) * u;
+    const bool small = u < 0.125f;
+    t = small ? t : 1.f - a;
+    a = small ? 1.f - t : a;
+    q = fmaf(t, a, t);
 }
-__device__ __forceinline__ f32x2 one_minus_square2(f32x2 a, f32x2 y) {
-    const float2 f = unpack2(a), v = unpack2(y);
-    return pack2(one_minus_square(f.x, v.x), one_minus_square(f.y, v.y));
+__device__ __forceinline__ void lru_decay2(f32x2 &a, f32x2 &q, f32x2 u) {
+    float2 f = unpack2(a), r, v = unpack2(u);
+    lru_decay(f.x, r.x, v.x), lru_decay(f.y, r.y, v.y);
+    a = pack2(f.x, f.y), q = pack2(r.x, r.y);
 }
 __device__ __forceinline__ f32x2 sqrt_2(f32x2 x) {
     float2 v = unpack2(x);
@@ -43,21 +50,21 @@ __device__ __forceinline__ f32x2 rsqrt_2(f32x2 x) {
     asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(v.y));
     return pack2(v.x, v.y);
 }
-// What a channel pair's gates are made with: -c softplus(lam) log2(e), 2 c softplus(lam).
+// What a channel pair's gates are made with: -c softplus(lam) log2(e), c softplus(lam).
 struct LruDecay {
-    f32x2 base, twice;
+    f32x2 base, rate;
     __device__ __forceinline__ LruDecay(const float *lam, float c, int nc) {
         const float2 s = softplus2(make_float2(nc > 0 ? lam[0] : 0.f, nc > 1 ? lam[1] : 0.f));
-        base = pack2(-kLog2e * (c * s.x), -kLog2e * (c * s.y)), twice = pack2(2.f * (c * s.x), 2.f * (c * s.y));
+        base = pack2(-kLog2e * (c * s.x), -kLog2e * (c * s.y)), rate = pack2(c * s.x, c * s.y);
     }
 };
-// u = c softplus(lam) sigmoid(r): a = exp(-u), q = 1 - a^2, u2 = 2 u
+// u = c softplus(lam) sigmoid(r): a = exp(-u), q = 1 - a^2
 struct LruGate {
-    f32x2 u2, a, q, gr, gi;
+    f32x2 a, q, gr, gi;
     __device__ __forceinline__ LruGate(f32x2 r, f32x2 i, const LruDecay &d) {
         gr = sigmoid_2(r), gi = sigmoid_2(i);
-        u2 = mul2(d.twice, gr), a = ex2_2(mul2(d.base, gr));
-        q = one_minus_square2(a, u2);
+        a = ex2_2(mul2(d.base, gr));
+        lru_decay2(a, q, mul2(d.rate, gr));
     }
 };
 // Which of a warp's tokens t0 .. t0 + L - 1 of a packed batch begin a

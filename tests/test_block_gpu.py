@@ -490,6 +490,26 @@ def test_lru_malformed_cu_seqlens_is_reported():
         assert gdn.lib().gdn_last_device_error(ctypes.c_void_p(ws.data_ptr()), stream, ctypes.byref(word)) == 9
 
 
+def test_lru_decays_near_one():
+    """A state of one and no input leave a itself. For u = c softplus(lam) sigmoid(r) below 1/8 it is 1 - t, rounded to half a
+    step of the values below one (2^-25), with t = 1 - exp(-u) right to 2^-20: the sigmoid's exponential, sum and reciprocal
+    2^-21.4, softplus and its product 2^-22, the series 2^-22.5. (An exponential good to 2^-22 would not pass where t < 2^-5.)"""
+    C = 4096
+    lam = decays(C, 0.985, 0.9999, seed=97)
+    r = torch.linspace(-9, 9, C, dtype=F64)[torch.randperm(C, generator=torch.Generator().manual_seed(98))].float()[None]
+    u = 8 * torch.nn.functional.softplus(f64(lam), threshold=200) * torch.sigmoid(f64(r))
+    assert u.max() < 0.125
+    state, zero = torch.ones(1, C, device=DEV), torch.zeros(1, C, device=DEV)
+    gdn.gdn_lru_step(zero, dev(r), zero, dev(lam), state)
+    t = -torch.expm1(-u)
+    off = (state.cpu().double() - (1 - t)).abs()
+    assert (off <= 2.0**-25 + t * 2.0**-20).all(), (off / (2.0**-25 + t * 2.0**-20)).max()
+    # the same a in whole sequences: the final state of one token
+    final = torch.empty(1, C, device=DEV)
+    gdn.gdn_lru_fwd(zero[None], dev(r)[None], zero[None], dev(lam), h0=torch.ones(1, C, device=DEV), h_final=final)
+    assert torch.equal(final, state)
+
+
 @pytest.mark.parametrize("n,C,pool", [(1, 4096, 1), (1, 1, 1), (5, 64, 9), (3, 7, 3), (64, 130, 80), (256, 512, 300)])
 @pytest.mark.parametrize("dtype,full", [(BF, True), (F32, False)])
 def test_lru_step(n, C, pool, dtype, full):
