@@ -11,6 +11,10 @@ two directions' gradients.
 The gradient kernels take the upstream gradient of the output in the
 inputs' precision: for bf16 inputs an fp32 upstream gradient is rounded to
 bf16 first; fp32 inputs (the fp32 path) keep it in fp32.
+
+A backward pass is captured into a CUDA graph only while no eager graph of the
+same leaves is alive: torch's nodes that accumulate their gradients would wait
+on the eager graph's stream amid the capture, which ends the process.
 """
 from __future__ import annotations
 

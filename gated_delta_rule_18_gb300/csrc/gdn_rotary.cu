@@ -16,6 +16,12 @@
 // two vectors of the halves, 4 as one interleaved) of one token, its cosines
 // and sines in registers, and walks the token's heads with several heads'
 // loads under way.
+//
+// Measured, bf16 (copy rate 6.78 TB/s): 4 x 4096 tokens, 32 + 8 heads of 128
+// channels, halves, 56 us (49.5 at the copy rate); 2 x 8192, 16 + 16 heads of 112
+// with 64 turning, interleaved, 44, out of wider rows (34.6). Loads on their way
+// are the largest stall (20 warps a SM, 80 registers). With cosines read again
+// for every head and fp64 angles it took 66 and 68.
 #include "gdn_ssm.cuh"
 #include "gdn_block.cuh"
 
