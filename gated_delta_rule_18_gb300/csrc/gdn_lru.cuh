@@ -219,18 +219,23 @@ struct LruFetch {
                                           reinterpret_cast<const uint32_t *>(at[k] + (t + j) * st[k]) + w);
             cp_async_commit();
         } else {
+            // (with a branch an element the loads wait for one another, 328 us for 226
+            // with 4 x 17498 tokens of 167 channels: rows and channels that are not
+            // there take the last that are)
+            const int d0 = min(2 * lane, n - 1) - 2 * lane, d1 = min(2 * lane + 1, n - 1) - 2 * lane;
+            if (rows > 0) {
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                uint32_t w[L];
+                for (int k = 0; k < N; ++k) {
+                    unsigned short lo[L], hi[L];
 #pragma unroll
-                for (int j = 0; j < L; ++j) {
-                    const unsigned short *e = reinterpret_cast<const unsigned short *>(at[k] + (int64_t)(t + j) * st[k]);
-                    w[j] = j < rows && 2 * lane < n ? e[0] : 0u;
-                    if (j < rows && 2 * lane + 1 < n) w[j] |= (uint32_t)e[1] << 16;
+                    for (int j = 0; j < L; ++j) {
+                        const unsigned short *e = reinterpret_cast<const unsigned short *>(at[k] + (int64_t)(t + min(j, rows - 1)) * st[k]);
+                        lo[j] = e[d0], hi[j] = e[d1];
+                    }
+#pragma unroll
+                    for (int j = 0; j < L; ++j)
+                        *reinterpret_cast<uint32_t *>(dst + k * kRows + j * kLruCh + 2 * lane) = lo[j] | (uint32_t)hi[j] << 16;
                 }
-#pragma unroll
-                for (int j = 0; j < L; ++j)
-                    *reinterpret_cast<uint32_t *>(dst + k * kRows + j * kLruCh + 2 * lane) = w[j];
             }
             cp_async_commit();
         }

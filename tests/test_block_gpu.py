@@ -375,6 +375,29 @@ def test_lru_bwd(B, T, C, lens, dtype, full):
         assert all(torch.equal(got[k], other[k]) for k in got)
 
 
+@pytest.mark.parametrize("B,T,C,dtype", [(24, 300, 640, BF), (24, 300, 636, BF), (24, 300, 640, F32), (8, 300, 2560, BF), (8, 300, 2560, F32)])
+def test_lru_many_lines(B, T, C, dtype):
+    """As many lines and channels as fill the GPU alone (whole lines, eight warps), or leave a part of it (clusters)."""
+    x, r, i, lam, z, h0, n = lru_inputs(B, T, C, None, dtype, True, seed=140)
+    do, dh = randn((B, T, C), dtype, 150), randn((n, C), F32, 151)
+    leaf = [f64(t).requires_grad_() for t in (x, r, i, lam, z, h0)]
+    u = 8 * torch.nn.functional.softplus(leaf[3], threshold=200) * torch.sigmoid(leaf[1])
+    a, b = torch.exp(-u), torch.sqrt(-torch.expm1(-2 * u)) * torch.sigmoid(leaf[2]) * leaf[0]
+    h, rows = leaf[5], []
+    for t in range(T):
+        h = a[:, t] * h + b[:, t]
+        rows.append(h)
+    ref = torch.stack(rows, 1) * leaf[4] * torch.sigmoid(leaf[4])
+    want = torch.autograd.grad((ref * f64(do)).sum() + (h * f64(dh)).sum(), leaf)
+    args, kw = [dev(t) for t in (x, r, i, lam)], dict(z=dev(z), h0=dev(h0))
+    final, ck = torch.empty(n, C, device=DEV), torch.empty(B, (T + 63) // 64, C, device=DEV)
+    got = gdn.gdn_lru_fwd(*args, h_final=final, checkpoints=ck, **kw)
+    assert rel(got, ref.detach()) <= tol(dtype, TOL_LRU) and rel(final, h.detach()) <= TOL_LRU
+    g = gdn.gdn_lru_bwd(*args, dev(do), dh_final=dev(dh), checkpoints=ck, **kw)
+    for k, w in zip(("dx", "dr", "di", "dlam", "dz", "dh0"), want):
+        assert rel(g[k], w) <= tol(g[k].dtype, TOL_LRU_BWD), k
+
+
 def test_lru_long_lines_cross_tiles_and_clusters():
     """Every place of a sequence's end in a warp, a tile, a cluster's step; more tokens than one step of a cluster takes."""
     lens = [1500, 63, 1, 64, 65, 7, 8, 9, 511, 512, 513, 30]
