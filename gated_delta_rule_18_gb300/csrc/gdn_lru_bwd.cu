@@ -230,8 +230,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
                 const f32x2 u = mul2(decay.rate, gr);
                 const f32x2 xv = get(0, j), ix = mul2(gi, xv);
                 const f32x2 dx = mul2(mul2(g, root), gi), di = mul2(mul2(dx, xv), fma2(gi, minus, one));
-                // u g (a^2 i x / sqrt(q) - a prev)
-                const f32x2 w = mul2(mul2(ag, u), fma2(prev, minus, mul2(mul2(rs, a[j]), ix)));
+                // u g (a^2 i x / sqrt(q) - a prev); u goes with 1 / sqrt(q) first, which
+                // a masked token's x, however large, then meets as a zero
+                const f32x2 w = mul2(ag, fma2(mul2(u, prev), minus, mul2(mul2(mul2(u, rs), a[j]), ix)));
                 dlam = add2(dlam, w);
                 if (nc > 0) {
                     lru_put<T, HOW>((T *)p.dx + at, dx, nc), lru_put<T, HOW>((T *)p.di + at, di, nc);

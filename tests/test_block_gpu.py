@@ -463,6 +463,26 @@ def test_lru_masked_tokens_and_extremes(dtype):
     assert all(v.isfinite().all() for v in g.values())
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_lru_largest_inputs_behind_a_closed_gate(dtype):
+    """Padding of the type's lowest or largest value under a closed r adds nothing, forward or back."""
+    B, T, C = 2, 70, 40
+    x, r, i, lam, z, h0, n = lru_inputs(B, T, C, None, dtype, True, seed=160)
+    do, pad = randn((B, T, C), dtype, 170), slice(20, 45)
+    r[:, pad] = torch.finfo(dtype).min
+    x[:, pad] = 0.0
+    args = lambda: ([dev(t) for t in (x, r, i, lam)], dict(z=dev(z), h0=dev(h0)))  # noqa: E731
+    a, kw = args()
+    want, grads = gdn.gdn_lru_fwd(*a, **kw), gdn.gdn_lru_bwd(*a, dev(do), **kw)
+    for value in (torch.finfo(dtype).min, torch.finfo(dtype).max):
+        x[:, pad] = value
+        a, kw = args()
+        assert torch.equal(gdn.gdn_lru_fwd(*a, **kw), want)
+        got = gdn.gdn_lru_bwd(*a, dev(do), **kw)
+        assert all(torch.equal(got[k], grads[k]) for k in got)
+        assert all((got[k][:, pad] == 0).all() for k in ("dx", "dr", "di"))
+
+
 def test_lru_non_finite_values_stay_in_their_channel_and_sequence():
     lens = [70, 3, 500, 27]
     T, C = sum(lens), 64
