@@ -16,14 +16,15 @@
 // cross warps through shared memory. Sums and norms are fp32.
 //
 // Measured (copy rate 6.78 TB/s): forward, 4 x 4096 rows of 4096 channels with a
-// gate a token, fp32 residual 152 us (91 %), bf16 113 (87 %); gradient 294 (74 %)
-// and 281 (56 %). 2 x 8192 rows of 1792 channels, bf16, gate shared: 48, and 109
-// in three launches (91, 10, 5). In bf16 the gradient's instructions come before
+// gate a token, fp32 residual 152 us (91 %), bf16 113 (87 %); gradient 298 (73 %)
+// and 287 (55 %). 2 x 8192 rows of 1792 channels, bf16, gate shared: 48, and 111
+// in three launches (96, 10, 5). In bf16 the gradient's instructions come before
 // its bytes: 136 a warp and channel pair (two norms' sums and gradients), at 0.56
-// to 0.59 a cycle from the 16 warps a SM that 128 registers leave.
+// a cycle from the 16 warps a SM that 128 registers leave.
 #include "gdn_block.cuh"
 #include "gdn_ssm.cuh"
 
+#include <cfloat>
 #include <type_traits>
 
 namespace gdn {
@@ -195,6 +196,9 @@ struct Slots {
     __device__ __forceinline__ void copy(int stage, int piece, const T *src) const {
 #pragma unroll
         for (int k = 0; k < kVecN * (int)sizeof(T) / 16; ++k) copy_async<16>(at(stage, piece + k), src + k * 16 / sizeof(T));
+    }
+    __device__ __forceinline__ void clear(int stage, int piece, int n) const {
+        for (int k = 0; k < n; ++k) *at(stage, piece + k) = make_uint4(0u, 0u, 0u, 0u);
     }
     template <typename T>
     __device__ __forceinline__ void get(f32x2 (&v)[kPairs], int stage, int piece) const {
@@ -379,8 +383,9 @@ __global__ void __launch_bounds__(NV == 1 && VEC ? 128 : 512, NV == 1 && VEC ? 8
 struct NormGrad {
     f32x2 k, ke;
     float S, G, inv;
-    __device__ __forceinline__ NormGrad(float S_, float G_, float rd, float eps) : S(S_), G(G_) {
-        inv = rsqrtf(S * rd + eps);
+    // `none`: the norm is zeros, and so is its gradient
+    __device__ __forceinline__ NormGrad(float S_, float G_, float rd, float eps, bool none) : S(S_), G(G_) {
+        inv = none ? 0.f : rsqrtf(S * rd + eps);
         const float a = inv * (inv * inv * rd), b = inv * (eps * inv * inv);
         k = pack2(a, a), ke = pack2(b, b);
     }
@@ -477,14 +482,22 @@ __global__ void __launch_bounds__(NV == 1 && VEC && !TOKEN ? 128 : 512, NV == 1 
             const int ahead = stage == 0 ? stages - 1 : stage - 1;
             slots_arrived(stages - 2), fetch(ahead);
         }
+        // rows whose squares' sum passes fp32's range: their norms are zeros, so they are taken as zeros from then on
+        bool no_s = false, no_y = false;
+        auto clear = [&](f32x2 (&v)[kPairs]) {
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) v[j] = zero;
+        };
         auto take_y = [&](f32x2 (&v)[kPairs], int i, int n) {
             if (AHEAD) slots.get<TX>(v, stage, i * vec_pieces);
             else get<TX, VEC>(v, y + i * cs, n);
+            if (!AHEAD && no_y) clear(v);
         };
         auto take_s = [&](f32x2 (&vs)[kPairs], f32x2 (&vd)[kPairs], int i, int n) {  // and dout
             const int o = i * vec_pieces + NX + n_dres;
             if (AHEAD) slots.get<TR>(vs, stage, o), slots.get<TX>(vd, stage, o + NR);
             else get<TR, VEC>(vs, s + i * cs, n), get<TX, VEC>(vd, dout + i * cs, n);
+            if (!AHEAD && no_s) clear(vs);
         };
         f32x2 a = zero, b = zero, d = zero;  // of s^2, pre dout s, y^2
 #pragma unroll
@@ -507,8 +520,20 @@ __global__ void __launch_bounds__(NV == 1 && VEC && !TOKEN ? 128 : 512, NV == 1 
         const float2 fa = unpack2(a), fb = unpack2(b), fd = unpack2(d);
         float v[3] = {fa.x + fa.y, fb.x + fb.y, fd.x + fd.y};
         row_sums3(v, red3[flip], warps);
-        const NormGrad ns(v[0], v[1], rd, p.eps);
-        const float inv_y = p.post ? rsqrtf(v[2] * rd + p.eps) : 1.f;
+        no_s = v[0] > FLT_MAX, no_y = v[2] > FLT_MAX;
+        if (no_s || no_y) {
+            if (AHEAD) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    if (no_s) slots.clear(stage, i * vec_pieces + NX + n_dres, NR);
+                    if (no_y) slots.clear(stage, i * vec_pieces, NX);
+                }
+            }
+            if (no_s) v[0] = v[1] = 0.f;
+            if (no_y) v[2] = 0.f;
+        }
+        const NormGrad ns(v[0], v[1], rd, p.eps, no_s);
+        const float inv_y = !p.post ? 1.f : no_y ? 0.f : rsqrtf(v[2] * rd + p.eps);
         const f32x2 iy2 = pack2(inv_y, inv_y), is2 = pack2(ns.inv, ns.inv);
         f32x2 e[kHeld][kPairs], g2 = zero;  // k post f ds, the gradient behind y's norm; of e y
         // The stream's gradient and what follows from it. again: e alone (rows
@@ -572,7 +597,7 @@ __global__ void __launch_bounds__(NV == 1 && VEC && !TOKEN ? 128 : 512, NV == 1 
             const float2 fg = unpack2(g2);
             ge = row_sum(fg.x + fg.y, red1[flip], warps);
         }
-        const NormGrad ny(v[2], ge, rd, p.eps);
+        const NormGrad ny(v[2], ge, rd, p.eps, no_y);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * cs, at = HOLD ? i : 0;

@@ -278,6 +278,33 @@ def test_block_norm_closed_and_non_finite_rows_stay_apart():
         assert (bwd["dy"][0, 0] == 0).all() and (bwd["dgate"][0, 0] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [256, 100, 1792])
+@pytest.mark.parametrize("gate", ["token", "sequence"])
+def test_block_norm_padding_of_extreme_values(dtype, D, gate):
+    """Padded rows of the type's lowest value, whose squares pass fp32's range: they are normed to zeros and add none to the
+    weights' gradients, and a stream row of them passes its own gradient on."""
+    y, r, wp, wn, g, sc = block_inputs(1, 9, D, dtype, dtype, True, True, gate, True)
+    do, dr = randn((1, 9, D), dtype, 45), randn((1, 9, D), dtype, 46)
+    low = torch.finfo(dtype).min
+    pad, keep = [2, 6], [0, 1, 3, 4, 5, 7, 8]
+    kw = dict(post_weight=dev(wp), pre_weight=dev(wn), gate=dev(g), gate_act="sigmoid", scale=dev(sc))
+    y[0, pad] = low
+    f = gdn.gdn_block_norm_fwd(dev(y), dev(r), **kw)
+    assert torch.equal(f["residual"][0, pad].cpu(), r[0, pad])
+    b = gdn.gdn_block_norm_bwd(dev(y), f["residual"], dout=dev(do), dres=dev(dr), **kw)
+    assert all(b[k].isfinite().all() for k in b) and (b["dy"][0, pad] == 0).all()
+    s = f["residual"].clone()
+    s[0, pad] = low
+    b = gdn.gdn_block_norm_bwd(dev(y), s, dout=dev(do), dres=dev(dr), **kw)
+    assert all(b[k].isfinite().all() for k in b) and torch.equal(b["dresidual"][0, pad].cpu(), dr[0, pad])
+    few = dict(kw, gate=dev(g)[:, keep].contiguous() if gate == "token" else dev(g))
+    alone = gdn.gdn_block_norm_bwd(dev(y)[:, keep].contiguous(), s[:, keep].contiguous(), dout=dev(do)[:, keep].contiguous(),
+                                   dres=dev(dr)[:, keep].contiguous(), **few)
+    for k in ("dpost_weight", "dpre_weight", "dscale"):
+        assert rel(b[k], f64(alone[k])) <= TOL_NORM, k
+
+
 def test_block_norm_gradient_by_differences():
     y, r, wp, wn, g, sc = block_inputs(2, 6, 72, F32, F32, True, True, "sequence", True)
     do, dr = dev(randn((2, 6, 72), F32, 41)), dev(randn((2, 6, 72), F32, 42))
