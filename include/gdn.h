@@ -682,9 +682,10 @@ gdn_status gdn_ssm_step(const void *x, int64_t x_st, const void *dt,
  *   strides over B, T and H in elements; k and k_out both NULL with Hk == 0
  *   for q alone. An output may be its own input (same strides); else outputs
  *   overlap neither inputs nor one another (layouts of three separate strides
- *   are told apart by the range of their bytes; an output's have to nest). inv_freq: rot / 2 doubles,
- *   radians a position. positions: int32 or int64 (pos_bits), strides pos_sb
- *   over B and pos_st over T (0 shares), or NULL: offset + t.
+ *   are told apart by the range of their bytes; an output's have to nest).
+ *   inv_freq: rot / 2 finite doubles, radians a position. positions: int32 or
+ *   int64 (pos_bits), strides pos_sb over B and pos_st over T (0 shares), or
+ *   NULL: offset + t.
  *   rot even, 2 <= rot <= D <= 512; B T <= 2^31 - 65536.
  *   The angle is reduced in fixed point: any int64 position is as good as its
  *   frequency's own 53 bits.
@@ -732,7 +733,8 @@ gdn_status gdn_block_norm_fwd(const void *y, int64_t y_st, int y_dtype,
  * the stream's own gradient dres (or NULL; s_dtype as s). dy, dgate: y_dtype
  * (dgate (R / gate_rows, D), summed in fp32); dresidual: s_dtype; dpost_weight,
  * dpre_weight, dscale: (D) fp32, or NULL. s and dout are not read without
- * pre_weight. Every sum has a fixed order.
+ * pre_weight. A row whose sum of squares passes fp32's range is normed to
+ * zeros and has zeros for that norm's gradient. Every sum has a fixed order.
  *   workspace: gdn_block_norm_bwd_workspace_size(R, D, gate_rows) bytes.
  */
 size_t gdn_block_norm_bwd_workspace_size(int R, int D, int gate_rows);
@@ -759,7 +761,8 @@ gdn_status gdn_block_norm_bwd(const void *y, int64_t y_st, int y_dtype,
  *   h0, h_final: (n_seq, C) fp32 or NULL. checkpoints: (B, ceil(T / 64), C)
  *   fp32 or NULL: the state before every 64th token, for the gradient.
  *   out may lie on x, r, i or z. workspace: 256 bytes, needed with cu_seqlens
- *   only.
+ *   only. A state that is not finite stays so in its channel to its sequence's
+ *   end. A wait inside the kernel that runs out (half a second) leaves NaN.
  */
 #define GDN_LRU_TILE 64 /* tokens a checkpoint stands for */
 gdn_status gdn_lru_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
