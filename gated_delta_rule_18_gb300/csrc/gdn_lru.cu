@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_kernel(const LruParams p, 
     };
     fetch(0), fetch_z(0);
     const LruDecay decay(p.lam + c, p.c, nc);
+    const bool near = decay.near(nc);
     f32x2 carry = PACKED ? zero : lru_ld_state(p.h0, line, p.C, c, nc);  // the state before the cluster's tiles
     bool lost = false;
     if (K > 1) {
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_kernel(const LruParams p, 
         auto get = [&](int k, int j) { return lru_pair(stage + 2 * lane + k * M::kRows + j * kLruCh); };  // a pair of x, r or i
         f32x2 a[L], b[L];
         LruRun run{one, zero};
-        auto gates = [&](auto form) {  // whole: all tokens are there, none begins a sequence
+        auto gates = [&](auto form, auto close) {  // whole: all tokens are there, none begins a sequence
             constexpr bool whole = decltype(form)::value;
 #pragma unroll
             for (int j = 0; j < L; ++j) {
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_kernel(const LruParams p, 
                     a[j] = one, b[j] = zero;
                     continue;
                 }
-                const LruGate g(get(1, j), get(2, j), decay);
+                const LruGate<decltype(close)::value> g(get(1, j), get(2, j), decay);
                 a[j] = g.a, b[j] = mul2(mul2(sqrt_2(g.q), g.gi), get(0, j));
                 if (PACKED && !whole && m.cut >> j & 1) {
                     if (p.h0) b[j] = fma2(g.a, lru_ld_state(p.h0, lru_seq(p.cu, p.n_seq, p.T, t0 + j), p.C, c, nc), b[j]);
@@ -114,8 +115,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_kernel(const LruParams p, 
                 }
             }
         };
-        if (len == L && !m.cut) gates(std::true_type());
-        else gates(std::false_type());
+        if (HOW == kLruWide && near && len == L && !m.cut) gates(std::true_type(), std::bool_constant<HOW == kLruWide>());
+        else if (len == L && !m.cut) gates(std::true_type(), std::false_type());
+        else gates(std::false_type(), std::false_type());
         runs[flip][warp][lane] = run;
         __syncwarp();  // every lane has read what the next copies overwrite
         fetch(n + 1);
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(128) lru_step_kernel(const LruStepParams p) {
     float o[4];
 #pragma unroll
     for (int k = 0; k < 4; k += 2) {
-        const LruGate g(pack2(r[k], r[k + 1]), pack2(i[k], i[k + 1]), LruDecay(lam + k, p.c, 2));
+        const LruGate<false> g(pack2(r[k], r[k + 1]), pack2(i[k], i[k + 1]), LruDecay(lam + k, p.c, 2));
         const float2 v = unpack2(fma2(g.a, pack2(h[k], h[k + 1]), mul2(mul2(sqrt_2(g.q), g.gi), pack2(x[k], x[k + 1]))));
         h[k] = o[k] = v.x, h[k + 1] = o[k + 1] = v.y;
         if (p.z) {

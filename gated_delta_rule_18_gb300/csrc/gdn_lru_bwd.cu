@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
     };
     fetch(0);
     const LruDecay decay(p.lam + c, p.c, nc);
+    const bool near = decay.near(nc);
     // a g of the token behind the cluster's tiles
     f32x2 carry = PACKED ? zero : lru_ld_state(p.dh_final, line, p.C, c, nc), dlam = zero;
     bool lost = false;
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
         const bool all_inside = len == L && !(m.cut | m.fin);
         f32x2 a[L], b[L], back = zero;
         LruRun run{one, zero};
-        auto gates = [&](auto form) {  // whole: all tokens are there, within a sequence
+        auto gates = [&](auto form, auto close) {  // whole: all tokens are there, within a sequence
             constexpr bool whole = decltype(form)::value;
             bool open = true;  // no sequence has begun in the run
 #pragma unroll
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
                     a[j] = one, b[j] = zero;
                     continue;
                 }
-                const LruGate g(get(1, j), get(2, j), decay);
+                const LruGate<decltype(close)::value> g(get(1, j), get(2, j), decay);
                 const f32x2 root = sqrt_2(g.q);
                 a[j] = g.a, b[j] = mul2(mul2(root, g.gi), get(0, j));
                 if constexpr (M::kInPlace) {
@@ -137,8 +138,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
                 if (whole || open) back = fma2(run.A, gd, back);
             }
         };
-        if (all_inside) gates(std::true_type());
-        else gates(std::false_type());
+        if (HOW == kLruWide && near && all_inside) gates(std::true_type(), std::bool_constant<HOW == kLruWide>());
+        else if (all_inside) gates(std::true_type(), std::false_type());
+        else gates(std::false_type(), std::false_type());
         runs[flip][warp][lane] = run, backs[flip][warp][lane] = back;
         __syncthreads();
         f32x2 gm = carry;  // a g of the token behind this one
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
                 if constexpr (M::kInPlace) {
                     gr = get(1, j), gi = get(2, j);
                     f32x2 av = a[j], q;  // (1 - a itself is not in a as exactly)
-                    lru_decay2(av, q, mul2(decay.rate, gr));
+                    lru_decay2<false>(av, q, mul2(decay.rate, gr));
                     rs = rsqrt_2(q), root = mul2(q, rs);
                 } else {
                     const uint4 v = gates_at[j * 32];

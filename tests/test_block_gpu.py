@@ -580,6 +580,24 @@ def test_lru_decays_near_one():
     assert torch.equal(final, state)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_lru_channels_do_not_see_their_neighbours_decay(dtype):
+    """Warps whose channels all decay slowly take a shorter way to a; one fast channel sends them the other one, to the same bits."""
+    B, T, C = 2, 150, 128
+    x, r, i, lam, z, h0, n = lru_inputs(B, T, C, None, dtype, True, seed=180)
+    do, fast = dev(randn((B, T, C), dtype, 190)), lam.clone()
+    fast[[5, 127]] = 4.0
+    rest = [c for c in range(C) if c not in (5, 127)]
+    out = []
+    for v in (lam, fast):
+        args, kw = [dev(t) for t in (x, r, i, v)], dict(z=dev(z), h0=dev(h0))
+        final = torch.empty(n, C, device=DEV)
+        g = gdn.gdn_lru_bwd(*args, do, **kw)
+        out.append([gdn.gdn_lru_fwd(*args, h_final=final, **kw), final, *(g[k] for k in sorted(g))])
+    for a, b in zip(*out):
+        assert torch.equal(a[..., rest], b[..., rest])
+
+
 @pytest.mark.parametrize("n,C,pool", [(1, 4096, 1), (1, 1, 1), (5, 64, 9), (3, 7, 3), (64, 130, 80), (256, 512, 300)])
 @pytest.mark.parametrize("dtype,full", [(BF, True), (F32, False)])
 def test_lru_step(n, C, pool, dtype, full):
