@@ -15,12 +15,13 @@
 // copies as soon as the gates are formed, z after the walk. Results repeat bit
 // for bit.
 //
-// Measured (copy rate 6.78 TB/s): 4 x 4096 tokens of 4096 channels 140 us in
-// bf16 (71 % of the copy rate), 209 in fp32 (95 %); 8 x 1024 of 4096 channels,
-// bf16, 72: 77 instructions a warp and channel pair at 0.55 a cycle from 14
-// warps a SM, 16 of them for the exponential unit, whose queue is the largest
-// stall. 32768 tokens of 1024 channels 113 (44 %): with 16 tiles of channels
-// only, 10 warps a SM, and an exchange over the cluster every 1536 tokens.
+// Measured (copy rate 6.78 TB/s): 4 x 4096 tokens of 4096 channels 132 us in
+// bf16 (75 % of the copy rate), 206 in fp32 (96 %); 8 x 1024 of 4096 channels,
+// bf16, 68: 74 instructions a warp and channel pair at 0.56 a cycle from 14
+// warps a SM, 14 of them for the exponential unit (16 where a channel decays
+// fast), whose queue is a large stall. 32768 tokens of 1024 channels 105 (47 %):
+// with 16 tiles of channels only, 10 warps a SM, and an exchange over the
+// cluster every 1536 tokens.
 #include <cudaTypedefs.h>
 
 #include <mutex>
