@@ -170,7 +170,7 @@ class _Once(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, *grads):
-        raise RuntimeError("the state-space layer's gradients are not differentiable")
+        raise RuntimeError("the gradients of the layer's and the block's operators are not differentiable")
 
 
 def _once(backward):
