@@ -197,9 +197,6 @@ struct Slots {
 #pragma unroll
         for (int k = 0; k < kVecN * (int)sizeof(T) / 16; ++k) copy_async<16>(at(stage, piece + k), src + k * 16 / sizeof(T));
     }
-    __device__ __forceinline__ void clear(int stage, int piece, int n) const {
-        for (int k = 0; k < n; ++k) *at(stage, piece + k) = make_uint4(0u, 0u, 0u, 0u);
-    }
     template <typename T>
     __device__ __forceinline__ void get(f32x2 (&v)[kPairs], int stage, int piece) const {
         uint32_t w[RowVec<T, kVecN>::kWords];
@@ -209,6 +206,24 @@ struct Slots {
             w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
         }
         to_pairs<T>(v, w);
+    }
+    // n pieces of values times a power of two, which every type holds; zeros for 0. (Few rows need it: as
+    // loops, for the registers.)
+    template <typename T>
+    __device__ __forceinline__ void scale(int stage, int piece, int n, float power) const {
+#pragma unroll 1
+        for (int k = 0; k < n; ++k) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(at(stage, piece + k));
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(T) == 4) {
+                    w[j] = power == 0.f ? 0u : __float_as_uint(__uint_as_float(w[j]) * power);
+                } else {
+                    const float lo = __uint_as_float(w[j] << 16) * power, hi = __uint_as_float(w[j] & 0xffff0000u) * power;
+                    w[j] = power == 0.f ? 0u : __float_as_uint(lo) >> 16 | (__float_as_uint(hi) & 0xffff0000u);
+                }
+            }
+        }
     }
 };
 __device__ __forceinline__ void slots_arrived(int ahead) {  // all but the last `ahead` rows
@@ -375,6 +390,25 @@ __global__ void __launch_bounds__(NV == 1 && VEC ? 128 : 512, NV == 1 && VEC ? 8
     }
 }
 
+// A row as a norm's gradient takes it: its values times `power`, a power of two
+// that brings their root mean square into fp32's middle where it is far out
+// (2^30 either way: past that inv^3 / D becomes a denormal, from 1e13 on, or
+// gw S overflows, and gradients that are finite come out as zeros or NaN). The
+// norm does not see the factor, and no rounding does. A row whose S passes
+// fp32's range is normed to zeros: its power is 0.
+struct NormRow {
+    float S, inv;  // of the row times its power
+    __device__ __forceinline__ NormRow(float S_, float rd, float eps) : S(S_), inv(rsqrtf(S_ * rd + eps)) {}
+    __device__ __forceinline__ bool far() const { return inv < 0x1p-30f || inv > 0x1p30f; }
+    __device__ __forceinline__ float bring_near() {  // the row's power
+        if (!far()) return 1.f;
+        const int bits = __float_as_int(inv);
+        const bool none = S > FLT_MAX;
+        const float power = none ? 0.f : __int_as_float(bits & 0x7f800000);
+        inv = none ? 0.f : __int_as_float((bits & 0x7fffff) | 0x3f800000), S = none ? 0.f : S * power * power;
+        return power;
+    }
+};
 // The gradient of a norm at channel pair x for the weighted gradient gw = w dy,
 // with S = sum x^2, G = sum gw x, inv, added to `more`: both sums lose the
 // channel's own terms first, rounded as the sums have them, which cancel
@@ -382,11 +416,9 @@ __global__ void __launch_bounds__(NV == 1 && VEC ? 128 : 512, NV == 1 && VEC ? 8
 // subtractions, as packed ones may be fused with the products).
 struct NormGrad {
     f32x2 k, ke;
-    float S, G, inv;
-    // `none`: the norm is zeros, and so is its gradient
-    __device__ __forceinline__ NormGrad(float S_, float G_, float rd, float eps, bool none) : S(S_), G(G_) {
-        inv = none ? 0.f : rsqrtf(S * rd + eps);
-        const float a = inv * (inv * inv * rd), b = inv * (eps * inv * inv);
+    float S, G;
+    __device__ __forceinline__ NormGrad(const NormRow &r, float power, float G_, float rd, float eps) : S(r.S), G(G_) {
+        const float inv = r.inv * power, a = inv * (r.inv * r.inv * rd), b = inv * (eps * inv * inv);
         k = pack2(a, a), ke = pack2(b, b);
     }
     __device__ __forceinline__ f32x2 at(f32x2 x, f32x2 gw, f32x2 more) const {
@@ -395,6 +427,11 @@ struct NormGrad {
         return fma2(k, fma2(gw, so, mul2(x, go)), fma2(ke, gw, more));
     }
 };
+// times a row's power; what is not finite goes with a row of zeros
+__device__ __forceinline__ void scale_row(f32x2 (&v)[kPairs], float power) {
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) v[j] = power == 0.f ? pack2(0.f, 0.f) : mul2(v[j], pack2(power, power));
+}
 
 // Runs as in the forward. A thread keeps its channels' sums, in registers with
 // up to two vectors a thread, else in its own slots of shared memory. A row is
@@ -482,22 +519,18 @@ __global__ void __launch_bounds__(NV == 1 && VEC && !TOKEN ? 128 : 512, NV == 1 
             const int ahead = stage == 0 ? stages - 1 : stage - 1;
             slots_arrived(stages - 2), fetch(ahead);
         }
-        // rows whose squares' sum passes fp32's range: their norms are zeros, so they are taken as zeros from then on
-        bool no_s = false, no_y = false;
-        auto clear = [&](f32x2 (&v)[kPairs]) {
-#pragma unroll
-            for (int j = 0; j < kPairs; ++j) v[j] = zero;
-        };
+        bool far = false;  // the row's powers (NormRow) are not one
+        float of_s = 1.f, of_y = 1.f;
         auto take_y = [&](f32x2 (&v)[kPairs], int i, int n) {
             if (AHEAD) slots.get<TX>(v, stage, i * vec_pieces);
             else get<TX, VEC>(v, y + i * cs, n);
-            if (!AHEAD && no_y) clear(v);
+            if (!AHEAD && far) scale_row(v, of_y);
         };
         auto take_s = [&](f32x2 (&vs)[kPairs], f32x2 (&vd)[kPairs], int i, int n) {  // and dout
             const int o = i * vec_pieces + NX + n_dres;
             if (AHEAD) slots.get<TR>(vs, stage, o), slots.get<TX>(vd, stage, o + NR);
             else get<TR, VEC>(vs, s + i * cs, n), get<TX, VEC>(vd, dout + i * cs, n);
-            if (!AHEAD && no_s) clear(vs);
+            if (!AHEAD && far) scale_row(vs, of_s);
         };
         f32x2 a = zero, b = zero, d = zero;  // of s^2, pre dout s, y^2
 #pragma unroll
@@ -520,21 +553,24 @@ __global__ void __launch_bounds__(NV == 1 && VEC && !TOKEN ? 128 : 512, NV == 1 
         const float2 fa = unpack2(a), fb = unpack2(b), fd = unpack2(d);
         float v[3] = {fa.x + fa.y, fb.x + fb.y, fd.x + fd.y};
         row_sums3(v, red3[flip], warps);
-        no_s = v[0] > FLT_MAX, no_y = v[2] > FLT_MAX;
-        if (no_s || no_y) {
+        NormRow row_s(v[0], rd, p.eps), row_y(v[2], rd, p.eps);
+        far = (p.pre && row_s.far()) || (p.post && row_y.far());
+        if (far) {
+            if (p.pre) of_s = row_s.bring_near();
+            if (p.post) of_y = row_y.bring_near();
+            v[1] = of_s == 0.f ? 0.f : v[1] * of_s;
             if (AHEAD) {
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < NV; ++i) {
-                    if (no_s) slots.clear(stage, i * vec_pieces + NX + n_dres, NR);
-                    if (no_y) slots.clear(stage, i * vec_pieces, NX);
+                    const int o = i * vec_pieces;
+                    if (p.pre) slots.scale<TR>(stage, o + NX + n_dres, NR, of_s);
+                    slots.scale<TX>(stage, o, NX, of_y);
                 }
             }
-            if (no_s) v[0] = v[1] = 0.f;
-            if (no_y) v[2] = 0.f;
         }
-        const NormGrad ns(v[0], v[1], rd, p.eps, no_s);
-        const float inv_y = !p.post ? 1.f : no_y ? 0.f : rsqrtf(v[2] * rd + p.eps);
-        const f32x2 iy2 = pack2(inv_y, inv_y), is2 = pack2(ns.inv, ns.inv);
+        const NormGrad ns(row_s, of_s, v[1], rd, p.eps);
+        const float inv_y = p.post ? row_y.inv : 1.f;
+        const f32x2 iy2 = pack2(inv_y, inv_y), is2 = pack2(row_s.inv, row_s.inv);
         f32x2 e[kHeld][kPairs], g2 = zero;  // k post f ds, the gradient behind y's norm; of e y
         // The stream's gradient and what follows from it. again: e alone (rows
         // whose e is not held).
@@ -597,7 +633,7 @@ __global__ void __launch_bounds__(NV == 1 && VEC && !TOKEN ? 128 : 512, NV == 1 
             const float2 fg = unpack2(g2);
             ge = row_sum(fg.x + fg.y, red1[flip], warps);
         }
-        const NormGrad ny(v[2], ge, rd, p.eps, no_y);
+        const NormGrad ny(row_y, of_y, ge, rd, p.eps);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * cs, at = HOLD ? i : 0;

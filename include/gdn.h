@@ -734,7 +734,9 @@ gdn_status gdn_block_norm_fwd(const void *y, int64_t y_st, int y_dtype,
  * (dgate (R / gate_rows, D), summed in fp32); dresidual: s_dtype; dpost_weight,
  * dpre_weight, dscale: (D) fp32, or NULL. s and dout are not read without
  * pre_weight. A row whose sum of squares passes fp32's range is normed to
- * zeros and has zeros for that norm's gradient. Every sum has a fixed order.
+ * zeros and has zeros for that norm's gradient; below it gradients are right
+ * as long as a row's products of values and gradients stay in fp32's range.
+ * Every sum has a fixed order.
  *   workspace: gdn_block_norm_bwd_workspace_size(R, D, gate_rows) bytes.
  */
 size_t gdn_block_norm_bwd_workspace_size(int R, int D, int gate_rows);

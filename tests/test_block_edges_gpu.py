@@ -1,0 +1,72 @@
+"""The block's operators on the GPU at the ends of their ranges, against plain
+fp64 forms: rows of very large values, non-finite values beside a sequence's
+end, waits that run out, callers on two threads, far positions, lines of several
+steps of a cluster, forms of rows that few calls have.
+
+Tolerances as derived in test_block_gpu.py; others beside their tests.
+"""
+import math
+
+import pytest
+import torch
+
+import gated_delta_rule_18_gb300 as gdn
+from test_block_gpu import TOL_NORM, block_inputs, norm, ref_block, tol
+from test_layer_gpu import BF, DEV, F32, F64, built, dev, f64, randn  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------ block norm ---
+
+
+def rows_rel(got, ref):
+    """Largest error of any row, of the row's largest value."""
+    got, ref = f64(got).flatten(0, -2), f64(ref).flatten(0, -2)
+    assert got.isfinite().all()
+    return ((got - ref).abs().amax(-1) / ref.abs().amax(-1).clamp(min=1e-300)).max().item()
+
+
+@pytest.mark.parametrize("D", [8, 100, 256, 1792, 4096, 9000])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("gate", [None, "token", "sequence"])
+def test_block_norm_gradient_of_large_rows(D, dtype, gate):
+    """Rows of up to the largest values whose squares' sum fp32 holds, of one value and of random ones, beside usual rows and
+    rows near zero: the norms' gradients are inv gw and its projections, however small inv is. Row by row, as their sizes
+    differ by 1e30; errors are those of a usual row (the scaling by a power of two adds none). Where a row's sum does pass
+    fp32's range (of 9000 channels 2.5e17), it is normed to zeros and has zeros for that norm's gradients."""
+    top = math.sqrt(0.9 * torch.finfo(F32).max / D)
+    sizes = [1.0, 1e-12, 1e8, 1e12, 1e13, 1e14, 1e15, 1e16, 1e17, 1e18 if D <= 256 else 2.5e17, top]
+    T = 2 * len(sizes)
+    y, r, wp, wn, g, _ = block_inputs(1, T, D, dtype, dtype, True, True, gate, False, seed=200)
+    do, dr = randn((1, T, D), dtype, 210, 1.5), randn((1, T, D), dtype, 211)
+    for t in (y, r):
+        for k, v in enumerate(sizes):
+            t[0, 2 * k] = -v * 0.99                                                       # padding of one value
+            t[0, 2 * k + 1] = (t[0, 2 * k + 1].float().clamp(-4, 4) * (v / 4)).to(dtype)  # (sum of squares below the constant row's)
+    kw = dict(post_weight=dev(wp), pre_weight=dev(wn), gate=dev(g), gate_act=None if gate is None else "sigmoid")
+    # the stream's norm alone, at large s and usual y; then y's norm alone, at large y and usual s
+    usual, small = block_inputs(1, T, D, dtype, dtype, True, True, gate, False, seed=220)[:2]
+    for yy, s, dres in ((usual, r, None), (y, small, dr)):
+        none = {k: f64(t).square().sum(-1, keepdim=True) > torch.finfo(F32).max for k, t in dict(y=yy, s=s).items()}
+        leaf = {k: f64(t).requires_grad_() for k, t in dict(y=yy, s=s, wp=wp, wn=wn, g=g).items() if t is not None}
+        t, _ = ref_block(leaf["y"].masked_fill(none["y"], 0), torch.zeros(1, T, D, dtype=F64), leaf["wp"], None, leaf.get("g"), kw["gate_act"], None, 1.0, 1e-6)
+        t = t - t.detach() + leaf["s"]
+        loss = (norm(t.masked_fill(none["s"], 0), leaf["wn"], 1e-6) * f64(do)).sum()
+        if dres is not None:
+            loss = loss + (t * f64(dres)).sum()
+        want = dict(zip(leaf, torch.autograd.grad(loss, tuple(leaf.values()))))
+        b = gdn.gdn_block_norm_bwd(dev(yy), dev(s), dout=dev(do), dres=dev(dres), **kw)
+        assert rows_rel(b["dresidual"], want["s"]) <= tol(dtype, TOL_NORM)
+        assert rows_rel(b["dy"], want["y"]) <= tol(dtype, TOL_NORM)
+        assert rows_rel(b["dpost_weight"][None], want["wp"][None]) <= TOL_NORM
+        assert rows_rel(b["dpre_weight"][None], want["wn"][None]) <= TOL_NORM
+        if gate is not None:
+            assert rows_rel(b["dgate"], want["g"]) <= tol(dtype, TOL_NORM)
+
+
+def test_block_norm_gradient_with_a_small_eps():
+    """Rows of zeros under a small eps, whose inverse root's third power fp32 does not hold: the gradient is gw / sqrt(eps)."""
+    y, do, w = torch.zeros(1, 2, 64, device=DEV), dev(randn((1, 2, 64), F32, 230)), torch.ones(64, device=DEV)
+    b = gdn.gdn_block_norm_bwd(y, y, dres=do, post_weight=w, eps=1e-30)
+    assert rows_rel(b["dy"], f64(do) * 1e15) <= TOL_NORM
