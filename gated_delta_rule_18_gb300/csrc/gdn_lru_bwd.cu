@@ -134,8 +134,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
                         continue;
                     }
                 }
-                run.A = mul2(run.A, a[j]), run.H = fma2(a[j], run.H, b[j]);
-                if (whole || open) back = fma2(run.A, gd, back);
+                run.H = fma2(a[j], run.H, b[j]);
+                // (behind a cut A stays -0: a decay that is NaN would take the mark off)
+                if (whole || open) run.A = mul2(run.A, a[j]), back = fma2(run.A, gd, back);
             }
         };
         if (HOW == kLruWide && near && all_inside) gates(std::true_type(), std::bool_constant<HOW == kLruWide>());

@@ -11,8 +11,8 @@ import pytest
 import torch
 
 import gated_delta_rule_18_gb300 as gdn
-from test_block_gpu import TOL_NORM, block_inputs, norm, ref_block, tol
-from test_layer_gpu import BF, DEV, F32, F64, built, dev, f64, randn  # noqa: F401
+from test_block_gpu import TOL_NORM, block_inputs, lru_inputs, norm, ref_block, tol
+from test_layer_gpu import BF, DEV, F32, F64, built, cu_of, dev, f64, randn, spans  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +70,38 @@ def test_block_norm_gradient_with_a_small_eps():
     y, do, w = torch.zeros(1, 2, 64, device=DEV), dev(randn((1, 2, 64), F32, 230)), torch.ones(64, device=DEV)
     b = gdn.gdn_block_norm_bwd(y, y, dres=do, post_weight=w, eps=1e-30)
     assert rows_rel(b["dy"], f64(do) * 1e15) <= TOL_NORM
+
+
+# ------------------------------------------------------ gated recurrence ---
+
+
+@pytest.mark.parametrize("lens,at", [
+    ([70, 3, 500, 27], 75),       # a sequence starts at 73, in a run of eight from 72: 12 tiles, a cluster
+    ([20, 40], 22),               # one tile
+    ([3, 2, 2, 90, 5], 6),        # several in a run; the second to last of those before it
+    ([64, 64, 64], 65), ([1] * 40, 17), ([13, 650, 20], 664), ([700, 9, 3000, 1], 703), ([2500, 64, 1], 2502)])
+@pytest.mark.parametrize("where", ["x", "r", "i", "z", "dout"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_lru_non_finite_values_beside_a_cut(lens, at, where, dtype):
+    """A NaN among the first tokens of a packed sequence, in the run of tokens in which it begins: the sequences before and
+    behind keep their outputs and gradients to the bit."""
+    T, C = sum(lens), 70
+    x, r, i, lam, z, h0, n = lru_inputs(1, T, C, lens, dtype, True, seed=240)
+    do, dh = randn((1, T, C), dtype, 250), randn((n, C), F32, 251)
+    (seq, (_, p, q)), = [(k, s) for k, s in enumerate(spans(1, T, lens)) if s[1] <= at < s[2]]
+    cu, out = dev(cu_of(lens)), []
+    for value in (0.5, float("nan")):
+        dict(x=x, r=r, i=i, z=z, dout=do)[where][0, at] = value
+        args, kw = [dev(t) for t in (x, r, i, lam)], dict(z=dev(z), h0=dev(h0), cu_seqlens=cu)
+        final, ck = torch.empty(n, C, device=DEV), torch.empty(1, (T + 63) // 64, C, device=DEV)
+        y = gdn.gdn_lru_fwd(*args, h_final=final, checkpoints=ck, **kw)
+        b = gdn.gdn_lru_bwd(*args, dev(do), dh_final=dev(dh), checkpoints=ck, **kw)
+        out.append(([y] + [b[k] for k in ("dx", "dr", "di", "dz")], [final, b["dh0"]]))
+    rest = torch.ones(T, dtype=torch.bool)
+    rest[p:q] = False
+    for a, b in zip(out[0][0], out[1][0]):
+        assert torch.equal(a[0, dev(rest)], b[0, dev(rest)])
+    rest = [k for k in range(n) if k != seq]
+    for a, b in zip(out[0][1], out[1][1]):
+        assert torch.equal(a[rest], b[rest])
+    assert not all(a.isfinite().all() for a in out[1][0])
