@@ -604,8 +604,9 @@ def gdn_set_fused(on: bool = True) -> None:
 
 def gdn_set_stall_test(cta: int = -1, limit_us: int = 1000) -> None:
     """Testing aid of the time-out path (see include/gdn.h): block `cta` of
-    later intra-chunk and state-pass launches stalls, gives up after about
-    limit_us and reports a time-out; cta < 0 turns it off."""
+    later intra-chunk and state-pass launches and of the gated recurrence's
+    stalls, gives up after about limit_us and reports a time-out; cta < 0 turns
+    it off."""
     lib().gdn_set_stall_test(int(cta), int(limit_us))
 
 

@@ -310,7 +310,9 @@ def gdn_lru_fwd(x, r, i, lam, z=None, c=8.0, h0=None, cu_seqlens=None, h_final=N
     silu(z) (h without z). x, r, i, z (B, T, C); lam (C) fp32; h0 / h_final
     (n_seq, C) fp32; cu_seqlens int32 (n_seq + 1) with B == 1; checkpoints (B,
     ceil(T / LRU_TILE), C) fp32, written: the states gdn_lru_bwd starts its
-    tiles from. out may be x, r, i or z. Returns out."""
+    tiles from. out may be x, r, i or z. workspace: 256 bytes, whose error word
+    (gdn_last_device_error) tells of malformed cu_seqlens and of a wait that ran
+    out, which leaves NaN. Returns out."""
     if stream is not None or _elsewhere(x):
         with _guard(x, stream):
             return gdn_lru_fwd(x, r, i, lam, z, c, h0, cu_seqlens, h_final, checkpoints, out, workspace)
@@ -326,7 +328,7 @@ def gdn_lru_fwd(x, r, i, lam, z=None, c=8.0, h0=None, cu_seqlens=None, h_final=N
     else:
         at = _act(out, "out", shape, x)
     ws = wp = wn = 0
-    if cp:
+    if cp or workspace is not None:
         ws, wp, wn = _workspace(workspace, 256, x)
     f = torch.float32
     st = L.gdn_lru_fwd(*_act(x, "x", shape, x), *_act(r, "r", shape, x), *_act(i, "i", shape, x), _flat(lam, "lam", (C,), f, x),

@@ -24,9 +24,6 @@ namespace {
 
 using namespace gdn;  // launch(), its kinds, FwdParams
 
-// the testing aid of gdn_set_stall_test (-1: off)
-std::atomic<int> g_stall_cta{-1}, g_stall_us{1000};
-
 // ------------------------------------------------------------- workspace ---
 
 constexpr size_t kAlign = 256;
@@ -269,8 +266,8 @@ gdn_status fwd_setup(const void *q, const void *k, gdn_tensor_desc qkd, const vo
     p.snap_ld = (L.Vt + 7) / 8 * 8;
     p.max_chunks = L.max_chunks;
     p.n_vt = L.n_vt;
-    p.stall_cta = g_stall_cta.load();
-    p.stall_us = g_stall_us.load();
+    p.stall_cta = stall_test_set().cta.load();
+    p.stall_us = stall_test_set().us.load();
     return GDN_OK;
 }
 
@@ -1167,8 +1164,8 @@ void gdn_set_state_tile(int bv) { gdn::set_state_tile(bv); }
 void gdn_set_fused(int on) { gdn::set_fused(on); }
 
 void gdn_set_stall_test(int cta, int limit_us) {
-    g_stall_us.store(limit_us > 0 ? limit_us : 1);
-    g_stall_cta.store(cta >= 0 ? cta : -1);
+    stall_test_set().us.store(limit_us > 0 ? limit_us : 1);
+    stall_test_set().cta.store(cta >= 0 ? cta : -1);
 }
 
 void gdn_profile_enable(int on) {

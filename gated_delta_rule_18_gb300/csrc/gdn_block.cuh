@@ -82,7 +82,9 @@ struct LruParams {
     int how;    // rows of all activations lie on 16 bytes (0), on words in pairs (1) or anywhere (2)
     int ranks;  // CTAs of a cluster, which take a line's tiles in turn
     int warps;  // of a CTA (the forward over wide rows): 4 or 8
-    int *err;
+    int *err;   // or null: the call's error word
+    int first;  // the call's first kernel: it clears the word and checks cu
+    int wait_us, stall_cta;  // limit of a wait; testing aid: a CTA whose waits run out (-1: none)
     // gradient; activations' gradients contiguous in x's type
     const void *dout;
     int64_t do_sb, do_st;

@@ -245,6 +245,8 @@ gdn_status lru_setup(const void *x, int64_t x_sb, int64_t x_st, const void *r, i
     p.x = x, p.x_sb = x_sb, p.x_st = x_st, p.r = r, p.r_sb = r_sb, p.r_st = r_st, p.i = i, p.i_sb = i_sb, p.i_st = i_st;
     p.lam = lam, p.z = z, p.z_sb = z_sb, p.z_st = z_st, p.c = c, p.h0 = h0, p.cu = cu, p.n_seq = n_seq;
     p.B = B, p.T = T, p.C = C, p.bf16 = dtype == GDN_BF16;
+    p.first = 1, p.stall_cta = stall_test_set().cta.load();
+    p.wait_us = p.stall_cta >= 0 ? stall_test_set().us.load() : 500000;
     return GDN_OK;
 }
 }  // namespace
@@ -277,7 +279,7 @@ gdn_status gdn_lru_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
     p.how = rows.how(C, dtype);
     const LruShape shape = lru_shape(B, T, C, p.bf16, p.how == 0);
     p.ranks = shape.ranks, p.warps = shape.warps;
-    p.err = cu_seqlens ? static_cast<int *>(workspace) : nullptr;
+    p.err = ws_ok(workspace, ws_bytes, kAlign) ? static_cast<int *>(workspace) : nullptr;
     return cuda_status(launch(KLru, stream, [&] { return launch_lru(p, stream); }));
 }
 
@@ -312,7 +314,7 @@ gdn_status gdn_lru_bwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
     const LruWs L = lru_bwd_ws(B, T, C, checkpoints != nullptr);
     if (!ws_ok(workspace, ws_bytes, L.total)) return GDN_ERR_WORKSPACE;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
-    p.err = cu_seqlens ? reinterpret_cast<int *>(ws) : nullptr;
+    p.err = reinterpret_cast<int *>(ws);
     p.how = rows.how(C, dtype);
     cudaError_t e = cudaSuccess;
     p.ck = const_cast<float *>(checkpoints);
@@ -323,6 +325,7 @@ gdn_status gdn_lru_bwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
         const LruShape shape = lru_shape(B, T, C, p.bf16, p.how == 0);
         f.ranks = shape.ranks, f.warps = shape.warps;
         e = launch(KLru, stream, [&] { return launch_lru(f, stream); });
+        p.first = 0;
     }
     p.dout = dout, p.do_sb = dout_sb, p.do_st = dout_st, p.dh_final = dh_final;
     p.dx = dx, p.dr = dr, p.di = di, p.dz = dz, p.dlam = dlam, p.dh0 = dh0;

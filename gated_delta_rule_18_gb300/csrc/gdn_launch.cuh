@@ -50,6 +50,15 @@ inline std::atomic<long long> &launches() {
     return n;
 }
 
+// the testing aid of gdn_set_stall_test (-1: off)
+struct StallTest {
+    std::atomic<int> cta{-1}, us{1000};
+};
+inline StallTest &stall_test_set() {
+    static StallTest s;
+    return s;
+}
+
 inline cudaEvent_t take_event(Profiler &P) {
     if (!P.pool.empty()) {
         cudaEvent_t e = P.pool.back();

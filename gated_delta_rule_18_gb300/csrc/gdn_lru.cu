@@ -54,8 +54,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_kernel(const LruParams p, 
     const int K = p.ranks, rank = blockIdx.x % K, line = blockIdx.y;
     const int c0 = (blockIdx.x / K) * kLruCh, c = c0 + 2 * lane, nc = p.C - c;  // nc: channels of the pair that exist
     const f32x2 one = pack2(1.f, 1.f), zero = pack2(0.f, 0.f);
+    lru_begin<PACKED>(p);
     if (PACKED) {
-        if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
         if (p.h_final && rank == 0) {  // sequences without tokens keep their states
             for (int s = warp; s < p.n_seq; s += W)
                 if (p.cu[s + 1] <= p.cu[s]) lru_st_state(p.h_final, s, p.C, c, nc, lru_ld_state(p.h0, s, p.C, c, nc));
@@ -80,21 +80,38 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_kernel(const LruParams p, 
         if (Z && n < steps) zs.copy(z_stage, first(n), p.T - first(n), smem_u32(&bars[warp][1]));
         else cp_async_commit();
     };
-    fetch(0), fetch_z(0);
+    const bool stalled = lru_stalled(p);
+    if (!stalled) fetch(0);
+    fetch_z(0);
     const LruDecay decay(p.lam + c, p.c, nc);
     const bool near = decay.near(nc);
     f32x2 carry = PACKED ? zero : lru_ld_state(p.h0, line, p.C, c, nc);  // the state before the cluster's tiles
-    bool lost = false;
+    int lost = 0, n = 0;
+    const f32x2 nan = pack2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
+    auto lose = [&](int n) {  // this warp's tokens of step n
+        const int t0 = first(n), len = min(max(p.T - t0, 0), L);
+        LruMarks m{0u, 0u};
+        if (PACKED) m = lru_marks<L>(p.cu, p.n_seq, p.T, t0);
+        if (p.ck && warp * L % kLruTile == 0 && t0 < p.T)
+            lru_st_state(p.ck, (int64_t)line * ((p.T + kLruTile - 1) / kLruTile) + t0 / kLruTile, p.C, c, nc, nan);
+#pragma unroll 1
+        for (int j = 0; j < len; ++j) {
+            if (p.out && nc > 0) lru_put<T, HOW>(out + (int64_t)(t0 + j) * p.o_st, nan, nc);
+            if (PACKED && p.h_final && m.fin >> j & 1)
+                lru_st_state(p.h_final, lru_seq(p.cu, p.n_seq, p.T, t0 + j), p.C, c, nc, nan);
+        }
+    };
     if (K > 1) {
         ranks.init();
         cluster_sync();
     }
 #pragma unroll 1
-    for (int n = 0; n < steps; ++n) {
+    for (; n < steps; ++n) {
         const int t0 = first(n), len = min(max(p.T - t0, 0), L), flip = n & 1;
         LruMarks m{0u, 0u};
         if (PACKED) m = lru_marks<L>(p.cu, p.n_seq, p.T, t0);
-        if (!xri.template wait<1>(smem_u32(&bars[warp][0]), n & 1)) lost = true;
+        if (!xri.template wait<1>(smem_u32(&bars[warp][0]), n & 1, p.wait_us)) lost |= kLostRows;
+        if (HOW != kLruWide && stalled) lost |= kLostRuns;
         auto get = [&](int k, int j) { return lru_pair(stage + 2 * lane + k * M::kRows + j * kLruCh); };  // a pair of x, r or i
         f32x2 a[L], b[L];
         LruRun run{one, zero};
@@ -121,8 +138,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_kernel(const LruParams p, 
         else gates(std::false_type(), std::false_type());
         runs[flip][warp][lane] = run;
         __syncwarp();  // every lane has read what the next copies overwrite
-        fetch(n + 1);
-        __syncthreads();
+        if (!(lost & kLostRows)) fetch(n + 1);
+        if (__syncthreads_or(lost)) break;
         f32x2 h = carry;
         if (K > 1) {
             if (warp == 0) {
@@ -134,7 +151,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_kernel(const LruParams p, 
                 }
                 ranks.send(n, rank, all);
             }
-            if (!lost && !ranks.wait(n)) lost = true;  // (once is enough)
+            if (!ranks.wait(n, p.wait_us)) lost |= kLostRuns;
 #pragma unroll 8
             for (int k = 0; k < ranks.places; ++k) {
                 const LruRun v = ranks.at(n, k);
@@ -157,8 +174,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_kernel(const LruParams p, 
         }
         if (p.ck && warp * L % kLruTile == 0 && t0 < p.T)
             lru_st_state(p.ck, (int64_t)line * ((p.T + kLruTile - 1) / kLruTile) + t0 / kLruTile, p.C, c, nc, h);
-        if (Z && !zs.template wait<1>(smem_u32(&bars[warp][1]), n & 1)) lost = true;
-        if (lost) h = carry = pack2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
+        if (Z && !zs.template wait<1>(smem_u32(&bars[warp][1]), n & 1, p.wait_us)) lost |= kLostZ;
         T *o = out + (int64_t)t0 * p.o_st;
         auto walk = [&](auto form) {
             constexpr bool whole = decltype(form)::value;
@@ -181,7 +197,21 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_kernel(const LruParams p, 
             else walk(std::false_type());
         }
         __syncwarp();  // every lane is through with the stages
-        fetch_z(n + 1);
+        if (!(lost & kLostZ)) fetch_z(n + 1);
+    }
+    if (n < steps || __any_sync(0xffffffffu, lost)) {
+        if (lost && p.err) atomicOr(p.err, kDevErrTimeout);
+        carry = nan;
+        const int from = lost & (kLostRuns | kLostZ) ? max(n - 1, 0) : n;
+        if (HOW != kLruWide) {
+            cp_async_wait<0>();
+        } else if (lane == 0) {  // (of the last copies that were asked for)
+            const int left = n < steps ? n : steps - 1, rows = n < steps && !(lost & kLostRows) ? min(n + 1, steps - 1) : left;
+            lru_wait(smem_u32(&bars[warp][0]), rows & 1, p.wait_us);
+            if (Z) lru_wait(smem_u32(&bars[warp][1]), (n < steps && lost & kLostZ ? n - 1 : left) & 1, p.wait_us);
+        }
+#pragma unroll 1
+        for (n = from; n < steps; ++n) lose(n);
     }
     if (!PACKED && p.h_final && rank == 0 && warp == 0) lru_st_state(p.h_final, line, p.C, c, nc, carry);
     if (K > 1) cluster_sync();  // no CTA leaves before all have what it sent

@@ -131,8 +131,42 @@ constexpr int kLruRanks = 16;  // most CTAs of a cluster
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Waits for a phase of a barrier of this CTA; false after about half a second.
-__device__ __forceinline__ bool lru_wait(uint32_t bar, uint32_t parity) { return wait_bar(bar, parity, nullptr); }
+// Waits for a phase of a barrier of this CTA; false after the limit.
+__device__ __forceinline__ bool lru_wait(uint32_t bar, uint32_t parity, int limit_us) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((it & 255) == 0) {
+            const uint64_t t = now_ns();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > (uint64_t)limit_us * 1000u) return false;
+        }
+    }
+}
+// What a warp has given up waiting for. The CTA agrees at the next barrier of the
+// walk, before anything that follows from what did not come is passed on, and
+// leaves the walk: the warp's tokens of the step in which it gave up, the rest of
+// the CTA's tokens and its states become NaN. It sends no more runs, so that the
+// other CTAs of the cluster, whose places it may not write any longer, run into
+// their own limits. A CTA gives up once and waits (once more, at most) for its
+// copies in flight.
+enum { kLostRows = 1, kLostRuns = 2, kLostZ = 4 };
+// the error word: cleared, with a packed batch's bounds checked, by the call's first kernel
+template <bool PACKED>
+__device__ __forceinline__ void lru_begin(const LruParams &p) {
+    if (!p.err || !p.first || blockIdx.x != 0 || blockIdx.y != 0) return;
+    if (PACKED) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
+    else if (threadIdx.x == 0) *p.err = 0;
+}
+__device__ __forceinline__ bool lru_stalled(const LruParams &p) {
+    return p.stall_cta >= 0 && (int64_t)blockIdx.y * gridDim.x + blockIdx.x == p.stall_cta;
+}
 // The runs of the cluster's CTAs in a step. They are sent by asynchronous
 // stores that count their bytes on the receiver's barrier: no fence, and no
 // wait for a CTA's outputs on their way to memory, as a barrier of the cluster
@@ -167,7 +201,7 @@ struct LruRanks {
                 "r"(__float_as_uint(H.y))
                 : "memory");
     }
-    __device__ __forceinline__ bool wait(int n) const { return lru_wait(smem_u32(&bar[n & 1]), n >> 1 & 1); }
+    __device__ __forceinline__ bool wait(int n, int limit_us) const { return lru_wait(smem_u32(&bar[n & 1]), n >> 1 & 1, limit_us); }
 };
 
 // --------------------------------------------------------- staging ----------
@@ -256,9 +290,9 @@ struct LruFetch {
     }
     // the copy that is followed by LATER others has arrived
     template <int LATER>
-    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int limit_us) const {
         bool ok = true;
-        if constexpr (HOW == kLruWide) ok = lru_wait(bar, parity);
+        if constexpr (HOW == kLruWide) ok = lru_wait(bar, parity, limit_us);
         else cp_async_wait<LATER>();
         __syncwarp();
         return ok;

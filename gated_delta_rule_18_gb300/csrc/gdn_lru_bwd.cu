@@ -24,11 +24,11 @@
 namespace gdn {
 namespace {
 
-// L tokens a warp, W warps, S stages.
-// shared memory: the stages of the tensors by warp, the warps' runs both ways, the ranks'
-template <typename T, bool Z, int L, int W, int S>
+// L tokens a warp, W warps.
+// shared memory: the stage of the tensors by warp, the warps' runs both ways, the ranks'
+template <typename T, bool Z, int L, int W>
 struct LruBwdSmem {
-    static constexpr int kTensors = Z ? 5 : 4, kRows = L * kLruCh, kStage = kTensors * kRows, kWarp = S * kStage;
+    static constexpr int kTensors = Z ? 5 : 4, kRows = L * kLruCh, kWarp = kTensors * kRows;
     static constexpr bool kInPlace = sizeof(T) == 4;  // the gates take the places of r and i
     static constexpr int kGates = W * kWarp * (int)sizeof(T);
     static constexpr int kRuns = kGates + (kInPlace ? 0 : W * L * 32 * (int)sizeof(uint4)), kBacks = kRuns + 2 * W * 32 * (int)sizeof(LruRun);
@@ -36,11 +36,11 @@ struct LruBwdSmem {
     static constexpr int bytes(int K) { return kRanks + 2 * LruRanks::places_of(K) * 32 * (int)sizeof(LruRun); }
 };
 
-template <typename T, int HOW, bool PACKED, bool Z, int L, int W, int S>
+template <typename T, int HOW, bool PACKED, bool Z, int L, int W>
 __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams p, const __grid_constant__ LruMaps maps) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ unsigned long long bars[W][S], rank_bars[2];
-    using M = LruBwdSmem<T, Z, L, W, S>;
+    __shared__ unsigned long long bars[W], rank_bars[2];
+    using M = LruBwdSmem<T, Z, L, W>;
     constexpr int N = M::kTensors, kTile = W * L;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int K = p.ranks, rank = blockIdx.x % K, line = blockIdx.y;
@@ -49,8 +49,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
     auto backs = reinterpret_cast<f32x2(*)[W][32]>(smem + M::kBacks);  // what they add to the gradient before them
     const LruRanks ranks{reinterpret_cast<LruRun *>(smem + M::kRanks), rank_bars, K, LruRanks::places_of(K)};
     const f32x2 one = pack2(1.f, 1.f), zero = pack2(0.f, 0.f), minus = pack2(-1.f, -1.f);
+    lru_begin<PACKED>(p);
     if (PACKED) {
-        if (p.err && blockIdx.x == 0) ssm_check_cu(p.cu, p.n_seq, p.T, p.err);
         if (p.dh0 && rank == 0) {  // of sequences without tokens
             for (int s = warp; s < p.n_seq; s += W)
                 if (p.cu[s + 1] <= p.cu[s]) lru_st_state(p.dh0, s, p.C, c, nc, lru_ld_state(p.dh_final, s, p.C, c, nc));
@@ -67,32 +67,49 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
     const LruFetch<T, HOW, N, L> rows(base, stride, maps.m, c0, line, p.C);
     T *const stage = (T *)smem + warp * M::kWarp;
     uint4 *const gates_at = reinterpret_cast<uint4 *>(smem + M::kGates) + warp * L * 32 + lane;
-    if (lane == 0) lru_init_bars(bars[warp], S);
+    if (lane == 0) lru_init_bars(&bars[warp], 1);
     __syncwarp();
     auto first = [&](int n) { return ((steps - 1 - n) * K + rank) * kTile + warp * L; };
     auto fetch = [&](int n) {
-        if (n < steps) rows.copy(stage + n % S * M::kStage, first(n), p.T - first(n), smem_u32(&bars[warp][n % S]));
+        if (n < steps) rows.copy(stage, first(n), p.T - first(n), smem_u32(&bars[warp]));
         else cp_async_commit();
     };
-    fetch(0);
+    const bool stalled = lru_stalled(p);
+    if (!stalled) fetch(0);
     const LruDecay decay(p.lam + c, p.c, nc);
     const bool near = decay.near(nc);
     // a g of the token behind the cluster's tiles
     f32x2 carry = PACKED ? zero : lru_ld_state(p.dh_final, line, p.C, c, nc), dlam = zero;
-    bool lost = false;
+    int lost = 0, n = 0;
+    const f32x2 nan = pack2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
+    auto lose = [&](int n) {  // this warp's tokens of step n
+        const int t0 = first(n), len = min(max(p.T - t0, 0), L);
+        LruMarks m{0u, 0u};
+        if (PACKED) m = lru_marks<L>(p.cu, p.n_seq, p.T, t0);
+#pragma unroll 1
+        for (int j = 0; j < len; ++j) {
+            const int64_t at = ((int64_t)line * p.T + t0 + j) * p.C + c;
+            if (nc > 0) {
+                lru_put<T, HOW>((T *)p.dx + at, nan, nc), lru_put<T, HOW>((T *)p.dr + at, nan, nc);
+                lru_put<T, HOW>((T *)p.di + at, nan, nc);
+                if (Z) lru_put<T, HOW>((T *)p.dz + at, nan, nc);
+            }
+            if (PACKED && p.dh0 && m.cut >> j & 1) lru_st_state(p.dh0, lru_seq(p.cu, p.n_seq, p.T, t0 + j), p.C, c, nc, nan);
+        }
+    };
     if (K > 1) {
         ranks.init();
         cluster_sync();
     }
 #pragma unroll 1
-    for (int n = 0; n < steps; ++n) {
+    for (; n < steps; ++n) {
         const int t0 = first(n), len = min(max(p.T - t0, 0), L), flip = n & 1, tile = t0 / kLruTile;
         LruMarks m{0u, 0u};
         if (PACKED) m = lru_marks<L>(p.cu, p.n_seq, p.T, t0);
         f32x2 h = tile < tiles ? lru_ld_state(p.ck, (int64_t)line * tiles + tile, p.C, c, nc) : zero;
-        if (S == 2) fetch(n + 1);  // (its place was read a step ago)
-        if (!rows.template wait<S - 1>(smem_u32(&bars[warp][n % S]), n / S & 1)) lost = true;
-        T *const staged = stage + n % S * M::kStage + 2 * lane;
+        if (!rows.template wait<0>(smem_u32(&bars[warp]), n & 1, p.wait_us)) lost |= kLostRows;
+        if (HOW != kLruWide && stalled) lost |= kLostRuns;
+        T *const staged = stage + 2 * lane;
         auto get = [&](int k, int j) { return lru_pair(staged + k * M::kRows + j * kLruCh); };  // of x, r, i, dout, z
         const bool all_inside = len == L && !(m.cut | m.fin);
         f32x2 a[L], b[L], back = zero;
@@ -143,7 +160,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
         else if (all_inside) gates(std::true_type(), std::false_type());
         else gates(std::false_type(), std::false_type());
         runs[flip][warp][lane] = run, backs[flip][warp][lane] = back;
-        __syncthreads();
+        if (__syncthreads_or(lost)) break;
         f32x2 gm = carry;  // a g of the token behind this one
         if (K > 1) {
             if (warp == 0) {
@@ -169,7 +186,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
         for (int j = 0; j < L; ++j)  // b becomes h (it stays where tokens end)
             h = b[j] = PACKED && m.cut >> j & 1 ? b[j] : fma2(a[j], h, b[j]);
         if (K > 1) {
-            if (!lost && !ranks.wait(n)) lost = true;  // (once is enough)
+            if (!ranks.wait(n, p.wait_us)) lost |= kLostRuns;
 #pragma unroll 8
             for (int k = ranks.places - 1; k >= 0; --k) {
                 const LruRun v = ranks.at(n, k);
@@ -188,7 +205,6 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
                 carry = lru_apply2<PACKED>(runs[flip][w][lane].A, backs[flip][w][lane], carry);
             }
         }
-        if (lost) gm = carry = pack2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
         const int64_t at0 = ((int64_t)line * p.T + t0) * p.C + c;
         auto walk = [&](auto form) {
             constexpr bool whole = decltype(form)::value;
@@ -247,7 +263,15 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
         else walk(std::false_type());
         if (HOW == kLruWide) fence_async_smem();  // (what was kept in their places, before the copies)
         __syncwarp();  // every lane is through with the stage
-        if (S == 1) fetch(n + 1);
+        fetch(n + 1);
+    }
+    if (n < steps || __any_sync(0xffffffffu, lost)) {
+        if (lost && p.err) atomicOr(p.err, kDevErrTimeout);
+        carry = dlam = nan;
+        // (rows that did arrive have none behind them)
+        if (HOW == kLruWide && lane == 0 && lost & kLostRows) lru_wait(smem_u32(&bars[warp]), n & 1, p.wait_us);
+#pragma unroll 1
+        for (n = lost & kLostRuns ? max(n - 1, 0) : n; n < steps; ++n) lose(n);
     }
     if (!PACKED && p.dh0 && rank == 0 && warp == 0) lru_st_state(p.dh0, line, p.C, c, nc, carry);
     // the channels' sums over the warps, in one order
@@ -274,12 +298,12 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
 
 cudaError_t launch_lru_bwd(const LruParams &p, cudaStream_t st) {
     LruMaps m{};
-    constexpr int L = 8, W = 8, S = 1;
+    constexpr int L = 8, W = 8;
     const int how = p.how == kLruWide && !lru_maps(p, true, L, &m) ? (int)kLruWords : p.how;
     return lru_by_form(p, how, p.z != nullptr, [&](auto type, auto how, auto packed, auto z) {
         using T = decltype(type);
-        const int smem = LruBwdSmem<T, z(), L, W, S>::bytes(p.ranks);
-        return lru_launch((const void *)lru_bwd_kernel<T, how(), packed(), z(), L, W, S>, W, smem, p, m, st);
+        const int smem = LruBwdSmem<T, z(), L, W>::bytes(p.ranks);
+        return lru_launch((const void *)lru_bwd_kernel<T, how(), packed(), z(), L, W>, W, smem, p, m, st);
     });
 }
 

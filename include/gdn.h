@@ -762,9 +762,13 @@ gdn_status gdn_block_norm_bwd(const void *y, int64_t y_st, int y_dtype,
  *   x, r, i, z, out: (B, T, C) of `dtype`; lam (C) fp32; c >= 0.
  *   h0, h_final: (n_seq, C) fp32 or NULL. checkpoints: (B, ceil(T / 64), C)
  *   fp32 or NULL: the state before every 64th token, for the gradient.
- *   out may lie on x, r, i or z. workspace: 256 bytes, needed with cu_seqlens
- *   only. A state that is not finite stays so in its channel to its sequence's
- *   end. A wait inside the kernel that runs out (half a second) leaves NaN.
+ *   out may lie on x, r, i or z. workspace: 256 bytes, needed with cu_seqlens;
+ *   its error word (gdn_last_device_error) is this call's. A state that is not
+ *   finite stays so in its channel to its sequence's end. A wait inside the
+ *   kernel that runs out (half a second) is reported as GDN_DEVERR_TIMEOUT in the
+ *   error word, where there is a workspace, and leaves NaN: a CTA writes NaN for
+ *   all that it has not finished (outputs, checkpoints, states), and so do
+ *   those that wait for what it knows.
  */
 #define GDN_LRU_TILE 64 /* tokens a checkpoint stands for */
 gdn_status gdn_lru_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
@@ -781,7 +785,8 @@ gdn_status gdn_lru_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
  * h_final). dx, dr, di, dz (B, T, C) in `dtype`, contiguous; dlam (C), dh0
  * (n_seq, C) fp32. dz goes with z; dh0 may be NULL. checkpoints: the
  * forward's for the same inputs, or NULL: they are formed again. Every sum
- * has a fixed order: results repeat bit for bit.
+ * has a fixed order: results repeat bit for bit. Malformed cu_seqlens and waits
+ * that run out are reported and leave NaN as in the forward (dlam, too).
  *   workspace: gdn_lru_bwd_workspace_size(B, T, C, with_checkpoints) bytes.
  */
 size_t gdn_lru_bwd_workspace_size(int B, int T, int C, int with_checkpoints);
@@ -811,7 +816,7 @@ const char *gdn_status_string(gdn_status s);
 
 /*
  * gdn_last_device_error -- synchronise `stream`, read the device error word
- * that gdn_chunk_fwd keeps in `workspace`, store it in *word (GDN_DEVERR_*
+ * that a call (gdn_chunk_fwd, say) keeps in `workspace`, store it in *word (GDN_DEVERR_*
  * bits, may be NULL) and clear it. Returns GDN_ERR_TIMEOUT if a bounded
  * wait gave up, GDN_ERR_DEVICE for other set bits, GDN_ERR_CUDA on a CUDA
  * failure, else GDN_OK. The word describes the last call that used this
@@ -871,7 +876,9 @@ void gdn_set_fused(int on);
  * barrier that nothing completes, gives up after about `limit_us`
  * microseconds, records GDN_DEVERR_TIMEOUT in the call's error word and
  * leaves without issuing any copy or tensor-core operation; every other
- * block works as usual (the call's results are then incomplete).
+ * block works as usual (the call's results are then incomplete). In launches of
+ * gdn_lru_fwd and gdn_lru_bwd the block asks for no rows, so that its wait for
+ * them runs out after `limit_us`, as do others' waits for what it knows.
  * cta < 0 turns it off (the default). Process-wide; affects later launches.
  */
 void gdn_set_stall_test(int cta, int limit_us);

@@ -105,3 +105,64 @@ def test_lru_non_finite_values_beside_a_cut(lens, at, where, dtype):
     for a, b in zip(out[0][1], out[1][1]):
         assert torch.equal(a[rest], b[rest])
     assert not all(a.isfinite().all() for a in out[1][0])
+
+
+@pytest.mark.parametrize("B,T,C,lens", [
+    (1, 50, 192, None), (3, 700, 192, None), (1, 2500, 128, None), (1, 2500, 128, [3, 0, 1900, 597]), (2, 2500, 126, None),
+    (1, 1500, 130, [700, 800]), (4, 300, 130, None)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cta", [0, 1, 7])
+def test_lru_waits_that_run_out(B, T, C, lens, dtype, cta):
+    """A CTA that asks for no rows (the library's testing aid) gives up after 20 ms: the error word says so, all that it or the
+    CTAs of its cluster would have written (one line of 64 channels) is NaN, the rest is right to the bit, and so is the
+    next call. Where rows go by words or elements there is no wait for them, and the CTA gives up without one."""
+    x, r, i, lam, z, h0, n = lru_inputs(B, T, C, lens, dtype, True, seed=260)
+    args, cu = [dev(t) for t in (x, r, i, lam)], dev(cu_of(lens))
+    kw = dict(z=dev(z), h0=dev(h0), cu_seqlens=cu)
+    do, dh = dev(randn((B, T, C), dtype, 270)), dev(randn((n, C), F32, 271))
+    ws = torch.zeros(gdn.lib().gdn_lru_bwd_workspace_size(B, T, C, 0), dtype=torch.uint8, device=DEV)
+
+    def forward():
+        final, ck = torch.zeros(n, C, device=DEV), torch.zeros(B, (T + 63) // 64, C, device=DEV)
+        y = gdn.gdn_lru_fwd(*args, h_final=final, checkpoints=ck, workspace=ws, **kw)
+        return dict(y=y, final=final, ck=ck)
+
+    saved = forward()["ck"]
+
+    def backward(**how):
+        return gdn.gdn_lru_bwd(*args, do, dh_final=dh, workspace=ws, **how, **kw)
+
+    for run, how in ((forward, {}), (backward, dict(checkpoints=saved)), (backward, {})):
+        want = run(**how)
+        assert gdn.gdn_last_device_error(ws) == 0
+        gdn.gdn_set_stall_test(cta, 20000)
+        try:
+            got = run(**how)
+            word = gdn.gdn_last_device_error(ws)
+        finally:
+            gdn.gdn_set_stall_test(-1, 0)
+        again = run(**how)
+        assert gdn.gdn_last_device_error(ws) == 0 and all(torch.equal(want[k], again[k]) for k in want)
+        lost = got["y" if run is forward else "dr"].isnan()
+        if not lost.any():  # (fewer CTAs than that)
+            assert word == 0
+            continue
+        assert word == 2
+        tiles = sorted({(line, c // 64) for line, c in lost.any(1).nonzero().tolist()})
+        here = torch.zeros(B, 1, C, dtype=torch.bool, device=DEV)
+        for line, c in tiles:
+            here[line, 0, 64 * c:64 * c + 64] = True
+        # without checkpoints the states are formed by a launch of its own, one of whose CTAs gives up, too: what follows
+        # from them (dr, dz, dlam) is NaN there as far as its states go
+        alone = run is forward or how
+        assert len(tiles) == 1 or (not alone and len(tiles) == 2)
+        for k in got:
+            if k == "dlam":
+                mine = here.any(0)[0]
+            elif k in ("final", "dh0"):
+                some = torch.ones(n, 1, dtype=torch.bool, device=DEV) if lens is None else dev(torch.tensor(lens) > 0)[:, None]
+                mine = (here[:, 0] if lens is None else here[0]).expand(n, C) & some
+            else:
+                mine = here.expand(got[k].shape)
+            assert not alone or got[k][mine].isnan().all(), k
+            assert torch.equal(got[k][~mine], want[k][~mine]), k
