@@ -719,11 +719,13 @@ __global__ void __launch_bounds__(kSumX *kSumY) block_norm_reduce_kernel(const B
 }
 
 // Stages of `row` bytes that leave `ctas` CTAs a SM: two or three.
-int stages_for(int row, int kept, int ctas) { return (3 * row + kept) * ctas <= 216 * 1024 ? 3 : 2; }
+constexpr int kMostSmem = 216 * 1024;
+int stages_for(int row, int kept, int ctas) { return (3 * row + kept) * ctas <= kMostSmem ? 3 : 2; }
+// (the limit is the kernel's, not the call's: a smaller call's own size would lower it under another thread's launch)
 template <class K>
 cudaError_t with_smem(K *k, int smem) {
     if (smem <= 40 * 1024) return cudaSuccess;  // 48 KB with the static part
-    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
 }
 template <typename TX, typename TR>
 cudaError_t norm_nv(BlockNormParams p, cudaStream_t st) {
@@ -777,7 +779,7 @@ cudaError_t norm_bwd_nv(BlockNormBwdParams p, cudaStream_t st) {
         if (s.nv == 1) return by_gate(std::integral_constant<int, 1>(), vec, vec);
         // (two rows of five tensors have to fit: not those of 8192 fp32 channels)
         const int x = sizeof(TX), r = sizeof(TR), row = kVecN * 2 * nt * (x * (1 + token + (p.pre ? 1 : 0)) + r * ((p.dres ? 1 : 0) + (p.pre ? 1 : 0)));
-        if (s.nv == 2 && 2 * row > 216 * 1024) return by_gate(std::integral_constant<int, 2>(), vec, std::false_type());
+        if (s.nv == 2 && 2 * row > kMostSmem) return by_gate(std::integral_constant<int, 2>(), vec, std::false_type());
         if (s.nv == 2) return by_gate(std::integral_constant<int, 2>(), vec, vec);
         return by_gate(std::integral_constant<int, 4>(), vec, std::false_type());
     };

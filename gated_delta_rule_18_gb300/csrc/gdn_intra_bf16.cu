@@ -688,7 +688,8 @@ cudaError_t launch_t(const FwdParams &p, cudaStream_t st) {
     const int VP = p.n_vt * 64;
     const size_t bytes = L::bytes(VP);
     auto kern = p.stall_cta >= 0 ? intra_kernel<PERKEY, true> : intra_kernel<PERKEY, false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    // (for the widest V: a smaller call's own size would lower the kernel's limit under another thread's launch)
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes(256));
     if (e != cudaSuccess) return e;
     // the whole shared-memory carveout, so that 4 (scalar) / 2 (per-key) CTAs fit per SM
     e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);

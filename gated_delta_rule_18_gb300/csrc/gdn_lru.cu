@@ -319,8 +319,9 @@ bool lru_maps(const LruParams &p, bool gradient, int len, LruMaps *m) {
            (!gradient || add(p.dout, p.do_sb, p.do_st)) && add(p.z, p.z_sb, p.z_st);
 }
 
-cudaError_t lru_launch(const void *kernel, int warps, int smem, const LruParams &p, const LruMaps &m, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+cudaError_t lru_launch(const void *kernel, int warps, int smem, int most, const LruParams &p, const LruMaps &m, cudaStream_t st) {
+    // (the limit is the kernel's, not the call's: a smaller call's own size would lower it under another thread's launch)
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e == cudaSuccess && p.ranks > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -342,7 +343,8 @@ cudaError_t launch_lru(const LruParams &p, cudaStream_t st) {
     return lru_by_form(p, how, p.z != nullptr, [&](auto type, auto how, auto packed, auto z) {
         using T = decltype(type);
         auto run = [&](auto w) {
-            return lru_launch((const void *)lru_kernel<T, how(), packed(), z(), w()>, w(), LruSmem<T, z(), w()>::bytes(p.ranks), p, m, st);
+            using S = LruSmem<T, z(), w()>;
+            return lru_launch((const void *)lru_kernel<T, how(), packed(), z(), w()>, w(), S::bytes(p.ranks), S::bytes(kLruRanks), p, m, st);
         };
         if constexpr (how() == kLruWide) {
             if (p.warps == 8) return run(std::integral_constant<int, 8>());

@@ -350,6 +350,7 @@ cudaError_t lru_by_form(const LruParams &p, int how, bool with_z, F &&f) {
 // the maps of a call's tensors, boxes of len tokens, into m; false where they have none (a stride
 // of zero): its rows are then copied by words
 bool lru_maps(const LruParams &p, bool gradient, int len, LruMaps *m);
-cudaError_t lru_launch(const void *kernel, int warps, int smem, const LruParams &p, const LruMaps &m, cudaStream_t st);
+// smem: what the call takes, most: what any of the kernel's calls does
+cudaError_t lru_launch(const void *kernel, int warps, int smem, int most, const LruParams &p, const LruMaps &m, cudaStream_t st);
 
 }  // namespace gdn

@@ -302,8 +302,8 @@ cudaError_t launch_lru_bwd(const LruParams &p, cudaStream_t st) {
     const int how = p.how == kLruWide && !lru_maps(p, true, L, &m) ? (int)kLruWords : p.how;
     return lru_by_form(p, how, p.z != nullptr, [&](auto type, auto how, auto packed, auto z) {
         using T = decltype(type);
-        const int smem = LruBwdSmem<T, z(), L, W>::bytes(p.ranks);
-        return lru_launch((const void *)lru_bwd_kernel<T, how(), packed(), z(), L, W>, W, smem, p, m, st);
+        using S = LruBwdSmem<T, z(), L, W>;
+        return lru_launch((const void *)lru_bwd_kernel<T, how(), packed(), z(), L, W>, W, S::bytes(p.ranks), S::bytes(kLruRanks), p, m, st);
     });
 }
 

@@ -439,9 +439,11 @@ cudaError_t norm_bwd_nv(const NormBwdParams &p, cudaStream_t st) {
     const unsigned grid = norm_bwd_parts(p.R, p.D) / s.rpb, nt = s.tpr * s.rpb;
     auto run = [&](auto nv, auto vec, auto ahead) -> cudaError_t {
         auto *k = rmsnorm_bwd_kernel<TS, TY, nv(), vec(), ahead()>;
-        const int smem = ahead() ? kRowsAhead<TS, TY> * nv() * (2 * sizeof(TS) + sizeof(TY)) * kVecN * nt : 0;
+        constexpr int each = ahead() ? kRowsAhead<TS, TY> * nv() * (2 * sizeof(TS) + sizeof(TY)) * kVecN : 0;
+        const int smem = each * nt;
         if (smem > 40 * 1024) {  // 48 KB with the static part
-            const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            // (of 512 threads: a smaller call's own size would lower the kernel's limit under another thread's launch)
+            const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, each * 512);
             if (e != cudaSuccess) return e;
         }
         k<<<grid, nt, smem, st>>>(p, s.tpr);

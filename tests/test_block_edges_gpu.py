@@ -6,6 +6,7 @@ steps of a cluster, forms of rows that few calls have.
 Tolerances as derived in test_block_gpu.py; others beside their tests.
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -166,3 +167,64 @@ def test_lru_waits_that_run_out(B, T, C, lens, dtype, cta):
                 mine = here.expand(got[k].shape)
             assert not alone or got[k][mine].isnan().all(), k
             assert torch.equal(got[k][~mine], want[k][~mine]), k
+
+
+# --------------------------------------------------------- as used together ---
+
+
+def _sizes_of(name):
+    """Two calls that one kernel takes with different amounts of shared memory."""
+    bf = dict(dtype=BF, device=DEV)
+    if name.startswith("lru"):
+        def call(T):
+            t, lam = torch.zeros(1, T, 64, **bf), torch.zeros(64, device=DEV)
+            ws = torch.zeros(gdn.lib().gdn_lru_bwd_workspace_size(1, T, 64, 0), dtype=torch.uint8, device=DEV)
+            if name == "lru_bwd":
+                return lambda: gdn.gdn_lru_bwd(t, t, t, lam, t, z=t, workspace=ws)
+            return lambda: gdn.gdn_lru_fwd(t, t, t, lam, z=t, out=torch.empty_like(t))
+        return call(1500), call(100)
+    if name.startswith("chunk"):
+        def call(V):
+            q, v, b = torch.zeros(1, 64, 1, 64, **bf), torch.zeros(1, 64, 1, V, **bf), torch.zeros(1, 64, 1, device=DEV)
+            gk = torch.zeros(1, 64, 1, 64, device=DEV) if name == "chunk_gk" else None
+            return lambda: gdn.gdn_chunk_fwd(q, q, v, b, g=None if gk is not None else b, gk=gk)
+        return call(256), call(64)
+
+    def call(D):
+        t, w = torch.zeros(2, D, **bf), torch.zeros(D, device=DEV)
+        if name == "rms_bwd":
+            return lambda: gdn.gdn_rmsnorm_bwd(t, w, t)
+        kw = dict(post_weight=w, pre_weight=w, gate=t, gate_act="silu")
+        if name == "block_bwd":
+            return lambda: gdn.gdn_block_norm_bwd(t, t, dout=t, dres=t, **kw)
+        return lambda: gdn.gdn_block_norm_fwd(t, t, **kw)
+    return call(8192), call(5120)
+
+
+@pytest.mark.parametrize("name", ["lru", "lru_bwd", "block", "block_bwd", "rms_bwd", "chunk", "chunk_gk"])
+def test_calls_of_different_sizes_on_two_threads(name):
+    """Each call sets what shared memory its kernel may take; a smaller call between another's setting and launch must not
+    lower it."""
+    calls, failed = _sizes_of(name), []
+    for call in calls:
+        call()
+    start = threading.Barrier(len(calls))
+
+    def work(call):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                start.wait()
+                for k in range(4000):
+                    call()
+                    if k % 500 == 0:
+                        torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
