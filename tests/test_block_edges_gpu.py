@@ -7,6 +7,7 @@ Tolerances as derived in test_block_gpu.py; others beside their tests.
 """
 import math
 import threading
+from fractions import Fraction
 
 import pytest
 import torch
@@ -16,6 +17,37 @@ from test_block_gpu import TOL_NORM, block_inputs, lru_inputs, norm, ref_block, 
 from test_layer_gpu import BF, DEV, F32, F64, built, cu_of, dev, f64, randn, spans  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- rotary ---
+
+
+def _two_pi(bits=320):
+    """2 pi by Machin's formula, to about `bits` bits."""
+    def arctan(x):
+        s = t = (1 << bits) // x
+        n, sign = 3, -1
+        while t:
+            t //= x * x
+            s += sign * (t // n)
+            n, sign = n + 2, -sign
+        return s
+    return Fraction(8 * (4 * arctan(5) - arctan(239)), 1 << bits)
+
+
+@pytest.mark.parametrize("p", [1, 2**30 + 1, 2**40 + 12345, 2**53 + 1, -2**53 - 1, 2**60 + 3, 2**62, -2**62, 2**63 - 1, -2**63])
+def test_rotary_far_positions_of_exact_frequencies(p):
+    """Frequencies as the doubles they are, reduced exactly. The kernel's 2 / pi is rounded to 64 bits: 0.0151 of its last
+    place, which is 1.28e-21 of it, so the angle is 1.3e-21 |p| f radians off, beside the fp32 result's 4e-7."""
+    f = torch.tensor([1.0, 0.5, 3.0, math.pi, 10000.0**-0.125, 1e-4, 1.5e-7, 2.0**-40], dtype=F64)
+    x = torch.zeros(1, 1, 1, 16)
+    x[..., :8] = 1.0
+    got = gdn.gdn_rotary(dev(x), dev(f), positions=torch.tensor([[p]], dtype=torch.int64, device=DEV)).cpu().to(F64)[0, 0, 0]
+    turn = _two_pi()
+    for k in range(8):
+        angle = float(p * Fraction(f[k].item()) % turn)
+        bound = 4e-7 + abs(p) * f[k].item() * 1.3e-21
+        assert abs(got[k] - math.cos(angle)) <= bound and abs(got[8 + k] - math.sin(angle)) <= bound, (k, bound)
 
 
 # ------------------------------------------------------------ block norm ---
