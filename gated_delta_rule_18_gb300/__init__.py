@@ -22,7 +22,7 @@ from .build import LIB
 __all__ = ["GDNError", "gdn_prep", "gdn_chunk_fwd", "gdn_chunk_fwd_noalloc",
            "gdn_merge", "gdn_frame_fwd", "gdn_frame_workspace_size", "gdn_workspace_size",
            "gdn_status_string", "gdn_last_device_error", "gdn_noalloc_last_device_error",
-           "gdn_set_stall_test", "gdn_set_fused", "gdn_forward", "lib",
+           "gdn_set_stall_test", "gdn_set_lru_cluster", "gdn_set_fused", "gdn_forward", "lib",
            "PREP_L2", "PREP_RMS", "PREP_RELU", "gdn_prep_bwd", "gdn_frame_bwd", "gdn_merge_bwd", "profile_enable", "profile_collect", "gdn_set_state_tile",
            "launch_count", "kernel_names", "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd", "gdn_conv_fwd", "gdn_conv_bwd",
            "gdn_conv_step", "gdn_ssm_fwd", "gdn_ssm_bwd", "gdn_ssm_step", "gdn_rotary", "rotary_frequencies",
@@ -139,6 +139,8 @@ def lib():
     L.gdn_last_device_error.argtypes = [P, P, ctypes.POINTER(I)]
     L.gdn_noalloc_last_device_error.restype = I
     L.gdn_noalloc_last_device_error.argtypes = [P, ctypes.POINTER(I)]
+    L.gdn_set_lru_cluster.restype = None
+    L.gdn_set_lru_cluster.argtypes = [I]
     L.gdn_set_stall_test.restype = None
     L.gdn_set_stall_test.argtypes = [I, I]
     L.gdn_set_fused.restype = None
@@ -600,6 +602,12 @@ def gdn_set_fused(on: bool = True) -> None:
     direction (on) or as the split intra-chunk + state passes (off, the
     default); see include/gdn.h."""
     lib().gdn_set_fused(int(bool(on)))
+
+
+def gdn_set_lru_cluster(most: int = 0) -> None:
+    """Most CTAs of a cluster in later launches of the gated recurrence; 0: by
+    the grid, the default (see include/gdn.h)."""
+    lib().gdn_set_lru_cluster(int(most))
 
 
 def gdn_set_stall_test(cta: int = -1, limit_us: int = 1000) -> None:

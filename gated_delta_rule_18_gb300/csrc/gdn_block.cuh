@@ -98,8 +98,10 @@ struct LruShape {
 };
 LruShape lru_shape(int lines, int T, int C, bool bf16, bool wide);
 int lru_bwd_ranks(int lines, int T, int C);
-cudaError_t launch_lru(const LruParams &p, cudaStream_t st);
-cudaError_t launch_lru_bwd(const LruParams &p, cudaStream_t st);
+// p.ranks may come back smaller: as many as fit
+cudaError_t launch_lru(LruParams &p, cudaStream_t st);
+cudaError_t launch_lru_bwd(LruParams &p, cudaStream_t st);
+void set_lru_cluster(int most);
 struct LruStepParams {
     const void *x, *r, *i, *z;  // (n, C); z or null
     int64_t x_st, r_st, i_st, z_st;

@@ -337,6 +337,8 @@ gdn_status gdn_lru_bwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
     return cuda_status(e);
 }
 
+void gdn_set_lru_cluster(int most) { set_lru_cluster(most); }
+
 gdn_status gdn_lru_step(const void *x, int64_t x_st, const void *r, int64_t r_st, const void *i, int64_t i_st,
                         const float *lam, const void *z, int64_t z_st, float c, float *state, const int32_t *slots,
                         int n_slots, void *out, int64_t out_st, int n, int C, int dtype, cudaStream_t stream) {

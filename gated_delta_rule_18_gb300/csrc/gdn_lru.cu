@@ -24,6 +24,7 @@
 // cluster every 1536 tokens.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "gdn_lru.cuh"
@@ -319,32 +320,43 @@ bool lru_maps(const LruParams &p, bool gradient, int len, LruMaps *m) {
            (!gradient || add(p.dout, p.do_sb, p.do_st)) && add(p.z, p.z_sb, p.z_st);
 }
 
-cudaError_t lru_launch(const void *kernel, int warps, int smem, int most, const LruParams &p, const LruMaps &m, cudaStream_t st) {
+static std::atomic<int> g_most{0};
+void set_lru_cluster(int most) { g_most.store(most > 0 ? most : 0); }
+
+cudaError_t lru_launch(const void *kernel, int warps, int (*smem)(int ranks), LruParams &p, const LruMaps &m, cudaStream_t st) {
     // (the limit is the kernel's, not the call's: a smaller call's own size would lower it under another thread's launch)
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e == cudaSuccess && p.ranks > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem(kLruRanks));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((p.C + kLruCh - 1) / kLruCh * p.ranks, p.B);
-    cfg.blockDim = dim3(32 * warps);
-    cfg.dynamicSmemBytes = smem, cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = p.ranks, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
-    cfg.attrs = &at, cfg.numAttrs = 1;
-    void *args[] = {const_cast<LruParams *>(&p), const_cast<LruMaps *>(&m)};
+    at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+    cfg.blockDim = dim3(32 * warps), cfg.stream = st, cfg.attrs = &at, cfg.numAttrs = 1;
+    const auto of = [&](int ranks) {
+        cfg.gridDim = dim3((p.C + kLruCh - 1) / kLruCh * ranks, p.B), cfg.dynamicSmemBytes = smem(ranks), at.val.clusterDim.x = ranks;
+    };
+    const int most = g_most.load(std::memory_order_relaxed);
+    if (most && p.ranks > most) p.ranks = most;
+    of(p.ranks);
+    if (p.ranks > 8) {  // eight are portable; more need a group of SMs that holds them, which not every GPU (or part of one) has
+        int n = 0;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        if (e != cudaSuccess) cudaGetLastError();  // (not the call's)
+        if (e != cudaSuccess || n < 1) p.ranks = 8, of(8);
+    }
+    void *args[] = {&p, const_cast<LruMaps *>(&m)};
     e = cudaLaunchKernelExC(&cfg, kernel, args);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-cudaError_t launch_lru(const LruParams &p, cudaStream_t st) {
+cudaError_t launch_lru(LruParams &p, cudaStream_t st) {
     LruMaps m{};
     const int how = p.how == kLruWide && !lru_maps(p, false, L, &m) ? (int)kLruWords : p.how;
     return lru_by_form(p, how, p.z != nullptr, [&](auto type, auto how, auto packed, auto z) {
         using T = decltype(type);
         auto run = [&](auto w) {
-            using S = LruSmem<T, z(), w()>;
-            return lru_launch((const void *)lru_kernel<T, how(), packed(), z(), w()>, w(), S::bytes(p.ranks), S::bytes(kLruRanks), p, m, st);
+            return lru_launch((const void *)lru_kernel<T, how(), packed(), z(), w()>, w(), LruSmem<T, z(), w()>::bytes, p, m, st);
         };
         if constexpr (how() == kLruWide) {
             if (p.warps == 8) return run(std::integral_constant<int, 8>());

@@ -350,7 +350,7 @@ cudaError_t lru_by_form(const LruParams &p, int how, bool with_z, F &&f) {
 // the maps of a call's tensors, boxes of len tokens, into m; false where they have none (a stride
 // of zero): its rows are then copied by words
 bool lru_maps(const LruParams &p, bool gradient, int len, LruMaps *m);
-// smem: what the call takes, most: what any of the kernel's calls does
-cudaError_t lru_launch(const void *kernel, int warps, int smem, int most, const LruParams &p, const LruMaps &m, cudaStream_t st);
+// smem: the shared memory of a CTA in a cluster of so many
+cudaError_t lru_launch(const void *kernel, int warps, int (*smem)(int ranks), LruParams &p, const LruMaps &m, cudaStream_t st);
 
 }  // namespace gdn

@@ -296,14 +296,13 @@ __global__ void __launch_bounds__(32 * W, 16 / W) lru_bwd_kernel(const LruParams
 
 }  // namespace
 
-cudaError_t launch_lru_bwd(const LruParams &p, cudaStream_t st) {
+cudaError_t launch_lru_bwd(LruParams &p, cudaStream_t st) {
     LruMaps m{};
     constexpr int L = 8, W = 8;
     const int how = p.how == kLruWide && !lru_maps(p, true, L, &m) ? (int)kLruWords : p.how;
     return lru_by_form(p, how, p.z != nullptr, [&](auto type, auto how, auto packed, auto z) {
         using T = decltype(type);
-        using S = LruBwdSmem<T, z(), L, W>;
-        return lru_launch((const void *)lru_bwd_kernel<T, how(), packed(), z(), L, W>, W, S::bytes(p.ranks), S::bytes(kLruRanks), p, m, st);
+        return lru_launch((const void *)lru_bwd_kernel<T, how(), packed(), z(), L, W>, W, LruBwdSmem<T, z(), L, W>::bytes, p, m, st);
     });
 }
 

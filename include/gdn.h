@@ -854,6 +854,14 @@ long long gdn_launch_count(void);
 void gdn_set_state_tile(int bv);
 
 /*
+ * Most CTAs of a cluster in gdn_lru_fwd and gdn_lru_bwd, which take a line's
+ * tiles side by side. most <= 0 (the default): by the grid, up to 16, or 8
+ * where the GPU has no group of SMs that holds more. Process-wide; affects
+ * later launches. Results agree to rounding order.
+ */
+void gdn_set_lru_cluster(int most);
+
+/*
  * Path of the bf16 forward with a scalar gate. on = 0 (the default) runs the
  * split path: an intra-chunk pass writing per-chunk operand images, then the
  * chunk-serial state pass. on = 1 runs each scan direction as one kernel in

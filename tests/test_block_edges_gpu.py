@@ -13,8 +13,8 @@ import pytest
 import torch
 
 import gated_delta_rule_18_gb300 as gdn
-from test_block_gpu import TOL_NORM, block_inputs, lru_inputs, norm, ref_block, tol
-from test_layer_gpu import BF, DEV, F32, F64, built, cu_of, dev, f64, randn, spans  # noqa: F401
+from test_block_gpu import TOL_LRU, TOL_LRU_BWD, TOL_NORM, block_inputs, decays, lru_inputs, norm, ref_block, ref_lru, tol
+from test_layer_gpu import BF, DEV, F32, F64, built, cu_of, dev, f64, randn, rel, spans, strided  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -199,6 +199,55 @@ def test_lru_waits_that_run_out(B, T, C, lens, dtype, cta):
                 mine = here.expand(got[k].shape)
             assert not alone or got[k][mine].isnan().all(), k
             assert torch.equal(got[k][~mine], want[k][~mine]), k
+
+
+@pytest.mark.parametrize("B,T,C,lens,off", [
+    (2, 2501, 72, None, False),                                 # tensor copies
+    (1, 2501, 128, [1500, 63, 1, 0, 64, 65, 200, 608], False),  # sequences that end inside, at and across steps
+    (1, 2501, 66, [768, 768, 768, 197], True), (2, 1300, 34, None, True),    # words (in bf16 of pairs)
+    (1, 2501, 65, [1024, 1024, 453], True), (2, 1300, 33, None, True)])      # bf16: elements
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_lru_lines_of_several_cluster_steps(B, T, C, lens, off, dtype):
+    """Lines that a cluster walks in three steps and more, so that its barriers and the runs' places are used again, forward
+    and back, by clusters of the default size (12, or 16 where rows are not wide), of the size taken where those do not fit,
+    and of few CTAs, whose lines have up to 40 steps. Short memories: the tolerances' steps stay below 600."""
+    x, r, i, _, z, h0, n = lru_inputs(B, T, C, lens, dtype, True, seed=280)
+    lam, do, dh = decays(C, 0.5, 0.9), randn((B, T, C), dtype, 290), randn((n, C), F32, 291)
+    leaf = [f64(t).requires_grad_() for t in (x, r, i, lam, z, h0)]
+    ref, fin = ref_lru(*leaf, lens)
+    want = torch.autograd.grad((ref * f64(do)).sum() + (fin * f64(dh)).sum(), leaf)
+    at = (lambda t: strided(dev(t))) if off else dev
+    args, kw = [at(t) for t in (x, r, i)] + [dev(lam)], dict(z=at(z), h0=dev(h0), cu_seqlens=dev(cu_of(lens)))
+    for most in (0, 8, 1, 2, 3):
+        gdn.gdn_set_lru_cluster(most)
+        try:
+            final, ck = torch.empty(n, C, device=DEV), torch.empty(B, (T + 63) // 64, C, device=DEV)
+            got = gdn.gdn_lru_fwd(*args, h_final=final, checkpoints=ck, **kw)
+            grads = [gdn.gdn_lru_bwd(*args, at(do), dh_final=dev(dh), **saved, **kw) for saved in (dict(checkpoints=ck), {})]
+        finally:
+            gdn.gdn_set_lru_cluster(0)
+        assert rel(got, ref.detach()) <= tol(dtype, TOL_LRU) and rel(final, fin.detach()) <= TOL_LRU, most
+        for g in grads:
+            for k, w in zip(("dx", "dr", "di", "dlam", "dz", "dh0"), want):
+                assert rel(g[k], w) <= tol(g[k].dtype, TOL_LRU_BWD), (most, k)
+
+
+def test_lru_large_clusters_in_a_graph():
+    """Whether a cluster of twelve fits is asked on the host, in a captured call as well."""
+    x, r, i, lam, z, h0, n = lru_inputs(1, 1500, 72, None, BF, True, seed=300)
+    args, kw = [dev(t) for t in (x, r, i, lam)], dict(z=dev(z), h0=dev(h0))
+
+    def run():
+        g = gdn.gdn_lru_bwd(*args, args[0], **kw)
+        return [gdn.gdn_lru_fwd(*args, **kw)] + [g[k] for k in sorted(g)]
+
+    want, graph, side = run(), torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        got = run()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 # --------------------------------------------------------- as used together ---
