@@ -252,24 +252,31 @@ __global__ void __launch_bounds__(128) lru_step_kernel(const LruStepParams p) {
 
 }  // namespace
 
-// Whether `tiles` CTAs fill what waves they take of `slots` at a time to three quarters.
-static bool lru_fills(int64_t tiles, int slots) { return tiles * 4 >= (tiles + slots - 1) / slots * slots * 3; }
+// Whether `tiles` CTAs fill what waves they take of `slots` at a time to so many percent.
+static bool lru_fills(int64_t tiles, int slots, int percent) {
+    return tiles * 100 >= (tiles + slots - 1) / slots * slots * percent;
+}
 // CTAs of a cluster, which take a line's tiles side by side, and warps of a CTA.
-// In bf16 a cluster pays for its exchange at every step, so a line's channel
-// tile goes to one CTA of eight warps where those fill the SMs (16 x 1024 tokens
-// of 4096 channels: 126 us, to four CTAs of four warps 144; 24 x 512: 99 for
-// 132), and to four where they do not (8 x 2048 tokens of 2560 channels: 101 for
-// 109) or lines are long (4 x 4096 and 8 x 4096 tokens of 4096 channels: 138 and
-// 261 for 141 and 267). In fp32, which HBM bounds, one CTA of four warps is best
-// (8 x 1024 tokens of 2048 channels: 62, with eight warps 64, four CTAs 72). With
-// few tiles, eight warps and as many CTAs as make 256, up to twelve a line (32768
-// tokens of 1024 channels with 8, 12, 16: 148, 109, 130 us; sixteen warps with
-// 6, 8, 12: 113, 163, 124).
+// In bf16 a cluster pays for its exchange at every step, and a line of one CTA
+// for the SMs that stand idle at the end. So a line's channel tile goes to one
+// CTA of eight warps where those fill the SMs to three quarters and lines are
+// short (4096 channels, one CTA and four: 24 x 512 tokens 93 us and 125, 16 x 1024
+// 116 and 136, 8 x 1700 111 and 113), and for longer lines only where they fill
+// them to nine tenths (9 x 4096: 251 and 268) or are many (16 x 8192: 854 and 887);
+// else to four (8 x 2048: 128.3 and 127.7, 12 x 4096: 365 and 348, 4 x 8192: 251
+// and 239). Rows by words are the same (four warps; 4098 channels, 8 x 1024: 107 and
+// 109, 8 x 4096: 407 and 390, 16 x 4000: 689 and 735), and so are channels that
+// decay fast. In fp32, which HBM bounds, one CTA of four warps is best (8 x 1024
+// tokens of 2048 channels: 62, with eight warps 64, four CTAs 72). With few tiles,
+// eight warps and as many CTAs as make 256, up to twelve a line (32768 tokens of
+// 1024 channels with 8, 12, 16: 148, 109, 130 us; sixteen warps with 6, 8, 12: 113,
+// 163, 124).
 LruShape lru_shape(int lines, int T, int C, bool bf16, bool wide) {
     const int64_t tiles = (int64_t)lines * ((C + kLruCh - 1) / kLruCh);
     LruShape s{1, 4};
     if (tiles >= 192) {
-        const bool whole = lru_fills(tiles, wide ? 304 : 608) && T < 4096;
+        const int slots = wide ? 304 : 608;
+        const bool whole = lru_fills(tiles, slots, T < 2048 || tiles >= 1024 ? 75 : 90);
         s.ranks = !bf16 || whole ? 1 : 4, s.warps = bf16 && whole && wide ? 8 : 4;
     } else {
         const int most = wide ? 12 : 16, all = wide ? 256 : 512;
@@ -286,7 +293,7 @@ LruShape lru_shape(int lines, int T, int C, bool bf16, bool wide) {
 // 8 x 2048 of 2560 channels 262 and 217, fp32 349 and 265).
 int lru_bwd_ranks(int lines, int T, int C) {
     const int64_t tiles = (int64_t)lines * ((C + kLruCh - 1) / kLruCh);
-    int k = tiles >= 192 ? lru_fills(tiles, 304) ? 1 : 4 : (int)(tiles * 12 <= 256 ? 12 : 256 / tiles);
+    int k = tiles >= 192 ? lru_fills(tiles, 304, 75) ? 1 : 4 : (int)(tiles * 12 <= 256 ? 12 : 256 / tiles);
     const int steps = (T + kLruTile - 1) / kLruTile;
     return k > steps ? steps > 0 ? steps : 1 : k;
 }
