@@ -13,7 +13,8 @@ import pytest
 import torch
 
 import gated_delta_rule_18_gb300 as gdn
-from test_block_gpu import TOL_LRU, TOL_LRU_BWD, TOL_NORM, block_inputs, decays, lru_inputs, norm, ref_block, ref_lru, tol
+import test_block_gpu as base
+from test_block_gpu import TOL_LRU, TOL_LRU_BWD, TOL_NORM, TOL_ROT, block_inputs, decays, freqs, lru_inputs, norm, ref_block, ref_lru, ref_rotary, tol
 from test_layer_gpu import BF, DEV, F32, F64, built, cu_of, dev, f64, randn, rel, spans, strided  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -50,7 +51,48 @@ def test_rotary_far_positions_of_exact_frequencies(p):
         assert abs(got[k] - math.cos(angle)) <= bound and abs(got[8 + k] - math.sin(angle)) <= bound, (k, bound)
 
 
+@pytest.mark.parametrize("D,axes,interleaved", [(112, (32, 40, 40), True), (112, (32, 40, 40), False), (128, (64, 32, 32), True), (96, (24, 36, 36), False)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rotary_of_several_axes(D, axes, interleaved, dtype):
+    """A video's tokens by frame, row and column: each axis turns channels of its own, a call on a slice of the head, in place."""
+    B, F, H, W, n = 2, 3, 5, 4, 6
+    q, k = randn((B, F * H * W, n, D), dtype, 300), randn((B, F * H * W, 2, D), dtype, 301)
+    at = torch.stack(torch.meshgrid(torch.arange(F), torch.arange(H), torch.arange(W), indexing="ij")).reshape(3, -1)
+    gq, gk, want, c = dev(q), dev(k), [f64(q), f64(k)], 0
+    for pos, rot in zip(at, axes):
+        f = freqs(rot)
+        a, b = (t[..., c:c + rot] for t in (gq, gk))
+        gdn.gdn_rotary(a, dev(f), k=b, positions=dev(pos.to(torch.int32)), interleaved=interleaved, out=a, k_out=b)
+        for t, x in zip(want, (q, k)):
+            t[..., c:c + rot] = ref_rotary(x[..., c:c + rot], pos.expand(B, -1), f, interleaved, 1.0)
+        c += rot
+    assert rel(gq, want[0]) <= tol(dtype, TOL_ROT) and rel(gk, want[1]) <= tol(dtype, TOL_ROT)
+
+
+@pytest.mark.parametrize("D,rot", [(96, 24), (80, 20), (80, 40), (112, 28), (112, 56), (64, 12), (72, 72)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rotary_parts_off_whole_vectors(D, rot, interleaved, dtype):
+    """Parts of a head whose half is not whole 16-byte vectors, of more heads and tokens than a CTA has under way."""
+    B, T, Hq, Hk = 2, 150, 20, 3
+    q, k, f = randn((B, T, Hq, D), dtype, 310), randn((B, T, Hk, D), dtype, 311), freqs(rot)
+    pos = torch.randint(0, 1 << 20, (B, T), generator=torch.Generator().manual_seed(312))
+    for t in ((dev(q), dev(k)), (strided(dev(q), 8, 8), strided(dev(k), 8, 8))):
+        gq, gk = gdn.gdn_rotary(t[0], dev(f), k=t[1], positions=dev(pos), interleaved=interleaved)
+        for got, x in ((gq, q), (gk, k)):
+            assert rel(got, ref_rotary(x, pos, f, interleaved, 1.0)) <= tol(dtype, TOL_ROT)
+            assert torch.equal(got[..., rot:].cpu(), x[..., rot:])
+
+
 # ------------------------------------------------------------ block norm ---
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 3, 5001), (2, 2, 9001), (1, 3, 4097), (1, 2, 16383)])
+@pytest.mark.parametrize("form", range(len(base.FORMS)))
+def test_block_norm_of_wide_rows_off_vectors(B, T, D, form):
+    """Rows of two and of four vectors a thread that are taken by elements."""
+    base.test_block_norm(B, T, D, form)
+    base.test_block_norm_bwd(B, T, D, form)
 
 
 def rows_rel(got, ref):
