@@ -57,7 +57,10 @@ def rotary_frequencies(rot, base=10000.0, factor=1.0, original_length=None, beta
     positions a model was trained on: every frequency is divided by it, or,
     with original_length (the trained positions), only those that make fewer
     than beta_slow turns in it; those of more than beta_fast turns stay, a linear
-    ramp over the turns lies between, and scale is 0.1 log(factor) + 1."""
+    ramp over the turns lies between, and scale is 0.1 log(factor) + 1. (Code
+    released with checkpoints may ramp over the channel's index between rounded
+    bounds instead, which gives other frequencies: such a model's own table is
+    then inv_freq.)"""
     if rot < 2 or rot % 2:
         raise ValueError(f"rot must be even and at least 2, got {rot}")
     if not base > 0 or not factor >= 1:
@@ -95,7 +98,9 @@ def gdn_rotary(q, inv_freq, k=None, positions=None, offset=0, interleaved=False,
     (j, j + rot / 2) or with interleaved (2 j, 2 j + 1), by the angle p
     inv_freq[j] (fp64 radians), times scale. positions: int32 or int64, (T) or
     (B, T), or None for offset + 0 .. T - 1. inverse turns back: the gradient's
-    map. out and k_out may be q and k. Returns the turned q, or (q, k)."""
+    map. out and k_out may be q and k. Positions of several axes (a video's frame,
+    row and column) are a call each, in place on the axis' slice of the channels.
+    Returns the turned q, or (q, k)."""
     if stream is not None or _elsewhere(q):
         with _guard(q, stream):
             return gdn_rotary(q, inv_freq, k, positions, offset, interleaved, scale, inverse, out, k_out)
@@ -307,7 +312,9 @@ def gdn_lru_fwd(x, r, i, lam, z=None, c=8.0, h0=None, cu_seqlens=None, h_final=N
                 workspace=None, stream=None):
     """The gated linear recurrence: with u = c softplus(lam) sigmoid(r) and a =
     exp(-u), per channel h <- a h + sqrt(1 - a^2) sigmoid(i) x and out = h
-    silu(z) (h without z). x, r, i, z (B, T, C); lam (C) fp32; h0 / h_final
+    silu(z) (h without z). Every token's input takes the root, a sequence's first
+    too: for a model that leaves it out there, that token's x is given divided by
+    it; for another gate than SiLU, z is left out. x, r, i, z (B, T, C); lam (C) fp32; h0 / h_final
     (n_seq, C) fp32; cu_seqlens int32 (n_seq + 1) with B == 1; checkpoints (B,
     ceil(T / LRU_TILE), C) fp32, written: the states gdn_lru_bwd starts its
     tiles from. out may be x, r, i or z. workspace: 256 bytes, whose error word

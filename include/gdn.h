@@ -686,7 +686,10 @@ gdn_status gdn_ssm_step(const void *x, int64_t x_st, const void *dt,
  *   inv_freq: rot / 2 finite doubles, radians a position. positions: int32 or
  *   int64 (pos_bits), strides pos_sb over B and pos_st over T (0 shares), or
  *   NULL: offset + t.
- *   rot even, 2 <= rot <= D <= 512; B T <= 2^31 - 65536.
+ *   rot even, 2 <= rot <= D <= 512; B T <= 2^31 - 65536. One position a token:
+ *   several axes are a call each, on the axis' slice of the channels. Fastest
+ *   where rows lie on 16 bytes and D and a turning half (interleaved: rot) are
+ *   whole vectors of 16 bytes; else single elements are moved.
  *   The angle is reduced in fixed point: any int64 position is as good as its
  *   frequency's own 53 bits.
  */
@@ -759,6 +762,9 @@ gdn_status gdn_block_norm_bwd(const void *y, int64_t y_st, int y_dtype,
  *   u_t = c softplus(lam) sigmoid(r_t),  a_t = exp(-u_t)
  *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t      (fp32)
  *   out = h_t silu(z_t)  (h_t with z NULL)
+ *   The root scales every token's input, a sequence's first too (models that
+ *   leave it out there give that token's x divided by it), and the gate is
+ *   SiLU (for another one z is left out).
  *   x, r, i, z, out: (B, T, C) of `dtype`; lam (C) fp32; c >= 0.
  *   h0, h_final: (n_seq, C) fp32 or NULL. checkpoints: (B, ceil(T / 64), C)
  *   fp32 or NULL: the state before every 64th token, for the gradient.
