@@ -542,7 +542,9 @@ gdn_status gdn_rmsnorm_fwd(const void *x, int64_t x_st, int x_dtype,
  *   dx = inv weight dy - s inv^3 mean(weight dy s) + dres,
  *   dweight = sum over rows of dy s inv (fp32, in a fixed order).
  *   s, dres (or NULL), dx: (R, D), s_dtype; dy: (R, D), dy_dtype. dx is the
- *   gradient of s: of x and of the residual alike.
+ *   gradient of s: of x and of the residual alike. A row whose sum of squares,
+ *   alone or times one of its |weight dy|, passes fp32's range has a dx that is
+ *   not finite; other rows and dweight stay right.
  *   workspace: gdn_rmsnorm_bwd_workspace_size(R, D) bytes, 256-byte aligned.
  */
 size_t gdn_rmsnorm_bwd_workspace_size(int R, int D);

@@ -140,6 +140,19 @@ def test_block_norm_gradient_of_large_rows(D, dtype, gate):
             assert rows_rel(b["dgate"], want["g"]) <= tol(dtype, TOL_NORM)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rms_norm_weights_gradient_beside_large_rows(dtype):
+    """The layer's norm has no finite dx for rows whose sum of squares comes near the end of fp32's range; the weights' gradient
+    and the other rows' stay right."""
+    s, w, dy = randn((12, 256), dtype, 320), randn((256,), F32, 321, 0.1, 1.0), randn((12, 256), dtype, 322, 1.5)
+    s[3], s[7], s[8], s[11] = -1e18, torch.finfo(dtype).min, 1e12, 1e16
+    leaf = f64(s).requires_grad_(), f64(w).requires_grad_()
+    ds, dw = torch.autograd.grad((norm(leaf[0].masked_fill(f64(s) == f64(s[7]).min(), 0), leaf[1], 1e-6) * f64(dy)).sum(), leaf)
+    got = gdn.gdn_rmsnorm_bwd(dev(s), dev(w), dev(dy))
+    rest = [k for k in range(12) if k not in (3, 7)]
+    assert rows_rel(got["dx"][rest], ds[rest]) <= tol(dtype, TOL_NORM) and rows_rel(got["dweight"][None], dw[None]) <= TOL_NORM
+
+
 def test_block_norm_gradient_with_a_small_eps():
     """Rows of zeros under a small eps, whose inverse root's third power fp32 does not hold: the gradient is gw / sqrt(eps)."""
     y, do, w = torch.zeros(1, 2, 64, device=DEV), dev(randn((1, 2, 64), F32, 230)), torch.ones(64, device=DEV)
@@ -272,6 +285,15 @@ def test_lru_lines_of_several_cluster_steps(B, T, C, lens, off, dtype):
         for g in grads:
             for k, w in zip(("dx", "dr", "di", "dlam", "dz", "dh0"), want):
                 assert rel(g[k], w) <= tol(g[k].dtype, TOL_LRU_BWD), (most, k)
+
+
+def test_lru_without_tokens_clears_the_error_word():
+    t, lam, ws = torch.empty(1, 0, 64, dtype=BF, device=DEV), torch.zeros(64, device=DEV), torch.full((512,), 255, dtype=torch.uint8, device=DEV)
+    for call in (lambda: gdn.gdn_lru_fwd(t, t, t, lam, workspace=ws), lambda: gdn.gdn_lru_bwd(t, t, t, lam, t, workspace=ws),
+                 lambda: gdn.gdn_lru_fwd(t, t, t, lam, cu_seqlens=torch.zeros(3, dtype=torch.int32, device=DEV), workspace=ws)):
+        ws.fill_(255)
+        call()
+        assert gdn.gdn_last_device_error(ws) == 0
 
 
 def test_lru_large_clusters_in_a_graph():
