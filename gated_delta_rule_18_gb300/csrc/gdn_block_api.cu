@@ -274,12 +274,12 @@ gdn_status gdn_lru_fwd(const void *x, int64_t x_sb, int64_t x_st, const void *r,
                  {Area(lam, GDN_F32, C), Area(h0, GDN_F32, states)});
     if (a != GDN_OK) return a;
     if (cu_seqlens && !ws_ok(workspace, ws_bytes, kAlign)) return GDN_ERR_WORKSPACE;
+    if (T == 0 && !h_final && !cu_seqlens) return GDN_OK;
     p.out = out, p.o_sb = out_sb, p.o_st = out_st, p.h_final = h_final, p.ck = checkpoints;
     p.how = rows.how(C, dtype);
     const LruShape shape = lru_shape(B, T, C, p.bf16, p.how == 0);
     p.ranks = shape.ranks, p.warps = shape.warps;
     p.err = ws_ok(workspace, ws_bytes, kAlign) ? static_cast<int *>(workspace) : nullptr;
-    if (T == 0 && !h_final && !p.err) return GDN_OK;
     return cuda_status(launch(KLru, stream, [&] { return launch_lru(p, stream); }));
 }
 

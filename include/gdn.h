@@ -771,7 +771,8 @@ gdn_status gdn_block_norm_bwd(const void *y, int64_t y_st, int y_dtype,
  *   h0, h_final: (n_seq, C) fp32 or NULL. checkpoints: (B, ceil(T / 64), C)
  *   fp32 or NULL: the state before every 64th token, for the gradient.
  *   out may lie on x, r, i or z. workspace: 256 bytes, needed with cu_seqlens;
- *   its error word (gdn_last_device_error) is this call's. A state that is not
+ *   its error word (gdn_last_device_error) is this call's (a dense call without
+ *   tokens and h_final has nothing to do and leaves it). A state that is not
  *   finite stays so in its channel to its sequence's end. A wait inside the
  *   kernel that runs out (half a second) is reported as GDN_DEVERR_TIMEOUT in the
  *   error word, where there is a workspace, and leaves NaN: a CTA writes NaN for

@@ -289,7 +289,8 @@ def test_lru_lines_of_several_cluster_steps(B, T, C, lens, off, dtype):
 
 def test_lru_without_tokens_clears_the_error_word():
     t, lam, ws = torch.empty(1, 0, 64, dtype=BF, device=DEV), torch.zeros(64, device=DEV), torch.full((512,), 255, dtype=torch.uint8, device=DEV)
-    for call in (lambda: gdn.gdn_lru_fwd(t, t, t, lam, workspace=ws), lambda: gdn.gdn_lru_bwd(t, t, t, lam, t, workspace=ws),
+    final = torch.empty(1, 64, device=DEV)
+    for call in (lambda: gdn.gdn_lru_fwd(t, t, t, lam, h_final=final, workspace=ws), lambda: gdn.gdn_lru_bwd(t, t, t, lam, t, workspace=ws),
                  lambda: gdn.gdn_lru_fwd(t, t, t, lam, cu_seqlens=torch.zeros(3, dtype=torch.int32, device=DEV), workspace=ws)):
         ws.fill_(255)
         call()
