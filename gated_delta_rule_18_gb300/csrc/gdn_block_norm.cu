@@ -16,8 +16,8 @@
 // cross warps through shared memory. Sums and norms are fp32.
 //
 // Measured (copy rate 6.78 TB/s): forward, 4 x 4096 rows of 4096 channels with a
-// gate a token, fp32 residual 152 us (91 %), bf16 113 (87 %); gradient 298 (73 %)
-// and 287 (55 %). 2 x 8192 rows of 1792 channels, bf16, gate shared: 48, and 111
+// gate a token, fp32 residual 152 us (91 %), bf16 113 (87 %), all fp32 214 (93 %);
+// gradient 300 (72 %), 289 (55 %) and 361 (88 %). 2 x 8192 rows of 1792 channels, bf16, gate shared: 48, and 111
 // in three launches (98, 10, 5). In bf16 the gradient's instructions come before
 // its bytes: 140 a warp and channel pair (two norms' sums and gradients), at 0.56
 // a cycle from the 16 warps a SM that 128 registers leave.

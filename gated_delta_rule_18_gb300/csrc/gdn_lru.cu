@@ -15,13 +15,15 @@
 // copies as soon as the gates are formed, z after the walk. Results repeat bit
 // for bit.
 //
-// Measured (copy rate 6.78 TB/s): 4 x 4096 tokens of 4096 channels 132 us in
-// bf16 (75 % of the copy rate), 206 in fp32 (96 %); 8 x 1024 of 4096 channels,
-// bf16, 68: 74 instructions a warp and channel pair at 0.56 a cycle from 14
-// warps a SM, 14 of them for the exponential unit (16 where a channel decays
-// fast), whose queue is a large stall. 32768 tokens of 1024 channels 105 (47 %):
-// with 16 tiles of channels only, 10 warps a SM, and an exchange over the
-// cluster every 1536 tokens.
+// Measured (calls among others, copy rate 6.78 TB/s): 4 x 4096 tokens of 4096
+// channels with z in bf16 125 us (79 % of the copy rate) where all of a tile's
+// channels decay slowly (c softplus(lam) < 1/8) and 133 (74 %) where one does not, in
+// fp32 194 and 198 (all of it); 8 x 1024 of 4096 channels, bf16, 68 and 73: 75
+// instructions a warp and channel pair at 0.56 a cycle from 14 warps a SM, 14 of
+// them for the exponential unit (16 where a channel decays fast), whose queue is
+// a large stall. 32768 tokens of 1024 channels 106 and 113 (47 %): with 16 tiles of
+// channels only, 10 warps a SM, and an exchange over the cluster every 1536
+// tokens.
 #include <cudaTypedefs.h>
 
 #include <atomic>

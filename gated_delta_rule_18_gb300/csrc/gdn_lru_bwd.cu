@@ -14,11 +14,11 @@
 // too. The walk back takes the gates and roots as the sweep before it left them:
 // in shared memory, and in the places of r and i, which only the sweep reads.
 //
-// Measured: 4 x 4096 tokens of 4096 channels, bf16, 319 us (56 % of the copy
-// rate, where the bytes take 178), fp32 386 (92 %). 173 instructions a warp and
-// channel pair at 0.53 a cycle, 14 warps a SM (126 registers, 86 KB a CTA).
-// Next rows in two halves, the first asked for amid the walk: 332 for 321; sigmoid(z)
-// kept as well: 327.
+// Measured: 4 x 4096 tokens of 4096 channels, bf16, 314 us (57 % of the copy
+// rate, where the bytes take 178; 317 where channels decay fast), fp32 351 (all of
+// it); out of wider rows 320 and 381. 174 instructions a warp and channel pair at
+// 0.53 a cycle, 14 warps a SM (128 registers, 86 KB a CTA). Next rows in two halves,
+// the first asked for amid the walk: 332 for 321; sigmoid(z) kept as well: 327.
 #include "gdn_lru.cuh"
 
 namespace gdn {

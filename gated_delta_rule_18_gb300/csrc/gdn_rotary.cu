@@ -20,8 +20,12 @@
 // Measured, bf16 (copy rate 6.78 TB/s): 4 x 4096 tokens, 32 + 8 heads of 128
 // channels, halves, 56 us (49.5 at the copy rate); 2 x 8192, 16 + 16 heads of 112
 // with 64 turning, interleaved, 44, out of wider rows (34.6). Loads on their way
-// are the largest stall (20 warps a SM, 80 registers). With cosines read again
-// for every head and fp64 angles it took 66 and 68.
+// are the largest stall (20 warps a SM, 80 registers). In fp32 103 (96 %) and 73 (95 %).
+// With cosines read again for every head and fp64 angles it took 66 and 68. Parts whose
+// half is not whole vectors (interleaved: the part) and rows off 16 bytes go by
+// single elements, two heads under way: 4 x 4096 tokens, 32 + 8 heads of 96 channels
+// with 24 turning in halves, bf16, 177 us (37 at the copy rate; interleaved, by vectors,
+// 46), of 80 with 20 or 40 turning 157 (31).
 #include "gdn_ssm.cuh"
 #include "gdn_block.cuh"
 
